@@ -5,11 +5,12 @@ only turns torch tensors into pointers, allocates outputs and the workspace on
 the caller's behalf (torch owns that memory), and raises on a non-OK status.
 The library must have been built (``build.py``); there is no fallback.
 
-The function names follow the C ABI in include/gdn.h.
+The function names follow the C ABI in include/gdn.h, gdn_conv.h and gdn_layer.h.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -32,6 +33,12 @@ GDN_WS_SAVED = 2
 # include/gdn_conv.h
 CONV_EXPORTS = ["gdn_conv_workspace_bytes", "gdn_conv_fwd", "gdn_conv_bwd"]
 CONV_ACT = {"none": 0, "silu": 1}
+# include/gdn_layer.h
+LAYER_EXPORTS = ["gdn_step", "gdn_conv_step", "gdn_prep_fwd", "gdn_prep_bwd",
+                 "gdn_prep_workspace_bytes", "gdn_gate_norm_fwd", "gdn_gate_norm_bwd",
+                 "gdn_gate_norm_workspace_bytes", "gdn_res_norm_fwd", "gdn_res_norm_bwd",
+                 "gdn_res_norm_workspace_bytes"]
+GATE_ACT = {"silu": 1, "sigmoid": 2}
 
 
 class GdnError(RuntimeError):
@@ -48,6 +55,34 @@ class gdn_shape(ctypes.Structure):
 class gdn_conv_shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("C", ctypes.c_int),
                 ("W", ctypes.c_int), ("dtype", ctypes.c_int), ("act", ctypes.c_int)]
+
+
+_I, _L, _F = ctypes.c_int, ctypes.c_longlong, ctypes.c_float
+
+
+class gdn_step_shape(ctypes.Structure):
+    _fields_ = [("N", _I), ("n_tok", _I), ("n_slots", _I), ("H", _I), ("Hk", _I), ("dk", _I),
+                ("dv", _I), ("dtype", _I), ("ldq", _L), ("ldk", _L), ("ldv", _L), ("ldg", _L),
+                ("ldb", _L), ("q_scale", _F), ("eps", _F)]
+
+
+class gdn_conv_step_shape(ctypes.Structure):
+    _fields_ = [("N", _I), ("n_tok", _I), ("n_slots", _I), ("C", _I), ("W", _I), ("dtype", _I),
+                ("act", _I), ("ldx", _L)]
+
+
+class gdn_prep_shape(ctypes.Structure):
+    _fields_ = [("rows", _I), ("H", _I), ("Hk", _I), ("dk", _I), ("dtype", _I), ("ldq", _L),
+                ("ldk", _L), ("ldg", _L), ("ldb", _L), ("q_scale", _F), ("eps", _F)]
+
+
+class gdn_gate_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", _I), ("H", _I), ("d", _I), ("dtype", _I), ("act", _I), ("ldz", _L),
+                ("eps", _F)]
+
+
+class gdn_res_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", _I), ("C", _I), ("dtype", _I), ("res_dtype", _I), ("eps", _F)]
 
 
 _lib = None
@@ -110,6 +145,22 @@ def load(build_if_missing: bool = False):
     lib.gdn_conv_fwd.restype = I
     lib.gdn_conv_bwd.argtypes = [CP] + [P] * 10 + [P, Z, P]
     lib.gdn_conv_bwd.restype = I
+    for name, shape, nptr, ws in (("gdn_step", gdn_step_shape, 13, False),
+                                  ("gdn_conv_step", gdn_conv_step_shape, 9, False),
+                                  ("gdn_prep_fwd", gdn_prep_shape, 10, False),
+                                  ("gdn_prep_bwd", gdn_prep_shape, 16, True),
+                                  ("gdn_gate_norm_fwd", gdn_gate_norm_shape, 4, False),
+                                  ("gdn_gate_norm_bwd", gdn_gate_norm_shape, 7, True),
+                                  ("gdn_res_norm_fwd", gdn_res_norm_shape, 7, False),
+                                  ("gdn_res_norm_bwd", gdn_res_norm_shape, 12, True)):
+        f = getattr(lib, name)
+        f.argtypes = [ctypes.POINTER(shape)] + [P] * nptr + ([P, Z, P] if ws else [P])
+        f.restype = I
+    for name, shape in (("prep", gdn_prep_shape), ("gate_norm", gdn_gate_norm_shape),
+                        ("res_norm", gdn_res_norm_shape)):
+        f = getattr(lib, f"gdn_{name}_workspace_bytes")
+        f.argtypes = [ctypes.POINTER(shape)]
+        f.restype = Z
     lib.gdn_profile_arm.argtypes = [P, I]
     lib.gdn_profile_arm.restype = None
     lib.gdn_profile_count.argtypes = []
@@ -352,6 +403,302 @@ def gdn_conv_bwd(x, w, b, state_in, dy, dstate_out=None, act="silu", dx=None, dw
                           workspace.numel(), _stream(stream))
     _check(rc, "gdn_conv_bwd")
     return dx, dw, db, dstate_in
+
+
+# ------------------------------------------------- layer operators (include/gdn_layer.h)
+def _own_stream(fn):
+    """With stream=..., run fn with that stream current, so that what it
+    allocates (outputs, workspace) belongs to the stream its kernels run on."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _on_gpu(name, t, ndim):
+    if not t.is_cuda or t.dim() < ndim:
+        raise ValueError(f"{name}: a CUDA tensor with {ndim} dimensions is expected, got "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _want(name, t, shape, dtype, device):
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _want_c(name, t, shape, dtype, device):
+    """As _want, and contiguous; returns the pointer (None for an absent tensor)."""
+    if t is None:
+        return None
+    _want(name, t, shape, dtype, device)
+    return _p(t)
+
+
+def _rows(name, t, ndim):
+    """Stride of the rows of t [..., n1, .., nk] (k = ndim trailing dimensions that
+    have to be dense) when its leading dimensions flatten to one."""
+    inner = 1
+    for i in range(1, ndim + 1):
+        if t.shape[-i] != 1 and t.stride(-i) != inner:
+            raise ValueError(f"{name}: the last {ndim} dimensions must be dense")
+        inner *= t.shape[-i]
+    ld, n = inner, 1
+    for i in range(t.dim() - ndim - 1, -1, -1):
+        if t.shape[i] == 1:
+            continue
+        if n == 1:
+            ld = t.stride(i)
+        elif t.stride(i) != ld * n:
+            raise ValueError(f"{name}: the rows must have one stride")
+        n *= t.shape[i]
+    return ld
+
+
+def _cache_args(N, n_tok, device, slot_in, slot_out, cu_seqlens, n_commit):
+    i32 = torch.int32
+    return (_want_c("slot_in", slot_in, (N,), i32, device),
+            _want_c("slot_out", slot_out, (N,), i32, device),
+            _want_c("cu_seqlens", cu_seqlens, (N + 1,), i32, device),
+            _want_c("n_commit", n_commit, (N,), i32, device))
+
+
+@_own_stream
+def gdn_step(q, k, v, g, beta, S, slot_in=None, slot_out=None, cu_seqlens=None, n_commit=None,
+             gate=None, q_scale=1.0, eps=1e-6, o=None):
+    """The gated delta rule token by token over the states S [n_slots, H, dk, dv]
+    (fp32, updated in place) of N sequences whose new tokens are packed:
+    q, k [n_tok, Hk, dk], v [n_tok, H, dv], g, beta [n_tok, H], rows strided.
+
+    cu_seqlens [N + 1]: the sequences' rows (None: one token each). slot_in /
+    slot_out [N]: the slot a sequence's state is read from (-1: zero state) and
+    written to (-1: nowhere); None: slot s for sequence s. n_commit [N]: the state
+    after that many of its tokens is written (None: all). All int32 on the device.
+    gate = (rate, bias) [H] fp32: g and beta are the inputs of gdn_prep_fwd's maps
+    and q, k are normalised. Returns o [n_tok, H, dv]."""
+    _on_gpu("q", q, 3)
+    _on_gpu("v", v, 3)
+    n, Hk, dk = q.shape
+    H, dv = v.shape[1:]
+    dt, dev = q.dtype, q.device
+    N = n if cu_seqlens is None else cu_seqlens.numel() - 1
+    _want("k", k, (n, Hk, dk), dt, dev)
+    _want("v", v, (n, H, dv), dt, dev)
+    _want("g", g, (n, H), dt, dev)
+    _want("beta", beta, (n, H), dt, dev)
+    rate, bias = gate if gate is not None else (None, None)
+    s = gdn_step_shape(N, n, S.shape[0], H, Hk, dk, dv, _dtype_code(q), _rows("q", q, 2),
+                       _rows("k", k, 2), _rows("v", v, 2), _rows("g", g, 1),
+                       _rows("beta", beta, 1), q_scale, eps)
+    if o is None:
+        o = torch.empty(n, H, dv, dtype=dt, device=dev)
+    f32 = torch.float32
+    rc = load().gdn_step(
+        s, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+        _want_c("rate", rate, (H,), f32, dev), _want_c("bias", bias, (H,), f32, dev),
+        _want_c("S", S, (S.shape[0], H, dk, dv), f32, dev),
+        *_cache_args(N, n, dev, slot_in, slot_out, cu_seqlens, n_commit),
+        _want_c("o", o, (n, H, dv), dt, dev), _stream(None))
+    _check(rc, "gdn_step")
+    return o
+
+
+@_own_stream
+def gdn_conv_step(x, w, b, state, slot_in=None, slot_out=None, cu_seqlens=None, n_commit=None,
+                  act="silu", y=None):
+    """The short convolution of packed new tokens x [n_tok, C] (rows strided) over
+    the cached last inputs state [n_slots, W - 1, C] (updated in place), for the
+    sequences of gdn_step. Returns y [n_tok, C]."""
+    _on_gpu("x", x, 2)
+    _on_gpu("w", w, 2)
+    n, C = x.shape
+    W = w.shape[1]
+    dt, dev, f32 = x.dtype, x.device, torch.float32
+    N = n if cu_seqlens is None else cu_seqlens.numel() - 1
+    s = gdn_conv_step_shape(N, n, state.shape[0], C, W, _dtype_code(x), CONV_ACT[act],
+                            _rows("x", x, 1))
+    if y is None:
+        y = torch.empty(n, C, dtype=dt, device=dev)
+    rc = load().gdn_conv_step(
+        s, x.data_ptr(), _want_c("w", w, (C, W), f32, dev), _want_c("b", b, (C,), f32, dev),
+        _want_c("state", state, (state.shape[0], W - 1, C), dt, dev),
+        *_cache_args(N, n, dev, slot_in, slot_out, cu_seqlens, n_commit),
+        _want_c("y", y, (n, C), dt, dev), _stream(None))
+    _check(rc, "gdn_conv_step")
+    return y
+
+
+def _prep_shape_of(q, k, xg, xb, q_scale, eps):
+    _on_gpu("q", q, 4)
+    _on_gpu("xg", xg, 3)
+    B, T, Hk, dk = q.shape
+    H = xg.shape[2]
+    _want("k", k, (B, T, Hk, dk), q.dtype, q.device)
+    _want("xg", xg, (B, T, H), q.dtype, q.device)
+    _want("xb", xb, (B, T, H), q.dtype, q.device)
+    return gdn_prep_shape(B * T, H, Hk, dk, _dtype_code(q), _rows("q", q, 2), _rows("k", k, 2),
+                          _rows("xg", xg, 1), _rows("xb", xb, 1), q_scale, eps)
+
+
+@_own_stream
+def gdn_prep_fwd(q, k, xg, xb, rate, bias, q_scale=1.0, eps=1e-6):
+    """The maps before the recurrence. q, k [B, T, Hk, dk] and xg, xb [B, T, H] (rows
+    strided), rate, bias [H] fp32. Returns (q, k [B, T, H, dk], g, beta [B, T, H]) as
+    gdn_chunk_fwd takes them: q and k of unit norm (q times q_scale), each key
+    head repeated for its H / Hk value heads, g = -exp(rate) softplus(xg + bias),
+    beta = sigmoid(xb)."""
+    s = _prep_shape_of(q, k, xg, xb, q_scale, eps)
+    B, T, _, dk = q.shape
+    H, dt, dev, f32 = s.H, q.dtype, q.device, torch.float32
+    qn = torch.empty(B, T, H, dk, dtype=dt, device=dev)
+    kn = torch.empty(B, T, H, dk, dtype=dt, device=dev)
+    g = torch.empty(B, T, H, dtype=dt, device=dev)
+    beta = torch.empty(B, T, H, dtype=dt, device=dev)
+    rc = load().gdn_prep_fwd(s, q.data_ptr(), k.data_ptr(), xg.data_ptr(), xb.data_ptr(),
+                             _want_c("rate", rate, (H,), f32, dev),
+                             _want_c("bias", bias, (H,), f32, dev), qn.data_ptr(), kn.data_ptr(),
+                             g.data_ptr(), beta.data_ptr(), _stream(None))
+    _check(rc, "gdn_prep_fwd")
+    return qn, kn, g, beta
+
+
+@_own_stream
+def gdn_prep_bwd(q, k, xg, xb, rate, bias, dq, dk, dg, dbeta, q_scale=1.0, eps=1e-6,
+                 workspace=None):
+    """Gradients of gdn_prep_fwd from those of its outputs, as gdn_chunk_bwd
+    returns them. Returns (dq, dk [B, T, Hk, dk], dxg, dxb [B, T, H], drate, dbias [H])."""
+    lib = load()
+    s = _prep_shape_of(q, k, xg, xb, q_scale, eps)
+    B, T, Hk, D = q.shape
+    H, dt, dev, f32 = s.H, q.dtype, q.device, torch.float32
+    if workspace is None:
+        workspace = alloc_workspace(lib.gdn_prep_workspace_bytes(s), dev)
+    oq = torch.empty(B, T, Hk, D, dtype=dt, device=dev)
+    ok = torch.empty(B, T, Hk, D, dtype=dt, device=dev)
+    og = torch.empty(B, T, H, dtype=dt, device=dev)
+    ob = torch.empty(B, T, H, dtype=dt, device=dev)
+    par = torch.empty(2, H, dtype=f32, device=dev)
+    rc = lib.gdn_prep_bwd(s, q.data_ptr(), k.data_ptr(), xg.data_ptr(), xb.data_ptr(),
+                          _want_c("rate", rate, (H,), f32, dev),
+                          _want_c("bias", bias, (H,), f32, dev),
+                          _want_c("dq", dq, (B, T, H, D), dt, dev),
+                          _want_c("dk", dk, (B, T, H, D), dt, dev),
+                          _want_c("dg", dg, (B, T, H), dt, dev),
+                          _want_c("dbeta", dbeta, (B, T, H), dt, dev), oq.data_ptr(),
+                          ok.data_ptr(), og.data_ptr(), ob.data_ptr(), par.data_ptr(),
+                          par.data_ptr() + 4 * H, _p(workspace), workspace.numel(),
+                          _stream(None))
+    _check(rc, "gdn_prep_bwd")
+    return oq, ok, og, ob, par[0], par[1]
+
+
+def _gate_norm_shape_of(o, z, act, eps):
+    _on_gpu("o", o, 4)
+    B, T, H, d = o.shape
+    _want("z", z, (B, T, H, d), o.dtype, o.device)
+    return gdn_gate_norm_shape(B * T, H, d, _dtype_code(o), GATE_ACT[act], _rows("z", z, 2), eps)
+
+
+@_own_stream
+def gdn_gate_norm_fwd(o, z, w, act="silu", eps=1e-6, y=None):
+    """y = rms_norm(o) * w * act(z) over the last dimension of o [B, T, H, d]; z [B, T, H, d]
+    with strided token rows, w [d] fp32, act "silu" or "sigmoid"."""
+    s = _gate_norm_shape_of(o, z, act, eps)
+    if y is None:
+        y = torch.empty(o.shape, dtype=o.dtype, device=o.device)
+    rc = load().gdn_gate_norm_fwd(s, _p(o), z.data_ptr(),
+                                  _want_c("w", w, (s.d,), torch.float32, o.device),
+                                  _want_c("y", y, o.shape, o.dtype, o.device), _stream(None))
+    _check(rc, "gdn_gate_norm_fwd")
+    return y
+
+
+@_own_stream
+def gdn_gate_norm_bwd(o, z, w, dy, act="silu", eps=1e-6, workspace=None):
+    """Backward of gdn_gate_norm_fwd. Returns (do, dz, dw)."""
+    lib = load()
+    s = _gate_norm_shape_of(o, z, act, eps)
+    if workspace is None:
+        workspace = alloc_workspace(lib.gdn_gate_norm_workspace_bytes(s), o.device)
+    do = torch.empty(o.shape, dtype=o.dtype, device=o.device)
+    dz = torch.empty(o.shape, dtype=o.dtype, device=o.device)
+    dw = torch.empty(s.d, dtype=torch.float32, device=o.device)
+    rc = lib.gdn_gate_norm_bwd(s, _p(o), z.data_ptr(),
+                               _want_c("w", w, (s.d,), torch.float32, o.device),
+                               _want_c("dy", dy, o.shape, o.dtype, o.device), do.data_ptr(),
+                               dz.data_ptr(), dw.data_ptr(), _p(workspace), workspace.numel(),
+                               _stream(None))
+    _check(rc, "gdn_gate_norm_bwd")
+    return do, dz, dw
+
+
+def _res_norm_shape_of(h, like, eps):
+    _on_gpu("h", h, 1)
+    C = h.shape[-1]
+    return gdn_res_norm_shape(h.numel() // C if C else 0, C, _dtype_code(like), _dtype_code(h),
+                              eps)
+
+
+@_own_stream
+def gdn_res_norm_fwd(h, x, w, w_post=None, scale=None, eps=1e-6, h_out=None, y=None,
+                     dtype=None):
+    """Block boundary: h_out = h + scale * (rms_norm(x) * w_post), y = rms_norm(h_out) * w.
+
+    h [..., C] is the residual stream (fp32, or x's dtype), x [..., C] the block's
+    output; w, w_post, scale [C] fp32. w_post None: x as it is; scale None: 1; x None
+    (before the first block): y is the norm of h, in `dtype` (default h's).
+    h_out may be h. Returns (h_out, y); h_out is None where x is."""
+    dt = x.dtype if x is not None else dtype or h.dtype
+    dev, C, f32 = h.device, h.shape[-1], torch.float32
+    if y is None:
+        y = torch.empty(h.shape, dtype=dt, device=dev)
+    if h_out is None and x is not None:
+        h_out = torch.empty(h.shape, dtype=h.dtype, device=dev)
+    s = _res_norm_shape_of(h, y, eps)
+    rc = load().gdn_res_norm_fwd(s, _p(h), _want_c("x", x, h.shape, dt, dev),
+                                 _want_c("w", w, (C,), f32, dev),
+                                 _want_c("w_post", w_post, (C,), f32, dev),
+                                 _want_c("scale", scale, (C,), f32, dev),
+                                 _want_c("h_out", h_out, h.shape, h.dtype, dev),
+                                 _want_c("y", y, h.shape, dt, dev), _stream(None))
+    _check(rc, "gdn_res_norm_fwd")
+    return h_out, y
+
+
+@_own_stream
+def gdn_res_norm_bwd(h_out, x, w, dy, dh_out=None, w_post=None, scale=None, eps=1e-6, dh=None,
+                     workspace=None):
+    """Backward of gdn_res_norm_fwd at the residual it returned (for x None: at h).
+    dh may be dh_out. Returns (dh, dx, dw, dw_post, dscale); dx is dh itself where
+    they are equal (no w_post, no scale, one dtype)."""
+    lib = load()
+    C, dev, f32 = h_out.shape[-1], h_out.device, torch.float32
+    s = _res_norm_shape_of(h_out, dy, eps)
+    if workspace is None:
+        workspace = alloc_workspace(lib.gdn_res_norm_workspace_bytes(s), dev)
+    if dh is None:
+        dh = torch.empty(h_out.shape, dtype=h_out.dtype, device=dev)
+    same = w_post is None and scale is None and (dy.dtype == h_out.dtype or x is None)
+    dx = None if same else torch.empty(h_out.shape, dtype=dy.dtype, device=dev)
+    dw = torch.empty(C, dtype=f32, device=dev)
+    dpost = None if w_post is None else torch.empty(C, dtype=f32, device=dev)
+    dscale = None if scale is None else torch.empty(C, dtype=f32, device=dev)
+    rc = lib.gdn_res_norm_bwd(s, _p(h_out), _want_c("x", x, h_out.shape, dy.dtype, dev),
+                              _want_c("w", w, (C,), f32, dev),
+                              _want_c("w_post", w_post, (C,), f32, dev),
+                              _want_c("scale", scale, (C,), f32, dev),
+                              _want_c("dy", dy, h_out.shape, dy.dtype, dev),
+                              _want_c("dh_out", dh_out, h_out.shape, h_out.dtype, dev),
+                              _want_c("dh", dh, h_out.shape, h_out.dtype, dev), _p(dx), _p(dw),
+                              _p(dpost), _p(dscale), _p(workspace), workspace.numel(),
+                              _stream(None))
+    _check(rc, "gdn_res_norm_bwd")
+    return dh, (dh if same else dx), dw, dpost, dscale
 
 
 def gdn_workspace_status(workspace, stream=None) -> int:
