@@ -22,6 +22,32 @@ __device__ __forceinline__ void ld8(const __nv_bfloat16* p, float* v) {
     v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
 }
+// 8 elements as loaded, converted when used.
+template <typename T>
+struct Raw8 {
+  uint4 u[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> ldraw8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+__device__ __forceinline__ void cvt8(const Raw8<float>& a, float* v) {
+  const uint32_t u[8] = {a.u[0].x, a.u[0].y, a.u[0].z, a.u[0].w,
+                         a.u[1].x, a.u[1].y, a.u[1].z, a.u[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void cvt8(const Raw8<__nv_bfloat16>& a, float* v) {
+  const uint32_t u[4] = {a.u[0].x, a.u[0].y, a.u[0].z, a.u[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
 __device__ __forceinline__ void st8(float* p, const float* v) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -44,7 +70,35 @@ __device__ __forceinline__ float lane_sum(float x) {
   return x;
 }
 
+// n / d and n % d for 0 <= n < 2^31 without a division: with l = ceil(log2 d)
+// and m = ceil(2^(31+l) / d), m d - 2^(31+l) < d <= 2^l, so n (m d - 2^(31+l)) <
+// 2^(31+l) and floor(n m / 2^(31+l)) is the quotient; m < 2^32.
+struct FastDiv {
+  uint32_t d, m;
+  int s;
+  explicit FastDiv(int div) : d((uint32_t)div), s(31) {
+    while ((1ull << (s - 31)) < d) ++s;
+    m = (uint32_t)(((1ull << s) + d - 1) / d);
+  }
+  __device__ __forceinline__ void operator()(uint32_t n, uint32_t& q, uint32_t& r) const {
+    q = (uint32_t)(((unsigned long long)n * m) >> s);
+    r = n - q * d;
+  }
+};
+
 __device__ __forceinline__ float sigmoidf_(float x) { return 1.f / (1.f + expf(-x)); }
+// sigmoid of a value that is stored as T: for bf16 results the hardware's
+// approximate exponential and reciprocal (relative error below 1e-6 for
+// |x| < 10, against bf16's 4e-3) instead of the exact library sequences, which
+// cost several times the instructions.
+template <typename T>
+__device__ __forceinline__ float sigmoid_as(float x) {
+  return sigmoidf_(x);
+}
+template <>
+__device__ __forceinline__ float sigmoid_as<__nv_bfloat16>(float x) {
+  return __fdividef(1.f, 1.f + __expf(-x));
+}
 // log(1 + e^x) without overflow for large x and without cancellation for small
 __device__ __forceinline__ float softplusf_(float x) {
   return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));

@@ -6,16 +6,20 @@
 #include <algorithm>
 
 #include "gdn_layer.cuh"
+#include "gdn_mma.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int GN_NT = 256;     // threads of a block
+constexpr int GN_U = 4;        // rows a thread has in flight (forward)
+constexpr int GN_UB = 2;       // rows a thread has in flight (backward)
 constexpr int GN_PARTS = 608;  // most partial sums of dw
 
 // act(z) and its derivative
+template <typename T>
 __device__ __forceinline__ void gate(float z, int act, float& a, float& da) {
-  const float s = sigmoidf_(z);
+  const float s = sigmoid_as<T>(z);
   if (act == GDN_GATE_SILU) {
     a = z * s;
     da = s * (1.f + z * (1.f - s));
@@ -25,253 +29,423 @@ __device__ __forceinline__ void gate(float z, int act, float& a, float& da) {
   }
 }
 
-// L lanes (a power of two >= d / 8) per row of d values.
-template <typename T, int L>
-__global__ void __launch_bounds__(GN_NT)
-    k_gate_norm_fwd(long long nrow, int H, int d, int act, long long ldz, float eps,
-                    const T* __restrict__ o, const T* __restrict__ z,
-                    const float* __restrict__ w, T* __restrict__ y) {
-  const int c = (threadIdx.x % L) * 8;
-  const long long r = (long long)blockIdx.x * (GN_NT / L) + threadIdx.x / L;
-  const bool live = r < nrow && c < d;
-  float x[8] = {}, zz[8] = {}, ss = 0.f;
-  if (live) {
-    const long long t = r / H;
-    ld8(o + (size_t)r * d + c, x);
-    ld8(z + (size_t)t * ldz + (size_t)(r - t * H) * d + c, zz);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-  ss = lane_sum<L>(ss);
-  if (!live) return;
-  const float rr = 1.f / sqrtf(ss / (float)d + eps);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float a, da;
-    gate(zz[i], act, a, da);
-    x[i] = x[i] * rr * w[c + i] * a;
-  }
-  st8(y + (size_t)r * d + c, x);
+// z of (token t, head h), row r = t H + h.
+__device__ __forceinline__ size_t z_at(uint32_t r, const FastDiv& byH, int d, long long ldz) {
+  uint32_t t, h;
+  byH(r, t, h);
+  return (size_t)t * ldz + (size_t)h * d;
 }
 
+// L lanes (a power of two >= d / 8) per row of d values, GN_U rows per thread.
 template <typename T, int L>
 __global__ void __launch_bounds__(GN_NT)
-    k_gate_norm_bwd(long long nrow, int H, int d, int act, long long ldz, float eps,
-                    const T* __restrict__ o, const T* __restrict__ z,
+    k_gate_norm_fwd(uint32_t nrow, FastDiv byH, int d, float inv_d, int act, long long ldz,
+                    float eps, const T* __restrict__ o, const T* __restrict__ z,
+                    const float* __restrict__ w, T* __restrict__ y) {
+  constexpr int NG = GN_NT / L;
+  const int c = (threadIdx.x % L) * 8;
+  const uint32_t r0 = blockIdx.x * (NG * GN_U) + threadIdx.x / L;
+  Raw8<T> xr[GN_U], zr[GN_U];
+#pragma unroll
+  for (int u = 0; u < GN_U; ++u) {
+    const uint32_t r = r0 + u * NG;
+    xr[u] = zr[u] = Raw8<T>{};
+    if (r < nrow && c < d) {
+      xr[u] = ldraw8(o + (size_t)r * d + c);
+      zr[u] = ldraw8(z + z_at(r, byH, d, ldz) + c);
+    }
+  }
+  float wv[8] = {};
+  if (c < d) ld8(w + c, wv);
+#pragma unroll
+  for (int u = 0; u < GN_U; ++u) {
+    const uint32_t r = r0 + u * NG;
+    float x[8], zz[8], ss = 0.f;
+    cvt8(xr[u], x);
+    cvt8(zr[u], zz);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    ss = lane_sum<L>(ss);
+    const float rr = rsqrtf(fmaf(ss, inv_d, eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, da;
+      gate<T>(zz[i], act, a, da);
+      x[i] = x[i] * rr * (wv[i] * a);
+    }
+    if (r < nrow && c < d) st8(y + (size_t)r * d + c, x);
+  }
+}
+
+// Blocks take every gridDim.x-th group of rows; each thread keeps the dw of its
+// 8 columns, part[block] = the block's sum.
+template <typename T, int L>
+__global__ void __launch_bounds__(GN_NT)
+    k_gate_norm_bwd(uint32_t nrow, FastDiv byH, int d, float inv_d, int act, long long ldz,
+                    float eps, const T* __restrict__ o, const T* __restrict__ z,
                     const float* __restrict__ w, const T* __restrict__ dy, T* __restrict__ dout,
                     T* __restrict__ dz, float* __restrict__ part) {
-  __shared__ float red[GN_NT / L][L * 8];
+  constexpr int NG = GN_NT / L;
+  __shared__ float red[NG][L * 8];
   const int c = (threadIdx.x % L) * 8, gi = threadIdx.x / L;
-  const long long step = (long long)gridDim.x * (GN_NT / L);
   float acc[8] = {}, wv[8] = {};
   if (c < d) ld8(w + c, wv);
-  for (long long r0 = (long long)blockIdx.x * (GN_NT / L); r0 < nrow; r0 += step) {
-    const long long r = r0 + gi;
-    const bool live = r < nrow && c < d;
-    float x[8] = {}, zz[8] = {}, gy[8] = {}, ss = 0.f, sd = 0.f, a[8], da[8];
-    if (live) {
-      const long long t = r / H;
-      ld8(o + (size_t)r * d + c, x);
-      ld8(z + (size_t)t * ldz + (size_t)(r - t * H) * d + c, zz);
-      ld8(dy + (size_t)r * d + c, gy);
+  for (uint32_t b = blockIdx.x * (NG * GN_UB); b < nrow; b += gridDim.x * (NG * GN_UB)) {
+    Raw8<T> xr[GN_UB], zr[GN_UB], gr[GN_UB];
+#pragma unroll
+    for (int u = 0; u < GN_UB; ++u) {
+      const uint32_t r = b + u * NG + gi;
+      xr[u] = zr[u] = gr[u] = Raw8<T>{};
+      if (r < nrow && c < d) {
+        xr[u] = ldraw8(o + (size_t)r * d + c);
+        zr[u] = ldraw8(z + z_at(r, byH, d, ldz) + c);
+        gr[u] = ldraw8(dy + (size_t)r * d + c);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      gate(zz[i], act, a[i], da[i]);
-      ss = fmaf(x[i], x[i], ss);
-      sd = fmaf(gy[i] * a[i] * wv[i], x[i], sd);
-    }
-    ss = lane_sum<L>(ss);
-    sd = lane_sum<L>(sd);
-    const float rr = 1.f / sqrtf(ss / (float)d + eps), m = sd * rr / (float)d;
-    if (!live) continue;
-    float go[8], gz[8];
+    for (int u = 0; u < GN_UB; ++u) {
+      const uint32_t r = b + u * NG + gi;
+      float x[8], zz[8], gy[8], go[8], ss = 0.f, sd = 0.f;
+      cvt8(xr[u], x);
+      cvt8(zr[u], zz);
+      cvt8(gr[u], gy);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float n = x[i] * rr;
-      go[i] = rr * (gy[i] * a[i] * wv[i] - n * m);
-      gz[i] = gy[i] * n * wv[i] * da[i];
-      acc[i] = fmaf(gy[i] * a[i], n, acc[i]);
+      for (int i = 0; i < 8; ++i) {
+        float a, da;
+        gate<T>(zz[i], act, a, da);
+        zz[i] = gy[i] * (wv[i] * da);
+        gy[i] *= a;
+        go[i] = gy[i] * wv[i];
+        ss = fmaf(x[i], x[i], ss);
+        sd = fmaf(go[i], x[i], sd);
+      }
+      ss = lane_sum<L>(ss);
+      sd = lane_sum<L>(sd);
+      const float rr = rsqrtf(fmaf(ss, inv_d, eps)), m = sd * rr * inv_d;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = x[i] * rr;
+        go[i] = rr * fmaf(-n, m, go[i]);
+        zz[i] *= n;
+        acc[i] = fmaf(gy[i], n, acc[i]);
+      }
+      if (r < nrow && c < d) {
+        st8(dout + (size_t)r * d + c, go);
+        st8(dz + (size_t)r * d + c, zz);
+      }
     }
-    st8(dout + (size_t)r * d + c, go);
-    st8(dz + (size_t)r * d + c, gz);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) red[gi][c + i] = acc[i];
   __syncthreads();
   for (int i = threadIdx.x; i < d; i += GN_NT) {
     float a = 0.f;
-    for (int u = 0; u < GN_NT / L; ++u) a += red[u][i];
+    for (int u = 0; u < NG; ++u) a += red[u][i];
     part[(size_t)blockIdx.x * d + i] = a;
   }
 }
 
 // ------------------------------------------------------------ block boundary
-constexpr int RN_PARTS = 304;  // most partial sums of dw, dw_post, dscale
+// A team of threads works on one row, 8 columns per thread, so the parameters,
+// the row and (backward) the columns' running sums stay in registers. Rows
+// wider than RN_COLS are split over the CTAs of a cluster, which exchange their
+// sums through distributed shared memory. Each thread prefetches its own 8
+// columns of the team's next rows with cp.async into shared-memory slots that
+// only it reads: the loads of several rows stay in flight across the two
+// reductions of a row, without a barrier of their own.
+constexpr int RN_COLS = 4096;  // columns of a CTA: 512 threads
+constexpr int RN_SMS = 152;
 
-// Sums of K values over the block (every thread gets them).
-template <int K>
-__device__ __forceinline__ void block_sum(float* v, float* sm) {
-  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+struct Team {
+  int C, c;         // row width, this thread's first column
+  int rows, first, step;  // this team takes rows first, first + step, ..
+  bool on;          // the thread has columns
+};
+
+// Sums of K values over the team (and cluster); buf alternates between calls,
+// so one barrier separates a call's reads from the next but one's writes.
+template <int K, int CL>
+__device__ __forceinline__ void team_sum(float* v, float* red, int& buf) {
+  const int nt = blockDim.x, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int i = 0; i < K; ++i) v[i] = lane_sum<32>(v[i]);
-  __syncthreads();  // sm may still be read from the sum before
-  if ((threadIdx.x & 31) == 0)
+  if (CL == 1 && nt == 32) return;
+  float* slot = red + buf * (4 * CL * 16);  // [K][CL][16 warps], unused ones stay 0
+  buf ^= 1;
+  if (CL == 1) {
+    if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int i = 0; i < K; ++i) sm[warp * K + i] = v[i];
-  __syncthreads();
+      for (int i = 0; i < K; ++i) slot[i * 16 + warp] = v[i];
+    named_bar(threadIdx.y + 1, nt);
+  } else {
+    uint32_t rank;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    if ((threadIdx.x & 31) < CL) {  // lane p: into CTA p of the cluster
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"(smem_u32(slot + (i * CL + rank) * 16 + warp)),
+                       "r"(threadIdx.x & 31));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[i]) : "memory");
+      }
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
 #pragma unroll
   for (int i = 0; i < K; ++i) {
+    const float4* p = reinterpret_cast<const float4*>(slot + i * CL * 16);
     v[i] = 0.f;
-    for (int u = 0; u < nw; ++u) v[i] += sm[u * K + i];
+#pragma unroll
+    for (int u = 0; u < CL * 4; ++u) {
+      if (CL == 1 && u * 4 >= (nt >> 5)) break;
+      const float4 a = p[u];
+      v[i] += (a.x + a.y) + (a.z + a.w);
+    }
   }
 }
 
-// One block per row, NC 8-element pieces per thread.
-template <typename T, typename R, int NC>
-__global__ void __launch_bounds__(512)
-    k_res_norm_fwd(int C, float eps, const R* h, const T* __restrict__ x,
+template <int CL>
+__device__ __forceinline__ Team team_of(int rows, int C, float* red) {
+  Team t;
+  t.C = C;
+  t.rows = rows;
+  const int per = (C / 8 + CL - 1) / CL;  // column groups of a CTA
+  const int rank = CL == 1 ? 0 : blockIdx.x % CL;
+  t.c = (rank * per + threadIdx.x) * 8;
+  t.on = (int)threadIdx.x < per && t.c < C;
+  t.first = blockIdx.x / CL * blockDim.y + threadIdx.y;
+  t.step = gridDim.x / CL * blockDim.y;
+  if (CL > 1 || blockDim.x > 32) {
+    for (int i = threadIdx.x; i < 2 * 4 * CL * 16; i += blockDim.x) red[i] = 0.f;
+    if (CL == 1) {
+      named_bar(threadIdx.y + 1, blockDim.x);
+    } else {
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+  }
+  return t;
+}
+
+// Prefetch slots of a thread: slot k of stage s, 16 bytes each, consecutive
+// threads consecutive. E elements of 16-byte pieces per tensor.
+template <int SLOTS>
+struct Ring {
+  uint4* base;  // this thread's slot 0 of stage 0
+  int nt;
+  __device__ __forceinline__ uint4* at(int stage, int k) const {
+    return base + (size_t)(stage * SLOTS + k) * nt;
+  }
+  template <typename T>
+  __device__ __forceinline__ void fetch(int stage, int k, const T* p) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      cp16(at(stage, k + i), reinterpret_cast<const uint4*>(p) + i, true);
+  }
+  template <typename T>
+  __device__ __forceinline__ void read(int stage, int k, float* v) const {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = *at(stage, k + i);
+    cvt8(r, v);
+  }
+};
+
+template <typename T>
+constexpr int pieces() { return (int)sizeof(T) / 2; }  // 16-byte pieces of 8 elements
+template <typename T, typename R>
+constexpr int fwd_slots() { return pieces<R>() + pieces<T>(); }
+template <typename T, typename R>
+constexpr int fwd_stages() { return fwd_slots<T, R>() == 2 ? 4 : 3; }
+template <typename T, typename R>
+constexpr int bwd_slots() { return 2 * pieces<R>() + 2 * pieces<T>(); }
+template <typename T, typename R>
+constexpr int bwd_stages() { return bwd_slots<T, R>() == 4 ? 4 : 3; }
+
+__device__ __forceinline__ void ld8_or(const float* p, bool have, float other, float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = other;
+  if (have) ld8(p, v);
+}
+
+template <typename T, typename R, int CL>
+__global__ void __launch_bounds__(512, 2)
+    k_res_norm_fwd(int rows, int C, float inv_C, float eps, const R* h, const T* __restrict__ x,
                    const float* __restrict__ w, const float* __restrict__ w_post,
                    const float* __restrict__ scale, R* h_out, T* __restrict__ y) {
-  __shared__ float sm[16];
-  const size_t base = (size_t)blockIdx.x * C;
-  float hv[NC][8] = {}, xv[NC][8] = {};
-#pragma unroll
-  for (int n = 0; n < NC; ++n) {
-    const int c = (n * blockDim.x + threadIdx.x) * 8;
-    if (c < C) {
-      ld8(h + base + c, hv[n]);
-      if (x) ld8(x + base + c, xv[n]);
+  constexpr int S = fwd_stages<T, R>(), KX = pieces<R>();
+  extern __shared__ uint4 smem[];
+  __shared__ float red_all[16 * 2 * 4 * 16];
+  float* red = red_all + threadIdx.y * (2 * 4 * 16);
+  const int nt = blockDim.x * blockDim.y;
+  Ring<fwd_slots<T, R>()> ring = {smem + threadIdx.y * blockDim.x + threadIdx.x, nt};
+  const Team t = team_of<CL>(rows, C, red);
+  auto fetch = [&](int stage, int row) {
+    if (t.on && row < t.rows) {
+      const size_t at = (size_t)row * C + t.c;
+      ring.template fetch<R>(stage, 0, h + at);
+      if (x) ring.template fetch<T>(stage, KX, x + at);
     }
-  }
-  if (w_post) {
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
+  float wv[8], pv[8], sv[8];
+  ld8_or(w + t.c, t.on, 0.f, wv);
+  ld8_or(w_post + t.c, t.on && w_post, 1.f, pv);
+  ld8_or(scale + t.c, t.on && scale, 1.f, sv);
+  int stage = 0, buf = 0;
+  for (int row = t.first; row < t.rows; row += t.step) {
+    cp_wait<S - 1>();
+    float hv[8] = {}, xv[8] = {};
+    if (t.on) {
+      ring.template read<R>(stage, 0, hv);
+      if (x) ring.template read<T>(stage, KX, xv);
+    }
+    const size_t at = (size_t)row * C + t.c;
+    if (w_post) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(xv[i], xv[i], s);
+      team_sum<1, CL>(&s, red, buf);
+      const float rx = rsqrtf(fmaf(s, inv_C, eps));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xv[i] *= rx * pv[i];
+    }
     float s = 0.f;
 #pragma unroll
-    for (int n = 0; n < NC; ++n)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(xv[n][i], xv[n][i], s);
-    block_sum<1>(&s, sm);
-    const float rx = 1.f / sqrtf(s / (float)C + eps);
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      const int c = (n * blockDim.x + threadIdx.x) * 8;
-      if (c < C)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) xv[n][i] *= rx * w_post[c + i];
+    for (int i = 0; i < 8; ++i) {
+      hv[i] = fmaf(sv[i], xv[i], hv[i]);
+      s = fmaf(hv[i], hv[i], s);
     }
+    if (h_out && t.on) st8(h_out + at, hv);
+    fetch(stage, row + S * t.step);  // the slot has been read
+    if (++stage == S) stage = 0;
+    team_sum<1, CL>(&s, red, buf);
+    const float r = rsqrtf(fmaf(s, inv_C, eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hv[i] *= r * wv[i];
+    if (t.on) st8(y + at, hv);
   }
-  float s = 0.f;
-#pragma unroll
-  for (int n = 0; n < NC; ++n) {
-    const int c = (n * blockDim.x + threadIdx.x) * 8;
-    if (c < C) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        hv[n][i] = scale ? fmaf(scale[c + i], xv[n][i], hv[n][i]) : hv[n][i] + xv[n][i];
-        s = fmaf(hv[n][i], hv[n][i], s);
-      }
-      if (h_out) st8(h_out + base + c, hv[n]);
-    }
-  }
-  block_sum<1>(&s, sm);
-  const float r = 1.f / sqrtf(s / (float)C + eps);
-#pragma unroll
-  for (int n = 0; n < NC; ++n) {
-    const int c = (n * blockDim.x + threadIdx.x) * 8;
-    if (c < C) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) hv[n][i] *= r * w[c + i];
-      st8(y + base + c, hv[n]);
-    }
-  }
+  cp_wait<0>();
 }
 
-// Each block takes every gridDim.x-th row; its sums of dw, dw_post and dscale
-// stay in shared memory, every column owned by one thread.
-template <typename T, typename R, int NC>
-__global__ void __launch_bounds__(512)
-    k_res_norm_bwd(int rows, int C, float eps, const R* __restrict__ h, const T* __restrict__ x,
-                   const float* __restrict__ w, const float* __restrict__ w_post,
-                   const float* __restrict__ scale, const T* __restrict__ dy, const R* dh_out,
-                   R* dh, T* __restrict__ dx, int want, float* __restrict__ part) {
-  extern __shared__ float acc[];  // [3][C]
-  __shared__ float sm[48];
-  const int wpost = want & 1, wscale = want & 2;
-  for (int i = threadIdx.x; i < 3 * C; i += blockDim.x) acc[i] = 0.f;
-  __syncthreads();
-  const float inv = 1.f / (float)C;
-  for (int row = blockIdx.x; row < rows; row += gridDim.x) {
-    const size_t base = (size_t)row * C;
-    float hv[NC][8] = {}, gv[NC][8] = {}, xv[NC][8] = {}, dv[NC][8] = {};
-    float s[3] = {};
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      const int c = (n * blockDim.x + threadIdx.x) * 8;
-      if (c < C) {
-        ld8(h + base + c, hv[n]);
-        ld8(dy + base + c, gv[n]);
-        if (wpost || wscale) ld8(x + base + c, xv[n]);
-        if (dh_out) ld8(dh_out + base + c, dv[n]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[0] = fmaf(hv[n][i], hv[n][i], s[0]);
-          s[1] = fmaf(gv[n][i] * w[c + i], hv[n][i], s[1]);
-          s[2] = fmaf(xv[n][i], xv[n][i], s[2]);
-        }
-      }
+// part [blocks][1 + (w_post) + (scale)][C]: the blocks' sums of dw, dw_post, dscale.
+template <typename T, typename R, int CL>
+__global__ void __launch_bounds__(512, 1)
+    k_res_norm_bwd(int rows, int C, float inv_C, float eps, const R* __restrict__ h,
+                   const T* __restrict__ x, const float* __restrict__ w,
+                   const float* __restrict__ w_post, const float* __restrict__ scale,
+                   const T* __restrict__ dy, const R* dh_out, R* dh, T* __restrict__ dx,
+                   float* __restrict__ part) {
+  constexpr int S = bwd_stages<T, R>(), KD = pieces<R>(), KG = 2 * pieces<R>(),
+                KX = KG + pieces<T>();
+  extern __shared__ uint4 smem[];
+  __shared__ float red_all[16 * 2 * 4 * 16];
+  float* red = red_all + threadIdx.y * (2 * 4 * 16);
+  const int nt = blockDim.x * blockDim.y;
+  Ring<bwd_slots<T, R>()> ring = {smem + threadIdx.y * blockDim.x + threadIdx.x, nt};
+  const Team t = team_of<CL>(rows, C, red);
+  const bool with_x = w_post || scale;
+  auto fetch = [&](int stage, int row) {
+    if (t.on && row < t.rows) {
+      const size_t at = (size_t)row * C + t.c;
+      ring.template fetch<R>(stage, 0, h + at);
+      if (dh_out) ring.template fetch<R>(stage, KD, dh_out + at);
+      ring.template fetch<T>(stage, KG, dy + at);
+      if (with_x) ring.template fetch<T>(stage, KX, x + at);
     }
-    block_sum<3>(s, sm);
-    const float r = 1.f / sqrtf(s[0] * inv + eps), m = r * s[1] * inv;
-    const float rx = wpost ? 1.f / sqrtf(s[2] * inv + eps) : 1.f;
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
+  float wv[8], pv[8], sv[8], aw[8] = {}, ap[8] = {}, as[8] = {};
+  ld8_or(w + t.c, t.on, 0.f, wv);
+  ld8_or(w_post + t.c, t.on && w_post, 1.f, pv);
+  ld8_or(scale + t.c, t.on && scale, 1.f, sv);
+  int stage = 0, buf = 0;
+  for (int row = t.first; row < t.rows; row += t.step) {
+    cp_wait<S - 1>();
+    float hv[8] = {}, gv[8] = {}, xv[8] = {}, dv[8] = {}, s[3] = {};
+    if (t.on) {
+      ring.template read<R>(stage, 0, hv);
+      if (dh_out) ring.template read<R>(stage, KD, dv);
+      ring.template read<T>(stage, KG, gv);
+      if (with_x) ring.template read<T>(stage, KX, xv);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[0] = fmaf(hv[i], hv[i], s[0]);
+      s[1] = fmaf(gv[i] * wv[i], hv[i], s[1]);
+      s[2] = fmaf(xv[i], xv[i], s[2]);
+    }
+    fetch(stage, row + S * t.step);  // the slot has been read
+    if (++stage == S) stage = 0;
+    team_sum<3, CL>(s, red, buf);
+    const size_t at = (size_t)row * C + t.c;
+    const float r = rsqrtf(fmaf(s[0], inv_C, eps)), m = r * s[1] * inv_C;
+    const float rx = w_post ? rsqrtf(fmaf(s[2], inv_C, eps)) : 1.f;
     float e = 0.f;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      const int c = (n * blockDim.x + threadIdx.x) * 8;
-      if (c < C) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float nn = hv[n][i] * r;
-          acc[c + i] += gv[n][i] * nn;
-          dv[n][i] += r * (gv[n][i] * w[c + i] - nn * m);  // dh'
-          xv[n][i] *= rx;
-        }
-        st8(dh + base + c, dv[n]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float dp = dv[n][i];
-          if (wscale) {
-            acc[2 * C + c + i] += dp * (wpost ? xv[n][i] * w_post[c + i] : xv[n][i]);
-            dp *= scale[c + i];
-          }
-          if (wpost) {
-            acc[C + c + i] += dp * xv[n][i];
-            dp *= w_post[c + i];
-            e = fmaf(dp, xv[n][i], e);
-          }
-          dv[n][i] = dp;
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float n = hv[i] * r;
+      aw[i] = fmaf(gv[i], n, aw[i]);
+      dv[i] = fmaf(r, fmaf(-n, m, gv[i] * wv[i]), dv[i]);  // dh
+      xv[i] *= rx;
     }
-    if (wpost) {
-      block_sum<1>(&e, sm);
-      e *= inv;
-    }
-    if (dx) {
+    if (t.on) st8(dh + at, dv);
 #pragma unroll
-      for (int n = 0; n < NC; ++n) {
-        const int c = (n * blockDim.x + threadIdx.x) * 8;
-        if (c < C) {
-          if (wpost)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dv[n][i] = rx * (dv[n][i] - xv[n][i] * e);
-          st8(dx + base + c, dv[n]);
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      as[i] = fmaf(dv[i], xv[i] * pv[i], as[i]);
+      dv[i] *= sv[i];
+      ap[i] = fmaf(dv[i], xv[i], ap[i]);
+      dv[i] *= pv[i];
+      e = fmaf(dv[i], xv[i], e);
     }
+    if (w_post) {
+      team_sum<1, CL>(&e, red, buf);
+      e *= inv_C;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dv[i] = rx * fmaf(-xv[i], e, dv[i]);
+    }
+    if (dx && t.on) st8(dx + at, dv);
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 3 * C; i += blockDim.x)
-    part[(size_t)blockIdx.x * 3 * C + i] = acc[i];
+  cp_wait<0>();
+  // the block's sums: teams joined through shared memory (the ring is drained)
+  float* join = reinterpret_cast<float*>(smem);  // [teams][blockDim.x * 8]
+  const int narr = 1 + (w_post != nullptr) + (scale != nullptr);
+  float* out = part + (size_t)(blockIdx.x / CL) * narr * C;
+  for (int a = 0; a < 3; ++a) {
+    if ((a == 1 && !w_post) || (a == 2 && !scale)) continue;
+    if (blockDim.y > 1) {
+      __syncthreads();
+      float* mine = join + (size_t)(threadIdx.y * blockDim.x + threadIdx.x) * 8;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = a == 0 ? aw[i] : a == 1 ? ap[i] : as[i];
+      st8(mine, v);
+      __syncthreads();
+      if (threadIdx.y == 0 && t.on) {
+        for (int u = 1; u < (int)blockDim.y; ++u) {
+          float o[8];
+          ld8(mine + (size_t)u * blockDim.x * 8, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += o[i];
+        }
+        st8(out + t.c, v);
+      }
+    } else if (t.on) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = a == 0 ? aw[i] : a == 1 ? ap[i] : as[i];
+      st8(out + t.c, v);
+    }
+    out += C;
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -280,7 +454,7 @@ gdn_status check_gate(const gdn_gate_norm_shape* s) {
   if (s->act != GDN_GATE_SILU && s->act != GDN_GATE_SIGMOID) return GDN_ERR_INVALID_ARG;
   if (!dtype_ok(s->dtype) || s->d % 8 || s->d > 256 || s->H > (1 << 16))
     return GDN_ERR_UNSUPPORTED;
-  if ((long long)s->rows * s->H >= (1ll << 32)) return GDN_ERR_UNSUPPORTED;
+  if ((long long)s->rows * s->H >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 int lanes_of(int d) {
@@ -289,19 +463,21 @@ int lanes_of(int d) {
   return L;
 }
 int gate_parts(const gdn_gate_norm_shape& s) {
-  const long long g = GN_NT / lanes_of(s.d), n = (long long)s.rows * s.H;
+  const long long g = GN_NT / lanes_of(s.d) * GN_UB, n = (long long)s.rows * s.H;
   return (int)std::min<long long>(GN_PARTS, (n + g - 1) / g);
 }
 
 template <typename T, int L>
 void launch_gate(const gdn_gate_norm_shape& s, const void* o, const void* z, const float* w,
                  const void* dy, void* out, void* dz, float* part, cudaStream_t st) {
-  const long long n = (long long)s.rows * s.H;
+  const uint32_t n = (uint32_t)s.rows * (uint32_t)s.H, per = GN_NT / L * GN_U;
+  const FastDiv byH(s.H);
+  const float inv = 1.f / (float)s.d;
   if (!dy)
-    k_gate_norm_fwd<T, L><<<(unsigned)((n + GN_NT / L - 1) / (GN_NT / L)), GN_NT, 0, st>>>(
-        n, s.H, s.d, s.act, s.ldz, s.eps, (const T*)o, (const T*)z, w, (T*)out);
+    k_gate_norm_fwd<T, L><<<(n + per - 1) / per, GN_NT, 0, st>>>(
+        n, byH, s.d, inv, s.act, s.ldz, s.eps, (const T*)o, (const T*)z, w, (T*)out);
   else
-    k_gate_norm_bwd<T, L><<<gate_parts(s), GN_NT, 0, st>>>(n, s.H, s.d, s.act, s.ldz, s.eps,
+    k_gate_norm_bwd<T, L><<<gate_parts(s), GN_NT, 0, st>>>(n, byH, s.d, inv, s.act, s.ldz, s.eps,
                                                            (const T*)o, (const T*)z, w,
                                                            (const T*)dy, (T*)out, (T*)dz, part);
 }
@@ -325,8 +501,28 @@ gdn_status check_res(const gdn_res_norm_shape* s) {
   if (s->res_dtype != s->dtype && s->res_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
-int res_parts(const gdn_res_norm_shape& s) { return std::min(RN_PARTS, s.rows); }
-int res_threads(int C, int nc) { return (C / 8 + 32 * nc - 1) / (32 * nc) * 32; }
+
+// How a call's rows are laid out over CTAs; a function of the shape alone, so
+// the order of the parameter gradients' sums is too.
+struct ResPlan {
+  int cl, team, teams;  // CTAs per row, threads of a CTA per row, rows per CTA
+  int blocks(int rows, int threads) const {  // CTAs, so that each SM has up to `threads`
+    const int all = (rows + teams - 1) / teams;
+    return cl * std::min(all, std::max(1, RN_SMS * (threads / (team * teams)) / cl));
+  }
+};
+ResPlan res_plan(int C) {
+  ResPlan p;
+  p.cl = C <= RN_COLS ? 1 : C <= 2 * RN_COLS ? 2 : 4;
+  const int groups = (C / 8 + p.cl - 1) / p.cl;
+  p.team = (groups + 31) / 32 * 32;
+  p.teams = p.team >= 256 || p.cl > 1 ? 1 : 256 / p.team;
+  return p;
+}
+int res_parts(const gdn_res_norm_shape& s) {
+  const ResPlan p = res_plan(s.C);
+  return p.blocks(s.rows, 512) / p.cl;
+}
 
 struct ResArgs {
   const void *h, *x, *dy, *dh_out;
@@ -334,28 +530,48 @@ struct ResArgs {
   void *ho, *y;  // forward: h_out, y; backward: dh, dx
   float* part;
 };
-template <typename T, typename R, int NC>
-cudaError_t launch_res(const gdn_res_norm_shape& s, const ResArgs& a, cudaStream_t st) {
-  const int nt = res_threads(s.C, NC);
-  if (!a.dy) {
-    k_res_norm_fwd<T, R, NC><<<s.rows, nt, 0, st>>>(s.C, s.eps, (const R*)a.h, (const T*)a.x, a.w,
-                                                    a.w_post, a.scale, (R*)a.ho, (T*)a.y);
-    return cudaGetLastError();
-  }
-  const int smem = 3 * s.C * (int)sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(k_res_norm_bwd<T, R, NC>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename K, typename... A>
+cudaError_t launch_rows(K kernel, const ResPlan& p, int blocks, int smem, cudaStream_t st,
+                        A... args) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e) return e;
-  k_res_norm_bwd<T, R, NC><<<res_parts(s), nt, smem, st>>>(
-      s.rows, s.C, s.eps, (const R*)a.h, (const T*)a.x, a.w, a.w_post, a.scale, (const T*)a.dy,
-      (const R*)a.dh_out, (R*)a.ho, (T*)a.y, (a.w_post ? 1 : 0) | (a.scale ? 2 : 0), a.part);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(p.team, p.teams);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = p.cl;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.cl > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename T, typename R, int CL>
+cudaError_t launch_res(const gdn_res_norm_shape& s, const ResArgs& a, const ResPlan& p,
+                       cudaStream_t st) {
+  const int nt = p.team * p.teams;
+  const float inv = 1.f / (float)s.C;
+  if (!a.dy)
+    return launch_rows(k_res_norm_fwd<T, R, CL>, p, p.blocks(s.rows, 1024),
+                       nt * 16 * fwd_slots<T, R>() * fwd_stages<T, R>(), st, s.rows, s.C, inv,
+                       s.eps, (const R*)a.h, (const T*)a.x, a.w, a.w_post, a.scale, (R*)a.ho,
+                       (T*)a.y);
+  return launch_rows(k_res_norm_bwd<T, R, CL>, p, p.blocks(s.rows, 512),
+                     nt * 16 * bwd_slots<T, R>() * bwd_stages<T, R>(), st, s.rows, s.C, inv,
+                     s.eps, (const R*)a.h, (const T*)a.x, a.w, a.w_post, a.scale,
+                     (const T*)a.dy, (const R*)a.dh_out, (R*)a.ho, (T*)a.y, a.part);
 }
 template <typename T, typename R>
 cudaError_t dispatch_res(const gdn_res_norm_shape& s, const ResArgs& a, cudaStream_t st) {
-  if (s.C <= 4096) return launch_res<T, R, 1>(s, a, st);
-  if (s.C <= 8192) return launch_res<T, R, 2>(s, a, st);
-  return launch_res<T, R, 4>(s, a, st);
+  const ResPlan p = res_plan(s.C);
+  switch (p.cl) {
+    case 1: return launch_res<T, R, 1>(s, a, p, st);
+    case 2: return launch_res<T, R, 2>(s, a, p, st);
+    default: return launch_res<T, R, 4>(s, a, p, st);
+  }
 }
 cudaError_t run_res(const gdn_res_norm_shape& s, const ResArgs& a, cudaStream_t st) {
   if (s.dtype == GDN_DTYPE_F32) return dispatch_res<float, float>(s, a, st);
@@ -479,7 +695,9 @@ gdn_status gdn_res_norm_bwd(const gdn_res_norm_shape* shape, const void* h_out, 
     const ResArgs a = {h_out, x, dy, dh_out, w, w_post, scale, dh, dx, part};
     if (run_res(s, a, st)) return GDN_ERR_CUDA;
   }
-  const cudaError_t ce = col_sum(part, res_parts(s), 3 * s.C, s.C, dw, dw_post, dscale, st);
+  const int narr = 1 + (w_post != nullptr) + (scale != nullptr);
+  const cudaError_t ce = col_sum(part, res_parts(s), narr * s.C, s.C, dw,
+                                 w_post ? dw_post : dscale, dscale, st);
   prof_mark(st, nullptr);
   return ce ? GDN_ERR_CUDA : GDN_OK;
 }

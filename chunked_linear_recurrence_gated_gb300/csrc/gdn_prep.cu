@@ -12,139 +12,215 @@ namespace gdn {
 namespace {
 
 constexpr int PR_NT = 256;     // threads of a block
+constexpr int PR_U = 4;        // rows a thread has in flight (forward)
+constexpr int PR_UB = 2;       // rows a thread has in flight (backward)
+constexpr int PR_G = 4;        // value heads' gradients loaded together (backward)
 constexpr int PR_PARTS = 304;  // most partial sums of drate / dbias
 
-// q / k rows: DK / 8 lanes per (token, q or k, key head). Blocks past
+// Row r of the 2 Hk (q heads, then k heads) rows of each token.
+struct HeadRow {
+  uint32_t t;
+  int hk;
+  bool is_k;
+};
+__device__ __forceinline__ HeadRow head_row(uint32_t r, const FastDiv& by2Hk, int Hk) {
+  HeadRow h;
+  uint32_t j;
+  by2Hk(r, h.t, j);
+  h.is_k = (int)j >= Hk;
+  h.hk = (int)j - (h.is_k ? Hk : 0);
+  return h;
+}
+
+// q / k rows: DK / 8 lanes per row, PR_U rows per thread. Blocks past
 // row_blocks: one thread per (token, value head) of the gates.
 template <typename T, int DK>
 __global__ void __launch_bounds__(PR_NT)
-    k_prep_fwd(int rows, int H, int Hk, int row_blocks, long long ldq, long long ldk,
-               long long ldg, long long ldb, float q_scale, float eps, const T* __restrict__ q,
-               const T* __restrict__ k, const T* __restrict__ xg, const T* __restrict__ xb,
-               const float* __restrict__ rate, const float* __restrict__ bias, T* __restrict__ qn,
-               T* __restrict__ kn, T* __restrict__ g, T* __restrict__ beta) {
+    k_prep_fwd(uint32_t nrow, uint32_t ngate, FastDiv by2Hk, FastDiv byH, int G, int row_blocks,
+               long long ldq, long long ldk, long long ldg, long long ldb, float q_scale,
+               float eps, const T* __restrict__ q, const T* __restrict__ k,
+               const T* __restrict__ xg, const T* __restrict__ xb, const float* __restrict__ rate,
+               const float* __restrict__ bias, T* __restrict__ qn, T* __restrict__ kn,
+               T* __restrict__ g, T* __restrict__ beta) {
+  const int H = (int)byH.d, Hk = (int)by2Hk.d / 2;
   if ((int)blockIdx.x >= row_blocks) {
-    const long long i = (long long)(blockIdx.x - row_blocks) * PR_NT + threadIdx.x;
-    if (i >= (long long)rows * H) return;
-    const long long t = i / H;
-    const int h = (int)(i - t * H);
-    stf(g + i, -expf(rate[h]) * softplusf_(ldf(xg + t * ldg + h) + bias[h]));
-    stf(beta + i, sigmoidf_(ldf(xb + t * ldb + h)));
+    const uint32_t i = (blockIdx.x - row_blocks) * PR_NT + threadIdx.x;
+    if (i >= ngate) return;
+    uint32_t t, h;
+    byH(i, t, h);
+    stf(g + i, -expf(rate[h]) * softplusf_(ldf(xg + (size_t)t * ldg + h) + bias[h]));
+    stf(beta + i, sigmoidf_(ldf(xb + (size_t)t * ldb + h)));
     return;
   }
-  constexpr int L = DK / 8;
-  const int lane = threadIdx.x % L, G = H / Hk;
-  const long long r = (long long)blockIdx.x * (PR_NT / L) + threadIdx.x / L;
-  const bool live = r < (long long)rows * 2 * Hk;
-  const long long t = live ? r / (2 * Hk) : 0;
-  const int j = live ? (int)(r - t * 2 * Hk) : 0, is_k = j >= Hk, hk = j - is_k * Hk;
-  float x[8];
-  ld8((is_k ? k + t * ldk : q + t * ldq) + (size_t)hk * DK + lane * 8, x);
-  float ss = 0.f;
+  constexpr int L = DK / 8, NG = PR_NT / L;
+  const int c = threadIdx.x % L * 8;
+  const uint32_t r0 = blockIdx.x * (NG * PR_U) + threadIdx.x / L;
+  Raw8<T> raw[PR_U];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-  ss = lane_sum<L>(ss);
-  const float s = (is_k ? 1.f : q_scale) / sqrtf(ss + eps);
+  for (int u = 0; u < PR_U; ++u) {
+    const uint32_t r = r0 + u * NG;
+    raw[u] = Raw8<T>{};
+    if (r < nrow) {
+      const HeadRow h = head_row(r, by2Hk, Hk);
+      raw[u] = ldraw8((h.is_k ? k + h.t * ldk : q + h.t * ldq) + (size_t)h.hk * DK + c);
+    }
+  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] *= s;
-  if (!live) return;
-  T* out = (is_k ? kn : qn) + ((size_t)t * H + (size_t)hk * G) * DK + lane * 8;
-  for (int i = 0; i < G; ++i) st8(out + (size_t)i * DK, x);
+  for (int u = 0; u < PR_U; ++u) {
+    const uint32_t r = r0 + u * NG;
+    float x[8], ss = 0.f;
+    cvt8(raw[u], x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    ss = lane_sum<L>(ss);
+    if (r >= nrow) continue;
+    const HeadRow h = head_row(r, by2Hk, Hk);
+    const float s = (h.is_k ? 1.f : q_scale) * rsqrtf(ss + eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= s;
+    T* out = (h.is_k ? kn : qn) + ((size_t)h.t * H + (size_t)h.hk * G) * DK + c;
+    for (int i = 0; i < G; ++i) st8(out + (size_t)i * DK, x);
+  }
 }
 
-template <typename T, int DK>
-__global__ void __launch_bounds__(PR_NT)
-    k_prep_bwd(int rows, int H, int Hk, long long ldq, long long ldk, float q_scale, float eps,
-               const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ dqn,
-               const T* __restrict__ dkn, T* __restrict__ dq, T* __restrict__ dk) {
-  constexpr int L = DK / 8;
-  const int lane = threadIdx.x % L, G = H / Hk;
-  const long long r = (long long)blockIdx.x * (PR_NT / L) + threadIdx.x / L;
-  const bool live = r < (long long)rows * 2 * Hk;
-  const long long t = live ? r / (2 * Hk) : 0;
-  const int j = live ? (int)(r - t * 2 * Hk) : 0, is_k = j >= Hk, hk = j - is_k * Hk;
-  float x[8], d[8] = {};
-  ld8((is_k ? k + t * ldk : q + t * ldq) + (size_t)hk * DK + lane * 8, x);
-  const T* dp = (is_k ? dkn : dqn) + ((size_t)t * H + (size_t)hk * G) * DK + lane * 8;
-  for (int i = 0; i < G; ++i) {
-    float e[8];
-    ld8(dp + (size_t)i * DK, e);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) d[u] += e[u];
-  }
-  float ss = 0.f, xd = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    ss = fmaf(x[i], x[i], ss);
-    xd = fmaf(x[i], d[i], xd);
-  }
-  ss = lane_sum<L>(ss);
-  xd = lane_sum<L>(xd);
-  const float rr = 1.f / sqrtf(ss + eps), c = (is_k ? 1.f : q_scale) * rr, m = rr * rr * xd;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) d[i] = c * (d[i] - x[i] * m);
-  if (live) st8((is_k ? dk : dq) + ((size_t)t * Hk + hk) * DK + lane * 8, d);
-}
-
-// Gates: block = a run of tokens, 32 heads at a time (lane = head, 8 tokens in
-// parallel); part[block] = its sums of drate [H] and dbias [H].
+// The gates of a run of tokens, HP heads (a power of two <= 32) at a time, the
+// block's other thread dimension over tokens; part[block] = its sums of
+// drate [H] and dbias [H].
 template <typename T>
-__global__ void __launch_bounds__(PR_NT)
-    k_prep_bwd_gates(int rows, int H, int per, long long ldg, long long ldb,
-                     const T* __restrict__ xg, const T* __restrict__ xb,
-                     const float* __restrict__ rate, const float* __restrict__ bias,
-                     const T* __restrict__ dg, const T* __restrict__ dbeta, T* __restrict__ dxg,
-                     T* __restrict__ dxb, float* __restrict__ part) {
-  __shared__ float red[2][8][32];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const long long t0 = (long long)blockIdx.x * per, t1 = min(t0 + per, (long long)rows);
-  for (int h0 = 0; h0 < H; h0 += 32) {
+__device__ __forceinline__ void prep_bwd_gates(int blk, int rows, int H, int hp_log, int per,
+                                               long long ldg, long long ldb, const T* xg,
+                                               const T* xb, const float* rate, const float* bias,
+                                               const T* dg, const T* dbeta, T* dxg, T* dxb,
+                                               float* part) {
+  __shared__ float red[2][PR_NT];
+  const int hp = 1 << hp_log, tx = threadIdx.x & (hp - 1), ty = threadIdx.x >> hp_log;
+  const int ny = PR_NT >> hp_log;
+  const int t0 = blk * per, t1 = min(t0 + per, rows);
+  for (int h0 = 0; h0 < H; h0 += hp) {
     const int h = h0 + tx;
     float sr = 0.f, sb = 0.f;
     if (h < H) {
       const float er = expf(rate[h]), bi = bias[h];
-      for (long long t = t0 + ty; t < t1; t += 8) {
-        const float x = ldf(xg + t * ldg + h) + bi, d = ldf(dg + t * H + h);
+#pragma unroll 2
+      for (int t = t0 + ty; t < t1; t += ny) {
+        const size_t at = (size_t)t * H + h;
+        const float x = ldf(xg + (size_t)t * ldg + h) + bi, d = ldf(dg + at);
+        const float b = sigmoidf_(ldf(xb + (size_t)t * ldb + h)), db = ldf(dbeta + at);
         const float dx = -d * er * sigmoidf_(x);
         sr = fmaf(d, -er * softplusf_(x), sr);
         sb += dx;
-        stf(dxg + t * H + h, dx);
-        const float b = sigmoidf_(ldf(xb + t * ldb + h));
-        stf(dxb + t * H + h, ldf(dbeta + t * H + h) * b * (1.f - b));
+        stf(dxg + at, dx);
+        stf(dxb + at, db * b * (1.f - b));
       }
     }
-    red[0][ty][tx] = sr;
-    red[1][ty][tx] = sb;
+    red[0][threadIdx.x] = sr;
+    red[1][threadIdx.x] = sb;
     __syncthreads();
     if (ty < 2 && h < H) {
       float a = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a += red[ty][i][tx];
-      part[((size_t)blockIdx.x * 2 + ty) * H + h] = a;
+      for (int i = 0; i < ny; ++i) a += red[ty][(i << hp_log) + tx];
+      part[((size_t)blk * 2 + ty) * H + h] = a;
     }
     __syncthreads();
   }
 }
 
-__global__ void __launch_bounds__(256)
+// The first gate_blocks blocks take the gates (their loops over tokens are the
+// longest), the others rows as k_prep_fwd.
+template <typename T, int DK>
+__global__ void __launch_bounds__(PR_NT)
+    k_prep_bwd(uint32_t nrow, FastDiv by2Hk, int G, int gate_blocks, int rows, int H, int hp_log,
+               int per, long long ldq, long long ldk, long long ldg, long long ldb, float q_scale,
+               float eps, const T* __restrict__ q, const T* __restrict__ k,
+               const T* __restrict__ xg, const T* __restrict__ xb, const float* __restrict__ rate,
+               const float* __restrict__ bias, const T* __restrict__ dqn,
+               const T* __restrict__ dkn, const T* __restrict__ dg, const T* __restrict__ dbeta,
+               T* __restrict__ dq, T* __restrict__ dk, T* __restrict__ dxg, T* __restrict__ dxb,
+               float* __restrict__ part) {
+  if ((int)blockIdx.x < gate_blocks) {
+    prep_bwd_gates<T>(blockIdx.x, rows, H, hp_log, per, ldg, ldb, xg, xb, rate, bias, dg, dbeta,
+                      dxg, dxb, part);
+    return;
+  }
+  constexpr int L = DK / 8, NG = PR_NT / L;
+  const int c = threadIdx.x % L * 8, Hk = (int)by2Hk.d / 2;
+  const uint32_t r0 = (blockIdx.x - gate_blocks) * (NG * PR_UB) + threadIdx.x / L;
+  float d[PR_UB][8] = {};
+  Raw8<T> xr[PR_UB];
+  const T* src[PR_UB];
+#pragma unroll
+  for (int u = 0; u < PR_UB; ++u) {
+    const uint32_t r = r0 + u * NG;
+    xr[u] = Raw8<T>{};
+    src[u] = nullptr;
+    if (r < nrow) {
+      const HeadRow h = head_row(r, by2Hk, Hk);
+      xr[u] = ldraw8((h.is_k ? k + h.t * ldk : q + h.t * ldq) + (size_t)h.hk * DK + c);
+      src[u] = (h.is_k ? dkn : dqn) + ((size_t)h.t * H + (size_t)h.hk * G) * DK + c;
+    }
+  }
+  for (int i0 = 0; i0 < G; i0 += PR_G) {
+    Raw8<T> e[PR_UB][PR_G];
+#pragma unroll
+    for (int u = 0; u < PR_UB; ++u)
+#pragma unroll
+      for (int i = 0; i < PR_G; ++i) {
+        e[u][i] = Raw8<T>{};
+        if (src[u] && i0 + i < G) e[u][i] = ldraw8(src[u] + (size_t)(i0 + i) * DK);
+      }
+#pragma unroll
+    for (int u = 0; u < PR_UB; ++u)
+#pragma unroll
+      for (int i = 0; i < PR_G; ++i) {
+        if (i0 + i >= G) break;
+        float v[8];
+        cvt8(e[u][i], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[u][j] += v[j];
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < PR_UB; ++u) {
+    const uint32_t r = r0 + u * NG;
+    float x[8], ss = 0.f, xd = 0.f;
+    cvt8(xr[u], x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ss = fmaf(x[i], x[i], ss);
+      xd = fmaf(x[i], d[u][i], xd);
+    }
+    ss = lane_sum<L>(ss);
+    xd = lane_sum<L>(xd);
+    if (r >= nrow) continue;
+    const HeadRow h = head_row(r, by2Hk, Hk);
+    const float rr = rsqrtf(ss + eps), s = (h.is_k ? 1.f : q_scale) * rr, m = rr * rr * xd;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[u][i] = s * fmaf(-x[i], m, d[u][i]);
+    st8((h.is_k ? dk : dq) + ((size_t)h.t * Hk + h.hk) * DK + c, d[u]);
+  }
+}
+
+// Block: 32 columns, 32 partials at a time; then warp j adds up column j.
+__global__ void __launch_bounds__(1024)
     k_col_sum(const float* __restrict__ part, int np, int n, int C, float* o0, float* o1,
               float* o2) {
-  __shared__ float red[8][33];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, i = blockIdx.x * 32 + tx;
+  __shared__ float red[32][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, i0 = blockIdx.x * 32;
   float a = 0.f;
-  if (i < n)
-    for (int p = ty; p < np; p += 8) a += part[(size_t)p * n + i];
+  if (i0 + tx < n) {
+#pragma unroll 4
+    for (int p = ty; p < np; p += 32) a += part[(size_t)p * n + i0 + tx];
+  }
   red[ty][tx] = a;
   __syncthreads();
-  if (ty || i >= n) return;
-  a = 0.f;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) a += red[u][tx];
+  a = lane_sum<32>(red[tx][ty]);
+  const int i = i0 + ty;
+  if (tx || i >= n) return;
   float* o = i < C ? o0 : i < 2 * C ? o1 : o2;
   if (o) o[i % C] = a;
 }
 
-int prep_parts(int rows) { return std::min(PR_PARTS, (rows + 31) / 32); }
+int prep_parts(int rows) { return std::min(PR_PARTS, (rows + 15) / 16); }
 
 gdn_status check_prep(const gdn_prep_shape* s) {
   if (!s || s->rows < 0 || s->H < 1 || s->Hk < 1 || s->H % s->Hk || !(s->eps > 0.f) ||
@@ -152,24 +228,20 @@ gdn_status check_prep(const gdn_prep_shape* s) {
     return GDN_ERR_INVALID_ARG;
   if (!dtype_ok(s->dtype) || (s->dk != 64 && s->dk != 128) || s->H > (1 << 16))
     return GDN_ERR_UNSUPPORTED;
-  if ((long long)s->rows * s->H >= (1ll << 33)) return GDN_ERR_UNSUPPORTED;
+  if ((long long)s->rows * 2 * s->H >= (1ll << 31)) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
-}
-
-long long row_blocks_of(const gdn_prep_shape& s) {
-  const int groups = PR_NT / (s.dk / 8);
-  return ((long long)s.rows * 2 * s.Hk + groups - 1) / groups;
 }
 
 template <typename T, int DK>
 void launch_prep_fwd(const gdn_prep_shape& s, const void* q, const void* k, const void* xg,
                      const void* xb, const float* rate, const float* bias, void* qn, void* kn,
                      void* g, void* beta, cudaStream_t st) {
-  const long long rb = row_blocks_of(s);
-  const long long gb = ((long long)s.rows * s.H + PR_NT - 1) / PR_NT;
-  k_prep_fwd<T, DK><<<(unsigned)(rb + gb), PR_NT, 0, st>>>(
-      s.rows, s.H, s.Hk, (int)rb, s.ldq, s.ldk, s.ldg, s.ldb, s.q_scale, s.eps, (const T*)q,
-      (const T*)k, (const T*)xg, (const T*)xb, rate, bias, (T*)qn, (T*)kn, (T*)g, (T*)beta);
+  const uint32_t nrow = (uint32_t)s.rows * 2 * s.Hk, ngate = (uint32_t)s.rows * s.H;
+  const uint32_t per = PR_NT / (DK / 8) * PR_U, rb = (nrow + per - 1) / per;
+  k_prep_fwd<T, DK><<<rb + (ngate + PR_NT - 1) / PR_NT, PR_NT, 0, st>>>(
+      nrow, ngate, FastDiv(2 * s.Hk), FastDiv(s.H), s.H / s.Hk, (int)rb, s.ldq, s.ldk, s.ldg,
+      s.ldb, s.q_scale, s.eps, (const T*)q, (const T*)k, (const T*)xg, (const T*)xb, rate, bias,
+      (T*)qn, (T*)kn, (T*)g, (T*)beta);
 }
 
 template <typename T, int DK>
@@ -177,13 +249,16 @@ void launch_prep_bwd(const gdn_prep_shape& s, const void* q, const void* k, cons
                      const void* xb, const float* rate, const float* bias, const void* dqn,
                      const void* dkn, const void* dg, const void* dbeta, void* dq, void* dk,
                      void* dxg, void* dxb, float* part, cudaStream_t st) {
-  k_prep_bwd<T, DK><<<(unsigned)row_blocks_of(s), PR_NT, 0, st>>>(
-      s.rows, s.H, s.Hk, s.ldq, s.ldk, s.q_scale, s.eps, (const T*)q, (const T*)k, (const T*)dqn,
-      (const T*)dkn, (T*)dq, (T*)dk);
+  const uint32_t nrow = (uint32_t)s.rows * 2 * s.Hk;
+  const uint32_t per = PR_NT / (DK / 8) * PR_UB, rb = (nrow + per - 1) / per;
   const int np = prep_parts(s.rows);
-  k_prep_bwd_gates<T><<<np, PR_NT, 0, st>>>(s.rows, s.H, (s.rows + np - 1) / np, s.ldg, s.ldb,
-                                            (const T*)xg, (const T*)xb, rate, bias, (const T*)dg,
-                                            (const T*)dbeta, (T*)dxg, (T*)dxb, part);
+  int hp_log = 0;
+  while ((1 << hp_log) < s.H && hp_log < 5) ++hp_log;
+  k_prep_bwd<T, DK><<<np + rb, PR_NT, 0, st>>>(
+      nrow, FastDiv(2 * s.Hk), s.H / s.Hk, np, s.rows, s.H, hp_log, (s.rows + np - 1) / np, s.ldq,
+      s.ldk, s.ldg, s.ldb, s.q_scale, s.eps, (const T*)q, (const T*)k, (const T*)xg, (const T*)xb,
+      rate, bias, (const T*)dqn, (const T*)dkn, (const T*)dg, (const T*)dbeta, (T*)dq, (T*)dk,
+      (T*)dxg, (T*)dxb, part);
 }
 
 }  // namespace
@@ -191,7 +266,7 @@ void launch_prep_bwd(const gdn_prep_shape& s, const void* q, const void* k, cons
 cudaError_t col_sum(const float* part, int np, int n, int C, float* o0, float* o1, float* o2,
                     cudaStream_t st) {
   prof_mark(st, "layer_col_sum");
-  k_col_sum<<<(n + 31) / 32, 256, 0, st>>>(part, np, n, C, o0, o1, o2);
+  k_col_sum<<<(n + 31) / 32, 1024, 0, st>>>(part, np, n, C, o0, o1, o2);
   return cudaGetLastError();
 }
 

@@ -406,6 +406,8 @@ def gdn_conv_bwd(x, w, b, state_in, dy, dstate_out=None, act="silu", dx=None, dw
 
 
 # ------------------------------------------------- layer operators (include/gdn_layer.h)
+# A generation step makes these calls once per layer and token, so what they do
+# on the host is kept short: one look at each tensor's shape, type and device.
 def _own_stream(fn):
     """With stream=..., run fn with that stream current, so that what it
     allocates (outputs, workspace) belongs to the stream its kernels run on."""
@@ -420,52 +422,81 @@ def _own_stream(fn):
     return call
 
 
+def _raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same value without a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811
+
+
+def _bad(name, t, shape, dtype, dev):
+    return ValueError(f"{name}: expected a contiguous {tuple(shape)} {dtype} tensor on cuda:{dev}, "
+                      f"got {tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
+
+
 def _on_gpu(name, t, ndim):
-    if not t.is_cuda or t.dim() < ndim:
+    """Index of the GPU that holds t."""
+    dev = t.get_device()
+    if dev < 0 or t.dim() < ndim:
         raise ValueError(f"{name}: a CUDA tensor with {ndim} dimensions is expected, got "
                          f"{tuple(t.shape)} on {t.device}")
+    return dev
 
 
-def _want(name, t, shape, dtype, device):
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+def _want(name, t, shape, dtype, dev):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise _bad(name, t, shape, dtype, dev)
 
 
-def _want_c(name, t, shape, dtype, device):
+def _want_c(name, t, shape, dtype, dev):
     """As _want, and contiguous; returns the pointer (None for an absent tensor)."""
     if t is None:
         return None
-    _want(name, t, shape, dtype, device)
-    return _p(t)
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise _bad(name, t, shape, dtype, dev)
+    return t.data_ptr()
 
 
 def _rows(name, t, ndim):
     """Stride of the rows of t [..., n1, .., nk] (k = ndim trailing dimensions that
     have to be dense) when its leading dimensions flatten to one."""
+    st, sh = t.stride(), t.shape
+    if st[-1] == 1 and (ndim == 1 or st[-2] == sh[-1]):  # dense rows: the usual layouts
+        lead = len(st) - ndim
+        if lead == 1 or (lead == 2 and sh[0] == 1):
+            return st[lead - 1]
     inner = 1
     for i in range(1, ndim + 1):
-        if t.shape[-i] != 1 and t.stride(-i) != inner:
+        if sh[-i] != 1 and st[-i] != inner:
             raise ValueError(f"{name}: the last {ndim} dimensions must be dense")
-        inner *= t.shape[-i]
+        inner *= sh[-i]
     ld, n = inner, 1
-    for i in range(t.dim() - ndim - 1, -1, -1):
-        if t.shape[i] == 1:
+    for i in range(len(sh) - ndim - 1, -1, -1):
+        if sh[i] == 1:
             continue
         if n == 1:
-            ld = t.stride(i)
-        elif t.stride(i) != ld * n:
+            ld = st[i]
+        elif st[i] != ld * n:
             raise ValueError(f"{name}: the rows must have one stride")
-        n *= t.shape[i]
+        n *= sh[i]
     return ld
 
 
-def _cache_args(N, n_tok, device, slot_in, slot_out, cu_seqlens, n_commit):
-    i32 = torch.int32
-    return (_want_c("slot_in", slot_in, (N,), i32, device),
-            _want_c("slot_out", slot_out, (N,), i32, device),
-            _want_c("cu_seqlens", cu_seqlens, (N + 1,), i32, device),
-            _want_c("n_commit", n_commit, (N,), i32, device))
+def _index(name, t, n, dev):
+    """Pointer of an int32 index array of n entries (None for an absent one)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise _bad(name, t, (n,), torch.int32, dev)
+    return t.data_ptr()
+
+
+def _scratch(t, dev):
+    """Pointer and bytes of a workspace."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
+    return t.data_ptr(), t.nbytes
 
 
 @_own_stream
@@ -481,30 +512,32 @@ def gdn_step(q, k, v, g, beta, S, slot_in=None, slot_out=None, cu_seqlens=None, 
     after that many of its tokens is written (None: all). All int32 on the device.
     gate = (rate, bias) [H] fp32: g and beta are the inputs of gdn_prep_fwd's maps
     and q, k are normalised. Returns o [n_tok, H, dv]."""
-    _on_gpu("q", q, 3)
-    _on_gpu("v", v, 3)
+    dev, dt, f32 = _on_gpu("q", q, 3), q.dtype, torch.float32
     n, Hk, dk = q.shape
-    H, dv = v.shape[1:]
-    dt, dev = q.dtype, q.device
-    N = n if cu_seqlens is None else cu_seqlens.numel() - 1
+    _, H, dv = v.shape
+    n_slots = S.shape[0]
+    N = n if cu_seqlens is None else cu_seqlens.shape[0] - 1
     _want("k", k, (n, Hk, dk), dt, dev)
     _want("v", v, (n, H, dv), dt, dev)
     _want("g", g, (n, H), dt, dev)
     _want("beta", beta, (n, H), dt, dev)
     rate, bias = gate if gate is not None else (None, None)
-    s = gdn_step_shape(N, n, S.shape[0], H, Hk, dk, dv, _dtype_code(q), _rows("q", q, 2),
+    s = gdn_step_shape(N, n, n_slots, H, Hk, dk, dv, _dtype_code(q), _rows("q", q, 2),
                        _rows("k", k, 2), _rows("v", v, 2), _rows("g", g, 1),
                        _rows("beta", beta, 1), q_scale, eps)
     if o is None:
-        o = torch.empty(n, H, dv, dtype=dt, device=dev)
-    f32 = torch.float32
+        o = torch.empty((n, H, dv), dtype=dt, device=q.device)
+        po = o.data_ptr()
+    else:
+        po = _want_c("o", o, (n, H, dv), dt, dev)
     rc = load().gdn_step(
         s, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
         _want_c("rate", rate, (H,), f32, dev), _want_c("bias", bias, (H,), f32, dev),
-        _want_c("S", S, (S.shape[0], H, dk, dv), f32, dev),
-        *_cache_args(N, n, dev, slot_in, slot_out, cu_seqlens, n_commit),
-        _want_c("o", o, (n, H, dv), dt, dev), _stream(None))
-    _check(rc, "gdn_step")
+        _want_c("S", S, (n_slots, H, dk, dv), f32, dev), _index("slot_in", slot_in, N, dev),
+        _index("slot_out", slot_out, N, dev), _index("cu_seqlens", cu_seqlens, N + 1, dev),
+        _index("n_commit", n_commit, N, dev), po, _raw_stream(dev))
+    if rc:
+        raise GdnError(rc, "gdn_step")
     return o
 
 
@@ -514,33 +547,34 @@ def gdn_conv_step(x, w, b, state, slot_in=None, slot_out=None, cu_seqlens=None, 
     """The short convolution of packed new tokens x [n_tok, C] (rows strided) over
     the cached last inputs state [n_slots, W - 1, C] (updated in place), for the
     sequences of gdn_step. Returns y [n_tok, C]."""
-    _on_gpu("x", x, 2)
-    _on_gpu("w", w, 2)
+    dev, dt, f32 = _on_gpu("x", x, 2), x.dtype, torch.float32
     n, C = x.shape
-    W = w.shape[1]
-    dt, dev, f32 = x.dtype, x.device, torch.float32
-    N = n if cu_seqlens is None else cu_seqlens.numel() - 1
-    s = gdn_conv_step_shape(N, n, state.shape[0], C, W, _dtype_code(x), CONV_ACT[act],
+    W, n_slots = w.shape[1], state.shape[0]
+    N = n if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    s = gdn_conv_step_shape(N, n, n_slots, C, W, _dtype_code(x), CONV_ACT[act],
                             _rows("x", x, 1))
     if y is None:
-        y = torch.empty(n, C, dtype=dt, device=dev)
+        y = torch.empty((n, C), dtype=dt, device=x.device)
+        py = y.data_ptr()
+    else:
+        py = _want_c("y", y, (n, C), dt, dev)
     rc = load().gdn_conv_step(
         s, x.data_ptr(), _want_c("w", w, (C, W), f32, dev), _want_c("b", b, (C,), f32, dev),
-        _want_c("state", state, (state.shape[0], W - 1, C), dt, dev),
-        *_cache_args(N, n, dev, slot_in, slot_out, cu_seqlens, n_commit),
-        _want_c("y", y, (n, C), dt, dev), _stream(None))
-    _check(rc, "gdn_conv_step")
+        _want_c("state", state, (n_slots, W - 1, C), dt, dev), _index("slot_in", slot_in, N, dev),
+        _index("slot_out", slot_out, N, dev), _index("cu_seqlens", cu_seqlens, N + 1, dev),
+        _index("n_commit", n_commit, N, dev), py, _raw_stream(dev))
+    if rc:
+        raise GdnError(rc, "gdn_conv_step")
     return y
 
 
 def _prep_shape_of(q, k, xg, xb, q_scale, eps):
-    _on_gpu("q", q, 4)
-    _on_gpu("xg", xg, 3)
+    dev = _on_gpu("q", q, 4)
     B, T, Hk, dk = q.shape
-    H = xg.shape[2]
-    _want("k", k, (B, T, Hk, dk), q.dtype, q.device)
-    _want("xg", xg, (B, T, H), q.dtype, q.device)
-    _want("xb", xb, (B, T, H), q.dtype, q.device)
+    _, _, H = xg.shape
+    _want("k", k, (B, T, Hk, dk), q.dtype, dev)
+    _want("xg", xg, (B, T, H), q.dtype, dev)
+    _want("xb", xb, (B, T, H), q.dtype, dev)
     return gdn_prep_shape(B * T, H, Hk, dk, _dtype_code(q), _rows("q", q, 2), _rows("k", k, 2),
                           _rows("xg", xg, 1), _rows("xb", xb, 1), q_scale, eps)
 
@@ -554,15 +588,16 @@ def gdn_prep_fwd(q, k, xg, xb, rate, bias, q_scale=1.0, eps=1e-6):
     beta = sigmoid(xb)."""
     s = _prep_shape_of(q, k, xg, xb, q_scale, eps)
     B, T, _, dk = q.shape
-    H, dt, dev, f32 = s.H, q.dtype, q.device, torch.float32
-    qn = torch.empty(B, T, H, dk, dtype=dt, device=dev)
-    kn = torch.empty(B, T, H, dk, dtype=dt, device=dev)
-    g = torch.empty(B, T, H, dtype=dt, device=dev)
-    beta = torch.empty(B, T, H, dtype=dt, device=dev)
+    H, dt, dev, f32 = s.H, q.dtype, q.get_device(), torch.float32
+    at = q.device
+    qn = torch.empty(B, T, H, dk, dtype=dt, device=at)
+    kn = torch.empty(B, T, H, dk, dtype=dt, device=at)
+    g = torch.empty(B, T, H, dtype=dt, device=at)
+    beta = torch.empty(B, T, H, dtype=dt, device=at)
     rc = load().gdn_prep_fwd(s, q.data_ptr(), k.data_ptr(), xg.data_ptr(), xb.data_ptr(),
                              _want_c("rate", rate, (H,), f32, dev),
                              _want_c("bias", bias, (H,), f32, dev), qn.data_ptr(), kn.data_ptr(),
-                             g.data_ptr(), beta.data_ptr(), _stream(None))
+                             g.data_ptr(), beta.data_ptr(), _raw_stream(dev))
     _check(rc, "gdn_prep_fwd")
     return qn, kn, g, beta
 
@@ -575,14 +610,15 @@ def gdn_prep_bwd(q, k, xg, xb, rate, bias, dq, dk, dg, dbeta, q_scale=1.0, eps=1
     lib = load()
     s = _prep_shape_of(q, k, xg, xb, q_scale, eps)
     B, T, Hk, D = q.shape
-    H, dt, dev, f32 = s.H, q.dtype, q.device, torch.float32
+    H, dt, dev, f32 = s.H, q.dtype, q.get_device(), torch.float32
+    at = q.device
     if workspace is None:
-        workspace = alloc_workspace(lib.gdn_prep_workspace_bytes(s), dev)
-    oq = torch.empty(B, T, Hk, D, dtype=dt, device=dev)
-    ok = torch.empty(B, T, Hk, D, dtype=dt, device=dev)
-    og = torch.empty(B, T, H, dtype=dt, device=dev)
-    ob = torch.empty(B, T, H, dtype=dt, device=dev)
-    par = torch.empty(2, H, dtype=f32, device=dev)
+        workspace = alloc_workspace(lib.gdn_prep_workspace_bytes(s), at)
+    oq = torch.empty(B, T, Hk, D, dtype=dt, device=at)
+    ok = torch.empty(B, T, Hk, D, dtype=dt, device=at)
+    og = torch.empty(B, T, H, dtype=dt, device=at)
+    ob = torch.empty(B, T, H, dtype=dt, device=at)
+    par = torch.empty(2, H, dtype=f32, device=at)
     rc = lib.gdn_prep_bwd(s, q.data_ptr(), k.data_ptr(), xg.data_ptr(), xb.data_ptr(),
                           _want_c("rate", rate, (H,), f32, dev),
                           _want_c("bias", bias, (H,), f32, dev),
@@ -591,16 +627,14 @@ def gdn_prep_bwd(q, k, xg, xb, rate, bias, dq, dk, dg, dbeta, q_scale=1.0, eps=1
                           _want_c("dg", dg, (B, T, H), dt, dev),
                           _want_c("dbeta", dbeta, (B, T, H), dt, dev), oq.data_ptr(),
                           ok.data_ptr(), og.data_ptr(), ob.data_ptr(), par.data_ptr(),
-                          par.data_ptr() + 4 * H, _p(workspace), workspace.numel(),
-                          _stream(None))
+                          par.data_ptr() + 4 * H, *_scratch(workspace, dev), _raw_stream(dev))
     _check(rc, "gdn_prep_bwd")
     return oq, ok, og, ob, par[0], par[1]
 
 
 def _gate_norm_shape_of(o, z, act, eps):
-    _on_gpu("o", o, 4)
     B, T, H, d = o.shape
-    _want("z", z, (B, T, H, d), o.dtype, o.device)
+    _want("z", z, (B, T, H, d), o.dtype, _on_gpu("o", o, 4))
     return gdn_gate_norm_shape(B * T, H, d, _dtype_code(o), GATE_ACT[act], _rows("z", z, 2), eps)
 
 
@@ -609,11 +643,12 @@ def gdn_gate_norm_fwd(o, z, w, act="silu", eps=1e-6, y=None):
     """y = rms_norm(o) * w * act(z) over the last dimension of o [B, T, H, d]; z [B, T, H, d]
     with strided token rows, w [d] fp32, act "silu" or "sigmoid"."""
     s = _gate_norm_shape_of(o, z, act, eps)
+    dev, shape, dt, f32 = o.get_device(), o.shape, o.dtype, torch.float32
     if y is None:
         y = torch.empty(o.shape, dtype=o.dtype, device=o.device)
-    rc = load().gdn_gate_norm_fwd(s, _p(o), z.data_ptr(),
-                                  _want_c("w", w, (s.d,), torch.float32, o.device),
-                                  _want_c("y", y, o.shape, o.dtype, o.device), _stream(None))
+    rc = load().gdn_gate_norm_fwd(s, _want_c("o", o, shape, dt, dev), z.data_ptr(),
+                                  _want_c("w", w, (s.d,), f32, dev),
+                                  _want_c("y", y, shape, dt, dev), _raw_stream(dev))
     _check(rc, "gdn_gate_norm_fwd")
     return y
 
@@ -623,22 +658,22 @@ def gdn_gate_norm_bwd(o, z, w, dy, act="silu", eps=1e-6, workspace=None):
     """Backward of gdn_gate_norm_fwd. Returns (do, dz, dw)."""
     lib = load()
     s = _gate_norm_shape_of(o, z, act, eps)
+    dev, shape, dt, f32 = o.get_device(), o.shape, o.dtype, torch.float32
     if workspace is None:
         workspace = alloc_workspace(lib.gdn_gate_norm_workspace_bytes(s), o.device)
     do = torch.empty(o.shape, dtype=o.dtype, device=o.device)
     dz = torch.empty(o.shape, dtype=o.dtype, device=o.device)
     dw = torch.empty(s.d, dtype=torch.float32, device=o.device)
-    rc = lib.gdn_gate_norm_bwd(s, _p(o), z.data_ptr(),
-                               _want_c("w", w, (s.d,), torch.float32, o.device),
-                               _want_c("dy", dy, o.shape, o.dtype, o.device), do.data_ptr(),
-                               dz.data_ptr(), dw.data_ptr(), _p(workspace), workspace.numel(),
-                               _stream(None))
+    rc = lib.gdn_gate_norm_bwd(s, _want_c("o", o, shape, dt, dev), z.data_ptr(),
+                               _want_c("w", w, (s.d,), f32, dev),
+                               _want_c("dy", dy, shape, dt, dev), do.data_ptr(),
+                               dz.data_ptr(), dw.data_ptr(), *_scratch(workspace, dev),
+                               _raw_stream(dev))
     _check(rc, "gdn_gate_norm_bwd")
     return do, dz, dw
 
 
 def _res_norm_shape_of(h, like, eps):
-    _on_gpu("h", h, 1)
     C = h.shape[-1]
     return gdn_res_norm_shape(h.numel() // C if C else 0, C, _dtype_code(like), _dtype_code(h),
                               eps)
@@ -654,18 +689,18 @@ def gdn_res_norm_fwd(h, x, w, w_post=None, scale=None, eps=1e-6, h_out=None, y=N
     (before the first block): y is the norm of h, in `dtype` (default h's).
     h_out may be h. Returns (h_out, y); h_out is None where x is."""
     dt = x.dtype if x is not None else dtype or h.dtype
-    dev, C, f32 = h.device, h.shape[-1], torch.float32
+    dev, at, C, f32 = _on_gpu("h", h, 1), h.device, h.shape[-1], torch.float32
     if y is None:
-        y = torch.empty(h.shape, dtype=dt, device=dev)
+        y = torch.empty(h.shape, dtype=dt, device=at)
     if h_out is None and x is not None:
-        h_out = torch.empty(h.shape, dtype=h.dtype, device=dev)
+        h_out = torch.empty(h.shape, dtype=h.dtype, device=at)
     s = _res_norm_shape_of(h, y, eps)
     rc = load().gdn_res_norm_fwd(s, _p(h), _want_c("x", x, h.shape, dt, dev),
                                  _want_c("w", w, (C,), f32, dev),
                                  _want_c("w_post", w_post, (C,), f32, dev),
                                  _want_c("scale", scale, (C,), f32, dev),
                                  _want_c("h_out", h_out, h.shape, h.dtype, dev),
-                                 _want_c("y", y, h.shape, dt, dev), _stream(None))
+                                 _want_c("y", y, h.shape, dt, dev), _raw_stream(dev))
     _check(rc, "gdn_res_norm_fwd")
     return h_out, y
 
@@ -677,17 +712,17 @@ def gdn_res_norm_bwd(h_out, x, w, dy, dh_out=None, w_post=None, scale=None, eps=
     dh may be dh_out. Returns (dh, dx, dw, dw_post, dscale); dx is dh itself where
     they are equal (no w_post, no scale, one dtype)."""
     lib = load()
-    C, dev, f32 = h_out.shape[-1], h_out.device, torch.float32
+    dev, at, C, f32 = _on_gpu("h_out", h_out, 1), h_out.device, h_out.shape[-1], torch.float32
     s = _res_norm_shape_of(h_out, dy, eps)
     if workspace is None:
-        workspace = alloc_workspace(lib.gdn_res_norm_workspace_bytes(s), dev)
+        workspace = alloc_workspace(lib.gdn_res_norm_workspace_bytes(s), at)
     if dh is None:
-        dh = torch.empty(h_out.shape, dtype=h_out.dtype, device=dev)
+        dh = torch.empty(h_out.shape, dtype=h_out.dtype, device=at)
     same = w_post is None and scale is None and (dy.dtype == h_out.dtype or x is None)
-    dx = None if same else torch.empty(h_out.shape, dtype=dy.dtype, device=dev)
-    dw = torch.empty(C, dtype=f32, device=dev)
-    dpost = None if w_post is None else torch.empty(C, dtype=f32, device=dev)
-    dscale = None if scale is None else torch.empty(C, dtype=f32, device=dev)
+    dx = None if same else torch.empty(h_out.shape, dtype=dy.dtype, device=at)
+    dw = torch.empty(C, dtype=f32, device=at)
+    dpost = None if w_post is None else torch.empty(C, dtype=f32, device=at)
+    dscale = None if scale is None else torch.empty(C, dtype=f32, device=at)
     rc = lib.gdn_res_norm_bwd(s, _p(h_out), _want_c("x", x, h_out.shape, dy.dtype, dev),
                               _want_c("w", w, (C,), f32, dev),
                               _want_c("w_post", w_post, (C,), f32, dev),
@@ -695,8 +730,8 @@ def gdn_res_norm_bwd(h_out, x, w, dy, dh_out=None, w_post=None, scale=None, eps=
                               _want_c("dy", dy, h_out.shape, dy.dtype, dev),
                               _want_c("dh_out", dh_out, h_out.shape, h_out.dtype, dev),
                               _want_c("dh", dh, h_out.shape, h_out.dtype, dev), _p(dx), _p(dw),
-                              _p(dpost), _p(dscale), _p(workspace), workspace.numel(),
-                              _stream(None))
+                              _p(dpost), _p(dscale), *_scratch(workspace, dev),
+                              _raw_stream(dev))
     _check(rc, "gdn_res_norm_bwd")
     return dh, (dh if same else dx), dw, dpost, dscale
 
