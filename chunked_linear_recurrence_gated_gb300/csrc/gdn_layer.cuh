@@ -7,6 +7,38 @@
 
 namespace gdn {
 
+// Two fp32 lanes in one register pair (one instruction for both).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 both2(float a) { return pack2(a, a); }
+__device__ __forceinline__ float sum2(f32x2 a) {
+  float lo, hi;
+  unpack2(a, lo, hi);
+  return lo + hi;
+}
+
 // 8 consecutive elements: one 16-byte access of bf16, two of fp32.
 __device__ __forceinline__ void ld8(const float* p, float* v) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
@@ -60,6 +92,27 @@ __device__ __forceinline__ void st8(__nv_bfloat16* p, const float* v) {
     u[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// 8 elements as 4 pairs.
+__device__ __forceinline__ void cvt8(const Raw8<float>& a, f32x2* v) {
+  float f[8];
+  cvt8(a, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void cvt8(const Raw8<__nv_bfloat16>& a, f32x2* v) {
+  float f[8];
+  cvt8(a, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void st8(T* p, const f32x2* v) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+  st8(p, f);
 }
 
 // Sum over the L consecutive lanes (L a power of two) that share a row.

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(GN_NT)
 // Blocks take every gridDim.x-th group of rows; each thread keeps the dw of its
 // 8 columns, part[block] = the block's sum.
 template <typename T, int L>
-__global__ void __launch_bounds__(GN_NT)
+__global__ void __launch_bounds__(GN_NT, sizeof(T) == 2 ? GN_PARTS / 152 : 2)
     k_gate_norm_bwd(uint32_t nrow, FastDiv byH, int d, float inv_d, int act, long long ldz,
                     float eps, const T* __restrict__ o, const T* __restrict__ z,
                     const float* __restrict__ w, const T* __restrict__ dy, T* __restrict__ dout,
@@ -162,54 +162,102 @@ struct Team {
   bool on;          // the thread has columns
 };
 
-// Sums of K values over the team (and cluster); buf alternates between calls,
-// so one barrier separates a call's reads from the next but one's writes.
+// What a team's reductions go through; buf alternates between calls, so one
+// barrier separates a call's reads from the next but one's writes.
+template <int CL>
+struct TeamRed {
+  float* warp;     // [2][4][16] the warps' sums (unused ones stay 0)
+  float4* cta;     // CL > 1: [2][CL] the CTAs' sums, written by their owners
+  uint64_t* bar;   // CL > 1: [2] completed by CL such writes
+  int buf, phase;  // of the next call
+  bool dead;       // a wait gave up: every later sum is NaN, so the failure shows
+};
+
+// Sums of K values over the team and, for rows split over a cluster, over its
+// CTAs: each CTA writes its sums into every CTA's shared memory with
+// st.async, which also completes the receiver's mbarrier. (A cluster barrier
+// instead would have to order the row's global stores too: its release waits
+// for them, 6 us per row of 16384 columns against DRAM's 2.)
 template <int K, int CL>
-__device__ __forceinline__ void team_sum(float* v, float* red, int& buf) {
+__device__ __forceinline__ void team_sum(float* v, TeamRed<CL>& red) {
   const int nt = blockDim.x, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int i = 0; i < K; ++i) v[i] = lane_sum<32>(v[i]);
-  if (CL == 1 && nt == 32) return;
-  float* slot = red + buf * (4 * CL * 16);  // [K][CL][16 warps], unused ones stay 0
-  buf ^= 1;
-  if (CL == 1) {
+  if (CL > 1 || nt > 32) {
+    float* slot = red.warp + red.buf * 64;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
       for (int i = 0; i < K; ++i) slot[i * 16 + warp] = v[i];
     named_bar(threadIdx.y + 1, nt);
-  } else {
-    uint32_t rank;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    if ((threadIdx.x & 31) < CL) {  // lane p: into CTA p of the cluster
 #pragma unroll
-      for (int i = 0; i < K; ++i) {
-        uint32_t at;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(at)
-                     : "r"(smem_u32(slot + (i * CL + rank) * 16 + warp)),
-                       "r"(threadIdx.x & 31));
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[i]) : "memory");
+    for (int i = 0; i < K; ++i) {
+      v[i] = 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (u * 4 >= (nt >> 5)) break;
+        const float4 a = reinterpret_cast<const float4*>(slot + i * 16)[u];
+        v[i] += (a.x + a.y) + (a.z + a.w);
       }
     }
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const float4* p = reinterpret_cast<const float4*>(slot + i * CL * 16);
-    v[i] = 0.f;
-#pragma unroll
-    for (int u = 0; u < CL * 4; ++u) {
-      if (CL == 1 && u * 4 >= (nt >> 5)) break;
-      const float4 a = p[u];
-      v[i] += (a.x + a.y) + (a.z + a.w);
+  if (CL > 1) {
+    uint64_t* bar = red.bar + red.buf;
+    float4* all = red.cta + red.buf * CL;
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, CL * 16);
+    if (threadIdx.x < CL) {
+      uint32_t rank, to, tobar;
+      asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+      asm("mapa.shared::cluster.u32 %0, %1, %2;"
+          : "=r"(to)
+          : "r"(smem_u32(all + rank)), "r"(threadIdx.x));
+      asm("mapa.shared::cluster.u32 %0, %1, %2;"
+          : "=r"(tobar)
+          : "r"(smem_u32(bar)), "r"(threadIdx.x));
+      asm volatile(
+          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], "
+          "{%1, %2, %3, %4}, [%5];" ::"r"(to),
+          "f"(v[0]), "f"(v[K > 1 ? 1 : 0]), "f"(v[K > 2 ? 2 : 0]), "f"(0.f), "r"(tobar)
+          : "memory");
     }
+    const long long t0 = clock64();
+    for (uint32_t ok = red.dead; !ok;) {
+      asm volatile(
+          "{\n .reg .pred p;\n"
+          " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+          " selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"((uint32_t)red.phase)
+          : "memory");
+      if (!ok && clock64() - t0 > (1ll << 32)) ok = red.dead = true;
+    }
+    float s[3] = {};
+#pragma unroll
+    for (int r = 0; r < CL; ++r) {
+      const float4 a = all[r];
+      s[0] += a.x, s[1] += a.y, s[2] += a.z;
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = red.dead ? __int_as_float(0x7fc00000) : s[i];
+    red.phase ^= red.buf;  // both buffers of this phase used: the next phase
+  }
+  red.buf ^= 1;
+}
+
+// A CTA that exits must not be written to any more: every CTA of the cluster
+// has received all sums.
+template <int CL>
+__device__ __forceinline__ void team_end() {
+  if (CL > 1) {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
 }
 
 template <int CL>
-__device__ __forceinline__ Team team_of(int rows, int C, float* red) {
+__device__ __forceinline__ Team team_of(int rows, int C, TeamRed<CL>& red) {
+  __shared__ __align__(16) float warp_sums[8 * 2 * 64];  // at most 8 teams
+  __shared__ float4 cta_sums[2 * CL];
+  __shared__ uint64_t bars[2];
   Team t;
   t.C = C;
   t.rows = rows;
@@ -219,14 +267,23 @@ __device__ __forceinline__ Team team_of(int rows, int C, float* red) {
   t.on = (int)threadIdx.x < per && t.c < C;
   t.first = blockIdx.x / CL * blockDim.y + threadIdx.y;
   t.step = gridDim.x / CL * blockDim.y;
-  if (CL > 1 || blockDim.x > 32) {
-    for (int i = threadIdx.x; i < 2 * 4 * CL * 16; i += blockDim.x) red[i] = 0.f;
-    if (CL == 1) {
-      named_bar(threadIdx.y + 1, blockDim.x);
-    } else {
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  red.warp = warp_sums + threadIdx.y * 128;
+  red.cta = cta_sums;
+  red.bar = bars;
+  red.buf = red.phase = 0;
+  red.dead = false;
+  for (int i = threadIdx.x; i < 128; i += blockDim.x) red.warp[i] = 0.f;
+  if (CL > 1) {
+    if (threadIdx.x == 0) {
+      mbar_init(bars, 1);
+      mbar_init(bars + 1, 1);
+      fence_mbar_init();
     }
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    named_bar(threadIdx.y + 1, blockDim.x);
   }
   return t;
 }
@@ -243,11 +300,18 @@ struct Ring {
   template <typename T>
   __device__ __forceinline__ void fetch(int stage, int k, const T* p) const {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      cp16(at(stage, k + i), reinterpret_cast<const uint4*>(p) + i, true);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint4* src = reinterpret_cast<const uint4*>(p) + i;
+      if (sizeof(T) == 2)
+        cp16(at(stage, k + i), src, true);
+      else  // through L1: the two halves of a sector are fetched by two instructions
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;\n" ::"r"(
+                         smem_u32(at(stage, k + i))),
+                     "l"(src));
+    }
   }
   template <typename T>
-  __device__ __forceinline__ void read(int stage, int k, float* v) const {
+  __device__ __forceinline__ void read(int stage, int k, f32x2* v) const {
     Raw8<T> r;
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = *at(stage, k + i);
@@ -266,10 +330,10 @@ constexpr int bwd_slots() { return 2 * pieces<R>() + 2 * pieces<T>(); }
 template <typename T, typename R>
 constexpr int bwd_stages() { return bwd_slots<T, R>() == 4 ? 4 : 3; }
 
-__device__ __forceinline__ void ld8_or(const float* p, bool have, float other, float* v) {
+__device__ __forceinline__ void ld8_or(const float* p, bool have, float other, f32x2* v) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = other;
-  if (have) ld8(p, v);
+  for (int i = 0; i < 4; ++i) v[i] = both2(other);
+  if (have) cvt8(ldraw8(p), v);
 }
 
 template <typename T, typename R, int CL>
@@ -279,10 +343,9 @@ __global__ void __launch_bounds__(512, 2)
                    const float* __restrict__ scale, R* h_out, T* __restrict__ y) {
   constexpr int S = fwd_stages<T, R>(), KX = pieces<R>();
   extern __shared__ uint4 smem[];
-  __shared__ float red_all[16 * 2 * 4 * 16];
-  float* red = red_all + threadIdx.y * (2 * 4 * 16);
   const int nt = blockDim.x * blockDim.y;
   Ring<fwd_slots<T, R>()> ring = {smem + threadIdx.y * blockDim.x + threadIdx.x, nt};
+  TeamRed<CL> red;
   const Team t = team_of<CL>(rows, C, red);
   auto fetch = [&](int stage, int row) {
     if (t.on && row < t.rows) {
@@ -294,44 +357,47 @@ __global__ void __launch_bounds__(512, 2)
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
-  float wv[8], pv[8], sv[8];
+  f32x2 wv[4], pv[4], sv[4];
   ld8_or(w + t.c, t.on, 0.f, wv);
   ld8_or(w_post + t.c, t.on && w_post, 1.f, pv);
   ld8_or(scale + t.c, t.on && scale, 1.f, sv);
-  int stage = 0, buf = 0;
+  int stage = 0;
   for (int row = t.first; row < t.rows; row += t.step) {
     cp_wait<S - 1>();
-    float hv[8] = {}, xv[8] = {};
+    f32x2 hv[4] = {}, xv[4] = {};
     if (t.on) {
       ring.template read<R>(stage, 0, hv);
       if (x) ring.template read<T>(stage, KX, xv);
     }
     const size_t at = (size_t)row * C + t.c;
     if (w_post) {
-      float s = 0.f;
+      f32x2 a = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(xv[i], xv[i], s);
-      team_sum<1, CL>(&s, red, buf);
-      const float rx = rsqrtf(fmaf(s, inv_C, eps));
+      for (int i = 0; i < 4; ++i) a = fma2(xv[i], xv[i], a);
+      float s = sum2(a);
+      team_sum<1, CL>(&s, red);
+      const f32x2 rx = both2(rsqrtf(fmaf(s, inv_C, eps)));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xv[i] *= rx * pv[i];
+      for (int i = 0; i < 4; ++i) xv[i] = mul2(xv[i], mul2(rx, pv[i]));
     }
-    float s = 0.f;
+    f32x2 a = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      hv[i] = fmaf(sv[i], xv[i], hv[i]);
-      s = fmaf(hv[i], hv[i], s);
+    for (int i = 0; i < 4; ++i) {
+      hv[i] = fma2(sv[i], xv[i], hv[i]);
+      a = fma2(hv[i], hv[i], a);
     }
     if (h_out && t.on) st8(h_out + at, hv);
     fetch(stage, row + S * t.step);  // the slot has been read
     if (++stage == S) stage = 0;
-    team_sum<1, CL>(&s, red, buf);
-    const float r = rsqrtf(fmaf(s, inv_C, eps));
+    float s = sum2(a);
+    team_sum<1, CL>(&s, red);
+    const f32x2 r = both2(rsqrtf(fmaf(s, inv_C, eps)));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) hv[i] *= r * wv[i];
+    for (int i = 0; i < 4; ++i) hv[i] = mul2(hv[i], mul2(r, wv[i]));
     if (t.on) st8(y + at, hv);
   }
   cp_wait<0>();
+  team_end<CL>();
 }
 
 // part [blocks][1 + (w_post) + (scale)][C]: the blocks' sums of dw, dw_post, dscale.
@@ -345,10 +411,9 @@ __global__ void __launch_bounds__(512, 1)
   constexpr int S = bwd_stages<T, R>(), KD = pieces<R>(), KG = 2 * pieces<R>(),
                 KX = KG + pieces<T>();
   extern __shared__ uint4 smem[];
-  __shared__ float red_all[16 * 2 * 4 * 16];
-  float* red = red_all + threadIdx.y * (2 * 4 * 16);
   const int nt = blockDim.x * blockDim.y;
   Ring<bwd_slots<T, R>()> ring = {smem + threadIdx.y * blockDim.x + threadIdx.x, nt};
+  TeamRed<CL> red;
   const Team t = team_of<CL>(rows, C, red);
   const bool with_x = w_post || scale;
   auto fetch = [&](int stage, int row) {
@@ -363,14 +428,14 @@ __global__ void __launch_bounds__(512, 1)
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
-  float wv[8], pv[8], sv[8], aw[8] = {}, ap[8] = {}, as[8] = {};
+  f32x2 wv[4], pv[4], sv[4], aw[4] = {}, ap[4] = {}, as[4] = {};
   ld8_or(w + t.c, t.on, 0.f, wv);
   ld8_or(w_post + t.c, t.on && w_post, 1.f, pv);
   ld8_or(scale + t.c, t.on && scale, 1.f, sv);
-  int stage = 0, buf = 0;
+  int stage = 0;
   for (int row = t.first; row < t.rows; row += t.step) {
     cp_wait<S - 1>();
-    float hv[8] = {}, gv[8] = {}, xv[8] = {}, dv[8] = {}, s[3] = {};
+    f32x2 hv[4] = {}, gv[4] = {}, xv[4] = {}, dv[4] = {}, a[3] = {};
     if (t.on) {
       ring.template read<R>(stage, 0, hv);
       if (dh_out) ring.template read<R>(stage, KD, dv);
@@ -378,43 +443,47 @@ __global__ void __launch_bounds__(512, 1)
       if (with_x) ring.template read<T>(stage, KX, xv);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s[0] = fmaf(hv[i], hv[i], s[0]);
-      s[1] = fmaf(gv[i] * wv[i], hv[i], s[1]);
-      s[2] = fmaf(xv[i], xv[i], s[2]);
+    for (int i = 0; i < 4; ++i) {
+      a[0] = fma2(hv[i], hv[i], a[0]);
+      a[1] = fma2(mul2(gv[i], wv[i]), hv[i], a[1]);
+      a[2] = fma2(xv[i], xv[i], a[2]);
     }
     fetch(stage, row + S * t.step);  // the slot has been read
     if (++stage == S) stage = 0;
-    team_sum<3, CL>(s, red, buf);
+    float s[3] = {sum2(a[0]), sum2(a[1]), sum2(a[2])};
+    team_sum<3, CL>(s, red);
     const size_t at = (size_t)row * C + t.c;
-    const float r = rsqrtf(fmaf(s[0], inv_C, eps)), m = r * s[1] * inv_C;
-    const float rx = w_post ? rsqrtf(fmaf(s[2], inv_C, eps)) : 1.f;
-    float e = 0.f;
+    // n = h r, dh = dh_out + r (dy w - n m) with m = mean(dy w n): r m = r^2 s1 / C
+    const float r = rsqrtf(fmaf(s[0], inv_C, eps)), rx = rsqrtf(fmaf(s[2], inv_C, eps));
+    const f32x2 r2 = both2(r), rm = both2(-r * r * s[1] * inv_C), rx2 = both2(w_post ? rx : 1.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float n = hv[i] * r;
-      aw[i] = fmaf(gv[i], n, aw[i]);
-      dv[i] = fmaf(r, fmaf(-n, m, gv[i] * wv[i]), dv[i]);  // dh
-      xv[i] *= rx;
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 n = mul2(hv[i], r2), gr = mul2(mul2(gv[i], wv[i]), r2);
+      aw[i] = fma2(gv[i], n, aw[i]);
+      dv[i] = add2(dv[i], fma2(n, rm, gr));
+      xv[i] = mul2(xv[i], rx2);
     }
     if (t.on) st8(dh + at, dv);
+    f32x2 e2 = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      as[i] = fmaf(dv[i], xv[i] * pv[i], as[i]);
-      dv[i] *= sv[i];
-      ap[i] = fmaf(dv[i], xv[i], ap[i]);
-      dv[i] *= pv[i];
-      e = fmaf(dv[i], xv[i], e);
+    for (int i = 0; i < 4; ++i) {
+      as[i] = fma2(dv[i], mul2(xv[i], pv[i]), as[i]);
+      dv[i] = mul2(dv[i], sv[i]);
+      ap[i] = fma2(dv[i], xv[i], ap[i]);
+      dv[i] = mul2(dv[i], pv[i]);
+      e2 = fma2(dv[i], xv[i], e2);
     }
     if (w_post) {
-      team_sum<1, CL>(&e, red, buf);
-      e *= inv_C;
+      float e = sum2(e2);
+      team_sum<1, CL>(&e, red);
+      const f32x2 em = both2(-e * inv_C);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dv[i] = rx * fmaf(-xv[i], e, dv[i]);
+      for (int i = 0; i < 4; ++i) dv[i] = mul2(rx2, fma2(xv[i], em, dv[i]));
     }
     if (dx && t.on) st8(dx + at, dv);
   }
   cp_wait<0>();
+  team_end<CL>();
   // the block's sums: teams joined through shared memory (the ring is drained)
   float* join = reinterpret_cast<float*>(smem);  // [teams][blockDim.x * 8]
   const int narr = 1 + (w_post != nullptr) + (scale != nullptr);
@@ -424,24 +493,24 @@ __global__ void __launch_bounds__(512, 1)
     if (blockDim.y > 1) {
       __syncthreads();
       float* mine = join + (size_t)(threadIdx.y * blockDim.x + threadIdx.x) * 8;
-      float v[8];
+      f32x2 v[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = a == 0 ? aw[i] : a == 1 ? ap[i] : as[i];
+      for (int i = 0; i < 4; ++i) v[i] = a == 0 ? aw[i] : a == 1 ? ap[i] : as[i];
       st8(mine, v);
       __syncthreads();
       if (threadIdx.y == 0 && t.on) {
         for (int u = 1; u < (int)blockDim.y; ++u) {
-          float o[8];
-          ld8(mine + (size_t)u * blockDim.x * 8, o);
+          f32x2 o[4];
+          cvt8(ldraw8(mine + (size_t)u * blockDim.x * 8), o);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += o[i];
+          for (int i = 0; i < 4; ++i) v[i] = add2(v[i], o[i]);
         }
         st8(out + t.c, v);
       }
     } else if (t.on) {
-      float v[8];
+      f32x2 v[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = a == 0 ? aw[i] : a == 1 ? ap[i] : as[i];
+      for (int i = 0; i < 4; ++i) v[i] = a == 0 ? aw[i] : a == 1 ? ap[i] : as[i];
       st8(out + t.c, v);
     }
     out += C;

@@ -13,7 +13,8 @@ namespace {
 
 constexpr int PR_NT = 256;     // threads of a block
 constexpr int PR_U = 4;        // rows a thread has in flight (forward)
-constexpr int PR_UB = 2;       // rows a thread has in flight (backward)
+// Rows a thread has in flight (backward): more where a row has one gradient.
+constexpr int prep_bwd_rows(bool shared) { return shared ? 2 : 4; }
 constexpr int PR_G = 4;        // value heads' gradients loaded together (backward)
 constexpr int PR_PARTS = 304;  // most partial sums of drate / dbias
 
@@ -127,7 +128,7 @@ __device__ __forceinline__ void prep_bwd_gates(int blk, int rows, int H, int hp_
 
 // The first gate_blocks blocks take the gates (their loops over tokens are the
 // longest), the others rows as k_prep_fwd.
-template <typename T, int DK>
+template <typename T, int DK, bool SHARED>
 __global__ void __launch_bounds__(PR_NT)
     k_prep_bwd(uint32_t nrow, FastDiv by2Hk, int G, int gate_blocks, int rows, int H, int hp_log,
                int per, long long ldq, long long ldk, long long ldg, long long ldb, float q_scale,
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(PR_NT)
                       dxg, dxb, part);
     return;
   }
-  constexpr int L = DK / 8, NG = PR_NT / L;
+  constexpr int L = DK / 8, NG = PR_NT / L, PR_UB = prep_bwd_rows(SHARED), GL = SHARED ? PR_G : 1;
   const int c = threadIdx.x % L * 8, Hk = (int)by2Hk.d / 2;
   const uint32_t r0 = (blockIdx.x - gate_blocks) * (NG * PR_UB) + threadIdx.x / L;
   float d[PR_UB][8] = {};
@@ -159,20 +160,20 @@ __global__ void __launch_bounds__(PR_NT)
       src[u] = (h.is_k ? dkn : dqn) + ((size_t)h.t * H + (size_t)h.hk * G) * DK + c;
     }
   }
-  for (int i0 = 0; i0 < G; i0 += PR_G) {
-    Raw8<T> e[PR_UB][PR_G];
+  for (int i0 = 0; i0 < (SHARED ? G : 1); i0 += GL) {
+    Raw8<T> e[PR_UB][GL];
 #pragma unroll
     for (int u = 0; u < PR_UB; ++u)
 #pragma unroll
-      for (int i = 0; i < PR_G; ++i) {
+      for (int i = 0; i < GL; ++i) {
         e[u][i] = Raw8<T>{};
-        if (src[u] && i0 + i < G) e[u][i] = ldraw8(src[u] + (size_t)(i0 + i) * DK);
+        if (src[u] && (!SHARED || i0 + i < G)) e[u][i] = ldraw8(src[u] + (size_t)(i0 + i) * DK);
       }
 #pragma unroll
     for (int u = 0; u < PR_UB; ++u)
 #pragma unroll
-      for (int i = 0; i < PR_G; ++i) {
-        if (i0 + i >= G) break;
+      for (int i = 0; i < GL; ++i) {
+        if (SHARED && i0 + i >= G) break;
         float v[8];
         cvt8(e[u][i], v);
 #pragma unroll
@@ -250,11 +251,13 @@ void launch_prep_bwd(const gdn_prep_shape& s, const void* q, const void* k, cons
                      const void* dkn, const void* dg, const void* dbeta, void* dq, void* dk,
                      void* dxg, void* dxb, float* part, cudaStream_t st) {
   const uint32_t nrow = (uint32_t)s.rows * 2 * s.Hk;
-  const uint32_t per = PR_NT / (DK / 8) * PR_UB, rb = (nrow + per - 1) / per;
+  const bool shared = s.H > s.Hk;
+  const uint32_t per = PR_NT / (DK / 8) * prep_bwd_rows(shared), rb = (nrow + per - 1) / per;
   const int np = prep_parts(s.rows);
   int hp_log = 0;
   while ((1 << hp_log) < s.H && hp_log < 5) ++hp_log;
-  k_prep_bwd<T, DK><<<np + rb, PR_NT, 0, st>>>(
+  const auto kernel = shared ? k_prep_bwd<T, DK, true> : k_prep_bwd<T, DK, false>;
+  kernel<<<np + rb, PR_NT, 0, st>>>(
       nrow, FastDiv(2 * s.Hk), s.H / s.Hk, np, s.rows, s.H, hp_log, (s.rows + np - 1) / np, s.ldq,
       s.ldk, s.ldg, s.ldb, s.q_scale, s.eps, (const T*)q, (const T*)k, (const T*)xg, (const T*)xb,
       rate, bias, (const T*)dqn, (const T*)dkn, (const T*)dg, (const T*)dbeta, (T*)dq, (T*)dk,

@@ -99,7 +99,8 @@ typedef struct {
 } gdn_conv_step_shape;
 
 /* y [n_tok, C] and the cache [n_slots, W - 1, C] of the last inputs, with
- * w [C, W], b [C] (may be NULL) as in gdn_conv.h. x: 4 elements aligned. */
+ * w [C, W], b [C] (may be NULL) as in gdn_conv.h, 16-byte aligned. x: 4 elements
+ * aligned. */
 gdn_status gdn_conv_step(const gdn_conv_step_shape* shape, const void* x, const float* w,
                          const float* b, void* state, const int* slot_in, const int* slot_out,
                          const int* cu_seqlens, const int* n_commit, void* y, void* stream);
