@@ -40,134 +40,415 @@ __device__ __forceinline__ SeqCall seq_call(const Cache& c, int s) {
   return r;
 }
 
-// 4 consecutive fp32 of shared memory, read again although they have been read
-// before: the update of the state must not keep DK registers of k from the dot
-// products (the volatile load is what stops the compiler from doing that).
-__device__ __forceinline__ ulonglong2 lds4(const float* p) {
-  ulonglong2 r;
-  asm volatile("ld.volatile.shared.v2.u64 {%0, %1}, [%2];"
-               : "=l"(r.x), "=l"(r.y)
-               : "r"(smem_u32(p))
-               : "memory");
+// Blocks of 4 warps take 64 columns; calls that would not fill the GPU with
+// those (6 of them fit an SM) take blocks of 2, for twice as many SMs: one
+// sequence of 16 heads, 128 x 128, 8 tokens: 4.5 us in blocks of 2 warps, 4.9 in
+// blocks of 4; 256 sequences of 32 heads: 190 against 188 us.
+constexpr int ST_TILE = 8;  // tokens evaluated together: the N extent of the MMAs
+constexpr int ST_WARPS = 24;  // warps of an SM: what its shared memory holds states for
+constexpr int ST_WIDE_COLS = 152 * (ST_WARPS / 4) * 64;  // columns of a call for blocks of 64
+
+// Two consecutive elements.
+__device__ __forceinline__ void ld2(const float* p, float* v) {
+  const float2 a = *reinterpret_cast<const float2*>(p);
+  v[0] = a.x;
+  v[1] = a.y;
+}
+__device__ __forceinline__ void ld2(const __nv_bfloat16* p, float* v) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+  v[0] = __uint_as_float(u << 16);
+  v[1] = __uint_as_float(u & 0xffff0000u);
+}
+
+__device__ __forceinline__ void st2(float* p, float a, float b) {
+  *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
+__device__ __forceinline__ void st2(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+
+// Shared memory read again: an ordinary load would be merged with the one for
+// the dot products, and the whole state kept in registers between the two.
+__device__ __forceinline__ float2 ld2_again(const float* p) {
+  float2 r;
+  asm volatile("ld.volatile.shared.v2.f32 {%0, %1}, [%2];"
+               : "=f"(r.x), "=f"(r.y)
+               : "r"(smem_u32(p)));
   return r;
 }
 
-constexpr int ST_TILE = 8;  // tokens prepared together
+// fp32 as two TF32 values (11 bits each of the significand).
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+}
+// Two values of k or q as TF32 operands: bf16 values are exact in the first
+// part, fp32 ones take both.
+__device__ __forceinline__ void operand2(const __nv_bfloat16* p, uint32_t* hi, uint32_t*) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+  hi[0] = u << 16;
+  hi[1] = u & 0xffff0000u;
+}
+__device__ __forceinline__ void operand2(const float* p, uint32_t* hi, uint32_t* lo) {
+  const float2 u = *reinterpret_cast<const float2*>(p);
+  split_tf32(u.x, hi[0], lo[0]);
+  split_tf32(u.y, hi[1], lo[1]);
+}
+__device__ __forceinline__ void operand1(const __nv_bfloat16* p, uint32_t& hi, uint32_t&) {
+  hi = (uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16;
+}
+__device__ __forceinline__ void operand1(const float* p, uint32_t& hi, uint32_t& lo) {
+  split_tf32(*p, hi, lo);
+}
+// D = A B
+__device__ __forceinline__ void mma_tf32z(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 
-// One warp: 32 value columns of one head of one sequence, a whole column of
-// the state (DK rows) in each lane's registers. With c = S^T k and p = S^T q of
-// the old state,
-//   u = beta (v - alpha c),   S <- alpha S + k u^T,   o = alpha p + (q.k) u,
-// so a lane needs nothing from other lanes: a token is one pass over its
-// registers for c and p and one for the update, with k and q broadcast from
-// shared memory. The block's warps share the head; its threads prepare ST_TILE
-// tokens' k, q, v, alpha, beta together.
-template <typename T, int DK, int dv>
-__global__ void __launch_bounds__(dv < 128 ? dv : 128, (DK == 128 ? 3 : 4) * (dv < 128 ? 2 : 1))
-    k_step(Cache cache, int H, int G, long long ldq, long long ldk,
-           long long ldv, long long ldg, long long ldb, float q_scale, float eps,
-           const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-           const T* __restrict__ g, const T* __restrict__ beta, const float* __restrict__ rate,
+// One block: 16 NW value columns of one head of one sequence, 16 per warp; the
+// state's columns stay in shared memory. ST_TILE tokens at a time, with S the
+// state before them, Gamma_t = alpha_0 .. alpha_t and D_tj = alpha_{j+1} .. alpha_t
+// (running products, no quotients of decays):
+//   c_t = S^T k_t, p_t = S^T q_t
+//   u_t = beta_t (v_t - Gamma_t c_t - sum_{j<t} D_tj (k_t.k_j) u_j)
+//   o_t = Gamma_t p_t + sum_{j<=t} D_tj (q_t.k_j) u_j
+//   S  <- Gamma_n S + sum_j (D_nj k_j) u_j^T
+// which is the token-by-token rule with the state's updates inside the tile
+// written out, so the state is read and written once per tile. c, p, the dot
+// products and the sum over tokens in the last line are m16n8k8 TF32 MMAs; fp32
+// operands (the state, u, fp32 k and q) are taken as two TF32 parts each, so
+// products are good to about 2^-21. k and q are used as they are in memory; their
+// norms scale the results. S^T (16 columns x 8 rows) is read as A fragments with
+// the reduced rows in the order 0 2 4 6 1 3 5 7, in which the fragment is also the
+// accumulator's of the update. The state itself is only ever updated by an fp32
+// multiply-add (the tensor core's own accumulation would truncate). The sums over
+// j are done with selects, never by multiplying with zero: a token that is NaN
+// leaves the tokens before it alone. A tile of one token (generation) takes fp32
+// multiply-adds in the same layout: the MMAs would use an eighth of their N.
+// Lane (g, t) = (lane / 4, lane % 4): columns 2g, 2g + 1, tokens 2t, 2t + 1.
+//
+// Bound by the state's bytes. What decided: 24 warps per SM (states in registers
+// left room for 12 to 16, and the phases of load, compute and store did not
+// overlap: 8 tokens, 256 x 32 heads of 128 x 128, 330 us token by token, 234 in
+// tiles; in shared memory 186), the swizzle (24 warps instead of 20, 208 us), and
+// loads of whole lines (see below). 256 sequences x 32 heads of 128 x 128: one
+// token 159 us (2.1 GB, 6.8 TB/s), 8 tokens 188 us.
+template <typename T, int DK, int NW>
+struct StepTile {
+  static constexpr int COLS = 16 * NW;
+  static constexpr int LD = DK + 8;  // the rows of a fragment start in different banks
+  // the block's columns of the state; column c of row r is at c ^ (8 (r / 2 mod 4)),
+  // which puts the rows of a fragment into different banks too
+  float s[DK * COLS];
+  T k[ST_TILE * LD], q[ST_TILE * LD];
+};
+
+template <typename T, int DK, int DV, int NW>
+__global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
+    k_step(Cache cache, FastDiv byHP, int G, long long ldq, long long ldk, long long ldv,
+           long long ldg, long long ldb, float q_scale, float eps, const T* __restrict__ q,
+           const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ g,
+           const T* __restrict__ beta, const float* __restrict__ rate,
            const float* __restrict__ bias, float* S, T* __restrict__ o) {
-  constexpr int E = DK / 32;  // elements of k and q per lane while preparing
-  constexpr int nt = dv < 128 ? dv : 128, parts = dv / nt;  // threads, blocks per head
-  __shared__ __align__(16) float sk[ST_TILE][DK], sq[ST_TILE][DK];
-  __shared__ float sv[ST_TILE][nt];
-  __shared__ float4 sc4[ST_TILE];  // alpha, beta, q.k
-  const uint32_t hp = blockIdx.x % (uint32_t)(H * parts), seq = blockIdx.x / (uint32_t)(H * parts);
+  using Tile = StepTile<T, DK, NW>;
+  constexpr int COLS = Tile::COLS, PARTS = DV / COLS, KS = DK / 8, NT = NW * 32;
+  constexpr int LD = Tile::LD;
+  constexpr int EP = 16 / (int)sizeof(T);      // elements of 16 bytes
+  constexpr int KP = DK / EP;                  // 16-byte pieces of a row
+  constexpr int RP = COLS / 4;                 // of a state row
+  constexpr int SB = 4;                        // 8-row steps whose loads go ahead of their stores
+  constexpr bool TWO = sizeof(T) == 4;         // k and q take two parts
+  extern __shared__ __align__(16) unsigned char smem[];
+  Tile& sm = *reinterpret_cast<Tile*>(smem);
+  uint32_t seq, hp;
+  byHP(blockIdx.x, seq, hp);
   const SeqCall sc = seq_call(cache, seq);
   if (sc.len == 0 && !sc.store) return;
-  const int h = hp / parts;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c0 = (hp - h * parts) * nt, col = c0 + tid;  // this lane's column
-  f32x2 st[DK / 2];
-  if (sc.in >= 0) {
-    const float* p = S + ((size_t)sc.in * H + h) * DK * dv + col;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lg = lane >> 2, lt = lane & 3;
+  const int H = (int)byHP.d / PARTS, h = hp / PARTS, c0 = (hp - h * PARTS) * COLS;
+  const int lcol = warp * 16 + 2 * lg;  // this lane's first column of the block's
+  auto tile = [&](int tb) {
+    int n = min(ST_TILE, sc.len - tb);
+    if (sc.store && tb < sc.commit) n = min(n, sc.commit - tb);  // a tile ends at the commit
+    return n;
+  };
+  // A tile's rows of k and q into shared memory (rows past nb: zeros), its gates
+  // (lane i: token i mod 8) and v (this lane's columns and tokens) into registers.
+  float al, be, a[2][2];
+  auto fetch = [&](int tb, int nb) {
+    for (int i = tid; i < ST_TILE * 2 * KP; i += NT) {
+      const int t = i / (2 * KP), e = i % KP * EP;
+      const bool is_q = i / KP & 1;
+      const size_t row = (size_t)(sc.t0 + tb + (t < nb ? t : 0));
+      cp16((is_q ? sm.q : sm.k) + t * LD + e,
+           (is_q ? q + row * ldq : k + row * ldk) + (size_t)(h / G) * DK + e, t < nb);
+    }
+    al = be = 0.f;
+    if ((lane & 7) < nb) {
+      const size_t row = (size_t)(sc.t0 + tb + (lane & 7));
+      al = ldf(g + row * ldg + h);
+      be = ldf(beta + row * ldb + h);
+    }
 #pragma unroll
-    for (int r = 0; r < DK / 2; ++r)
-      st[r] = pack2(p[(size_t)(2 * r) * dv], p[(size_t)(2 * r + 1) * dv]);
-  } else {
-#pragma unroll
-    for (int r = 0; r < DK / 2; ++r) st[r] = 0;
-  }
-  auto store = [&]() {
-    float* p = S + ((size_t)sc.out * H + h) * DK * dv + col;
-#pragma unroll
-    for (int r = 0; r < DK / 2; ++r) {
-      float lo, hi;
-      unpack2(st[r], lo, hi);
-      p[(size_t)(2 * r) * dv] = lo;
-      p[(size_t)(2 * r + 1) * dv] = hi;
+    for (int y = 0; y < 2; ++y) {
+      a[0][y] = a[1][y] = 0.f;
+      if (2 * lt + y < nb) {
+        float x[2];
+        ld2(v + (size_t)(sc.t0 + tb + 2 * lt + y) * ldv + (size_t)h * DV + c0 + lcol, x);
+        a[0][y] = x[0];
+        a[1][y] = x[1];
+      }
     }
   };
-  if (sc.store && sc.commit == 0) store();
-  for (int tb = 0; tb < sc.len; tb += ST_TILE) {
-    const int nb = min(ST_TILE, sc.len - tb);
-    if (tb) __syncthreads();  // the tile before is done with
-    for (int i = warp; i < nb; i += nt >> 5) {
-      const size_t row = (size_t)(sc.t0 + tb + i);
-      const T* qp = q + row * ldq + (size_t)(h / G) * DK + lane * E;
-      const T* kp = k + row * ldk + (size_t)(h / G) * DK + lane * E;
-      float qv[E], kv[E], qq = 0.f, kk = 0.f, qk = 0.f;
+  int nb = tile(0);
+  if (nb > 0) fetch(0, nb);
+  // The block's part of the state, whole 128-byte lines at a time: an SM gets
+  // about one line request in 5 cycles to L2, so the 64 bytes that a warp's
+  // fragments take of a row would halve the rate.
+  const size_t base = ((size_t)h * DK + tid / RP) * DV + c0 + tid % RP * 4;
+  float* mine = sm.s + tid / RP * COLS + (tid % RP * 4 ^ 8 * (tid / RP >> 1 & 3));
+  static_assert(NT / RP == 8, "a thread's rows have the same swizzle");
+  if (sc.in >= 0) {
+    const float* p = S + (size_t)sc.in * H * DK * DV + base;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        qv[e] = ldf(qp + e);
-        kv[e] = ldf(kp + e);
-      }
-      float gg = ldf(g + row * ldg + h), bb = ldf(beta + row * ldb + h);
+    for (int i = 0; i < DK * RP / NT; ++i)
+      cp16(mine + i * (NT / RP) * COLS, p + i * (NT / RP) * DV, true);
+  } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        qq = fmaf(qv[e], qv[e], qq);
-        kk = fmaf(kv[e], kv[e], kk);
-        qk = fmaf(qv[e], kv[e], qk);
-      }
-      qk = lane_sum<32>(qk);
-      float qs = 1.f, ks = 1.f;
-      if (rate) {
-        qs = q_scale / sqrtf(lane_sum<32>(qq) + eps);
-        ks = 1.f / sqrtf(lane_sum<32>(kk) + eps);
-        gg = -expf(rate[h]) * softplusf_(gg + bias[h]);
-        bb = sigmoidf_(bb);
-      }
+    for (int i = 0; i < DK * RP / NT; ++i)
+      *reinterpret_cast<float4*>(mine + i * (NT / RP) * COLS) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  cp_commit();
+  auto store = [&]() {  // between barriers
+    float* p = S + (size_t)sc.out * H * DK * DV + base;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        sq[i][lane * E + e] = qv[e] * qs;
-        sk[i][lane * E + e] = kv[e] * ks;
-      }
-      if (lane == 0) sc4[i] = make_float4(expf(gg), bb, qk * qs * ks, 0.f);
+    for (int i = 0; i < DK * RP / NT; ++i)
+      *reinterpret_cast<float4*>(p + i * (NT / RP) * DV) =
+          *reinterpret_cast<const float4*>(mine + i * (NT / RP) * COLS);
+  };
+  const float er = rate ? -expf(rate[h]) : 0.f, bi = rate ? bias[h] : 0.f;
+  // This lane's state elements of 8 rows: (column 2g, row 8s+2t), (2g+1, ..), and row 8s+2t+1
+  float* frag = sm.s + 2 * lt * COLS + (lcol ^ 8 * lt);
+  if (sc.store && sc.commit == 0) {
+    cp_wait<0>();  // a thread's own pieces
+    store();
+  }
+  for (int tb = 0; tb < sc.len; tb += nb) {
+    if (tb) {
+      nb = tile(tb);
+      __syncthreads();  // the tile before is done with
+      fetch(tb, nb);
+      cp_commit();
     }
-    {
-      const T* vp = v + (size_t)(sc.t0 + tb) * ldv + (size_t)h * dv + col;
-#pragma unroll
-      for (int i = 0; i < ST_TILE; ++i)
-        if (i < nb) sv[i][tid] = ldf(vp + (size_t)i * ldv);
+    const int done = tb + nb;
+    if (rate) {
+      al = er * softplusf_(al + bi);
+      be = sigmoidf_(be);
     }
+    al = (lane & 7) < nb ? expf(al) : 1.f;
+    cp_wait<0>();
     __syncthreads();
-#pragma unroll 1
-    for (int i = 0; i < nb; ++i) {
-      const float4 f = sc4[i];
-      f32x2 c[2] = {0, 0}, p[2] = {0, 0};
+    if (nb == 1) {
+      // this lane's rows' parts of c and p of its columns, |k|^2, |q|^2, q.k
+      float c[2] = {}, p[2] = {}, n[3] = {};
 #pragma unroll
-      for (int r = 0; r < DK / 4; ++r) {
-        const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(&sk[i][4 * r]), q4 = *reinterpret_cast<const ulonglong2*>(&sq[i][4 * r]);
-        c[0] = fma2(k4.x, st[2 * r], c[0]);
-        p[0] = fma2(q4.x, st[2 * r], p[0]);
-        c[1] = fma2(k4.y, st[2 * r + 1], c[1]);
-        p[1] = fma2(q4.y, st[2 * r + 1], p[1]);
+      for (int s = 0; s < KS; ++s) {
+        float kr[2], qr[2];
+        ld2(sm.k + 8 * s + 2 * lt, kr);
+        ld2(sm.q + 8 * s + 2 * lt, qr);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float2 x = *reinterpret_cast<const float2*>(frag + (8 * s + r) * COLS);
+          c[0] = fmaf(kr[r], x.x, c[0]);
+          c[1] = fmaf(kr[r], x.y, c[1]);
+          p[0] = fmaf(qr[r], x.x, p[0]);
+          p[1] = fmaf(qr[r], x.y, p[1]);
+          n[0] = fmaf(kr[r], kr[r], n[0]);
+          n[1] = fmaf(qr[r], qr[r], n[1]);
+          n[2] = fmaf(qr[r], kr[r], n[2]);
+        }
       }
-      const float u = f.y * (sv[i][tid] - f.x * (sum2(c[0]) + sum2(c[1])));
-      const float out = fmaf(f.x, sum2(p[0]) + sum2(p[1]), f.z * u);
-      stf(o + ((size_t)(sc.t0 + tb + i) * H + h) * dv + col, out);
-      const int done = tb + i + 1;
+      const float ks = rate ? rsqrtf(lane_sum<4>(n[0]) + eps) : 1.f;
+      const float qs = rate ? q_scale * rsqrtf(lane_sum<4>(n[1]) + eps) : 1.f;
+      const float alpha = __shfl_sync(0xffffffffu, al, 0), bk = ks * __shfl_sync(0xffffffffu, be, 0);
+      const float qk = qs * lane_sum<4>(n[2]);
+      float u[2], w[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float vx = __shfl_sync(0xffffffffu, a[x][0], lane & ~3);
+        u[x] = bk * fmaf(-alpha * ks, lane_sum<4>(c[x]), vx);  // with the factor of k
+        w[x] = fmaf(alpha * qs, lane_sum<4>(p[x]), qk * u[x]);
+      }
+      if (lt == 0) {
+        T* op = o + ((size_t)(sc.t0 + tb) * H + h) * DV + c0 + lcol;
+        st2(op, w[0], w[1]);
+      }
       if (done == sc.len && !(sc.store && sc.commit == done)) break;  // nobody needs this state
-      const f32x2 aa = pack2(f.x, f.x), uu = pack2(u, u);
 #pragma unroll
-      for (int r = 0; r < DK / 4; ++r) {
-        const ulonglong2 k4 = lds4(&sk[i][4 * r]);
-        st[2 * r] = fma2(aa, st[2 * r], mul2(k4.x, uu));
-        st[2 * r + 1] = fma2(aa, st[2 * r + 1], mul2(k4.y, uu));
+      for (int s0 = 0; s0 < KS; s0 += SB) {
+        float kr[SB][2];
+        float2 old[SB][2];
+#pragma unroll
+        for (int s = 0; s < SB; ++s) {
+          ld2(sm.k + 8 * (s0 + s) + 2 * lt, kr[s]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) old[s][r] = ld2_again(frag + (8 * (s0 + s) + r) * COLS);
+        }
+#pragma unroll
+        for (int s = 0; s < SB; ++s)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float2*>(frag + (8 * (s0 + s) + r) * COLS) =
+                make_float2(fmaf(alpha, old[s][r].x, kr[s][r] * u[0]),
+                            fmaf(alpha, old[s][r].y, kr[s][r] * u[1]));
       }
-      if (sc.store && done == sc.commit) store();
+      if (sc.store && done == sc.commit) {
+        __syncthreads();
+        store();
+      }
+      continue;
+    }
+    // c, p [column][token] and dot products [k token, q token][k token]; the
+    // second parts of the split products are summed apart
+    float c[2][4] = {}, p[2][4] = {}, d[2][4] = {}, k2 = 0.f, q2 = 0.f;
+    const T *kp = sm.k + lg * LD + 2 * lt, *qp = sm.q + lg * LD + 2 * lt;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      uint32_t kh[2], kl[2], qh[2], ql[2], sh[4], sl[4];
+      operand2(kp + 8 * s, kh, kl);
+      operand2(qp + 8 * s, qh, ql);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 x = *reinterpret_cast<const float2*>(frag + (8 * s + r) * COLS);
+        split_tf32(x.x, sh[2 * r], sl[2 * r]);
+        split_tf32(x.y, sh[2 * r + 1], sl[2 * r + 1]);
+      }
+      mma_tf32(c[0], sh, kh[0], kh[1]);
+      mma_tf32(p[0], sh, qh[0], qh[1]);
+      const uint32_t ah[4] = {kh[0], qh[0], kh[1], qh[1]};
+      mma_tf32(d[0], ah, kh[0], kh[1]);
+      mma_tf32(c[1], sl, kh[0], kh[1]);
+      mma_tf32(p[1], sl, qh[0], qh[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = __uint_as_float(kh[i]), y = __uint_as_float(qh[i]);
+        if (TWO) x += __uint_as_float(kl[i]), y += __uint_as_float(ql[i]);
+        k2 = fmaf(x, x, k2);
+        q2 = fmaf(y, y, q2);
+      }
+      if (TWO) {
+        const uint32_t al4[4] = {kl[0], ql[0], kl[1], ql[1]};
+        mma_tf32(d[1], ah, kl[0], kl[1]);
+        mma_tf32(c[1], sh, kl[0], kl[1]);
+        mma_tf32(p[1], sh, ql[0], ql[1]);
+        mma_tf32(d[1], al4, kh[0], kh[1]);
+      }
+    }
+    float ks = 1.f, qs = 1.f;  // factors of k and q of token g
+    if (rate) {
+      ks = rsqrtf(lane_sum<4>(k2) + eps);
+      qs = q_scale * rsqrtf(lane_sum<4>(q2) + eps);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[0][i] += c[1][i];
+      p[0][i] += p[1][i];
+      d[0][i] = (d[0][i] + d[1][i]) * (i < 2 ? ks : qs);  // rows: k token g, q token g
+    }
+    // Of this lane's tokens t = 2 lt + y: f[y] = Gamma_t, last[y] = D_nt and, for
+    // j <= t, the factors of u_j: ek[y][j] = -D_tj k_t.k_j, eq[y][j] = D_tj q_t.k_j.
+    float ek[2][ST_TILE], eq[2][ST_TILE], f[2] = {1.f, 1.f}, last[2] = {1.f, 1.f}, gamma = 1.f;
+#pragma unroll
+    for (int j = ST_TILE - 1; j >= 0; --j) {
+      const float aj = __shfl_sync(0xffffffffu, al, j);
+      gamma *= aj;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int from = 8 * lt + 4 * y + (j >> 1);  // row t of d
+        ek[y][j] = -f[y] * __shfl_sync(0xffffffffu, d[0][j & 1], from);
+        eq[y][j] = f[y] * __shfl_sync(0xffffffffu, d[0][2 + (j & 1)], from);
+        if (j <= 2 * lt + y)
+          f[y] *= aj;
+        else
+          last[y] *= aj;
+      }
+    }
+    float w[2][2], bt[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int t = 2 * lt + y;
+      const float kt = __shfl_sync(0xffffffffu, ks, 4 * t);
+      const float qt = __shfl_sync(0xffffffffu, qs, 4 * t);
+      bt[y] = kt * __shfl_sync(0xffffffffu, be, t);  // u_j = beta_j a_j, with the factor of k_j
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        a[x][y] = fmaf(-f[y] * kt, c[0][2 * x + y], a[x][y]);
+        w[x][y] = f[y] * qt * p[0][2 * x + y];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < ST_TILE; ++j) {
+      if (j >= nb) break;
+      const int src = (lane & ~3) | (j >> 1);
+      const float u0 = __shfl_sync(0xffffffffu, bt[j & 1] * a[0][j & 1], src);
+      const float u1 = __shfl_sync(0xffffffffu, bt[j & 1] * a[1][j & 1], src);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int t = 2 * lt + y;
+        if (t > j) {
+          a[0][y] = fmaf(ek[y][j], u0, a[0][y]);
+          a[1][y] = fmaf(ek[y][j], u1, a[1][y]);
+        }
+        if (t >= j) {
+          w[0][y] = fmaf(eq[y][j], u0, w[0][y]);
+          w[1][y] = fmaf(eq[y][j], u1, w[1][y]);
+        }
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      if (2 * lt + y < nb) {
+        T* op = o + ((size_t)(sc.t0 + tb + 2 * lt + y) * H + h) * DV + c0 + lcol;
+        st2(op, w[0][y], w[1][y]);
+      }
+    if (done == sc.len && !(sc.store && sc.commit == done)) break;  // nobody needs this state
+    uint32_t uh[4], ul[4];  // A fragment of D_nj u_j: columns x tokens
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        split_tf32(2 * lt + y < nb ? last[y] * (bt[y] * a[x][y]) : 0.f, uh[2 * y + x],
+                   ul[2 * y + x]);
+#pragma unroll
+    for (int s0 = 0; s0 < KS; s0 += SB) {
+      float e[SB][4];
+      float2 old[SB][2];
+#pragma unroll
+      for (int s = 0; s < SB; ++s) {
+        uint32_t kh[2], kl[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          operand1(sm.k + (2 * lt + y) * LD + 8 * (s0 + s) + lg, kh[y], kl[y]);
+          old[s][y] = *reinterpret_cast<const float2*>(frag + (8 * (s0 + s) + y) * COLS);
+        }
+        mma_tf32z(e[s], ul, kh[0], kh[1]);
+        if (TWO) mma_tf32(e[s], uh, kl[0], kl[1]);
+        mma_tf32(e[s], uh, kh[0], kh[1]);
+      }
+#pragma unroll
+      for (int s = 0; s < SB; ++s)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          *reinterpret_cast<float2*>(frag + (8 * (s0 + s) + r) * COLS) =
+              make_float2(fmaf(gamma, old[s][r].x, e[s][r]), fmaf(gamma, old[s][r].y, e[s][2 + r]));
+    }
+    if (sc.store && done == sc.commit) {
+      __syncthreads();
+      store();
     }
   }
 }
@@ -281,14 +562,22 @@ gdn_status check_cache(int N, int n_tok, int n_slots, const int* slot_in, const 
   return GDN_OK;
 }
 
-template <typename T, int DK, int DV>
-void launch_step(const gdn_step_shape& s, const Cache& c, const void* q, const void* k,
-                 const void* v, const void* g, const void* beta, const float* rate,
-                 const float* bias, float* S, void* o, cudaStream_t st) {
-  constexpr int nt = DV < 128 ? DV : 128;
-  k_step<T, DK, DV><<<(unsigned)s.N * s.H * (DV / nt), nt, 0, st>>>(
-      c, s.H, s.H / s.Hk, s.ldq, s.ldk, s.ldv, s.ldg, s.ldb, s.q_scale, s.eps, (const T*)q,
-      (const T*)k, (const T*)v, (const T*)g, (const T*)beta, rate, bias, S, (T*)o);
+template <typename T, int DK, int DV, int NW>
+void launch_step_warps(const gdn_step_shape& s, const Cache& c, const void* q, const void* k,
+                       const void* v, const void* g, const void* beta, const float* rate,
+                       const float* bias, float* S, void* o, cudaStream_t st) {
+  constexpr int smem = sizeof(StepTile<T, DK, NW>), parts = DV / (16 * NW);
+  static_assert(smem <= 48 << 10, "what a kernel may use without asking");
+  k_step<T, DK, DV, NW><<<(unsigned)s.N * s.H * parts, NW * 32, smem, st>>>(
+      c, FastDiv(s.H * parts), s.H / s.Hk, s.ldq, s.ldk, s.ldv, s.ldg, s.ldb, s.q_scale, s.eps,
+      (const T*)q, (const T*)k, (const T*)v, (const T*)g, (const T*)beta, rate, bias, S, (T*)o);
+}
+template <typename T, int DK, int DV, typename... A>
+void launch_step(const gdn_step_shape& s, A... a) {
+  if ((long long)s.N * s.H * DV < ST_WIDE_COLS)
+    launch_step_warps<T, DK, DV, 2>(s, a...);
+  else
+    launch_step_warps<T, DK, DV, 4>(s, a...);
 }
 template <typename T, int DK, typename... A>
 void dispatch_step(const gdn_step_shape& s, A... a) {
@@ -339,7 +628,7 @@ gdn_status gdn_step(const gdn_step_shape* shape, const void* q, const void* k, c
   if (e != GDN_OK) return e;
   if (s.H < 1 || s.Hk < 1 || s.H % s.Hk) return GDN_ERR_INVALID_ARG;
   if (!dtype_ok(s.dtype) || (s.dk != 64 && s.dk != 128) ||
-      (s.dv != 64 && s.dv != 128 && s.dv != 256) || 2ll * s.N * s.H >= (1ll << 31))
+      (s.dv != 64 && s.dv != 128 && s.dv != 256) || 8ll * s.N * s.H >= (1ll << 31))
     return GDN_ERR_UNSUPPORTED;
   if (s.n_tok > 0 && (!q || !k || !v || !g || !beta || !o)) return GDN_ERR_INVALID_ARG;
   if ((s.n_slots > 0 && !S) || (rate == nullptr) != (bias == nullptr)) return GDN_ERR_INVALID_ARG;
