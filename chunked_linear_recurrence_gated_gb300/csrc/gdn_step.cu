@@ -172,9 +172,9 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
   const int H = (int)byHP.d / PARTS, h = hp / PARTS, c0 = (hp - h * PARTS) * COLS;
   const int lcol = warp * 16 + 2 * lg;  // this lane's first column of the block's
   auto tile = [&](int tb) {
-    int n = min(ST_TILE, sc.len - tb);
-    if (sc.store && tb < sc.commit) n = min(n, sc.commit - tb);  // a tile ends at the commit
-    return n;
+    const int n = min(ST_TILE, sc.len - tb), c = sc.commit - tb;
+    // a tile that is not the last one ends at the commit
+    return sc.store && c > 0 && c < n && tb + n < sc.len ? c : n;
   };
   // A tile's rows of k and q into shared memory (rows past nb: zeros), its gates
   // (lane i: token i mod 8) and v (this lane's columns and tokens) into registers.
@@ -245,6 +245,9 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
       cp_commit();
     }
     const int done = tb + nb;
+    // whether the state after the tile's first nu tokens is needed
+    const bool keep = sc.store && tb < sc.commit && sc.commit <= done;
+    const int nu = keep ? sc.commit - tb : nb;
     if (rate) {
       al = er * softplusf_(al + bi);
       be = sigmoidf_(be);
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
         T* op = o + ((size_t)(sc.t0 + tb) * H + h) * DV + c0 + lcol;
         st2(op, w[0], w[1]);
       }
-      if (done == sc.len && !(sc.store && sc.commit == done)) break;  // nobody needs this state
+      if (done == sc.len && !keep) break;
 #pragma unroll
       for (int s0 = 0; s0 < KS; s0 += SB) {
         float kr[SB][2];
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
                 make_float2(fmaf(alpha, old[s][r].x, kr[s][r] * u[0]),
                             fmaf(alpha, old[s][r].y, kr[s][r] * u[1]));
       }
-      if (sc.store && done == sc.commit) {
+      if (keep) {
         __syncthreads();
         store();
       }
@@ -359,13 +362,13 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
       p[0][i] += p[1][i];
       d[0][i] = (d[0][i] + d[1][i]) * (i < 2 ? ks : qs);  // rows: k token g, q token g
     }
-    // Of this lane's tokens t = 2 lt + y: f[y] = Gamma_t, last[y] = D_nt and, for
+    // Of this lane's tokens t = 2 lt + y: f[y] = Gamma_t, last[y] = D_nt (n = nu) and, for
     // j <= t, the factors of u_j: ek[y][j] = -D_tj k_t.k_j, eq[y][j] = D_tj q_t.k_j.
     float ek[2][ST_TILE], eq[2][ST_TILE], f[2] = {1.f, 1.f}, last[2] = {1.f, 1.f}, gamma = 1.f;
 #pragma unroll
     for (int j = ST_TILE - 1; j >= 0; --j) {
       const float aj = __shfl_sync(0xffffffffu, al, j);
-      gamma *= aj;
+      if (j < nu) gamma *= aj;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int from = 8 * lt + 4 * y + (j >> 1);  // row t of d
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
         eq[y][j] = f[y] * __shfl_sync(0xffffffffu, d[0][2 + (j & 1)], from);
         if (j <= 2 * lt + y)
           f[y] *= aj;
-        else
+        else if (j < nu)
           last[y] *= aj;
       }
     }
@@ -415,13 +418,13 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
         T* op = o + ((size_t)(sc.t0 + tb + 2 * lt + y) * H + h) * DV + c0 + lcol;
         st2(op, w[0][y], w[1][y]);
       }
-    if (done == sc.len && !(sc.store && sc.commit == done)) break;  // nobody needs this state
+    if (done == sc.len && !keep) break;
     uint32_t uh[4], ul[4];  // A fragment of D_nj u_j: columns x tokens
 #pragma unroll
     for (int y = 0; y < 2; ++y)
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        split_tf32(2 * lt + y < nb ? last[y] * (bt[y] * a[x][y]) : 0.f, uh[2 * y + x],
+        split_tf32(2 * lt + y < nu ? last[y] * (bt[y] * a[x][y]) : 0.f, uh[2 * y + x],
                    ul[2 * y + x]);
 #pragma unroll
     for (int s0 = 0; s0 < KS; s0 += SB) {
@@ -433,6 +436,7 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           operand1(sm.k + (2 * lt + y) * LD + 8 * (s0 + s) + lg, kh[y], kl[y]);
+          if (2 * lt + y >= nu) kh[y] = kl[y] = 0;  // 0 times a NaN would reach the state
           old[s][y] = *reinterpret_cast<const float2*>(frag + (8 * (s0 + s) + y) * COLS);
         }
         mma_tf32z(e[s], ul, kh[0], kh[1]);
@@ -446,7 +450,7 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
           *reinterpret_cast<float2*>(frag + (8 * (s0 + s) + r) * COLS) =
               make_float2(fmaf(gamma, old[s][r].x, e[s][r]), fmaf(gamma, old[s][r].y, e[s][2 + r]));
     }
-    if (sc.store && done == sc.commit) {
+    if (keep) {
       __syncthreads();
       store();
     }
@@ -454,8 +458,8 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
 }
 
 constexpr int CS_NT = 128;  // threads of a block, 4 channels each
-constexpr int CS_LA = 4;    // tokens loaded ahead
-constexpr int CS_BLOCKS = 152 * 8;
+constexpr int CS_LA = 4;    // tokens of a sequence loaded ahead
+constexpr int CS_BLOCKS = 152 * 16;  // twice what is resident, so that blocks overlap
 
 // 4 channels as loaded, converted when used.
 template <typename T>
@@ -491,64 +495,99 @@ __device__ __forceinline__ void st4(__nv_bfloat16* p, const float* v) {
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// One thread: 4 channels, whose weights it keeps, of every gridDim.y-th
-// sequence; the last W - 1 inputs in registers, the next CS_LA tokens' loads in flight.
+// 4 channels into shared memory without a register in between.
+__device__ __forceinline__ void cp4(Raw4<float>* to, const float* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(to)), "l"(p));
+}
+__device__ __forceinline__ void cp4(Raw4<__nv_bfloat16>* to, const __nv_bfloat16* p) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(to)), "l"(p));
+}
+
+// Sequences whose inputs a thread has in flight: 3, or what 48 KB hold.
 template <typename T, int W>
-__global__ void __launch_bounds__(CS_NT)
+constexpr int conv_stages() {
+  constexpr int one = (W - 1 + CS_LA) * CS_NT * (int)sizeof(Raw4<T>);
+  return 3 * one <= 48 << 10 ? 3 : 2;
+}
+
+// One thread: 4 channels, whose weights it keeps, of every gridDim.y-th
+// sequence; the last W - 1 inputs in registers. Bound by the bytes of the cache
+// and of x and y, behind the latency of the index entries and then of the inputs:
+// the cached rows and the first CS_LA new ones of the next sequences are in
+// flight into shared-memory slots that only this thread reads. 1024 sequences of
+// 6144 bf16 channels, one token: 25 us (97 MB, 3.8 TB/s); with plain loads 29, two
+// sequences ahead in registers 38.
+template <typename T, int W>
+__global__ void __launch_bounds__(CS_NT, W <= 4 && sizeof(T) == 2 ? 8 : 4)
     k_conv_step(Cache cache, int C, int act, long long ldx, const T* __restrict__ x,
                 const float* __restrict__ w, const float* __restrict__ b, T* state,
                 T* __restrict__ y) {
+  constexpr int ST = conv_stages<T, W>(), SLOTS = W - 1 + CS_LA;
+  __shared__ __align__(16) Raw4<T> ring[ST * SLOTS * CS_NT];
   const int c0 = (blockIdx.x * CS_NT + threadIdx.x) * 4;
   if (c0 >= C) return;
+  x += c0, y += c0, state += c0;
+  Raw4<T>* mine = ring + threadIdx.x;  // slot i of stage s: mine[(s SLOTS + i) CS_NT]
+  auto fetch = [&](int stage, int seq) {
+    if (seq < cache.N) {
+      const SeqCall sc = seq_call(cache, seq);
+      Raw4<T>* to = mine + stage * SLOTS * CS_NT;
+      if (sc.in >= 0 && (sc.len > 0 || sc.store)) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+          cp4(to + j * CS_NT, state + ((size_t)sc.in * (W - 1) + j) * C);
+      }
+#pragma unroll
+      for (int u = 0; u < CS_LA; ++u)
+        if (u < sc.len) cp4(to + (W - 1 + u) * CS_NT, x + (size_t)(sc.t0 + u) * ldx);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < ST; ++s) fetch(s, blockIdx.y + s * gridDim.y);
   float wr[4 * W], br[4] = {};
 #pragma unroll
   for (int i = 0; i < W; ++i) cvt4(ldraw4(w + (size_t)c0 * W + 4 * i), wr + 4 * i);
   if (b) cvt4(ldraw4(b + c0), br);
+  int stage = 0;
   for (int seq = blockIdx.y; seq < cache.N; seq += gridDim.y) {
     const SeqCall sc = seq_call(cache, seq);
-    if (sc.len == 0 && !sc.store) continue;
-    const T* xp = x + (size_t)sc.t0 * ldx + c0;
-    Raw4<T> xr[CS_LA];
-#pragma unroll
-    for (int u = 0; u < CS_LA; ++u)
-      if (u < sc.len) xr[u] = ldraw4(xp + (size_t)u * ldx);
+    cp_wait<ST - 1>();
+    const Raw4<T>* from = mine + stage * SLOTS * CS_NT;
     float win[W - 1][4] = {};
     if (sc.in >= 0) {
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-        cvt4(ldraw4(state + ((size_t)sc.in * (W - 1) + j) * C + c0), win[j]);
+      for (int j = 0; j < W - 1; ++j) cvt4(from[j * CS_NT], win[j]);
     }
     auto store = [&]() {
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-        st4(state + ((size_t)sc.out * (W - 1) + j) * C + c0, win[j]);
+      for (int j = 0; j < W - 1; ++j) st4(state + ((size_t)sc.out * (W - 1) + j) * C, win[j]);
     };
     if (sc.store && sc.commit == 0) store();
-    T* yp = y + (size_t)sc.t0 * C + c0;
-    for (int t0 = 0; t0 < sc.len; t0 += CS_LA) {
+    Raw4<T> past;  // the next token's input past the first CS_LA
+    if (sc.len > CS_LA) past = ldraw4(x + (size_t)(sc.t0 + CS_LA) * ldx);
+    for (int t = 0; t < sc.len; ++t) {
+      float xc[4], out[4];
+      cvt4(t < CS_LA ? from[(W - 1 + t) * CS_NT] : past, xc);
+      if (t >= CS_LA && t + 1 < sc.len) past = ldraw4(x + (size_t)(sc.t0 + t + 1) * ldx);
 #pragma unroll
-      for (int u = 0; u < CS_LA; ++u) {
-        const int t = t0 + u;
-        if (t >= sc.len) break;
-        float xc[4], out[4];
-        cvt4(xr[u], xc);
-        if (t + CS_LA < sc.len) xr[u] = ldraw4(xp + (size_t)(t + CS_LA) * ldx);
+      for (int i = 0; i < 4; ++i) {
+        float z = br[i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float z = br[i];
+        for (int j = 0; j < W - 1; ++j) z = fmaf(wr[i * W + j], win[j][i], z);
+        z = fmaf(wr[i * W + W - 1], xc[i], z);
+        out[i] = act == GDN_CONV_ACT_SILU ? z * sigmoid_as<T>(z) : z;
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) z = fmaf(wr[i * W + j], win[j][i], z);
-          z = fmaf(wr[i * W + W - 1], xc[i], z);
-          out[i] = act == GDN_CONV_ACT_SILU ? z * sigmoid_as<T>(z) : z;
-#pragma unroll
-          for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
-          win[W - 2][i] = xc[i];
-        }
-        st4(yp + (size_t)t * C, out);
-        if (sc.store && t + 1 == sc.commit) store();
+        for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
+        win[W - 2][i] = xc[i];
       }
+      st4(y + (size_t)(sc.t0 + t) * C, out);
+      if (sc.store && t + 1 == sc.commit) store();
     }
+    fetch(stage, seq + ST * gridDim.y);  // the stage has been read
+    if (++stage == ST) stage = 0;
   }
+  cp_wait<0>();
 }
 
 // ------------------------------------------------------------------ host side

@@ -172,6 +172,23 @@ def test_step_nan_stays_in_its_head():
     assert torch.isfinite(S[:, [0, 2]]).all() and torch.isfinite(S[1]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,commit", [(2, 1), (8, 3), (12, 8), (20, 17)])
+def test_step_nan_in_a_draft_stays_behind_the_commit(dtype, n, commit):
+    """A NaN in what follows the committed tokens reaches neither the cache nor
+    the outputs before it."""
+    a = step_inputs([n], 2, 2, 64, 64, DT[dtype], False, n, 1)
+    q, k, v, g, beta, S, _, cu = a
+    S0, sound = S.clone(), [t.clone() for t in (q, k, v, g, beta)]
+    want = gdn.gdn_step(*sound, S0, cu_seqlens=cu, n_commit=i32([commit]))
+    for t in (q, k, v, g, beta):
+        t[commit:] = float("nan")
+    o = gdn.gdn_step(q, k, v, g, beta, S, cu_seqlens=cu, n_commit=i32([commit]))
+    torch.cuda.synchronize()
+    assert torch.equal(S, S0) and torch.equal(o[:commit], want[:commit])
+    assert torch.isnan(o[commit:]).all()
+
+
 @pytest.mark.parametrize("dtype,dk,dv,tol", [("f32", 64, 64, 1e-4), ("bf16", 128, 128, 2e-2),
                                              ("bf16", 128, 256, 2e-2)])
 def test_step_continues_a_chunk(dtype, dk, dv, tol):
