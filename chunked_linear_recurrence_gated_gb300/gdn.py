@@ -10,7 +10,6 @@ The function names follow the C ABI in include/gdn.h, gdn_conv.h and gdn_layer.h
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -407,19 +406,16 @@ def gdn_conv_bwd(x, w, b, state_in, dy, dstate_out=None, act="silu", dx=None, dw
 
 # ------------------------------------------------- layer operators (include/gdn_layer.h)
 # A generation step makes these calls once per layer and token, so what they do
-# on the host is kept short: one look at each tensor's shape, type and device.
-def _own_stream(fn):
-    """With stream=..., run fn with that stream current, so that what it
-    allocates (outputs, workspace) belongs to the stream its kernels run on."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
+# on the host is kept short: one condition over all arguments that holds for
+# every well-formed call (plain attribute reads, no calls of our own), and the
+# checks that name the offending argument only where it does not.
+def _on_stream(fn, stream, *args, **kw):
+    """fn with `stream` current, so that what it allocates (outputs, workspace)
+    belongs to the stream its kernels run on."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 def _raw_stream(dev):
@@ -429,10 +425,15 @@ def _raw_stream(dev):
 if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same value without a Stream object
     _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811
 
+_f32, _i32 = torch.float32, torch.int32
+_codes = {torch.float32: GDN_DTYPE_F32, torch.bfloat16: GDN_DTYPE_BF16}
 
-def _bad(name, t, shape, dtype, dev):
-    return ValueError(f"{name}: expected a contiguous {tuple(shape)} {dtype} tensor on cuda:{dev}, "
-                      f"got {tuple(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
+
+def _code(dtype):
+    code = _codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def _on_gpu(name, t, ndim):
@@ -446,15 +447,18 @@ def _on_gpu(name, t, ndim):
 
 def _want(name, t, shape, dtype, dev):
     if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
-        raise _bad(name, t, shape, dtype, dev)
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{dev}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _want_c(name, t, shape, dtype, dev):
-    """As _want, and contiguous; returns the pointer (None for an absent tensor)."""
+def _ptr(name, t, shape, dtype, dev):
+    """Pointer of a contiguous tensor (None for an absent one)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
-        raise _bad(name, t, shape, dtype, dev)
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != dev
+            or not t.is_contiguous()):
+        _want(name, t, shape, dtype, dev)
+        raise ValueError(f"{name}: must be contiguous, got strides {t.stride()}")
     return t.data_ptr()
 
 
@@ -462,10 +466,6 @@ def _rows(name, t, ndim):
     """Stride of the rows of t [..., n1, .., nk] (k = ndim trailing dimensions that
     have to be dense) when its leading dimensions flatten to one."""
     st, sh = t.stride(), t.shape
-    if st[-1] == 1 and (ndim == 1 or st[-2] == sh[-1]):  # dense rows: the usual layouts
-        lead = len(st) - ndim
-        if lead == 1 or (lead == 2 and sh[0] == 1):
-            return st[lead - 1]
     inner = 1
     for i in range(1, ndim + 1):
         if sh[-i] != 1 and st[-i] != inner:
@@ -483,13 +483,12 @@ def _rows(name, t, ndim):
     return ld
 
 
-def _index(name, t, n, dev):
-    """Pointer of an int32 index array of n entries (None for an absent one)."""
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
-        raise _bad(name, t, (n,), torch.int32, dev)
-    return t.data_ptr()
+def _cache_ptrs(N, dev, slot_in, slot_out, cu_seqlens, n_commit):
+    """Pointers of the index arrays of gdn_step and gdn_conv_step."""
+    return (None if slot_in is None else _ptr("slot_in", slot_in, (N,), _i32, dev),
+            None if slot_out is None else _ptr("slot_out", slot_out, (N,), _i32, dev),
+            None if cu_seqlens is None else _ptr("cu_seqlens", cu_seqlens, (N + 1,), _i32, dev),
+            None if n_commit is None else _ptr("n_commit", n_commit, (N,), _i32, dev))
 
 
 def _scratch(t, dev):
@@ -499,9 +498,8 @@ def _scratch(t, dev):
     return t.data_ptr(), t.nbytes
 
 
-@_own_stream
 def gdn_step(q, k, v, g, beta, S, slot_in=None, slot_out=None, cu_seqlens=None, n_commit=None,
-             gate=None, q_scale=1.0, eps=1e-6, o=None):
+             gate=None, q_scale=1.0, eps=1e-6, o=None, stream=None):
     """The gated delta rule token by token over the states S [n_slots, H, dk, dv]
     (fp32, updated in place) of N sequences whose new tokens are packed:
     q, k [n_tok, Hk, dk], v [n_tok, H, dv], g, beta [n_tok, H], rows strided.
@@ -512,227 +510,263 @@ def gdn_step(q, k, v, g, beta, S, slot_in=None, slot_out=None, cu_seqlens=None, 
     after that many of its tokens is written (None: all). All int32 on the device.
     gate = (rate, bias) [H] fp32: g and beta are the inputs of gdn_prep_fwd's maps
     and q, k are normalised. Returns o [n_tok, H, dv]."""
-    dev, dt, f32 = _on_gpu("q", q, 3), q.dtype, torch.float32
-    n, Hk, dk = q.shape
+    if stream is not None:
+        return _on_stream(gdn_step, stream, q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens,
+                          n_commit, gate, q_scale, eps, o)
+    dt, dev = q.dtype, q.get_device()
+    n, Hk, dk = shape = q.shape
     _, H, dv = v.shape
     n_slots = S.shape[0]
-    N = n if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    _want("k", k, (n, Hk, dk), dt, dev)
-    _want("v", v, (n, H, dv), dt, dev)
-    _want("g", g, (n, H), dt, dev)
-    _want("beta", beta, (n, H), dt, dev)
-    rate, bias = gate if gate is not None else (None, None)
-    s = gdn_step_shape(N, n, n_slots, H, Hk, dk, dv, _dtype_code(q), _rows("q", q, 2),
-                       _rows("k", k, 2), _rows("v", v, 2), _rows("g", g, 1),
-                       _rows("beta", beta, 1), q_scale, eps)
+    gates = (n, H)
+    sq, sk, sv, sg, sb = q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()
+    if (dev >= 0 and k.shape == shape and v.shape[0] == n and g.shape == gates
+            and beta.shape == gates and k.dtype is dt and v.dtype is dt and g.dtype is dt
+            and beta.dtype is dt and k.get_device() == dev and v.get_device() == dev
+            and g.get_device() == dev and beta.get_device() == dev
+            and sq[2] == sk[2] == sv[2] == sg[1] == sb[1] == 1 and sq[1] == sk[1] == dk
+            and sv[1] == dv):
+        ldq, ldk, ldv, ldg, ldb = sq[0], sk[0], sv[0], sg[0], sb[0]
+    else:
+        _on_gpu("q", q, 3)
+        for name, t, sh in (("k", k, shape), ("v", v, (n, H, dv)), ("g", g, gates),
+                            ("beta", beta, gates)):
+            _want(name, t, sh, dt, dev)
+        ldq, ldk, ldv = _rows("q", q, 2), _rows("k", k, 2), _rows("v", v, 2)
+        ldg, ldb = _rows("g", g, 1), _rows("beta", beta, 1)
     if o is None:
         o = torch.empty((n, H, dv), dtype=dt, device=q.device)
         po = o.data_ptr()
     else:
-        po = _want_c("o", o, (n, H, dv), dt, dev)
+        po = _ptr("o", o, (n, H, dv), dt, dev)
+    if gate is None:
+        rate = bias = None
+    else:
+        rate, bias = _ptr("rate", gate[0], (H,), _f32, dev), _ptr("bias", gate[1], (H,), _f32, dev)
+    N = n if cu_seqlens is None else cu_seqlens.shape[0] - 1
     rc = load().gdn_step(
-        s, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-        _want_c("rate", rate, (H,), f32, dev), _want_c("bias", bias, (H,), f32, dev),
-        _want_c("S", S, (n_slots, H, dk, dv), f32, dev), _index("slot_in", slot_in, N, dev),
-        _index("slot_out", slot_out, N, dev), _index("cu_seqlens", cu_seqlens, N + 1, dev),
-        _index("n_commit", n_commit, N, dev), po, _raw_stream(dev))
+        gdn_step_shape(N, n, n_slots, H, Hk, dk, dv, _code(dt), ldq, ldk, ldv, ldg, ldb, q_scale,
+                       eps),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), rate, bias,
+        _ptr("S", S, (n_slots, H, dk, dv), _f32, dev),
+        *_cache_ptrs(N, dev, slot_in, slot_out, cu_seqlens, n_commit), po, _raw_stream(dev))
     if rc:
         raise GdnError(rc, "gdn_step")
     return o
 
 
-@_own_stream
 def gdn_conv_step(x, w, b, state, slot_in=None, slot_out=None, cu_seqlens=None, n_commit=None,
-                  act="silu", y=None):
+                  act="silu", y=None, stream=None):
     """The short convolution of packed new tokens x [n_tok, C] (rows strided) over
     the cached last inputs state [n_slots, W - 1, C] (updated in place), for the
     sequences of gdn_step. Returns y [n_tok, C]."""
-    dev, dt, f32 = _on_gpu("x", x, 2), x.dtype, torch.float32
-    n, C = x.shape
+    if stream is not None:
+        return _on_stream(gdn_conv_step, stream, x, w, b, state, slot_in, slot_out, cu_seqlens,
+                          n_commit, act, y)
+    dt, dev = x.dtype, _on_gpu("x", x, 2)
+    n, C = shape = x.shape
     W, n_slots = w.shape[1], state.shape[0]
-    N = n if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    s = gdn_conv_step_shape(N, n, n_slots, C, W, _dtype_code(x), CONV_ACT[act],
-                            _rows("x", x, 1))
+    sx = x.stride()
     if y is None:
-        y = torch.empty((n, C), dtype=dt, device=x.device)
+        y = torch.empty(shape, dtype=dt, device=x.device)
         py = y.data_ptr()
     else:
-        py = _want_c("y", y, (n, C), dt, dev)
+        py = _ptr("y", y, shape, dt, dev)
+    N = n if cu_seqlens is None else cu_seqlens.shape[0] - 1
     rc = load().gdn_conv_step(
-        s, x.data_ptr(), _want_c("w", w, (C, W), f32, dev), _want_c("b", b, (C,), f32, dev),
-        _want_c("state", state, (n_slots, W - 1, C), dt, dev), _index("slot_in", slot_in, N, dev),
-        _index("slot_out", slot_out, N, dev), _index("cu_seqlens", cu_seqlens, N + 1, dev),
-        _index("n_commit", n_commit, N, dev), py, _raw_stream(dev))
+        gdn_conv_step_shape(N, n, n_slots, C, W, _code(dt), CONV_ACT[act],
+                            sx[0] if sx[1] == 1 else _rows("x", x, 1)),
+        x.data_ptr(), _ptr("w", w, (C, W), _f32, dev), _ptr("b", b, (C,), _f32, dev),
+        _ptr("state", state, (n_slots, W - 1, C), dt, dev),
+        *_cache_ptrs(N, dev, slot_in, slot_out, cu_seqlens, n_commit), py, _raw_stream(dev))
     if rc:
         raise GdnError(rc, "gdn_conv_step")
     return y
 
 
-def _prep_shape_of(q, k, xg, xb, q_scale, eps):
-    dev = _on_gpu("q", q, 4)
-    B, T, Hk, dk = q.shape
-    _, _, H = xg.shape
-    _want("k", k, (B, T, Hk, dk), q.dtype, dev)
-    _want("xg", xg, (B, T, H), q.dtype, dev)
-    _want("xb", xb, (B, T, H), q.dtype, dev)
-    return gdn_prep_shape(B * T, H, Hk, dk, _dtype_code(q), _rows("q", q, 2), _rows("k", k, 2),
-                          _rows("xg", xg, 1), _rows("xb", xb, 1), q_scale, eps)
+def _prep_shape_of(q, k, xg, xb, rate, bias, q_scale, eps):
+    """(shape, GPU, pointers of the inputs) of gdn_prep_fwd and gdn_prep_bwd."""
+    dt, dev = q.dtype, q.get_device()
+    B, T, Hk, dk = shape = q.shape
+    H = xg.shape[-1]
+    gates = (B, T, H)
+    sq, sk, sg, sb = q.stride(), k.stride(), xg.stride(), xb.stride()
+    if (dev >= 0 and B == 1 and k.shape == shape and xg.shape == gates and xb.shape == gates
+            and k.dtype is dt and xg.dtype is dt and xb.dtype is dt and k.get_device() == dev
+            and xg.get_device() == dev and xb.get_device() == dev
+            and sq[3] == sk[3] == sg[2] == sb[2] == 1 and sq[2] == sk[2] == dk):
+        ldq, ldk, ldg, ldb = sq[1], sk[1], sg[1], sb[1]
+    else:
+        _on_gpu("q", q, 4)
+        _want("k", k, shape, dt, dev)
+        _want("xg", xg, gates, dt, dev)
+        _want("xb", xb, gates, dt, dev)
+        ldq, ldk, ldg, ldb = (_rows("q", q, 2), _rows("k", k, 2), _rows("xg", xg, 1),
+                              _rows("xb", xb, 1))
+    return (gdn_prep_shape(B * T, H, Hk, dk, _code(dt), ldq, ldk, ldg, ldb, q_scale, eps), dev,
+            (q.data_ptr(), k.data_ptr(), xg.data_ptr(), xb.data_ptr(),
+             _ptr("rate", rate, (H,), _f32, dev), _ptr("bias", bias, (H,), _f32, dev)))
 
 
-@_own_stream
-def gdn_prep_fwd(q, k, xg, xb, rate, bias, q_scale=1.0, eps=1e-6):
+def gdn_prep_fwd(q, k, xg, xb, rate, bias, q_scale=1.0, eps=1e-6, stream=None):
     """The maps before the recurrence. q, k [B, T, Hk, dk] and xg, xb [B, T, H] (rows
     strided), rate, bias [H] fp32. Returns (q, k [B, T, H, dk], g, beta [B, T, H]) as
     gdn_chunk_fwd takes them: q and k of unit norm (q times q_scale), each key
     head repeated for its H / Hk value heads, g = -exp(rate) softplus(xg + bias),
     beta = sigmoid(xb)."""
-    s = _prep_shape_of(q, k, xg, xb, q_scale, eps)
+    if stream is not None:
+        return _on_stream(gdn_prep_fwd, stream, q, k, xg, xb, rate, bias, q_scale, eps)
+    s, dev, ins = _prep_shape_of(q, k, xg, xb, rate, bias, q_scale, eps)
     B, T, _, dk = q.shape
-    H, dt, dev, f32 = s.H, q.dtype, q.get_device(), torch.float32
-    at = q.device
-    qn = torch.empty(B, T, H, dk, dtype=dt, device=at)
-    kn = torch.empty(B, T, H, dk, dtype=dt, device=at)
-    g = torch.empty(B, T, H, dtype=dt, device=at)
-    beta = torch.empty(B, T, H, dtype=dt, device=at)
-    rc = load().gdn_prep_fwd(s, q.data_ptr(), k.data_ptr(), xg.data_ptr(), xb.data_ptr(),
-                             _want_c("rate", rate, (H,), f32, dev),
-                             _want_c("bias", bias, (H,), f32, dev), qn.data_ptr(), kn.data_ptr(),
-                             g.data_ptr(), beta.data_ptr(), _raw_stream(dev))
-    _check(rc, "gdn_prep_fwd")
+    dt, at = q.dtype, q.device
+    heads, gates = (B, T, s.H, dk), (B, T, s.H)
+    qn = torch.empty(heads, dtype=dt, device=at)
+    kn = torch.empty(heads, dtype=dt, device=at)
+    g = torch.empty(gates, dtype=dt, device=at)
+    beta = torch.empty(gates, dtype=dt, device=at)
+    rc = load().gdn_prep_fwd(s, *ins, qn.data_ptr(), kn.data_ptr(), g.data_ptr(),
+                             beta.data_ptr(), _raw_stream(dev))
+    if rc:
+        raise GdnError(rc, "gdn_prep_fwd")
     return qn, kn, g, beta
 
 
-@_own_stream
 def gdn_prep_bwd(q, k, xg, xb, rate, bias, dq, dk, dg, dbeta, q_scale=1.0, eps=1e-6,
-                 workspace=None):
+                 workspace=None, stream=None):
     """Gradients of gdn_prep_fwd from those of its outputs, as gdn_chunk_bwd
     returns them. Returns (dq, dk [B, T, Hk, dk], dxg, dxb [B, T, H], drate, dbias [H])."""
+    if stream is not None:
+        return _on_stream(gdn_prep_bwd, stream, q, k, xg, xb, rate, bias, dq, dk, dg, dbeta,
+                          q_scale, eps, workspace)
     lib = load()
-    s = _prep_shape_of(q, k, xg, xb, q_scale, eps)
-    B, T, Hk, D = q.shape
-    H, dt, dev, f32 = s.H, q.dtype, q.get_device(), torch.float32
-    at = q.device
+    s, dev, ins = _prep_shape_of(q, k, xg, xb, rate, bias, q_scale, eps)
+    B, T, _, D = shape = q.shape
+    H, dt, at = s.H, q.dtype, q.device
+    heads, gates = (B, T, H, D), (B, T, H)
     if workspace is None:
         workspace = alloc_workspace(lib.gdn_prep_workspace_bytes(s), at)
-    oq = torch.empty(B, T, Hk, D, dtype=dt, device=at)
-    ok = torch.empty(B, T, Hk, D, dtype=dt, device=at)
-    og = torch.empty(B, T, H, dtype=dt, device=at)
-    ob = torch.empty(B, T, H, dtype=dt, device=at)
-    par = torch.empty(2, H, dtype=f32, device=at)
-    rc = lib.gdn_prep_bwd(s, q.data_ptr(), k.data_ptr(), xg.data_ptr(), xb.data_ptr(),
-                          _want_c("rate", rate, (H,), f32, dev),
-                          _want_c("bias", bias, (H,), f32, dev),
-                          _want_c("dq", dq, (B, T, H, D), dt, dev),
-                          _want_c("dk", dk, (B, T, H, D), dt, dev),
-                          _want_c("dg", dg, (B, T, H), dt, dev),
-                          _want_c("dbeta", dbeta, (B, T, H), dt, dev), oq.data_ptr(),
-                          ok.data_ptr(), og.data_ptr(), ob.data_ptr(), par.data_ptr(),
-                          par.data_ptr() + 4 * H, *_scratch(workspace, dev), _raw_stream(dev))
-    _check(rc, "gdn_prep_bwd")
-    return oq, ok, og, ob, par[0], par[1]
+    oq = torch.empty(shape, dtype=dt, device=at)
+    ok = torch.empty(shape, dtype=dt, device=at)
+    og = torch.empty(gates, dtype=dt, device=at)
+    ob = torch.empty(gates, dtype=dt, device=at)
+    drate = torch.empty(H, dtype=_f32, device=at)
+    dbias = torch.empty(H, dtype=_f32, device=at)
+    rc = lib.gdn_prep_bwd(s, *ins, _ptr("dq", dq, heads, dt, dev), _ptr("dk", dk, heads, dt, dev),
+                          _ptr("dg", dg, gates, dt, dev), _ptr("dbeta", dbeta, gates, dt, dev),
+                          oq.data_ptr(), ok.data_ptr(), og.data_ptr(), ob.data_ptr(),
+                          drate.data_ptr(), dbias.data_ptr(), *_scratch(workspace, dev),
+                          _raw_stream(dev))
+    if rc:
+        raise GdnError(rc, "gdn_prep_bwd")
+    return oq, ok, og, ob, drate, dbias
 
 
-def _gate_norm_shape_of(o, z, act, eps):
-    B, T, H, d = o.shape
-    _want("z", z, (B, T, H, d), o.dtype, _on_gpu("o", o, 4))
-    return gdn_gate_norm_shape(B * T, H, d, _dtype_code(o), GATE_ACT[act], _rows("z", z, 2), eps)
+def _gate_norm_shape_of(o, z, w, act, eps):
+    """(shape, GPU, pointers of the inputs) of gdn_gate_norm_fwd and gdn_gate_norm_bwd."""
+    dt, dev = o.dtype, _on_gpu("o", o, 4)
+    B, T, H, d = shape = o.shape
+    sz = z.stride()
+    if (B == 1 and z.shape == shape and z.dtype is dt and z.get_device() == dev and sz[3] == 1
+            and sz[2] == d):
+        ldz = sz[1]
+    else:
+        _want("z", z, shape, dt, dev)
+        ldz = _rows("z", z, 2)
+    return (gdn_gate_norm_shape(B * T, H, d, _code(dt), GATE_ACT[act], ldz, eps), dev,
+            (_ptr("o", o, shape, dt, dev), z.data_ptr(), _ptr("w", w, (d,), _f32, dev)))
 
 
-@_own_stream
-def gdn_gate_norm_fwd(o, z, w, act="silu", eps=1e-6, y=None):
+def gdn_gate_norm_fwd(o, z, w, act="silu", eps=1e-6, y=None, stream=None):
     """y = rms_norm(o) * w * act(z) over the last dimension of o [B, T, H, d]; z [B, T, H, d]
     with strided token rows, w [d] fp32, act "silu" or "sigmoid"."""
-    s = _gate_norm_shape_of(o, z, act, eps)
-    dev, shape, dt, f32 = o.get_device(), o.shape, o.dtype, torch.float32
+    if stream is not None:
+        return _on_stream(gdn_gate_norm_fwd, stream, o, z, w, act, eps, y)
+    s, dev, ins = _gate_norm_shape_of(o, z, w, act, eps)
     if y is None:
-        y = torch.empty(o.shape, dtype=o.dtype, device=o.device)
-    rc = load().gdn_gate_norm_fwd(s, _want_c("o", o, shape, dt, dev), z.data_ptr(),
-                                  _want_c("w", w, (s.d,), f32, dev),
-                                  _want_c("y", y, shape, dt, dev), _raw_stream(dev))
-    _check(rc, "gdn_gate_norm_fwd")
+        y = torch.empty_like(o)
+    rc = load().gdn_gate_norm_fwd(s, *ins, _ptr("y", y, o.shape, o.dtype, dev), _raw_stream(dev))
+    if rc:
+        raise GdnError(rc, "gdn_gate_norm_fwd")
     return y
 
 
-@_own_stream
-def gdn_gate_norm_bwd(o, z, w, dy, act="silu", eps=1e-6, workspace=None):
+def gdn_gate_norm_bwd(o, z, w, dy, act="silu", eps=1e-6, workspace=None, stream=None):
     """Backward of gdn_gate_norm_fwd. Returns (do, dz, dw)."""
+    if stream is not None:
+        return _on_stream(gdn_gate_norm_bwd, stream, o, z, w, dy, act, eps, workspace)
     lib = load()
-    s = _gate_norm_shape_of(o, z, act, eps)
-    dev, shape, dt, f32 = o.get_device(), o.shape, o.dtype, torch.float32
+    s, dev, ins = _gate_norm_shape_of(o, z, w, act, eps)
     if workspace is None:
         workspace = alloc_workspace(lib.gdn_gate_norm_workspace_bytes(s), o.device)
-    do = torch.empty(o.shape, dtype=o.dtype, device=o.device)
-    dz = torch.empty(o.shape, dtype=o.dtype, device=o.device)
-    dw = torch.empty(s.d, dtype=torch.float32, device=o.device)
-    rc = lib.gdn_gate_norm_bwd(s, _want_c("o", o, shape, dt, dev), z.data_ptr(),
-                               _want_c("w", w, (s.d,), f32, dev),
-                               _want_c("dy", dy, shape, dt, dev), do.data_ptr(),
+    do, dz, dw = torch.empty_like(o), torch.empty_like(o), torch.empty_like(w)
+    rc = lib.gdn_gate_norm_bwd(s, *ins, _ptr("dy", dy, o.shape, o.dtype, dev), do.data_ptr(),
                                dz.data_ptr(), dw.data_ptr(), *_scratch(workspace, dev),
                                _raw_stream(dev))
-    _check(rc, "gdn_gate_norm_bwd")
+    if rc:
+        raise GdnError(rc, "gdn_gate_norm_bwd")
     return do, dz, dw
 
 
-def _res_norm_shape_of(h, like, eps):
-    C = h.shape[-1]
-    return gdn_res_norm_shape(h.numel() // C if C else 0, C, _dtype_code(like), _dtype_code(h),
-                              eps)
-
-
-@_own_stream
-def gdn_res_norm_fwd(h, x, w, w_post=None, scale=None, eps=1e-6, h_out=None, y=None,
-                     dtype=None):
+def gdn_res_norm_fwd(h, x, w, w_post=None, scale=None, eps=1e-6, h_out=None, y=None, dtype=None,
+                     stream=None):
     """Block boundary: h_out = h + scale * (rms_norm(x) * w_post), y = rms_norm(h_out) * w.
 
     h [..., C] is the residual stream (fp32, or x's dtype), x [..., C] the block's
     output; w, w_post, scale [C] fp32. w_post None: x as it is; scale None: 1; x None
     (before the first block): y is the norm of h, in `dtype` (default h's).
     h_out may be h. Returns (h_out, y); h_out is None where x is."""
-    dt = x.dtype if x is not None else dtype or h.dtype
-    dev, at, C, f32 = _on_gpu("h", h, 1), h.device, h.shape[-1], torch.float32
+    if stream is not None:
+        return _on_stream(gdn_res_norm_fwd, stream, h, x, w, w_post, scale, eps, h_out, y, dtype)
+    rt, dev, shape = h.dtype, _on_gpu("h", h, 1), h.shape
+    C = shape[-1]
+    row = (C,)
+    dt = x.dtype if x is not None else dtype or rt
     if y is None:
-        y = torch.empty(h.shape, dtype=dt, device=at)
+        y = torch.empty(shape, dtype=dt, device=h.device)
     if h_out is None and x is not None:
-        h_out = torch.empty(h.shape, dtype=h.dtype, device=at)
-    s = _res_norm_shape_of(h, y, eps)
-    rc = load().gdn_res_norm_fwd(s, _p(h), _want_c("x", x, h.shape, dt, dev),
-                                 _want_c("w", w, (C,), f32, dev),
-                                 _want_c("w_post", w_post, (C,), f32, dev),
-                                 _want_c("scale", scale, (C,), f32, dev),
-                                 _want_c("h_out", h_out, h.shape, h.dtype, dev),
-                                 _want_c("y", y, h.shape, dt, dev), _raw_stream(dev))
-    _check(rc, "gdn_res_norm_fwd")
+        h_out = torch.empty_like(h)
+    rc = load().gdn_res_norm_fwd(
+        gdn_res_norm_shape(h.numel() // max(C, 1), C, _code(dt), _code(rt), eps),
+        _ptr("h", h, shape, rt, dev), _ptr("x", x, shape, dt, dev), _ptr("w", w, row, _f32, dev),
+        _ptr("w_post", w_post, row, _f32, dev), _ptr("scale", scale, row, _f32, dev),
+        _ptr("h_out", h_out, shape, rt, dev), _ptr("y", y, shape, dt, dev), _raw_stream(dev))
+    if rc:
+        raise GdnError(rc, "gdn_res_norm_fwd")
     return h_out, y
 
 
-@_own_stream
 def gdn_res_norm_bwd(h_out, x, w, dy, dh_out=None, w_post=None, scale=None, eps=1e-6, dh=None,
-                     workspace=None):
+                     workspace=None, stream=None):
     """Backward of gdn_res_norm_fwd at the residual it returned (for x None: at h).
     dh may be dh_out. Returns (dh, dx, dw, dw_post, dscale); dx is dh itself where
     they are equal (no w_post, no scale, one dtype)."""
+    if stream is not None:
+        return _on_stream(gdn_res_norm_bwd, stream, h_out, x, w, dy, dh_out, w_post, scale, eps,
+                          dh, workspace)
     lib = load()
-    dev, at, C, f32 = _on_gpu("h_out", h_out, 1), h_out.device, h_out.shape[-1], torch.float32
-    s = _res_norm_shape_of(h_out, dy, eps)
+    rt, dt, dev, shape = h_out.dtype, dy.dtype, _on_gpu("h_out", h_out, 1), h_out.shape
+    C = shape[-1]
+    row = (C,)
+    s = gdn_res_norm_shape(h_out.numel() // max(C, 1), C, _code(dt), _code(rt), eps)
     if workspace is None:
-        workspace = alloc_workspace(lib.gdn_res_norm_workspace_bytes(s), at)
+        workspace = alloc_workspace(lib.gdn_res_norm_workspace_bytes(s), h_out.device)
     if dh is None:
-        dh = torch.empty(h_out.shape, dtype=h_out.dtype, device=at)
-    same = w_post is None and scale is None and (dy.dtype == h_out.dtype or x is None)
-    dx = None if same else torch.empty(h_out.shape, dtype=dy.dtype, device=at)
-    dw = torch.empty(C, dtype=f32, device=at)
-    dpost = None if w_post is None else torch.empty(C, dtype=f32, device=at)
-    dscale = None if scale is None else torch.empty(C, dtype=f32, device=at)
-    rc = lib.gdn_res_norm_bwd(s, _p(h_out), _want_c("x", x, h_out.shape, dy.dtype, dev),
-                              _want_c("w", w, (C,), f32, dev),
-                              _want_c("w_post", w_post, (C,), f32, dev),
-                              _want_c("scale", scale, (C,), f32, dev),
-                              _want_c("dy", dy, h_out.shape, dy.dtype, dev),
-                              _want_c("dh_out", dh_out, h_out.shape, h_out.dtype, dev),
-                              _want_c("dh", dh, h_out.shape, h_out.dtype, dev), _p(dx), _p(dw),
-                              _p(dpost), _p(dscale), *_scratch(workspace, dev),
-                              _raw_stream(dev))
-    _check(rc, "gdn_res_norm_bwd")
+        dh = torch.empty_like(h_out)
+    same = w_post is None and scale is None and (dt is rt or x is None)
+    dx = None if same else torch.empty_like(dy)
+    dw = torch.empty_like(w)
+    dpost = None if w_post is None else torch.empty_like(w_post)
+    dscale = None if scale is None else torch.empty_like(scale)
+    rc = lib.gdn_res_norm_bwd(
+        s, _ptr("h_out", h_out, shape, rt, dev), _ptr("x", x, shape, dt, dev),
+        _ptr("w", w, row, _f32, dev), _ptr("w_post", w_post, row, _f32, dev),
+        _ptr("scale", scale, row, _f32, dev), _ptr("dy", dy, shape, dt, dev),
+        _ptr("dh_out", dh_out, shape, rt, dev), _ptr("dh", dh, shape, rt, dev),
+        None if dx is None else dx.data_ptr(), dw.data_ptr(),
+        None if dpost is None else dpost.data_ptr(),
+        None if dscale is None else dscale.data_ptr(), *_scratch(workspace, dev),
+        _raw_stream(dev))
+    if rc:
+        raise GdnError(rc, "gdn_res_norm_bwd")
     return dh, (dh if same else dx), dw, dpost, dscale
 
 
