@@ -1,15 +1,20 @@
-"""Build libgdn.so (the C-ABI library of sm_103a CUDA kernels) in-tree.
+"""Build libgdn.so (the C-ABI library of sm_103a CUDA kernels) in-tree, and
+``_gdn_torch``, the host-side Python entry of the layer operators.
 
-Each translation unit under csrc/ is compiled by its own nvcc process (in
-parallel), then linked into ``_build/libgdn.so``. Only sm_103a is targeted.
+Each translation unit under csrc/ is compiled by its own process (in parallel),
+then linked into ``_build/libgdn.so`` (the .cu files; only sm_103a is targeted)
+and ``_build/_gdn_torch.so`` (gdn_torch.cpp, against the installed torch's
+headers; it is rebuilt when torch or Python changes).
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +22,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libgdn.so")
 INCLUDE = os.path.join(ROOT, "include")
+EXT = os.path.join(OUT, "_gdn_torch.so")
+EXT_SRC = os.path.join(CSRC, "gdn_torch.cpp")
+EXT_FOR = os.path.join(OUT, "_gdn_torch.for")  # what the extension was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -34,22 +42,64 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _torch_root() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch not found: its headers are required to build _gdn_torch")
+    return os.path.dirname(spec.origin)
+
+
+def _built_for() -> str:
+    with open(os.path.join(_torch_root(), "version.py")) as f:
+        return sys.version + "\n" + f.read()
+
+
+def _older(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _stale() -> bool:
+    return _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
+                  + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _ext_stale() -> bool:
+    if _older(EXT, [EXT_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return True
+    if not os.path.exists(EXT_FOR):
+        return True
+    with open(EXT_FOR) as f:
+        return f.read() != _built_for()
+
+
+def _ext_compile(obj: str) -> list:
+    torch = os.path.join(_torch_root(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE]
+    for d in (torch, os.path.join(torch, "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], cuda):
+        cmd += ["-isystem", d]
+    return cmd + ["-c", EXT_SRC, "-o", obj]
+
+
+def _ext_link(obj: str, to: str) -> list:
+    lib = os.path.join(_torch_root(), "lib")
+    return ["g++", "-shared", "-o", to, obj, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", LIB, "-Wl,-rpath,$ORIGIN"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    kernels, ext = force or _stale(), force or _ext_stale()
+    if not kernels and not ext:
         return LIB
     os.makedirs(OUT, exist_ok=True)
     cc = nvcc()
     procs = []
     objs = []
-    for src in sources():
+    for src in sources() if kernels else []:
         obj = os.path.join(OUT, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         cmd = [cc, *ARCH, *FLAGS, "-c", src, "-o", obj]
@@ -57,6 +107,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                             stderr=subprocess.STDOUT, text=True)))
+    ext_obj = os.path.join(OUT, "gdn_torch.o")
+    if ext:
+        procs.append((EXT_SRC, subprocess.Popen(_ext_compile(ext_obj), stdout=subprocess.PIPE,
+                                                stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -65,10 +119,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.returncode:
             failed.append(src)
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(failed))
-    tmp = LIB + f".tmp{os.getpid()}"
-    subprocess.check_call([cc, *ARCH, "-shared", "-o", tmp, *objs])
-    os.replace(tmp, LIB)
+        raise RuntimeError("compilation failed for: " + ", ".join(failed))
+    if kernels:
+        tmp = LIB + f".tmp{os.getpid()}"
+        subprocess.check_call([cc, *ARCH, "-shared", "-Xlinker", "-soname=libgdn.so", "-o", tmp,
+                               *objs])
+        os.replace(tmp, LIB)
+    if ext:
+        tmp = EXT + f".tmp{os.getpid()}"
+        subprocess.check_call(_ext_link(ext_obj, tmp))
+        os.replace(tmp, EXT)
+        with open(EXT_FOR, "w") as f:
+            f.write(_built_for())
     return LIB
 
 

@@ -10,6 +10,8 @@ The function names follow the C ABI in include/gdn.h, gdn_conv.h and gdn_layer.h
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -405,97 +407,41 @@ def gdn_conv_bwd(x, w, b, state_in, dy, dstate_out=None, act="silu", dx=None, dw
 
 
 # ------------------------------------------------- layer operators (include/gdn_layer.h)
-# A generation step makes these calls once per layer and token, so what they do
-# on the host is kept short: one condition over all arguments that holds for
-# every well-formed call (plain attribute reads, no calls of our own), and the
-# checks that name the offending argument only where it does not.
-def _on_stream(fn, stream, *args, **kw):
+# A generation step makes these calls once per layer and token, so their checks,
+# allocations and the call itself are native (csrc/gdn_torch.cpp).
+_ext_module = None
+
+
+def ext():
+    """The native entry of the layer operators. Raises if it has not been built."""
+    global _ext_module
+    if _ext_module is None:
+        load()
+        if not os.path.exists(_build.EXT):
+            raise RuntimeError(f"_gdn_torch not built ({_build.EXT}); run "
+                               "`python -m chunked_linear_recurrence_gated_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_gdn_torch", _build.EXT)
+        spec = importlib.util.spec_from_loader("_gdn_torch", loader)
+        m = importlib.util.module_from_spec(spec)
+        loader.exec_module(m)
+        m.set_error(GdnError)
+        _ext_module = m
+    return _ext_module
+
+
+def _on_stream(fn, stream, *args):
     """fn with `stream` current, so that what it allocates (outputs, workspace)
     belongs to the stream its kernels run on."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(stream):
-        return fn(*args, **kw)
-
-
-def _raw_stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same value without a Stream object
-    _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811
-
-_f32, _i32 = torch.float32, torch.int32
-_codes = {torch.float32: GDN_DTYPE_F32, torch.bfloat16: GDN_DTYPE_BF16}
-
-
-def _code(dtype):
-    code = _codes.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return code
-
-
-def _on_gpu(name, t, ndim):
-    """Index of the GPU that holds t."""
-    dev = t.get_device()
-    if dev < 0 or t.dim() < ndim:
-        raise ValueError(f"{name}: a CUDA tensor with {ndim} dimensions is expected, got "
-                         f"{tuple(t.shape)} on {t.device}")
-    return dev
-
-
-def _want(name, t, shape, dtype, dev):
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{dev}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
-
-
-def _ptr(name, t, shape, dtype, dev):
-    """Pointer of a contiguous tensor (None for an absent one)."""
-    if t is None:
-        return None
-    if (t.shape != shape or t.dtype is not dtype or t.get_device() != dev
-            or not t.is_contiguous()):
-        _want(name, t, shape, dtype, dev)
-        raise ValueError(f"{name}: must be contiguous, got strides {t.stride()}")
-    return t.data_ptr()
+        return fn(*args)
 
 
 def _rows(name, t, ndim):
     """Stride of the rows of t [..., n1, .., nk] (k = ndim trailing dimensions that
     have to be dense) when its leading dimensions flatten to one."""
-    st, sh = t.stride(), t.shape
-    inner = 1
-    for i in range(1, ndim + 1):
-        if sh[-i] != 1 and st[-i] != inner:
-            raise ValueError(f"{name}: the last {ndim} dimensions must be dense")
-        inner *= sh[-i]
-    ld, n = inner, 1
-    for i in range(len(sh) - ndim - 1, -1, -1):
-        if sh[i] == 1:
-            continue
-        if n == 1:
-            ld = st[i]
-        elif st[i] != ld * n:
-            raise ValueError(f"{name}: the rows must have one stride")
-        n *= sh[i]
-    return ld
-
-
-def _cache_ptrs(N, dev, slot_in, slot_out, cu_seqlens, n_commit):
-    """Pointers of the index arrays of gdn_step and gdn_conv_step."""
-    return (None if slot_in is None else _ptr("slot_in", slot_in, (N,), _i32, dev),
-            None if slot_out is None else _ptr("slot_out", slot_out, (N,), _i32, dev),
-            None if cu_seqlens is None else _ptr("cu_seqlens", cu_seqlens, (N + 1,), _i32, dev),
-            None if n_commit is None else _ptr("n_commit", n_commit, (N,), _i32, dev))
-
-
-def _scratch(t, dev):
-    """Pointer and bytes of a workspace."""
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
-    return t.data_ptr(), t.nbytes
+    return ext().row_stride(name, t, ndim)
 
 
 def gdn_step(q, k, v, g, beta, S, slot_in=None, slot_out=None, cu_seqlens=None, n_commit=None,
@@ -513,45 +459,9 @@ def gdn_step(q, k, v, g, beta, S, slot_in=None, slot_out=None, cu_seqlens=None, 
     if stream is not None:
         return _on_stream(gdn_step, stream, q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens,
                           n_commit, gate, q_scale, eps, o)
-    dt, dev = q.dtype, q.get_device()
-    n, Hk, dk = shape = q.shape
-    _, H, dv = v.shape
-    n_slots = S.shape[0]
-    gates = (n, H)
-    sq, sk, sv, sg, sb = q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()
-    if (dev >= 0 and k.shape == shape and v.shape[0] == n and g.shape == gates
-            and beta.shape == gates and k.dtype is dt and v.dtype is dt and g.dtype is dt
-            and beta.dtype is dt and k.get_device() == dev and v.get_device() == dev
-            and g.get_device() == dev and beta.get_device() == dev
-            and sq[2] == sk[2] == sv[2] == sg[1] == sb[1] == 1 and sq[1] == sk[1] == dk
-            and sv[1] == dv):
-        ldq, ldk, ldv, ldg, ldb = sq[0], sk[0], sv[0], sg[0], sb[0]
-    else:
-        _on_gpu("q", q, 3)
-        for name, t, sh in (("k", k, shape), ("v", v, (n, H, dv)), ("g", g, gates),
-                            ("beta", beta, gates)):
-            _want(name, t, sh, dt, dev)
-        ldq, ldk, ldv = _rows("q", q, 2), _rows("k", k, 2), _rows("v", v, 2)
-        ldg, ldb = _rows("g", g, 1), _rows("beta", beta, 1)
-    if o is None:
-        o = torch.empty((n, H, dv), dtype=dt, device=q.device)
-        po = o.data_ptr()
-    else:
-        po = _ptr("o", o, (n, H, dv), dt, dev)
-    if gate is None:
-        rate = bias = None
-    else:
-        rate, bias = _ptr("rate", gate[0], (H,), _f32, dev), _ptr("bias", gate[1], (H,), _f32, dev)
-    N = n if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    rc = load().gdn_step(
-        gdn_step_shape(N, n, n_slots, H, Hk, dk, dv, _code(dt), ldq, ldk, ldv, ldg, ldb, q_scale,
-                       eps),
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), rate, bias,
-        _ptr("S", S, (n_slots, H, dk, dv), _f32, dev),
-        *_cache_ptrs(N, dev, slot_in, slot_out, cu_seqlens, n_commit), po, _raw_stream(dev))
-    if rc:
-        raise GdnError(rc, "gdn_step")
-    return o
+    rate, bias = gate if gate is not None else (None, None)
+    return (_ext_module or ext()).step(q, k, v, g, beta, S, slot_in, slot_out, cu_seqlens,
+                                       n_commit, rate, bias, q_scale, eps, o)
 
 
 def gdn_conv_step(x, w, b, state, slot_in=None, slot_out=None, cu_seqlens=None, n_commit=None,
@@ -562,49 +472,8 @@ def gdn_conv_step(x, w, b, state, slot_in=None, slot_out=None, cu_seqlens=None, 
     if stream is not None:
         return _on_stream(gdn_conv_step, stream, x, w, b, state, slot_in, slot_out, cu_seqlens,
                           n_commit, act, y)
-    dt, dev = x.dtype, _on_gpu("x", x, 2)
-    n, C = shape = x.shape
-    W, n_slots = w.shape[1], state.shape[0]
-    sx = x.stride()
-    if y is None:
-        y = torch.empty(shape, dtype=dt, device=x.device)
-        py = y.data_ptr()
-    else:
-        py = _ptr("y", y, shape, dt, dev)
-    N = n if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    rc = load().gdn_conv_step(
-        gdn_conv_step_shape(N, n, n_slots, C, W, _code(dt), CONV_ACT[act],
-                            sx[0] if sx[1] == 1 else _rows("x", x, 1)),
-        x.data_ptr(), _ptr("w", w, (C, W), _f32, dev), _ptr("b", b, (C,), _f32, dev),
-        _ptr("state", state, (n_slots, W - 1, C), dt, dev),
-        *_cache_ptrs(N, dev, slot_in, slot_out, cu_seqlens, n_commit), py, _raw_stream(dev))
-    if rc:
-        raise GdnError(rc, "gdn_conv_step")
-    return y
-
-
-def _prep_shape_of(q, k, xg, xb, rate, bias, q_scale, eps):
-    """(shape, GPU, pointers of the inputs) of gdn_prep_fwd and gdn_prep_bwd."""
-    dt, dev = q.dtype, q.get_device()
-    B, T, Hk, dk = shape = q.shape
-    H = xg.shape[-1]
-    gates = (B, T, H)
-    sq, sk, sg, sb = q.stride(), k.stride(), xg.stride(), xb.stride()
-    if (dev >= 0 and B == 1 and k.shape == shape and xg.shape == gates and xb.shape == gates
-            and k.dtype is dt and xg.dtype is dt and xb.dtype is dt and k.get_device() == dev
-            and xg.get_device() == dev and xb.get_device() == dev
-            and sq[3] == sk[3] == sg[2] == sb[2] == 1 and sq[2] == sk[2] == dk):
-        ldq, ldk, ldg, ldb = sq[1], sk[1], sg[1], sb[1]
-    else:
-        _on_gpu("q", q, 4)
-        _want("k", k, shape, dt, dev)
-        _want("xg", xg, gates, dt, dev)
-        _want("xb", xb, gates, dt, dev)
-        ldq, ldk, ldg, ldb = (_rows("q", q, 2), _rows("k", k, 2), _rows("xg", xg, 1),
-                              _rows("xb", xb, 1))
-    return (gdn_prep_shape(B * T, H, Hk, dk, _code(dt), ldq, ldk, ldg, ldb, q_scale, eps), dev,
-            (q.data_ptr(), k.data_ptr(), xg.data_ptr(), xb.data_ptr(),
-             _ptr("rate", rate, (H,), _f32, dev), _ptr("bias", bias, (H,), _f32, dev)))
+    return (_ext_module or ext()).conv_step(x, w, b, state, slot_in, slot_out, cu_seqlens,
+                                            n_commit, CONV_ACT[act], y)
 
 
 def gdn_prep_fwd(q, k, xg, xb, rate, bias, q_scale=1.0, eps=1e-6, stream=None):
@@ -615,19 +484,7 @@ def gdn_prep_fwd(q, k, xg, xb, rate, bias, q_scale=1.0, eps=1e-6, stream=None):
     beta = sigmoid(xb)."""
     if stream is not None:
         return _on_stream(gdn_prep_fwd, stream, q, k, xg, xb, rate, bias, q_scale, eps)
-    s, dev, ins = _prep_shape_of(q, k, xg, xb, rate, bias, q_scale, eps)
-    B, T, _, dk = q.shape
-    dt, at = q.dtype, q.device
-    heads, gates = (B, T, s.H, dk), (B, T, s.H)
-    qn = torch.empty(heads, dtype=dt, device=at)
-    kn = torch.empty(heads, dtype=dt, device=at)
-    g = torch.empty(gates, dtype=dt, device=at)
-    beta = torch.empty(gates, dtype=dt, device=at)
-    rc = load().gdn_prep_fwd(s, *ins, qn.data_ptr(), kn.data_ptr(), g.data_ptr(),
-                             beta.data_ptr(), _raw_stream(dev))
-    if rc:
-        raise GdnError(rc, "gdn_prep_fwd")
-    return qn, kn, g, beta
+    return (_ext_module or ext()).prep_fwd(q, k, xg, xb, rate, bias, q_scale, eps)
 
 
 def gdn_prep_bwd(q, k, xg, xb, rate, bias, dq, dk, dg, dbeta, q_scale=1.0, eps=1e-6,
@@ -637,42 +494,8 @@ def gdn_prep_bwd(q, k, xg, xb, rate, bias, dq, dk, dg, dbeta, q_scale=1.0, eps=1
     if stream is not None:
         return _on_stream(gdn_prep_bwd, stream, q, k, xg, xb, rate, bias, dq, dk, dg, dbeta,
                           q_scale, eps, workspace)
-    lib = load()
-    s, dev, ins = _prep_shape_of(q, k, xg, xb, rate, bias, q_scale, eps)
-    B, T, _, D = shape = q.shape
-    H, dt, at = s.H, q.dtype, q.device
-    heads, gates = (B, T, H, D), (B, T, H)
-    if workspace is None:
-        workspace = alloc_workspace(lib.gdn_prep_workspace_bytes(s), at)
-    oq = torch.empty(shape, dtype=dt, device=at)
-    ok = torch.empty(shape, dtype=dt, device=at)
-    og = torch.empty(gates, dtype=dt, device=at)
-    ob = torch.empty(gates, dtype=dt, device=at)
-    drate = torch.empty(H, dtype=_f32, device=at)
-    dbias = torch.empty(H, dtype=_f32, device=at)
-    rc = lib.gdn_prep_bwd(s, *ins, _ptr("dq", dq, heads, dt, dev), _ptr("dk", dk, heads, dt, dev),
-                          _ptr("dg", dg, gates, dt, dev), _ptr("dbeta", dbeta, gates, dt, dev),
-                          oq.data_ptr(), ok.data_ptr(), og.data_ptr(), ob.data_ptr(),
-                          drate.data_ptr(), dbias.data_ptr(), *_scratch(workspace, dev),
-                          _raw_stream(dev))
-    if rc:
-        raise GdnError(rc, "gdn_prep_bwd")
-    return oq, ok, og, ob, drate, dbias
-
-
-def _gate_norm_shape_of(o, z, w, act, eps):
-    """(shape, GPU, pointers of the inputs) of gdn_gate_norm_fwd and gdn_gate_norm_bwd."""
-    dt, dev = o.dtype, _on_gpu("o", o, 4)
-    B, T, H, d = shape = o.shape
-    sz = z.stride()
-    if (B == 1 and z.shape == shape and z.dtype is dt and z.get_device() == dev and sz[3] == 1
-            and sz[2] == d):
-        ldz = sz[1]
-    else:
-        _want("z", z, shape, dt, dev)
-        ldz = _rows("z", z, 2)
-    return (gdn_gate_norm_shape(B * T, H, d, _code(dt), GATE_ACT[act], ldz, eps), dev,
-            (_ptr("o", o, shape, dt, dev), z.data_ptr(), _ptr("w", w, (d,), _f32, dev)))
+    return (_ext_module or ext()).prep_bwd(q, k, xg, xb, rate, bias, dq, dk, dg, dbeta, q_scale,
+                                           eps, workspace)
 
 
 def gdn_gate_norm_fwd(o, z, w, act="silu", eps=1e-6, y=None, stream=None):
@@ -680,30 +503,14 @@ def gdn_gate_norm_fwd(o, z, w, act="silu", eps=1e-6, y=None, stream=None):
     with strided token rows, w [d] fp32, act "silu" or "sigmoid"."""
     if stream is not None:
         return _on_stream(gdn_gate_norm_fwd, stream, o, z, w, act, eps, y)
-    s, dev, ins = _gate_norm_shape_of(o, z, w, act, eps)
-    if y is None:
-        y = torch.empty_like(o)
-    rc = load().gdn_gate_norm_fwd(s, *ins, _ptr("y", y, o.shape, o.dtype, dev), _raw_stream(dev))
-    if rc:
-        raise GdnError(rc, "gdn_gate_norm_fwd")
-    return y
+    return (_ext_module or ext()).gate_norm_fwd(o, z, w, GATE_ACT[act], eps, y)
 
 
 def gdn_gate_norm_bwd(o, z, w, dy, act="silu", eps=1e-6, workspace=None, stream=None):
     """Backward of gdn_gate_norm_fwd. Returns (do, dz, dw)."""
     if stream is not None:
         return _on_stream(gdn_gate_norm_bwd, stream, o, z, w, dy, act, eps, workspace)
-    lib = load()
-    s, dev, ins = _gate_norm_shape_of(o, z, w, act, eps)
-    if workspace is None:
-        workspace = alloc_workspace(lib.gdn_gate_norm_workspace_bytes(s), o.device)
-    do, dz, dw = torch.empty_like(o), torch.empty_like(o), torch.empty_like(w)
-    rc = lib.gdn_gate_norm_bwd(s, *ins, _ptr("dy", dy, o.shape, o.dtype, dev), do.data_ptr(),
-                               dz.data_ptr(), dw.data_ptr(), *_scratch(workspace, dev),
-                               _raw_stream(dev))
-    if rc:
-        raise GdnError(rc, "gdn_gate_norm_bwd")
-    return do, dz, dw
+    return (_ext_module or ext()).gate_norm_bwd(o, z, w, dy, GATE_ACT[act], eps, workspace)
 
 
 def gdn_res_norm_fwd(h, x, w, w_post=None, scale=None, eps=1e-6, h_out=None, y=None, dtype=None,
@@ -716,22 +523,10 @@ def gdn_res_norm_fwd(h, x, w, w_post=None, scale=None, eps=1e-6, h_out=None, y=N
     h_out may be h. Returns (h_out, y); h_out is None where x is."""
     if stream is not None:
         return _on_stream(gdn_res_norm_fwd, stream, h, x, w, w_post, scale, eps, h_out, y, dtype)
-    rt, dev, shape = h.dtype, _on_gpu("h", h, 1), h.shape
-    C = shape[-1]
-    row = (C,)
-    dt = x.dtype if x is not None else dtype or rt
-    if y is None:
-        y = torch.empty(shape, dtype=dt, device=h.device)
-    if h_out is None and x is not None:
-        h_out = torch.empty_like(h)
-    rc = load().gdn_res_norm_fwd(
-        gdn_res_norm_shape(h.numel() // max(C, 1), C, _code(dt), _code(rt), eps),
-        _ptr("h", h, shape, rt, dev), _ptr("x", x, shape, dt, dev), _ptr("w", w, row, _f32, dev),
-        _ptr("w_post", w_post, row, _f32, dev), _ptr("scale", scale, row, _f32, dev),
-        _ptr("h_out", h_out, shape, rt, dev), _ptr("y", y, shape, dt, dev), _raw_stream(dev))
-    if rc:
-        raise GdnError(rc, "gdn_res_norm_fwd")
-    return h_out, y
+    if dtype is not None and dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {dtype}")
+    return (_ext_module or ext()).res_norm_fwd(h, x, w, w_post, scale, eps, h_out, y,
+                                               None if dtype is None else dtype == torch.bfloat16)
 
 
 def gdn_res_norm_bwd(h_out, x, w, dy, dh_out=None, w_post=None, scale=None, eps=1e-6, dh=None,
@@ -742,32 +537,8 @@ def gdn_res_norm_bwd(h_out, x, w, dy, dh_out=None, w_post=None, scale=None, eps=
     if stream is not None:
         return _on_stream(gdn_res_norm_bwd, stream, h_out, x, w, dy, dh_out, w_post, scale, eps,
                           dh, workspace)
-    lib = load()
-    rt, dt, dev, shape = h_out.dtype, dy.dtype, _on_gpu("h_out", h_out, 1), h_out.shape
-    C = shape[-1]
-    row = (C,)
-    s = gdn_res_norm_shape(h_out.numel() // max(C, 1), C, _code(dt), _code(rt), eps)
-    if workspace is None:
-        workspace = alloc_workspace(lib.gdn_res_norm_workspace_bytes(s), h_out.device)
-    if dh is None:
-        dh = torch.empty_like(h_out)
-    same = w_post is None and scale is None and (dt is rt or x is None)
-    dx = None if same else torch.empty_like(dy)
-    dw = torch.empty_like(w)
-    dpost = None if w_post is None else torch.empty_like(w_post)
-    dscale = None if scale is None else torch.empty_like(scale)
-    rc = lib.gdn_res_norm_bwd(
-        s, _ptr("h_out", h_out, shape, rt, dev), _ptr("x", x, shape, dt, dev),
-        _ptr("w", w, row, _f32, dev), _ptr("w_post", w_post, row, _f32, dev),
-        _ptr("scale", scale, row, _f32, dev), _ptr("dy", dy, shape, dt, dev),
-        _ptr("dh_out", dh_out, shape, rt, dev), _ptr("dh", dh, shape, rt, dev),
-        None if dx is None else dx.data_ptr(), dw.data_ptr(),
-        None if dpost is None else dpost.data_ptr(),
-        None if dscale is None else dscale.data_ptr(), *_scratch(workspace, dev),
-        _raw_stream(dev))
-    if rc:
-        raise GdnError(rc, "gdn_res_norm_bwd")
-    return dh, (dh if same else dx), dw, dpost, dscale
+    return (_ext_module or ext()).res_norm_bwd(h_out, x, w, dy, dh_out, w_post, scale, eps, dh,
+                                               workspace)
 
 
 def gdn_workspace_status(workspace, stream=None) -> int:
