@@ -153,7 +153,9 @@ __global__ void __launch_bounds__(GN_NT, sizeof(T) == 2 ? GN_PARTS / 152 : 2)
 // columns of the team's next rows with cp.async into shared-memory slots that
 // only it reads: the loads of several rows stay in flight across the two
 // reductions of a row, without a barrier of their own.
-constexpr int RN_COLS = 4096;  // columns of a CTA: 512 threads
+constexpr int RN_COLS_F = 8192;  // columns of a CTA, forward: 1024 threads of 64 registers
+constexpr int RN_COLS_B = 4096;  // backward: 512 threads of 128 registers
+constexpr int RN_SLOT = 128;     // floats of a reduction: 8 values of 16 warps, or 1 of 32
 constexpr int RN_SMS = 152;
 
 struct Team {
@@ -166,80 +168,132 @@ struct Team {
 // barrier separates a call's reads from the next but one's writes.
 template <int CL>
 struct TeamRed {
-  float* warp;     // [2][4][16] the warps' sums (unused ones stay 0)
-  float4* cta;     // CL > 1: [2][CL] the CTAs' sums, written by their owners
+  float* warp;     // [2][RN_SLOT] the warps' sums (unused ones stay 0)
+  float4* cta;     // CL > 1: [2][CL][2] the CTAs' sums, written by their owners
   uint64_t* bar;   // CL > 1: [2] completed by CL such writes
   int buf, phase;  // of the next call
   bool dead;       // a wait gave up: every later sum is NaN, so the failure shows
 };
 
-// Sums of K values over the team and, for rows split over a cluster, over its
-// CTAs: each CTA writes its sums into every CTA's shared memory with
-// st.async, which also completes the receiver's mbarrier. (A cluster barrier
-// instead would have to order the row's global stores too: its release waits
-// for them, 6 us per row of 16384 columns against DRAM's 2.)
-template <int K, int CL>
-__device__ __forceinline__ void team_sum(float* v, TeamRed<CL>& red) {
-  const int nt = blockDim.x, warp = threadIdx.x >> 5;
+// Sum over the warp of each of 8 values in 9 shuffles: each exchange halves the
+// values that a lane still carries. Lane l returns value l / 4.
+__device__ __forceinline__ float warp_sum8(const float* v) {
+  const int lane = threadIdx.x & 31;
+  float a[4], b[2];
 #pragma unroll
-  for (int i = 0; i < K; ++i) v[i] = lane_sum<32>(v[i]);
-  if (CL > 1 || nt > 32) {
-    float* slot = red.warp + red.buf * 64;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-      for (int i = 0; i < K; ++i) slot[i * 16 + warp] = v[i];
-    named_bar(threadIdx.y + 1, nt);
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      v[i] = 0.f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (u * 4 >= (nt >> 5)) break;
-        const float4 a = reinterpret_cast<const float4*>(slot + i * 16)[u];
-        v[i] += (a.x + a.y) + (a.z + a.w);
-      }
-    }
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 16;
+    a[i] = (up ? v[4 + i] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[4 + i], 16);
   }
-  if (CL > 1) {
-    uint64_t* bar = red.bar + red.buf;
-    float4* all = red.cta + red.buf * CL;
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, CL * 16);
-    if (threadIdx.x < CL) {
-      uint32_t rank, to, tobar;
-      asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-      asm("mapa.shared::cluster.u32 %0, %1, %2;"
-          : "=r"(to)
-          : "r"(smem_u32(all + rank)), "r"(threadIdx.x));
-      asm("mapa.shared::cluster.u32 %0, %1, %2;"
-          : "=r"(tobar)
-          : "r"(smem_u32(bar)), "r"(threadIdx.x));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 8;
+    b[i] = (up ? a[2 + i] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[2 + i], 8);
+  }
+  const bool up = lane & 4;
+  float c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
+// The sums of a row split over a cluster: each CTA writes its own (up to 8) into
+// every CTA's shared memory with st.async, which also completes the receiver's
+// mbarrier. (A cluster barrier instead would have to order the row's global
+// stores too: its release waits for them, 6 us per row of 16384 columns against
+// DRAM's 2.)
+template <int K, int CL>
+__device__ __forceinline__ void cluster_sum(float* v, TeamRed<CL>& red) {
+  constexpr int N4 = K > 4 ? 2 : 1;  // float4 per CTA
+  uint64_t* bar = red.bar + red.buf;
+  float4* all = red.cta + red.buf * CL * 2;
+  if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, CL * 16 * N4);
+  if (threadIdx.x < CL) {
+    uint32_t rank, to, tobar;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(to)
+        : "r"(smem_u32(all + 2 * rank)), "r"(threadIdx.x));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(tobar)
+        : "r"(smem_u32(bar)), "r"(threadIdx.x));
+#pragma unroll
+    for (int i = 0; i < N4; ++i) {
+      float w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = 4 * i + j < K ? v[4 * i + j] : 0.f;
       asm volatile(
           "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], "
-          "{%1, %2, %3, %4}, [%5];" ::"r"(to),
-          "f"(v[0]), "f"(v[K > 1 ? 1 : 0]), "f"(v[K > 2 ? 2 : 0]), "f"(0.f), "r"(tobar)
+          "{%1, %2, %3, %4}, [%5];" ::"r"(to + 16 * i),
+          "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3]), "r"(tobar)
           : "memory");
     }
-    const long long t0 = clock64();
-    for (uint32_t ok = red.dead; !ok;) {
-      asm volatile(
-          "{\n .reg .pred p;\n"
-          " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-          " selp.u32 %0, 1, 0, p;\n}\n"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"((uint32_t)red.phase)
-          : "memory");
-      if (!ok && clock64() - t0 > (1ll << 32)) ok = red.dead = true;
-    }
-    float s[3] = {};
-#pragma unroll
-    for (int r = 0; r < CL; ++r) {
-      const float4 a = all[r];
-      s[0] += a.x, s[1] += a.y, s[2] += a.z;
-    }
-#pragma unroll
-    for (int i = 0; i < K; ++i) v[i] = red.dead ? __int_as_float(0x7fc00000) : s[i];
-    red.phase ^= red.buf;  // both buffers of this phase used: the next phase
   }
+  const long long t0 = clock64();
+  for (uint32_t ok = red.dead; !ok;) {
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"((uint32_t)red.phase)
+        : "memory");
+    if (!ok && clock64() - t0 > (1ll << 32)) ok = red.dead = true;
+  }
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = red.dead ? __int_as_float(0x7fc00000) : 0.f;
+#pragma unroll
+  for (int r = 0; r < CL; ++r)
+#pragma unroll
+    for (int i = 0; i < N4; ++i) {
+      const float4 a = all[2 * r + i];
+      const float w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (4 * i + j < K) v[4 * i + j] += w[j];
+    }
+  red.phase ^= red.buf;  // both buffers of this phase used: the next phase
+}
+
+// Sum over the team and, for rows split over a cluster, over its CTAs.
+template <int CL>
+__device__ __forceinline__ float team_sum(float v, TeamRed<CL>& red) {
+  const int nt = blockDim.x;
+  v = lane_sum<32>(v);
+  if (CL > 1 || nt > 32) {
+    float* slot = red.warp + red.buf * RN_SLOT;
+    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+    named_bar(threadIdx.y + 1, nt);
+    v = 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (u * 128 >= nt) break;
+      const float4 a = reinterpret_cast<const float4*>(slot)[u];
+      v += (a.x + a.y) + (a.z + a.w);
+    }
+  }
+  if (CL > 1) cluster_sum<1, CL>(&v, red);
+  red.buf ^= 1;
+  return v;
+}
+// The same for 6 values (v has room for 8), teams of up to 16 warps.
+template <int CL>
+__device__ __forceinline__ void team_sum6(float* v, TeamRed<CL>& red) {
+  const int nt = blockDim.x, lane = threadIdx.x & 31;
+  v[6] = v[7] = 0.f;
+  float mine = warp_sum8(v);
+  if (CL > 1 || nt > 32) {
+    float* slot = red.warp + red.buf * RN_SLOT;  // [8 values][16 warps]
+    if ((lane & 3) == 0) slot[(lane >> 2) * 16 + (threadIdx.x >> 5)] = mine;
+    named_bar(threadIdx.y + 1, nt);
+    // lane l: value l / 4, warps 4 (l % 4) ..
+    const float4 a = reinterpret_cast<const float4*>(slot)[lane];
+    mine = (a.x + a.y) + (a.z + a.w);
+    mine += __shfl_xor_sync(0xffffffffu, mine, 1);
+    mine += __shfl_xor_sync(0xffffffffu, mine, 2);
+  }
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, mine, 4 * i);
+  if (CL > 1) cluster_sum<6, CL>(v, red);
   red.buf ^= 1;
 }
 
@@ -255,8 +309,8 @@ __device__ __forceinline__ void team_end() {
 
 template <int CL>
 __device__ __forceinline__ Team team_of(int rows, int C, TeamRed<CL>& red) {
-  __shared__ __align__(16) float warp_sums[8 * 2 * 64];  // at most 8 teams
-  __shared__ float4 cta_sums[2 * CL];
+  __shared__ __align__(16) float warp_sums[8 * 2 * RN_SLOT];  // at most 8 teams
+  __shared__ float4 cta_sums[2 * CL * 2];
   __shared__ uint64_t bars[2];
   Team t;
   t.C = C;
@@ -267,12 +321,12 @@ __device__ __forceinline__ Team team_of(int rows, int C, TeamRed<CL>& red) {
   t.on = (int)threadIdx.x < per && t.c < C;
   t.first = blockIdx.x / CL * blockDim.y + threadIdx.y;
   t.step = gridDim.x / CL * blockDim.y;
-  red.warp = warp_sums + threadIdx.y * 128;
+  red.warp = warp_sums + threadIdx.y * 2 * RN_SLOT;
   red.cta = cta_sums;
   red.bar = bars;
   red.buf = red.phase = 0;
   red.dead = false;
-  for (int i = threadIdx.x; i < 128; i += blockDim.x) red.warp[i] = 0.f;
+  for (int i = threadIdx.x; i < 2 * RN_SLOT; i += blockDim.x) red.warp[i] = 0.f;
   if (CL > 1) {
     if (threadIdx.x == 0) {
       mbar_init(bars, 1);
@@ -337,7 +391,7 @@ __device__ __forceinline__ void ld8_or(const float* p, bool have, float other, f
 }
 
 template <typename T, typename R, int CL>
-__global__ void __launch_bounds__(512, 2)
+__global__ void __launch_bounds__(1024, 1)
     k_res_norm_fwd(int rows, int C, float inv_C, float eps, const R* h, const T* __restrict__ x,
                    const float* __restrict__ w, const float* __restrict__ w_post,
                    const float* __restrict__ scale, R* h_out, T* __restrict__ y) {
@@ -374,9 +428,7 @@ __global__ void __launch_bounds__(512, 2)
       f32x2 a = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) a = fma2(xv[i], xv[i], a);
-      float s = sum2(a);
-      team_sum<1, CL>(&s, red);
-      const f32x2 rx = both2(rsqrtf(fmaf(s, inv_C, eps)));
+      const f32x2 rx = both2(rsqrtf(fmaf(team_sum(sum2(a), red), inv_C, eps)));
 #pragma unroll
       for (int i = 0; i < 4; ++i) xv[i] = mul2(xv[i], mul2(rx, pv[i]));
     }
@@ -389,9 +441,7 @@ __global__ void __launch_bounds__(512, 2)
     if (h_out && t.on) st8(h_out + at, hv);
     fetch(stage, row + S * t.step);  // the slot has been read
     if (++stage == S) stage = 0;
-    float s = sum2(a);
-    team_sum<1, CL>(&s, red);
-    const f32x2 r = both2(rsqrtf(fmaf(s, inv_C, eps)));
+    const f32x2 r = both2(rsqrtf(fmaf(team_sum(sum2(a), red), inv_C, eps)));
 #pragma unroll
     for (int i = 0; i < 4; ++i) hv[i] = mul2(hv[i], mul2(r, wv[i]));
     if (t.on) st8(y + at, hv);
@@ -428,14 +478,20 @@ __global__ void __launch_bounds__(512, 1)
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
-  f32x2 wv[4], pv[4], sv[4], aw[4] = {}, ap[4] = {}, as[4] = {};
+  f32x2 wv[4], sp[4], aw[4] = {}, am[4] = {};  // sp = scale w_post
   ld8_or(w + t.c, t.on, 0.f, wv);
-  ld8_or(w_post + t.c, t.on && w_post, 1.f, pv);
-  ld8_or(scale + t.c, t.on && scale, 1.f, sv);
+  ld8_or(scale + t.c, t.on && scale, 1.f, sp);
+  if (w_post) {
+    f32x2 pv[4];
+    ld8_or(w_post + t.c, t.on, 0.f, pv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sp[i] = mul2(sp[i], pv[i]);
+  }
   int stage = 0;
   for (int row = t.first; row < t.rows; row += t.step) {
     cp_wait<S - 1>();
-    f32x2 hv[4] = {}, gv[4] = {}, xv[4] = {}, dv[4] = {}, a[3] = {};
+    f32x2 hv[4] = {}, gw[4] = {}, xv[4] = {}, dv[4] = {}, a[6] = {};
+    f32x2 gv[4] = {};
     if (t.on) {
       ring.template read<R>(stage, 0, hv);
       if (dh_out) ring.template read<R>(stage, KD, dv);
@@ -444,76 +500,89 @@ __global__ void __launch_bounds__(512, 1)
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      gw[i] = mul2(gv[i], wv[i]);
       a[0] = fma2(hv[i], hv[i], a[0]);
-      a[1] = fma2(mul2(gv[i], wv[i]), hv[i], a[1]);
-      a[2] = fma2(xv[i], xv[i], a[2]);
+      a[1] = fma2(gw[i], hv[i], a[1]);
+    }
+    if (w_post) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x2 q = mul2(sp[i], xv[i]);
+        a[2] = fma2(xv[i], xv[i], a[2]);
+        a[3] = fma2(q, dv[i], a[3]);
+        a[4] = fma2(q, gw[i], a[4]);
+        a[5] = fma2(q, hv[i], a[5]);
+      }
     }
     fetch(stage, row + S * t.step);  // the slot has been read
     if (++stage == S) stage = 0;
-    float s[3] = {sum2(a[0]), sum2(a[1]), sum2(a[2])};
-    team_sum<3, CL>(s, red);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s[i] = sum2(a[i]);
+    team_sum6(s, red);
     const size_t at = (size_t)row * C + t.c;
-    // n = h r, dh = dh_out + r (dy w - n m) with m = mean(dy w n): r m = r^2 s1 / C
-    const float r = rsqrtf(fmaf(s[0], inv_C, eps)), rx = rsqrtf(fmaf(s[2], inv_C, eps));
-    const f32x2 r2 = both2(r), rm = both2(-r * r * s[1] * inv_C), rx2 = both2(w_post ? rx : 1.f);
+    const float r = rsqrtf(fmaf(s[0], inv_C, eps));
+    const float rx = w_post ? rsqrtf(fmaf(s[2], inv_C, eps)) : 1.f;
+    const float hc = -r * r * r * s[1] * inv_C;  // factor of h in dh
+    const f32x2 r2 = both2(r), hc2 = both2(hc), rx2 = both2(rx);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const f32x2 n = mul2(hv[i], r2), gr = mul2(mul2(gv[i], wv[i]), r2);
-      aw[i] = fma2(gv[i], n, aw[i]);
-      dv[i] = add2(dv[i], fma2(n, rm, gr));
-      xv[i] = mul2(xv[i], rx2);
+      aw[i] = fma2(gv[i], mul2(hv[i], r2), aw[i]);
+      dv[i] = fma2(hv[i], hc2, fma2(gw[i], r2, dv[i]));  // dh
+      xv[i] = mul2(xv[i], rx2);                          // m
+      am[i] = fma2(dv[i], xv[i], am[i]);
     }
     if (t.on) st8(dh + at, dv);
-    f32x2 e2 = 0;
+    if (dx) {
+      if (w_post) {
+        // mean(sp dh m) from the sums of its terms
+        const f32x2 e = both2(-rx * inv_C * fmaf(hc, s[5], fmaf(r, s[4], s[3])));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      as[i] = fma2(dv[i], mul2(xv[i], pv[i]), as[i]);
-      dv[i] = mul2(dv[i], sv[i]);
-      ap[i] = fma2(dv[i], xv[i], ap[i]);
-      dv[i] = mul2(dv[i], pv[i]);
-      e2 = fma2(dv[i], xv[i], e2);
-    }
-    if (w_post) {
-      float e = sum2(e2);
-      team_sum<1, CL>(&e, red);
-      const f32x2 em = both2(-e * inv_C);
+        for (int i = 0; i < 4; ++i) dv[i] = mul2(rx2, fma2(xv[i], e, mul2(dv[i], sp[i])));
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dv[i] = mul2(rx2, fma2(xv[i], em, dv[i]));
+        for (int i = 0; i < 4; ++i) dv[i] = mul2(dv[i], sp[i]);
+      }
+      if (t.on) st8(dx + at, dv);
     }
-    if (dx && t.on) st8(dx + at, dv);
   }
   cp_wait<0>();
   team_end<CL>();
-  // the block's sums: teams joined through shared memory (the ring is drained)
-  float* join = reinterpret_cast<float*>(smem);  // [teams][blockDim.x * 8]
+  // the block's sums, teams joined through shared memory (the ring is drained);
+  // sum dh m times scale is dw_post, times w_post dscale
+  float* mine = reinterpret_cast<float*>(smem) + (threadIdx.y * blockDim.x + threadIdx.x) * 8;
   const int narr = 1 + (w_post != nullptr) + (scale != nullptr);
-  float* out = part + (size_t)(blockIdx.x / CL) * narr * C;
-  for (int a = 0; a < 3; ++a) {
-    if ((a == 1 && !w_post) || (a == 2 && !scale)) continue;
-    if (blockDim.y > 1) {
-      __syncthreads();
-      float* mine = join + (size_t)(threadIdx.y * blockDim.x + threadIdx.x) * 8;
-      f32x2 v[4];
+  float* out = part + (size_t)(blockIdx.x / CL) * narr * C + t.c;
+  auto join = [&](f32x2* v) {
+    if (blockDim.y == 1) return;
+    __syncthreads();
+    st8(mine, v);
+    __syncthreads();
+    if (threadIdx.y) return;
+    for (int u = 1; u < (int)blockDim.y; ++u) {
+      f32x2 o[4];
+      cvt8(ldraw8(mine + (size_t)u * blockDim.x * 8), o);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = a == 0 ? aw[i] : a == 1 ? ap[i] : as[i];
-      st8(mine, v);
-      __syncthreads();
-      if (threadIdx.y == 0 && t.on) {
-        for (int u = 1; u < (int)blockDim.y; ++u) {
-          f32x2 o[4];
-          cvt8(ldraw8(mine + (size_t)u * blockDim.x * 8), o);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = add2(v[i], o[i]);
-        }
-        st8(out + t.c, v);
-      }
-    } else if (t.on) {
-      f32x2 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = a == 0 ? aw[i] : a == 1 ? ap[i] : as[i];
-      st8(out + t.c, v);
+      for (int i = 0; i < 4; ++i) v[i] = add2(v[i], o[i]);
     }
-    out += C;
+  };
+  join(aw);
+  if (with_x) join(am);
+  if (threadIdx.y || !t.on) return;
+  st8(out, aw);
+  if (w_post) {
+    f32x2 sv[4];
+    ld8_or(scale + t.c, scale, 1.f, sv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sv[i] = mul2(am[i], sv[i]);
+    st8(out += C, sv);
+  }
+  if (scale) {
+    f32x2 pv[4];
+    ld8_or(w_post + t.c, w_post, 1.f, pv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pv[i] = mul2(am[i], pv[i]);
+    st8(out += C, pv);
   }
 }
 
@@ -580,16 +649,16 @@ struct ResPlan {
     return cl * std::min(all, std::max(1, RN_SMS * (threads / (team * teams)) / cl));
   }
 };
-ResPlan res_plan(int C) {
+ResPlan res_plan(int C, int cols) {
   ResPlan p;
-  p.cl = C <= RN_COLS ? 1 : C <= 2 * RN_COLS ? 2 : 4;
+  p.cl = C <= cols ? 1 : C <= 2 * cols ? 2 : 4;
   const int groups = (C / 8 + p.cl - 1) / p.cl;
   p.team = (groups + 31) / 32 * 32;
   p.teams = p.team >= 256 || p.cl > 1 ? 1 : 256 / p.team;
   return p;
 }
 int res_parts(const gdn_res_norm_shape& s) {
-  const ResPlan p = res_plan(s.C);
+  const ResPlan p = res_plan(s.C, RN_COLS_B);
   return p.blocks(s.rows, 512) / p.cl;
 }
 
@@ -602,9 +671,11 @@ struct ResArgs {
 template <typename K, typename... A>
 cudaError_t launch_rows(K kernel, const ResPlan& p, int blocks, int smem, cudaStream_t st,
                         A... args) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e) return e;
+  if (smem > 32 << 10) {  // with the static part, past what needs no asking
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(p.team, p.teams);
@@ -635,7 +706,7 @@ cudaError_t launch_res(const gdn_res_norm_shape& s, const ResArgs& a, const ResP
 }
 template <typename T, typename R>
 cudaError_t dispatch_res(const gdn_res_norm_shape& s, const ResArgs& a, cudaStream_t st) {
-  const ResPlan p = res_plan(s.C);
+  const ResPlan p = res_plan(s.C, a.dy ? RN_COLS_B : RN_COLS_F);
   switch (p.cl) {
     case 1: return launch_res<T, R, 1>(s, a, p, st);
     case 2: return launch_res<T, R, 2>(s, a, p, st);
