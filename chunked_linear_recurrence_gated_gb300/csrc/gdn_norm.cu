@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_layer.cuh"
 #include "gdn_mma.cuh"
@@ -147,33 +148,129 @@ __global__ void __launch_bounds__(GN_NT, sizeof(T) == 2 ? GN_PARTS / 152 : 2)
 
 // ------------------------------------------------------------ block boundary
 // A team of threads works on one row, 8 columns per thread, so the parameters,
-// the row and (backward) the columns' running sums stay in registers. Rows
-// wider than RN_COLS are split over the CTAs of a cluster, which exchange their
-// sums through distributed shared memory. Each thread prefetches its own 8
-// columns of the team's next rows with cp.async into shared-memory slots that
-// only it reads: the loads of several rows stay in flight across the two
-// reductions of a row, without a barrier of their own.
+// the row and (backward) the columns' running sums stay in registers. Rows wider
+// than a CTA are split over the CTAs of a cluster, which exchange their sums
+// through distributed shared memory. Each thread prefetches its own columns of
+// the team's next rows with cp.async into shared-memory slots that only it
+// reads: the loads of several rows stay in flight across a row's reductions,
+// without a barrier of their own.
 constexpr int RN_COLS_F = 8192;  // columns of a CTA, forward: 1024 threads of 64 registers
 constexpr int RN_COLS_B = 4096;  // backward: 512 threads of 128 registers
 constexpr int RN_SLOT = 128;     // floats of a reduction: 8 values of 16 warps, or 1 of 32
+constexpr int RN_BUFS = 3;       // reductions that may be open at the same time, plus one
 constexpr int RN_SMS = 152;
 
+// The rows of a team and the columns of a thread. With an fp32 stream a
+// thread's columns are two groups of 4 that lie a team apart, so that a warp's
+// 16-byte accesses are whole lines (8 consecutive ones make twice the requests:
+// backward, fp32, 4096 columns 176 us instead of 140); otherwise 8 consecutive.
+template <bool SPLIT>
 struct Team {
-  int C, c;         // row width, this thread's first column
-  int rows, first, step;  // this team takes rows first, first + step, ..
-  bool on;          // the thread has columns
+  int C, rows, first, step;  // this team takes rows first, first + step, ..
+  int c0, c1;                // first columns of the two groups of 4
+  bool on0, on1;             // whether they exist
+  __device__ __forceinline__ bool on() const { return on0; }
 };
 
-// What a team's reductions go through; buf alternates between calls, so one
-// barrier separates a call's reads from the next but one's writes.
-template <int CL>
-struct TeamRed {
-  float* warp;     // [2][RN_SLOT] the warps' sums (unused ones stay 0)
-  float4* cta;     // CL > 1: [2][CL][2] the CTAs' sums, written by their owners
-  uint64_t* bar;   // CL > 1: [2] completed by CL such writes
-  int buf, phase;  // of the next call
-  bool dead;       // a wait gave up: every later sum is NaN, so the failure shows
+template <bool SPLIT, int CL>
+__device__ __forceinline__ Team<SPLIT> team_of(int rows, int C) {
+  Team<SPLIT> t;
+  t.C = C;
+  t.rows = rows;
+  const int per = (C / 8 + CL - 1) / CL * 8;  // columns of a CTA
+  const int base = CL == 1 ? 0 : blockIdx.x % CL * per, end = min(base + per, C);
+  t.c0 = base + (SPLIT ? 4 : 8) * threadIdx.x;
+  t.c1 = SPLIT ? t.c0 + 4 * blockDim.x : t.c0 + 4;
+  t.on0 = t.c0 < end;
+  t.on1 = t.c1 < end;
+  t.first = blockIdx.x / CL * blockDim.y + threadIdx.y;
+  t.step = gridDim.x / CL * blockDim.y;
+  return t;
+}
+
+// 4 values of an fp32 row, or `other`.
+__device__ __forceinline__ void ld4_or(const float* p, bool have, float other, f32x2* v) {
+  v[0] = v[1] = both2(other);
+  if (have) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = pack2(a.x, a.y);
+    v[1] = pack2(a.z, a.w);
+  }
+}
+__device__ __forceinline__ void st4(float* p, const f32x2* v) {
+  *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
+}
+__device__ __forceinline__ void st4(__nv_bfloat16* p, const f32x2* v) {
+  float f[4];
+  unpack2(v[0], f[0], f[1]);
+  unpack2(v[1], f[2], f[3]);
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+// A thread's columns of a parameter row (`other` without one) and of an output row.
+template <bool SPLIT>
+__device__ __forceinline__ void ld_cols(const float* p, const Team<SPLIT>& t, float other,
+                                        f32x2* v) {
+  ld4_or(p + t.c0, p && t.on0, other, v);
+  ld4_or(p + t.c1, p && t.on1, other, v + 2);
+}
+template <bool SPLIT, typename T>
+__device__ __forceinline__ void st_cols(T* p, const Team<SPLIT>& t, const f32x2* v) {
+  if (SPLIT || sizeof(T) == 4) {
+    if (t.on0) st4(p + t.c0, v);
+    if (t.on1) st4(p + t.c1, v + 2);
+  } else if (t.on0) {
+    st8(p + t.c0, v);
+  }
+}
+
+// Prefetch slots of a thread: slot k of stage s, 16 bytes each, consecutive
+// threads consecutive. 8 bf16 values take one, 8 fp32 values two.
+template <int SLOTS, bool SPLIT>
+struct Ring {
+  uint4* base;  // this thread's slot 0 of stage 0
+  int nt;
+  __device__ __forceinline__ uint4* at(int stage, int k) const {
+    return base + (size_t)(stage * SLOTS + k) * nt;
+  }
+  __device__ __forceinline__ void clear(int stages) const {  // what no fetch writes reads as 0
+    for (int i = 0; i < stages * SLOTS; ++i) base[(size_t)i * nt] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void fetch(int stage, int k, const float* p,
+                                        const Team<SPLIT>& t) const {
+    if (t.on0) cp16(at(stage, k), p + t.c0, true);
+    if (t.on1) cp16(at(stage, k + 1), p + t.c1, true);
+  }
+  __device__ __forceinline__ void fetch(int stage, int k, const __nv_bfloat16* p,
+                                        const Team<SPLIT>& t) const {
+    if (!SPLIT) {
+      if (t.on0) cp16(at(stage, k), p + t.c0, true);
+      return;
+    }
+    const uint32_t to = smem_u32(at(stage, k));
+    if (t.on0)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(p + t.c0));
+    if (t.on1)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to + 8), "l"(p + t.c1));
+  }
+  template <typename T>
+  __device__ __forceinline__ void read(int stage, int k, f32x2* v) const {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = *at(stage, k + i);
+    cvt8(r, v);
+  }
 };
+
+template <typename T>
+constexpr int pieces() { return (int)sizeof(T) / 2; }  // 16-byte pieces of 8 elements
+template <typename T, typename R>
+constexpr int fwd_slots() { return pieces<R>() + pieces<T>(); }
+template <typename T, typename R>
+constexpr int bwd_slots() { return 2 * pieces<R>() + 2 * pieces<T>(); }
+template <typename T, typename R>
+constexpr int bwd_stages() { return bwd_slots<T, R>() == 4 ? 4 : 3; }
 
 // Sum over the warp of each of 8 values in 9 shuffles: each exchange halves the
 // values that a lane still carries. Lane l returns value l / 4.
@@ -196,261 +293,226 @@ __device__ __forceinline__ float warp_sum8(const float* v) {
   return c + __shfl_xor_sync(0xffffffffu, c, 1);
 }
 
-// The sums of a row split over a cluster: each CTA writes its own (up to 8) into
-// every CTA's shared memory with st.async, which also completes the receiver's
-// mbarrier. (A cluster barrier instead would have to order the row's global
-// stores too: its release waits for them, 6 us per row of 16384 columns against
-// DRAM's 2.)
-template <int K, int CL>
-__device__ __forceinline__ void cluster_sum(float* v, TeamRed<CL>& red) {
-  constexpr int N4 = K > 4 ? 2 : 1;  // float4 per CTA
-  uint64_t* bar = red.bar + red.buf;
-  float4* all = red.cta + red.buf * CL * 2;
-  if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, CL * 16 * N4);
-  if (threadIdx.x < CL) {
-    uint32_t rank, to, tobar;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    asm("mapa.shared::cluster.u32 %0, %1, %2;"
-        : "=r"(to)
-        : "r"(smem_u32(all + 2 * rank)), "r"(threadIdx.x));
-    asm("mapa.shared::cluster.u32 %0, %1, %2;"
-        : "=r"(tobar)
-        : "r"(smem_u32(bar)), "r"(threadIdx.x));
-#pragma unroll
-    for (int i = 0; i < N4; ++i) {
-      float w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = 4 * i + j < K ? v[4 * i + j] : 0.f;
-      asm volatile(
-          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], "
-          "{%1, %2, %3, %4}, [%5];" ::"r"(to + 16 * i),
-          "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3]), "r"(tobar)
-          : "memory");
-    }
-  }
-  const long long t0 = clock64();
-  for (uint32_t ok = red.dead; !ok;) {
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"((uint32_t)red.phase)
-        : "memory");
-    if (!ok && clock64() - t0 > (1ll << 32)) ok = red.dead = true;
-  }
-#pragma unroll
-  for (int i = 0; i < K; ++i) v[i] = red.dead ? __int_as_float(0x7fc00000) : 0.f;
-#pragma unroll
-  for (int r = 0; r < CL; ++r)
-#pragma unroll
-    for (int i = 0; i < N4; ++i) {
-      const float4 a = all[2 * r + i];
-      const float w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (4 * i + j < K) v[4 * i + j] += w[j];
-    }
-  red.phase ^= red.buf;  // both buffers of this phase used: the next phase
-}
+// Sums over a team of 1 (ONE) or 6 values, in two halves: post() gives this
+// thread's part, collect() returns the sums of the oldest post not yet collected.
+// At most one other post may lie between the two, which is what the three
+// buffers are for: a post's barrier separates it from the reads three posts back.
+// For rows split over a cluster post() also sends the CTA's sums into every
+// CTA's shared memory with st.async, which completes the receiver's mbarrier. (A
+// cluster barrier instead would have to order the row's global stores too: its
+// release waits for them, 6 us per row of 16384 columns against DRAM's 2.)
+template <bool ONE, int CL>
+struct TeamSum {
+  static constexpr int K = ONE ? 1 : 6, N4 = ONE ? 1 : 2;  // values; float4 per CTA's sums
+  float* warps;    // [RN_BUFS][RN_SLOT] the warps' sums (unused ones stay 0)
+  float4* ctas;    // [RN_BUFS][CL][N4] the CTAs' sums
+  uint64_t* bars;  // [RN_BUFS] completed by CL sends
+  int in, out;     // buffers of the next post and the next collect
+  uint32_t phase;  // parity of the mbarrier of `out`
+  bool dead;       // a wait gave up: every later sum is NaN, so the failure shows
 
-// Sum over the team and, for rows split over a cluster, over its CTAs.
-template <int CL>
-__device__ __forceinline__ float team_sum(float v, TeamRed<CL>& red) {
-  const int nt = blockDim.x;
-  v = lane_sum<32>(v);
-  if (CL > 1 || nt > 32) {
-    float* slot = red.warp + red.buf * RN_SLOT;
-    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
-    named_bar(threadIdx.y + 1, nt);
-    v = 0.f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (u * 128 >= nt) break;
-      const float4 a = reinterpret_cast<const float4*>(slot)[u];
-      v += (a.x + a.y) + (a.z + a.w);
+  __device__ __forceinline__ void init() {
+    __shared__ __align__(16) float warp_sums[8 * RN_BUFS * RN_SLOT];  // at most 8 teams
+    __shared__ float4 cta_sums[RN_BUFS * CL * N4];
+    __shared__ uint64_t mbars[RN_BUFS];
+    warps = warp_sums + threadIdx.y * RN_BUFS * RN_SLOT;
+    ctas = cta_sums;
+    bars = mbars;
+    in = out = 0;
+    phase = 0;
+    dead = false;
+    for (int i = threadIdx.x; i < RN_BUFS * RN_SLOT; i += blockDim.x) warps[i] = 0.f;
+    if (CL > 1) {
+      if (threadIdx.x == 0) {
+        for (int i = 0; i < RN_BUFS; ++i) mbar_init(mbars + i, 1);
+        fence_mbar_init();
+      }
+      __syncthreads();
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+      named_bar(threadIdx.y + 1, blockDim.x);
     }
   }
-  if (CL > 1) cluster_sum<1, CL>(&v, red);
-  red.buf ^= 1;
-  return v;
-}
-// The same for 6 values (v has room for 8), teams of up to 16 warps.
-template <int CL>
-__device__ __forceinline__ void team_sum6(float* v, TeamRed<CL>& red) {
-  const int nt = blockDim.x, lane = threadIdx.x & 31;
-  v[6] = v[7] = 0.f;
-  float mine = warp_sum8(v);
-  if (CL > 1 || nt > 32) {
-    float* slot = red.warp + red.buf * RN_SLOT;  // [8 values][16 warps]
-    if ((lane & 3) == 0) slot[(lane >> 2) * 16 + (threadIdx.x >> 5)] = mine;
-    named_bar(threadIdx.y + 1, nt);
-    // lane l: value l / 4, warps 4 (l % 4) ..
-    const float4 a = reinterpret_cast<const float4*>(slot)[lane];
-    mine = (a.x + a.y) + (a.z + a.w);
-    mine += __shfl_xor_sync(0xffffffffu, mine, 1);
-    mine += __shfl_xor_sync(0xffffffffu, mine, 2);
-  }
-#pragma unroll
-  for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, mine, 4 * i);
-  if (CL > 1) cluster_sum<6, CL>(v, red);
-  red.buf ^= 1;
-}
-
-// A CTA that exits must not be written to any more: every CTA of the cluster
-// has received all sums.
-template <int CL>
-__device__ __forceinline__ void team_end() {
-  if (CL > 1) {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  }
-}
-
-template <int CL>
-__device__ __forceinline__ Team team_of(int rows, int C, TeamRed<CL>& red) {
-  __shared__ __align__(16) float warp_sums[8 * 2 * RN_SLOT];  // at most 8 teams
-  __shared__ float4 cta_sums[2 * CL * 2];
-  __shared__ uint64_t bars[2];
-  Team t;
-  t.C = C;
-  t.rows = rows;
-  const int per = (C / 8 + CL - 1) / CL;  // column groups of a CTA
-  const int rank = CL == 1 ? 0 : blockIdx.x % CL;
-  t.c = (rank * per + threadIdx.x) * 8;
-  t.on = (int)threadIdx.x < per && t.c < C;
-  t.first = blockIdx.x / CL * blockDim.y + threadIdx.y;
-  t.step = gridDim.x / CL * blockDim.y;
-  red.warp = warp_sums + threadIdx.y * 2 * RN_SLOT;
-  red.cta = cta_sums;
-  red.bar = bars;
-  red.buf = red.phase = 0;
-  red.dead = false;
-  for (int i = threadIdx.x; i < 2 * RN_SLOT; i += blockDim.x) red.warp[i] = 0.f;
-  if (CL > 1) {
-    if (threadIdx.x == 0) {
-      mbar_init(bars, 1);
-      mbar_init(bars + 1, 1);
-      fence_mbar_init();
-    }
-    __syncthreads();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  } else {
-    named_bar(threadIdx.y + 1, blockDim.x);
-  }
-  return t;
-}
-
-// Prefetch slots of a thread: slot k of stage s, 16 bytes each, consecutive
-// threads consecutive. E elements of 16-byte pieces per tensor.
-template <int SLOTS>
-struct Ring {
-  uint4* base;  // this thread's slot 0 of stage 0
-  int nt;
-  __device__ __forceinline__ uint4* at(int stage, int k) const {
-    return base + (size_t)(stage * SLOTS + k) * nt;
-  }
-  template <typename T>
-  __device__ __forceinline__ void fetch(int stage, int k, const T* p) const {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-      const uint4* src = reinterpret_cast<const uint4*>(p) + i;
-      if (sizeof(T) == 2)
-        cp16(at(stage, k + i), src, true);
-      else  // through L1: the two halves of a sector are fetched by two instructions
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;\n" ::"r"(
-                         smem_u32(at(stage, k + i))),
-                     "l"(src));
+  // A CTA that exits must not be written to any more: every CTA of the cluster
+  // has received all sums.
+  __device__ __forceinline__ void end() {
+    if (CL > 1) {
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
   }
-  template <typename T>
-  __device__ __forceinline__ void read(int stage, int k, f32x2* v) const {
-    Raw8<T> r;
+  // The CTA's sums from the warps'.
+  __device__ __forceinline__ void read_warps(int buf, float* v) const {
+    const float4* slot = reinterpret_cast<const float4*>(warps + buf * RN_SLOT);
+    if (ONE) {
+      v[0] = 0.f;
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = *at(stage, k + i);
-    cvt8(r, v);
+      for (int u = 0; u < 8; ++u) {
+        if (u * 128 >= (int)blockDim.x) break;
+        const float4 a = slot[u];
+        v[0] += (a.x + a.y) + (a.z + a.w);
+      }
+    } else {  // lane l: value l / 4, warps 4 (l % 4) ..
+      const float4 a = slot[threadIdx.x & 31];
+      float s = (a.x + a.y) + (a.z + a.w);
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[i] = __shfl_sync(0xffffffffu, s, 4 * i);
+    }
+  }
+  __device__ __forceinline__ void post(float* v) {
+    const int lane = threadIdx.x & 31;
+    float* slot = warps + in * RN_SLOT;
+    if (ONE) {
+      const float s = lane_sum<32>(v[0]);
+      if (lane == 0) slot[threadIdx.x >> 5] = s;
+    } else {  // [8 values][16 warps]
+      v[6] = v[7] = 0.f;
+      const float s = warp_sum8(v);
+      if ((lane & 3) == 0) slot[(lane >> 2) * 16 + (threadIdx.x >> 5)] = s;
+    }
+    if (blockDim.x > 32)
+      named_bar(threadIdx.y + 1, blockDim.x);
+    else
+      __syncwarp();
+    if (CL > 1 && threadIdx.x < 32) {
+      float s[8] = {};
+      read_warps(in, s);
+      if (lane == 0) mbar_arrive_expect_tx(bars + in, CL * 16 * N4);
+      if (lane < CL) {
+        uint32_t rank, to, bar;
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(to)
+            : "r"(smem_u32(ctas + (in * CL + rank) * N4)), "r"(lane));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(bar)
+            : "r"(smem_u32(bars + in)), "r"(lane));
+#pragma unroll
+        for (int i = 0; i < N4; ++i)
+          asm volatile(
+              "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], "
+              "{%1, %2, %3, %4}, [%5];" ::"r"(to + 16 * i),
+              "f"(s[4 * i]), "f"(s[4 * i + 1]), "f"(s[4 * i + 2]), "f"(s[4 * i + 3]), "r"(bar)
+              : "memory");
+      }
+    }
+    if (++in == RN_BUFS) in = 0;
+  }
+  __device__ __forceinline__ void collect(float* v) {
+    if (CL == 1) {
+      read_warps(out, v);
+    } else {
+      const long long t0 = clock64();
+      for (uint32_t ok = dead; !ok;) {
+        asm volatile(
+            "{\n .reg .pred p;\n"
+            " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bars + out)), "r"(phase)
+            : "memory");
+        if (!ok && clock64() - t0 > (1ll << 32)) ok = dead = true;
+      }
+      float s[4 * N4] = {};
+#pragma unroll
+      for (int r = 0; r < CL; ++r)
+#pragma unroll
+        for (int i = 0; i < N4; ++i) {
+          const float4 a = ctas[(out * CL + r) * N4 + i];
+          s[4 * i] += a.x, s[4 * i + 1] += a.y, s[4 * i + 2] += a.z, s[4 * i + 3] += a.w;
+        }
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[i] = dead ? __int_as_float(0x7fc00000) : s[i];
+    }
+    if (++out == RN_BUFS) {
+      out = 0;
+      phase ^= 1;
+    }
   }
 };
 
-template <typename T>
-constexpr int pieces() { return (int)sizeof(T) / 2; }  // 16-byte pieces of 8 elements
-template <typename T, typename R>
-constexpr int fwd_slots() { return pieces<R>() + pieces<T>(); }
-template <typename T, typename R>
-constexpr int fwd_stages() { return fwd_slots<T, R>() == 2 ? 4 : 3; }
-template <typename T, typename R>
-constexpr int bwd_slots() { return 2 * pieces<R>() + 2 * pieces<T>(); }
-template <typename T, typename R>
-constexpr int bwd_stages() { return bwd_slots<T, R>() == 4 ? 4 : 3; }
-
-__device__ __forceinline__ void ld8_or(const float* p, bool have, float other, f32x2* v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = both2(other);
-  if (have) cvt8(ldraw8(p), v);
-}
-
-template <typename T, typename R, int CL>
+// Bound by the bytes of h, x, h_out and y: 20011 rows of 4096 columns, fp32 stream
+// and bf16 branch, both norms: 157 us (984 MB, 6.3 TB/s); one row per block with
+// plain loads took 305.
+template <typename T, typename R, int CL, int S>
 __global__ void __launch_bounds__(1024, 1)
     k_res_norm_fwd(int rows, int C, float inv_C, float eps, const R* h, const T* __restrict__ x,
                    const float* __restrict__ w, const float* __restrict__ w_post,
                    const float* __restrict__ scale, R* h_out, T* __restrict__ y) {
-  constexpr int S = fwd_stages<T, R>(), KX = pieces<R>();
+  constexpr int KX = pieces<R>();
+  constexpr bool SPLIT = sizeof(R) == 4;
   extern __shared__ uint4 smem[];
-  const int nt = blockDim.x * blockDim.y;
-  Ring<fwd_slots<T, R>()> ring = {smem + threadIdx.y * blockDim.x + threadIdx.x, nt};
-  TeamRed<CL> red;
-  const Team t = team_of<CL>(rows, C, red);
+  const Ring<fwd_slots<T, R>(), SPLIT> ring = {
+      smem + threadIdx.y * blockDim.x + threadIdx.x, (int)(blockDim.x * blockDim.y)};
+  const Team<SPLIT> t = team_of<SPLIT, CL>(rows, C);
+  if (!t.on0 || !t.on1 || !x) ring.clear(S);
   auto fetch = [&](int stage, int row) {
-    if (t.on && row < t.rows) {
-      const size_t at = (size_t)row * C + t.c;
-      ring.template fetch<R>(stage, 0, h + at);
-      if (x) ring.template fetch<T>(stage, KX, x + at);
+    if (row < t.rows) {
+      ring.fetch(stage, 0, h + (size_t)row * C, t);
+      if (x) ring.fetch(stage, KX, x + (size_t)row * C, t);
     }
     cp_commit();
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
+  TeamSum<true, CL> sum;
+  sum.init();
   f32x2 wv[4], pv[4], sv[4];
-  ld8_or(w + t.c, t.on, 0.f, wv);
-  ld8_or(w_post + t.c, t.on && w_post, 1.f, pv);
-  ld8_or(scale + t.c, t.on && scale, 1.f, sv);
+  ld_cols(w, t, 0.f, wv);
+  ld_cols(w_post, t, 1.f, pv);
+  ld_cols(scale, t, 1.f, sv);
   int stage = 0;
   for (int row = t.first; row < t.rows; row += t.step) {
     cp_wait<S - 1>();
-    f32x2 hv[4] = {}, xv[4] = {};
-    if (t.on) {
-      ring.template read<R>(stage, 0, hv);
-      if (x) ring.template read<T>(stage, KX, xv);
-    }
-    const size_t at = (size_t)row * C + t.c;
+    f32x2 hv[4], xv[4], a = 0;
+    float s;
+    ring.template read<R>(stage, 0, hv);
+    ring.template read<T>(stage, KX, xv);
     if (w_post) {
-      f32x2 a = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) a = fma2(xv[i], xv[i], a);
-      const f32x2 rx = both2(rsqrtf(fmaf(team_sum(sum2(a), red), inv_C, eps)));
+      s = sum2(a);
+      sum.post(&s);
+      sum.collect(&s);
+      const f32x2 rx = both2(rsqrtf(fmaf(s, inv_C, eps)));
 #pragma unroll
       for (int i = 0; i < 4; ++i) xv[i] = mul2(xv[i], mul2(rx, pv[i]));
+      a = 0;
     }
-    f32x2 a = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       hv[i] = fma2(sv[i], xv[i], hv[i]);
       a = fma2(hv[i], hv[i], a);
     }
-    if (h_out && t.on) st8(h_out + at, hv);
+    if (h_out) st_cols(h_out + (size_t)row * C, t, hv);
     fetch(stage, row + S * t.step);  // the slot has been read
     if (++stage == S) stage = 0;
-    const f32x2 r = both2(rsqrtf(fmaf(team_sum(sum2(a), red), inv_C, eps)));
+    s = sum2(a);
+    sum.post(&s);
+    sum.collect(&s);
+    const f32x2 r = both2(rsqrtf(fmaf(s, inv_C, eps)));
 #pragma unroll
     for (int i = 0; i < 4; ++i) hv[i] = mul2(hv[i], mul2(r, wv[i]));
-    if (t.on) st8(y + at, hv);
+    st_cols(y + (size_t)row * C, t, hv);
   }
   cp_wait<0>();
-  team_end<CL>();
+  sum.end();
 }
 
 // part [blocks][1 + (w_post) + (scale)][C]: the blocks' sums of dw, dw_post, dscale.
+// With n = h r, m = x rx (x without w_post), sp = scale w_post:
+//   dh = dh_out + r dy w - r^3 mean(dy w h) h
+//   dx = rx (sp dh - m mean(sp dh m)),   dw_post = scale sum dh m,   dscale = w_post sum dh m
+// and mean(sp dh m) is a combination of sums that do not need dh, so a row takes
+// one reduction, of 6 sums. In a cluster the next row's sums are formed and posted
+// before this row's are collected, so that the exchange's latency passes behind a
+// row's work (4000 rows of 16384 bf16 columns 369 -> 320 us); within a CTA reading
+// the row twice for that costs more than it hides (32768 rows of 2048: 135 us
+// against 127). Bound by the bytes of h, dh_out, dy, x, dh and dx: 32768 rows of
+// 2048 bf16 columns, both norms, 127 us (805 MB, 6.4 TB/s).
 template <typename T, typename R, int CL>
 __global__ void __launch_bounds__(512, 1)
     k_res_norm_bwd(int rows, int C, float inv_C, float eps, const R* __restrict__ h,
@@ -460,99 +522,121 @@ __global__ void __launch_bounds__(512, 1)
                    float* __restrict__ part) {
   constexpr int S = bwd_stages<T, R>(), KD = pieces<R>(), KG = 2 * pieces<R>(),
                 KX = KG + pieces<T>();
+  constexpr bool SPLIT = sizeof(R) == 4;
   extern __shared__ uint4 smem[];
-  const int nt = blockDim.x * blockDim.y;
-  Ring<bwd_slots<T, R>()> ring = {smem + threadIdx.y * blockDim.x + threadIdx.x, nt};
-  TeamRed<CL> red;
-  const Team t = team_of<CL>(rows, C, red);
+  const Ring<bwd_slots<T, R>(), SPLIT> ring = {
+      smem + threadIdx.y * blockDim.x + threadIdx.x, (int)(blockDim.x * blockDim.y)};
+  const Team<SPLIT> t = team_of<SPLIT, CL>(rows, C);
   const bool with_x = w_post || scale;
+  if (!t.on0 || !t.on1 || !dh_out || !with_x) ring.clear(S);
   auto fetch = [&](int stage, int row) {
-    if (t.on && row < t.rows) {
-      const size_t at = (size_t)row * C + t.c;
-      ring.template fetch<R>(stage, 0, h + at);
-      if (dh_out) ring.template fetch<R>(stage, KD, dh_out + at);
-      ring.template fetch<T>(stage, KG, dy + at);
-      if (with_x) ring.template fetch<T>(stage, KX, x + at);
+    if (row < t.rows) {
+      const size_t at = (size_t)row * C;
+      ring.fetch(stage, 0, h + at, t);
+      if (dh_out) ring.fetch(stage, KD, dh_out + at, t);
+      ring.fetch(stage, KG, dy + at, t);
+      if (with_x) ring.fetch(stage, KX, x + at, t);
     }
     cp_commit();
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
-  f32x2 wv[4], sp[4], aw[4] = {}, am[4] = {};  // sp = scale w_post
-  ld8_or(w + t.c, t.on, 0.f, wv);
-  ld8_or(scale + t.c, t.on && scale, 1.f, sp);
-  if (w_post) {
+  TeamSum<false, CL> sum;
+  sum.init();
+  f32x2 wv[4], sp[4], aw[4] = {}, am[4] = {};
+  ld_cols(w, t, 0.f, wv);
+  {
     f32x2 pv[4];
-    ld8_or(w_post + t.c, t.on, 0.f, pv);
+    ld_cols(scale, t, 1.f, sp);
+    ld_cols(w_post, t, 1.f, pv);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sp[i] = mul2(sp[i], pv[i]);
   }
-  int stage = 0;
-  for (int row = t.first; row < t.rows; row += t.step) {
-    cp_wait<S - 1>();
-    f32x2 hv[4] = {}, gw[4] = {}, xv[4] = {}, dv[4] = {}, a[6] = {};
-    f32x2 gv[4] = {};
-    if (t.on) {
-      ring.template read<R>(stage, 0, hv);
-      if (dh_out) ring.template read<R>(stage, KD, dv);
-      ring.template read<T>(stage, KG, gv);
-      if (with_x) ring.template read<T>(stage, KX, xv);
-    }
+  struct Row {
+    f32x2 h[4], g[4], x[4], d[4];
+  };
+  auto read = [&](int stage, Row& v) {
+    ring.template read<R>(stage, 0, v.h);
+    ring.template read<R>(stage, KD, v.d);
+    ring.template read<T>(stage, KG, v.g);
+    ring.template read<T>(stage, KX, v.x);
+  };
+  auto post = [&](const Row& v) {
+    f32x2 a[6] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      gw[i] = mul2(gv[i], wv[i]);
-      a[0] = fma2(hv[i], hv[i], a[0]);
-      a[1] = fma2(gw[i], hv[i], a[1]);
-    }
-    if (w_post) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x2 q = mul2(sp[i], xv[i]);
-        a[2] = fma2(xv[i], xv[i], a[2]);
-        a[3] = fma2(q, dv[i], a[3]);
-        a[4] = fma2(q, gw[i], a[4]);
-        a[5] = fma2(q, hv[i], a[5]);
+      const f32x2 gw = mul2(v.g[i], wv[i]);
+      a[0] = fma2(v.h[i], v.h[i], a[0]);
+      a[1] = fma2(gw, v.h[i], a[1]);
+      if (w_post) {
+        const f32x2 q = mul2(sp[i], v.x[i]);
+        a[2] = fma2(v.x[i], v.x[i], a[2]);
+        a[3] = fma2(q, v.d[i], a[3]);
+        a[4] = fma2(q, gw, a[4]);
+        a[5] = fma2(q, v.h[i], a[5]);
       }
     }
-    fetch(stage, row + S * t.step);  // the slot has been read
-    if (++stage == S) stage = 0;
     float s[8];
 #pragma unroll
     for (int i = 0; i < 6; ++i) s[i] = sum2(a[i]);
-    team_sum6(s, red);
-    const size_t at = (size_t)row * C + t.c;
+    sum.post(s);
+  };
+  int stage = 0;
+  if (CL > 1 && t.first < t.rows) {
+    Row v;
+    cp_wait<S - 1>();
+    read(0, v);
+    post(v);
+  }
+  for (int row = t.first; row < t.rows; row += t.step) {
+    const int next = stage + 1 == S ? 0 : stage + 1;
+    Row v;
+    if (CL == 1) {
+      cp_wait<S - 1>();
+      read(stage, v);
+      post(v);
+    } else if (row + t.step < t.rows) {
+      cp_wait<S - 2>();
+      read(next, v);
+      post(v);
+    }
+    float s[8];
+    sum.collect(s);
+    if (CL > 1) read(stage, v);
+    f32x2 *hv = v.h, *gv = v.g, *xv = v.x, *dv = v.d;
+    const size_t at = (size_t)row * C;
+    fetch(stage, row + S * t.step);  // the slot has been read
+    stage = next;
     const float r = rsqrtf(fmaf(s[0], inv_C, eps));
     const float rx = w_post ? rsqrtf(fmaf(s[2], inv_C, eps)) : 1.f;
     const float hc = -r * r * r * s[1] * inv_C;  // factor of h in dh
     const f32x2 r2 = both2(r), hc2 = both2(hc), rx2 = both2(rx);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      aw[i] = fma2(gv[i], mul2(hv[i], r2), aw[i]);
-      dv[i] = fma2(hv[i], hc2, fma2(gw[i], r2, dv[i]));  // dh
+      const f32x2 gr = mul2(gv[i], r2);
+      aw[i] = fma2(gr, hv[i], aw[i]);
+      dv[i] = fma2(hv[i], hc2, fma2(gr, wv[i], dv[i]));  // dh
       xv[i] = mul2(xv[i], rx2);                          // m
       am[i] = fma2(dv[i], xv[i], am[i]);
     }
-    if (t.on) st8(dh + at, dv);
+    st_cols(dh + at, t, dv);
     if (dx) {
-      if (w_post) {
-        // mean(sp dh m) from the sums of its terms
-        const f32x2 e = both2(-rx * inv_C * fmaf(hc, s[5], fmaf(r, s[4], s[3])));
+      // mean(sp dh m) from the sums of its terms
+      const f32x2 e = both2(w_post ? -rx * inv_C * fmaf(hc, s[5], fmaf(r, s[4], s[3])) : 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dv[i] = mul2(rx2, fma2(xv[i], e, mul2(dv[i], sp[i])));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dv[i] = mul2(dv[i], sp[i]);
+      for (int i = 0; i < 4; ++i) {
+        dv[i] = mul2(dv[i], sp[i]);
+        if (w_post) dv[i] = mul2(rx2, fma2(xv[i], e, dv[i]));
       }
-      if (t.on) st8(dx + at, dv);
+      st_cols(dx + at, t, dv);
     }
   }
   cp_wait<0>();
-  team_end<CL>();
-  // the block's sums, teams joined through shared memory (the ring is drained);
-  // sum dh m times scale is dw_post, times w_post dscale
+  sum.end();
+  // the block's sums, teams joined through shared memory (the ring is drained)
   float* mine = reinterpret_cast<float*>(smem) + (threadIdx.y * blockDim.x + threadIdx.x) * 8;
   const int narr = 1 + (w_post != nullptr) + (scale != nullptr);
-  float* out = part + (size_t)(blockIdx.x / CL) * narr * C + t.c;
+  float* out = part + (size_t)(blockIdx.x / CL) * narr * C;
   auto join = [&](f32x2* v) {
     if (blockDim.y == 1) return;
     __syncthreads();
@@ -568,22 +652,17 @@ __global__ void __launch_bounds__(512, 1)
   };
   join(aw);
   if (with_x) join(am);
-  if (threadIdx.y || !t.on) return;
-  st8(out, aw);
-  if (w_post) {
-    f32x2 sv[4];
-    ld8_or(scale + t.c, scale, 1.f, sv);
+  if (threadIdx.y) return;
+  st_cols(out, t, aw);
+  auto times = [&](const float* p) {
+    f32x2 v[4];
+    ld_cols(p, t, 1.f, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sv[i] = mul2(am[i], sv[i]);
-    st8(out += C, sv);
-  }
-  if (scale) {
-    f32x2 pv[4];
-    ld8_or(w_post + t.c, w_post, 1.f, pv);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pv[i] = mul2(am[i], pv[i]);
-    st8(out += C, pv);
-  }
+    for (int i = 0; i < 4; ++i) v[i] = mul2(am[i], v[i]);
+    st_cols(out += C, t, v);
+  };
+  if (w_post) times(scale);
+  if (scale) times(w_post);
 }
 
 // ------------------------------------------------------------------ host side
@@ -694,11 +773,23 @@ cudaError_t launch_res(const gdn_res_norm_shape& s, const ResArgs& a, const ResP
                        cudaStream_t st) {
   const int nt = p.team * p.teams;
   const float inv = 1.f / (float)s.C;
-  if (!a.dy)
-    return launch_rows(k_res_norm_fwd<T, R, CL>, p, p.blocks(s.rows, 1024),
-                       nt * 16 * fwd_slots<T, R>() * fwd_stages<T, R>(), st, s.rows, s.C, inv,
-                       s.eps, (const R*)a.h, (const T*)a.x, a.w, a.w_post, a.scale, (R*)a.ho,
-                       (T*)a.y);
+  if (!a.dy) {
+    // rows in flight: 4, where that is what an SM's shared memory holds for 1024
+    // threads; 3 for fp32 streams, and for mixed types in CTAs of 1024 threads
+    // (mixed, 4096 columns: 152 us with 4, 171 with 3; 8192: 135 with 4, 123 with 3)
+    constexpr int slots = fwd_slots<T, R>();
+    auto go = [&](auto stages) {
+      constexpr int S = decltype(stages)::value;
+      return launch_rows(k_res_norm_fwd<T, R, CL, S>, p, p.blocks(s.rows, 1024),
+                         nt * 16 * slots * S, st, s.rows, s.C, inv, s.eps, (const R*)a.h,
+                         (const T*)a.x, a.w, a.w_post, a.scale, (R*)a.ho, (T*)a.y);
+    };
+    if constexpr (slots == 3 && CL == 1) {
+      if (p.team > 512) return go(std::integral_constant<int, 3>());
+    }
+    constexpr int usual = slots == 4 || (slots == 3 && CL != 1) ? 3 : 4;
+    return go(std::integral_constant<int, usual>());
+  }
   return launch_rows(k_res_norm_bwd<T, R, CL>, p, p.blocks(s.rows, 512),
                      nt * 16 * bwd_slots<T, R>() * bwd_stages<T, R>(), st, s.rows, s.C, inv,
                      s.eps, (const R*)a.h, (const T*)a.x, a.w, a.w_post, a.scale,
