@@ -725,7 +725,10 @@ struct ResPlan {
   int cl, team, teams;  // CTAs per row, threads of a CTA per row, rows per CTA
   int blocks(int rows, int threads) const {  // CTAs, so that each SM has up to `threads`
     const int all = (rows + teams - 1) / teams;
-    return cl * std::min(all, std::max(1, RN_SMS * (threads / (team * teams)) / cl));
+    // clusters of 4 leave some SMs without a place in one: 36 of them fit, not 38,
+    // and two more than fit would run after the others
+    const int sms = cl == 4 ? 36 * 4 : RN_SMS;
+    return cl * std::min(all, std::max(1, sms * (threads / (team * teams)) / cl));
   }
 };
 ResPlan res_plan(int C, int cols) {
