@@ -15,19 +15,15 @@ namespace {
 constexpr int GN_NT = 256;     // threads of a block
 constexpr int GN_U = 4;        // rows a thread has in flight (forward)
 constexpr int GN_UB = 2;       // rows a thread has in flight (backward)
-constexpr int GN_PARTS = 608;  // most partial sums of dw
-
-// act(z) and its derivative
+// Blocks of the backward on an SM: bf16 3 of 80 registers, fp32 2; its grid is one
+// wave of them (bf16; 4 blocks of 64 registers spill, 110 us against 106) or two.
 template <typename T>
-__device__ __forceinline__ void gate(float z, int act, float& a, float& da) {
+constexpr int gate_blocks() { return sizeof(T) == 2 ? 3 : 2; }
+
+template <typename T>
+__device__ __forceinline__ float gate(float z, int act) {
   const float s = sigmoid_as<T>(z);
-  if (act == GDN_GATE_SILU) {
-    a = z * s;
-    da = s * (1.f + z * (1.f - s));
-  } else {
-    a = s;
-    da = s * (1.f - s);
-  }
+  return act == GDN_GATE_SILU ? z * s : s;
 }
 
 // z of (token t, head h), row r = t H + h.
@@ -37,7 +33,9 @@ __device__ __forceinline__ size_t z_at(uint32_t r, const FastDiv& byH, int d, lo
   return (size_t)t * ldz + (size_t)h * d;
 }
 
-// L lanes (a power of two >= d / 8) per row of d values, GN_U rows per thread.
+// L lanes (a power of two >= d / 8) per row of d values, GN_U rows per thread, all
+// loaded before the first is used. Bound by the bytes of o, z and y: 131072 x 16
+// rows of 128 bf16 values 224 us (1.61 GB, 7.2 TB/s).
 template <typename T, int L>
 __global__ void __launch_bounds__(GN_NT)
     k_gate_norm_fwd(uint32_t nrow, FastDiv byH, int d, float inv_d, int act, long long ldz,
@@ -70,27 +68,29 @@ __global__ void __launch_bounds__(GN_NT)
     const float rr = rsqrtf(fmaf(ss, inv_d, eps));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float a, da;
-      gate<T>(zz[i], act, a, da);
-      x[i] = x[i] * rr * (wv[i] * a);
+      x[i] = x[i] * rr * (wv[i] * gate<T>(zz[i], act));
     }
     if (r < nrow && c < d) st8(y + (size_t)r * d + c, x);
   }
 }
 
-// Blocks take every gridDim.x-th group of rows; each thread keeps the dw of its
-// 8 columns, part[block] = the block's sum.
+// Blocks take every gridDim.x-th group of rows; each thread keeps the dw of its 8
+// columns, part[block] = the block's sum. The elementwise arithmetic is in pairs:
+// the instructions of an element (sigmoid and its derivative among them) come
+// close to the memory's time. Bound by the bytes of o, z, dy, do and dz: 16411 x 16
+// rows of 256 bf16 values 106 us (672 MB, 6.3 TB/s; 110 with unpaired arithmetic,
+// 126 with the next rows in flight through shared memory).
 template <typename T, int L>
-__global__ void __launch_bounds__(GN_NT, sizeof(T) == 2 ? GN_PARTS / 152 : 2)
+__global__ void __launch_bounds__(GN_NT, gate_blocks<T>())
     k_gate_norm_bwd(uint32_t nrow, FastDiv byH, int d, float inv_d, int act, long long ldz,
                     float eps, const T* __restrict__ o, const T* __restrict__ z,
                     const float* __restrict__ w, const T* __restrict__ dy, T* __restrict__ dout,
                     T* __restrict__ dz, float* __restrict__ part) {
   constexpr int NG = GN_NT / L;
-  __shared__ float red[NG][L * 8];
+  __shared__ __align__(16) float red[NG][L * 8];
   const int c = (threadIdx.x % L) * 8, gi = threadIdx.x / L;
-  float acc[8] = {}, wv[8] = {};
-  if (c < d) ld8(w + c, wv);
+  f32x2 acc[4] = {}, wv[4] = {};
+  if (c < d) cvt8(ldraw8(w + c), wv);
   for (uint32_t b = blockIdx.x * (NG * GN_UB); b < nrow; b += gridDim.x * (NG * GN_UB)) {
     Raw8<T> xr[GN_UB], zr[GN_UB], gr[GN_UB];
 #pragma unroll
@@ -106,38 +106,47 @@ __global__ void __launch_bounds__(GN_NT, sizeof(T) == 2 ? GN_PARTS / 152 : 2)
 #pragma unroll
     for (int u = 0; u < GN_UB; ++u) {
       const uint32_t r = b + u * NG + gi;
-      float x[8], zz[8], gy[8], go[8], ss = 0.f, sd = 0.f;
-      cvt8(xr[u], x);
-      cvt8(zr[u], zz);
-      cvt8(gr[u], gy);
+      f32x2 x[4], ga[4], go[4], gz[4], ss = 0, sd = 0;
+      {
+        float zz[8];
+        f32x2 gy[4];
+        cvt8(xr[u], x);
+        cvt8(zr[u], zz);
+        cvt8(gr[u], gy);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float a, da;
-        gate<T>(zz[i], act, a, da);
-        zz[i] = gy[i] * (wv[i] * da);
-        gy[i] *= a;
-        go[i] = gy[i] * wv[i];
-        ss = fmaf(x[i], x[i], ss);
-        sd = fmaf(go[i], x[i], sd);
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 s = pack2(sigmoid_as<T>(zz[2 * i]), sigmoid_as<T>(zz[2 * i + 1]));
+          const f32x2 t = fma2(s, both2(-1.f), both2(1.f));  // 1 - s
+          f32x2 a = s, da = mul2(s, t);
+          if (act == GDN_GATE_SILU) {
+            a = mul2(s, pack2(zz[2 * i], zz[2 * i + 1]));
+            da = fma2(a, t, s);  // s (1 + z (1 - s))
+          }
+          gz[i] = mul2(mul2(gy[i], wv[i]), da);
+          ga[i] = mul2(gy[i], a);
+          go[i] = mul2(ga[i], wv[i]);
+          ss = fma2(x[i], x[i], ss);
+          sd = fma2(go[i], x[i], sd);
+        }
       }
-      ss = lane_sum<L>(ss);
-      sd = lane_sum<L>(sd);
-      const float rr = rsqrtf(fmaf(ss, inv_d, eps)), m = sd * rr * inv_d;
+      const float s1 = lane_sum<L>(sum2(ss)), s2 = lane_sum<L>(sum2(sd));
+      const float rr = rsqrtf(fmaf(s1, inv_d, eps));
+      // n = x r; do = r (go - n mean(go n)); dz = gz n; dw += ga n
+      const f32x2 r2 = both2(rr), m2 = both2(-s2 * rr * rr * inv_d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float n = x[i] * rr;
-        go[i] = rr * fmaf(-n, m, go[i]);
-        zz[i] *= n;
-        acc[i] = fmaf(gy[i], n, acc[i]);
+      for (int i = 0; i < 4; ++i) {
+        const f32x2 n = mul2(x[i], r2);
+        go[i] = fma2(n, m2, mul2(go[i], r2));
+        gz[i] = mul2(gz[i], n);
+        acc[i] = fma2(ga[i], n, acc[i]);
       }
       if (r < nrow && c < d) {
         st8(dout + (size_t)r * d + c, go);
-        st8(dz + (size_t)r * d + c, zz);
+        st8(dz + (size_t)r * d + c, gz);
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) red[gi][c + i] = acc[i];
+  st8(&red[gi][c], acc);
   __syncthreads();
   for (int i = threadIdx.x; i < d; i += GN_NT) {
     float a = 0.f;
@@ -681,25 +690,30 @@ int lanes_of(int d) {
 }
 int gate_parts(const gdn_gate_norm_shape& s) {
   const long long g = GN_NT / lanes_of(s.d) * GN_UB, n = (long long)s.rows * s.H;
-  return (int)std::min<long long>(GN_PARTS, (n + g - 1) / g);
+  const int most = s.dtype == GDN_DTYPE_BF16 ? 152 * gate_blocks<__nv_bfloat16>()
+                                             : 152 * 2 * gate_blocks<float>();
+  return (int)std::min<long long>(most, (n + g - 1) / g);
 }
 
 template <typename T, int L>
-void launch_gate(const gdn_gate_norm_shape& s, const void* o, const void* z, const float* w,
-                 const void* dy, void* out, void* dz, float* part, cudaStream_t st) {
+cudaError_t launch_gate(const gdn_gate_norm_shape& s, const void* o, const void* z,
+                        const float* w, const void* dy, void* out, void* dz, float* part,
+                        cudaStream_t st) {
   const uint32_t n = (uint32_t)s.rows * (uint32_t)s.H, per = GN_NT / L * GN_U;
   const FastDiv byH(s.H);
   const float inv = 1.f / (float)s.d;
-  if (!dy)
+  if (!dy) {
     k_gate_norm_fwd<T, L><<<(n + per - 1) / per, GN_NT, 0, st>>>(
         n, byH, s.d, inv, s.act, s.ldz, s.eps, (const T*)o, (const T*)z, w, (T*)out);
-  else
-    k_gate_norm_bwd<T, L><<<gate_parts(s), GN_NT, 0, st>>>(n, byH, s.d, inv, s.act, s.ldz, s.eps,
-                                                           (const T*)o, (const T*)z, w,
-                                                           (const T*)dy, (T*)out, (T*)dz, part);
+  } else {
+    k_gate_norm_bwd<T, L><<<gate_parts(s), GN_NT, 0, st>>>(
+        n, byH, s.d, inv, s.act, s.ldz, s.eps, (const T*)o, (const T*)z, w, (const T*)dy, (T*)out,
+        (T*)dz, part);
+  }
+  return cudaGetLastError();
 }
 template <typename T>
-void dispatch_gate(const gdn_gate_norm_shape& s, const void* o, const void* z, const float* w,
+cudaError_t dispatch_gate(const gdn_gate_norm_shape& s, const void* o, const void* z, const float* w,
                    const void* dy, void* out, void* dz, float* part, cudaStream_t st) {
   switch (lanes_of(s.d)) {
     case 1: return launch_gate<T, 1>(s, o, z, w, dy, out, dz, part, st);
@@ -830,12 +844,12 @@ gdn_status gdn_gate_norm_fwd(const gdn_gate_norm_shape* shape, const void* o, co
   if (s.rows == 0) return GDN_OK;
   cudaStream_t st = (cudaStream_t)stream;
   prof_mark(st, "gate_norm_fwd");
-  if (s.dtype == GDN_DTYPE_BF16)
-    dispatch_gate<__nv_bfloat16>(s, o, z, w, nullptr, y, nullptr, nullptr, st);
-  else
-    dispatch_gate<float>(s, o, z, w, nullptr, y, nullptr, nullptr, st);
+  const cudaError_t ce =
+      s.dtype == GDN_DTYPE_BF16
+          ? dispatch_gate<__nv_bfloat16>(s, o, z, w, nullptr, y, nullptr, nullptr, st)
+          : dispatch_gate<float>(s, o, z, w, nullptr, y, nullptr, nullptr, st);
   prof_mark(st, nullptr);
-  return cudaGetLastError() ? GDN_ERR_CUDA : GDN_OK;
+  return ce ? GDN_ERR_CUDA : GDN_OK;
 }
 
 size_t gdn_gate_norm_workspace_bytes(const gdn_gate_norm_shape* shape) {
@@ -862,11 +876,10 @@ gdn_status gdn_gate_norm_bwd(const gdn_gate_norm_shape* shape, const void* o, co
   float* part = (float*)workspace;
   if (s.rows > 0) {
     prof_mark(st, "gate_norm_bwd");
-    if (s.dtype == GDN_DTYPE_BF16)
-      dispatch_gate<__nv_bfloat16>(s, o, z, w, dy, dout, dz, part, st);
-    else
-      dispatch_gate<float>(s, o, z, w, dy, dout, dz, part, st);
-    if (cudaGetLastError()) return GDN_ERR_CUDA;
+    if (s.dtype == GDN_DTYPE_BF16
+            ? dispatch_gate<__nv_bfloat16>(s, o, z, w, dy, dout, dz, part, st)
+            : dispatch_gate<float>(s, o, z, w, dy, dout, dz, part, st))
+      return GDN_ERR_CUDA;
   }
   const cudaError_t ce = col_sum(part, gate_parts(s), s.d, s.d, dw, nullptr, nullptr, st);
   prof_mark(st, nullptr);
