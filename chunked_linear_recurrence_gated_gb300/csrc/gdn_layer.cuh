@@ -157,6 +157,15 @@ __device__ __forceinline__ float softplusf_(float x) {
   return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
 }
 
+// The column sums that end a backward start while its kernel still runs (their
+// launch takes as long as a small call's work) and wait for its results here.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // out[i] = sum over p of part[p][i], i < n, p < np, in a fixed order; column i
 // belongs to array i / C of up to three outputs (NULL: dropped).
 cudaError_t col_sum(const float* part, int np, int n, int C, float* o0, float* o1, float* o2,

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(GN_NT, gate_blocks<T>())
                     T* __restrict__ dz, float* __restrict__ part) {
   constexpr int NG = GN_NT / L;
   __shared__ __align__(16) float red[NG][L * 8];
+  let_next_start();
   const int c = (threadIdx.x % L) * 8, gi = threadIdx.x / L;
   f32x2 acc[4] = {}, wv[4] = {};
   if (c < d) cvt8(ldraw8(w + c), wv);
@@ -537,6 +538,7 @@ __global__ void __launch_bounds__(512, 1)
       smem + threadIdx.y * blockDim.x + threadIdx.x, (int)(blockDim.x * blockDim.y)};
   const Team<SPLIT> t = team_of<SPLIT, CL>(rows, C);
   const bool with_x = w_post || scale;
+  let_next_start();
   if (!t.on0 || !t.on1 || !dh_out || !with_x) ring.clear(S);
   auto fetch = [&](int stage, int row) {
     if (row < t.rows) {

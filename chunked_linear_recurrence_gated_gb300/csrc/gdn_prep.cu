@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(PR_NT)
                const T* __restrict__ dkn, const T* __restrict__ dg, const T* __restrict__ dbeta,
                T* __restrict__ dq, T* __restrict__ dk, T* __restrict__ dxg, T* __restrict__ dxb,
                float* __restrict__ part) {
+  let_next_start();
   if ((int)blockIdx.x < gate_blocks) {
     prep_bwd_gates<T>(blockIdx.x, rows, H, hp_log, per, ldg, ldb, xg, xb, rate, bias, dg, dbeta,
                       dxg, dxb, part);
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(1024)
               float* o2) {
   __shared__ float red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, i0 = blockIdx.x * 32;
+  after_previous();
   float a = 0.f;
   if (i0 + tx < n) {
 #pragma unroll 4
@@ -269,8 +271,16 @@ void launch_prep_bwd(const gdn_prep_shape& s, const void* q, const void* k, cons
 cudaError_t col_sum(const float* part, int np, int n, int C, float* o0, float* o1, float* o2,
                     cudaStream_t st) {
   prof_mark(st, "layer_col_sum");
-  k_col_sum<<<(n + 31) / 32, 1024, 0, st>>>(part, np, n, C, o0, o1, o2);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((n + 31) / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_col_sum, part, np, n, C, o0, o1, o2);
 }
 
 }  // namespace gdn
