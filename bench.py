@@ -126,9 +126,27 @@ def kernel_model(name, dk, dv, esz=2, C=64):
         by = (C * (2 * dk + 2 * dv) * esz + C * esz + C * C * esz + C * f4 + 2 * dk * dv * esz
               + 2 * C * dv * esz + C * (2 * dk + dv) * esz + 2 * C * esz)
         fl = 6 * C * dk * dv + 4 * C * C * dv + 14 * C * C * dk + 4 * C ** 3
+    elif name in LAYER_KERNELS:
+        by, fl = LAYER_KERNELS[name](dk, dv, esz, C)
     else:
         return None
     return by, fl
+
+
+# The layer operators' kernels (include/gdn_layer.h), per 64 tokens of a head;
+# none of them runs in this benchmark's workloads. The norms' rows: dv columns.
+LAYER_KERNELS = {
+    "step": lambda dk, dv, e, C: (C * (8 * dk * dv + (2 * dk + 2 * dv + 2) * e), 8 * C * dk * dv),
+    "conv_step": lambda dk, dv, e, C: (C * (2 * 3 + 2) * (2 * dk + dv) * e,
+                                       C * 12 * (2 * dk + dv)),
+    "prep_fwd": lambda dk, dv, e, C: (C * (4 * dk + 4) * e, C * 6 * dk),
+    "prep_bwd": lambda dk, dv, e, C: (C * (6 * dk + 6) * e, C * 12 * dk),
+    "gate_norm_fwd": lambda dk, dv, e, C: (3 * C * dv * e, 8 * C * dv),
+    "gate_norm_bwd": lambda dk, dv, e, C: (5 * C * dv * e, 18 * C * dv),
+    "res_norm_fwd": lambda dk, dv, e, C: (4 * C * dv * e, 8 * C * dv),
+    "res_norm_bwd": lambda dk, dv, e, C: (6 * C * dv * e, 24 * C * dv),
+    "layer_col_sum": lambda dk, dv, e, C: (4 * dv, dv),
+}
 
 
 # ---------------------------------------------------------------- clocks
@@ -575,7 +593,8 @@ def op_roofline(w, ms, which="fwd+bwd"):
 # Which phase of the op each kernel belongs to: its roofline credits it with
 # that phase's algorithmic bytes for the token-heads it processes.
 KERNEL_PHASE = {"tc_grad": "bwd", "simt_grad": "bwd", "tc_chains_bwd": "bwd",
-                "tc_chain_rev": "bwd", "simt_st_bwd": "bwd"}
+                "tc_chain_rev": "bwd", "simt_st_bwd": "bwd",
+                "prep_bwd": "bwd", "gate_norm_bwd": "bwd", "res_norm_bwd": "bwd"}
 
 
 def kernel_roofline(name, per_launch_ms, units_per_launch, w, hbm, peak_kind):
