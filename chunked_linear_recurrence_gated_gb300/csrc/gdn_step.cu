@@ -77,9 +77,12 @@ __device__ __forceinline__ float2 ld2_again(const float* p) {
   return r;
 }
 
-// fp32 as two TF32 values (11 bits each of the significand).
+// fp32 as two TF32 values (11 significant bits each): the first rounded to
+// nearest, so the second holds the rest to 2^-24 of x (truncating the first would
+// leave 2^-22, and errors of one sign). A NaN that the addition carries out of the
+// first stays in the second.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 // Two values of k or q as TF32 operands: bf16 values are exact in the first
@@ -121,7 +124,7 @@ __device__ __forceinline__ void mma_tf32z(float* c, const uint32_t* a, uint32_t 
 // written out, so the state is read and written once per tile. c, p, the dot
 // products and the sum over tokens in the last line are m16n8k8 TF32 MMAs; fp32
 // operands (the state, u, fp32 k and q) are taken as two TF32 parts each, so
-// products are good to about 2^-21. k and q are used as they are in memory; their
+// products are good to about 2^-23. k and q are used as they are in memory; their
 // norms scale the results. S^T (16 columns x 8 rows) is read as A fragments with
 // the reduced rows in the order 0 2 4 6 1 3 5 7, in which the fragment is also the
 // accumulator's of the update. The state itself is only ever updated by an fp32
