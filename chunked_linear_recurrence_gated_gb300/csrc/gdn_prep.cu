@@ -202,9 +202,11 @@ __global__ void __launch_bounds__(PR_NT)
   }
 }
 
-// Block: 32 columns, 32 partials at a time; then warp j adds up column j.
+// Block: 32 columns, 32 partials at a time; then warp j adds up column j. The
+// partials change while this kernel is resident, so `part` is not __restrict__:
+// its loads stay ordinary ones, behind after_previous().
 __global__ void __launch_bounds__(1024)
-    k_col_sum(const float* __restrict__ part, int np, int n, int C, float* o0, float* o1,
+    k_col_sum(const float* part, int np, int n, int C, float* o0, float* o1,
               float* o2) {
   __shared__ float red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, i0 = blockIdx.x * 32;
