@@ -39,8 +39,8 @@ __device__ __forceinline__ size_t z_at(uint32_t r, const FastDiv& byH, int d, lo
 template <typename T, int L>
 __global__ void __launch_bounds__(GN_NT)
     k_gate_norm_fwd(uint32_t nrow, FastDiv byH, int d, float inv_d, int act, long long ldz,
-                    float eps, const T* __restrict__ o, const T* __restrict__ z,
-                    const float* __restrict__ w, T* __restrict__ y) {
+                    float eps, const T* o, const T* z, const float* w, T* y) {
+  chain();
   constexpr int NG = GN_NT / L;
   const int c = (threadIdx.x % L) * 8;
   const uint32_t r0 = blockIdx.x * (NG * GN_U) + threadIdx.x / L;
@@ -83,11 +83,11 @@ __global__ void __launch_bounds__(GN_NT)
 template <typename T, int L>
 __global__ void __launch_bounds__(GN_NT, gate_blocks<T>())
     k_gate_norm_bwd(uint32_t nrow, FastDiv byH, int d, float inv_d, int act, long long ldz,
-                    float eps, const T* __restrict__ o, const T* __restrict__ z,
-                    const float* __restrict__ w, const T* __restrict__ dy, T* __restrict__ dout,
-                    T* __restrict__ dz, float* __restrict__ part) {
+                    float eps, const T* o, const T* z, const float* w, const T* dy, T* dout, T* dz,
+                    float* part) {
   constexpr int NG = GN_NT / L;
   __shared__ __align__(16) float red[NG][L * 8];
+  chain();
   let_next_start();
   const int c = (threadIdx.x % L) * 8, gi = threadIdx.x / L;
   f32x2 acc[4] = {}, wv[4] = {};
@@ -179,7 +179,6 @@ struct Team {
   int C, rows, first, step;  // this team takes rows first, first + step, ..
   int c0, c1;                // first columns of the two groups of 4
   bool on0, on1;             // whether they exist
-  __device__ __forceinline__ bool on() const { return on0; }
 };
 
 template <bool SPLIT, int CL>
@@ -449,15 +448,15 @@ struct TeamSum {
 // plain loads took 305.
 template <typename T, typename R, int CL, int S>
 __global__ void __launch_bounds__(1024, 1)
-    k_res_norm_fwd(int rows, int C, float inv_C, float eps, const R* h, const T* __restrict__ x,
-                   const float* __restrict__ w, const float* __restrict__ w_post,
-                   const float* __restrict__ scale, R* h_out, T* __restrict__ y) {
+    k_res_norm_fwd(int rows, int C, float inv_C, float eps, const R* h, const T* x, const float* w,
+                   const float* w_post, const float* scale, R* h_out, T* y) {
   constexpr int KX = pieces<R>();
   constexpr bool SPLIT = sizeof(R) == 4;
   extern __shared__ uint4 smem[];
   const Ring<fwd_slots<T, R>(), SPLIT> ring = {
       smem + threadIdx.y * blockDim.x + threadIdx.x, (int)(blockDim.x * blockDim.y)};
   const Team<SPLIT> t = team_of<SPLIT, CL>(rows, C);
+  chain();
   if (!t.on0 || !t.on1 || !x) ring.clear(S);
   auto fetch = [&](int stage, int row) {
     if (row < t.rows) {
@@ -525,11 +524,9 @@ __global__ void __launch_bounds__(1024, 1)
 // 2048 bf16 columns, both norms, 127 us (805 MB, 6.4 TB/s).
 template <typename T, typename R, int CL>
 __global__ void __launch_bounds__(512, 1)
-    k_res_norm_bwd(int rows, int C, float inv_C, float eps, const R* __restrict__ h,
-                   const T* __restrict__ x, const float* __restrict__ w,
-                   const float* __restrict__ w_post, const float* __restrict__ scale,
-                   const T* __restrict__ dy, const R* dh_out, R* dh, T* __restrict__ dx,
-                   float* __restrict__ part) {
+    k_res_norm_bwd(int rows, int C, float inv_C, float eps, const R* h, const T* x, const float* w,
+                   const float* w_post, const float* scale, const T* dy, const R* dh_out, R* dh,
+                   T* dx, float* part) {
   constexpr int S = bwd_stages<T, R>(), KD = pieces<R>(), KG = 2 * pieces<R>(),
                 KX = KG + pieces<T>();
   constexpr bool SPLIT = sizeof(R) == 4;
@@ -538,6 +535,7 @@ __global__ void __launch_bounds__(512, 1)
       smem + threadIdx.y * blockDim.x + threadIdx.x, (int)(blockDim.x * blockDim.y)};
   const Team<SPLIT> t = team_of<SPLIT, CL>(rows, C);
   const bool with_x = w_post || scale;
+  chain();
   let_next_start();
   if (!t.on0 || !t.on1 || !dh_out || !with_x) ring.clear(S);
   auto fetch = [&](int stage, int row) {
@@ -705,14 +703,12 @@ cudaError_t launch_gate(const gdn_gate_norm_shape& s, const void* o, const void*
   const FastDiv byH(s.H);
   const float inv = 1.f / (float)s.d;
   if (!dy) {
-    k_gate_norm_fwd<T, L><<<(n + per - 1) / per, GN_NT, 0, st>>>(
-        n, byH, s.d, inv, s.act, s.ldz, s.eps, (const T*)o, (const T*)z, w, (T*)out);
-  } else {
-    k_gate_norm_bwd<T, L><<<gate_parts(s), GN_NT, 0, st>>>(
-        n, byH, s.d, inv, s.act, s.ldz, s.eps, (const T*)o, (const T*)z, w, (const T*)dy, (T*)out,
-        (T*)dz, part);
+    return launch(k_gate_norm_fwd<T, L>, dim3((n + per - 1) / per), dim3(GN_NT), 0, st, 1, n, byH,
+                  s.d, inv, s.act, (long long)s.ldz, s.eps, (const T*)o, (const T*)z, w, (T*)out);
   }
-  return cudaGetLastError();
+  return launch(k_gate_norm_bwd<T, L>, dim3(gate_parts(s)), dim3(GN_NT), 0, st, 1, n, byH, s.d,
+                inv, s.act, (long long)s.ldz, s.eps, (const T*)o, (const T*)z, w, (const T*)dy,
+                (T*)out, (T*)dz, part);
 }
 template <typename T>
 cudaError_t dispatch_gate(const gdn_gate_norm_shape& s, const void* o, const void* z, const float* w,
@@ -774,18 +770,7 @@ cudaError_t launch_rows(K kernel, const ResPlan& p, int blocks, int smem, cudaSt
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(p.team, p.teams);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = p.cl;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = p.cl > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return launch(kernel, dim3(blocks), dim3(p.team, p.teams), smem, st, p.cl, args...);
 }
 template <typename T, typename R, int CL>
 cudaError_t launch_res(const gdn_res_norm_shape& s, const ResArgs& a, const ResPlan& p,

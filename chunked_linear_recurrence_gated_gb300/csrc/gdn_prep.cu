@@ -39,10 +39,9 @@ template <typename T, int DK>
 __global__ void __launch_bounds__(PR_NT)
     k_prep_fwd(uint32_t nrow, uint32_t ngate, FastDiv by2Hk, FastDiv byH, int G, int row_blocks,
                long long ldq, long long ldk, long long ldg, long long ldb, float q_scale,
-               float eps, const T* __restrict__ q, const T* __restrict__ k,
-               const T* __restrict__ xg, const T* __restrict__ xb, const float* __restrict__ rate,
-               const float* __restrict__ bias, T* __restrict__ qn, T* __restrict__ kn,
-               T* __restrict__ g, T* __restrict__ beta) {
+               float eps, const T* q, const T* k, const T* xg, const T* xb, const float* rate,
+               const float* bias, T* qn, T* kn, T* g, T* beta) {
+  chain();
   const int H = (int)byH.d, Hk = (int)by2Hk.d / 2;
   if ((int)blockIdx.x >= row_blocks) {
     const uint32_t i = (blockIdx.x - row_blocks) * PR_NT + threadIdx.x;
@@ -102,7 +101,6 @@ __device__ __forceinline__ void prep_bwd_gates(int blk, int rows, int H, int hp_
     float sr = 0.f, sb = 0.f;
     if (h < H) {
       const float er = expf(rate[h]), bi = bias[h];
-#pragma unroll 2
       for (int t = t0 + ty; t < t1; t += ny) {
         const size_t at = (size_t)t * H + h;
         const float x = ldf(xg + (size_t)t * ldg + h) + bi, d = ldf(dg + at);
@@ -132,12 +130,10 @@ template <typename T, int DK, bool SHARED>
 __global__ void __launch_bounds__(PR_NT)
     k_prep_bwd(uint32_t nrow, FastDiv by2Hk, int G, int gate_blocks, int rows, int H, int hp_log,
                int per, long long ldq, long long ldk, long long ldg, long long ldb, float q_scale,
-               float eps, const T* __restrict__ q, const T* __restrict__ k,
-               const T* __restrict__ xg, const T* __restrict__ xb, const float* __restrict__ rate,
-               const float* __restrict__ bias, const T* __restrict__ dqn,
-               const T* __restrict__ dkn, const T* __restrict__ dg, const T* __restrict__ dbeta,
-               T* __restrict__ dq, T* __restrict__ dk, T* __restrict__ dxg, T* __restrict__ dxb,
-               float* __restrict__ part) {
+               float eps, const T* q, const T* k, const T* xg, const T* xb, const float* rate,
+               const float* bias, const T* dqn, const T* dkn, const T* dg, const T* dbeta, T* dq,
+               T* dk, T* dxg, T* dxb, float* part) {
+  chain();
   let_next_start();
   if ((int)blockIdx.x < gate_blocks) {
     prep_bwd_gates<T>(blockIdx.x, rows, H, hp_log, per, ldg, ldb, xg, xb, rate, bias, dg, dbeta,
@@ -202,15 +198,13 @@ __global__ void __launch_bounds__(PR_NT)
   }
 }
 
-// Block: 32 columns, 32 partials at a time; then warp j adds up column j. The
-// partials change while this kernel is resident, so `part` is not __restrict__:
-// its loads stay ordinary ones, behind after_previous().
+// Block: 32 columns, 32 partials at a time; then warp j adds up column j.
 __global__ void __launch_bounds__(1024)
     k_col_sum(const float* part, int np, int n, int C, float* o0, float* o1,
               float* o2) {
   __shared__ float red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, i0 = blockIdx.x * 32;
-  after_previous();
+  chain();
   float a = 0.f;
   if (i0 + tx < n) {
 #pragma unroll 4
@@ -243,10 +237,10 @@ void launch_prep_fwd(const gdn_prep_shape& s, const void* q, const void* k, cons
                      void* g, void* beta, cudaStream_t st) {
   const uint32_t nrow = (uint32_t)s.rows * 2 * s.Hk, ngate = (uint32_t)s.rows * s.H;
   const uint32_t per = PR_NT / (DK / 8) * PR_U, rb = (nrow + per - 1) / per;
-  k_prep_fwd<T, DK><<<rb + (ngate + PR_NT - 1) / PR_NT, PR_NT, 0, st>>>(
-      nrow, ngate, FastDiv(2 * s.Hk), FastDiv(s.H), s.H / s.Hk, (int)rb, s.ldq, s.ldk, s.ldg,
-      s.ldb, s.q_scale, s.eps, (const T*)q, (const T*)k, (const T*)xg, (const T*)xb, rate, bias,
-      (T*)qn, (T*)kn, (T*)g, (T*)beta);
+  launch(k_prep_fwd<T, DK>, dim3(rb + (ngate + PR_NT - 1) / PR_NT), dim3(PR_NT), 0, st, 1, nrow,
+         ngate, FastDiv(2 * s.Hk), FastDiv(s.H), s.H / s.Hk, (int)rb, s.ldq, s.ldk, s.ldg, s.ldb,
+         s.q_scale, s.eps, (const T*)q, (const T*)k, (const T*)xg, (const T*)xb, rate, bias, (T*)qn,
+         (T*)kn, (T*)g, (T*)beta);
 }
 
 template <typename T, int DK>
@@ -261,11 +255,10 @@ void launch_prep_bwd(const gdn_prep_shape& s, const void* q, const void* k, cons
   int hp_log = 0;
   while ((1 << hp_log) < s.H && hp_log < 5) ++hp_log;
   const auto kernel = shared ? k_prep_bwd<T, DK, true> : k_prep_bwd<T, DK, false>;
-  kernel<<<np + rb, PR_NT, 0, st>>>(
-      nrow, FastDiv(2 * s.Hk), s.H / s.Hk, np, s.rows, s.H, hp_log, (s.rows + np - 1) / np, s.ldq,
-      s.ldk, s.ldg, s.ldb, s.q_scale, s.eps, (const T*)q, (const T*)k, (const T*)xg, (const T*)xb,
-      rate, bias, (const T*)dqn, (const T*)dkn, (const T*)dg, (const T*)dbeta, (T*)dq, (T*)dk,
-      (T*)dxg, (T*)dxb, part);
+  launch(kernel, dim3(np + rb), dim3(PR_NT), 0, st, 1, nrow, FastDiv(2 * s.Hk), s.H / s.Hk, np,
+         s.rows, s.H, hp_log, (s.rows + np - 1) / np, s.ldq, s.ldk, s.ldg, s.ldb, s.q_scale, s.eps,
+         (const T*)q, (const T*)k, (const T*)xg, (const T*)xb, rate, bias, (const T*)dqn,
+         (const T*)dkn, (const T*)dg, (const T*)dbeta, (T*)dq, (T*)dk, (T*)dxg, (T*)dxb, part);
 }
 
 }  // namespace
@@ -273,16 +266,7 @@ void launch_prep_bwd(const gdn_prep_shape& s, const void* q, const void* k, cons
 cudaError_t col_sum(const float* part, int np, int n, int C, float* o0, float* o1, float* o2,
                     cudaStream_t st) {
   prof_mark(st, "layer_col_sum");
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((n + 31) / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_col_sum, part, np, n, C, o0, o1, o2);
+  return launch(k_col_sum, dim3((n + 31) / 32), dim3(1024), 0, st, 1, part, np, n, C, o0, o1, o2);
 }
 
 }  // namespace gdn

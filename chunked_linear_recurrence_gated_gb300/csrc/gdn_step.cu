@@ -153,10 +153,9 @@ struct StepTile {
 template <typename T, int DK, int DV, int NW>
 __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
     k_step(Cache cache, FastDiv byHP, int G, long long ldq, long long ldk, long long ldv,
-           long long ldg, long long ldb, float q_scale, float eps, const T* __restrict__ q,
-           const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ g,
-           const T* __restrict__ beta, const float* __restrict__ rate,
-           const float* __restrict__ bias, float* S, T* __restrict__ o) {
+           long long ldg, long long ldb, float q_scale, float eps, const T* q, const T* k,
+           const T* v, const T* g, const T* beta, const float* rate, const float* bias, float* S,
+           T* o) {
   using Tile = StepTile<T, DK, NW>;
   constexpr int COLS = Tile::COLS, PARTS = DV / COLS, KS = DK / 8, NT = NW * 32;
   constexpr int LD = Tile::LD;
@@ -165,6 +164,7 @@ __global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
   constexpr int RP = COLS / 4;                 // of a state row
   constexpr int SB = 4;                        // 8-row steps whose loads go ahead of their stores
   constexpr bool TWO = sizeof(T) == 4;         // k and q take two parts
+  chain();
   extern __shared__ __align__(16) unsigned char smem[];
   Tile& sm = *reinterpret_cast<Tile*>(smem);
   uint32_t seq, hp;
@@ -522,11 +522,11 @@ constexpr int conv_stages() {
 // sequences ahead in registers 38.
 template <typename T, int W>
 __global__ void __launch_bounds__(CS_NT, W <= 4 && sizeof(T) == 2 ? 8 : 4)
-    k_conv_step(Cache cache, int C, int act, long long ldx, const T* __restrict__ x,
-                const float* __restrict__ w, const float* __restrict__ b, T* state,
-                T* __restrict__ y) {
+    k_conv_step(Cache cache, int C, int act, long long ldx, const T* x, const float* w,
+                const float* b, T* state, T* y) {
   constexpr int ST = conv_stages<T, W>(), SLOTS = W - 1 + CS_LA;
   __shared__ __align__(16) Raw4<T> ring[ST * SLOTS * CS_NT];
+  chain();
   const int c0 = (blockIdx.x * CS_NT + threadIdx.x) * 4;
   if (c0 >= C) return;
   x += c0, y += c0, state += c0;
@@ -610,16 +610,15 @@ void launch_step_warps(const gdn_step_shape& s, const Cache& c, const void* q, c
                        const float* bias, float* S, void* o, cudaStream_t st) {
   constexpr int smem = sizeof(StepTile<T, DK, NW>), parts = DV / (16 * NW);
   static_assert(smem <= 48 << 10, "what a kernel may use without asking");
-  k_step<T, DK, DV, NW><<<(unsigned)s.N * s.H * parts, NW * 32, smem, st>>>(
-      c, FastDiv(s.H * parts), s.H / s.Hk, s.ldq, s.ldk, s.ldv, s.ldg, s.ldb, s.q_scale, s.eps,
-      (const T*)q, (const T*)k, (const T*)v, (const T*)g, (const T*)beta, rate, bias, S, (T*)o);
+  launch(k_step<T, DK, DV, NW>, dim3((unsigned)s.N * s.H * parts), dim3(NW * 32), smem, st, 1, c,
+         FastDiv(s.H * parts), s.H / s.Hk, s.ldq, s.ldk, s.ldv, s.ldg, s.ldb, s.q_scale, s.eps,
+         (const T*)q, (const T*)k, (const T*)v, (const T*)g, (const T*)beta, rate, bias, S, (T*)o);
 }
 template <typename T, int DK, int DV, typename... A>
 void launch_step(const gdn_step_shape& s, A... a) {
   if ((long long)s.N * s.H * DV < ST_WIDE_COLS)
-    launch_step_warps<T, DK, DV, 2>(s, a...);
-  else
-    launch_step_warps<T, DK, DV, 4>(s, a...);
+    return launch_step_warps<T, DK, DV, 2>(s, a...);
+  return launch_step_warps<T, DK, DV, 4>(s, a...);
 }
 template <typename T, int DK, typename... A>
 void dispatch_step(const gdn_step_shape& s, A... a) {
@@ -635,8 +634,8 @@ void launch_conv_step(const gdn_conv_step_shape& s, const Cache& c, const void* 
                       const float* b, void* state, void* y, cudaStream_t st) {
   // as many sequences per thread as leave the GPU CS_BLOCKS blocks
   const int gx = (s.C / 4 + CS_NT - 1) / CS_NT, gy = std::min(s.N, (CS_BLOCKS + gx - 1) / gx);
-  k_conv_step<T, W><<<dim3(gx, gy), CS_NT, 0, st>>>(c, s.C, s.act, s.ldx, (const T*)x, w, b,
-                                                    (T*)state, (T*)y);
+  launch(k_conv_step<T, W>, dim3(gx, gy), dim3(CS_NT), 0, st, 1, c, s.C, s.act,
+         (long long)s.ldx, (const T*)x, w, b, (T*)state, (T*)y);
 }
 
 template <typename T>
