@@ -12,11 +12,12 @@ namespace gdn {
 namespace {
 
 constexpr int PR_NT = 256;     // threads of a block
-constexpr int PR_U = 4;        // rows a thread has in flight (forward)
-// Rows a thread has in flight (backward): more where a row has one gradient.
-constexpr int prep_bwd_rows(bool shared) { return shared ? 2 : 4; }
+constexpr int PR_U = 3;        // rows a thread has in flight (forward)
+// Rows a thread has in flight (backward): fewer where a row has several gradients.
+// (32768 x 16 heads of 128 bf16: 1 row 132 us, 2 rows 117, 4 rows 125.)
+constexpr int prep_bwd_rows(bool shared) { return shared ? 1 : 2; }
 constexpr int PR_G = 4;        // value heads' gradients loaded together (backward)
-constexpr int PR_PARTS = 304;  // most partial sums of drate / dbias
+constexpr int PR_PARTS = 152;  // most partial sums of drate / dbias
 
 // Row r of the 2 Hk (q heads, then k heads) rows of each token.
 struct HeadRow {
@@ -33,8 +34,11 @@ __device__ __forceinline__ HeadRow head_row(uint32_t r, const FastDiv& by2Hk, in
   return h;
 }
 
-// q / k rows: DK / 8 lanes per row, PR_U rows per thread. Blocks past
-// row_blocks: one thread per (token, value head) of the gates.
+// q / k rows: x r with r = 1 / sqrt(sum x^2 + eps), DK / 8 lanes per row, PR_U
+// rows per thread, all loaded before the first is used. Blocks past row_blocks: one
+// thread per (token, value head) of the gates. Bound by the bytes of q, k, qn and
+// kn: 32768 tokens of 16 heads of 128 bf16 values 83 us (541 MB, 6.5 TB/s; with 1,
+// 2 and 4 rows in flight 98, 90 and 84).
 template <typename T, int DK>
 __global__ void __launch_bounds__(PR_NT)
     k_prep_fwd(uint32_t nrow, uint32_t ngate, FastDiv by2Hk, FastDiv byH, int G, int row_blocks,
@@ -124,8 +128,13 @@ __device__ __forceinline__ void prep_bwd_gates(int blk, int rows, int H, int hp_
   }
 }
 
+// With d the sum of a key head's G gradients and r as in k_prep_fwd,
+//   dx = r (d - r^2 (x . d) x)   (times q_scale for q).
 // The first gate_blocks blocks take the gates (their loops over tokens are the
-// longest), the others rows as k_prep_fwd.
+// longest), the others rows as k_prep_fwd. Bound by the bytes of q, k and the
+// gradients: 32768 tokens of 16 heads of 128 bf16 values 116 us (812 MB, 7.0 TB/s);
+// 8193 of 24 value on 8 key heads, of 128, 30 us (170 MB, 5.6 TB/s: a sixth of it
+// is the column sums and the launches).
 template <typename T, int DK, bool SHARED>
 __global__ void __launch_bounds__(PR_NT)
     k_prep_bwd(uint32_t nrow, FastDiv by2Hk, int G, int gate_blocks, int rows, int H, int hp_log,
