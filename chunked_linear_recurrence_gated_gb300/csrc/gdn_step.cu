@@ -40,11 +40,13 @@ __device__ __forceinline__ SeqCall seq_call(const Cache& c, int s) {
   return r;
 }
 
-constexpr int ST_TILE = 8;    // tokens evaluated together: the N extent of the MMAs
+// Blocks of 4 warps take 64 columns; calls that would not fill the GPU with
+// those (6 of them fit an SM) take blocks of 2, for twice as many SMs: one
+// sequence of 16 heads, 128 x 128, 8 tokens: 4.5 us in blocks of 2 warps, 4.9 in
+// blocks of 4; 256 sequences of 32 heads: 190 against 188 us.
+constexpr int ST_TILE = 8;  // tokens evaluated together: the N extent of the MMAs
 constexpr int ST_WARPS = 24;  // warps of an SM: what its shared memory holds states for
-// Warps of a block: 32 columns, a whole line of a state row. (Blocks of 4 were
-// never faster: 45 sequences of 16 x 128 x 256, up to 8 tokens, 32.2 us against 31.7.)
-constexpr int ST_NW = 2;
+constexpr int ST_WIDE_COLS = 152 * (ST_WARPS / 4) * 64;  // columns of a call for blocks of 64
 
 // Two consecutive elements.
 __device__ __forceinline__ void ld2(const float* p, float* v) {
@@ -110,7 +112,7 @@ __device__ __forceinline__ void mma_tf32z(float* c, const uint32_t* a, uint32_t 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// One block: 32 value columns of one head of one sequence, 16 per warp; the
+// One block: 16 NW value columns of one head of one sequence, 16 per warp; the
 // state's columns stay in shared memory. ST_TILE tokens at a time, with S the
 // state before them, Gamma_t = alpha_0 .. alpha_t and D_tj = alpha_{j+1} .. alpha_t
 // (running products, no quotients of decays):
@@ -132,16 +134,15 @@ __device__ __forceinline__ void mma_tf32z(float* c, const uint32_t* a, uint32_t 
 // multiply-adds in the same layout: the MMAs would use an eighth of their N.
 // Lane (g, t) = (lane / 4, lane % 4): columns 2g, 2g + 1, tokens 2t, 2t + 1.
 //
-// Bound by the state's bytes; with drafted tokens also by the phases of a block
-// (load, compute, store), which the few waves of a call pass together. What decided
-// (256 x 32 heads of 128 x 128, 8 tokens): 24 warps per SM (states in registers left
-// room for 12 to 16, and the phases did not overlap: 330 us token by token, 234 in
+// Bound by the state's bytes. What decided: 24 warps per SM (states in registers
+// left room for 12 to 16, and the phases of load, compute and store did not
+// overlap: 8 tokens, 256 x 32 heads of 128 x 128, 330 us token by token, 234 in
 // tiles; in shared memory 186), the swizzle (24 warps instead of 20, 208 us), and
-// loads of whole lines (see below). One token: 153 us (1.03 GB, 6.8 TB/s). 45
-// sequences of 16 heads of 128 x 256 with up to 8 tokens: 31.7 us (142 MB, 4.5 TB/s).
-template <typename T, int DK>
+// loads of whole lines (see below). 256 sequences x 32 heads of 128 x 128: one
+// token 159 us (2.1 GB, 6.8 TB/s), 8 tokens 188 us.
+template <typename T, int DK, int NW>
 struct StepTile {
-  static constexpr int COLS = 16 * ST_NW;
+  static constexpr int COLS = 16 * NW;
   static constexpr int LD = DK + 8;  // the rows of a fragment start in different banks
   // the block's columns of the state; column c of row r is at c ^ (8 (r / 2 mod 4)),
   // which puts the rows of a fragment into different banks too
@@ -149,14 +150,14 @@ struct StepTile {
   T k[ST_TILE * LD], q[ST_TILE * LD];
 };
 
-template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(ST_NW * 32, ST_WARPS / ST_NW)
+template <typename T, int DK, int DV, int NW>
+__global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
     k_step(Cache cache, FastDiv byHP, int G, long long ldq, long long ldk, long long ldv,
            long long ldg, long long ldb, float q_scale, float eps, const T* q, const T* k,
            const T* v, const T* g, const T* beta, const float* rate, const float* bias, float* S,
            T* o) {
-  using Tile = StepTile<T, DK>;
-  constexpr int COLS = Tile::COLS, PARTS = DV / COLS, KS = DK / 8, NT = ST_NW * 32;
+  using Tile = StepTile<T, DK, NW>;
+  constexpr int COLS = Tile::COLS, PARTS = DV / COLS, KS = DK / 8, NT = NW * 32;
   constexpr int LD = Tile::LD;
   constexpr int EP = 16 / (int)sizeof(T);      // elements of 16 bytes
   constexpr int KP = DK / EP;                  // 16-byte pieces of a row
@@ -517,7 +518,7 @@ constexpr int conv_stages() {
 // and of x and y, behind the latency of the index entries and then of the inputs:
 // the cached rows and the first CS_LA new ones of the next sequences are in
 // flight into shared-memory slots that only this thread reads. 1024 sequences of
-// 6144 bf16 channels, one token: 24.6 us (97 MB, 4.0 TB/s); with plain loads 29, two
+// 6144 bf16 channels, one token: 25 us (97 MB, 3.8 TB/s); with plain loads 29, two
 // sequences ahead in registers 38.
 template <typename T, int W>
 __global__ void __launch_bounds__(CS_NT, W <= 4 && sizeof(T) == 2 ? 8 : 4)
@@ -603,15 +604,21 @@ gdn_status check_cache(int N, int n_tok, int n_slots, const int* slot_in, const 
   return GDN_OK;
 }
 
-template <typename T, int DK, int DV>
-void launch_step(const gdn_step_shape& s, const Cache& c, const void* q, const void* k,
-                 const void* v, const void* g, const void* beta, const float* rate,
-                 const float* bias, float* S, void* o, cudaStream_t st) {
-  constexpr int smem = sizeof(StepTile<T, DK>), parts = DV / StepTile<T, DK>::COLS;
+template <typename T, int DK, int DV, int NW>
+void launch_step_warps(const gdn_step_shape& s, const Cache& c, const void* q, const void* k,
+                       const void* v, const void* g, const void* beta, const float* rate,
+                       const float* bias, float* S, void* o, cudaStream_t st) {
+  constexpr int smem = sizeof(StepTile<T, DK, NW>), parts = DV / (16 * NW);
   static_assert(smem <= 48 << 10, "what a kernel may use without asking");
-  launch(k_step<T, DK, DV>, dim3((unsigned)s.N * s.H * parts), dim3(ST_NW * 32), smem, st, 1, c,
+  launch(k_step<T, DK, DV, NW>, dim3((unsigned)s.N * s.H * parts), dim3(NW * 32), smem, st, 1, c,
          FastDiv(s.H * parts), s.H / s.Hk, s.ldq, s.ldk, s.ldv, s.ldg, s.ldb, s.q_scale, s.eps,
          (const T*)q, (const T*)k, (const T*)v, (const T*)g, (const T*)beta, rate, bias, S, (T*)o);
+}
+template <typename T, int DK, int DV, typename... A>
+void launch_step(const gdn_step_shape& s, A... a) {
+  if ((long long)s.N * s.H * DV < ST_WIDE_COLS)
+    return launch_step_warps<T, DK, DV, 2>(s, a...);
+  return launch_step_warps<T, DK, DV, 4>(s, a...);
 }
 template <typename T, int DK, typename... A>
 void dispatch_step(const gdn_step_shape& s, A... a) {
