@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(GN_NT)
 // columns, part[block] = the block's sum. The elementwise arithmetic is in pairs:
 // the instructions of an element (sigmoid and its derivative among them) come
 // close to the memory's time. Bound by the bytes of o, z, dy, do and dz: 16411 x 16
-// rows of 256 bf16 values 106 us (672 MB, 6.3 TB/s; 110 with unpaired arithmetic,
+// rows of 256 bf16 values 105 us (672 MB, 6.4 TB/s; 110 with unpaired arithmetic,
 // 126 with the next rows in flight through shared memory).
 template <typename T, int L>
 __global__ void __launch_bounds__(GN_NT, gate_blocks<T>())
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(GN_NT, gate_blocks<T>())
 // without a barrier of their own.
 constexpr int RN_COLS_F = 8192;  // columns of a CTA, forward: 1024 threads of 64 registers
 constexpr int RN_COLS_B = 4096;  // backward: 512 threads of 128 registers
-constexpr int RN_SLOT = 128;     // floats of a reduction: 8 values of 16 warps, or 1 of 32
+constexpr int RN_SLOT = 128;     // floats of a reduction: 8 values of 16 warps, or 2 of 32
 constexpr int RN_BUFS = 3;       // reductions that may be open at the same time, plus one
 constexpr int RN_SMS = 152;
 
@@ -302,7 +302,7 @@ __device__ __forceinline__ float warp_sum8(const float* v) {
   return c + __shfl_xor_sync(0xffffffffu, c, 1);
 }
 
-// Sums over a team of 1 (ONE) or 6 values, in two halves: post() gives this
+// Sums over a team of K values (1, 2 or 6), in two halves: post() gives this
 // thread's part, collect() returns the sums of the oldest post not yet collected.
 // At most one other post may lie between the two, which is what the three
 // buffers are for: a post's barrier separates it from the reads three posts back.
@@ -310,9 +310,9 @@ __device__ __forceinline__ float warp_sum8(const float* v) {
 // CTA's shared memory with st.async, which completes the receiver's mbarrier. (A
 // cluster barrier instead would have to order the row's global stores too: its
 // release waits for them, 6 us per row of 16384 columns against DRAM's 2.)
-template <bool ONE, int CL>
+template <int K, int CL>
 struct TeamSum {
-  static constexpr int K = ONE ? 1 : 6, N4 = ONE ? 1 : 2;  // values; float4 per CTA's sums
+  static constexpr int N4 = K > 4 ? 2 : 1;  // float4 per CTA's sums
   float* warps;    // [RN_BUFS][RN_SLOT] the warps' sums (unused ones stay 0)
   float4* ctas;    // [RN_BUFS][CL][N4] the CTAs' sums
   uint64_t* bars;  // [RN_BUFS] completed by CL sends
@@ -354,13 +354,17 @@ struct TeamSum {
   // The CTA's sums from the warps'.
   __device__ __forceinline__ void read_warps(int buf, float* v) const {
     const float4* slot = reinterpret_cast<const float4*>(warps + buf * RN_SLOT);
-    if (ONE) {
-      v[0] = 0.f;
+    if (K <= 2) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[i] = 0.f;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         if (u * 128 >= (int)blockDim.x) break;
-        const float4 a = slot[u];
-        v[0] += (a.x + a.y) + (a.z + a.w);
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          const float4 a = slot[8 * i + u];
+          v[i] += (a.x + a.y) + (a.z + a.w);
+        }
       }
     } else {  // lane l: value l / 4, warps 4 (l % 4) ..
       const float4 a = slot[threadIdx.x & 31];
@@ -374,9 +378,12 @@ struct TeamSum {
   __device__ __forceinline__ void post(float* v) {
     const int lane = threadIdx.x & 31;
     float* slot = warps + in * RN_SLOT;
-    if (ONE) {
-      const float s = lane_sum<32>(v[0]);
-      if (lane == 0) slot[threadIdx.x >> 5] = s;
+    if (K <= 2) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const float s = lane_sum<32>(v[i]);
+        if (lane == 0) slot[32 * i + (threadIdx.x >> 5)] = s;
+      }
     } else {  // [8 values][16 warps]
       v[6] = v[7] = 0.f;
       const float s = warp_sum8(v);
@@ -443,8 +450,12 @@ struct TeamSum {
   }
 };
 
+// With rx = 1 / sqrt(mean x^2 + eps) (1 without w_post) and r the same of h':
+//   h' = h + scale w_post rx x,   y = r w h'.
+// In a cluster the sum of the next row's x^2 goes with the row's own sum of h'^2,
+// one exchange a row instead of two (5000 rows of 16384 bf16 columns 165 -> 115 us).
 // Bound by the bytes of h, x, h_out and y: 20011 rows of 4096 columns, fp32 stream
-// and bf16 branch, both norms: 157 us (984 MB, 6.3 TB/s); one row per block with
+// and bf16 branch, both norms: 151 us (984 MB, 6.5 TB/s); one row per block with
 // plain loads took 305.
 template <typename T, typename R, int CL, int S>
 __global__ void __launch_bounds__(1024, 1)
@@ -467,29 +478,43 @@ __global__ void __launch_bounds__(1024, 1)
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
-  TeamSum<true, CL> sum;
+  TeamSum<CL == 1 ? 1 : 2, CL> sum;
   sum.init();
   f32x2 wv[4], pv[4], sv[4];
   ld_cols(w, t, 0.f, wv);
   ld_cols(w_post, t, 1.f, pv);
   ld_cols(scale, t, 1.f, sv);
+  float s[2] = {};  // sums over a row of h_out^2 and of the branch's x^2
+  auto square = [&](int stage) {
+    f32x2 xv[4], a = 0;
+    ring.template read<T>(stage, KX, xv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a = fma2(xv[i], xv[i], a);
+    return sum2(a);
+  };
   int stage = 0;
-  for (int row = t.first; row < t.rows; row += t.step) {
+  if (CL > 1 && w_post && t.first < t.rows) {
     cp_wait<S - 1>();
+    s[1] = square(0);
+    sum.post(s);
+    sum.collect(s);
+  }
+  for (int row = t.first; row < t.rows; row += t.step) {
+    const int next = stage + 1 == S ? 0 : stage + 1;
+    cp_wait<CL == 1 ? S - 1 : S - 2>();
     f32x2 hv[4], xv[4], a = 0;
-    float s;
     ring.template read<R>(stage, 0, hv);
     ring.template read<T>(stage, KX, xv);
     if (w_post) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a = fma2(xv[i], xv[i], a);
-      s = sum2(a);
-      sum.post(&s);
-      sum.collect(&s);
-      const f32x2 rx = both2(rsqrtf(fmaf(s, inv_C, eps)));
+      float x2 = s[1];
+      if (CL == 1) {
+        x2 = square(stage);
+        sum.post(&x2);
+        sum.collect(&x2);
+      }
+      const f32x2 rx = both2(rsqrtf(fmaf(x2, inv_C, eps)));
 #pragma unroll
       for (int i = 0; i < 4; ++i) xv[i] = mul2(xv[i], mul2(rx, pv[i]));
-      a = 0;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -498,11 +523,12 @@ __global__ void __launch_bounds__(1024, 1)
     }
     if (h_out) st_cols(h_out + (size_t)row * C, t, hv);
     fetch(stage, row + S * t.step);  // the slot has been read
-    if (++stage == S) stage = 0;
-    s = sum2(a);
-    sum.post(&s);
-    sum.collect(&s);
-    const f32x2 r = both2(rsqrtf(fmaf(s, inv_C, eps)));
+    stage = next;
+    s[0] = sum2(a);
+    if (CL > 1 && w_post) s[1] = row + t.step < t.rows ? square(next) : 0.f;
+    sum.post(s);
+    sum.collect(s);
+    const f32x2 r = both2(rsqrtf(fmaf(s[0], inv_C, eps)));
 #pragma unroll
     for (int i = 0; i < 4; ++i) hv[i] = mul2(hv[i], mul2(r, wv[i]));
     st_cols(y + (size_t)row * C, t, hv);
@@ -518,10 +544,11 @@ __global__ void __launch_bounds__(1024, 1)
 // and mean(sp dh m) is a combination of sums that do not need dh, so a row takes
 // one reduction, of 6 sums. In a cluster the next row's sums are formed and posted
 // before this row's are collected, so that the exchange's latency passes behind a
-// row's work (4000 rows of 16384 bf16 columns 369 -> 320 us); within a CTA reading
-// the row twice for that costs more than it hides (32768 rows of 2048: 135 us
-// against 127). Bound by the bytes of h, dh_out, dy, x, dh and dx: 32768 rows of
-// 2048 bf16 columns, both norms, 127 us (805 MB, 6.4 TB/s).
+// row's work (4000 rows of 16384 bf16 columns 369 -> 320 us, 177 since with as many
+// clusters as fit); within a CTA reading the row twice for that costs more than it
+// hides (32768 rows of 2048: 135 us against 127). Bound by the bytes of h, dh_out,
+// dy, x, dh and dx: 32768 rows of 2048 bf16 columns, both norms, 123 us (805 MB,
+// 6.5 TB/s).
 template <typename T, typename R, int CL>
 __global__ void __launch_bounds__(512, 1)
     k_res_norm_bwd(int rows, int C, float inv_C, float eps, const R* h, const T* x, const float* w,
@@ -550,7 +577,7 @@ __global__ void __launch_bounds__(512, 1)
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
-  TeamSum<false, CL> sum;
+  TeamSum<6, CL> sum;
   sum.init();
   f32x2 wv[4], sp[4], aw[4] = {}, am[4] = {};
   ld_cols(w, t, 0.f, wv);
@@ -711,8 +738,9 @@ cudaError_t launch_gate(const gdn_gate_norm_shape& s, const void* o, const void*
                 (T*)out, (T*)dz, part);
 }
 template <typename T>
-cudaError_t dispatch_gate(const gdn_gate_norm_shape& s, const void* o, const void* z, const float* w,
-                   const void* dy, void* out, void* dz, float* part, cudaStream_t st) {
+cudaError_t dispatch_gate(const gdn_gate_norm_shape& s, const void* o, const void* z,
+                          const float* w, const void* dy, void* out, void* dz, float* part,
+                          cudaStream_t st) {
   switch (lanes_of(s.d)) {
     case 1: return launch_gate<T, 1>(s, o, z, w, dy, out, dz, part, st);
     case 2: return launch_gate<T, 2>(s, o, z, w, dy, out, dz, part, st);
