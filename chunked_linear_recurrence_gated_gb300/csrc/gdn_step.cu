@@ -40,13 +40,14 @@ __device__ __forceinline__ SeqCall seq_call(const Cache& c, int s) {
   return r;
 }
 
-// Blocks of 4 warps take 64 columns; calls that would not fill the GPU with
-// those (6 of them fit an SM) take blocks of 2, for twice as many SMs: one
-// sequence of 16 heads, 128 x 128, 8 tokens: 4.5 us in blocks of 2 warps, 4.9 in
-// blocks of 4; 256 sequences of 32 heads: 190 against 188 us.
-constexpr int ST_TILE = 8;  // tokens evaluated together: the N extent of the MMAs
+constexpr int ST_TILE = 8;    // tokens evaluated together: the N extent of the MMAs
 constexpr int ST_WARPS = 24;  // warps of an SM: what its shared memory holds states for
-constexpr int ST_WIDE_COLS = 152 * (ST_WARPS / 4) * 64;  // columns of a call for blocks of 64
+// Blocks of 2 warps take 32 columns of a state, a whole line of its rows. Calls of
+// more than 8 waves take blocks of 4, which fetch k and q half as often, where the
+// coarser last wave costs less than that: 128 sequences of 32 heads of 128 x 128,
+// fp32, up to 16 tokens, 149 us in blocks of 4, 169 of 2; 45 of 16 heads of
+// 128 x 256, bf16, up to 8 tokens, 32.2 against 31.7.
+constexpr int ST_WIDE_COLS = 8 * 152 * ST_WARPS * 16;  // columns of a call for blocks of 4
 
 // Two consecutive elements.
 __device__ __forceinline__ void ld2(const float* p, float* v) {
@@ -134,12 +135,13 @@ __device__ __forceinline__ void mma_tf32z(float* c, const uint32_t* a, uint32_t 
 // multiply-adds in the same layout: the MMAs would use an eighth of their N.
 // Lane (g, t) = (lane / 4, lane % 4): columns 2g, 2g + 1, tokens 2t, 2t + 1.
 //
-// Bound by the state's bytes. What decided: 24 warps per SM (states in registers
-// left room for 12 to 16, and the phases of load, compute and store did not
-// overlap: 8 tokens, 256 x 32 heads of 128 x 128, 330 us token by token, 234 in
+// Bound by the state's bytes; with drafted tokens also by the phases of a block
+// (load, compute, store), which the few waves of a call pass together. What decided
+// (256 x 32 heads of 128 x 128, 8 tokens): 24 warps per SM (states in registers left
+// room for 12 to 16, and the phases did not overlap: 330 us token by token, 234 in
 // tiles; in shared memory 186), the swizzle (24 warps instead of 20, 208 us), and
-// loads of whole lines (see below). 256 sequences x 32 heads of 128 x 128: one
-// token 159 us (2.1 GB, 6.8 TB/s), 8 tokens 188 us.
+// loads of whole lines (see below). One token: 153 us (1.03 GB, 6.8 TB/s). 45
+// sequences of 16 heads of 128 x 256 with up to 8 tokens: 31.7 us (142 MB, 4.5 TB/s).
 template <typename T, int DK, int NW>
 struct StepTile {
   static constexpr int COLS = 16 * NW;
@@ -518,7 +520,7 @@ constexpr int conv_stages() {
 // and of x and y, behind the latency of the index entries and then of the inputs:
 // the cached rows and the first CS_LA new ones of the next sequences are in
 // flight into shared-memory slots that only this thread reads. 1024 sequences of
-// 6144 bf16 channels, one token: 25 us (97 MB, 3.8 TB/s); with plain loads 29, two
+// 6144 bf16 channels, one token: 24.6 us (97 MB, 4.0 TB/s); with plain loads 29, two
 // sequences ahead in registers 38.
 template <typename T, int W>
 __global__ void __launch_bounds__(CS_NT, W <= 4 && sizeof(T) == 2 ? 8 : 4)
