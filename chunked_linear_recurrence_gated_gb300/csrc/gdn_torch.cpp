@@ -3,7 +3,7 @@
 // the current stream of the tensors' device. Host code only. A generation step
 // makes these calls once per layer and token, and on the Grace host a dozen
 // tensors' attributes read from Python cost several times the launch: one step
-// of one sequence takes 15 us of host time that way and 6 us this way.
+// of one sequence takes 15.5 us of host time that way and 4.6 us this way.
 #include <Python.h>
 
 #include <initializer_list>

@@ -1,9 +1,10 @@
-"""Thin ctypes binding of libgdn.so (argument marshalling only).
+"""Thin binding of libgdn.so (argument marshalling only): ctypes for the chunk
+and convolution calls, the compiled module _gdn_torch for the layer operators.
 
 Every step of the computation runs in the library's CUDA kernels; this module
 only turns torch tensors into pointers, allocates outputs and the workspace on
 the caller's behalf (torch owns that memory), and raises on a non-OK status.
-The library must have been built (``build.py``); there is no fallback.
+Both must have been built (``build.py``); there is no fallback.
 
 The function names follow the C ABI in include/gdn.h, gdn_conv.h and gdn_layer.h.
 """

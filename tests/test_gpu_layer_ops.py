@@ -454,3 +454,40 @@ def test_captured_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, want) and torch.equal(S, S1)
+
+
+@pytest.mark.parametrize("N", [1, 200])
+def test_dependent_calls_back_to_back(N):
+    """A call may be launched before its predecessor has ended: calls that read, and
+    write over, what the one before has just written or read give the same bits as
+    with a synchronisation after each."""
+    def run(wait):
+        r = gen(11)
+        wait = torch.cuda.synchronize if wait else (lambda: None)
+        cw, cb, conv = r(512, 4), r(512), r(N, 3, 512)
+        S, gates, gate = r(N, 4, 64, 64), (r(N, 4), r(N, 4)), (r(4), r(4))
+        wn, w, wp = r(64), r(256), r(256)
+        x, z, h = r(N, 512), r(1, N, 4, 64), r(N, 256)
+        dy, kept = r(1, N, 4, 64), []
+        for _ in range(20):
+            y = gdn.gdn_conv_step(x, cw, cb, conv)
+            wait()
+            q, k, v = (u.unflatten(-1, (-1, 64)) for u in y.split((128, 128, 256), -1))
+            o = gdn.gdn_step(q, k, v, *gates, S, gate=gate)
+            wait()
+            z = gdn.gdn_gate_norm_fwd(o[None], z, wn)
+            wait()
+            h, z = gdn.gdn_res_norm_fwd(h, z.view(N, 256), w, w_post=wp)
+            wait()
+            z = z.view(1, N, 4, 64)
+            do, dz, dw = gdn.gdn_gate_norm_bwd(o[None], z, wn, dy)
+            wait()
+            dx = gdn.gdn_res_norm_bwd(h, do.view(N, 256), w, dz.view(N, 256), w_post=wp)
+            wait()
+            dy = dx[0].view(1, N, 4, 64)
+            kept += [o, z, dw, dx[2]]
+        torch.cuda.synchronize()
+        return kept + [S, conv, h, dy]
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
