@@ -167,7 +167,6 @@ __global__ void __launch_bounds__(GN_NT, gate_blocks<T>())
 constexpr int RN_COLS_F = 8192;  // columns of a CTA, forward: 1024 threads of 64 registers
 constexpr int RN_COLS_B = 4096;  // backward: 512 threads of 128 registers
 constexpr int RN_SLOT = 128;     // floats of a reduction: 8 values of 16 warps, or 2 of 32
-constexpr int RN_BUFS = 3;       // reductions that may be open at the same time, plus one
 constexpr int RN_SMS = 152;
 
 // The rows of a team and the columns of a thread. With an fp32 stream a
@@ -303,37 +302,40 @@ __device__ __forceinline__ float warp_sum8(const float* v) {
 }
 
 // Sums over a team of K values (1, 2 or 6), in two halves: post() gives this
-// thread's part, collect() returns the sums of the oldest post not yet collected.
-// At most one other post may lie between the two, which is what the three
-// buffers are for: a post's barrier separates it from the reads three posts back.
+// thread's part, collect() returns the sums of the oldest post not yet collected;
+// AHEAD other posts lie between the two. A CTA of a cluster posts p after it has
+// collected p - AHEAD - 1, so every other CTA has posted that, so it has collected
+// p - 2 AHEAD - 2: what lies in the buffer of post p - BUFS has been read.
 // For rows split over a cluster post() also sends the CTA's sums into every
 // CTA's shared memory with st.async, which completes the receiver's mbarrier. (A
 // cluster barrier instead would have to order the row's global stores too: its
 // release waits for them, 6 us per row of 16384 columns against DRAM's 2.)
-template <int K, int CL>
+template <int K, int CL, int AHEAD>
 struct TeamSum {
   static constexpr int N4 = K > 4 ? 2 : 1;  // float4 per CTA's sums
-  float* warps;    // [RN_BUFS][RN_SLOT] the warps' sums (unused ones stay 0)
-  float4* ctas;    // [RN_BUFS][CL][N4] the CTAs' sums
-  uint64_t* bars;  // [RN_BUFS] completed by CL sends
+  static constexpr int BUFS = 2 * AHEAD + 2;
+  float* warps;    // [BUFS][RN_SLOT] the warps' sums (unused ones stay 0)
+  float4* ctas;    // [BUFS][CL][N4] the CTAs' sums
+  uint64_t* bars;  // [BUFS] completed by CL sends
   int in, out;     // buffers of the next post and the next collect
   uint32_t phase;  // parity of the mbarrier of `out`
   bool dead;       // a wait gave up: every later sum is NaN, so the failure shows
 
   __device__ __forceinline__ void init() {
-    __shared__ __align__(16) float warp_sums[8 * RN_BUFS * RN_SLOT];  // at most 8 teams
-    __shared__ float4 cta_sums[RN_BUFS * CL * N4];
-    __shared__ uint64_t mbars[RN_BUFS];
-    warps = warp_sums + threadIdx.y * RN_BUFS * RN_SLOT;
+    constexpr int TEAMS = CL > 1 ? 1 : 8;  // at most
+    __shared__ __align__(16) float warp_sums[TEAMS * BUFS * RN_SLOT];
+    __shared__ float4 cta_sums[BUFS * CL * N4];
+    __shared__ uint64_t mbars[BUFS];
+    warps = warp_sums + threadIdx.y * BUFS * RN_SLOT;
     ctas = cta_sums;
     bars = mbars;
     in = out = 0;
     phase = 0;
     dead = false;
-    for (int i = threadIdx.x; i < RN_BUFS * RN_SLOT; i += blockDim.x) warps[i] = 0.f;
+    for (int i = threadIdx.x; i < BUFS * RN_SLOT; i += blockDim.x) warps[i] = 0.f;
     if (CL > 1) {
       if (threadIdx.x == 0) {
-        for (int i = 0; i < RN_BUFS; ++i) mbar_init(mbars + i, 1);
+        for (int i = 0; i < BUFS; ++i) mbar_init(mbars + i, 1);
         fence_mbar_init();
       }
       __syncthreads();
@@ -415,7 +417,7 @@ struct TeamSum {
               : "memory");
       }
     }
-    if (++in == RN_BUFS) in = 0;
+    if (++in == BUFS) in = 0;
   }
   __device__ __forceinline__ void collect(float* v) {
     if (CL == 1) {
@@ -443,7 +445,7 @@ struct TeamSum {
 #pragma unroll
       for (int i = 0; i < K; ++i) v[i] = dead ? __int_as_float(0x7fc00000) : s[i];
     }
-    if (++out == RN_BUFS) {
+    if (++out == BUFS) {
       out = 0;
       phase ^= 1;
     }
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(1024, 1)
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
-  TeamSum<CL == 1 ? 1 : 2, CL> sum;
+  TeamSum<CL == 1 ? 1 : 2, CL, 0> sum;
   sum.init();
   f32x2 wv[4], pv[4], sv[4];
   ld_cols(w, t, 0.f, wv);
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(512, 1)
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
-  TeamSum<6, CL> sum;
+  TeamSum<6, CL, CL == 1 ? 0 : 1> sum;
   sum.init();
   f32x2 wv[4], sp[4], aw[4] = {}, am[4] = {};
   ld_cols(w, t, 0.f, wv);
