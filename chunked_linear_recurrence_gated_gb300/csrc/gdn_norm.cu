@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(GN_NT, gate_blocks<T>())
 constexpr int RN_COLS_F = 8192;  // columns of a CTA, forward: 1024 threads of 64 registers
 constexpr int RN_COLS_B = 4096;  // backward: 512 threads of 128 registers
 constexpr int RN_SLOT = 128;     // floats of a reduction: 8 values of 16 warps, or 2 of 32
+constexpr int RN_STAGES_B = 3;   // rows a team holds, backward (4 to 6: no faster)
 constexpr int RN_SMS = 152;
 
 // The rows of a team and the columns of a thread. With an fp32 stream a
@@ -277,9 +278,6 @@ template <typename T, typename R>
 constexpr int fwd_slots() { return pieces<R>() + pieces<T>(); }
 template <typename T, typename R>
 constexpr int bwd_slots() { return 2 * pieces<R>() + 2 * pieces<T>(); }
-template <typename T, typename R>
-constexpr int bwd_stages() { return bwd_slots<T, R>() == 4 ? 4 : 3; }
-
 // Sum over the warp of each of 8 values in 9 shuffles: each exchange halves the
 // values that a lane still carries. Lane l returns value l / 4.
 __device__ __forceinline__ float warp_sum8(const float* v) {
@@ -547,17 +545,19 @@ __global__ void __launch_bounds__(1024, 1)
 // one reduction, of 6 sums. In a cluster the next row's sums are formed and posted
 // before this row's are collected, so that the exchange's latency passes behind a
 // row's work (4000 rows of 16384 bf16 columns 369 -> 320 us, 177 since with as many
-// clusters as fit); within a CTA reading the row twice for that costs more than it
-// hides (32768 rows of 2048: 135 us against 127). Bound by the bytes of h, dh_out,
-// dy, x, dh and dx: 32768 rows of 2048 bf16 columns, both norms, 123 us (805 MB,
-// 6.5 TB/s).
+// clusters as fit, and 191 two rows ahead); within a CTA reading the row twice for
+// that costs more than it hides (32768 rows of 2048: 135 us against 127). Bound by
+// the bytes of h, dh_out, dy, x, dh and dx: 32768 rows of 2048 bf16 columns, both
+// norms, 123 us (805 MB, 6.5 TB/s); bf16 rows of 16384 columns by the instructions of
+// the 16 warps that the registers leave an SM (as many fp32 values: 94 % of the
+// bytes' time).
 template <typename T, typename R, int CL>
 __global__ void __launch_bounds__(512, 1)
     k_res_norm_bwd(int rows, int C, float inv_C, float eps, const R* h, const T* x, const float* w,
                    const float* w_post, const float* scale, const T* dy, const R* dh_out, R* dh,
                    T* dx, float* part) {
-  constexpr int S = bwd_stages<T, R>(), KD = pieces<R>(), KG = 2 * pieces<R>(),
-                KX = KG + pieces<T>();
+  constexpr int S = RN_STAGES_B, AHEAD = CL == 1 ? 0 : 1;
+  constexpr int KD = pieces<R>(), KG = 2 * pieces<R>(), KX = KG + pieces<T>();
   constexpr bool SPLIT = sizeof(R) == 4;
   extern __shared__ uint4 smem[];
   const Ring<bwd_slots<T, R>(), SPLIT> ring = {
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(512, 1)
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) fetch(s, t.first + s * t.step);
-  TeamSum<6, CL, CL == 1 ? 0 : 1> sum;
+  TeamSum<6, CL, AHEAD> sum;
   sum.init();
   f32x2 wv[4], sp[4], aw[4] = {}, am[4] = {};
   ld_cols(w, t, 0.f, wv);
@@ -619,32 +619,27 @@ __global__ void __launch_bounds__(512, 1)
     for (int i = 0; i < 6; ++i) s[i] = sum2(a[i]);
     sum.post(s);
   };
-  int stage = 0;
-  if (CL > 1 && t.first < t.rows) {
+  if (AHEAD > 0 && t.first < t.rows) {
     Row v;
     cp_wait<S - 1>();
     read(0, v);
     post(v);
   }
+  int stage = 0;
   for (int row = t.first; row < t.rows; row += t.step) {
-    const int next = stage + 1 == S ? 0 : stage + 1;
     Row v;
-    if (CL == 1) {
-      cp_wait<S - 1>();
-      read(stage, v);
-      post(v);
-    } else if (row + t.step < t.rows) {
-      cp_wait<S - 2>();
-      read(next, v);
+    if (row + AHEAD * t.step < t.rows) {
+      cp_wait<S - 1 - AHEAD>();
+      read(stage + AHEAD < S ? stage + AHEAD : stage + AHEAD - S, v);
       post(v);
     }
     float s[8];
     sum.collect(s);
-    if (CL > 1) read(stage, v);
+    if (AHEAD > 0) read(stage, v);
     f32x2 *hv = v.h, *gv = v.g, *xv = v.x, *dv = v.d;
     const size_t at = (size_t)row * C;
     fetch(stage, row + S * t.step);  // the slot has been read
-    stage = next;
+    if (++stage == S) stage = 0;
     const float r = rsqrtf(fmaf(s[0], inv_C, eps));
     const float rx = w_post ? rsqrtf(fmaf(s[2], inv_C, eps)) : 1.f;
     const float hc = -r * r * r * s[1] * inv_C;  // factor of h in dh
@@ -825,9 +820,9 @@ cudaError_t launch_res(const gdn_res_norm_shape& s, const ResArgs& a, const ResP
     return go(std::integral_constant<int, usual>());
   }
   return launch_rows(k_res_norm_bwd<T, R, CL>, p, p.blocks(s.rows, 512),
-                     nt * 16 * bwd_slots<T, R>() * bwd_stages<T, R>(), st, s.rows, s.C, inv,
-                     s.eps, (const R*)a.h, (const T*)a.x, a.w, a.w_post, a.scale,
-                     (const T*)a.dy, (const R*)a.dh_out, (R*)a.ho, (T*)a.y, a.part);
+                     nt * 16 * bwd_slots<T, R>() * RN_STAGES_B, st, s.rows, s.C, inv, s.eps,
+                     (const R*)a.h, (const T*)a.x, a.w, a.w_post, a.scale, (const T*)a.dy,
+                     (const R*)a.dh_out, (R*)a.ho, (T*)a.y, a.part);
 }
 template <typename T, typename R>
 cudaError_t dispatch_res(const gdn_res_norm_shape& s, const ResArgs& a, cudaStream_t st) {
