@@ -311,7 +311,9 @@ __device__ __forceinline__ float warp_sum8(const float* v) {
 template <int K, int CL, int AHEAD>
 struct TeamSum {
   static constexpr int N4 = K > 4 ? 2 : 1;  // float4 per CTA's sums
-  static constexpr int BUFS = 2 * AHEAD + 2;
+  // 2 AHEAD + 2, and a third where two would do (forward, 5000 rows of 16384 bf16
+  // columns: 115 us with three, 133 with two)
+  static constexpr int BUFS = AHEAD > 0 ? 2 * AHEAD + 2 : 3;
   float* warps;    // [BUFS][RN_SLOT] the warps' sums (unused ones stay 0)
   float4* ctas;    // [BUFS][CL][N4] the CTAs' sums
   uint64_t* bars;  // [BUFS] completed by CL sends
