@@ -40,14 +40,17 @@ __device__ __forceinline__ SeqCall seq_call(const Cache& c, int s) {
   return r;
 }
 
-constexpr int ST_TILE = 8;    // tokens evaluated together: the N extent of the MMAs
-constexpr int ST_WARPS = 24;  // warps of an SM: what its shared memory holds states for
+constexpr int ST_TILE = 8;  // tokens evaluated together: the N extent of the MMAs
 // Blocks of 2 warps take 32 columns of a state, a whole line of its rows. Calls of
 // more than 8 waves take blocks of 4, which fetch k and q half as often, where the
 // coarser last wave costs less than that: 128 sequences of 32 heads of 128 x 128,
 // fp32, up to 16 tokens, 149 us in blocks of 4, 169 of 2; 45 of 16 heads of
-// 128 x 256, bf16, up to 8 tokens, 32.2 against 31.7.
-constexpr int ST_WIDE_COLS = 8 * 152 * ST_WARPS * 16;  // columns of a call for blocks of 4
+// 128 x 256, bf16, up to 8 tokens, 32.2 against 31.8.
+constexpr int ST_WIDE_COLS = 8 * 152 * 6 * 64;  // columns of a call for blocks of 4
+// Blocks of an SM: as many as its shared memory holds of dk 128 and bf16. (12 small
+// ones would leave 80 registers instead of 96: 16 tokens of one sequence 7.6 us
+// instead of 7.2.)
+constexpr int step_blocks(int warps) { return warps == 2 ? 10 : 6; }
 
 // Two consecutive elements.
 __device__ __forceinline__ void ld2(const float* p, float* v) {
@@ -137,11 +140,12 @@ __device__ __forceinline__ void mma_tf32z(float* c, const uint32_t* a, uint32_t 
 //
 // Bound by the state's bytes; with drafted tokens also by the phases of a block
 // (load, compute, store), which the few waves of a call pass together. What decided
-// (256 x 32 heads of 128 x 128, 8 tokens): 24 warps per SM (states in registers left
-// room for 12 to 16, and the phases did not overlap: 330 us token by token, 234 in
-// tiles; in shared memory 186), the swizzle (24 warps instead of 20, 208 us), and
-// loads of whole lines (see below). One token: 153 us (1.03 GB, 6.8 TB/s). 45
-// sequences of 16 heads of 128 x 256 with up to 8 tokens: 31.7 us (142 MB, 4.5 TB/s).
+// (256 x 32 heads of 128 x 128, 8 tokens): 20 to 24 warps per SM (states in
+// registers left room for 12 to 16, and the phases did not overlap: 330 us token by
+// token, 234 in tiles; in shared memory 186), the swizzle (without it one block less
+// per SM, 208 us), and loads of whole lines (see below). One token: 153 us (1.03 GB,
+// 6.8 TB/s). 45 sequences of 16 heads of 128 x 256 with up to 8 tokens: 31.8 us
+// (142 MB, 4.5 TB/s).
 template <typename T, int DK, int NW>
 struct StepTile {
   static constexpr int COLS = 16 * NW;
@@ -153,7 +157,7 @@ struct StepTile {
 };
 
 template <typename T, int DK, int DV, int NW>
-__global__ void __launch_bounds__(NW * 32, ST_WARPS / NW)
+__global__ void __launch_bounds__(NW * 32, step_blocks(NW))
     k_step(Cache cache, FastDiv byHP, int G, long long ldq, long long ldk, long long ldv,
            long long ldg, long long ldb, float q_scale, float eps, const T* q, const T* k,
            const T* v, const T* g, const T* beta, const float* rate, const float* bias, float* S,
