@@ -47,10 +47,14 @@ constexpr int ST_TILE = 8;  // tokens evaluated together: the N extent of the MM
 // fp32, up to 16 tokens, 149 us in blocks of 4, 169 of 2; 45 of 16 heads of
 // 128 x 256, bf16, up to 8 tokens, 32.2 against 31.8.
 constexpr int ST_WIDE_COLS = 8 * 152 * 6 * 64;  // columns of a call for blocks of 4
-// Blocks of an SM: as many as its shared memory holds of dk 128 and bf16. (12 small
-// ones would leave 80 registers instead of 96: 16 tokens of one sequence 7.6 us
-// instead of 7.2.)
-constexpr int step_blocks(int warps) { return warps == 2 ? 10 : 6; }
+// Blocks that an SM has to have registers for: with dk 128 what its shared memory
+// holds (for 12 of 2 warps, 80 registers instead of 96: 16 tokens of one sequence
+// 7.6 us instead of 7.2). Half the state leaves room for more: 512 sequences of 32
+// heads of 64 x 64, one token, 84 us with 8 blocks of 4 warps, 90 with 6; small fp32
+// calls lose by it (93 sequences of 6 heads of 64 x 64: 5.6 us with 10, 5.9 with 12).
+constexpr int step_blocks(int warps, int dk, bool bf16) {
+  return warps == 4 ? (dk == 64 ? 8 : 6) : dk == 64 && bf16 ? 12 : 10;
+}
 
 // Two consecutive elements.
 __device__ __forceinline__ void ld2(const float* p, float* v) {
@@ -157,7 +161,7 @@ struct StepTile {
 };
 
 template <typename T, int DK, int DV, int NW>
-__global__ void __launch_bounds__(NW * 32, step_blocks(NW))
+__global__ void __launch_bounds__(NW * 32, step_blocks(NW, DK, sizeof(T) == 2))
     k_step(Cache cache, FastDiv byHP, int G, long long ldq, long long ldk, long long ldv,
            long long ldg, long long ldb, float q_scale, float eps, const T* q, const T* k,
            const T* v, const T* g, const T* beta, const float* rate, const float* bias, float* S,
