@@ -471,7 +471,11 @@ __global__ void __launch_bounds__(NW * 32, step_blocks(NW, DK, sizeof(T) == 2))
 }
 
 constexpr int CS_NT = 128;  // threads of a block, 4 channels each
-constexpr int CS_LA = 4;    // tokens of a sequence loaded ahead
+// Tokens of a sequence loaded ahead (fp32, 1024 sequences of up to 7 tokens: 66 us
+// with 4, 61 with 6; bf16, 301 of up to 6: 13.1 with 4, 13.4 with 6). The widest fp32
+// rows of two sequences would pass 48 KB with 6.
+template <typename T, int W>
+constexpr int CS_LA = sizeof(T) == 4 && W < 8 ? 6 : 4;
 constexpr int CS_BLOCKS = 152 * 16;  // twice what is resident, so that blocks overlap
 
 // 4 channels as loaded, converted when used.
@@ -519,7 +523,8 @@ __device__ __forceinline__ void cp4(Raw4<__nv_bfloat16>* to, const __nv_bfloat16
 // Sequences whose inputs a thread has in flight: 3, or what 48 KB hold.
 template <typename T, int W>
 constexpr int conv_stages() {
-  constexpr int one = (W - 1 + CS_LA) * CS_NT * (int)sizeof(Raw4<T>);
+  constexpr int one = (W - 1 + CS_LA<T, W>) * CS_NT * (int)sizeof(Raw4<T>);
+  static_assert(2 * one <= 48 << 10, "what a kernel may use without asking");
   return 3 * one <= 48 << 10 ? 3 : 2;
 }
 
@@ -534,7 +539,7 @@ template <typename T, int W>
 __global__ void __launch_bounds__(CS_NT, W <= 4 && sizeof(T) == 2 ? 8 : 4)
     k_conv_step(Cache cache, int C, int act, long long ldx, const T* x, const float* w,
                 const float* b, T* state, T* y) {
-  constexpr int ST = conv_stages<T, W>(), SLOTS = W - 1 + CS_LA;
+  constexpr int ST = conv_stages<T, W>(), SLOTS = W - 1 + CS_LA<T, W>;
   __shared__ __align__(16) Raw4<T> ring[ST * SLOTS * CS_NT];
   chain();
   const int c0 = (blockIdx.x * CS_NT + threadIdx.x) * 4;
@@ -551,7 +556,7 @@ __global__ void __launch_bounds__(CS_NT, W <= 4 && sizeof(T) == 2 ? 8 : 4)
           cp4(to + j * CS_NT, state + ((size_t)sc.in * (W - 1) + j) * C);
       }
 #pragma unroll
-      for (int u = 0; u < CS_LA; ++u)
+      for (int u = 0; u < CS_LA<T, W>; ++u)
         if (u < sc.len) cp4(to + (W - 1 + u) * CS_NT, x + (size_t)(sc.t0 + u) * ldx);
     }
     cp_commit();
@@ -578,11 +583,11 @@ __global__ void __launch_bounds__(CS_NT, W <= 4 && sizeof(T) == 2 ? 8 : 4)
     };
     if (sc.store && sc.commit == 0) store();
     Raw4<T> past;  // the next token's input past the first CS_LA
-    if (sc.len > CS_LA) past = ldraw4(x + (size_t)(sc.t0 + CS_LA) * ldx);
+    if (sc.len > CS_LA<T, W>) past = ldraw4(x + (size_t)(sc.t0 + CS_LA<T, W>) * ldx);
     for (int t = 0; t < sc.len; ++t) {
       float xc[4], out[4];
-      cvt4(t < CS_LA ? from[(W - 1 + t) * CS_NT] : past, xc);
-      if (t >= CS_LA && t + 1 < sc.len) past = ldraw4(x + (size_t)(sc.t0 + t + 1) * ldx);
+      cvt4(t < CS_LA<T, W> ? from[(W - 1 + t) * CS_NT] : past, xc);
+      if (t >= CS_LA<T, W> && t + 1 < sc.len) past = ldraw4(x + (size_t)(sc.t0 + t + 1) * ldx);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float z = br[i];
