@@ -105,6 +105,16 @@ def test_step_one_token_each(N, H, dtype):
     run_step([1] * N, H, H, 128, 128, DT[dtype], True, N + H, N, packed=False, scale=0.1)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv,N", [(64, 64, 230), (64, 128, 116), (64, 256, 58), (128, 64, 230),
+                                     (128, 128, 116), (128, 256, 58)])
+def test_step_large_calls(dtype, dk, dv, N):
+    """Calls of many waves (32 heads): up to 10 tokens, some sequences with none."""
+    lens = [(1, 0, 2, 5, 10, 1)[i % 6] for i in range(N)]
+    commit = [min(n, i % 4) if i % 3 else n for i, n in enumerate(lens)]
+    run_step(lens, 32, 8, dk, dv, DT[dtype], True, dk + dv, N, commit=commit, scale=dk ** -0.5)
+
+
 @pytest.mark.parametrize("lens", [[1], [2], [5], [7], [8], [9], [16], [17], [33, 4, 70], [64, 1]])
 def test_step_token_counts(lens):
     run_step(lens, 2, 1, 128, 128, torch.bfloat16, True, sum(lens), len(lens), scale=0.1)
@@ -272,6 +282,41 @@ def test_conv_step_one_token_each():
     x, w, b, state = r(37, 96), r(96, 4), r(96), r(40, 3, 96)
     ry, rs = lo.conv_step(np64(x), np64(w), np64(b), np64(state))
     y = gdn.gdn_conv_step(x, w, b, state)
+    torch.cuda.synchronize()
+    check("y", y, ry, 1e-5)
+    assert np.array_equal(np64(state), rs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("W", [5, 6, 7])
+def test_conv_step_other_widths(dtype, W):
+    r = gen(40 + W)
+    lens = [0, 1, 3, 4, 5, 6, 7, 8, 12]
+    n, C = sum(lens), 68
+    x, w, b = r(n, C, dtype=DT[dtype]), r(C, W, by=W ** -0.5), r(C)
+    state = r(len(lens), W - 1, C, dtype=DT[dtype])
+    commit = [0, 1, 2, 4, 0, 5, 7, 3, 12]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    ry, rs = lo.conv_step(np64(x), np64(w), np64(b), np64(state), cu=cu, commit=commit)
+    y = gdn.gdn_conv_step(x, w, b, state, cu_seqlens=i32(cu), n_commit=i32(commit))
+    torch.cuda.synchronize()
+    check("y", y, ry, 1e-5)
+    assert np.array_equal(np64(state), rs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_conv_step_many_sequences(dtype):
+    """More sequences than threads per channel: each takes several, loads of the next in flight."""
+    r, rng = gen(5), np.random.default_rng(5)
+    N, C = 1300, 4096
+    lens = rng.integers(0, 8, N)
+    commit = np.minimum(rng.integers(0, 8, N), lens)
+    x, w, b = r(int(lens.sum()), C, dtype=DT[dtype]), r(C, 4, by=0.5), r(C)
+    state = r(N + 3, 3, C, dtype=DT[dtype])
+    si = rng.permutation(N + 3)[:N]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    ry, rs = lo.conv_step(np64(x), np64(w), np64(b), np64(state), si, si, cu, commit)
+    y = gdn.gdn_conv_step(x, w, b, state, i32(si), i32(si), i32(cu), i32(commit))
     torch.cuda.synchronize()
     check("y", y, ry, 1e-5)
     assert np.array_equal(np64(state), rs)
