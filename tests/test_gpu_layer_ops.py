@@ -369,6 +369,12 @@ def test_prep(dtype, dk, B, T, H, Hk):
         assert torch.equal(u, v)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prep_many_tokens(dtype):
+    """Several tokens of a head to a thread in the gates' backward."""
+    test_prep(dtype, 64, 1, 6007, 35, 5)
+
+
 # --------------------------------------------------------------------- gated norm
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("act", ["silu", "sigmoid"])
@@ -396,6 +402,13 @@ def test_gate_norm(dtype, act, B, T, H, d, pad):
     check("dw", got[2], ref[2], 2e-5, mag)
     for u, v in zip(got, again):
         assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,H,d", [(2, 9000, 3, 128), (1, 7001, 4, 256), (1, 9001, 8, 56)])
+def test_gate_norm_many_rows(dtype, B, T, H, d):
+    """More rows than the backward's blocks take at a time."""
+    test_gate_norm(dtype, "silu", B, T, H, d, 8)
 
 
 # ----------------------------------------------------------------- block boundary
@@ -428,6 +441,14 @@ def test_res_norm(types, post, scale, rows, C):
             check(name, u, v, 2e-5, m)
         for u, v in zip(got, again):
             assert u is None or torch.equal(u, v)
+
+
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("post,scale", [(False, False), (True, True)])
+@pytest.mark.parametrize("rows,C", [(613, 4104), (403, 8200), (307, 16376), (306, 16384)])
+def test_res_norm_many_split_rows(types, post, scale, rows, C):
+    """Rows split over CTAs of a cluster, several to each."""
+    test_res_norm(types, post, scale, rows, C)
 
 
 def test_res_norm_in_place_and_without_a_block():
