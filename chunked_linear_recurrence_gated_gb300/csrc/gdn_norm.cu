@@ -758,28 +758,37 @@ gdn_status check_res(const gdn_res_norm_shape* s) {
   return GDN_OK;
 }
 
+// SMs that clusters can fill: of 4 CTAs of an SM each 36 fit, not 38, and two more
+// than fit would run after the others (of 8, three CTAs to an SM, 51, not 54: 5000 rows
+// of 10240 bf16 columns 150 us, with 54 231).
+int cluster_sms(int cl) { return cl == 8 ? 136 : cl == 4 ? 144 : RN_SMS; }
+
 // How a call's rows are laid out over CTAs; a function of the shape alone, so
 // the order of the parameter gradients' sums is too.
 struct ResPlan {
   int cl, team, teams;  // CTAs per row, threads of a CTA per row, rows per CTA
   int blocks(int rows, int threads) const {  // CTAs, so that each SM has up to `threads`
     const int all = (rows + teams - 1) / teams;
-    // clusters of 4 leave some SMs without a place in one: 36 of them fit, not 38,
-    // and two more than fit would run after the others
-    const int sms = cl == 4 ? 36 * 4 : RN_SMS;
-    return cl * std::min(all, std::max(1, sms * (threads / (team * teams)) / cl));
+    return cl * std::min(all, std::max(1, cluster_sms(cl) * (threads / (team * teams)) / cl));
   }
 };
-ResPlan res_plan(int C, int cols) {
+ResPlan res_plan(int C, bool bwd) {
+  const int cols = bwd ? RN_COLS_B : RN_COLS_F, most = cols / 8;  // threads of an SM
+  const auto team = [&](int cl) { return ((C / 8 + cl - 1) / cl + 31) / 32 * 32; };
+  const auto filled = [&](int cl) { return most / team(cl) * team(cl) * cluster_sms(cl); };
   ResPlan p;
-  p.cl = C <= cols ? 1 : C <= 2 * cols ? 2 : 4;
-  const int groups = (C / 8 + p.cl - 1) / p.cl;
-  p.team = (groups + 31) / 32 * 32;
+  p.cl = 1;
+  while (C > p.cl * cols) p.cl *= 2;
+  // smaller CTAs where they fill the SMs better (backward, 16000 rows of 5120 bf16
+  // columns: 249 us in clusters of 2, 203 in 4; 5000 of 10240: 170 in 4, 150 in 8);
+  // not where one CTA holds a row (20000 of 2560: 120 either way, mixed 124 and 127)
+  if (bwd && p.cl > 1 && 10 * filled(2 * p.cl) > 11 * filled(p.cl)) p.cl *= 2;
+  p.team = team(p.cl);
   p.teams = p.team >= 256 || p.cl > 1 ? 1 : 256 / p.team;
   return p;
 }
 int res_parts(const gdn_res_norm_shape& s) {
-  const ResPlan p = res_plan(s.C, RN_COLS_B);
+  const ResPlan p = res_plan(s.C, true);
   return p.blocks(s.rows, 512) / p.cl;
 }
 
@@ -804,22 +813,24 @@ cudaError_t launch_res(const gdn_res_norm_shape& s, const ResArgs& a, const ResP
                        cudaStream_t st) {
   const int nt = p.team * p.teams;
   const float inv = 1.f / (float)s.C;
-  if (!a.dy) {
-    // rows in flight: 4, where that is what an SM's shared memory holds for 1024
-    // threads; 3 for fp32 streams, and for mixed types in CTAs of 1024 threads
-    // (mixed, 4096 columns: 152 us with 4, 171 with 3; 8192: 135 with 4, 123 with 3)
-    constexpr int slots = fwd_slots<T, R>();
-    auto go = [&](auto stages) {
-      constexpr int S = decltype(stages)::value;
-      return launch_rows(k_res_norm_fwd<T, R, CL, S>, p, p.blocks(s.rows, 1024),
-                         nt * 16 * slots * S, st, s.rows, s.C, inv, s.eps, (const R*)a.h,
-                         (const T*)a.x, a.w, a.w_post, a.scale, (R*)a.ho, (T*)a.y);
-    };
-    if constexpr (slots == 3 && CL == 1) {
-      if (p.team > 512) return go(std::integral_constant<int, 3>());
+  if constexpr (CL <= 2) {  // forward rows take two CTAs at most
+    if (!a.dy) {
+      // rows in flight: 4, where that is what an SM's shared memory holds for 1024
+      // threads; 3 for fp32 streams, and for mixed types in CTAs of 1024 threads
+      // (mixed, 4096 columns: 152 us with 4, 171 with 3; 8192: 135 with 4, 123 with 3)
+      constexpr int slots = fwd_slots<T, R>();
+      auto go = [&](auto stages) {
+        constexpr int S = decltype(stages)::value;
+        return launch_rows(k_res_norm_fwd<T, R, CL, S>, p, p.blocks(s.rows, 1024),
+                           nt * 16 * slots * S, st, s.rows, s.C, inv, s.eps, (const R*)a.h,
+                           (const T*)a.x, a.w, a.w_post, a.scale, (R*)a.ho, (T*)a.y);
+      };
+      if constexpr (slots == 3 && CL == 1) {
+        if (p.team > 512) return go(std::integral_constant<int, 3>());
+      }
+      constexpr int usual = slots == 4 || (slots == 3 && CL != 1) ? 3 : 4;
+      return go(std::integral_constant<int, usual>());
     }
-    constexpr int usual = slots == 4 || (slots == 3 && CL != 1) ? 3 : 4;
-    return go(std::integral_constant<int, usual>());
   }
   return launch_rows(k_res_norm_bwd<T, R, CL>, p, p.blocks(s.rows, 512),
                      nt * 16 * bwd_slots<T, R>() * RN_STAGES_B, st, s.rows, s.C, inv, s.eps,
@@ -828,11 +839,12 @@ cudaError_t launch_res(const gdn_res_norm_shape& s, const ResArgs& a, const ResP
 }
 template <typename T, typename R>
 cudaError_t dispatch_res(const gdn_res_norm_shape& s, const ResArgs& a, cudaStream_t st) {
-  const ResPlan p = res_plan(s.C, a.dy ? RN_COLS_B : RN_COLS_F);
+  const ResPlan p = res_plan(s.C, a.dy != nullptr);
   switch (p.cl) {
     case 1: return launch_res<T, R, 1>(s, a, p, st);
     case 2: return launch_res<T, R, 2>(s, a, p, st);
-    default: return launch_res<T, R, 4>(s, a, p, st);
+    case 4: return launch_res<T, R, 4>(s, a, p, st);
+    default: return launch_res<T, R, 8>(s, a, p, st);
   }
 }
 cudaError_t run_res(const gdn_res_norm_shape& s, const ResArgs& a, cudaStream_t st) {

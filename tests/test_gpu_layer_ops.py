@@ -445,7 +445,7 @@ def test_res_norm(types, post, scale, rows, C):
 
 @pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
 @pytest.mark.parametrize("post,scale", [(False, False), (True, True)])
-@pytest.mark.parametrize("rows,C", [(613, 4104), (403, 8200), (307, 16376), (306, 16384)])
+@pytest.mark.parametrize("rows,C", [(613, 4104), (501, 7000), (403, 8200), (307, 16376), (306, 16384)])
 def test_res_norm_many_split_rows(types, post, scale, rows, C):
     """Rows split over CTAs of a cluster, several to each."""
     test_res_norm(types, post, scale, rows, C)
