@@ -101,16 +101,22 @@ __device__ __forceinline__ void ldb_kn_x2n(uint32_t* b, const __nv_bfloat16* bas
   ldsm_x4_t(smem_u32(p), b[0], b[1], b[2], b[3]);
 }
 
-// cp.async of 16 bytes, zero-filling when `valid` is false.
+// cp.async of 16 bytes, zero-filling when `valid` is false. The copies and their
+// wait are barriers for the compiler: shared memory that only the copying thread
+// reads has no other one, and ordinary loads of a slot have to stay behind the wait
+// for it and ahead of the copy that fills it again.
 __device__ __forceinline__ void cp16(void* smem, const void* gmem, bool valid) {
   const int n = valid ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(smem)),
-               "l"(gmem), "r"(n));
+               "l"(gmem), "r"(n)
+               : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::); }
+__device__ __forceinline__ void cp_commit() {
+  asm volatile("cp.async.commit_group;\n" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N));
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
 }  // namespace gdn

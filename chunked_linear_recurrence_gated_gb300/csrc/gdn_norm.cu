@@ -259,9 +259,11 @@ struct Ring {
     }
     const uint32_t to = smem_u32(at(stage, k));
     if (t.on0)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(p + t.c0));
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(p + t.c0)
+                   : "memory");
     if (t.on1)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to + 8), "l"(p + t.c1));
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to + 8), "l"(p + t.c1)
+                   : "memory");
   }
   template <typename T>
   __device__ __forceinline__ void read(int stage, int k, f32x2* v) const {

@@ -514,10 +514,12 @@ __device__ __forceinline__ void st4(__nv_bfloat16* p, const float* v) {
 
 // 4 channels into shared memory without a register in between.
 __device__ __forceinline__ void cp4(Raw4<float>* to, const float* p) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(to)), "l"(p));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(to)), "l"(p)
+               : "memory");
 }
 __device__ __forceinline__ void cp4(Raw4<__nv_bfloat16>* to, const __nv_bfloat16* p) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(to)), "l"(p));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(to)), "l"(p)
+               : "memory");
 }
 
 // Sequences whose inputs a thread has in flight: 3, or what 48 KB hold.
