@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "../../include/gdn_profile.h"
 #include "gdn_layer.cuh"
 #include "gdn_mma.cuh"
 
@@ -169,6 +170,11 @@ constexpr int RN_COLS_B = 4096;  // backward: 512 threads of 128 registers
 constexpr int RN_SLOT = 128;     // floats of a reduction: 8 values of 16 warps, or 2 of 32
 constexpr int RN_STAGES_B = 3;   // rows a team holds, backward (4 to 6: no faster)
 constexpr int RN_SMS = 152;
+constexpr long long RN_WAIT = 1ll << 32;  // SM clock cycles (two seconds) that a wait may take
+constexpr long long RN_HOLD = 1ll << 26;  // and that a CTA stays after one that ran out
+
+// Set by a wait that ran out, read and cleared by gdn_layer_status.
+__device__ int g_exchange_status;
 
 // The rows of a team and the columns of a thread. With an fp32 stream a
 // thread's columns are two groups of 4 that lie a team apart, so that a warp's
@@ -310,6 +316,9 @@ __device__ __forceinline__ float warp_sum8(const float* v) {
 // CTA's shared memory with st.async, which completes the receiver's mbarrier. (A
 // cluster barrier instead would have to order the row's global stores too: its
 // release waits for them, 6 us per row of 16384 columns against DRAM's 2.)
+// A thread whose wait runs out sets g_exchange_status, takes every later sum as NaN
+// and sends no more: a send of post p relies on its thread having collected
+// p - AHEAD - 1. The other CTAs' waits then run out too, and all reach end().
 template <int K, int CL, int AHEAD>
 struct TeamSum {
   static constexpr int N4 = K > 4 ? 2 : 1;  // float4 per CTA's sums
@@ -321,7 +330,8 @@ struct TeamSum {
   uint64_t* bars;  // [BUFS] completed by CL sends
   int in, out;     // buffers of the next post and the next collect
   uint32_t phase;  // parity of the mbarrier of `out`
-  bool dead;       // a wait gave up: every later sum is NaN, so the failure shows
+  bool dead;       // this thread's wait ran out
+  long long limit = RN_WAIT;
 
   __device__ __forceinline__ void init() {
     constexpr int TEAMS = CL > 1 ? 1 : 8;  // at most
@@ -347,13 +357,45 @@ struct TeamSum {
       named_bar(threadIdx.y + 1, blockDim.x);
     }
   }
-  // A CTA that exits must not be written to any more: every CTA of the cluster
-  // has received all sums.
+  // A CTA that exits must not be written to any more. Past the barrier no CTA of the
+  // cluster sends, and whoever has collected all sums has received all sends to its
+  // CTA; a thread that gave up does not know that, and stays for far longer than a
+  // send can be under way.
   __device__ __forceinline__ void end() {
     if (CL > 1) {
+      __syncwarp();
       asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (dead) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < RN_HOLD) {
+        }
+      }
     }
+  }
+  __device__ __forceinline__ bool arrived() const {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bars + out)), "r"(phase)
+        : "memory");
+    return ok != 0;
+  }
+  // One more try after the time is up: a CTA that was not running meanwhile may find
+  // that the sends have long landed.
+  __device__ __forceinline__ void wait() {
+    if (dead || arrived()) return;
+    const long long t0 = clock64();
+    for (;;) {
+      const bool late = clock64() - t0 > limit;
+      if (arrived()) return;
+      if (late) break;
+    }
+    dead = true;
+    *(volatile int*)&g_exchange_status = DEV_TIMEOUT;
   }
   // The CTA's sums from the warps'.
   __device__ __forceinline__ void read_warps(int buf, float* v) const {
@@ -400,8 +442,8 @@ struct TeamSum {
     if (CL > 1 && threadIdx.x < 32) {
       float s[8] = {};
       read_warps(in, s);
-      if (lane == 0) mbar_arrive_expect_tx(bars + in, CL * 16 * N4);
-      if (lane < CL) {
+      if (lane == 0 && !dead) mbar_arrive_expect_tx(bars + in, CL * 16 * N4);
+      if (lane < CL && !dead) {
         uint32_t rank, to, bar;
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
         asm("mapa.shared::cluster.u32 %0, %1, %2;"
@@ -425,17 +467,7 @@ struct TeamSum {
     if (CL == 1) {
       read_warps(out, v);
     } else {
-      const long long t0 = clock64();
-      for (uint32_t ok = dead; !ok;) {
-        asm volatile(
-            "{\n .reg .pred p;\n"
-            " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(smem_u32(bars + out)), "r"(phase)
-            : "memory");
-        if (!ok && clock64() - t0 > (1ll << 32)) ok = dead = true;
-      }
+      wait();
       float s[4 * N4] = {};
 #pragma unroll
       for (int r = 0; r < CL; ++r)
@@ -453,6 +485,31 @@ struct TeamSum {
     }
   }
 };
+
+// The exchange by itself (gdn_diag_exchange): each of a cluster's CTAs posts
+// DIAG_POSTS sums of ones, one ahead of their collection as the backward does; CTA
+// `silent` sends nothing, as if its own wait had run out. sums[CTA]: the last sum.
+constexpr int DIAG_CL = 4, DIAG_NT = 64, DIAG_POSTS = 9;
+__global__ void __launch_bounds__(DIAG_NT) k_exchange(int silent, long long limit, float* sums) {
+  chain();
+  TeamSum<6, DIAG_CL, 1> sum;
+  sum.init();
+  sum.limit = limit;
+  sum.dead = (int)blockIdx.x == silent;
+  float v[8];
+  auto post = [&]() {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = 1.f;
+    sum.post(v);
+  };
+  post();
+  for (int p = 0; p < DIAG_POSTS; ++p) {
+    if (p + 1 < DIAG_POSTS) post();
+    sum.collect(v);
+  }
+  sum.end();
+  if (threadIdx.x == 0) sums[blockIdx.x] = v[5];
+}
 
 // With rx = 1 / sqrt(mean x^2 + eps) (1 without w_post) and r the same of h':
 //   h' = h + scale w_post rx x,   y = r w h'.
@@ -855,6 +912,21 @@ cudaError_t run_res(const gdn_res_norm_shape& s, const ResArgs& a, cudaStream_t 
   return dispatch_res<__nv_bfloat16, __nv_bfloat16>(s, a, st);
 }
 
+cudaError_t run_exchange(int silent, long long limit, float* sums, cudaStream_t st) {
+  return launch(k_exchange, dim3(DIAG_CL), dim3(DIAG_NT), 0, st, DIAG_CL, silent, limit, sums);
+}
+gdn_status take_status(cudaStream_t st) {
+  if (cudaStreamSynchronize(st) != cudaSuccess) return GDN_ERR_CUDA;
+  int word = 0;
+  const int zero = 0;
+  if (cudaMemcpyFromSymbol(&word, g_exchange_status, sizeof(int)) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  if (word == DEV_OK) return GDN_OK;
+  if (cudaMemcpyToSymbol(g_exchange_status, &zero, sizeof(int)) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  return GDN_ERR_TIMEOUT;
+}
+
 }  // namespace
 }  // namespace gdn
 
@@ -975,6 +1047,15 @@ gdn_status gdn_res_norm_bwd(const gdn_res_norm_shape* shape, const void* h_out, 
                                  w_post ? dw_post : dscale, dscale, st);
   prof_mark(st, nullptr);
   return ce ? GDN_ERR_CUDA : GDN_OK;
+}
+
+gdn_status gdn_layer_status(void* stream) { return gdn::take_status((cudaStream_t)stream); }
+
+int gdn_diag_exchange(float* sums, int silent, int limit_log2, void* stream) {
+  using namespace gdn;
+  if (!sums || !aligned(sums, 4) || silent < -1 || silent >= DIAG_CL) return GDN_ERR_INVALID_ARG;
+  const int lg = std::min(std::max(limit_log2, 10), 32);
+  return run_exchange(silent, 1ll << lg, sums, (cudaStream_t)stream) ? GDN_ERR_CUDA : GDN_OK;
 }
 
 }  // extern "C"

@@ -39,7 +39,7 @@ CONV_ACT = {"none": 0, "silu": 1}
 LAYER_EXPORTS = ["gdn_step", "gdn_conv_step", "gdn_prep_fwd", "gdn_prep_bwd",
                  "gdn_prep_workspace_bytes", "gdn_gate_norm_fwd", "gdn_gate_norm_bwd",
                  "gdn_gate_norm_workspace_bytes", "gdn_res_norm_fwd", "gdn_res_norm_bwd",
-                 "gdn_res_norm_workspace_bytes"]
+                 "gdn_res_norm_workspace_bytes", "gdn_layer_status"]
 GATE_ACT = {"silu": 1, "sigmoid": 2}
 
 
@@ -163,6 +163,10 @@ def load(build_if_missing: bool = False):
         f = getattr(lib, f"gdn_{name}_workspace_bytes")
         f.argtypes = [ctypes.POINTER(shape)]
         f.restype = Z
+    lib.gdn_layer_status.argtypes = [P]
+    lib.gdn_layer_status.restype = I
+    lib.gdn_diag_exchange.argtypes = [P, I, I, P]
+    lib.gdn_diag_exchange.restype = I
     lib.gdn_profile_arm.argtypes = [P, I]
     lib.gdn_profile_arm.restype = None
     lib.gdn_profile_count.argtypes = []
@@ -540,6 +544,18 @@ def gdn_res_norm_bwd(h_out, x, w, dy, dh_out=None, w_post=None, scale=None, eps=
                           dh, workspace)
     return (_ext_module or ext()).res_norm_bwd(h_out, x, w, dy, dh_out, w_post, scale, eps, dh,
                                                workspace)
+
+
+def gdn_layer_status(stream=None) -> int:
+    """What the layer operators recorded on the current device since the last query
+    (0, or GDN_ERR_TIMEOUT); synchronises the stream and resets it."""
+    return load().gdn_layer_status(_stream(stream))
+
+
+def diag_exchange(sums, silent=-1, limit_log2=20, stream=None) -> int:
+    """Runs the self-check of the exchange between the CTAs of a wide row
+    (include/gdn_profile.h); read the outcome with gdn_layer_status."""
+    return load().gdn_diag_exchange(_p(sums), silent, limit_log2, _stream(stream))
 
 
 def gdn_workspace_status(workspace, stream=None) -> int:

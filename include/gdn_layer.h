@@ -30,6 +30,10 @@
  *   enqueued on `stream` without synchronising, every argument checked on the
  *   host before any launch, GDN_ERR_CUDA if a launch fails. Calls with nothing
  *   to do (no tokens, no rows) still write their parameter gradients (zeros).
+ *   One condition shows on the device only: the CTAs that share a wide row of
+ *   gdn_res_norm_* wait for each other's sums, and a wait that runs out (after
+ *   about two seconds) leaves NaN in that call's outputs and is reported by
+ *   gdn_layer_status.
  * - Parameter gradients are summed in a fixed order: results are the same from
  *   run to run.
  */
@@ -191,6 +195,12 @@ gdn_status gdn_res_norm_bwd(const gdn_res_norm_shape* shape, const void* h_out, 
                             const void* dy, const void* dh_out, void* dh, void* dx, float* dw,
                             float* dw_post, float* dscale, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/* Synchronises `stream`, then returns what the calls of this header have
+ * recorded on the current device since the last such query (GDN_OK, or
+ * GDN_ERR_TIMEOUT for a wait that ran out) and resets it. One word for all
+ * streams of a device. */
+gdn_status gdn_layer_status(void* stream);
 
 #ifdef __cplusplus
 }

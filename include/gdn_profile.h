@@ -53,6 +53,16 @@ void gdn_diag_set_fwd_split(int segments, int first_permille, int chain_rg);
  * on the current device; read the outcome with gdn_noalloc_status. */
 int gdn_diag_wait_timeout_noalloc(int limit_log2, void* stream);
 
+/* Self-check of the exchange between the CTAs of a row in gdn_res_norm_*, and
+ * of its bounded wait. One cluster of four CTAs exchanges sums of ones nine
+ * times; sums (DEVICE float [4]) receives each CTA's last sum, 256. CTA
+ * `silent` (0..3; -1: none) sends nothing: then every wait runs out after
+ * 2^limit_log2 SM clock cycles (clamped to [10, 32]), the sums are NaN,
+ * gdn_layer_status reports GDN_ERR_TIMEOUT, and the context stays usable.
+ * Returns GDN_ERR_INVALID_ARG / GDN_ERR_CUDA on a bad argument / failed
+ * launch. */
+int gdn_diag_exchange(float* sums, int silent, int limit_log2, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
