@@ -141,9 +141,9 @@ struct FastDiv {
 
 __device__ __forceinline__ float sigmoidf_(float x) { return 1.f / (1.f + expf(-x)); }
 // sigmoid of a value that is stored as T: for bf16 results the hardware's
-// approximate exponential and reciprocal (relative error below 1e-6 for
-// |x| < 10, against bf16's 4e-3) instead of the exact library sequences, which
-// cost several times the instructions.
+// approximate exponential and reciprocal (below 2e-6 of the value for |x| <= 10, by
+// their published bounds, against bf16's 4e-3) instead of the exact library
+// sequences, which cost several times the instructions.
 template <typename T>
 __device__ __forceinline__ float sigmoid_as(float x) {
   return sigmoidf_(x);
@@ -151,6 +151,15 @@ __device__ __forceinline__ float sigmoid_as(float x) {
 template <>
 __device__ __forceinline__ float sigmoid_as<__nv_bfloat16>(float x) {
   return __fdividef(1.f, 1.f + __expf(-x));
+}
+// s = sigmoid(x) = 1 / (1 + e) and t = 1 - s = e s, with e = e^-x. The difference 1 - s
+// would lose t where s is near 1 (1 % of it at x = 12, all of it past 17). Where e is
+// infinite both are 0: s t and s + x s t vanish there too.
+template <typename T>
+__device__ __forceinline__ void sigmoid_pair(float x, float& s, float& t) {
+  const float e = sizeof(T) == 4 ? expf(-x) : __expf(-x);
+  s = sizeof(T) == 4 ? 1.f / (1.f + e) : __fdividef(1.f, 1.f + e);
+  t = fminf(e, 3e38f) * s;
 }
 // log(1 + e^x) without overflow for large x and without cancellation for small
 __device__ __forceinline__ float softplusf_(float x) {

@@ -117,8 +117,10 @@ __global__ void __launch_bounds__(GN_NT, gate_blocks<T>())
         cvt8(gr[u], gy);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f32x2 s = pack2(sigmoid_as<T>(zz[2 * i]), sigmoid_as<T>(zz[2 * i + 1]));
-          const f32x2 t = fma2(s, both2(-1.f), both2(1.f));  // 1 - s
+          float s0, s1, t0, t1;
+          sigmoid_pair<T>(zz[2 * i], s0, t0);
+          sigmoid_pair<T>(zz[2 * i + 1], s1, t1);
+          const f32x2 s = pack2(s0, s1), t = pack2(t0, t1);
           f32x2 a = s, da = mul2(s, t);
           if (act == GDN_GATE_SILU) {
             a = mul2(s, pack2(zz[2 * i], zz[2 * i + 1]));

@@ -108,12 +108,14 @@ __device__ __forceinline__ void prep_bwd_gates(int blk, int rows, int H, int hp_
       for (int t = t0 + ty; t < t1; t += ny) {
         const size_t at = (size_t)t * H + h;
         const float x = ldf(xg + (size_t)t * ldg + h) + bi, d = ldf(dg + at);
-        const float b = sigmoidf_(ldf(xb + (size_t)t * ldb + h)), db = ldf(dbeta + at);
+        const float db = ldf(dbeta + at);
+        float b, nb;  // sigmoid and 1 - sigmoid
+        sigmoid_pair<float>(ldf(xb + (size_t)t * ldb + h), b, nb);
         const float dx = -d * er * sigmoidf_(x);
         sr = fmaf(d, -er * softplusf_(x), sr);
         sb += dx;
         stf(dxg + at, dx);
-        stf(dxb + at, db * b * (1.f - b));
+        stf(dxb + at, db * b * nb);
       }
     }
     red[0][threadIdx.x] = sr;

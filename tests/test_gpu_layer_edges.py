@@ -1,10 +1,14 @@
 """Edges of the layer operators (include/gdn_layer.h) on the GPU: waits that run
 out, open gates, small eps, empty batches, and the precision of fp32 calls."""
+import numpy as np
 import pytest
 import torch
 
 from chunked_linear_recurrence_gated_gb300 import gdn
-from test_gpu_layer_ops import gen, test_res_norm as check_res_norm
+from helpers import np64
+from oracle import layer_ops as lo
+from test_gpu_layer_ops import HALF
+from test_gpu_layer_ops import test_res_norm as check_res_norm
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +34,45 @@ def test_exchange_wait_that_runs_out_is_reported(silent):
     assert torch.isnan(sums).all()
     check_res_norm(("bf16", "f32"), True, True, 37, 8200)
     assert gdn.gdn_layer_status() == 0
+
+# --------------------------------------------------------------- open and closed gates
+def gate_inputs(dtype):
+    """z over [-80, 80], the other factors of the gradient fixed, and s(z), 1 - s(z) in fp64."""
+    z = torch.linspace(-80, 80, 64 * 40, device="cuda").to(dtype)
+    x = np64(z)
+    return z, lo.sigmoid(x), lo.sigmoid(-x)
+
+
+# fp32: expf 2 ulp, reciprocal and products 1 each, rsqrtf 2: below 16 u. bf16 results:
+# __expf is good to 2 + 1.2 |x| ulp (98 at 80, 1.2e-5), then the result's rounding.
+GATE_TOL = {torch.float32: 1e-6, torch.bfloat16: 2e-5 + HALF}
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_gate_norm_gradient_of_open_and_closed_gates(dtype, act):
+    """dz element by element: the gate's derivative does not cancel where s is near 1."""
+    z, s, t = gate_inputs(dtype)
+    z = z.view(1, 40, 1, 64)
+    o, w = torch.ones_like(z), torch.ones(64, device="cuda")
+    _, dz, _ = gdn.gdn_gate_norm_bwd(o, z, w, o, act)
+    torch.cuda.synchronize()
+    n, x = 1.0 / np.sqrt(1.0 + 1e-6), np64(z).reshape(-1)
+    want = n * (s * t if act == "sigmoid" else s * (1.0 + x * t))
+    mag = n * (s * t if act == "sigmoid" else s * (1.0 + np.abs(x) * t))
+    off = np.abs(np64(dz).reshape(-1) - want) / mag
+    assert off.max() <= GATE_TOL[dtype], (off.max(), x[off.argmax()])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prep_gradient_of_open_and_closed_gates(dtype):
+    xb, s, t = gate_inputs(dtype)
+    xb = xb.view(1, -1, 4)
+    T = xb.shape[1]
+    qk = torch.ones(1, T, 4, 64, dtype=dtype, device="cuda")
+    one, zero = torch.ones_like(xb), torch.zeros(4, device="cuda")
+    dxb = gdn.gdn_prep_bwd(qk, qk, xb, xb, zero, zero, qk, qk, one, one)[3]
+    torch.cuda.synchronize()
+    off = np.abs(np64(dxb).reshape(-1) - s * t) / (s * t)
+    assert off.max() <= 1e-6 + (HALF if dtype == torch.bfloat16 else 0.0), off.max()
+
