@@ -705,7 +705,8 @@ __global__ void __launch_bounds__(512, 1)
     if (++stage == S) stage = 0;
     const float r = rsqrtf(fmaf(s[0], inv_C, eps));
     const float rx = w_post ? rsqrtf(fmaf(s[2], inv_C, eps)) : 1.f;
-    const float hc = -r * r * r * s[1] * inv_C;  // factor of h in dh
+    // factor of h in dh; r^3 by itself may overflow where eps is small and s[1] 0
+    const float hc = -r * (r * (r * s[1])) * inv_C;
     const f32x2 r2 = both2(r), hc2 = both2(hc), rx2 = both2(rx);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

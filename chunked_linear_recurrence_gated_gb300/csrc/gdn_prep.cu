@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(PR_NT)
     xd = lane_sum<L>(xd);
     if (r >= nrow) continue;
     const HeadRow h = head_row(r, by2Hk, Hk);
-    const float rr = rsqrtf(ss + eps), s = (h.is_k ? 1.f : q_scale) * rr, m = rr * rr * xd;
+    const float rr = rsqrtf(ss + eps), s = (h.is_k ? 1.f : q_scale) * rr, m = rr * (rr * xd);
 #pragma unroll
     for (int i = 0; i < 8; ++i) d[u][i] = s * fmaf(-x[i], m, d[u][i]);
     st8((h.is_k ? dk : dq) + ((size_t)h.t * Hk + h.hk) * DK + c, d[u]);

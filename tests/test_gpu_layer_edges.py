@@ -7,7 +7,7 @@ import torch
 from chunked_linear_recurrence_gated_gb300 import gdn
 from helpers import np64
 from oracle import layer_ops as lo
-from test_gpu_layer_ops import HALF
+from test_gpu_layer_ops import DT, HALF, check, gen
 from test_gpu_layer_ops import test_res_norm as check_res_norm
 
 pytestmark = pytest.mark.gpu
@@ -75,4 +75,46 @@ def test_prep_gradient_of_open_and_closed_gates(dtype):
     torch.cuda.synchronize()
     off = np.abs(np64(dxb).reshape(-1) - s * t) / (s * t)
     assert off.max() <= 1e-6 + (HALF if dtype == torch.bfloat16 else 0.0), off.max()
+
+# ------------------------------------------------------------------------- small eps
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("eps", [1e-30, 1e-40])
+def test_small_eps_and_small_rows(dtype, eps):
+    """Zero rows, and rows far below sqrt(eps), where 1 / rms is up to 1e20: its square
+    and cube must not be formed by themselves (0 times infinity)."""
+    dt, r = DT[dtype], gen(51)
+    x, h = r(6, 256, dtype=dt), r(6, 256, dtype=dt)
+    for u in (x, h):
+        u[0] = 0.0
+        if eps == 1e-30:
+            u[1] *= 1e-17
+    w, wp, dy, dh = r(256), r(256), r(6, 256, dtype=dt), r(6, 256, dtype=dt)
+    f = lambda *ts: [np64(t) for t in ts]
+
+    def rows(name, got, ref):
+        for i in range(got.shape[0]):
+            # 1 / rms of both norms is 1e20 in row 0: parts of its dx have no fp32 value
+            past = np.abs(ref[i]) > np.finfo(np.float32).max
+            assert (np64(got[i])[past] == np.sign(ref[i][past]) * np.inf).all(), (name, i)
+            keep = torch.from_numpy(~past)
+            mag = np.abs(ref[i]).max()
+            check(f"{name} row {i}", got[i].cpu()[keep], ref[i][~past], 5e-5, mag)
+
+    got = gdn.gdn_res_norm_bwd(h, x, w, dy, dh, w_post=wp, eps=eps)
+    ref = lo.res_norm_bwd(*f(h, x, w, dy, dh), w_post=np64(wp), eps=eps)[0]
+    for name, u, v in zip(("dh", "dx"), got, ref):
+        rows(name, u, v)
+    rows("y", gdn.gdn_res_norm_fwd(h, x, w, wp, eps=eps)[1],
+         lo.res_norm_fwd(*f(h, x, w, wp), eps=eps)[1])
+    o = lambda t: t.view(1, 6, 4, 64)
+    got = gdn.gdn_gate_norm_bwd(o(h), o(x), w[:64].clone(), o(dy), eps=eps)
+    ref = lo.gate_norm_bwd(*f(o(h), o(x), w[:64], o(dy)), eps=eps)[0]
+    for name, u, v in zip(("do", "dz"), got, ref):
+        rows(name, u.view(24, 64), v.reshape(24, 64))
+    gates = r(1, 6, 4, dtype=dt)
+    a = (o(h), o(x), gates, gates, r(4), r(4), o(dy), o(dh), gates, gates)
+    got = gdn.gdn_prep_bwd(*a, eps=eps)
+    ref = lo.prep_bwd(*f(*a), eps=eps)[0]
+    for name, u, v in zip(("dq", "dk"), got, ref):
+        rows(name, u.view(24, 64), v.reshape(24, 64))
 
