@@ -115,6 +115,7 @@ long long rows(const char* name, const Tensor& t, int64_t inner) {
                      " dimensions must be dense, got " + described(t));
     dense *= sh[i];
   }
+  if (t.numel() == 0) return dense;  // no rows: the strides say nothing
   int64_t ld = dense, n = 1;
   for (int64_t i = dim - inner - 1; i >= 0; --i) {
     if (sh[i] == 1) continue;

@@ -118,3 +118,18 @@ def test_small_eps_and_small_rows(dtype, eps):
     for name, u, v in zip(("dq", "dk"), got, ref):
         rows(name, u.view(24, 64), v.reshape(24, 64))
 
+# --------------------------------------------------------------------- empty batches
+def test_batches_without_tokens():
+    e = lambda *s: torch.empty(*s, device="cuda")
+    one = torch.ones(64, device="cuda")
+    a = (e(2, 0, 2, 64), e(2, 0, 2, 64), e(2, 0, 2), e(2, 0, 2), one[:2], one[:2])
+    assert gdn.gdn_prep_fwd(*a)[0].shape == (2, 0, 2, 64)
+    p = gdn.gdn_prep_bwd(*a, e(2, 0, 2, 64), e(2, 0, 2, 64), e(2, 0, 2), e(2, 0, 2))
+    assert gdn.gdn_gate_norm_fwd(e(2, 0, 1, 64), e(2, 0, 1, 64), one).shape == (2, 0, 1, 64)
+    g = gdn.gdn_gate_norm_bwd(e(2, 0, 1, 64), e(2, 0, 1, 64), one, e(2, 0, 1, 64))
+    assert gdn.gdn_res_norm_fwd(e(2, 0, 64), e(2, 0, 64), one)[1].shape == (2, 0, 64)
+    r = gdn.gdn_res_norm_bwd(e(2, 0, 64), e(2, 0, 64), one, e(2, 0, 64), None, one, one)
+    torch.cuda.synchronize()
+    for t in (p[4], p[5], g[2], *r[2:]):
+        assert not t.any()
+
