@@ -387,6 +387,8 @@ PyObject* res_norm_fwd(PyObject* const* a) {
                     : a[8] == Py_None ? h.scalar_type()
                     : choice(a[8])  ? at::kBFloat16
                                     : at::kFloat;
+  if ((x || yo) && a[8] != Py_None && (choice(a[8]) != 0) != (type == at::kBFloat16))
+    throw BadValue(std::string("dtype: ") + (x ? "x" : "y") + " is " + c10::toString(type));
   const Res p = res_args("h", h, type, a[2], a[3], a[4], a[5]);
   const void* px = like("x", x, h, type, p.dev);
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.dev);

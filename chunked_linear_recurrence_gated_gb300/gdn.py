@@ -524,7 +524,8 @@ def gdn_res_norm_fwd(h, x, w, w_post=None, scale=None, eps=1e-6, h_out=None, y=N
 
     h [..., C] is the residual stream (fp32, or x's dtype), x [..., C] the block's
     output; w, w_post, scale [C] fp32. w_post None: x as it is; scale None: 1; x None
-    (before the first block): y is the norm of h, in `dtype` (default h's).
+    (before the first block): y is the norm of h, in `dtype` (default h's; with x or a
+    given y, theirs is the only one).
     h_out may be h. Returns (h_out, y); h_out is None where x is."""
     if stream is not None:
         return _on_stream(gdn_res_norm_fwd, stream, h, x, w, w_post, scale, eps, h_out, y, dtype)

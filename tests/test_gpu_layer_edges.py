@@ -133,3 +133,14 @@ def test_batches_without_tokens():
     for t in (p[4], p[5], g[2], *r[2:]):
         assert not t.any()
 
+# ------------------------------------------------------------------ the type of a norm
+def test_res_norm_refuses_another_type_than_it_returns():
+    r = gen(52)
+    h, x, w = r(3, 64), r(3, 64, dtype=torch.bfloat16), r(64)
+    with pytest.raises(ValueError):
+        gdn.gdn_res_norm_fwd(h, x, w, dtype=torch.float32)
+    with pytest.raises(ValueError):
+        gdn.gdn_res_norm_fwd(h, None, w, y=torch.empty_like(h), dtype=torch.bfloat16)
+    assert gdn.gdn_res_norm_fwd(h, x, w, dtype=torch.bfloat16)[1].dtype == torch.bfloat16
+    assert gdn.gdn_res_norm_fwd(h, None, w, dtype=torch.bfloat16)[1].dtype == torch.bfloat16
+
