@@ -4,7 +4,9 @@
 Each translation unit under csrc/ is compiled by its own process (in parallel),
 then linked into ``_build/libgdn.so`` (the .cu files; only sm_103a is targeted)
 and ``_build/_gdn_torch.so`` (gdn_torch.cpp, against the installed torch's
-headers; it is rebuilt when torch or Python changes).
+headers; it is rebuilt when torch or Python changes). The library needs neither
+torch nor that module: without torch only the library is built, and it is linked
+before the module.
 """
 from __future__ import annotations
 
@@ -42,11 +44,10 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _torch_root() -> str:
+def _torch_root():
+    """Where torch is installed, or None."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.origin:
-        raise RuntimeError("torch not found: its headers are required to build _gdn_torch")
-    return os.path.dirname(spec.origin)
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
 
 
 def _built_for() -> str:
@@ -92,7 +93,8 @@ def _ext_link(obj: str, to: str) -> list:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    kernels, ext = force or _stale(), force or _ext_stale()
+    kernels = force or _stale()
+    ext = _torch_root() is not None and (force or _ext_stale())
     if not kernels and not ext:
         return LIB
     os.makedirs(OUT, exist_ok=True)
@@ -111,20 +113,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if ext:
         procs.append((EXT_SRC, subprocess.Popen(_ext_compile(ext_obj), stdout=subprocess.PIPE,
                                                 stderr=subprocess.STDOUT, text=True)))
-    failed = []
+    failed = set()
     for src, p in procs:
         out, _ = p.communicate()
         if verbose or p.returncode:
             sys.stdout.write(out)
         if p.returncode:
-            failed.append(src)
-    if failed:
-        raise RuntimeError("compilation failed for: " + ", ".join(failed))
-    if kernels:
+            failed.add(src)
+    if kernels and failed <= {EXT_SRC}:
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([cc, *ARCH, "-shared", "-Xlinker", "-soname=libgdn.so", "-o", tmp,
                                *objs])
         os.replace(tmp, LIB)
+    if failed:
+        raise RuntimeError("compilation failed for: " + ", ".join(sorted(failed)))
     if ext:
         tmp = EXT + f".tmp{os.getpid()}"
         subprocess.check_call(_ext_link(ext_obj, tmp))

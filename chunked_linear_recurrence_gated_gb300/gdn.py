@@ -424,7 +424,8 @@ def ext():
         load()
         if not os.path.exists(_build.EXT):
             raise RuntimeError(f"_gdn_torch not built ({_build.EXT}); run "
-                               "`python -m chunked_linear_recurrence_gated_gb300.build`")
+                               "`python -m chunked_linear_recurrence_gated_gb300.build` "
+                               "where torch is installed")
         loader = importlib.machinery.ExtensionFileLoader("_gdn_torch", _build.EXT)
         spec = importlib.util.spec_from_loader("_gdn_torch", loader)
         m = importlib.util.module_from_spec(spec)

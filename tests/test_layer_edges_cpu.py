@@ -32,3 +32,35 @@ def test_rows_of_empty_tensors(lib):
         gdn._rows("q", z(4, 8, 16)[:2, :1, ::2], 1)
     with pytest.raises(ValueError):
         gdn._rows("q", z(4, 8, 16)[:2, :3], 1)
+
+
+# ------------------------------------------------------------------------------ build
+@pytest.fixture
+def elsewhere(tmp_path, monkeypatch):
+    """build() into an empty folder, of one small kernel file."""
+    monkeypatch.setattr(build, "OUT", str(tmp_path))
+    for name, file in (("LIB", "libgdn.so"), ("EXT", "_gdn_torch.so"), ("EXT_FOR", "_gdn_torch.for")):
+        monkeypatch.setattr(build, name, str(tmp_path / file))
+    one = [s for s in build.sources() if s.endswith("gdn_noalloc.cu")]
+    monkeypatch.setattr(build, "sources", lambda: one)
+    return tmp_path
+
+
+def test_the_library_builds_without_torch(elsewhere, monkeypatch):
+    found = build.importlib.util.find_spec
+    monkeypatch.setattr(build.importlib.util, "find_spec",
+                        lambda name, *a: None if name == "torch" else found(name, *a))
+    assert build.build() == str(elsewhere / "libgdn.so")
+    assert (elsewhere / "libgdn.so").exists() and not (elsewhere / "_gdn_torch.so").exists()
+    made = (elsewhere / "libgdn.so").stat().st_mtime_ns
+    build.build()
+    assert (elsewhere / "libgdn.so").stat().st_mtime_ns == made
+
+
+def test_the_library_is_linked_when_the_python_entry_does_not_compile(elsewhere, monkeypatch):
+    bad = elsewhere / "bad.cpp"
+    bad.write_text("this is not C++\n")
+    monkeypatch.setattr(build, "EXT_SRC", str(bad))
+    with pytest.raises(RuntimeError, match="bad.cpp"):
+        build.build()
+    assert (elsewhere / "libgdn.so").exists() and not (elsewhere / "_gdn_torch.so").exists()
