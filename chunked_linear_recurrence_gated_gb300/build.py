@@ -68,12 +68,15 @@ def _stale() -> bool:
 
 
 def _ext_stale() -> bool:
-    if _older(EXT, [EXT_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
-        return True
+    return _older(EXT, [EXT_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))) or not ext_fits()
+
+
+def ext_fits() -> bool:
+    """Whether _gdn_torch was built against this Python and torch."""
     if not os.path.exists(EXT_FOR):
-        return True
+        return False
     with open(EXT_FOR) as f:
-        return f.read() != _built_for()
+        return f.read() == _built_for()
 
 
 def _ext_compile(obj: str) -> list:

@@ -426,6 +426,9 @@ def ext():
             raise RuntimeError(f"_gdn_torch not built ({_build.EXT}); run "
                                "`python -m chunked_linear_recurrence_gated_gb300.build` "
                                "where torch is installed")
+        if not _build.ext_fits():
+            raise RuntimeError(f"{_build.EXT} was built for another torch or Python; run "
+                               "`python -m chunked_linear_recurrence_gated_gb300.build` again")
         loader = importlib.machinery.ExtensionFileLoader("_gdn_torch", _build.EXT)
         spec = importlib.util.spec_from_loader("_gdn_torch", loader)
         m = importlib.util.module_from_spec(spec)

@@ -64,3 +64,14 @@ def test_the_library_is_linked_when_the_python_entry_does_not_compile(elsewhere,
     with pytest.raises(RuntimeError, match="bad.cpp"):
         build.build()
     assert (elsewhere / "libgdn.so").exists() and not (elsewhere / "_gdn_torch.so").exists()
+
+
+def test_a_module_of_another_torch_is_not_loaded(lib, tmp_path, monkeypatch):
+    """The module is compiled against torch's headers: another version's tensors have
+    another layout."""
+    other = tmp_path / "for"
+    other.write_text("3.12\n__version__ = '2.0.0'\n")
+    monkeypatch.setattr(build, "EXT_FOR", str(other))
+    monkeypatch.setattr(gdn, "_ext_module", None)
+    with pytest.raises(RuntimeError, match="another torch"):
+        gdn.ext()
