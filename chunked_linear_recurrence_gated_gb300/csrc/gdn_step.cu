@@ -131,8 +131,11 @@ __device__ __forceinline__ void mma_tf32z(float* c, const uint32_t* a, uint32_t 
 // which is the token-by-token rule with the state's updates inside the tile
 // written out, so the state is read and written once per tile. c, p, the dot
 // products and the sum over tokens in the last line are m16n8k8 TF32 MMAs; fp32
-// operands (the state, u, fp32 k and q) are taken as two TF32 parts each, so
-// products are good to about 2^-23. k and q are used as they are in memory; their
+// operands (the state, u, fp32 k and q) are taken as two TF32 parts each, to 2^-23 of
+// themselves, without the product of the second parts: products are good to 2^-21.6
+// (fp32 state off by 1.9e-7 of its 2-norm against 64 bits, about twice what plain fp32
+// is; token by token in fp32 the call below takes 330 us, not 186). k and q are used
+// as they are in memory; their
 // norms scale the results. S^T (16 columns x 8 rows) is read as A fragments with
 // the reduced rows in the order 0 2 4 6 1 3 5 7, in which the fragment is also the
 // accumulator's of the update. The state itself is only ever updated by an fp32

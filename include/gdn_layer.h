@@ -19,8 +19,9 @@
  * -----------
  * - dtype: GDN_DTYPE_F32 or GDN_DTYPE_BF16 of the activations and their
  *   gradients. Parameters (rate, bias, w, ...), their gradients and cached
- *   recurrence states are fp32. Arithmetic, sums and statistics are fp32; a
- *   result is rounded once, when it is stored.
+ *   recurrence states are fp32. Arithmetic, sums and statistics are fp32 (the
+ *   products of gdn_step with several tokens: see there); a result is rounded
+ *   once, when it is stored.
  * - Row strides (ld*) are in elements. "Vector rows" are rows read or written
  *   16 bytes at a time: their pointer must be 16-byte aligned and their stride
  *   a multiple of 16 bytes. Gate inputs (one value per head) need only their
@@ -65,7 +66,8 @@ extern "C" {
  * The cache is read and written in place. A slot written by one sequence must
  * not be read or written by another sequence of the same call. A sequence
  * whose cu_seqlens entries are negative, decreasing or past n_tok is treated
- * as having no tokens; rows that belong to no sequence are not written. */
+ * as having no tokens; rows that belong to no sequence are not written, and of a
+ * row that several claim either's output may be stored. */
 
 typedef struct {
   int N;         /* sequences */
@@ -87,7 +89,15 @@ typedef struct {
  * alpha = e^g. rate and bias NULL: q, k, g, beta are used as they are.
  * Otherwise ([H] fp32 each) they are the inputs of the maps of gdn_prep_fwd,
  * which are applied here. S: cache [n_slots, H, dk, dv] fp32, 16-byte aligned.
- * o [n_tok, H, dv]. q, k, v are vector rows. */
+ * o [n_tok, H, dv]. q, k, v are vector rows.
+ * The tokens of a sequence are taken up to 8 at a time. One token takes fp32
+ * multiply-adds. Several take their products on the tensor cores, each fp32
+ * operand (the state; with GDN_DTYPE_F32 also q and k) as the sum of two TF32
+ * values: an operand is held to 2^-23 of itself, a product is good to 2^-21.6,
+ * sums and the state are fp32. The bits of a result thus depend on how many
+ * tokens a call passes for its sequence, and an infinite operand may come out as
+ * NaN. A token behind the committed ones reaches neither the state nor the
+ * outputs before it, whatever it holds. */
 gdn_status gdn_step(const gdn_step_shape* shape, const void* q, const void* k, const void* v,
                     const void* g, const void* beta, const float* rate, const float* bias,
                     float* S, const int* slot_in, const int* slot_out, const int* cu_seqlens,

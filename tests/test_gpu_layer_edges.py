@@ -4,10 +4,11 @@ import numpy as np
 import pytest
 import torch
 
+import step_precision as sp
 from chunked_linear_recurrence_gated_gb300 import gdn
 from helpers import np64
 from oracle import layer_ops as lo
-from test_gpu_layer_ops import DT, HALF, check, gen
+from test_gpu_layer_ops import DT, HALF, check, gen, i32, ref_step, step_inputs
 from test_gpu_layer_ops import test_res_norm as check_res_norm
 
 pytestmark = pytest.mark.gpu
@@ -143,4 +144,33 @@ def test_res_norm_refuses_another_type_than_it_returns():
         gdn.gdn_res_norm_fwd(h, None, w, y=torch.empty_like(h), dtype=torch.bfloat16)
     assert gdn.gdn_res_norm_fwd(h, x, w, dtype=torch.bfloat16)[1].dtype == torch.bfloat16
     assert gdn.gdn_res_norm_fwd(h, None, w, dtype=torch.bfloat16)[1].dtype == torch.bfloat16
+
+# ------------------------------------------------------- precision of several tokens
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 256), (128, 128), (128, 256)])
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("wide", [False, True])
+def test_step_keeps_fp32(dtype, dk, dv, raw, wide):
+    """States of every call, and outputs of fp32 calls, to the bound of operands in two
+    TF32 parts (step_precision.py; one part is off by several times that). The wider
+    blocks take calls of 466944 columns and more."""
+    H, Hk = (32, 8) if wide else (4, 2)
+    lens = [2, 3, 8, 9, 16, 1, 0, 33] * (-(-466944 // (8 * H * dv)) if wide else 1)
+    q, k, v, g, beta, S, gate, cu = step_inputs(lens, H, Hk, dk, dv, DT[dtype], raw, dk + dv,
+                                                len(lens))
+    S *= 0.1
+    commit = i32([n - i % 3 if n > 2 and i % 2 else n for i, n in enumerate(lens)])
+    o = torch.zeros(q.shape[0], H, dv, dtype=DT[dtype], device="cuda")
+    ro, rS = ref_step(q, k, v, g, beta, S, None, None, cu, commit, gate, dk ** -0.5, o)
+    gdn.gdn_step(q, k, v, g, beta, S, cu_seqlens=cu, n_commit=commit, gate=gate,
+                 q_scale=dk ** -0.5, o=o)
+    torch.cuda.synchronize()
+    S, at = np64(S), cu.tolist()
+    for s, n in enumerate(lens):
+        assert sp.error(S[s], rS[s]) <= sp.bound([n]), (s, n, sp.error(S[s], rS[s]))
+    if dtype == "f32":
+        got, ref = sp.by_head(np64(o), at), sp.by_head(ro, at)
+        ns = [n for n in lens if n for _ in range(H)]
+        off = [sp.error(a, b) / sp.bound([n]) for a, b, n in zip(got, ref, ns)]
+        assert max(off) <= 1.0, max(off)
 

@@ -1,10 +1,13 @@
 """Edges of the layer operators' host side: statuses, refusals, empty calls, builds."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
+import step_precision as sp
 from chunked_linear_recurrence_gated_gb300 import build, gdn
+from oracle import layer_ops as lo
 
 P = ctypes.c_void_p
 FAKE = 1 << 20  # aligned, never dereferenced
@@ -75,3 +78,32 @@ def test_a_module_of_another_torch_is_not_loaded(lib, tmp_path, monkeypatch):
     monkeypatch.setattr(gdn, "_ext_module", None)
     with pytest.raises(RuntimeError, match="another torch"):
         gdn.ext()
+
+
+# -------------------------------------------------- the bound of the step's GPU tests
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_the_step_bound_tells_two_tf32_parts_from_one(bf16, dk, dv):
+    """The tile algorithm with operands in two TF32 parts stays far inside the bound of
+    the GPU tests; with one part per operand every head of every length is outside."""
+    rng = np.random.default_rng(dk + bf16)
+    f32 = lambda *s: rng.standard_normal(s).astype(np.float32)
+    kept = lambda x: torch.from_numpy(x).bfloat16().float().numpy() if bf16 else x
+    unit = lambda x: x / np.linalg.norm(x, axis=-1, keepdims=True)
+    for T in (2, 3, 8, 9, 16, 33):
+        q, k = kept(unit(f32(T, 2, dk))), kept(unit(f32(T, 2, dk)))
+        v, S = kept(f32(T, 2, dv)), 0.1 * f32(1, 2, dk, dv)
+        g, beta = kept(-lo.softplus(f32(T, 2))), kept(lo.sigmoid(f32(T, 2)))
+        args = (q, k, v, g, beta)
+        ro, rS = lo.step(*[x.astype(np.float64) for x in (*args, S)], cu=[0, T])
+        for h in range(2):
+            a = [np.ascontiguousarray(x[:, h]) for x in args]
+            for parts in (1, 2):
+                o, S1 = sp.tiles(*a, S[0, h], parts, bf16)
+                errs = [sp.error(S1[None], rS[0, h][None])]
+                if not bf16:
+                    errs.append(sp.error(o[None], ro[:, h][None]))
+                if parts == 2:
+                    assert max(errs) <= 0.1 * sp.bound([T]), (T, h, errs)
+                else:
+                    assert min(errs) > 2.0 * sp.bound([T]), (T, h, errs)
