@@ -174,3 +174,44 @@ def test_step_keeps_fp32(dtype, dk, dv, raw, wide):
         off = [sp.error(a, b) / sp.bound([n]) for a, b, n in zip(got, ref, ns)]
         assert max(off) <= 1.0, max(off)
 
+# ------------------------------------------------------------------- eps of each call
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("eps", [1e-5, 0.5])
+def test_eps_is_used(dtype, eps):
+    dt, r = DT[dtype], gen(53)
+    f = lambda *ts: [np64(t) for t in ts]
+    for lens in ([1, 1, 1], [3, 9, 2]):
+        q, k, v, g, beta, S, gate, cu = step_inputs(lens, 2, 1, 64, 64, dt, True, 54, 3)
+        q, k = q * 0.05, k * 0.05
+        o = torch.zeros(q.shape[0], 2, 64, dtype=dt, device="cuda")
+        ro, rS = lo.step(*f(q, k, v, g, beta, S), cu=cu.cpu().numpy(), gate=f(*gate), eps=eps)
+        gdn.gdn_step(q, k, v, g, beta, S, cu_seqlens=cu, gate=gate, eps=eps, o=o)
+        check("S", S, rS, 2e-5 * (1 + max(lens)))
+        check("o", o, ro, 2e-5 * (1 + max(lens)))
+    q, k, xg, xb = (r(2, 17, *s, dtype=dt, by=0.05) for s in ((2, 64), (2, 64), (4,), (4,)))
+    rate, bias = r(4, by=0.5), r(4)
+    for name, u, ref in zip(("q", "k"), gdn.gdn_prep_fwd(q, k, xg, xb, rate, bias, 0.3, eps),
+                            lo.prep_fwd(*f(q, k, xg, xb, rate, bias), 0.3, eps)):
+        check(name, u, ref, 1e-5)
+    d = [r(2, 17, *s, dtype=dt) for s in ((4, 64), (4, 64), (4,), (4,))]
+    got = gdn.gdn_prep_bwd(q, k, xg, xb, rate, bias, *d, q_scale=0.3, eps=eps)
+    ref, _ = lo.prep_bwd(*f(q, k, xg, xb, rate, bias, *d), q_scale=0.3, eps=eps)
+    for name, u, v in zip(("dq", "dk"), got, ref):
+        check(name, u, v, 5e-5)
+    o, z, dy, w = r(2, 17, 2, 64, dtype=dt, by=0.05), r(2, 17, 2, 64, dtype=dt), r(2, 17, 2, 64, dtype=dt), r(64)
+    check("y", gdn.gdn_gate_norm_fwd(o, z, w, eps=eps), lo.gate_norm_fwd(*f(o, z, w), eps=eps), 1e-5)
+    got = gdn.gdn_gate_norm_bwd(o, z, w, dy, eps=eps)
+    ref, _ = lo.gate_norm_bwd(*f(o, z, w, dy), eps=eps)
+    for name, u, v in zip(("do", "dz"), got, ref):
+        check(name, u, v, 5e-5)
+    for C in (128, 8200):
+        h, x, dy, dh = (r(9, C, dtype=dt, by=b) for b in (0.05, 0.05, 1.0, 1.0))
+        w, wp, sc = 1.0 + r(C, by=0.2), 1.0 + r(C, by=0.2), 0.5 + r(C, by=0.1)
+        got = gdn.gdn_res_norm_fwd(h, x, w, wp, sc, eps)
+        for name, u, v in zip(("h", "y"), got, lo.res_norm_fwd(*f(h, x, w, wp, sc), eps)):
+            check(name, u, v, 1e-5)
+        got = gdn.gdn_res_norm_bwd(h, x, w, dy, dh, wp, sc, eps)
+        ref, _ = lo.res_norm_bwd(*f(h, x, w, dy, dh, wp, sc), eps)
+        for name, u, v in zip(("dh", "dx"), got, ref):
+            check(name, u, v, 5e-5)
+    torch.cuda.synchronize()
