@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(GN_NT)
 // columns, part[block] = the block's sum. The elementwise arithmetic is in pairs:
 // the instructions of an element (sigmoid and its derivative among them) come
 // close to the memory's time. Bound by the bytes of o, z, dy, do and dz: 16411 x 16
-// rows of 256 bf16 values 105 us (672 MB, 6.4 TB/s; 110 with unpaired arithmetic,
+// rows of 256 bf16 values 106 us (672 MB, 6.3 TB/s; 110 with unpaired arithmetic,
 // 126 with the next rows in flight through shared memory).
 template <typename T, int L>
 __global__ void __launch_bounds__(GN_NT, gate_blocks<T>())
@@ -325,7 +325,7 @@ template <int K, int CL, int AHEAD>
 struct TeamSum {
   static constexpr int N4 = K > 4 ? 2 : 1;  // float4 per CTA's sums
   // 2 AHEAD + 2, and a third where two would do (forward, 5000 rows of 16384 bf16
-  // columns: 115 us with three, 133 with two)
+  // columns: 112 us with three, 130 with two)
   static constexpr int BUFS = AHEAD > 0 ? 2 * AHEAD + 2 : 3;
   float* warps;    // [BUFS][RN_SLOT] the warps' sums (unused ones stay 0)
   float4* ctas;    // [BUFS][CL][N4] the CTAs' sums
@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(DIAG_NT) k_exchange(int silent, long long limi
 // With rx = 1 / sqrt(mean x^2 + eps) (1 without w_post) and r the same of h':
 //   h' = h + scale w_post rx x,   y = r w h'.
 // In a cluster the sum of the next row's x^2 goes with the row's own sum of h'^2,
-// one exchange a row instead of two (5000 rows of 16384 bf16 columns 165 -> 115 us).
+// one exchange a row instead of two (5000 rows of 16384 bf16 columns 165 -> 115 us,
+// 112 as it is now).
 // Bound by the bytes of h, x, h_out and y: 20011 rows of 4096 columns, fp32 stream
 // and bf16 branch, both norms: 151 us (984 MB, 6.5 TB/s); one row per block with
 // plain loads took 305.
@@ -607,13 +608,15 @@ __global__ void __launch_bounds__(1024, 1)
 // and mean(sp dh m) is a combination of sums that do not need dh, so a row takes
 // one reduction, of 6 sums. In a cluster the next row's sums are formed and posted
 // before this row's are collected, so that the exchange's latency passes behind a
-// row's work (4000 rows of 16384 bf16 columns 369 -> 320 us, 177 since with as many
-// clusters as fit, and 191 two rows ahead); within a CTA reading the row twice for
+// row's work (4000 rows of 16384 bf16 columns 369 -> 320 us, 177 with as many clusters
+// as fit and then 191 two rows ahead; 169 as it is now); within a CTA reading the row twice for
 // that costs more than it hides (32768 rows of 2048: 135 us against 127). Bound by
 // the bytes of h, dh_out, dy, x, dh and dx: 32768 rows of 2048 bf16 columns, both
-// norms, 123 us (805 MB, 6.5 TB/s); bf16 rows of 16384 columns by the instructions of
-// the 16 warps that the registers leave an SM (as many fp32 values: 94 % of the
-// bytes' time).
+// norms, 124 us (805 MB, 6.5 TB/s). bf16 rows in clusters are bound by no one counter:
+// the 16 warps that the registers leave an SM issue in 62 % of the cycles at 5120 and
+// 16384 columns, DRAM at 60 % of its peak, the warps waiting in turn on fixed latencies,
+// shared memory, the barrier and the exchange (as many fp32 values take 92 % of the
+// bytes' time: theirs is twice as long).
 template <typename T, typename R, int CL>
 __global__ void __launch_bounds__(512, 1)
     k_res_norm_bwd(int rows, int C, float inv_C, float eps, const R* h, const T* x, const float* w,
@@ -821,8 +824,8 @@ gdn_status check_res(const gdn_res_norm_shape* s) {
 }
 
 // SMs that clusters can fill: of 4 CTAs of an SM each 36 fit, not 38, and two more
-// than fit would run after the others (of 8, three CTAs to an SM, 51, not 54: 5000 rows
-// of 10240 bf16 columns 150 us, with 54 231).
+// than fit would run after the others (4000 rows of 16384 bf16 columns 169 us, with 38
+// 305; of 8, three CTAs to an SM, 51, not 54: 5000 rows of 10240 columns 144, with 54 213).
 int cluster_sms(int cl) { return cl == 8 ? 136 : cl == 4 ? 144 : RN_SMS; }
 
 // How a call's rows are laid out over CTAs; a function of the shape alone, so
@@ -842,7 +845,7 @@ ResPlan res_plan(int C, bool bwd) {
   p.cl = 1;
   while (C > p.cl * cols) p.cl *= 2;
   // smaller CTAs where they fill the SMs better (backward, 16000 rows of 5120 bf16
-  // columns: 249 us in clusters of 2, 203 in 4; 5000 of 10240: 170 in 4, 150 in 8);
+  // columns: 234 us in clusters of 2, 196 in 4; 5000 of 10240: 164 in 4, 144 in 8);
   // not where one CTA holds a row (20000 of 2560: 120 either way, mixed 124 and 127)
   if (bwd && p.cl > 1 && 10 * filled(2 * p.cl) > 11 * filled(p.cl)) p.cl *= 2;
   p.team = team(p.cl);

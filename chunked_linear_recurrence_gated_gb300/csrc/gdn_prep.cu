@@ -134,8 +134,8 @@ __device__ __forceinline__ void prep_bwd_gates(int blk, int rows, int H, int hp_
 //   dx = r (d - r^2 (x . d) x)   (times q_scale for q).
 // The first gate_blocks blocks take the gates (their loops over tokens are the
 // longest), the others rows as k_prep_fwd. Bound by the bytes of q, k and the
-// gradients: 32768 tokens of 16 heads of 128 bf16 values 116 us (812 MB, 7.0 TB/s);
-// 8193 of 24 value on 8 key heads, of 128, 30 us (170 MB, 5.6 TB/s: a sixth of it
+// gradients: 32768 tokens of 16 heads of 128 bf16 values 117 us (812 MB, 6.9 TB/s);
+// 8193 of 24 value on 8 key heads, of 128, 31 us (170 MB, 5.5 TB/s: a sixth of it
 // is the column sums and the launches).
 template <typename T, int DK, bool SHARED>
 __global__ void __launch_bounds__(PR_NT)

@@ -50,8 +50,10 @@ constexpr int ST_WIDE_COLS = 8 * 152 * 6 * 64;  // columns of a call for blocks 
 // Blocks that an SM has to have registers for: with dk 128 what its shared memory
 // holds (for 12 of 2 warps, 80 registers instead of 96: 16 tokens of one sequence
 // 7.6 us instead of 7.2). Half the state leaves room for more: 512 sequences of 32
-// heads of 64 x 64, one token, 84 us with 8 blocks of 4 warps, 90 with 6; small fp32
-// calls lose by it (93 sequences of 6 heads of 64 x 64: 5.6 us with 10, 5.9 with 12).
+// heads of 64 x 64, one token, 84 us with 8 blocks of 4 warps, 90 with 6 (at 64
+// registers these kernels spill 64 to 84 bytes; calls of several tokens have not been
+// timed with 6); small fp32 calls lose by it (93 sequences of 6 heads of 64 x 64:
+// 5.6 us with 10, 5.9 with 12).
 constexpr int step_blocks(int warps, int dk, bool bf16) {
   return warps == 4 ? (dk == 64 ? 8 : 6) : dk == 64 && bf16 ? 12 : 10;
 }
@@ -135,8 +137,7 @@ __device__ __forceinline__ void mma_tf32z(float* c, const uint32_t* a, uint32_t 
 // themselves, without the product of the second parts: products are good to 2^-21.6
 // (fp32 state off by 1.9e-7 of its 2-norm against 64 bits, about twice what plain fp32
 // is; token by token in fp32 the call below takes 330 us, not 186). k and q are used
-// as they are in memory; their
-// norms scale the results. S^T (16 columns x 8 rows) is read as A fragments with
+// as they are in memory; their norms scale the results. S^T (16 columns x 8 rows) is read as A fragments with
 // the reduced rows in the order 0 2 4 6 1 3 5 7, in which the fragment is also the
 // accumulator's of the update. The state itself is only ever updated by an fp32
 // multiply-add (the tensor core's own accumulation would truncate). The sums over

@@ -46,8 +46,9 @@
  * -----------------------
  * The caller owns every buffer, including the workspace (size from the
  * *_workspace_bytes functions). The library allocates no device memory and
- * keeps no state between calls other than per-device kernel attributes (and
- * the fixed scratch array of gdn_chunk_fwd_noalloc, below).
+ * keeps no state between calls other than per-device kernel attributes, the
+ * fixed scratch array of gdn_chunk_fwd_noalloc (below) and the status word of
+ * the layer operators (gdn_layer.h).
  * All work is enqueued on `stream` (a cudaStream_t passed as void*, NULL =
  * the legacy default stream); calls return without synchronising. S_out may
  * alias S_in and dS_in may alias dS_out. Other outputs must not alias
