@@ -202,6 +202,10 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaSt
 cudaError_t col_sum(const float* part, int np, int n, int C, float* o0, float* o1, float* o2,
                     cudaStream_t st);
 
+// Most rows, sequences or channels where a thread's next ones are int indices: they lie
+// less than this margin past its present ones (at most 4 x 4864 rows).
+constexpr int MOST_INDEX = 0x7fffffff - (1 << 16);
+
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 inline size_t elem_size(int dtype) { return dtype == GDN_DTYPE_BF16 ? 2 : 4; }
 inline bool dtype_ok(int d) { return d == GDN_DTYPE_F32 || d == GDN_DTYPE_BF16; }

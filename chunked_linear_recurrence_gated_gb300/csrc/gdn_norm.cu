@@ -817,7 +817,8 @@ cudaError_t dispatch_gate(const gdn_gate_norm_shape& s, const void* o, const voi
 
 gdn_status check_res(const gdn_res_norm_shape* s) {
   if (!s || s->rows < 0 || s->C < 1 || !(s->eps > 0.f)) return GDN_ERR_INVALID_ARG;
-  if (!dtype_ok(s->dtype) || !dtype_ok(s->res_dtype) || s->C % 8 || s->C > 16384)
+  if (!dtype_ok(s->dtype) || !dtype_ok(s->res_dtype) || s->C % 8 || s->C > 16384 ||
+      s->rows > MOST_INDEX)
     return GDN_ERR_UNSUPPORTED;
   if (s->res_dtype != s->dtype && s->res_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;

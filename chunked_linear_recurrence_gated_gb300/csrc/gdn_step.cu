@@ -731,7 +731,9 @@ gdn_status gdn_conv_step(const gdn_conv_step_shape* shape, const void* x, const 
   if (e != GDN_OK) return e;
   if (s.C < 1 || (s.act != GDN_CONV_ACT_NONE && s.act != GDN_CONV_ACT_SILU))
     return GDN_ERR_INVALID_ARG;
-  if (!dtype_ok(s.dtype) || s.W < 2 || s.W > 8 || s.C % 4) return GDN_ERR_UNSUPPORTED;
+  if (!dtype_ok(s.dtype) || s.W < 2 || s.W > 8 || s.C % 4 || s.C > MOST_INDEX ||
+      s.N > MOST_INDEX)
+    return GDN_ERR_UNSUPPORTED;
   if ((s.n_tok > 0 && (!x || !y)) || !w || (s.n_slots > 0 && !state)) return GDN_ERR_INVALID_ARG;
   const size_t es = elem_size(s.dtype);
   if (!aligned(x, 4 * es) || s.ldx < 0 || s.ldx % 4 || !aligned(y, 16) || !aligned(state, 16) ||

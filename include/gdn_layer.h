@@ -27,6 +27,9 @@
  *   a multiple of 16 bytes. Gate inputs (one value per head) need only their
  *   type's alignment. Tensors without a stride are contiguous.
  * - Outputs must not alias inputs except where it is said that they may.
+ * - Counts of rows, sequences and channels that pass what the kernels' 32-bit
+ *   indices hold (2^31 - 2^16 of any; gdn_step 2^28 sequences x heads; prep and
+ *   the gated norm 2^30 and 2^31 rows x heads) are GDN_ERR_UNSUPPORTED.
  * - Ownership, execution and errors as in gdn.h: caller-owned buffers, work
  *   enqueued on `stream` without synchronising, every argument checked on the
  *   host before any launch, GDN_ERR_CUDA if a launch fails. Calls with nothing

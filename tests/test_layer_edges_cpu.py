@@ -107,3 +107,25 @@ def test_the_step_bound_tells_two_tf32_parts_from_one(bf16, dk, dv):
                     assert max(errs) <= 0.1 * sp.bound([T]), (T, h, errs)
                 else:
                     assert min(errs) > 2.0 * sp.bound([T]), (T, h, errs)
+
+
+# ------------------------------------------------------------------ the end of int
+def refused(status):
+    """The status of a call whose sizes are refused on the host. (Without that check it
+    would try to launch, which fails here where there is no GPU.)"""
+    return status == 2
+
+
+@pytest.mark.parametrize("rows", [2 ** 31 - 1, 2 ** 31 - 2 ** 14])
+def test_sizes_whose_row_indices_would_wrap_are_refused(lib, rows):
+    """A thread's next rows, sequences and channels are 32-bit numbers a few thousand
+    past its present ones."""
+    at = lambda n, ws=None: [P(FAKE)] * n + ([P(FAKE), 1 << 40] if ws else []) + [None]
+    s = gdn.gdn_res_norm_shape(rows, 8, 1, 1, 1e-6)
+    assert lib.gdn_res_norm_workspace_bytes(s) == 0
+    assert refused(lib.gdn_res_norm_fwd(s, *at(7)))
+    assert refused(lib.gdn_res_norm_bwd(s, *at(12, True)))
+    conv = lambda N, C: gdn.gdn_conv_step_shape(N, 0, N, C, 4, 1, 1, C)
+    assert refused(lib.gdn_conv_step(conv(rows, 64), *at(9)))
+    assert refused(lib.gdn_conv_step(conv(1, rows // 4 * 4), *at(9)))
+    assert not refused(lib.gdn_conv_step(conv(0, 64), *at(9)))
