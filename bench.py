@@ -133,7 +133,7 @@ def kernel_model(name, dk, dv, esz=2, C=64):
     return by, fl
 
 
-# The layer operators' kernels (include/gdn_layer.h), per 64 tokens of a head;
+# The layer operators' kernels (include/gdn_layer.h, gdn_lin.h), per 64 tokens of a head;
 # none of them runs in this benchmark's workloads. The norms' rows: dv columns.
 LAYER_KERNELS = {
     "step": lambda dk, dv, e, C: (C * (8 * dk * dv + (2 * dk + 2 * dv + 2) * e), 8 * C * dk * dv),
@@ -146,6 +146,17 @@ LAYER_KERNELS = {
     "res_norm_fwd": lambda dk, dv, e, C: (4 * C * dv * e, 8 * C * dv),
     "res_norm_bwd": lambda dk, dv, e, C: (6 * C * dv * e, 24 * C * dv),
     "layer_col_sum": lambda dk, dv, e, C: (4 * dv, dv),
+    "qk_norm_fwd": lambda dk, dv, e, C: (4 * C * dk * e, 20 * C * dk),
+    "qk_norm_bwd": lambda dk, dv, e, C: (6 * C * dk * e, 36 * C * dk),
+    "lin_step": lambda dk, dv, e, C: (C * (8 * dk * dv + (2 * dk + 2 * dv + 1) * e),
+                                      5 * C * dk * dv),
+    "lin_plan": lambda dk, dv, e, C: (8, 4),
+    "lin_sum": lambda dk, dv, e, C: (C * (dk + dv + 1) * e + 4 * dk * dv, 2 * C * dk * dv),
+    "lin_scan": lambda dk, dv, e, C: (8 * dk * dv, 2 * dk * dv),
+    "lin_out": lambda dk, dv, e, C: (C * (2 * dk + 2 * dv + 1) * e + 4 * dk * dv,
+                                     2 * C * dk * dv + 2 * C * C * (dk + dv)),
+    "lin_grad": lambda dk, dv, e, C: (C * (4 * dk + 3 * dv + 2) * e + 8 * dk * dv,
+                                      6 * C * dk * dv + 2 * C * C * (3 * dk + 2 * dv)),
 }
 
 
@@ -594,7 +605,8 @@ def op_roofline(w, ms, which="fwd+bwd"):
 # that phase's algorithmic bytes for the token-heads it processes.
 KERNEL_PHASE = {"tc_grad": "bwd", "simt_grad": "bwd", "tc_chains_bwd": "bwd",
                 "tc_chain_rev": "bwd", "simt_st_bwd": "bwd",
-                "prep_bwd": "bwd", "gate_norm_bwd": "bwd", "res_norm_bwd": "bwd"}
+                "prep_bwd": "bwd", "gate_norm_bwd": "bwd", "res_norm_bwd": "bwd",
+                "qk_norm_bwd": "bwd", "lin_grad": "bwd"}
 
 
 def kernel_roofline(name, per_launch_ms, units_per_launch, w, hbm, peak_kind):

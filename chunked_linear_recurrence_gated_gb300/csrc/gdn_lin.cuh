@@ -1,0 +1,79 @@
+// Shared pieces of linear attention over whole sequences (include/gdn_lin.h): the
+// units of tokens that the kernels work on, and the workspace.
+#pragma once
+
+#include "../../include/gdn_lin.h"
+#include "gdn_layer.cuh"
+
+namespace gdn {
+
+// Units of `unit` tokens, anchored at the start of every sequence. Fixed-length
+// calls: `per` units for each of the nseq sequences of T rows; packed ones: the
+// tables that k_lin_plan wrote.
+struct LinMap {
+  const int* cu;     // packed: DEVICE cu_seqlens; fixed: nullptr
+  const int* first;  // packed: first unit of each sequence [nseq + 1]
+  const int* owner;  // packed: sequence of each unit [cap] (-1: none)
+  int nseq, T, unit, per, cap;
+};
+struct LinUnit {
+  int seq, row, len;  // its sequence, first row and tokens
+  int at, n;          // its index in the sequence and the sequence's units
+};
+__device__ __forceinline__ bool lin_unit(const LinMap& m, int i, LinUnit& u) {
+  int t0, t1;
+  if (!m.cu) {
+    u.seq = i / m.per;
+    u.at = i - u.seq * m.per;
+    u.n = m.per;
+    t0 = u.seq * m.T;
+    t1 = t0 + m.T;
+  } else {
+    u.seq = m.owner[i];
+    if (u.seq < 0) return false;
+    const int f = m.first[u.seq];
+    u.at = i - f;
+    u.n = m.first[u.seq + 1] - f;
+    t0 = m.cu[u.seq];
+    t1 = m.cu[u.seq + 1];
+  }
+  u.row = t0 + u.at * m.unit;
+  u.len = min(m.unit, t1 - u.row);
+  return true;
+}
+// First unit and number of units of a sequence.
+__device__ __forceinline__ void lin_seq(const LinMap& m, int s, int& first, int& n) {
+  first = m.cu ? m.first[s] : s * m.per;
+  n = m.cu ? m.first[s + 1] - first : m.per;
+}
+
+// A log-decay of a token. Below -1e4 every factor is 0 all the same, and sums of
+// the clamped values stay finite where those of -inf would give NaN differences.
+__device__ __forceinline__ float lin_decay(float g) { return g < -1e4f ? -1e4f : g; }
+
+// What a whole call takes.
+struct LinCall {
+  gdn_lin_shape s;
+  const void *q, *k, *v, *g;
+  const float* decay;
+  const float* S_in;
+  const int* cu;
+  void* o;
+  float* S_out;
+  // backward
+  const void* dout;
+  const float* dS_out;
+  void *dq, *dk, *dv, *dg;
+  float *ddecay, *dS_in;
+  unsigned char* ws;
+  cudaStream_t st;
+};
+
+// Writes the tables of a packed call; the status word: DEV_OK or DEV_BAD_CU_SEQLENS.
+cudaError_t lin_plan(const LinMap& m, int* first, int* owner, int* status, cudaStream_t st);
+
+// fp32 kernels (gdn_lin.cu).
+size_t lin_simt_bytes(const gdn_lin_shape& s, bool packed, bool back);
+cudaError_t lin_simt(const LinCall& c, bool back);
+
+}  // namespace gdn

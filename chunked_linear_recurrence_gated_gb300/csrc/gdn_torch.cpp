@@ -1,4 +1,4 @@
-// Python entry of the layer operators (include/gdn_layer.h) for torch tensors:
+// Python entry of the layer operators (include/gdn_layer.h, gdn_lin.h) for torch tensors:
 // argument checks, output and workspace allocation, the call into the C ABI on
 // the current stream of the tensors' device. Host code only. A generation step
 // makes these calls once per layer and token, and on the Grace host a dozen
@@ -20,6 +20,7 @@
 
 #include "gdn_conv.h"
 #include "gdn_layer.h"
+#include "gdn_lin.h"
 
 namespace {
 
@@ -429,6 +430,197 @@ PyObject* res_norm_bwd(PyObject* const* a) {
   return tuple_of({&dh, &dx, &dw, &dpost, &dscale});
 }
 
+// A log-decay: g [.., H] of the activations' type with strided rows, or one fp32
+// value for each head.
+struct Decay {
+  const void* g;
+  const float* decay;
+  long long ld;
+};
+Decay decay_of(const Tensor& g, at::IntArrayRef sizes, at::ScalarType type, int dev) {
+  if (g.dim() == 1 && sizes.size() > 1)
+    return {nullptr, (const float*)ptr("g", g, {sizes.back()}, at::kFloat, dev), 0};
+  const long long ld = rows_of("g", g, sizes, 1, type, dev);
+  return {g.data_ptr(), nullptr, ld};
+}
+
+// q k v g S slot_in slot_out cu_seqlens n_commit scale o
+PyObject* lin_step(PyObject* const* a) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
+               &g = tensor(a[3], "g"), &S = tensor(a[4], "S");
+  const int dev = on_gpu("q", q, 3);
+  on_gpu("v", v, 3);
+  on_gpu("S", S, 4);
+  const auto type = q.scalar_type();
+  const int64_t n = q.size(0), Hk = q.size(1), dk = q.size(2), H = v.size(1), dv = v.size(2);
+  gdn_lin_step_shape s = {};
+  s.ldk = rows_of("k", k, {n, Hk, dk}, 2, type, dev);
+  s.ldv = rows_of("v", v, {n, H, dv}, 2, type, dev);
+  s.ldq = rows("q", q, 2);
+  const Decay d = decay_of(g, {n, H}, type, dev);
+  s.ldg = d.ld;
+  const Indices ix = indices(a + 5, n, dev);
+  s.N = narrow_int(ix.N), s.n_tok = narrow_int(n), s.n_slots = narrow_int(S.size(0));
+  s.H = narrow_int(H), s.Hk = narrow_int(Hk), s.dk = narrow_int(dk), s.dv = narrow_int(dv);
+  s.dtype = dtype_code(type), s.scale = number(a[9]);
+  void* pS = ptr("S", S, {S.size(0), H, dk, dv}, at::kFloat, dev);
+  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+  const Tensor* given = optional(a[10], "o");
+  const Tensor o = given ? *given : at::empty({n, H, dv}, q.options());
+  check(gdn_lin_step(&s, q.data_ptr(), k.data_ptr(), v.data_ptr(), d.g, d.decay, (float*)pS,
+                     ix.slot_in, ix.slot_out, ix.cu, ix.commit,
+                     ptr("o", o, {n, H, dv}, type, dev), stream_of(dev)),
+        "gdn_lin_step");
+  return THPVariable_Wrap(o);
+}
+
+struct Lin {
+  gdn_lin_shape s;
+  int dev;
+  int64_t B, T, H, dk, dv;
+  at::ScalarType type;
+  Decay d;
+  const float* S_in;
+  const int* cu;
+};
+// q k v g S_in, and at `at` scale cu_seqlens
+Lin lin_args(PyObject* const* a, int at) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
+               *cu = optional(a[at + 1], "cu_seqlens");
+  Lin p = {};
+  p.dev = on_gpu("q", q, 4);
+  on_gpu("v", v, 4);
+  p.type = q.scalar_type();
+  p.B = q.size(0), p.T = q.size(1), p.H = q.size(2), p.dk = q.size(3), p.dv = v.size(3);
+  if (cu && p.B != 1) throw BadValue("q: packed sequences have a batch of 1, got " + described(q));
+  const int64_t nseq = cu ? cu->numel() - 1 : p.B;
+  p.s.ldk = rows_of("k", k, q.sizes(), 2, p.type, p.dev);
+  p.s.ldv = rows_of("v", v, {p.B, p.T, p.H, p.dv}, 2, p.type, p.dev);
+  p.s.ldq = rows("q", q, 2);
+  p.d = decay_of(tensor(a[3], "g"), {p.B, p.T, p.H}, p.type, p.dev);
+  p.s.ldg = p.d.ld;
+  p.s.B = narrow_int(p.B), p.s.T = narrow_int(p.T), p.s.H = narrow_int(p.H);
+  p.s.dk = narrow_int(p.dk), p.s.dv = narrow_int(p.dv), p.s.nseq = narrow_int(nseq);
+  p.s.dtype = dtype_code(p.type), p.s.scale = number(a[at]);
+  p.cu = (const int*)ptr("cu_seqlens", cu, {nseq + 1}, at::kInt, p.dev);
+  p.S_in = (const float*)ptr("S_in", optional(a[4], "S_in"), {nseq, p.H, p.dk, p.dv}, at::kFloat,
+                             p.dev);
+  return p;
+}
+
+// q k v g S_in scale cu_seqlens o S_out want_state workspace
+PyObject* lin_fwd(PyObject* const* a) {
+  const Lin p = lin_args(a, 5);
+  const Tensor &q = tensor(a[0], "q"), *oo = optional(a[7], "o"), *so = optional(a[8], "S_out");
+  const Sizes states = {p.s.nseq, p.H, p.dk, p.dv}, values = {p.B, p.T, p.H, p.dv};
+  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.dev);
+  const Tensor ws = scratch(optional(a[10], "workspace"), gdn_lin_workspace_bytes(&p.s, 0), q, p.dev);
+  const Tensor o = oo ? *oo : at::empty(at::IntArrayRef(values), q.options());
+  const Tensor S = so             ? *so
+                   : choice(a[9]) ? at::empty(at::IntArrayRef(states), q.options().dtype(at::kFloat))
+                                  : Tensor();
+  check(gdn_lin_fwd(&p.s, q.data_ptr(), tensor(a[1], "k").data_ptr(), tensor(a[2], "v").data_ptr(),
+                    p.d.g, p.d.decay, p.S_in, p.cu, ptr("o", o, values, p.type, p.dev),
+                    (float*)ptr("S_out", S.defined() ? &S : nullptr, states, at::kFloat, p.dev),
+                    ws.data_ptr(), ws.nbytes(), stream_of(p.dev)),
+        "gdn_lin_fwd");
+  return tuple_of({&o, &S});
+}
+
+// q k v g S_in dout dS_out scale cu_seqlens want_state workspace
+PyObject* lin_bwd(PyObject* const* a) {
+  const Lin p = lin_args(a, 7);
+  const Tensor &q = tensor(a[0], "q"), &v = tensor(a[2], "v");
+  const Sizes states = {p.s.nseq, p.H, p.dk, p.dv}, values = {p.B, p.T, p.H, p.dv};
+  const void* dout = ptr("dout", tensor(a[5], "dout"), values, p.type, p.dev);
+  const float* dSo =
+      (const float*)ptr("dS_out", optional(a[6], "dS_out"), states, at::kFloat, p.dev);
+  const auto opt = q.options(), fopt = opt.dtype(at::kFloat);
+  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.dev);
+  const Tensor ws = scratch(optional(a[10], "workspace"), gdn_lin_workspace_bytes(&p.s, 1), q, p.dev);
+  const Tensor dq = at::empty(q.sizes(), opt), dk = at::empty(q.sizes(), opt),
+               dv = at::empty(v.sizes(), opt),
+               dg = p.d.decay ? at::empty({p.H}, fopt) : at::empty({p.B, p.T, p.H}, opt);
+  const Tensor dS = choice(a[9]) ? at::empty(at::IntArrayRef(states), fopt) : Tensor();
+  check(gdn_lin_bwd(&p.s, q.data_ptr(), tensor(a[1], "k").data_ptr(), v.data_ptr(), p.d.g,
+                    p.d.decay, p.S_in, p.cu, dout, dSo, dq.data_ptr(), dk.data_ptr(),
+                    dv.data_ptr(), p.d.decay ? nullptr : dg.data_ptr(),
+                    p.d.decay ? (float*)dg.data_ptr() : nullptr,
+                    dS.defined() ? (float*)dS.data_ptr() : nullptr, ws.data_ptr(), ws.nbytes(),
+                    stream_of(p.dev)),
+        "gdn_lin_bwd");
+  return tuple_of({&dq, &dk, &dv, &dg, &dS});
+}
+
+struct Qk {
+  gdn_qk_norm_shape s;
+  int dev;
+  int64_t B, T, d;
+  const void *q, *k;
+  const float *wq, *wk;
+  const double* freq;
+  const int* pos;
+};
+// q k wq wk inv_freq, and at `at` pos H style q_scale eps (H 0: heads as they are)
+Qk qk_args(PyObject* const* a, int at) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), *f = optional(a[4], "inv_freq");
+  Qk p = {};
+  p.dev = on_gpu("q", q, 4);
+  on_gpu("k", k, 4);
+  const auto type = q.scalar_type();
+  p.B = q.size(0), p.T = q.size(1), p.d = q.size(3);
+  p.s.ldk = rows_of("k", k, {p.B, p.T, k.size(2), p.d}, 2, type, p.dev);
+  p.s.ldq = rows("q", q, 2);
+  p.s.rows = narrow_int(p.B * p.T), p.s.T = narrow_int(std::max<int64_t>(p.T, 1));
+  p.s.Hq = narrow_int(q.size(2)), p.s.Hk = narrow_int(k.size(2)), p.s.H = choice(a[at + 1]);
+  p.s.d = narrow_int(p.d), p.s.rot = f ? narrow_int(2 * f->numel()) : 0;
+  p.s.style = choice(a[at + 2]), p.s.dtype = dtype_code(type);
+  p.s.q_scale = number(a[at + 3]), p.s.eps = number(a[at + 4]);
+  p.q = q.data_ptr(), p.k = k.data_ptr();
+  p.wq = (const float*)ptr("wq", optional(a[2], "wq"), {p.d}, at::kFloat, p.dev);
+  p.wk = (const float*)ptr("wk", optional(a[3], "wk"), {p.d}, at::kFloat, p.dev);
+  if (f) p.freq = (const double*)ptr("inv_freq", *f, {f->numel()}, at::kDouble, p.dev);
+  p.pos = (const int*)ptr("pos", optional(a[at], "pos"), {p.B, p.T}, at::kInt, p.dev);
+  if (p.s.H < 0 || (p.s.H && (!p.s.Hq || !p.s.Hk || p.s.H % p.s.Hq || p.s.H % p.s.Hk)))
+    throw BadValue("H: a multiple of the heads of q and of k is expected, got " +
+                   std::to_string(p.s.H));
+  return p;
+}
+
+// q k wq wk inv_freq pos H style q_scale eps
+PyObject* qk_norm_fwd(PyObject* const* a) {
+  const Qk p = qk_args(a, 5);
+  const auto opt = tensor(a[0], "q").options();
+  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.dev);
+  const Tensor qn = at::empty({p.B, p.T, p.s.H ? p.s.H : p.s.Hq, p.d}, opt),
+               kn = at::empty({p.B, p.T, p.s.H ? p.s.H : p.s.Hk, p.d}, opt);
+  check(gdn_qk_norm_fwd(&p.s, p.q, p.k, p.wq, p.wk, p.freq, p.pos, qn.data_ptr(), kn.data_ptr(),
+                        stream_of(p.dev)),
+        "gdn_qk_norm_fwd");
+  return tuple_of({&qn, &kn});
+}
+
+// q k wq wk inv_freq dqn dkn pos H style q_scale eps workspace
+PyObject* qk_norm_bwd(PyObject* const* a) {
+  const Qk p = qk_args(a, 7);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+  const auto opt = q.options(), fopt = opt.dtype(at::kFloat);
+  const auto type = q.scalar_type();
+  const void* dqn = ptr("dqn", tensor(a[5], "dqn"), {p.B, p.T, p.s.H ? p.s.H : p.s.Hq, p.d}, type, p.dev);
+  const void* dkn = ptr("dkn", tensor(a[6], "dkn"), {p.B, p.T, p.s.H ? p.s.H : p.s.Hk, p.d}, type, p.dev);
+  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.dev);
+  const Tensor ws = scratch(optional(a[12], "workspace"), gdn_qk_norm_workspace_bytes(&p.s), q, p.dev);
+  const Tensor dq = at::empty(q.sizes(), opt), dk = at::empty(k.sizes(), opt);
+  const Tensor dwq = p.wq ? at::empty({p.d}, fopt) : Tensor(),
+               dwk = p.wk ? at::empty({p.d}, fopt) : Tensor();
+  check(gdn_qk_norm_bwd(&p.s, p.q, p.k, p.wq, p.wk, p.freq, p.pos, dqn, dkn, dq.data_ptr(),
+                        dk.data_ptr(), p.wq ? (float*)dwq.data_ptr() : nullptr,
+                        p.wk ? (float*)dwk.data_ptr() : nullptr, ws.data_ptr(), ws.nbytes(),
+                        stream_of(p.dev)),
+        "gdn_qk_norm_bwd");
+  return tuple_of({&dq, &dk, &dwq, &dwk});
+}
+
 // name t inner
 PyObject* row_stride(PyObject* const* a) {
   const char* name = PyUnicode_AsUTF8(a[0]);
@@ -478,6 +670,11 @@ PyMethodDef methods[] = {ENTRY(step, 15),
                          ENTRY(gate_norm_bwd, 7),
                          ENTRY(res_norm_fwd, 9),
                          ENTRY(res_norm_bwd, 10),
+                         ENTRY(lin_step, 11),
+                         ENTRY(lin_fwd, 11),
+                         ENTRY(lin_bwd, 11),
+                         ENTRY(qk_norm_fwd, 10),
+                         ENTRY(qk_norm_bwd, 13),
                          ENTRY(row_stride, 3),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -6,7 +6,7 @@ only turns torch tensors into pointers, allocates outputs and the workspace on
 the caller's behalf (torch owns that memory), and raises on a non-OK status.
 Both must have been built (``build.py``); there is no fallback.
 
-The function names follow the C ABI in include/gdn.h, gdn_conv.h and gdn_layer.h.
+The function names follow the C ABI in include/gdn.h, gdn_conv.h, gdn_layer.h and gdn_lin.h.
 """
 from __future__ import annotations
 
@@ -39,8 +39,12 @@ CONV_ACT = {"none": 0, "silu": 1}
 LAYER_EXPORTS = ["gdn_step", "gdn_conv_step", "gdn_prep_fwd", "gdn_prep_bwd",
                  "gdn_prep_workspace_bytes", "gdn_gate_norm_fwd", "gdn_gate_norm_bwd",
                  "gdn_gate_norm_workspace_bytes", "gdn_res_norm_fwd", "gdn_res_norm_bwd",
-                 "gdn_res_norm_workspace_bytes", "gdn_layer_status"]
+                 "gdn_res_norm_workspace_bytes", "gdn_layer_status", "gdn_qk_norm_fwd",
+                 "gdn_qk_norm_bwd", "gdn_qk_norm_workspace_bytes"]
 GATE_ACT = {"silu": 1, "sigmoid": 2}
+ROPE_STYLE = {"half": 0, "pairs": 1}
+# include/gdn_lin.h
+LIN_EXPORTS = ["gdn_lin_workspace_bytes", "gdn_lin_fwd", "gdn_lin_bwd", "gdn_lin_step"]
 
 
 class GdnError(RuntimeError):
@@ -85,6 +89,23 @@ class gdn_gate_norm_shape(ctypes.Structure):
 
 class gdn_res_norm_shape(ctypes.Structure):
     _fields_ = [("rows", _I), ("C", _I), ("dtype", _I), ("res_dtype", _I), ("eps", _F)]
+
+
+class gdn_qk_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", _I), ("T", _I), ("Hq", _I), ("Hk", _I), ("H", _I), ("d", _I),
+                ("rot", _I), ("style", _I), ("dtype", _I), ("ldq", _L), ("ldk", _L),
+                ("q_scale", _F), ("eps", _F)]
+
+
+class gdn_lin_shape(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("H", _I), ("dk", _I), ("dv", _I), ("dtype", _I),
+                ("nseq", _I), ("ldq", _L), ("ldk", _L), ("ldv", _L), ("ldg", _L), ("scale", _F)]
+
+
+class gdn_lin_step_shape(ctypes.Structure):
+    _fields_ = [("N", _I), ("n_tok", _I), ("n_slots", _I), ("H", _I), ("Hk", _I), ("dk", _I),
+                ("dv", _I), ("dtype", _I), ("ldq", _L), ("ldk", _L), ("ldv", _L), ("ldg", _L),
+                ("scale", _F)]
 
 
 _lib = None
@@ -154,15 +175,22 @@ def load(build_if_missing: bool = False):
                                   ("gdn_gate_norm_fwd", gdn_gate_norm_shape, 4, False),
                                   ("gdn_gate_norm_bwd", gdn_gate_norm_shape, 7, True),
                                   ("gdn_res_norm_fwd", gdn_res_norm_shape, 7, False),
-                                  ("gdn_res_norm_bwd", gdn_res_norm_shape, 12, True)):
+                                  ("gdn_res_norm_bwd", gdn_res_norm_shape, 12, True),
+                                  ("gdn_qk_norm_fwd", gdn_qk_norm_shape, 8, False),
+                                  ("gdn_qk_norm_bwd", gdn_qk_norm_shape, 12, True),
+                                  ("gdn_lin_step", gdn_lin_step_shape, 11, False),
+                                  ("gdn_lin_fwd", gdn_lin_shape, 9, True),
+                                  ("gdn_lin_bwd", gdn_lin_shape, 15, True)):
         f = getattr(lib, name)
         f.argtypes = [ctypes.POINTER(shape)] + [P] * nptr + ([P, Z, P] if ws else [P])
         f.restype = I
     for name, shape in (("prep", gdn_prep_shape), ("gate_norm", gdn_gate_norm_shape),
-                        ("res_norm", gdn_res_norm_shape)):
+                        ("res_norm", gdn_res_norm_shape), ("qk_norm", gdn_qk_norm_shape)):
         f = getattr(lib, f"gdn_{name}_workspace_bytes")
         f.argtypes = [ctypes.POINTER(shape)]
         f.restype = Z
+    lib.gdn_lin_workspace_bytes.argtypes = [ctypes.POINTER(gdn_lin_shape), I]
+    lib.gdn_lin_workspace_bytes.restype = Z
     lib.gdn_layer_status.argtypes = [P]
     lib.gdn_layer_status.restype = I
     lib.gdn_diag_exchange.argtypes = [P, I, I, P]
@@ -411,7 +439,7 @@ def gdn_conv_bwd(x, w, b, state_in, dy, dstate_out=None, act="silu", dx=None, dw
     return dx, dw, db, dstate_in
 
 
-# ------------------------------------------------- layer operators (include/gdn_layer.h)
+# -------------------------------- layer operators (include/gdn_layer.h and gdn_lin.h)
 # A generation step makes these calls once per layer and token, so their checks,
 # allocations and the call itself are native (csrc/gdn_torch.cpp).
 _ext_module = None
@@ -549,6 +577,68 @@ def gdn_res_norm_bwd(h_out, x, w, dy, dh_out=None, w_post=None, scale=None, eps=
                           dh, workspace)
     return (_ext_module or ext()).res_norm_bwd(h_out, x, w, dy, dh_out, w_post, scale, eps, dh,
                                                workspace)
+
+
+def gdn_qk_norm_fwd(q, k, wq=None, wk=None, inv_freq=None, pos=None, H=None, style="half",
+                    q_scale=1.0, eps=1e-6, stream=None):
+    """RMS norm of each head of q [B, T, Hq, d] and k [B, T, Hk, d] (token rows strided)
+    with the weights wq, wk [d] fp32, then the rotation of its first 2 len(inv_freq) values
+    by the angles pos * inv_freq (inv_freq fp64, pos int32 [B, T]; None: 0 .. T - 1), q
+    times q_scale. style "half": value i is paired with i + len(inv_freq), "pairs": 2i with
+    2i + 1. Returns (q, k) contiguous; with H each head is repeated for H heads."""
+    if stream is not None:
+        return _on_stream(gdn_qk_norm_fwd, stream, q, k, wq, wk, inv_freq, pos, H, style, q_scale,
+                          eps)
+    return (_ext_module or ext()).qk_norm_fwd(q, k, wq, wk, inv_freq, pos, H or 0,
+                                              ROPE_STYLE[style], q_scale, eps)
+
+
+def gdn_qk_norm_bwd(q, k, wq, wk, inv_freq, dqn, dkn, pos=None, H=None, style="half", q_scale=1.0,
+                    eps=1e-6, workspace=None, stream=None):
+    """Backward of gdn_qk_norm_fwd from the gradients of its outputs (contiguous).
+    Returns (dq, dk, dwq, dwk); those of absent weights are None."""
+    if stream is not None:
+        return _on_stream(gdn_qk_norm_bwd, stream, q, k, wq, wk, inv_freq, dqn, dkn, pos, H, style,
+                          q_scale, eps, workspace)
+    return (_ext_module or ext()).qk_norm_bwd(q, k, wq, wk, inv_freq, dqn, dkn, pos, H or 0,
+                                              ROPE_STYLE[style], q_scale, eps, workspace)
+
+
+def gdn_lin_fwd(q, k, v, g, S_in=None, scale=1.0, cu_seqlens=None, o=None, S_out=None,
+                want_state=True, workspace=None, stream=None):
+    """Linear attention S_t = e^g S_{t-1} + k v^T, o = scale S_t^T q over whole sequences:
+    q, k [B, T, H, dk], v [B, T, H, dv], g [B, T, H] (token rows strided) or one log-decay
+    for each head, g [H] fp32; S_in [B, H, dk, dv] fp32 (None: zeros). cu_seqlens [N + 1]
+    int32 on the device: N packed sequences, B = 1, S_in [N, H, dk, dv]. Returns
+    (o [B, T, H, dv], S_out); S_out is the next chunk's S_in and may be S_in."""
+    if stream is not None:
+        return _on_stream(gdn_lin_fwd, stream, q, k, v, g, S_in, scale, cu_seqlens, o, S_out,
+                          want_state, workspace)
+    return (_ext_module or ext()).lin_fwd(q, k, v, g, S_in, scale, cu_seqlens, o, S_out,
+                                          int(want_state), workspace)
+
+
+def gdn_lin_bwd(q, k, v, g, S_in, dout, dS_out=None, scale=1.0, cu_seqlens=None, want_state=True,
+                workspace=None, stream=None):
+    """Backward of gdn_lin_fwd from dout and the gradient dS_out of S_out (None: zero).
+    Returns (dq, dk, dv, dg, dS_in); dg as g, or fp32 [H] for one decay for each head."""
+    if stream is not None:
+        return _on_stream(gdn_lin_bwd, stream, q, k, v, g, S_in, dout, dS_out, scale, cu_seqlens,
+                          want_state, workspace)
+    return (_ext_module or ext()).lin_bwd(q, k, v, g, S_in, dout, dS_out, scale, cu_seqlens,
+                                          int(want_state), workspace)
+
+
+def gdn_lin_step(q, k, v, g, S, slot_in=None, slot_out=None, cu_seqlens=None, n_commit=None,
+                 scale=1.0, o=None, stream=None):
+    """gdn_lin_fwd's recurrence token by token over the states S [n_slots, H, dk, dv] (fp32,
+    updated in place), for the sequences of gdn_step: q, k [n_tok, Hk, dk],
+    v [n_tok, H, dv], g [n_tok, H] (rows strided) or [H] fp32. Returns o [n_tok, H, dv]."""
+    if stream is not None:
+        return _on_stream(gdn_lin_step, stream, q, k, v, g, S, slot_in, slot_out, cu_seqlens,
+                          n_commit, scale, o)
+    return (_ext_module or ext()).lin_step(q, k, v, g, S, slot_in, slot_out, cu_seqlens, n_commit,
+                                           scale, o)
 
 
 def gdn_layer_status(stream=None) -> int:

@@ -11,6 +11,8 @@
  *   gdn_prep_fwd/bwd   the maps before the recurrence: unit-norm q and k
  *                      (key heads shared by several value heads), the
  *                      log-decay and the write strength
+ *   gdn_qk_norm_*      RMS norm of each query and key head, then the rotation by
+ *                      the token's position (before gdn_lin.h's recurrence)
  *   gdn_gate_norm_*    RMS norm of each head's output, times its gate
  *   gdn_res_norm_*     block boundary: norm of the block's output, residual
  *                      scale, addition, norm before the next block
@@ -29,7 +31,8 @@
  * - Outputs must not alias inputs except where it is said that they may.
  * - Counts of rows, sequences and channels that pass what the kernels' 32-bit
  *   indices hold (2^31 - 2^16 of any; gdn_step 2^28 sequences x heads; prep and
- *   the gated norm 2^30 and 2^31 rows x heads) are GDN_ERR_UNSUPPORTED.
+ *   the gated norm 2^30 and 2^31 rows x heads; gdn_qk_norm 2^31 rows x (Hq + Hk)) are
+ *   GDN_ERR_UNSUPPORTED.
  * - Ownership, execution and errors as in gdn.h: caller-owned buffers, work
  *   enqueued on `stream` without synchronising, every argument checked on the
  *   host before any launch, GDN_ERR_CUDA if a launch fails. Calls with nothing
@@ -152,6 +155,48 @@ gdn_status gdn_prep_bwd(const gdn_prep_shape* shape, const void* q, const void* 
                         const void* dkn, const void* dg, const void* dbeta, void* dq, void* dk,
                         void* dxg, void* dxb, float* drate, float* dbias, void* workspace,
                         size_t workspace_bytes, void* stream);
+
+/* ----------------------------------- norms of queries and keys, and rotation
+ *     n = x / sqrt(mean(x^2) + eps) * w        per head of d values (w NULL: no factor)
+ *     y = n with its first rot values turned, times q_scale for q
+ * Of the pair i (values i and i + rot / 2 for GDN_ROPE_HALF, 2i and 2i + 1 for
+ * GDN_ROPE_PAIRS), with a = pos inv_freq[i]: (x0, x1) -> (x0 cos a - x1 sin a,
+ * x1 cos a + x0 sin a). The angle is reduced to a fraction of a turn in 64-bit whole
+ * numbers, so far positions lose nothing (below 2^-32 of a turn for any int32).
+ * q [rows, Hq, d], k [rows, Hk, d] vector rows; wq, wk [d]; inv_freq DEVICE fp64
+ * [rot / 2], finite and below 2^40 in size; pos DEVICE int32 [rows] (NULL: row
+ * mod T). qn, kn contiguous: [rows, Hq, d] and [rows, Hk, d] (H = 0), or both
+ * [rows, H, d], each head repeated for its H / Hq (H / Hk) heads as gdn_prep_fwd
+ * does. Sines and cosines are fp32. */
+#define GDN_ROPE_HALF 0
+#define GDN_ROPE_PAIRS 1
+
+typedef struct {
+  int rows;      /* B * T tokens */
+  int T;         /* without pos: tokens of a sequence (>= 1) */
+  int Hq, Hk;
+  int H;         /* 0, or heads of both outputs, a multiple of Hq and of Hk */
+  int d;         /* 64, 128 or 256 */
+  int rot;       /* 0 .. d, a multiple of 16 */
+  int style;     /* GDN_ROPE_HALF or GDN_ROPE_PAIRS */
+  int dtype;
+  long long ldq, ldk; /* strides of the rows of q, k */
+  float q_scale, eps; /* eps > 0 */
+} gdn_qk_norm_shape;
+
+gdn_status gdn_qk_norm_fwd(const gdn_qk_norm_shape* shape, const void* q, const void* k,
+                           const float* wq, const float* wk, const double* inv_freq,
+                           const int* pos, void* qn, void* kn, void* stream);
+
+size_t gdn_qk_norm_workspace_bytes(const gdn_qk_norm_shape* shape);
+
+/* From dqn, dkn (the layout of qn, kn): dq [rows, Hq, d], dk [rows, Hk, d] contiguous
+ * (summed over repeated heads), dwq, dwk [d] fp32 (those of absent weights NULL). */
+gdn_status gdn_qk_norm_bwd(const gdn_qk_norm_shape* shape, const void* q, const void* k,
+                           const float* wq, const float* wk, const double* inv_freq,
+                           const int* pos, const void* dqn, const void* dkn, void* dq, void* dk,
+                           float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 /* ------------------------------------------------------------- gated norm
  *     y = o / sqrt(mean(o^2) + eps) * w * act(z)      per row of d values
