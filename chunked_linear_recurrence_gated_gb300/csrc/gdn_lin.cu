@@ -159,16 +159,18 @@ __global__ void __launch_bounds__(LN_NT)
   }
 }
 
-// In place over the chunks of a sequence: D_b becomes the state before chunk b
-// (z = 0), E_b the gradient of the state behind it (z = 1, from the last chunk).
+// In place over the units of a sequence: D_b becomes the state before unit b
+// (z = 0), E_b the gradient of the state behind it (z = 1, from the last unit). `open`:
+// the last one to be visited has no sum of its own, and nothing is wanted behind it.
 constexpr int SC_NT = 128, SC_U = 8;
 __global__ void __launch_bounds__(SC_NT)
-    k_lin_scan(LinMap m, int H, int n4, const float* whole, float* D, const float* S_in,
-               float* S_out, float* E, const float* dS_out, float* dS_in, int* status) {
+    k_lin_scan(LinMap m, int H, int n4, const float* whole_d, float* D, const float* S_in,
+               float* S_out, const float* whole_e, float* E, const float* dS_out, float* dS_in,
+               bool open, int* status) {
   chain();
   if (m.cu) {
     if (*status != DEV_OK) return;
-  } else if ((blockIdx.x | blockIdx.y | blockIdx.z | threadIdx.x) == 0) {
+  } else if (!open && (blockIdx.x | blockIdx.y | blockIdx.z | threadIdx.x) == 0) {
     *status = DEV_OK;
   }
   const int e = blockIdx.x * SC_NT + threadIdx.x, h = blockIdx.y % H, seq = blockIdx.y / H;
@@ -177,6 +179,7 @@ __global__ void __launch_bounds__(SC_NT)
   int first, n;
   lin_seq(m, seq, first, n);
   float4* at = reinterpret_cast<float4*>(back ? E : D) + e;
+  const float* whole = back ? whole_e : whole_d;
   const float* from = back ? dS_out : S_in;
   float* to = back ? dS_in : S_out;
   const size_t sh = (size_t)seq * H + h;
@@ -189,8 +192,9 @@ __global__ void __launch_bounds__(SC_NT)
     for (int i = 0; i < SC_U; ++i)
       if (b0 + i < n) {
         const size_t uh = (size_t)(first + (back ? n - 1 - b0 - i : b0 + i)) * H + h;
-        d[i] = at[uh * n4];
-        a[i] = whole[uh];
+        const bool has = !open || b0 + i < n - 1;
+        d[i] = has ? at[uh * n4] : make_float4(0.f, 0.f, 0.f, 0.f);
+        a[i] = has ? whole[uh] : 0.f;
       }
 #pragma unroll
     for (int i = 0; i < SC_U; ++i)
@@ -437,7 +441,8 @@ __global__ void __launch_bounds__(LN_NT)
   }
 }
 
-// The units of a packed call. One block: each thread counts a run of sequences.
+// The units of a packed call, one at least for each sequence. One block: each thread
+// counts a run of sequences.
 constexpr int PL_NT = 1024;
 __global__ void __launch_bounds__(PL_NT) k_lin_plan(LinMap m, int* first, int* owner, int* status) {
   __shared__ int sums[32], bad;
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(PL_NT) k_lin_plan(LinMap m, int* first, int* o
   for (int s = s0; s < s1; ++s) {
     const int len = m.cu[s + 1] - m.cu[s];
     wrong |= m.cu[s + 1] < m.cu[s];
-    n += (int)(((unsigned)max(len, 0) + m.unit - 1) / m.unit);
+    n += max(1, (int)(((unsigned)max(len, 0) + m.unit - 1) / m.unit));
   }
   if (wrong) bad = 1;
   int up = n;
@@ -468,7 +473,8 @@ __global__ void __launch_bounds__(PL_NT) k_lin_plan(LinMap m, int* first, int* o
   if (tid == 0) *status = off ? DEV_BAD_CU_SEQLENS : DEV_OK;
   for (int s = s0; s < s1; ++s) {
     first[s] = off ? 0 : before;
-    const int k = off ? 0 : (int)(((unsigned)(m.cu[s + 1] - m.cu[s]) + m.unit - 1) / m.unit);
+    const int k =
+        off ? 0 : max(1, (int)(((unsigned)(m.cu[s + 1] - m.cu[s]) + m.unit - 1) / m.unit));
     for (int i = 0; i < k; ++i)
       if (before + i < m.cap) owner[before + i] = s;
     before += k;
@@ -490,7 +496,7 @@ struct SimtPlan {
 SimtPlan simt_plan(const gdn_lin_shape& s, const int* cu, bool packed, bool back,
                    unsigned char* ws) {
   SimtPlan p = {};
-  const int per = (s.T + LC - 1) / LC;
+  const int per = std::max(1, (s.T + LC - 1) / LC);
   p.m = {cu, nullptr, nullptr, s.nseq, s.T, LC, per, packed ? per + s.nseq : per * s.nseq};
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -528,24 +534,21 @@ cudaError_t run_simt(const LinCall& c, bool back) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     return f ? f : launch(kernel, grid, dim3(LN_NT), smem, c.st, 1, p.m, in, a...);
   };
-  if (p.m.cap > 0) {
-    prof_mark(c.st, "lin_sum");
-    e = back ? go(k_lin_sum<T, DK, DV, true>, rows_k + rows_v, p.whole, p.D, p.E)
-             : go(k_lin_sum<T, DK, DV, false>, rows_k + rows_v, p.whole, p.D, p.E);
-    if (e) return e;
-  }
+  prof_mark(c.st, "lin_sum");
+  e = back ? go(k_lin_sum<T, DK, DV, true>, rows_k + rows_v, p.whole, p.D, p.E)
+           : go(k_lin_sum<T, DK, DV, false>, rows_k + rows_v, p.whole, p.D, p.E);
+  if (e) return e;
   const int n4 = DK * DV / 4;
   prof_mark(c.st, "lin_scan");
   e = launch(k_lin_scan, dim3((n4 + SC_NT - 1) / SC_NT, s.nseq * s.H, back ? 2 : 1), dim3(SC_NT), 0,
-             c.st, 1, p.m, s.H, n4, p.whole, p.D, c.S_in, c.S_out, p.E, c.dS_out, c.dS_in, p.status);
+             c.st, 1, p.m, s.H, n4, p.whole, p.D, c.S_in, c.S_out, p.whole, p.E, c.dS_out, c.dS_in,
+             false, p.status);
   if (e) return e;
-  if (p.m.cap > 0) {
-    prof_mark(c.st, back ? "lin_grad" : "lin_out");
-    e = back ? go(k_lin_grad<T, DK, DV>, 2 * (rows_k + rows_v + square), p.D, p.E, (T*)c.dq,
-                  (T*)c.dk, (T*)c.dv, (T*)c.dg, c.ddecay ? p.dgsum : nullptr)
-             : go(k_lin_out<T, DK, DV>, 2 * rows_k + rows_v + square, p.D, (T*)c.o);
-    if (e) return e;
-  }
+  prof_mark(c.st, back ? "lin_grad" : "lin_out");
+  e = back ? go(k_lin_grad<T, DK, DV>, 2 * (rows_k + rows_v + square), p.D, p.E, (T*)c.dq, (T*)c.dk,
+                (T*)c.dv, (T*)c.dg, c.ddecay ? p.dgsum : nullptr)
+           : go(k_lin_out<T, DK, DV>, 2 * rows_k + rows_v + square, p.D, (T*)c.o);
+  if (e) return e;
   if (back && c.ddecay) e = col_sum(p.dgsum, p.m.cap, s.H, s.H, c.ddecay, nullptr, nullptr, c.st);
   return e;
 }
@@ -562,7 +565,9 @@ gdn_status check_lin(const gdn_lin_shape* s) {
   return GDN_OK;
 }
 
+// A call of one sequence may be packed or not.
 size_t lin_bytes(const gdn_lin_shape& s, bool back) {
+  if (lin_tc_takes(s)) return std::max(lin_tc_bytes(s, true, back), lin_tc_bytes(s, false, back));
   return std::max(lin_simt_bytes(s, true, back), lin_simt_bytes(s, false, back));
 }
 
@@ -588,7 +593,7 @@ gdn_status run(const LinCall& c, size_t ws_bytes, bool back) {
     if (!aligned(c.o, 16) || !aligned(c.S_out, 16)) return GDN_ERR_INVALID_ARG;
   }
   if (!c.ws || !aligned(c.ws, 256) || ws_bytes < lin_bytes(s, back)) return GDN_ERR_WORKSPACE;
-  const cudaError_t e = lin_simt(c, back);
+  const cudaError_t e = lin_tc_takes(s) ? lin_tc(c, back) : lin_simt(c, back);
   prof_mark(c.st, nullptr);
   return e ? GDN_ERR_CUDA : GDN_OK;
 }
@@ -598,6 +603,16 @@ gdn_status run(const LinCall& c, size_t ws_bytes, bool back) {
 cudaError_t lin_plan(const LinMap& m, int* first, int* owner, int* status, cudaStream_t st) {
   prof_mark(st, "lin_plan");
   return launch(k_lin_plan, dim3(1), dim3(PL_NT), 0, st, 1, m, first, owner, status);
+}
+
+cudaError_t lin_scan(const LinMap& m, const gdn_lin_shape& s, const float* whole, float* D,
+                     const float* S_in, float* E, const float* whole_e, const float* dS_out,
+                     bool back, int* status, cudaStream_t st) {
+  prof_mark(st, "lin_scan");
+  const int n4 = s.dk * s.dv / 4;
+  return launch(k_lin_scan, dim3((n4 + SC_NT - 1) / SC_NT, s.nseq * s.H, back ? 2 : 1), dim3(SC_NT),
+                0, st, 1, m, s.H, n4, whole, D, S_in, (float*)nullptr, whole_e, E, dS_out,
+                (float*)nullptr, true, status);
 }
 
 size_t lin_simt_bytes(const gdn_lin_shape& s, bool packed, bool back) {

@@ -72,6 +72,18 @@ struct LinCall {
 // Writes the tables of a packed call; the status word: DEV_OK or DEV_BAD_CU_SEQLENS.
 cudaError_t lin_plan(const LinMap& m, int* first, int* owner, int* status, cudaStream_t st);
 
+// In place over the units of a sequence, D[unit, H, dk, dv] with the units' decays
+// whole[unit, H]: D becomes the state before each unit; with `back` also E the gradient
+// of the state behind it. The last unit's own D (the first one's E) is not read.
+cudaError_t lin_scan(const LinMap& m, const gdn_lin_shape& s, const float* whole, float* D,
+                     const float* S_in, float* E, const float* whole_e, const float* dS_out,
+                     bool back, int* status, cudaStream_t st);
+
+// bf16 kernels on tcgen05 (gdn_lin_tc.cu).
+bool lin_tc_takes(const gdn_lin_shape& s);
+size_t lin_tc_bytes(const gdn_lin_shape& s, bool packed, bool back);
+cudaError_t lin_tc(const LinCall& c, bool back);
+
 // fp32 kernels (gdn_lin.cu).
 size_t lin_simt_bytes(const gdn_lin_shape& s, bool packed, bool back);
 cudaError_t lin_simt(const LinCall& c, bool back);

@@ -463,15 +463,20 @@ EncodeTiledFn encode_fn() {
 // View of a [B][T][H][d] bf16 tensor (varlen: [1][total][H][d]) as a 4-D map
 // with 64-element x 1 head x 64-token boxes and the 128-byte swizzle.
 cudaError_t make_tok_map(CUtensorMap* map, const void* base, int d, const SeqMap& m) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
   const bool varlen = m.cu != nullptr;
   const cuuint64_t T = varlen ? (cuuint64_t)m.T_total : (cuuint64_t)m.T_fixed;
   const cuuint64_t Bn = varlen ? 1 : (cuuint64_t)m.nseq;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)m.H, T, Bn};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)m.H * d * 2,
                                  (cuuint64_t)m.H * d * 2 * T};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)BT, 1};
+  return make_tile_map(map, base, dims, strides, BT);
+}
+
+cudaError_t make_tile_map(CUtensorMap* map, const void* base, const cuuint64_t* dims,
+                          const cuuint64_t* strides, int tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)tokens, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
                         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
