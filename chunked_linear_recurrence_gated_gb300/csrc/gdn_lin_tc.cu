@@ -34,8 +34,10 @@ namespace {
 typedef __nv_bfloat16 bf;
 
 constexpr int TC = 128;          // tokens of a chunk
-constexpr int NEPI = 512;        // 16 warps on the accumulators: 4 lane quarters x 4 column groups
-constexpr int NTHR = NEPI + 32;  // and one that copies, issues the MMAs and forms the decay factors
+constexpr int NEPI = 256;        // 8 warps on the accumulators: 4 lane quarters x 2 column groups
+constexpr int CTL = 8, DEC = 9;  // a warp that copies and issues the MMAs, one for decay factors
+constexpr int NWORK = 320;       // threads of these
+constexpr int NTHR = 384;        // launched: whole warpgroups, for the registers' redistribution
 constexpr uint32_t HALF_TILE = TC * 128;  // 64 columns of a chunk's rows
 
 // ------------------------------------------------------------------ TMEM access
@@ -49,7 +51,7 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-// 16 columns of this thread's lane from registers; wait before telling others.
+// Columns of this thread's lane from registers; tmem_st_wait before telling others.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -58,18 +60,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 16 lanes x 16 columns as ldmatrix leaves them: in register 2 k + j thread i has lane
+// 8 j + i / 4, column 4 k + i % 4.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
-template <int N>  // 16 or 32 columns
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]),
+        "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
 #pragma unroll
-  for (int i = 0; i < N; i += 16) tmem_ld16(taddr + i, v + i);
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <int N>
-__device__ __forceinline__ void tmem_st_f(uint32_t taddr, const float* v) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
 #pragma unroll
-  for (int i = 0; i < N; i += 16) {
+  for (int i = 0; i < 32; i += 16) {
     uint32_t r[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(v[i + j]);
@@ -85,9 +108,6 @@ __device__ __forceinline__ uint64_t kmaj(uint32_t base, uint32_t half, int kk) {
 }
 __device__ __forceinline__ uint64_t mnmaj(uint32_t base, uint32_t half, int kk) {
   return umma_desc(base + 2048 * kk, half, 1024);
-}
-__device__ __forceinline__ float bf_at(const unsigned char* p) {
-  return __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16);
 }
 // Columns [c, c + 8) of row r of a tile of 64-wide halves.
 __device__ __forceinline__ unsigned char* at8(unsigned char* tile, uint32_t half, int r, int c) {
@@ -116,14 +136,23 @@ __device__ __forceinline__ void put_split(unsigned char* hi, unsigned char* lo, 
   }
 }
 
-// Decay factors of a chunk.
+// ------------------------------------------------------------------ decay factors
+// Weights of a state's update as pairs of bf16, first parts and rests.
+struct Weights {
+  uint32_t hi[TC / 2], lo[TC / 2];
+  float whole, pad[3];  // e^{gamma_C}
+};
+// Of a chunk: L_ts = row[t] tab[b - 1][s] for t in the block b of 32 behind that of s. Within
+// a block it is row[t] own[s] where the block's decay leaves the second factor small
+// (`mild`), else the exponential of the difference.
 struct Vec {
+  Weights w;
   float hi[TC], lo[TC];  // gamma, as the sum of two floats
-  float row[TC];         // e^{gamma_t - gamma_{b-1}}, b the first token of t's block of 32
-  float up[TC];          // e^{gamma_t}
-  float down[TC];        // e^{gamma_C - gamma_t}
+  float row[TC];         // e^{gamma_t - gamma_a}, a the last token before t's block
+  float far[TC];         // forward: e^{gamma_t}; back: e^{gamma_C - gamma_t}
+  float own[TC];         // e^{gamma_a - gamma_s}
   float tab[3][TC];      // [b - 1][s]: e^{gamma_{32 b - 1} - gamma_s} for s < 32 b
-  float whole, pad[3];   // e^{gamma_C}
+  int mild, pad[3];
 };
 
 // The log-decays of a chunk, 4 tokens for each lane of a warp, loaded ahead of their use.
@@ -141,42 +170,69 @@ __device__ __forceinline__ Raw raw_decay(int row, int len, int h, const bf* g, l
   }
   return r;
 }
-// gamma summed in 64 bits (differences of neighbours keep 24 bits however large it is).
+// gamma summed as pairs of floats (2^-47 of itself: differences of neighbours keep their
+// 24 bits however large it is; FP64 has 1/64 of the rate, and this warp is waited for).
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add_two(Two a, Two b) {
+  const float s = a.hi + b.hi, v = s - a.hi;
+  const float e = (a.hi - (s - v)) + (b.hi - v) + (a.lo + b.lo);
+  Two r;
+  r.hi = s + e;
+  r.lo = e - (r.hi - s);
+  return r;
+}
 __device__ __forceinline__ void sum_decay(const Raw& r, float* hi, float* lo) {
   const int l = threadIdx.x & 31;
-  double c[4], sum = 0.0;
+  Two c[4];
+  c[0] = {r.x[0], 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = (sum += (double)r.x[i]);
-  double all = sum;
+  for (int i = 1; i < 4; ++i) c[i] = add_two(c[i - 1], {r.x[i], 0.f});
+  Two all = c[3];
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, all, d);
-    if (l >= d) all += y;
+    const Two y = {__shfl_up_sync(0xffffffffu, all.hi, d), __shfl_up_sync(0xffffffffu, all.lo, d)};
+    if (l >= d) all = add_two(y, all);
   }
-  const double before = all - sum;
+  Two before = {__shfl_up_sync(0xffffffffu, all.hi, 1), __shfl_up_sync(0xffffffffu, all.lo, 1)};
+  if (l == 0) before = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const double x = before + c[i];
-    hi[i] = (float)x;
-    lo[i] = (float)(x - (double)hi[i]);
+    const Two x = add_two(before, c[i]);
+    hi[i] = x.hi;
+    lo[i] = x.lo;
   }
 }
 __device__ __forceinline__ float exp_diff(float h1, float l1, float h0, float l0) {
   return expf((h1 - h0) + (l1 - l0));
 }
-__device__ __forceinline__ void fill_vec(const Raw& r, Vec& v) {  // one warp
+// Weights of the state's update: to the chunk's end, or (BACK) scale times from its start.
+template <bool BACK>
+__device__ __forceinline__ void fill_weights(const float* hi, const float* lo, float scale, Weights& w) {
   const int l = threadIdx.x & 31;
-  float hi[4], lo[4], eh[4], el[4];
+  const float eh = __shfl_sync(0xffffffffu, hi[3], 31), el = __shfl_sync(0xffffffffu, lo[3], 31);
+  float o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = BACK ? scale * exp_diff(hi[i], lo[i], 0.f, 0.f) : exp_diff(eh, el, hi[i], lo[i]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) split2(o[2 * i], o[2 * i + 1], w.hi[2 * l + i], w.lo[2 * l + i]);
+  if (l == 0) w.whole = exp_diff(eh, el, 0.f, 0.f);
+}
+template <bool BACK>
+__device__ __forceinline__ void fill_vec(const Raw& r, float scale, Vec& v) {  // one warp
+  const int l = threadIdx.x & 31, blk = l >> 3;  // this lane's block of 32 tokens
+  float hi[4], lo[4], eh[4], el[4], o[4] = {};
   sum_decay(r, hi, lo);
+  fill_weights<BACK>(hi, lo, scale, v.w);
 #pragma unroll
   for (int b = 0; b < 4; ++b) {  // the ends of the blocks
     eh[b] = __shfl_sync(0xffffffffu, hi[3], 8 * b + 7);
     el[b] = __shfl_sync(0xffffffffu, lo[3], 8 * b + 7);
   }
-  const int blk = l >> 3;  // of 32 tokens
   const float ah = blk == 0 ? 0.f : blk == 1 ? eh[0] : blk == 2 ? eh[1] : eh[2];
   const float al = blk == 0 ? 0.f : blk == 1 ? el[0] : blk == 2 ? el[1] : el[2];
-  float o[4] = {};
   auto put = [&](float* to) {
     reinterpret_cast<float4*>(to)[l] = make_float4(o[0], o[1], o[2], o[3]);
   };
@@ -185,13 +241,19 @@ __device__ __forceinline__ void fill_vec(const Raw& r, Vec& v) {  // one warp
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = exp_diff(hi[i], lo[i], ah, al);
   put(v.row);
+  bool small = true;  // every factor between e^-40 and e^40
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = exp_diff(hi[i], lo[i], 0.f, 0.f);
-  put(v.up);
-  if (l == 31) v.whole = o[3];
+  for (int i = 0; i < 4; ++i) {
+    small = small && o[i] > 4.3e-18f && o[i] < 2.3e17f;
+    o[i] = exp_diff(ah, al, hi[i], lo[i]);
+  }
+  put(v.own);
+  if (l == 0) v.mild = 0;
+  if (__all_sync(0xffffffffu, small) && l == 0) v.mild = 1;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = exp_diff(eh[3], el[3], hi[i], lo[i]);
-  put(v.down);
+  for (int i = 0; i < 4; ++i)
+    o[i] = BACK ? exp_diff(eh[3], el[3], hi[i], lo[i]) : exp_diff(hi[i], lo[i], 0.f, 0.f);
+  put(v.far);
 #pragma unroll
   for (int b = 0; b < 3; ++b) {
 #pragma unroll
@@ -201,9 +263,8 @@ __device__ __forceinline__ void fill_vec(const Raw& r, Vec& v) {  // one warp
 }
 
 // ------------------------------------------------------------------ shared pieces
-struct Who {  // a thread's part of an accumulator
-  int tid, w, l, q4, cq, lane;
-  bool epi, ctl;  // works on accumulators; is the thread that copies and issues
+struct Who {  // a thread's part of an accumulator: row `lane`, column group cg
+  int tid, w, l, q4, cg, lane;
 };
 __device__ __forceinline__ Who who() {
   Who t;
@@ -211,17 +272,35 @@ __device__ __forceinline__ Who who() {
   t.w = t.tid >> 5;
   t.l = t.tid & 31;
   t.q4 = t.w & 3;
-  t.cq = (t.w >> 2) & 3;
+  t.cg = (t.w >> 2) & 1;
   t.lane = 32 * t.q4 + t.l;
-  t.epi = t.tid < NEPI;
-  t.ctl = t.tid == NEPI;
   return t;
+}
+// Registers of the working warpgroups and of the third: together within what was launched.
+constexpr int REG_EPI = 216, REG_CTL = 64, REG_LAUNCH = 168;
+static_assert(256 * REG_EPI + 128 * REG_CTL <= NTHR * REG_LAUNCH, "the pool of the launch");
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REG_EPI));
+}
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REG_CTL));
+}
+// All working warps meet; true if any has seen a wait run out.
+__device__ __forceinline__ bool meet(volatile int* abort) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(any)
+      : "r"(*abort), "n"(NWORK)
+      : "memory");
+  return any != 0;
 }
 
 // What the kernels of a call share.
 struct Args {
   LinMap m;
-  int H, chunks;  // heads; chunks of a unit
+  int H;
   float scale;
   const bf* g;
   const float* decay;
@@ -244,25 +323,46 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int len, int tid)
   for (int i = tid; i < (TC - len) * P; i += NEPI)
     *reinterpret_cast<uint4*>(at8(tile, HALF_TILE, len + i / P, i % P * 8)) = make_uint4(0, 0, 0, 0);
 }
-// The weighted transpose of a tile's column `lane` (tokens [32 cq, 32 cq + 32)) as packed
-// first parts and rests: an operand in tensor memory with the tokens as reduced dimension.
-__device__ __forceinline__ void weigh(const unsigned char* tile, const Who& t, const float* wt,
-                                      float by, int len, uint32_t* hi, uint32_t* lo) {
-  const unsigned char* col = tile + (t.lane >> 6) * HALF_TILE + (t.lane & 7) * 2;
-  const int piece = (t.lane & 63) >> 3, s0 = 32 * t.cq;
+__device__ __forceinline__ uint32_t bf2(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ __nv_bfloat162 bf2(uint32_t x) {
+  return *reinterpret_cast<__nv_bfloat162*>(&x);
+}
+// The weighted transpose of a warp's 32 columns of a tile (64 tokens) into tensor memory,
+// an operand with the tokens as reduced dimension: first parts at `to`, rests 64 columns
+// on. With y a value and w = wh + wl its weight, hi = y wh rounded, and y wh - hi + y wl is
+// the rest: fused multiply-adds of pairs, the first difference exact.
+__device__ __forceinline__ void weigh(const unsigned char* tile, const Who& t, const Weights& w,
+                                      int len, uint32_t to) {
+  const uint32_t base = smem_u32(tile) + (t.q4 >> 1) * HALF_TILE;
+  const int piece = (t.q4 & 1) * 4 + (t.l >> 3), r7 = t.l & 7;
+  const uint32_t at = base + (64 * t.cg + r7) * 128 + ((piece ^ r7) << 4);
+  const int p0 = 32 * t.cg + (t.l & 3);
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const float4 w4 = *reinterpret_cast<const float4*>(wt + s0 + i);
-    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-    float x[4];
+  for (int g = 0; g < 2; ++g) {  // 32 tokens
+    uint32_t hi[2][8], lo[2][8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int s = s0 + i + j;
-      const float y = bf_at(col + s * 128 + ((piece ^ (s & 7)) << 4));
-      x[j] = s < len ? y * (by * w[j]) : 0.f;
+    for (int k = 0; k < 4; ++k) {
+      uint32_t y[4];
+      ldsm_x4_t(at + (32 * g + 8 * k) * 128, y[0], y[1], y[2], y[3]);
+      const int p = p0 + 16 * g + 4 * k;
+      if (len < TC) {
+        const uint32_t keep = (2 * p < len ? 0xffffu : 0u) | (2 * p + 1 < len ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] &= keep;
+      }
+      const __nv_bfloat162 wh = bf2(w.hi[p]), wl = bf2(w.lo[p]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 v = bf2(y[j]), a = __hmul2_rn(v, wh);
+        hi[j >> 1][2 * k + (j & 1)] = bf2(a);
+        lo[j >> 1][2 * k + (j & 1)] = bf2(__hfma2(v, wl, __hfma2(v, wh, __hneg2(a))));
+      }
     }
-    split2(x[0], x[1], hi[i / 2], lo[i / 2]);
-    split2(x[2], x[3], hi[i / 2 + 1], lo[i / 2 + 1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // 16 lanes
+      tmem_st_frag(to + (16u * j << 16) + 32 * t.cg + 16 * g, hi[j]);
+      tmem_st_frag(to + (16u * j << 16) + 64 + 32 * t.cg + 16 * g, lo[j]);
+    }
   }
 }
 // This thread's N elements (row lane, columns c0..) of a state [DY][DZ], or of one that is
@@ -296,15 +396,32 @@ __device__ __forceinline__ void store_state(float* to, int lane, int c0, const f
           make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
   }
 }
-// N values times `by` as bf16 to consecutive addresses (16-byte aligned).
+// s <- by s + an accumulator's N columns (an even number of 32s).
 template <int N>
-__device__ __forceinline__ void store_row(bf* to, const float* v, float by) {
+__device__ __forceinline__ void add_state(uint32_t taddr, float by, float* s) {
 #pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    uint32_t u[4];
+  for (int i = 0; i < N; i += 32) {
+    float d[32];
+    tmem_ld32(taddr + i, d);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = pack2bf(by * v[i + 2 * j], by * v[i + 2 * j + 1]);
-    *reinterpret_cast<uint4*>(to + i) = make_uint4(u[0], u[1], u[2], u[3]);
+    for (int j = 0; j < 32; ++j) s[i + j] = fmaf(by, s[i + j], d[j]);
+  }
+}
+// An accumulator's N columns times `by` as bf16 to consecutive addresses (16-byte aligned).
+template <int N>
+__device__ __forceinline__ void store_row(uint32_t taddr, bf* to, float by, bool on) {
+#pragma unroll
+  for (int i = 0; i < N; i += 32) {
+    float v[32];
+    tmem_ld32(taddr + i, v);
+    if (!on) continue;
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) {
+      uint32_t u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = pack2bf(by * v[k + 2 * j], by * v[k + 2 * j + 1]);
+      *reinterpret_cast<uint4*>(to + i + k) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
   }
 }
 // After a wait that ran out: this CTA's copies still under way are waited for, with a
@@ -315,6 +432,33 @@ __device__ __forceinline__ void drain(uint64_t* bars, int n, uint32_t phases) {
     mbar_wait(bars + i, (phases >> i) & 1, &off, 1ll << 24);
   }
 }
+// Barriers, the abort flag and tensor memory; returns its address.
+__device__ __forceinline__ uint32_t set_up(const Who& t, uint64_t* bars, int n, uint32_t* tslot,
+                                           volatile int* abort) {
+  if (t.tid == CTL * 32) {
+    for (int i = 0; i < n; ++i) mbar_init(bars + i, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (t.w == CTL) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  return *tslot;
+}
+__device__ __forceinline__ void tear_down(const Who& t, uint64_t* full, int n, uint32_t tm,
+                                          volatile int* abort, int* status) {
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (t.tid == CTL * 32 && *abort) {
+    *status = DEV_TIMEOUT;
+    drain(full, n, 0);
+    drain(full, n, ~0u);
+  }
+  __syncthreads();
+  if (t.w == CTL) tmem_dealloc(tm, 512);
+}
 
 constexpr uint32_t slot_bytes(int a, int b) { return (a > b ? a : b) * TC * 2; }
 
@@ -323,14 +467,10 @@ constexpr uint32_t slot_bytes(int a, int b) { return (a > b ? a : b) * TC * 2; }
 // times scale) y z^T, and the unit's whole decay. Not for a sequence's last unit (REV: its
 // first), whose state nobody starts from. The MMAs of a chunk run under the weighing of
 // the next one and the update from the one before; three chunks' tiles are in flight.
-struct StateVec {
-  float w[TC];
-  float whole, pad[3];
-};
 template <int DY, int DZ>
 struct StateSm {
   static constexpr uint32_t SLOT = slot_bytes(DY, DZ), STAGES = 3;
-  static constexpr uint32_t VEC = 2 * STAGES * SLOT, BAR = VEC + 4 * sizeof(StateVec);
+  static constexpr uint32_t VEC = 2 * STAGES * SLOT, BAR = VEC + 4 * sizeof(Weights);
   static constexpr uint32_t BYTES = BAR + 128 + 1024;
 };
 template <int DY, int DZ, bool REV, bool TR>
@@ -338,7 +478,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     k_lin_tc_state(Args a, float* whole, float* out, bool clear, const __grid_constant__ CUtensorMap my,
                    const __grid_constant__ CUtensorMap mz) {
   using L = StateSm<DY, DZ>;
-  constexpr int N = DZ / 4;
+  constexpr int N = DZ / 2, ST = L::STAGES;
   constexpr uint32_t D0 = 0, Y0 = 256;  // two accumulators, two operands of two parts
   chain();
   if (clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = DEV_OK;
@@ -349,143 +489,122 @@ __global__ void __launch_bounds__(NTHR, 1)
   const Who t = who();
   extern __shared__ __align__(1024) unsigned char smraw[];
   unsigned char* sb = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
-  StateVec* vec = reinterpret_cast<StateVec*>(sb + L::VEC);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [STAGES]
-  uint64_t* done = full + L::STAGES;                          // [2] MMAs of a chunk
+  Weights* vec = reinterpret_cast<Weights*>(sb + L::VEC);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [ST]
+  uint64_t* done = full + ST;                                 // [2] MMAs of a chunk
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   const int nch = (u.len + TC - 1) / TC;
-  if (t.ctl) {
-    for (int i = 0; i < (int)L::STAGES + 2; ++i) mbar_init(full + i, 1);
-    *abort = 0;
-    fence_mbar_init();
-  }
-  if (t.w == NEPI / 32) tmem_alloc(tslot, 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = *tslot, tl = tm + ((uint32_t)(32 * t.q4) << 16);
+  const uint32_t tm = set_up(t, full, ST + 2, tslot, abort);
   auto chunk = [&](int i) { return REV ? nch - 1 - i : i; };
-  auto load = [&](int i) {  // the control thread
-    const int c = chunk(i), st = i % L::STAGES;
-    const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
-    unsigned char* to = sb + 2 * st * L::SLOT;
-    mbar_arrive_expect_tx(full + st, (DY + DZ) * TC * 2);
-#pragma unroll
-    for (int e = 0; e < DY; e += 64) tma_load_4d(to + (e >> 6) * HALF_TILE, &my, e, h, tok, seq, full + st);
-#pragma unroll
-    for (int e = 0; e < DZ; e += 64)
-      tma_load_4d(to + L::SLOT + (e >> 6) * HALF_TILE, &mz, e, h, tok, seq, full + st);
-  };
   auto raw = [&](int i) {
     const int c = chunk(i);
     return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
   };
-  auto fill = [&](const Raw& r, StateVec& v) {
-    float hi[4], lo[4];
-    sum_decay(r, hi, lo);
-    const float eh = __shfl_sync(0xffffffffu, hi[3], 31), el = __shfl_sync(0xffffffffu, lo[3], 31);
-    float o[4];
+  auto tile = [&](int i) { return sb + 2 * (i % ST) * L::SLOT; };  // y, and z a slot behind it
+  if (t.w < CTL) {
+    const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
+    float s[N], all = 1.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = REV ? a.scale * exp_diff(hi[i], lo[i], 0.f, 0.f) : exp_diff(eh, el, hi[i], lo[i]);
-    reinterpret_cast<float4*>(v.w)[t.l] = make_float4(o[0], o[1], o[2], o[3]);
-    if (t.l == 0) v.whole = exp_diff(eh, el, 0.f, 0.f);
-  };
-  if (t.ctl)
-    for (int i = 0; i < min(nch, (int)L::STAGES); ++i) load(i);
-  if (!t.epi) {
-    fill(raw(0), vec[0]);
-    if (nch > 1) fill(raw(1), vec[1]);
-  }
-  float s[N], all = 1.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = 0.f;
-  auto update = [&](int i) {  // from chunk i's accumulator
-    mbar_wait(done + (i & 1), (i >> 1) & 1, abort);
-    tc_fence_after();
-    if (t.lane < DY) {
-      float d[N];
-      tmem_ld<N>(tl + D0 + 128 * (i & 1) + N * t.cq, d);
+    for (int i = 0; i < N; ++i) s[i] = 0.f;
+    auto update = [&](int i) {  // from chunk i's accumulator
+      mbar_wait(done + (i & 1), (i >> 1) & 1, abort);
+      tc_fence_after();
       const float wh = vec[i & 3].whole;
-#pragma unroll
-      for (int j = 0; j < N; ++j) s[j] = fmaf(wh, s[j], d[j]);
-    }
-    all *= vec[i & 3].whole;
-    tc_fence_before();
-  };
-  __syncthreads();
-  for (int i = 0; i < nch; ++i) {
-    const int st = i % L::STAGES, len = min(TC, u.len - chunk(i) * TC);
-    unsigned char* y = sb + 2 * st * L::SLOT;
-    if (t.epi) {
-      mbar_wait(full + st, (i / L::STAGES) & 1, abort);
+      if (t.lane < DY) add_state<N>(tl + D0 + 128 * (i & 1) + N * t.cg, wh, s);
+      all *= wh;
+      tc_fence_before();
+    };
+    meet(abort);
+    for (int i = 0; i < nch; ++i) {
+      const int len = min(TC, u.len - chunk(i) * TC);
+      mbar_wait(full + i % ST, (i / ST) & 1, abort);
       if (t.lane < DY) {
-        uint32_t hi[16], lo[16];
-        weigh(y, t, vec[i & 3].w, 1.f, len, hi, lo);
-        tmem_st16(tl + Y0 + 128 * (i & 1) + 16 * t.cq, hi);
-        tmem_st16(tl + Y0 + 128 * (i & 1) + 64 + 16 * t.cq, lo);
+        weigh(tile(i), t, vec[i & 3], len, tl + Y0 + 128 * (i & 1));
         tmem_st_wait();
       }
       if (len < TC && a.m.cu) {
-        zero_rows<DZ>(y + L::SLOT, len, t.tid);
+        zero_rows<DZ>(tile(i) + L::SLOT, len, t.tid);
         fence_proxy_async_smem();
       }
       tc_fence_before();
-    }
-    if (__syncthreads_or(*abort != 0)) break;
-    if (t.epi) {
+      if (meet(abort)) break;
       if (i) update(i - 1);
-    } else {
+    }
+    if (nch) update(nch - 1);
+    const size_t uh = (size_t)unit * a.H + h;
+    store_state<DY, DZ, TR, N>(out + uh * DY * DZ, t.lane, N * t.cg, s);
+    if (t.tid == 0) whole[uh] = all;
+  } else if (t.w == CTL) {
+    auto load = [&](int i) {
+      const int c = chunk(i);
+      const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
+      uint64_t* bar = full + i % ST;
+      mbar_arrive_expect_tx(bar, (DY + DZ) * TC * 2);
+#pragma unroll
+      for (int e = 0; e < DY; e += 64)
+        tma_load_4d(tile(i) + (e >> 6) * HALF_TILE, &my, e, h, tok, seq, bar);
+#pragma unroll
+      for (int e = 0; e < DZ; e += 64)
+        tma_load_4d(tile(i) + L::SLOT + (e >> 6) * HALF_TILE, &mz, e, h, tok, seq, bar);
+    };
+    if (t.l == 0)
+      for (int i = 0; i < min(nch, ST); ++i) load(i);
+    __syncwarp();
+    meet(abort);
+    for (int i = 0; i < nch; ++i) {
+      if (meet(abort)) break;
       if (t.l == 0) {
         tc_fence_after();
-        mbar_wait(full + st, (i / L::STAGES) & 1, abort);
-        const uint32_t z = smem_u32(y + L::SLOT);
-        constexpr uint32_t id = umma_idesc(128, DZ, 0, 1);
+        mbar_wait(full + i % ST, (i / ST) & 1, abort);
+        const uint32_t z = smem_u32(tile(i) + L::SLOT);
 #pragma unroll 1
         for (int p = 0; p < 2; ++p)
-#pragma unroll 1
+#pragma unroll
           for (int kk = 0; kk < TC / 16; ++kk)
             umma_ts(tm + D0 + 128 * (i & 1), tm + Y0 + 128 * (i & 1) + 64 * p + 8 * kk,
-                    mnmaj(z, HALF_TILE, kk), id, p || kk);
+                    mnmaj(z, HALF_TILE, kk), umma_idesc(128, DZ, 0, 1), p || kk);
         umma_commit(done + (i & 1));
+        if (i) {  // the chunk before is done with its tiles
+          mbar_wait(done + ((i - 1) & 1), ((i - 1) >> 1) & 1, abort);
+          if (i - 1 + ST < nch && !*abort) load(i - 1 + ST);
+        }
       }
       __syncwarp();
-      // two ahead: visible behind the next chunk's barrier; four kept, for the chunk before
+    }
+  } else if (t.w == DEC) {
+    auto fill = [&](const Raw& r, int i) {
+      float hi[4], lo[4];
+      sum_decay(r, hi, lo);
+      fill_weights<REV>(hi, lo, a.scale, vec[i & 3]);
+    };
+    fill(raw(0), 0);
+    if (nch > 1) fill(raw(1), 1);
+    Raw ahead = {};
+    if (nch > 2) ahead = raw(2);
+    meet(abort);
+    for (int i = 0; i < nch; ++i) {
+      if (meet(abort)) break;
+      // two ahead: visible behind the next chunk's meeting; four kept, for the chunk before
       // this one is still to be added
-      if (i + 2 < nch) fill(raw(i + 2), vec[(i + 2) & 3]);
-      if (t.l == 0 && i) {  // the chunk before is done with its tiles
-        mbar_wait(done + ((i - 1) & 1), ((i - 1) >> 1) & 1, abort);
-        if (i - 1 + (int)L::STAGES < nch && !*abort) load(i - 1 + L::STAGES);
-      }
+      if (i + 2 < nch) fill(ahead, i + 2);
+      if (i + 3 < nch) ahead = raw(i + 3);
     }
   }
-  if (t.epi && nch) update(nch - 1);
-  const size_t uh = (size_t)unit * a.H + h;
-  if (t.epi) store_state<DY, DZ, TR, N>(out + uh * DY * DZ, t.lane, N * t.cq, s);
-  if (t.tid == 0) whole[uh] = all;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (t.ctl && *abort) {
-    *a.status = DEV_TIMEOUT;
-    drain(full, L::STAGES, 0);
-    drain(full, L::STAGES, ~0u);
-  }
-  __syncthreads();
-  if (t.w == NEPI / 32) tmem_dealloc(tm, 512);
+  tear_down(t, full, ST, tm, abort, a.status);
 }
 
 // ------------------------------------------------------------------ forward and dq
-// Per chunk: P = x y^T and x S (MMAs) under the weighing of y; P masked into tensor memory
-// and x S scaled in place; P z onto it and the state's sum (MMAs); result and state. The
-// tiles x, y, z take the four slots in turn: y and z of the next chunk are copied as soon
-// as x and y are done with, x of the one after behind z.
+// Per chunk, on the accumulators: P = x y^T masked, y weighed, x S scaled; then P z onto it,
+// the result, the state's sum. x y^T of the next chunk runs under the result and the state,
+// x S under P, so the MMAs that the warps wait for are P z and the sum. The tiles x, y, z
+// take the four slots in turn: y and z of the next chunk are copied as soon as x and y are
+// done with, x of the one after behind z.
 template <int DY, int DZ>
 struct PassSm {
   static constexpr uint32_t SLOT = slot_bytes(DY, DZ), STATE = DY * DZ * 2, HALF_S = DY * 128;
   static constexpr uint32_t S_HI = 4 * SLOT, S_LO = S_HI + STATE, VEC = S_LO + STATE;
-  static constexpr uint32_t PART = VEC + 2 * sizeof(Vec), BAR = PART + 4 * TC * 4;
+  static constexpr uint32_t PART = VEC + 2 * sizeof(Vec), BAR = PART + 2 * TC * 4;
   static constexpr uint32_t BYTES = BAR + 128 + 1024;
 };
 template <int DY, int DZ, bool DQ>
@@ -494,7 +613,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                   long long ldq, float* far, bool clear, const __grid_constant__ CUtensorMap mx,
                   const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz) {
   using L = PassSm<DY, DZ>;
-  constexpr int N = DZ / 4;
+  constexpr int N = DZ / 2;
   constexpr uint32_t P0 = 0, O0 = 128, Y0 = 256, D0 = 384;
   chain();
   if (clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = DEV_OK;
@@ -508,147 +627,116 @@ __global__ void __launch_bounds__(NTHR, 1)
   Vec* vec = reinterpret_cast<Vec*>(sb + L::VEC);
   float* part = reinterpret_cast<float*>(sb + L::PART);
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [4]
-  uint64_t *bar_a = full + 4, *bar_c = full + 5;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 6);
+  // MMAs: x y^T, x S, P z, the state's sum
+  uint64_t *bar_p = full + 4, *bar_s = full + 5, *bar_o = full + 6, *bar_d = full + 7;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 8);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   const int nch = (u.len + TC - 1) / TC;
-  if (t.ctl) {
-    for (int i = 0; i < 6; ++i) mbar_init(full + i, 1);
-    *abort = 0;
-    fence_mbar_init();
-  }
-  if (t.w == NEPI / 32) tmem_alloc(tslot, 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = *tslot, tl = tm + ((uint32_t)(32 * t.q4) << 16);
-  auto load = [&](int n) {  // tile n: x, y or z of chunk n / 3 (the control thread)
-    const int c = n / 3, kind = n - 3 * c;
-    if (c >= nch) return;
-    const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
-    unsigned char* to = sb + (n & 3) * L::SLOT;
-    if (kind == 0)
-      load_tile<DY>(to, &mx, h, tok, seq, full + (n & 3));
-    else if (kind == 1)
-      load_tile<DY>(to, &my, h, tok, seq, full + (n & 3));
-    else
-      load_tile<DZ>(to, &mz, h, tok, seq, full + (n & 3));
-  };
-  auto tile = [&](int n) { return sb + (n & 3) * L::SLOT; };
+  const uint32_t tm = set_up(t, full, 8, tslot, abort);
+  auto tile = [&](int n) { return sb + (n & 3) * L::SLOT; };  // tile n: x, y or z of chunk n / 3
   auto wait_tile = [&](int n) { return mbar_wait(full + (n & 3), (n >> 2) & 1, abort); };
-  auto raw = [&](int c) {
-    return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
-  };
-  if (t.ctl)
-    for (int n = 0; n < 4; ++n) load(n);
-  const size_t sh = ((size_t)u.seq * a.H + h) * DY * DZ, uh = ((size_t)unit * a.H + h) * DY * DZ;
-  float s[N];
-  if (t.epi) {
-    load_state<DY, DZ, DQ, N>(u.at ? S_unit + uh : S_in ? S_in + sh : nullptr, t.lane, N * t.cq, s);
-    if (t.lane < DY) put_split<N>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cq, s);
+  if (t.w < CTL) {
+    more_registers();
+    const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
+    const size_t sh = ((size_t)u.seq * a.H + h) * DY * DZ, uh = ((size_t)unit * a.H + h) * DY * DZ;
+    float s[N];
+    load_state<DY, DZ, DQ, N>(u.at ? S_unit + uh : S_in ? S_in + sh : nullptr, t.lane, N * t.cg, s);
+    if (t.lane < DY) put_split<N>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
     fence_proxy_async_smem();
-  } else if (nch) {
-    fill_vec(raw(0), vec[0]);
-  }
-  __syncthreads();
-  for (int c = 0; c < nch; ++c) {
-    const int len = min(TC, u.len - c * TC), n0 = 3 * c;
-    const Vec& v = vec[c & 1];
-    const int row = u.row + c * TC + t.lane;  // of this thread's result
-    const bool on = t.lane < len;
-    if (t.ctl) {
-      wait_tile(n0);
-      wait_tile(n0 + 1);
+    bool off = meet(abort);
+    for (int c = 0; c < nch && !off; ++c) {
+      const int len = min(TC, u.len - c * TC), n0 = 3 * c;
+      const Vec& v = vec[c & 1];
+      const int row = u.row + c * TC + t.lane;  // of this thread's result
+      const bool on = t.lane < len;
+      // P: this thread's row t, columns [64 cg, 64 cg + 64)
+      mbar_wait(bar_p, c & 1, abort);
       tc_fence_after();
-      const uint32_t x = smem_u32(tile(n0)), y = smem_u32(tile(n0 + 1));
-#pragma unroll 1
-      for (int kk = 0; kk < DY / 16; ++kk)
-        umma_bf16(tm + P0, kmaj(x, HALF_TILE, kk), kmaj(y, HALF_TILE, kk),
-                  umma_idesc(128, 128, 0, 0), kk > 0);
-#pragma unroll 1
-      for (int p = 0; p < 2; ++p)
-#pragma unroll 1
-        for (int kk = 0; kk < DY / 16; ++kk)
-          umma_bf16(tm + O0, kmaj(x, HALF_TILE, kk), mnmaj(smem_u32(p ? s_lo : s_hi), L::HALF_S, kk),
-                    umma_idesc(128, DZ, 0, 1), p || kk);
-      umma_commit(bar_a);
-    }
-    if (t.epi) {
-      uint4 qr[DQ ? N / 8 : 1];
-      if (DQ) {
+      {
+        float x[64];
 #pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-          qr[i] = make_uint4(0, 0, 0, 0);
-          if (on)
-            qr[i] = *reinterpret_cast<const uint4*>(q + (size_t)row * ldq + (size_t)h * DZ +
-                                                    N * t.cq + 8 * i);
+        for (int j = 0; j < 2; ++j)
+          if (2 * t.cg + j <= t.q4) tmem_ld32(tl + P0 + 64 * t.cg + 32 * j, x + 32 * j);
+        tc_fence_before();
+        named_bar(2 + t.q4, 64);  // the lane quarter's columns of x y^T have been read
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int blk = 2 * t.cg + j;
+          uint32_t p[16];
+          if (blk > t.q4) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] = 0;
+          } else if (blk < t.q4 || v.mild) {
+            const bool diag = blk == t.q4;
+            const float r = v.row[t.lane];
+            const float* tb = (diag ? v.own : v.tab[t.q4 - 1]) + 32 * blk;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(tb + i);
+              float* y = x + 32 * j + i;
+              y[0] *= r * f.x;
+              y[1] *= r * f.y;
+              y[2] *= r * f.z;
+              y[3] *= r * f.w;
+              if (diag) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = i + e <= t.l ? y[e] : 0.f;
+              }
+              p[i / 2] = pack2bf(y[0], y[1]);
+              p[i / 2 + 1] = pack2bf(y[2], y[3]);
+            }
+          } else {
+            const float gh = v.hi[t.lane], gl = v.lo[t.lane];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 h2 = *reinterpret_cast<const float2*>(v.hi + 32 * blk + i);
+              const float2 l2 = *reinterpret_cast<const float2*>(v.lo + 32 * blk + i);
+              float* y = x + 32 * j + i;
+              y[0] = i <= t.l ? y[0] * __expf((gh - h2.x) + (gl - l2.x)) : 0.f;
+              y[1] = i + 1 <= t.l ? y[1] * __expf((gh - h2.y) + (gl - l2.y)) : 0.f;
+              p[i / 2] = pack2bf(y[0], y[1]);
+            }
+          }
+          tmem_st16(tl + P0 + 32 * t.cg + 16 * j, p);
         }
       }
       wait_tile(n0 + 1);
-      if (t.lane < DY) {
-        uint32_t hi[16], lo[16];
-        weigh(tile(n0 + 1), t, v.down, 1.f, len, hi, lo);
-        tmem_st16(tl + Y0 + 16 * t.cq, hi);
-        tmem_st16(tl + Y0 + 64 + 16 * t.cq, lo);
-      }
-      mbar_wait(bar_a, c & 1, abort);
+      if (t.lane < DY) weigh(tile(n0 + 1), t, v.w, len, tl + Y0);
+      mbar_wait(bar_s, c & 1, abort);
       tc_fence_after();
-      // P: this thread's row t, columns [32 cq, 32 cq + 32)
-      uint32_t p[16];
-      if (t.cq > t.q4) {
+      const float up = v.far[t.lane];
+      float f = 0.f;  // q_t . (far part of dq_t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = 0;
-      } else {
-        float x[32];
-        tmem_ld<32>(tl + P0 + 32 * t.cq, x);
-        if (t.cq == t.q4) {
-          const float gh = v.hi[t.lane], gl = v.lo[t.lane];
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 h4 = *reinterpret_cast<const float4*>(v.hi + 32 * t.cq + i);
-            const float4 l4 = *reinterpret_cast<const float4*>(v.lo + 32 * t.cq + i);
-            const float hh[4] = {h4.x, h4.y, h4.z, h4.w}, ll[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              x[i + j] = i + j <= t.l ? x[i + j] * __expf((gh - hh[j]) + (gl - ll[j])) : 0.f;
-          }
-        } else {
-          const float r = v.row[t.lane];
-          const float* tb = v.tab[t.q4 - 1] + 32 * t.cq;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(tb + i);
-            x[i] *= r * f.x;
-            x[i + 1] *= r * f.y;
-            x[i + 2] *= r * f.z;
-            x[i + 3] *= r * f.w;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = pack2bf(x[2 * i], x[2 * i + 1]);
-      }
-      tc_fence_before();
-      named_bar(1 + t.q4, 128);  // the lane quarter's columns of x y^T have been read
-      tc_fence_after();
-      tmem_st16(tl + P0 + 16 * t.cq, p);
-      float o[N], up = v.up[t.lane];
-      tmem_ld<N>(tl + O0 + N * t.cq, o);
-#pragma unroll
-      for (int i = 0; i < N; ++i) o[i] *= up;
-      tmem_st_f<N>(tl + O0 + N * t.cq, o);
-      if (DQ) {  // q_t . (far part of dq_t)
-        float f = 0.f;
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-          const uint32_t w4[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
+      for (int i = 0; i < N; i += 32) {
+        uint4 qr[DQ ? 4 : 1];
+        if (DQ) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            f = fmaf(__uint_as_float(w4[j] << 16), o[8 * i + 2 * j], f);
-            f = fmaf(__uint_as_float(w4[j] & 0xffff0000u), o[8 * i + 2 * j + 1], f);
+            qr[j] = make_uint4(0, 0, 0, 0);
+            if (on)
+              qr[j] = *reinterpret_cast<const uint4*>(q + (size_t)row * ldq + (size_t)h * DZ +
+                                                      N * t.cg + i + 8 * j);
           }
         }
-        part[t.cq * TC + t.lane] = a.scale * f;
+        float o[32];
+        tmem_ld32(tl + O0 + N * t.cg + i, o);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] *= up;
+        tmem_st32(tl + O0 + N * t.cg + i, o);
+        if (DQ) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w4[4] = {qr[j].x, qr[j].y, qr[j].z, qr[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f = fmaf(__uint_as_float(w4[e] << 16), o[8 * j + 2 * e], f);
+              f = fmaf(__uint_as_float(w4[e] & 0xffff0000u), o[8 * j + 2 * e + 1], f);
+            }
+          }
+        }
       }
+      if (DQ) part[t.cg * TC + t.lane] = a.scale * f;
       tmem_st_wait();
       if (len < TC && a.m.cu) {
         wait_tile(n0 + 2);
@@ -656,73 +744,122 @@ __global__ void __launch_bounds__(NTHR, 1)
         fence_proxy_async_smem();
       }
       tc_fence_before();
-    }
-    __syncthreads();
-    if (!t.epi) {
-      if (t.l == 0) {
-        tc_fence_after();
-        if (!*abort) {
-          load(n0 + 4);
-          load(n0 + 5);
-        }
-        wait_tile(n0 + 2);
-        const uint32_t z = smem_u32(tile(n0 + 2));
-        constexpr uint32_t id = umma_idesc(128, DZ, 0, 1);
-#pragma unroll 1
-        for (int kk = 0; kk < TC / 16; ++kk)
-          umma_ts(tm + O0, tm + P0 + 8 * kk, mnmaj(z, HALF_TILE, kk), id, true);
-#pragma unroll 1
-        for (int p = 0; p < 2; ++p)
-#pragma unroll 1
-          for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + D0, tm + Y0 + 64 * p + 8 * kk, mnmaj(z, HALF_TILE, kk), id, p || kk);
-        umma_commit(bar_c);
-      }
-      __syncwarp();
-      if (c + 1 < nch) fill_vec(raw(c + 1), vec[(c + 1) & 1]);
-      if (t.l == 0) {
-        mbar_wait(bar_c, c & 1, abort);
-        if (!*abort) load(n0 + 6);
-      }
-    } else {
-      if (DQ && t.tid < len)
-        far[(size_t)row * a.H + h] = (part[t.tid] + part[TC + t.tid]) +
-                                     (part[2 * TC + t.tid] + part[3 * TC + t.tid]);
-      mbar_wait(bar_c, c & 1, abort);
+      off = meet(abort);
+      if (DQ && t.tid < len) far[(size_t)row * a.H + h] = part[t.tid] + part[TC + t.tid];
+      mbar_wait(bar_o, c & 1, abort);
       tc_fence_after();
-      float o[N];
+      store_row<N>(tl + O0 + N * t.cg, out + ((size_t)row * a.H + h) * DZ + N * t.cg, a.scale, on);
+      mbar_wait(bar_d, c & 1, abort);
+      tc_fence_after();
       if (t.lane < DY) {
-        tmem_ld<N>(tl + D0 + N * t.cq, o);
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = fmaf(v.whole, s[i], o[i]);
-        put_split<N>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cq, s);
+        add_state<N>(tl + D0 + N * t.cg, v.w.whole, s);
+        put_split<N>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
         fence_proxy_async_smem();
       }
-      tmem_ld<N>(tl + O0 + N * t.cq, o);
-      if (on) store_row<N>(out + ((size_t)row * a.H + h) * DZ + N * t.cq, o, a.scale);
       tc_fence_before();
+      off = meet(abort) || off;
     }
-    if (__syncthreads_or(*abort != 0)) break;
+    if (u.at == u.n - 1 && S_out) store_state<DY, DZ, DQ, N>(S_out + sh, t.lane, N * t.cg, s);
+  } else {
+    fewer_registers();
+    if (t.w == CTL) {
+      auto load = [&](int n) {
+        const int c = n / 3, kind = n - 3 * c;
+        if (c >= nch) return;
+        const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
+        uint64_t* bar = full + (n & 3);
+        if (kind == 0)
+          load_tile<DY>(tile(n), &mx, h, tok, seq, bar);
+        else if (kind == 1)
+          load_tile<DY>(tile(n), &my, h, tok, seq, bar);
+        else
+          load_tile<DZ>(tile(n), &mz, h, tok, seq, bar);
+      };
+      auto products = [&](int c) {  // x y^T
+        wait_tile(3 * c);
+        wait_tile(3 * c + 1);
+        const uint32_t x = smem_u32(tile(3 * c)), y = smem_u32(tile(3 * c + 1));
+#pragma unroll
+        for (int kk = 0; kk < DY / 16; ++kk)
+          umma_bf16(tm + P0, kmaj(x, HALF_TILE, kk), kmaj(y, HALF_TILE, kk),
+                    umma_idesc(128, 128, 0, 0), kk > 0);
+        umma_commit(bar_p);
+      };
+      if (t.l == 0) {
+        for (int n = 0; n < 4; ++n) load(n);
+        if (nch) products(0);
+      }
+      __syncwarp();
+      bool off = meet(abort);
+      for (int c = 0; c < nch && !off; ++c) {
+        const int n0 = 3 * c;
+        if (t.l == 0) {
+          tc_fence_after();
+          const uint32_t x = smem_u32(tile(n0));
+#pragma unroll 1
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int kk = 0; kk < DY / 16; ++kk)
+              umma_bf16(tm + O0, kmaj(x, HALF_TILE, kk), mnmaj(smem_u32(p ? s_lo : s_hi), L::HALF_S, kk),
+                        umma_idesc(128, DZ, 0, 1), p || kk);
+          umma_commit(bar_s);
+        }
+        __syncwarp();
+        off = meet(abort);
+        if (t.l == 0) {
+          tc_fence_after();
+          if (!*abort) {
+            load(n0 + 4);
+            load(n0 + 5);
+          }
+          wait_tile(n0 + 2);
+          const uint32_t z = smem_u32(tile(n0 + 2));
+          constexpr uint32_t id = umma_idesc(128, DZ, 0, 1);
+#pragma unroll
+          for (int kk = 0; kk < TC / 16; ++kk)
+            umma_ts(tm + O0, tm + P0 + 8 * kk, mnmaj(z, HALF_TILE, kk), id, true);
+          umma_commit(bar_o);
+#pragma unroll 1
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int kk = 0; kk < TC / 16; ++kk)
+              umma_ts(tm + D0, tm + Y0 + 64 * p + 8 * kk, mnmaj(z, HALF_TILE, kk), id, p || kk);
+          umma_commit(bar_d);
+          mbar_wait(bar_o, c & 1, abort);  // P has been read
+          if (c + 1 < nch) products(c + 1);
+          mbar_wait(bar_d, c & 1, abort);
+          if (!*abort) load(n0 + 6);
+        }
+        __syncwarp();
+        off = meet(abort) || off;
+      }
+    } else if (t.w == DEC) {
+      auto raw = [&](int c) {
+        return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
+      };
+      Raw ahead = {};
+      if (nch) fill_vec<false>(raw(0), 1.f, vec[0]);
+      if (nch > 1) ahead = raw(1);
+      bool off = meet(abort);
+      for (int c = 0; c < nch && !off; ++c) {
+        off = meet(abort);
+        if (c + 1 < nch) fill_vec<false>(ahead, 1.f, vec[(c + 1) & 1]);
+        if (c + 2 < nch) ahead = raw(c + 2);
+        off = meet(abort) || off;
+      }
+    }
   }
-  if (t.epi && u.at == u.n - 1 && S_out) store_state<DY, DZ, DQ, N>(S_out + sh, t.lane, N * t.cq, s);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (t.ctl && *abort) {
-    *a.status = DEV_TIMEOUT;
-    drain(full, 4, 0);
-    drain(full, 4, ~0u);
-  }
-  __syncthreads();
-  if (t.w == NEPI / 32) tmem_dealloc(tm, 512);
+  tear_down(t, full, 4, tm, abort, a.status);
 }
 
 // ------------------------------------------------------------------ dk, dv and dg
-// From a unit's last chunk to its first, with R in registers (row: key, as in memory).
-// Rows of the accumulators are the tokens s, columns the tokens t they act on:
-//   k q^T, v dO^T (masked, L_ts), v R^T and k R (scaled by e^{gamma_C - gamma_s});
-//   dk = P2 q onto the one, dv = P1 dO onto the other; then R's sum scale (e^gamma q)^T dO.
-// dg runs along: with rows and cols the sums of A (gdn_lin.cu) over s and over t,
+// From a unit's last chunk to its first, with R in registers (row: key, as in memory). The
+// rows of a chunk's accumulators are its tokens s, the columns the tokens t they act on:
+//   k q^T, v dO^T (masked by L_ts, t >= s), v R^T and k R (scaled by e^{gamma_C - gamma_s});
+//   dk = P2 q onto the one, dv = P1 dO onto the other.
+// R's sum scale (e^gamma q)^T dO needs only q and dO and comes first, so that R's next tiles
+// are written under the last products. dg runs along: with rows and cols the sums of A
+// (gdn_lin.cu) over s and over t,
 //   dg_u = X + sum_{t >= u} (rows_t + a_t - cols_t - b_t),  X' = X + sum_t (a_t - b_t),
 // X = <S, R> behind the chunk, taken from the states themselves at the unit's end.
 template <int DK, int DV>
@@ -731,7 +868,7 @@ struct BackSm {
   static constexpr uint32_t V = 0, K = SLOT, Q = 2 * SLOT, DO = 3 * SLOT;
   static constexpr uint32_t R_HI = 4 * SLOT, R_LO = R_HI + STATE, VEC = R_LO + STATE;
   static constexpr uint32_t ROWS = VEC + 2 * sizeof(Vec), COLS = ROWS + 4 * TC * 4,
-                            FAR = COLS + 4 * TC * 4, RED = FAR + 4 * TC * 4, BAR = RED + 64;
+                            FAR = COLS + 2 * TC * 4, RED = FAR + 2 * TC * 4, BAR = RED + 64;
   static constexpr uint32_t BYTES = BAR + 128 + 1024;
 };
 // x[0..31] summed over the warp's lanes; lane j returns the sum of x[j].
@@ -757,8 +894,9 @@ __global__ void __launch_bounds__(NTHR, 1)
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ CUtensorMap mo) {
   using L = BackSm<DK, DV>;
-  constexpr int NK = DK / 4, NV = DV / 4;
-  constexpr uint32_t A1 = 0, A2 = 128, G1 = 256, G2 = 384;  // G1: dk, then R's sum; G2: dv
+  constexpr int NK = DK / 2, NV = DV / 2;
+  // A1: k q^T, then P1 and P2; A2: v dO^T; G1: the weighed q, then dk; G2: R's sum, then dv
+  constexpr uint32_t A1 = 0, A2 = 128, G1 = 256, G2 = 384;
   chain();
   const int unit = blockIdx.x / a.H, h = blockIdx.x - unit * a.H;
   const size_t uh = (size_t)unit * a.H + h;
@@ -777,247 +915,173 @@ __global__ void __launch_bounds__(NTHR, 1)
   float* farb = reinterpret_cast<float*>(sb + L::FAR);   // [column group][s]
   float* red = reinterpret_cast<float*>(sb + L::RED);
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [4] v, k, q, dO
-  uint64_t *bar_a = full + 4, *bar_f = full + 5, *bar_c = full + 6, *bar_e = full + 7;
+  // MMAs: R's sum, k q^T and v dO^T, products with R, results
+  uint64_t *bar_e = full + 4, *bar_a = full + 5, *bar_f = full + 6, *bar_c = full + 7;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 8);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   const int nch = (u.len + TC - 1) / TC;
-  if (t.ctl) {
-    for (int i = 0; i < 8; ++i) mbar_init(full + i, 1);
-    *abort = 0;
-    fence_mbar_init();
-  }
-  if (t.w == NEPI / 32) tmem_alloc(tslot, 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = *tslot, tl = tm + ((uint32_t)(32 * t.q4) << 16);
-  auto load = [&](int kind, int i) {  // a tile of the i-th chunk from the end (control thread)
-    if (i >= nch) return;
-    const int c = nch - 1 - i;
-    const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
-    unsigned char* to = sb + kind * L::SLOT;
-    if (kind == 0)
-      load_tile<DV>(to, &mv, h, tok, seq, full);
-    else if (kind == 1)
-      load_tile<DK>(to, &mk, h, tok, seq, full + 1);
-    else if (kind == 2)
-      load_tile<DK>(to, &mq, h, tok, seq, full + 2);
-    else
-      load_tile<DV>(to, &mo, h, tok, seq, full + 3);
-  };
-  auto raw = [&](int i) {
-    const int c = nch - 1 - i;
-    return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
-  };
-  if (t.ctl)
-    for (int k = 0; k < 4; ++k) load(k, 0);
-  const size_t sh = ((size_t)u.seq * a.H + h) * DK * DV;
-  const bool last = u.at == u.n - 1;
-  float r[NV];
-  if (t.epi) {
+  const uint32_t tm = set_up(t, full, 8, tslot, abort);
+  if (t.w < CTL) {
+    more_registers();
+    const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
+    const size_t sh = ((size_t)u.seq * a.H + h) * DK * DV;
+    const bool last = u.at == u.n - 1;
+    float r[NV];
     const float* from = last ? (dS_out ? dS_out + sh : nullptr) : R_unit + uh * DK * DV;
-    load_state<DK, DV, false, NV>(from, t.lane, NV * t.cq, r);
-    if (t.lane < DK) put_split<NV>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cq, r);
+    load_state<DK, DV, false, NV>(from, t.lane, NV * t.cg, r);
+    if (t.lane < DK) put_split<NV>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
     fence_proxy_async_smem();
-    const float* S = !from ? nullptr : last ? S_end + sh : S_unit + (uh + a.H) * DK * DV;
-    float x = 0.f;
-    if (S && t.lane < DK) {
+    {
+      const float* S = !from ? nullptr : last ? S_end + sh : S_unit + (uh + a.H) * DK * DV;
+      float x = 0.f;
+      if (S && t.lane < DK) {
 #pragma unroll
-      for (int i = 0; i < NV; i += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(S + (size_t)t.lane * DV + NV * t.cq + i);
-        x = fmaf(r[i], y.x, x);
-        x = fmaf(r[i + 1], y.y, x);
-        x = fmaf(r[i + 2], y.z, x);
-        x = fmaf(r[i + 3], y.w, x);
+        for (int i = 0; i < NV; i += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(S + (size_t)t.lane * DV + NV * t.cg + i);
+          x = fmaf(r[i], y.x, x);
+          x = fmaf(r[i + 1], y.y, x);
+          x = fmaf(r[i + 2], y.z, x);
+          x = fmaf(r[i + 3], y.w, x);
+        }
       }
+      x = lane_sum<32>(x);
+      if (t.l == 0) red[t.w] = x;
     }
-    x = lane_sum<32>(x);
-    if (t.l == 0) red[t.w] = x;
-  } else if (nch) {
-    fill_vec(raw(0), vec[0]);
-  }
-  __syncthreads();
-  float X = 0.f, sum = 0.f;  // of warp 0
-  if (t.w == 0)
-    for (int i = 0; i < NEPI / 32; ++i) X += red[i];
-  for (int i = 0; i < nch; ++i) {
-    const int c = nch - 1 - i, len = min(TC, u.len - c * TC), ph = i & 1;
-    const Vec& v = vec[ph];
-    const int row0 = u.row + c * TC, row = row0 + t.lane;
-    const bool on = t.lane < len;
-    if (len < TC && a.m.cu) {
-      if (t.epi) {
-        mbar_wait(full + 2, ph, abort);
+    bool off = meet(abort);
+    float X = 0.f, sum = 0.f;  // of warp 0
+    if (t.w == 0)
+      for (int i = 0; i < NEPI / 32; ++i) X += red[i];
+    for (int i = 0; i < nch && !off; ++i) {
+      const int c = nch - 1 - i, len = min(TC, u.len - c * TC), ph = i & 1;
+      const Vec& v = vec[ph];
+      const int row0 = u.row + c * TC, row = row0 + t.lane;
+      const bool on = t.lane < len;
+      mbar_wait(full + 2, ph, abort);
+      if (len < TC && a.m.cu) {
         mbar_wait(full + 3, ph, abort);
         zero_rows<DK>(sb + L::Q, len, t.tid);
         zero_rows<DV>(sb + L::DO, len, t.tid);
         fence_proxy_async_smem();
+        named_bar(6, NEPI);
       }
-      __syncthreads();
-    }
-    if (t.ctl) {
-      const uint32_t sv = smem_u32(sb + L::V), sk = smem_u32(sb + L::K), sq = smem_u32(sb + L::Q),
-                     so = smem_u32(sb + L::DO);
-      tc_fence_after();
-      mbar_wait(full + 1, ph, abort);
-      mbar_wait(full + 2, ph, abort);
-#pragma unroll 1
-      for (int kk = 0; kk < DK / 16; ++kk)
-        umma_bf16(tm + A1, kmaj(sk, HALF_TILE, kk), kmaj(sq, HALF_TILE, kk),
-                  umma_idesc(128, 128, 0, 0), kk > 0);
-      mbar_wait(full + 0, ph, abort);
-      mbar_wait(full + 3, ph, abort);
-#pragma unroll 1
-      for (int kk = 0; kk < DV / 16; ++kk)
-        umma_bf16(tm + A2, kmaj(sv, HALF_TILE, kk), kmaj(so, HALF_TILE, kk),
-                  umma_idesc(128, 128, 0, 0), kk > 0);
-      umma_commit(bar_a);
-#pragma unroll 1
-      for (int p = 0; p < 2; ++p)
-#pragma unroll 1
-        for (int kk = 0; kk < DV / 16; ++kk)
-          umma_bf16(tm + G1, kmaj(sv, HALF_TILE, kk), kmaj(smem_u32(p ? r_lo : r_hi), L::HALF_R, kk),
-                    umma_idesc(128, DK, 0, 0), p || kk);
-#pragma unroll 1
-      for (int p = 0; p < 2; ++p)
-#pragma unroll 1
-        for (int kk = 0; kk < DK / 16; ++kk)
-          umma_bf16(tm + G2, kmaj(sk, HALF_TILE, kk), mnmaj(smem_u32(p ? r_lo : r_hi), L::HALF_R, kk),
-                    umma_idesc(128, DV, 0, 1), p || kk);
-      umma_commit(bar_f);
-    }
-    if (t.epi) {
-      uint32_t qh[16], ql[16], p1[16], p2[16];
-      mbar_wait(full + 2, ph, abort);
-      if (t.lane < DK) weigh(sb + L::Q, t, v.up, a.scale, len, qh, ql);
-      mbar_wait(bar_a, ph, abort);
-      tc_fence_after();
-      // this thread's row s, columns t in [32 cq, 32 cq + 32)
-      if (t.cq < t.q4) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) p1[j] = p2[j] = 0;
-        cols[t.cq * TC + t.lane] = 0.f;
-        rows[t.q4 * TC + 32 * t.cq + t.l] = 0.f;
-      } else {
-        float x[32], y[32], f[4], cs = 0.f;
-        tmem_ld<32>(tl + A1 + 32 * t.cq, x);
-        tmem_ld<32>(tl + A2 + 32 * t.cq, y);
-        const bool diag = t.cq == t.q4;
-        const float gh = v.hi[t.lane], gl = v.lo[t.lane];
-        const float tb = diag ? 0.f : a.scale * v.tab[t.cq - 1][t.lane];
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          if (diag) {
-            const float4 h4 = *reinterpret_cast<const float4*>(v.hi + 32 * t.cq + j);
-            const float4 l4 = *reinterpret_cast<const float4*>(v.lo + 32 * t.cq + j);
-            const float hh[4] = {h4.x, h4.y, h4.z, h4.w}, ll[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              f[e] = a.scale * __expf((hh[e] - gh) + (ll[e] - gl));
-          } else {
-            const float4 f4 = *reinterpret_cast<const float4*>(v.row + 32 * t.cq + j);
-            f[0] = tb * f4.x, f[1] = tb * f4.y, f[2] = tb * f4.z, f[3] = tb * f4.w;
-          }
-          float z[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool in = !diag || j + e >= t.l;
-            const float px = in ? x[j + e] * f[e] : 0.f, py = in ? y[j + e] * f[e] : 0.f;
-            z[e] = !diag || j + e > t.l ? x[j + e] * py : 0.f;
-            cs += z[e];
-            x[j + e] = px;
-            y[j + e] = py;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            p1[(j + e) / 2] = pack2bf(x[j + e], x[j + e + 1]);
-            p2[(j + e) / 2] = pack2bf(y[j + e], y[j + e + 1]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[j + e] = z[e];
-        }
-        cols[t.cq * TC + t.lane] = cs;
-        const float rs = lane_columns(x);
-        rows[t.q4 * TC + 32 * t.cq + t.l] = rs;
+      if (t.lane < DK) {
+        weigh(sb + L::Q, t, v.w, len, tl + G1);
+        tmem_st_wait();
       }
       tc_fence_before();
-      named_bar(1 + t.q4, 128);  // the lane quarter's products have been read
+      off = meet(abort);
+      mbar_wait(bar_e, ph, abort);
       tc_fence_after();
-      tmem_st16(tl + A1 + 16 * t.cq, p1);
-      tmem_st16(tl + A2 + 16 * t.cq, p2);
-      if (t.lane < DK) {
-        tmem_st16(tl + A1 + 64 + 16 * t.cq, qh);
-        tmem_st16(tl + A2 + 64 + 16 * t.cq, ql);
+      if (t.lane < DK) add_state<NV>(tl + G2 + NV * t.cg, v.w.whole, r);
+      tc_fence_before();
+      off = meet(abort) || off;  // G1 and G2 are free: the products with R follow
+      mbar_wait(bar_a, ph, abort);
+      tc_fence_after();
+      {  // this thread's row s, columns t in [64 cg, 64 cg + 64)
+        float x[64], cs = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (2 * t.cg + j >= t.q4) tmem_ld32(tl + A1 + 64 * t.cg + 32 * j, x + 32 * j);
+        tc_fence_before();
+        named_bar(2 + t.q4, 64);  // the lane quarter's k q^T has been read
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int blk = 2 * t.cg + j;
+          uint32_t p1[16], p2[16];
+          if (blk < t.q4) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) p1[e] = p2[e] = 0;
+            rows[t.q4 * TC + 32 * blk + t.l] = 0.f;
+          } else {
+            float y[32];
+            tmem_ld32(tl + A2 + 32 * blk, y);
+            const bool diag = blk == t.q4;
+            const float gh = v.hi[t.lane], gl = v.lo[t.lane];
+            const float tb = a.scale * (diag ? v.own[t.lane] : v.tab[blk - 1][t.lane]);
+            const bool direct = diag && !v.mild;
+            float* xx = x + 32 * j;
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 f2 = *reinterpret_cast<const float2*>(v.row + 32 * blk + e);
+              float f[2] = {tb * f2.x, tb * f2.y};
+              if (direct) {
+                const float2 h2 = *reinterpret_cast<const float2*>(v.hi + 32 * blk + e);
+                const float2 l2 = *reinterpret_cast<const float2*>(v.lo + 32 * blk + e);
+                f[0] = a.scale * __expf((h2.x - gh) + (l2.x - gl));
+                f[1] = a.scale * __expf((h2.y - gh) + (l2.y - gl));
+              }
+              float px[2], py[2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const bool in = !diag || e + z >= t.l;
+                px[z] = in ? xx[e + z] * f[z] : 0.f;
+                py[z] = in ? y[e + z] * f[z] : 0.f;
+                const float pair = !diag || e + z > t.l ? xx[e + z] * py[z] : 0.f;
+                xx[e + z] = pair;
+                cs += pair;
+              }
+              p1[e / 2] = pack2bf(px[0], px[1]);
+              p2[e / 2] = pack2bf(py[0], py[1]);
+            }
+            rows[t.q4 * TC + 32 * blk + t.l] = lane_columns(xx);
+          }
+          tmem_st16(tl + A1 + 32 * t.cg + 16 * j, p1);
+          tmem_st16(tl + A1 + 64 + 32 * t.cg + 16 * j, p2);
+        }
+        cols[t.cg * TC + t.lane] = cs;
       }
       mbar_wait(bar_f, ph, abort);
       tc_fence_after();
-      const float down = v.down[t.lane];
-      {
-        float x[NK], b = 0.f;
-        tmem_ld<NK>(tl + G1 + NK * t.cq, x);
+      const float down = v.far[t.lane];
+      float b = 0.f;
 #pragma unroll
-        for (int j = 0; j < NK; j += 8) {
+      for (int e = 0; e < NK; e += 32) {
+        float x[32];
+        tmem_ld32(tl + G1 + NK * t.cg + e, x);
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
           const uint4 k4 = *reinterpret_cast<const uint4*>(
-              at8(sb + L::K, HALF_TILE, t.lane, NK * t.cq + j));
+              at8(sb + L::K, HALF_TILE, t.lane, NK * t.cg + e + j));
           const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[j + 2 * e] *= down;
-            x[j + 2 * e + 1] *= down;
-            b = fmaf(__uint_as_float(kk[e] << 16), x[j + 2 * e], b);
-            b = fmaf(__uint_as_float(kk[e] & 0xffff0000u), x[j + 2 * e + 1], b);
+          for (int z = 0; z < 4; ++z) {
+            x[j + 2 * z] *= down;
+            x[j + 2 * z + 1] *= down;
+            b = fmaf(__uint_as_float(kk[z] << 16), x[j + 2 * z], b);
+            b = fmaf(__uint_as_float(kk[z] & 0xffff0000u), x[j + 2 * z + 1], b);
           }
         }
-        farb[t.cq * TC + t.lane] = b;
-        tmem_st_f<NK>(tl + G1 + NK * t.cq, x);
+        tmem_st32(tl + G1 + NK * t.cg + e, x);
       }
-      {
-        float x[NV];
-        tmem_ld<NV>(tl + G2 + NV * t.cq, x);
+      farb[t.cg * TC + t.lane] = b;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) x[j] *= down;
-        tmem_st_f<NV>(tl + G2 + NV * t.cq, x);
+      for (int e = 0; e < NV; e += 32) {
+        float x[32];
+        tmem_ld32(tl + G2 + NV * t.cg + e, x);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] *= down;
+        tmem_st32(tl + G2 + NV * t.cg + e, x);
       }
       tmem_st_wait();
       tc_fence_before();
-    }
-    __syncthreads();
-    if (!t.epi) {
-      if (t.l == 0) {
-        tc_fence_after();
-        const uint32_t sq = smem_u32(sb + L::Q), so = smem_u32(sb + L::DO);
-        if (!*abort) {
-          load(0, i + 1);
-          load(1, i + 1);
-        }
-#pragma unroll 1
-        for (int kk = 0; kk < TC / 16; ++kk)
-          umma_ts(tm + G1, tm + A2 + 8 * kk, mnmaj(sq, HALF_TILE, kk), umma_idesc(128, DK, 0, 1), true);
-#pragma unroll 1
-        for (int kk = 0; kk < TC / 16; ++kk)
-          umma_ts(tm + G2, tm + A1 + 8 * kk, mnmaj(so, HALF_TILE, kk), umma_idesc(128, DV, 0, 1), true);
-        umma_commit(bar_c);
-      }
-      __syncwarp();
-      if (i + 1 < nch) fill_vec(raw(i + 1), vec[ph ^ 1]);
-    } else {
+      off = meet(abort) || off;
+      if (t.lane < DK) put_split<NV>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
+      fence_proxy_async_smem();
       if (t.w == 0) {  // dg: 4 tokens for each lane
         float x[4], ab = 0.f, suf = 0.f;
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
           const int e = 4 * t.l + j;
-          float rw = 0.f, cl = 0.f, b = 0.f, f = 0.f;
+          float rw = 0.f, cl = 0.f, bb = 0.f, f = 0.f;
           if (e < len) {
             f = far[(size_t)(row0 + e) * a.H + h];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              rw += rows[p * TC + e];
-              cl += cols[p * TC + e];
-              b += farb[p * TC + e];
-            }
+            rw = (rows[e] + rows[TC + e]) + (rows[2 * TC + e] + rows[3 * TC + e]);
+            cl = cols[e] + cols[TC + e];
+            bb = farb[e] + farb[TC + e];
           }
-          ab += f - b;
-          x[j] = (suf += (rw - cl) + (f - b));
+          ab += f - bb;
+          x[j] = (suf += (rw - cl) + (f - bb));
         }
         float all = suf;
 #pragma unroll
@@ -1039,60 +1103,127 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       mbar_wait(bar_c, ph, abort);
       tc_fence_after();
-      float x[NK > NV ? NK : NV];
-      tmem_ld<NK>(tl + G1 + NK * t.cq, x);
-      if (on) store_row<NK>(dk + ((size_t)row * a.H + h) * DK + NK * t.cq, x, 1.f);
-      tmem_ld<NV>(tl + G2 + NV * t.cq, x);
-      if (on) store_row<NV>(dv + ((size_t)row * a.H + h) * DV + NV * t.cq, x, 1.f);
+      store_row<NK>(tl + G1 + NK * t.cg, dk + ((size_t)row * a.H + h) * DK + NK * t.cg, 1.f, on);
+      store_row<NV>(tl + G2 + NV * t.cg, dv + ((size_t)row * a.H + h) * DV + NV * t.cg, 1.f, on);
       tc_fence_before();
+      off = meet(abort) || off;
     }
-    __syncthreads();
-    if (!t.epi) {
-      if (t.l == 0) {
-        tc_fence_after();
-        if (!*abort) load(2, i + 1);
-        const uint32_t so = smem_u32(sb + L::DO);
-#pragma unroll 1
-        for (int p = 0; p < 2; ++p)
-#pragma unroll 1
-          for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + G1, tm + (p ? A2 : A1) + 64 + 8 * kk, mnmaj(so, HALF_TILE, kk),
-                    umma_idesc(128, DV, 0, 1), p || kk);
-        umma_commit(bar_e);
-        mbar_wait(bar_e, ph, abort);
-        if (!*abort) load(3, i + 1);
-      }
+    if (u.at == 0 && dS_in) store_state<DK, DV, false, NV>(dS_in + sh, t.lane, NV * t.cg, r);
+    if (t.w == 0 && dgsum) {
+      sum = lane_sum<32>(sum);
+      if (t.l == 0) dgsum[uh] = sum;
+    }
+  } else {
+    fewer_registers();
+    if (t.w == CTL) {
+      auto load = [&](int kind, int i) {  // a tile of the i-th chunk from the end
+        if (i >= nch) return;
+        const int c = nch - 1 - i;
+        const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
+        unsigned char* to = sb + kind * L::SLOT;
+        if (kind == 0)
+          load_tile<DV>(to, &mv, h, tok, seq, full);
+        else if (kind == 1)
+          load_tile<DK>(to, &mk, h, tok, seq, full + 1);
+        else if (kind == 2)
+          load_tile<DK>(to, &mq, h, tok, seq, full + 2);
+        else
+          load_tile<DV>(to, &mo, h, tok, seq, full + 3);
+      };
+      if (t.l == 0)
+        for (int k = 3; k >= 0; --k) load(k, 0);
       __syncwarp();
-    } else {
-      mbar_wait(bar_e, ph, abort);
-      tc_fence_after();
-      if (t.lane < DK) {
-        float x[NV];
-        tmem_ld<NV>(tl + G1 + NV * t.cq, x);
+      const uint32_t sv = smem_u32(sb + L::V), sk = smem_u32(sb + L::K), sq = smem_u32(sb + L::Q),
+                     so = smem_u32(sb + L::DO);
+      bool off = meet(abort);
+      for (int i = 0; i < nch && !off; ++i) {
+        const int ph = i & 1;
+        off = meet(abort);  // the weighed q is there (and a tail's rows are zeros)
+        if (t.l == 0) {
+          tc_fence_after();
+          mbar_wait(full + 3, ph, abort);
+#pragma unroll 1
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) r[j] = fmaf(v.whole, r[j], x[j]);
-        put_split<NV>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cq, r);
-        fence_proxy_async_smem();
+            for (int kk = 0; kk < TC / 16; ++kk)
+              umma_ts(tm + G2, tm + G1 + 64 * p + 8 * kk, mnmaj(so, HALF_TILE, kk),
+                      umma_idesc(128, DV, 0, 1), p || kk);
+          umma_commit(bar_e);
+          mbar_wait(full + 1, ph, abort);
+          mbar_wait(full + 2, ph, abort);
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            umma_bf16(tm + A1, kmaj(sk, HALF_TILE, kk), kmaj(sq, HALF_TILE, kk),
+                      umma_idesc(128, 128, 0, 0), kk > 0);
+          mbar_wait(full + 0, ph, abort);
+#pragma unroll
+          for (int kk = 0; kk < DV / 16; ++kk)
+            umma_bf16(tm + A2, kmaj(sv, HALF_TILE, kk), kmaj(so, HALF_TILE, kk),
+                      umma_idesc(128, 128, 0, 0), kk > 0);
+          umma_commit(bar_a);
+        }
+        __syncwarp();
+        off = meet(abort) || off;
+        if (t.l == 0) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int kk = 0; kk < DV / 16; ++kk)
+              umma_bf16(tm + G1, kmaj(sv, HALF_TILE, kk), kmaj(smem_u32(p ? r_lo : r_hi), L::HALF_R, kk),
+                        umma_idesc(128, DK, 0, 0), p || kk);
+          // dv takes the first part alone: it is rounded to as many bits when it is stored
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            umma_bf16(tm + G2, kmaj(sk, HALF_TILE, kk), mnmaj(smem_u32(r_hi), L::HALF_R, kk),
+                      umma_idesc(128, DV, 0, 1), kk > 0);
+          umma_commit(bar_f);
+        }
+        __syncwarp();
+        off = meet(abort) || off;
+        if (t.l == 0) {
+          tc_fence_after();
+          if (!*abort) {
+            load(0, i + 1);
+            load(1, i + 1);
+          }
+#pragma unroll
+          for (int kk = 0; kk < TC / 16; ++kk)
+            umma_ts(tm + G1, tm + A1 + 64 + 8 * kk, mnmaj(sq, HALF_TILE, kk),
+                    umma_idesc(128, DK, 0, 1), true);
+#pragma unroll
+          for (int kk = 0; kk < TC / 16; ++kk)
+            umma_ts(tm + G2, tm + A1 + 8 * kk, mnmaj(so, HALF_TILE, kk), umma_idesc(128, DV, 0, 1), true);
+          umma_commit(bar_c);
+          mbar_wait(bar_c, ph, abort);
+          if (!*abort) {
+            load(2, i + 1);
+            load(3, i + 1);
+          }
+        }
+        __syncwarp();
+        off = meet(abort) || off;
       }
-      tc_fence_before();
+    } else if (t.w == DEC) {
+      auto raw = [&](int i) {
+        const int c = nch - 1 - i;
+        return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
+      };
+      Raw ahead = {};
+      if (nch) fill_vec<true>(raw(0), a.scale, vec[0]);
+      if (nch > 1) ahead = raw(1);
+      bool off = meet(abort);
+      for (int i = 0; i < nch && !off; ++i) {
+        off = meet(abort);
+        if (i + 1 < nch) fill_vec<true>(ahead, a.scale, vec[(i + 1) & 1]);
+        if (i + 2 < nch) ahead = raw(i + 2);
+        off = meet(abort) || off;
+        off = meet(abort) || off;
+        off = meet(abort) || off;
+      }
     }
-    if (__syncthreads_or(*abort != 0)) break;
   }
-  if (t.epi && u.at == 0 && dS_in) store_state<DK, DV, false, NV>(dS_in + sh, t.lane, NV * t.cq, r);
-  if (t.w == 0 && dgsum) {
-    sum = lane_sum<32>(sum);
-    if (t.l == 0) dgsum[uh] = sum;
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (t.ctl && *abort) {
-    *a.status = DEV_TIMEOUT;
-    drain(full, 4, 0);
-    drain(full, 4, ~0u);
-  }
-  __syncthreads();
-  if (t.w == NEPI / 32) tmem_dealloc(tm, 512);
+  tear_down(t, full, 4, tm, abort, a.status);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1169,16 +1300,23 @@ cudaError_t tile_map(CUtensorMap* map, const void* base, const gdn_lin_shape& s,
   return make_tile_map(map, base, dims, strides, TC);
 }
 
-template <class K>
-cudaError_t allow(K kernel, uint32_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Shared memory of a kernel, and whether its launch holds the registers that its warpgroups
+// share out (a smaller pool would leave them waiting).
+template <auto KERNEL>
+cudaError_t allow(uint32_t bytes, int registers) {
+  static const int has = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (has < registers) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 template <int DK, int DV>
 cudaError_t run_tc(const LinCall& c, bool back) {
   const gdn_lin_shape& s = c.s;
   const TcPlan p = tc_plan(s, c.cu, c.cu != nullptr, back, c.ws);
-  const Args a = {p.m, s.H, p.chunks, s.scale, (const bf*)c.g, c.decay, s.ldg, p.status};
+  const Args a = {p.m, s.H, s.scale, (const bf*)c.g, c.decay, s.ldg, p.status};
   CUtensorMap mq, mk, mv, mo;
   cudaError_t e;
   if ((e = tile_map(&mq, c.q, s, DK, s.ldq)) || (e = tile_map(&mk, c.k, s, DK, s.ldk)) ||
@@ -1188,34 +1326,41 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   if (c.cu && (e = lin_plan(p.m, p.first, p.owner, p.status, c.st))) return e;
   bool clear = !c.cu;  // the first kernel of an unpacked call resets the status word
   const dim3 grid(p.m.cap * s.H), block(NTHR);
-  auto go = [&](auto kernel, uint32_t smem, auto... rest) {
-    const cudaError_t f = allow(kernel, smem);
-    return f ? f : launch(kernel, grid, block, (int)smem, c.st, 1, a, rest...);
+  auto go = [&](auto kernel, cudaError_t ready, uint32_t smem, auto... rest) {
+    return ready ? ready : launch(kernel, grid, block, (int)smem, c.st, 1, a, rest...);
   };
+#define GO(kernel, Sm, regs, ...) \
+  go(kernel, allow<kernel>(Sm::BYTES, regs), Sm::BYTES, __VA_ARGS__)
+  using SmKV = StateSm<DK, DV>;
+  using SmVK = StateSm<DV, DK>;
   if (p.many) {
     prof_mark(c.st, "lin_tc_state");
-    e = back ? go(k_lin_tc_state<DV, DK, false, true>, StateSm<DV, DK>::BYTES, p.whole[0], p.D, clear, mv, mk)
-             : go(k_lin_tc_state<DK, DV, false, false>, StateSm<DK, DV>::BYTES, p.whole[0], p.D, clear, mk, mv);
+    e = back ? GO((k_lin_tc_state<DV, DK, false, true>), SmVK, 0, p.whole[0], p.D, clear, mv, mk)
+             : GO((k_lin_tc_state<DK, DV, false, false>), SmKV, 0, p.whole[0], p.D, clear, mk, mv);
     if (e) return e;
     clear = false;
     if (back) {
       prof_mark(c.st, "lin_tc_state");
-      e = go(k_lin_tc_state<DK, DV, true, false>, StateSm<DK, DV>::BYTES, p.whole[1], p.E, false, mq, mo);
+      e = GO((k_lin_tc_state<DK, DV, true, false>), SmKV, 0, p.whole[1], p.E, false, mq, mo);
       if (e) return e;
     }
     e = lin_scan(p.m, s, p.whole[0], p.D, c.S_in, p.E, p.whole[1], c.dS_out, back, p.status, c.st);
     if (e) return e;
   }
+  using PassKV = PassSm<DK, DV>;
+  using PassVK = PassSm<DV, DK>;
+  using Back = BackSm<DK, DV>;
   prof_mark(c.st, back ? "lin_tc_dq" : "lin_tc_fwd");
   if (!back)
-    return go(k_lin_tc_pass<DK, DV, false>, PassSm<DK, DV>::BYTES, c.S_in, p.D, c.S_out, (bf*)c.o,
+    return GO((k_lin_tc_pass<DK, DV, false>), PassKV, REG_LAUNCH, c.S_in, p.D, c.S_out, (bf*)c.o,
               (const bf*)nullptr, 0ll, (float*)nullptr, clear, mq, mk, mv);
-  e = go(k_lin_tc_pass<DV, DK, true>, PassSm<DV, DK>::BYTES, c.S_in, p.D,
+  e = GO((k_lin_tc_pass<DV, DK, true>), PassVK, REG_LAUNCH, c.S_in, p.D,
          c.dS_out ? p.S_end : (float*)nullptr, (bf*)c.dq, (const bf*)c.q, s.ldq, p.far, clear, mo, mv, mk);
   if (e) return e;
   prof_mark(c.st, "lin_tc_back");
-  e = go(k_lin_tc_back<DK, DV>, BackSm<DK, DV>::BYTES, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
+  e = GO((k_lin_tc_back<DK, DV>), Back, REG_LAUNCH, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
          (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo);
+#undef GO
   if (e) return e;
   if (c.ddecay) e = col_sum(p.dgsum, p.m.cap, s.H, s.H, c.ddecay, nullptr, nullptr, c.st);
   return e;
