@@ -155,9 +155,10 @@ struct Vec {
   int mild, pad[3];
 };
 
-// The log-decays of a chunk, 4 tokens for each lane of a warp, loaded ahead of their use.
+// The log-decays of a chunk, 4 tokens for each lane of a warp: loaded a chunk ahead of their
+// use and not touched before it, so that nothing waits for them.
 struct Raw {
-  float x[4];
+  uint32_t x[4];
 };
 __device__ __forceinline__ Raw raw_decay(int row, int len, int h, const bf* g, long long ldg,
                                          const float* decay) {
@@ -166,9 +167,15 @@ __device__ __forceinline__ Raw raw_decay(int row, int len, int h, const bf* g, l
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = 4 * l + i;
-    r.x[i] = t < len ? lin_decay(decay ? decay[h] : ldf(g + (size_t)(row + t) * ldg + h)) : 0.f;
+    r.x[i] = 0;
+    if (t < len)
+      r.x[i] = decay ? __float_as_uint(decay[h])
+                     : *reinterpret_cast<const unsigned short*>(g + (size_t)(row + t) * ldg + h);
   }
   return r;
+}
+__device__ __forceinline__ float decay_value(uint32_t x, bool wide) {
+  return lin_decay(__uint_as_float(wide ? x : x << 16));
 }
 // gamma summed as pairs of floats (2^-47 of itself: differences of neighbours keep their
 // 24 bits however large it is; FP64 has 1/64 of the rate, and this warp is waited for).
@@ -183,12 +190,12 @@ __device__ __forceinline__ Two add_two(Two a, Two b) {
   r.lo = e - (r.hi - s);
   return r;
 }
-__device__ __forceinline__ void sum_decay(const Raw& r, float* hi, float* lo) {
+__device__ __forceinline__ void sum_decay(const Raw& r, bool wide, float* hi, float* lo) {
   const int l = threadIdx.x & 31;
   Two c[4];
-  c[0] = {r.x[0], 0.f};
+  c[0] = {decay_value(r.x[0], wide), 0.f};
 #pragma unroll
-  for (int i = 1; i < 4; ++i) c[i] = add_two(c[i - 1], {r.x[i], 0.f});
+  for (int i = 1; i < 4; ++i) c[i] = add_two(c[i - 1], {decay_value(r.x[i], wide), 0.f});
   Two all = c[3];
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -204,8 +211,10 @@ __device__ __forceinline__ void sum_decay(const Raw& r, float* hi, float* lo) {
     lo[i] = x.lo;
   }
 }
+// e^{a - b}. The hardware's exponential: off by 2^-21 and by 2^-24 of the exponent, far
+// below what bf16 products and 2^-16 of a weight keep of it.
 __device__ __forceinline__ float exp_diff(float h1, float l1, float h0, float l0) {
-  return expf((h1 - h0) + (l1 - l0));
+  return __expf((h1 - h0) + (l1 - l0));
 }
 // Weights of the state's update: to the chunk's end, or (BACK) scale times from its start.
 template <bool BACK>
@@ -221,10 +230,10 @@ __device__ __forceinline__ void fill_weights(const float* hi, const float* lo, f
   if (l == 0) w.whole = exp_diff(eh, el, 0.f, 0.f);
 }
 template <bool BACK>
-__device__ __forceinline__ void fill_vec(const Raw& r, float scale, Vec& v) {  // one warp
+__device__ __forceinline__ void fill_vec(const Raw& r, bool wide, float scale, Vec& v) {  // one warp
   const int l = threadIdx.x & 31, blk = l >> 3;  // this lane's block of 32 tokens
   float hi[4], lo[4], eh[4], el[4], o[4] = {};
-  sum_decay(r, hi, lo);
+  sum_decay(r, wide, hi, lo);
   fill_weights<BACK>(hi, lo, scale, v.w);
 #pragma unroll
   for (int b = 0; b < 4; ++b) {  // the ends of the blocks
@@ -407,22 +416,42 @@ __device__ __forceinline__ void add_state(uint32_t taddr, float by, float* s) {
     for (int j = 0; j < 32; ++j) s[i + j] = fmaf(by, s[i + j], d[j]);
   }
 }
-// An accumulator's N columns times `by` as bf16 to consecutive addresses (16-byte aligned).
+// An accumulator's N columns times `by` as packed bf16.
 template <int N>
-__device__ __forceinline__ void store_row(uint32_t taddr, bf* to, float by, bool on) {
+__device__ __forceinline__ void take_row(uint32_t taddr, float by, uint32_t* p) {
 #pragma unroll
   for (int i = 0; i < N; i += 32) {
     float v[32];
     tmem_ld32(taddr + i, v);
-    if (!on) continue;
 #pragma unroll
-    for (int k = 0; k < 32; k += 8) {
-      uint32_t u[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = pack2bf(by * v[k + 2 * j], by * v[k + 2 * j + 1]);
-      *reinterpret_cast<uint4*>(to + i + k) = make_uint4(u[0], u[1], u[2], u[3]);
-    }
+    for (int j = 0; j < 16; ++j) p[i / 2 + j] = pack2bf(by * v[2 * j], by * v[2 * j + 1]);
   }
+}
+// A result's row into a tile that the copy engine stores: a warp's own stores, whose lanes
+// hold different rows, would touch 32 lines each and take the load / store unit 2000 cycles a
+// chunk. Or into memory, where the tile's last rows are another sequence's.
+template <int N>
+__device__ __forceinline__ void put_row(const uint32_t* p, unsigned char* tile, int r, int c, bf* to,
+                                        bool direct, bool on) {
+#pragma unroll
+  for (int i = 0; i < N / 2; i += 4) {
+    const uint4 x = make_uint4(p[i], p[i + 1], p[i + 2], p[i + 3]);
+    if (!direct)
+      *reinterpret_cast<uint4*>(at8(tile, HALF_TILE, r, c + 2 * i)) = x;
+    else if (on)
+      *reinterpret_cast<uint4*>(to + 2 * i) = x;
+  }
+}
+template <int D>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, const unsigned char* tile, int h,
+                                           int tok, int seq) {
+#pragma unroll
+  for (int c = 0; c < D; c += 64)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(c), "r"(h), "r"(tok), "r"(seq), "r"(smem_u32(tile + (c >> 6) * HALF_TILE))
+        : "memory");
 }
 // After a wait that ran out: this CTA's copies still under way are waited for, with a
 // limit, before its shared memory is given up.
@@ -575,7 +604,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   } else if (t.w == DEC) {
     auto fill = [&](const Raw& r, int i) {
       float hi[4], lo[4];
-      sum_decay(r, hi, lo);
+      sum_decay(r, a.decay != nullptr, hi, lo);
       fill_weights<REV>(hi, lo, a.scale, vec[i & 3]);
     };
     fill(raw(0), 0);
@@ -611,7 +640,8 @@ template <int DY, int DZ, bool DQ>
 __global__ void __launch_bounds__(NTHR, 1)
     k_lin_tc_pass(Args a, const float* S_in, const float* S_unit, float* S_out, bf* out, const bf* q,
                   long long ldq, float* far, bool clear, const __grid_constant__ CUtensorMap mx,
-                  const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz) {
+                  const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz,
+                  const __grid_constant__ CUtensorMap mo) {
   using L = PassSm<DY, DZ>;
   constexpr int N = DZ / 2;
   constexpr uint32_t P0 = 0, O0 = 128, Y0 = 256, D0 = 384;
@@ -748,14 +778,17 @@ __global__ void __launch_bounds__(NTHR, 1)
       if (DQ && t.tid < len) far[(size_t)row * a.H + h] = part[t.tid] + part[TC + t.tid];
       mbar_wait(bar_o, c & 1, abort);
       tc_fence_after();
-      store_row<N>(tl + O0 + N * t.cg, out + ((size_t)row * a.H + h) * DZ + N * t.cg, a.scale, on);
+      uint32_t res[N / 2];
+      take_row<N>(tl + O0 + N * t.cg, a.scale, res);
       mbar_wait(bar_d, c & 1, abort);
       tc_fence_after();
       if (t.lane < DY) {
         add_state<N>(tl + D0 + N * t.cg, v.w.whole, s);
         put_split<N>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
-        fence_proxy_async_smem();
       }
+      put_row<N>(res, tile(n0 + 2), t.lane, N * t.cg,  // z is done with
+                 out + ((size_t)row * a.H + h) * DZ + N * t.cg, len < TC && a.m.cu, on);
+      fence_proxy_async_smem();
       tc_fence_before();
       off = meet(abort) || off;
     }
@@ -785,6 +818,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                     umma_idesc(128, 128, 0, 0), kk > 0);
         umma_commit(bar_p);
       };
+      int kept = -1;  // the chunk whose result was stored last
       if (t.l == 0) {
         for (int n = 0; n < 4; ++n) load(n);
         if (nch) products(0);
@@ -796,13 +830,18 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (t.l == 0) {
           tc_fence_after();
           const uint32_t x = smem_u32(tile(n0));
+          // the forward's result takes the first part alone, which is as good as its own bits
 #pragma unroll 1
-          for (int p = 0; p < 2; ++p)
+          for (int p = 0; p < (DQ ? 2 : 1); ++p)
 #pragma unroll
             for (int kk = 0; kk < DY / 16; ++kk)
               umma_bf16(tm + O0, kmaj(x, HALF_TILE, kk), mnmaj(smem_u32(p ? s_lo : s_hi), L::HALF_S, kk),
                         umma_idesc(128, DZ, 0, 1), p || kk);
           umma_commit(bar_s);
+          if (kept >= 0) {  // the result before has left z's tile: x of the next chunk takes it
+            bulk_wait_read();
+            load(3 * kept + 6);
+          }
         }
         __syncwarp();
         off = meet(abort);
@@ -827,24 +866,33 @@ __global__ void __launch_bounds__(NTHR, 1)
           umma_commit(bar_d);
           mbar_wait(bar_o, c & 1, abort);  // P has been read
           if (c + 1 < nch) products(c + 1);
-          mbar_wait(bar_d, c & 1, abort);
-          if (!*abort) load(n0 + 6);
         }
         __syncwarp();
         off = meet(abort) || off;
+        if (t.l == 0 && !off) {  // the result is in z's tile
+          if (!a.m.cu || u.len - c * TC >= TC) {
+            const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC;
+            store_tile<DZ>(&mo, tile(n0 + 2), h, tok, a.m.cu ? 0 : u.seq);
+            bulk_commit();
+          }
+          kept = c;
+        }
+        __syncwarp();
       }
+      if (t.l == 0) bulk_wait_all();
     } else if (t.w == DEC) {
       auto raw = [&](int c) {
         return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
       };
+      const bool wide = a.decay != nullptr;
       Raw ahead = {};
-      if (nch) fill_vec<false>(raw(0), 1.f, vec[0]);
+      if (nch) fill_vec<false>(raw(0), wide, 1.f, vec[0]);
       if (nch > 1) ahead = raw(1);
       bool off = meet(abort);
       for (int c = 0; c < nch && !off; ++c) {
-        off = meet(abort);
-        if (c + 1 < nch) fill_vec<false>(ahead, 1.f, vec[(c + 1) & 1]);
+        if (c + 1 < nch) fill_vec<false>(ahead, wide, 1.f, vec[(c + 1) & 1]);
         if (c + 2 < nch) ahead = raw(c + 2);
+        off = meet(abort);
         off = meet(abort) || off;
       }
     }
@@ -865,7 +913,6 @@ __global__ void __launch_bounds__(NTHR, 1)
 template <int DK, int DV>
 struct BackSm {
   static constexpr uint32_t SLOT = slot_bytes(DK, DV), STATE = DK * DV * 2, HALF_R = DK * 128;
-  static constexpr uint32_t V = 0, K = SLOT, Q = 2 * SLOT, DO = 3 * SLOT;
   static constexpr uint32_t R_HI = 4 * SLOT, R_LO = R_HI + STATE, VEC = R_LO + STATE;
   static constexpr uint32_t ROWS = VEC + 2 * sizeof(Vec), COLS = ROWS + 4 * TC * 4,
                             FAR = COLS + 2 * TC * 4, RED = FAR + 2 * TC * 4, BAR = RED + 64;
@@ -892,7 +939,8 @@ __global__ void __launch_bounds__(NTHR, 1)
                   const float* S_end, float* dS_in, const float* far, bf* dk, bf* dv, bf* dg,
                   float* dgsum, const __grid_constant__ CUtensorMap mq,
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                  const __grid_constant__ CUtensorMap mo) {
+                  const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mdk,
+                  const __grid_constant__ CUtensorMap mdv) {
   using L = BackSm<DK, DV>;
   constexpr int NK = DK / 2, NV = DV / 2;
   // A1: k q^T, then P1 and P2; A2: v dO^T; G1: the weighed q, then dk; G2: R's sum, then dv
@@ -915,6 +963,9 @@ __global__ void __launch_bounds__(NTHR, 1)
   float* farb = reinterpret_cast<float*>(sb + L::FAR);   // [column group][s]
   float* red = reinterpret_cast<float*>(sb + L::RED);
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [4] v, k, q, dO
+  // q and dO of a chunk take the slots of v and k of the one before, which are done with
+  // early; v and k those of q and dO, which first take the results on their way out
+  auto slot = [&](int kind, int i) { return sb + (kind ^ (i & 1 ? 2 : 0)) * L::SLOT; };
   // MMAs: R's sum, k q^T and v dO^T, products with R, results
   uint64_t *bar_e = full + 4, *bar_a = full + 5, *bar_f = full + 6, *bar_c = full + 7;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 8);
@@ -959,13 +1010,13 @@ __global__ void __launch_bounds__(NTHR, 1)
       mbar_wait(full + 2, ph, abort);
       if (len < TC && a.m.cu) {
         mbar_wait(full + 3, ph, abort);
-        zero_rows<DK>(sb + L::Q, len, t.tid);
-        zero_rows<DV>(sb + L::DO, len, t.tid);
+        zero_rows<DK>(slot(2, i), len, t.tid);
+        zero_rows<DV>(slot(3, i), len, t.tid);
         fence_proxy_async_smem();
         named_bar(6, NEPI);
       }
       if (t.lane < DK) {
-        weigh(sb + L::Q, t, v.w, len, tl + G1);
+        weigh(slot(2, i), t, v.w, len, tl + G1);
         tmem_st_wait();
       }
       tc_fence_before();
@@ -1042,7 +1093,7 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
           const uint4 k4 = *reinterpret_cast<const uint4*>(
-              at8(sb + L::K, HALF_TILE, t.lane, NK * t.cg + e + j));
+              at8(slot(1, i), HALF_TILE, t.lane, NK * t.cg + e + j));
           const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
@@ -1067,7 +1118,6 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc_fence_before();
       off = meet(abort) || off;
       if (t.lane < DK) put_split<NV>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
-      fence_proxy_async_smem();
       if (t.w == 0) {  // dg: 4 tokens for each lane
         float x[4], ab = 0.f, suf = 0.f;
 #pragma unroll
@@ -1103,8 +1153,17 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       mbar_wait(bar_c, ph, abort);
       tc_fence_after();
-      store_row<NK>(tl + G1 + NK * t.cg, dk + ((size_t)row * a.H + h) * DK + NK * t.cg, 1.f, on);
-      store_row<NV>(tl + G2 + NV * t.cg, dv + ((size_t)row * a.H + h) * DV + NV * t.cg, 1.f, on);
+      {
+        const bool direct = len < TC && a.m.cu;
+        uint32_t res[NK > NV ? NK / 2 : NV / 2];
+        take_row<NK>(tl + G1 + NK * t.cg, 1.f, res);
+        put_row<NK>(res, slot(2, i), t.lane, NK * t.cg, dk + ((size_t)row * a.H + h) * DK + NK * t.cg,
+                    direct, on);
+        take_row<NV>(tl + G2 + NV * t.cg, 1.f, res);
+        put_row<NV>(res, slot(3, i), t.lane, NV * t.cg, dv + ((size_t)row * a.H + h) * DV + NV * t.cg,
+                    direct, on);
+      }
+      fence_proxy_async_smem();
       tc_fence_before();
       off = meet(abort) || off;
     }
@@ -1120,7 +1179,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (i >= nch) return;
         const int c = nch - 1 - i;
         const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
-        unsigned char* to = sb + kind * L::SLOT;
+        unsigned char* to = slot(kind, i);
         if (kind == 0)
           load_tile<DV>(to, &mv, h, tok, seq, full);
         else if (kind == 1)
@@ -1133,11 +1192,17 @@ __global__ void __launch_bounds__(NTHR, 1)
       if (t.l == 0)
         for (int k = 3; k >= 0; --k) load(k, 0);
       __syncwarp();
-      const uint32_t sv = smem_u32(sb + L::V), sk = smem_u32(sb + L::K), sq = smem_u32(sb + L::Q),
-                     so = smem_u32(sb + L::DO);
       bool off = meet(abort);
       for (int i = 0; i < nch && !off; ++i) {
         const int ph = i & 1;
+        const uint32_t sv = smem_u32(slot(0, i)), sk = smem_u32(slot(1, i)),
+                       sq = smem_u32(slot(2, i)), so = smem_u32(slot(3, i));
+        if (t.l == 0 && i) {  // the results before have left: v and k
+          bulk_wait_read();
+          load(0, i);
+          load(1, i);
+        }
+        __syncwarp();
         off = meet(abort);  // the weighed q is there (and a tail's rows are zeros)
         if (t.l == 0) {
           tc_fence_after();
@@ -1184,8 +1249,8 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (t.l == 0) {
           tc_fence_after();
           if (!*abort) {
-            load(0, i + 1);
-            load(1, i + 1);
+            load(2, i + 1);
+            load(3, i + 1);
           }
 #pragma unroll
           for (int kk = 0; kk < TC / 16; ++kk)
@@ -1195,28 +1260,35 @@ __global__ void __launch_bounds__(NTHR, 1)
           for (int kk = 0; kk < TC / 16; ++kk)
             umma_ts(tm + G2, tm + A1 + 8 * kk, mnmaj(so, HALF_TILE, kk), umma_idesc(128, DV, 0, 1), true);
           umma_commit(bar_c);
-          mbar_wait(bar_c, ph, abort);
-          if (!*abort) {
-            load(2, i + 1);
-            load(3, i + 1);
-          }
         }
         __syncwarp();
         off = meet(abort) || off;
+        if (t.l == 0 && !off) {
+          const int c = nch - 1 - i;
+          if (!a.m.cu || u.len - c * TC >= TC) {
+            const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC;
+            store_tile<DK>(&mdk, slot(2, i), h, tok, a.m.cu ? 0 : u.seq);
+            store_tile<DV>(&mdv, slot(3, i), h, tok, a.m.cu ? 0 : u.seq);
+            bulk_commit();
+          }
+        }
+        __syncwarp();
       }
+      if (t.l == 0) bulk_wait_all();
     } else if (t.w == DEC) {
       auto raw = [&](int i) {
         const int c = nch - 1 - i;
         return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
       };
+      const bool wide = a.decay != nullptr;
       Raw ahead = {};
-      if (nch) fill_vec<true>(raw(0), a.scale, vec[0]);
+      if (nch) fill_vec<true>(raw(0), wide, a.scale, vec[0]);
       if (nch > 1) ahead = raw(1);
       bool off = meet(abort);
       for (int i = 0; i < nch && !off; ++i) {
-        off = meet(abort);
-        if (i + 1 < nch) fill_vec<true>(ahead, a.scale, vec[(i + 1) & 1]);
+        if (i + 1 < nch) fill_vec<true>(ahead, wide, a.scale, vec[(i + 1) & 1]);
         if (i + 2 < nch) ahead = raw(i + 2);
+        off = meet(abort);
         off = meet(abort) || off;
         off = meet(abort) || off;
         off = meet(abort) || off;
@@ -1317,12 +1389,19 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   const gdn_lin_shape& s = c.s;
   const TcPlan p = tc_plan(s, c.cu, c.cu != nullptr, back, c.ws);
   const Args a = {p.m, s.H, s.scale, (const bf*)c.g, c.decay, s.ldg, p.status};
-  CUtensorMap mq, mk, mv, mo;
+  CUtensorMap mq, mk, mv, mo, mdq, mdk, mdv;
   cudaError_t e;
   if ((e = tile_map(&mq, c.q, s, DK, s.ldq)) || (e = tile_map(&mk, c.k, s, DK, s.ldk)) ||
       (e = tile_map(&mv, c.v, s, DV, s.ldv)))
     return e;
-  if (back && (e = tile_map(&mo, c.dout, s, DV, (long long)s.H * DV))) return e;
+  const long long rk = (long long)s.H * DK, rv = (long long)s.H * DV;
+  if (back) {
+    if ((e = tile_map(&mo, c.dout, s, DV, rv)) || (e = tile_map(&mdq, c.dq, s, DK, rk)) ||
+        (e = tile_map(&mdk, c.dk, s, DK, rk)) || (e = tile_map(&mdv, c.dv, s, DV, rv)))
+      return e;
+  } else if ((e = tile_map(&mo, c.o, s, DV, rv))) {
+    return e;
+  }
   if (c.cu && (e = lin_plan(p.m, p.first, p.owner, p.status, c.st))) return e;
   bool clear = !c.cu;  // the first kernel of an unpacked call resets the status word
   const dim3 grid(p.m.cap * s.H), block(NTHR);
@@ -1353,13 +1432,15 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   prof_mark(c.st, back ? "lin_tc_dq" : "lin_tc_fwd");
   if (!back)
     return GO((k_lin_tc_pass<DK, DV, false>), PassKV, REG_LAUNCH, c.S_in, p.D, c.S_out, (bf*)c.o,
-              (const bf*)nullptr, 0ll, (float*)nullptr, clear, mq, mk, mv);
+              (const bf*)nullptr, 0ll, (float*)nullptr, clear, mq, mk, mv, mo);
   e = GO((k_lin_tc_pass<DV, DK, true>), PassVK, REG_LAUNCH, c.S_in, p.D,
-         c.dS_out ? p.S_end : (float*)nullptr, (bf*)c.dq, (const bf*)c.q, s.ldq, p.far, clear, mo, mv, mk);
+         c.dS_out ? p.S_end : (float*)nullptr, (bf*)c.dq, (const bf*)c.q, s.ldq, p.far, clear, mo, mv, mk,
+         mdq);
   if (e) return e;
   prof_mark(c.st, "lin_tc_back");
   e = GO((k_lin_tc_back<DK, DV>), Back, REG_LAUNCH, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
-         (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo);
+         (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo, mdk,
+         mdv);
 #undef GO
   if (e) return e;
   if (c.ddecay) e = col_sum(p.dgsum, p.m.cap, s.H, s.H, c.ddecay, nullptr, nullptr, c.st);
