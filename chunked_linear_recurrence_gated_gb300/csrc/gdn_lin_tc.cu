@@ -122,8 +122,8 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   hi = pack2bf(a, b);
   lo = pack2bf(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
 }
-// N values of row r from column c into the tiles of the first parts and of the rests.
-template <int N>
+// N values of row r from column c into the tiles of the first parts and (REST) of the rests.
+template <int N, bool REST>
 __device__ __forceinline__ void put_split(unsigned char* hi, unsigned char* lo, uint32_t half, int r,
                                           int c, const float* v) {
 #pragma unroll
@@ -132,7 +132,7 @@ __device__ __forceinline__ void put_split(unsigned char* hi, unsigned char* lo, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) split2(v[i + 2 * j], v[i + 2 * j + 1], h[j], l[j]);
     *reinterpret_cast<uint4*>(at8(hi, half, r, c + i)) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(at8(lo, half, r, c + i)) = make_uint4(l[0], l[1], l[2], l[3]);
+    if (REST) *reinterpret_cast<uint4*>(at8(lo, half, r, c + i)) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -294,14 +294,16 @@ __device__ __forceinline__ void more_registers() {
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REG_CTL));
 }
-// All working warps meet; true if any has seen a wait run out.
+// The working warps meet, with the one for decay factors (ALL) or without it; true if any
+// has seen a wait run out.
+template <bool ALL>
 __device__ __forceinline__ bool meet(volatile int* abort) {
   uint32_t any;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n"
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n"
       " selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(any)
-      : "r"(*abort), "n"(NWORK)
+      : "r"(*abort), "n"(ALL ? 1 : 7), "n"(ALL ? NWORK : NWORK - 32)
       : "memory");
   return any != 0;
 }
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       all *= wh;
       tc_fence_before();
     };
-    meet(abort);
+    meet<true>(abort);
     for (int i = 0; i < nch; ++i) {
       const int len = min(TC, u.len - chunk(i) * TC);
       mbar_wait(full + i % ST, (i / ST) & 1, abort);
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         fence_proxy_async_smem();
       }
       tc_fence_before();
-      if (meet(abort)) break;
+      if (meet<true>(abort)) break;
       if (i) update(i - 1);
     }
     if (nch) update(nch - 1);
@@ -580,9 +582,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (t.l == 0)
       for (int i = 0; i < min(nch, ST); ++i) load(i);
     __syncwarp();
-    meet(abort);
+    meet<true>(abort);
     for (int i = 0; i < nch; ++i) {
-      if (meet(abort)) break;
+      if (meet<true>(abort)) break;
       if (t.l == 0) {
         tc_fence_after();
         mbar_wait(full + i % ST, (i / ST) & 1, abort);
@@ -611,9 +613,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (nch > 1) fill(raw(1), 1);
     Raw ahead = {};
     if (nch > 2) ahead = raw(2);
-    meet(abort);
+    meet<true>(abort);
     for (int i = 0; i < nch; ++i) {
-      if (meet(abort)) break;
+      if (meet<true>(abort)) break;
       // two ahead: visible behind the next chunk's meeting; four kept, for the chunk before
       // this one is still to be added
       if (i + 2 < nch) fill(ahead, i + 2);
@@ -671,65 +673,67 @@ __global__ void __launch_bounds__(NTHR, 1)
     const size_t sh = ((size_t)u.seq * a.H + h) * DY * DZ, uh = ((size_t)unit * a.H + h) * DY * DZ;
     float s[N];
     load_state<DY, DZ, DQ, N>(u.at ? S_unit + uh : S_in ? S_in + sh : nullptr, t.lane, N * t.cg, s);
-    if (t.lane < DY) put_split<N>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
+    if (t.lane < DY) put_split<N, DQ>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
     fence_proxy_async_smem();
-    bool off = meet(abort);
+    bool off = meet<true>(abort);
     for (int c = 0; c < nch && !off; ++c) {
       const int len = min(TC, u.len - c * TC), n0 = 3 * c;
       const Vec& v = vec[c & 1];
       const int row = u.row + c * TC + t.lane;  // of this thread's result
       const bool on = t.lane < len;
-      // P: this thread's row t, columns [64 cg, 64 cg + 64)
-      mbar_wait(bar_p, c & 1, abort);
-      tc_fence_after();
-      {
-        float x[64];
+      // P: this thread's row t, columns [64 cg, 64 cg + 64) of x y^T, 32 at a time; as bf16 pairs
+      // into the first half of the same columns. So the second group, whose pairs go where the
+      // first one's products are, waits until those have been read. The factors are loaded
+      // together: under the MMAs a load of shared memory takes hundreds of cycles.
+      const float r = v.row[t.lane];
+      const bool mild = v.mild;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (2 * t.cg + j <= t.q4) tmem_ld32(tl + P0 + 64 * t.cg + 32 * j, x + 32 * j);
-        tc_fence_before();
-        named_bar(2 + t.q4, 64);  // the lane quarter's columns of x y^T have been read
-        tc_fence_after();
+      for (int j = 0; j < 2; ++j) {
+        const int blk = 2 * t.cg + j;
+        float f[32], x[32];
+        if (blk <= t.q4) {
+          const float* tb = (blk == t.q4 ? v.own : v.tab[t.q4 - 1]) + 32 * blk;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int blk = 2 * t.cg + j;
-          uint32_t p[16];
-          if (blk > t.q4) {
+          for (int i = 0; i < 32; i += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(tb + i);
+            f[i] = y.x, f[i + 1] = y.y, f[i + 2] = y.z, f[i + 3] = y.w;
+          }
+        }
+        if (j == 0) {
+          mbar_wait(bar_p, c & 1, abort);
+          tc_fence_after();
+        }
+        uint32_t p[16];
+        if (blk > t.q4) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] = 0;
-          } else if (blk < t.q4 || v.mild) {
-            const bool diag = blk == t.q4;
-            const float r = v.row[t.lane];
-            const float* tb = (diag ? v.own : v.tab[t.q4 - 1]) + 32 * blk;
+          for (int i = 0; i < 16; ++i) p[i] = 0;
+        } else {
+          tmem_ld32(tl + P0 + 32 * blk, x);
+          if (blk < t.q4) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(tb + i);
-              float* y = x + 32 * j + i;
-              y[0] *= r * f.x;
-              y[1] *= r * f.y;
-              y[2] *= r * f.z;
-              y[3] *= r * f.w;
-              if (diag) {
+            for (int i = 0; i < 32; i += 2) p[i / 2] = pack2bf(x[i] * (r * f[i]), x[i + 1] * (r * f[i + 1]));
+          } else if (mild) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = i + e <= t.l ? y[e] : 0.f;
-              }
-              p[i / 2] = pack2bf(y[0], y[1]);
-              p[i / 2 + 1] = pack2bf(y[2], y[3]);
-            }
+            for (int i = 0; i < 32; i += 2)
+              p[i / 2] = pack2bf(i <= t.l ? x[i] * (r * f[i]) : 0.f,
+                                 i < t.l ? x[i + 1] * (r * f[i + 1]) : 0.f);
           } else {
             const float gh = v.hi[t.lane], gl = v.lo[t.lane];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 h2 = *reinterpret_cast<const float2*>(v.hi + 32 * blk + i);
               const float2 l2 = *reinterpret_cast<const float2*>(v.lo + 32 * blk + i);
-              float* y = x + 32 * j + i;
-              y[0] = i <= t.l ? y[0] * __expf((gh - h2.x) + (gl - l2.x)) : 0.f;
-              y[1] = i + 1 <= t.l ? y[1] * __expf((gh - h2.y) + (gl - l2.y)) : 0.f;
-              p[i / 2] = pack2bf(y[0], y[1]);
+              p[i / 2] = pack2bf(i <= t.l ? x[i] * __expf((gh - h2.x) + (gl - l2.x)) : 0.f,
+                                 i < t.l ? x[i + 1] * __expf((gh - h2.y) + (gl - l2.y)) : 0.f);
             }
           }
-          tmem_st16(tl + P0 + 32 * t.cg + 16 * j, p);
         }
+        if (j != t.cg) {  // the first group behind its second read, the second before it writes
+          tc_fence_before();
+          named_bar(2 + t.q4, 64);
+          tc_fence_after();
+        }
+        tmem_st16(tl + P0 + 32 * t.cg + 16 * j, p);
       }
       wait_tile(n0 + 1);
       if (t.lane < DY) weigh(tile(n0 + 1), t, v.w, len, tl + Y0);
@@ -774,7 +778,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         fence_proxy_async_smem();
       }
       tc_fence_before();
-      off = meet(abort);
+      off = meet<false>(abort);
       if (DQ && t.tid < len) far[(size_t)row * a.H + h] = part[t.tid] + part[TC + t.tid];
       mbar_wait(bar_o, c & 1, abort);
       tc_fence_after();
@@ -784,13 +788,13 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc_fence_after();
       if (t.lane < DY) {
         add_state<N>(tl + D0 + N * t.cg, v.w.whole, s);
-        put_split<N>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
+        put_split<N, DQ>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
       }
       put_row<N>(res, tile(n0 + 2), t.lane, N * t.cg,  // z is done with
                  out + ((size_t)row * a.H + h) * DZ + N * t.cg, len < TC && a.m.cu, on);
       fence_proxy_async_smem();
       tc_fence_before();
-      off = meet(abort) || off;
+      off = meet<true>(abort) || off;
     }
     if (u.at == u.n - 1 && S_out) store_state<DY, DZ, DQ, N>(S_out + sh, t.lane, N * t.cg, s);
   } else {
@@ -824,7 +828,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (nch) products(0);
       }
       __syncwarp();
-      bool off = meet(abort);
+      bool off = meet<true>(abort);
       for (int c = 0; c < nch && !off; ++c) {
         const int n0 = 3 * c;
         if (t.l == 0) {
@@ -844,13 +848,9 @@ __global__ void __launch_bounds__(NTHR, 1)
           }
         }
         __syncwarp();
-        off = meet(abort);
+        off = meet<false>(abort);
         if (t.l == 0) {
           tc_fence_after();
-          if (!*abort) {
-            load(n0 + 4);
-            load(n0 + 5);
-          }
           wait_tile(n0 + 2);
           const uint32_t z = smem_u32(tile(n0 + 2));
           constexpr uint32_t id = umma_idesc(128, DZ, 0, 1);
@@ -864,11 +864,15 @@ __global__ void __launch_bounds__(NTHR, 1)
             for (int kk = 0; kk < TC / 16; ++kk)
               umma_ts(tm + D0, tm + Y0 + 64 * p + 8 * kk, mnmaj(z, HALF_TILE, kk), id, p || kk);
           umma_commit(bar_d);
+          if (!*abort) {  // x and y are done with
+            load(n0 + 4);
+            load(n0 + 5);
+          }
           mbar_wait(bar_o, c & 1, abort);  // P has been read
           if (c + 1 < nch) products(c + 1);
         }
         __syncwarp();
-        off = meet(abort) || off;
+        off = meet<true>(abort) || off;
         if (t.l == 0 && !off) {  // the result is in z's tile
           if (!a.m.cu || u.len - c * TC >= TC) {
             const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC;
@@ -888,12 +892,11 @@ __global__ void __launch_bounds__(NTHR, 1)
       Raw ahead = {};
       if (nch) fill_vec<false>(raw(0), wide, 1.f, vec[0]);
       if (nch > 1) ahead = raw(1);
-      bool off = meet(abort);
+      bool off = meet<true>(abort);
       for (int c = 0; c < nch && !off; ++c) {
         if (c + 1 < nch) fill_vec<false>(ahead, wide, 1.f, vec[(c + 1) & 1]);
         if (c + 2 < nch) ahead = raw(c + 2);
-        off = meet(abort);
-        off = meet(abort) || off;
+        off = meet<true>(abort);
       }
     }
   }
@@ -943,7 +946,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                   const __grid_constant__ CUtensorMap mdv) {
   using L = BackSm<DK, DV>;
   constexpr int NK = DK / 2, NV = DV / 2;
-  // A1: k q^T, then P1 and P2; A2: v dO^T; G1: the weighed q, then dk; G2: R's sum, then dv
+  // A1: k q^T, then P1; A2: v dO^T, then P2; G1: the weighed q, then dk; G2: R's sum, then dv
   constexpr uint32_t A1 = 0, A2 = 128, G1 = 256, G2 = 384;
   chain();
   const int unit = blockIdx.x / a.H, h = blockIdx.x - unit * a.H;
@@ -980,7 +983,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     float r[NV];
     const float* from = last ? (dS_out ? dS_out + sh : nullptr) : R_unit + uh * DK * DV;
     load_state<DK, DV, false, NV>(from, t.lane, NV * t.cg, r);
-    if (t.lane < DK) put_split<NV>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
+    if (t.lane < DK) put_split<NV, true>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
     fence_proxy_async_smem();
     {
       const float* S = !from ? nullptr : last ? S_end + sh : S_unit + (uh + a.H) * DK * DV;
@@ -998,15 +1001,22 @@ __global__ void __launch_bounds__(NTHR, 1)
       x = lane_sum<32>(x);
       if (t.l == 0) red[t.w] = x;
     }
-    bool off = meet(abort);
-    float X = 0.f, sum = 0.f;  // of warp 0
-    if (t.w == 0)
+    bool off = meet<true>(abort);
+    float X = 0.f, sum = 0.f;  // of the warp that forms dg: the one with the fewest pairs
+    const bool forms = t.w == 3;
+    if (forms)
       for (int i = 0; i < NEPI / 32; ++i) X += red[i];
     for (int i = 0; i < nch && !off; ++i) {
       const int c = nch - 1 - i, len = min(TC, u.len - c * TC), ph = i & 1;
       const Vec& v = vec[ph];
       const int row0 = u.row + c * TC, row = row0 + t.lane;
       const bool on = t.lane < len;
+      float fa[4] = {};  // a of the tokens 4 l ..
+      if (forms) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * t.l + j < len) fa[j] = far[(size_t)(row0 + 4 * t.l + j) * a.H + h];
+      }
       mbar_wait(full + 2, ph, abort);
       if (len < TC && a.m.cu) {
         mbar_wait(full + 3, ph, abort);
@@ -1020,22 +1030,16 @@ __global__ void __launch_bounds__(NTHR, 1)
         tmem_st_wait();
       }
       tc_fence_before();
-      off = meet(abort);
+      off = meet<false>(abort);
       mbar_wait(bar_e, ph, abort);
       tc_fence_after();
       if (t.lane < DK) add_state<NV>(tl + G2 + NV * t.cg, v.w.whole, r);
       tc_fence_before();
-      off = meet(abort) || off;  // G1 and G2 are free: the products with R follow
+      off = meet<false>(abort) || off;  // G1 and G2 are free: the products with R follow
       mbar_wait(bar_a, ph, abort);
       tc_fence_after();
-      {  // this thread's row s, columns t in [64 cg, 64 cg + 64)
-        float x[64], cs = 0.f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (2 * t.cg + j >= t.q4) tmem_ld32(tl + A1 + 64 * t.cg + 32 * j, x + 32 * j);
-        tc_fence_before();
-        named_bar(2 + t.q4, 64);  // the lane quarter's k q^T has been read
-        tc_fence_after();
+      {  // this thread's row s, columns t in [64 cg, 64 cg + 64); P1 and P2 in place as above
+        float cs = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int blk = 2 * t.cg + j;
@@ -1045,13 +1049,13 @@ __global__ void __launch_bounds__(NTHR, 1)
             for (int e = 0; e < 16; ++e) p1[e] = p2[e] = 0;
             rows[t.q4 * TC + 32 * blk + t.l] = 0.f;
           } else {
-            float y[32];
+            float x[32], y[32];
+            tmem_ld32(tl + A1 + 32 * blk, x);
             tmem_ld32(tl + A2 + 32 * blk, y);
             const bool diag = blk == t.q4;
             const float gh = v.hi[t.lane], gl = v.lo[t.lane];
             const float tb = a.scale * (diag ? v.own[t.lane] : v.tab[blk - 1][t.lane]);
             const bool direct = diag && !v.mild;
-            float* xx = x + 32 * j;
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 f2 = *reinterpret_cast<const float2*>(v.row + 32 * blk + e);
@@ -1066,19 +1070,24 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
               for (int z = 0; z < 2; ++z) {
                 const bool in = !diag || e + z >= t.l;
-                px[z] = in ? xx[e + z] * f[z] : 0.f;
+                px[z] = in ? x[e + z] * f[z] : 0.f;
                 py[z] = in ? y[e + z] * f[z] : 0.f;
-                const float pair = !diag || e + z > t.l ? xx[e + z] * py[z] : 0.f;
-                xx[e + z] = pair;
+                const float pair = !diag || e + z > t.l ? x[e + z] * py[z] : 0.f;
+                x[e + z] = pair;
                 cs += pair;
               }
               p1[e / 2] = pack2bf(px[0], px[1]);
               p2[e / 2] = pack2bf(py[0], py[1]);
             }
-            rows[t.q4 * TC + 32 * blk + t.l] = lane_columns(xx);
+            rows[t.q4 * TC + 32 * blk + t.l] = lane_columns(x);
+          }
+          if (j != t.cg) {
+            tc_fence_before();
+            named_bar(2 + t.q4, 64);
+            tc_fence_after();
           }
           tmem_st16(tl + A1 + 32 * t.cg + 16 * j, p1);
-          tmem_st16(tl + A1 + 64 + 32 * t.cg + 16 * j, p2);
+          tmem_st16(tl + A2 + 32 * t.cg + 16 * j, p2);
         }
         cols[t.cg * TC + t.lane] = cs;
       }
@@ -1116,16 +1125,16 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-      off = meet(abort) || off;
-      if (t.lane < DK) put_split<NV>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
-      if (t.w == 0) {  // dg: 4 tokens for each lane
+      off = meet<false>(abort) || off;
+      if (t.lane < DK) put_split<NV, true>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
+      if (forms) {  // dg: 4 tokens for each lane
         float x[4], ab = 0.f, suf = 0.f;
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
           const int e = 4 * t.l + j;
           float rw = 0.f, cl = 0.f, bb = 0.f, f = 0.f;
           if (e < len) {
-            f = far[(size_t)(row0 + e) * a.H + h];
+            f = fa[j];
             rw = (rows[e] + rows[TC + e]) + (rows[2 * TC + e] + rows[3 * TC + e]);
             cl = cols[e] + cols[TC + e];
             bb = farb[e] + farb[TC + e];
@@ -1159,16 +1168,18 @@ __global__ void __launch_bounds__(NTHR, 1)
         take_row<NK>(tl + G1 + NK * t.cg, 1.f, res);
         put_row<NK>(res, slot(2, i), t.lane, NK * t.cg, dk + ((size_t)row * a.H + h) * DK + NK * t.cg,
                     direct, on);
+        fence_proxy_async_smem();
+        off = meet<false>(abort) || off;  // dk is in q's slot
         take_row<NV>(tl + G2 + NV * t.cg, 1.f, res);
         put_row<NV>(res, slot(3, i), t.lane, NV * t.cg, dv + ((size_t)row * a.H + h) * DV + NV * t.cg,
                     direct, on);
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      off = meet(abort) || off;
+      off = meet<true>(abort) || off;
     }
     if (u.at == 0 && dS_in) store_state<DK, DV, false, NV>(dS_in + sh, t.lane, NV * t.cg, r);
-    if (t.w == 0 && dgsum) {
+    if (forms && dgsum) {
       sum = lane_sum<32>(sum);
       if (t.l == 0) dgsum[uh] = sum;
     }
@@ -1192,18 +1203,17 @@ __global__ void __launch_bounds__(NTHR, 1)
       if (t.l == 0)
         for (int k = 3; k >= 0; --k) load(k, 0);
       __syncwarp();
-      bool off = meet(abort);
+      bool off = meet<true>(abort);
       for (int i = 0; i < nch && !off; ++i) {
         const int ph = i & 1;
         const uint32_t sv = smem_u32(slot(0, i)), sk = smem_u32(slot(1, i)),
                        sq = smem_u32(slot(2, i)), so = smem_u32(slot(3, i));
-        if (t.l == 0 && i) {  // the results before have left: v and k
+        if (t.l == 0 && i) {  // dv of the chunk before has left: k
           bulk_wait_read();
-          load(0, i);
           load(1, i);
         }
         __syncwarp();
-        off = meet(abort);  // the weighed q is there (and a tail's rows are zeros)
+        off = meet<false>(abort);  // the weighed q is there (and a tail's rows are zeros)
         if (t.l == 0) {
           tc_fence_after();
           mbar_wait(full + 3, ph, abort);
@@ -1228,7 +1238,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           umma_commit(bar_a);
         }
         __syncwarp();
-        off = meet(abort) || off;
+        off = meet<false>(abort) || off;
         if (t.l == 0) {
           tc_fence_after();
 #pragma unroll 1
@@ -1245,7 +1255,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           umma_commit(bar_f);
         }
         __syncwarp();
-        off = meet(abort) || off;
+        off = meet<false>(abort) || off;
         if (t.l == 0) {
           tc_fence_after();
           if (!*abort) {
@@ -1254,7 +1264,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           }
 #pragma unroll
           for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + G1, tm + A1 + 64 + 8 * kk, mnmaj(sq, HALF_TILE, kk),
+            umma_ts(tm + G1, tm + A2 + 8 * kk, mnmaj(sq, HALF_TILE, kk),
                     umma_idesc(128, DK, 0, 1), true);
 #pragma unroll
           for (int kk = 0; kk < TC / 16; ++kk)
@@ -1262,12 +1272,21 @@ __global__ void __launch_bounds__(NTHR, 1)
           umma_commit(bar_c);
         }
         __syncwarp();
-        off = meet(abort) || off;
+        off = meet<false>(abort) || off;
+        const int c = nch - 1 - i, tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC;
+        const bool whole = !a.m.cu || u.len - c * TC >= TC;
         if (t.l == 0 && !off) {
-          const int c = nch - 1 - i;
-          if (!a.m.cu || u.len - c * TC >= TC) {
-            const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC;
+          if (whole) {
             store_tile<DK>(&mdk, slot(2, i), h, tok, a.m.cu ? 0 : u.seq);
+            bulk_commit();
+            bulk_wait_read();
+          }
+          load(0, i + 1);
+        }
+        __syncwarp();
+        off = meet<true>(abort) || off;
+        if (t.l == 0 && !off) {
+          if (whole) {
             store_tile<DV>(&mdv, slot(3, i), h, tok, a.m.cu ? 0 : u.seq);
             bulk_commit();
           }
@@ -1284,14 +1303,11 @@ __global__ void __launch_bounds__(NTHR, 1)
       Raw ahead = {};
       if (nch) fill_vec<true>(raw(0), wide, a.scale, vec[0]);
       if (nch > 1) ahead = raw(1);
-      bool off = meet(abort);
+      bool off = meet<true>(abort);
       for (int i = 0; i < nch && !off; ++i) {
         if (i + 1 < nch) fill_vec<true>(ahead, wide, a.scale, vec[(i + 1) & 1]);
         if (i + 2 < nch) ahead = raw(i + 2);
-        off = meet(abort);
-        off = meet(abort) || off;
-        off = meet(abort) || off;
-        off = meet(abort) || off;
+        off = meet<true>(abort);
       }
     }
   }

@@ -76,13 +76,22 @@ def lin_step(q, k, v, g, S, slot_in=None, slot_out=None, cu=None, commit=None, s
     return o, out
 
 
-def _turn(x, inv_freq, pos, style, back=False):
-    """The first 2 len(inv_freq) values of x [B, T, H, d] turned by pos * inv_freq."""
+def _turn(x, inv_freq, pos, style, back=False, magnitude=False):
+    """The first 2 len(inv_freq) values of x [B, T, H, d] turned by pos * inv_freq, or the
+    sum of the two terms' magnitudes that each turned value is made of."""
     n = 0 if inv_freq is None else len(inv_freq)
     if n == 0:
-        return x
+        return np.abs(x) if magnitude else x
     ang = pos.astype(np.float64)[..., None] * inv_freq
     c, s = np.cos(ang)[:, :, None], np.sin(ang)[:, :, None] * (-1.0 if back else 1.0)
+    if magnitude:
+        a, b = (slice(0, n), slice(n, 2 * n)) if style == "half" else (slice(0, 2 * n, 2),
+                                                                      slice(1, 2 * n, 2))
+        y = np.abs(x)
+        u, v = y[..., a].copy(), y[..., b].copy()
+        y[..., a] = u * np.abs(c) + v * np.abs(s)
+        y[..., b] = v * np.abs(c) + u * np.abs(s)
+        return y
     y = x.copy()
     a, b = (slice(0, n), slice(n, 2 * n)) if style == "half" else (slice(0, 2 * n, 2),
                                                                   slice(1, 2 * n, 2))
@@ -110,10 +119,12 @@ def qk_norm_bwd(q, k, wq, wk, inv_freq, dqn, dkn, pos=None, H=None, style="half"
     dx, dw, mag = [], [], []
     for x, w, by, d in ((q, wq, q_scale, dqn), (k, wk, 1.0, dkn)):
         B, T, h, D = x.shape
-        d = by * _turn(d.reshape(B, T, h, d.shape[2] // h, D).sum(3), inv_freq, pos, style, back=True)
+        d = d.reshape(B, T, h, d.shape[2] // h, D).sum(3)
+        big = abs(by) * _turn(d, inv_freq, pos, style, back=True, magnitude=True)
+        d = by * _turn(d, inv_freq, pos, style, back=True)
         r = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
         e = d if w is None else d * w
         dx.append(r * (e - x * r * (e * x * r).mean(-1, keepdims=True)))
         dw.append(None if w is None else (d * x * r).sum((0, 1, 2)))
-        mag.append(None if w is None else np.abs(d * x * r).sum((0, 1, 2)))
+        mag.append(None if w is None else (big * np.abs(x) * r).sum((0, 1, 2)))
     return (*dx, *dw), tuple(mag)

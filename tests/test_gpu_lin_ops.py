@@ -396,7 +396,8 @@ def qk_inputs(B, T, Hq, Hk, d, rot, dtype, weights, seed, far=0, H=0):
     w = [1.0 + r(d, by=0.2) if weights else None for _ in range(2)]
     f = (10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64, device="cuda") / rot)
          if rot else None)
-    pos = (far + torch.randint(-50, 50, (B, T), device="cuda")).to(torch.int32)
+    pos = far + torch.from_numpy(np.random.default_rng(seed).integers(-50, 50, (B, T)))
+    pos = pos.to(torch.int32).cuda()
     d2 = [r(B, T, H or h, d, dtype=dtype) for h in (Hq, Hk)]
     return q, k, w, f, pos, d2
 
