@@ -348,7 +348,7 @@ __device__ __forceinline__ void weigh(const unsigned char* tile, const Who& t, c
   const int piece = (t.q4 & 1) * 4 + (t.l >> 3), r7 = t.l & 7;
   const uint32_t at = base + (64 * t.cg + r7) * 128 + ((piece ^ r7) << 4);
   const int p0 = 32 * t.cg + (t.l & 3);
-#pragma unroll
+#pragma unroll 1
   for (int g = 0; g < 2; ++g) {  // 32 tokens
     uint32_t hi[2][8], lo[2][8];
 #pragma unroll
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       // together: under the MMAs a load of shared memory takes hundreds of cycles.
       const float r = v.row[t.lane];
       const bool mild = v.mild;
-#pragma unroll
+#pragma unroll 1
       for (int j = 0; j < 2; ++j) {
         const int blk = 2 * t.cg + j;
         float f[32], x[32];
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc_fence_after();
       const float up = v.far[t.lane];
       float f = 0.f;  // q_t . (far part of dq_t)
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < N; i += 32) {
         uint4 qr[DQ ? 4 : 1];
         if (DQ) {
@@ -1040,7 +1040,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc_fence_after();
       {  // this thread's row s, columns t in [64 cg, 64 cg + 64); P1 and P2 in place as above
         float cs = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < 2; ++j) {
           const int blk = 2 * t.cg + j;
           uint32_t p1[16], p2[16];
@@ -1095,7 +1095,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc_fence_after();
       const float down = v.far[t.lane];
       float b = 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int e = 0; e < NK; e += 32) {
         float x[32];
         tmem_ld32(tl + G1 + NK * t.cg + e, x);
@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         tmem_st32(tl + G1 + NK * t.cg + e, x);
       }
       farb[t.cg * TC + t.lane] = b;
-#pragma unroll
+#pragma unroll 1
       for (int e = 0; e < NV; e += 32) {
         float x[32];
         tmem_ld32(tl + G2 + NV * t.cg + e, x);
@@ -1164,15 +1164,22 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc_fence_after();
       {
         const bool direct = len < TC && a.m.cu;
-        uint32_t res[NK > NV ? NK / 2 : NV / 2];
-        take_row<NK>(tl + G1 + NK * t.cg, 1.f, res);
-        put_row<NK>(res, slot(2, i), t.lane, NK * t.cg, dk + ((size_t)row * a.H + h) * DK + NK * t.cg,
-                    direct, on);
+#pragma unroll 1
+        for (int e = 0; e < NK; e += 32) {
+          uint32_t res[16];
+          take_row<32>(tl + G1 + NK * t.cg + e, 1.f, res);
+          put_row<32>(res, slot(2, i), t.lane, NK * t.cg + e,
+                      dk + ((size_t)row * a.H + h) * DK + NK * t.cg + e, direct, on);
+        }
         fence_proxy_async_smem();
         off = meet<false>(abort) || off;  // dk is in q's slot
-        take_row<NV>(tl + G2 + NV * t.cg, 1.f, res);
-        put_row<NV>(res, slot(3, i), t.lane, NV * t.cg, dv + ((size_t)row * a.H + h) * DV + NV * t.cg,
-                    direct, on);
+#pragma unroll 1
+        for (int e = 0; e < NV; e += 32) {
+          uint32_t res[16];
+          take_row<32>(tl + G2 + NV * t.cg + e, 1.f, res);
+          put_row<32>(res, slot(3, i), t.lane, NV * t.cg + e,
+                      dv + ((size_t)row * a.H + h) * DV + NV * t.cg + e, direct, on);
+        }
       }
       fence_proxy_async_smem();
       tc_fence_before();
