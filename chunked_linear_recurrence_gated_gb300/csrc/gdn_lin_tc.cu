@@ -35,8 +35,8 @@ typedef __nv_bfloat16 bf;
 
 constexpr int TC = 128;          // tokens of a chunk
 constexpr int NEPI = 256;        // 8 warps on the accumulators: 4 lane quarters x 2 column groups
-constexpr int CTL = 8, DEC = 9;  // a warp that copies and issues the MMAs, one for decay factors
-constexpr int NWORK = 320;       // threads of these
+constexpr int CTL = 8, DEC = 9;  // a warp that copies and issues the MMAs, three for decay factors
+constexpr int NWORK = 384;       // threads of these
 constexpr int NTHR = 384;        // launched: whole warpgroups, for the registers' redistribution
 constexpr uint32_t HALF_TILE = TC * 128;  // 64 columns of a chunk's rows
 
@@ -229,45 +229,51 @@ __device__ __forceinline__ void fill_weights(const float* hi, const float* lo, f
   for (int i = 0; i < 2; ++i) split2(o[2 * i], o[2 * i + 1], w.hi[2 * l + i], w.lo[2 * l + i]);
   if (l == 0) w.whole = exp_diff(eh, el, 0.f, 0.f);
 }
+// One of three warps' part of a chunk's factors (each sums gamma for itself: one warp took
+// 9 thousand cycles for all of them, twice what the rest of a chunk needs).
+constexpr int DEC_WARPS = 3;
 template <bool BACK>
-__device__ __forceinline__ void fill_vec(const Raw& r, bool wide, float scale, Vec& v) {  // one warp
+__device__ __forceinline__ void fill_vec(int part, const Raw& r, bool wide, float scale, Vec& v) {
   const int l = threadIdx.x & 31, blk = l >> 3;  // this lane's block of 32 tokens
-  float hi[4], lo[4], eh[4], el[4], o[4] = {};
+  float hi[4], lo[4], o[4] = {};
   sum_decay(r, wide, hi, lo);
-  fill_weights<BACK>(hi, lo, scale, v.w);
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {  // the ends of the blocks
-    eh[b] = __shfl_sync(0xffffffffu, hi[3], 8 * b + 7);
-    el[b] = __shfl_sync(0xffffffffu, lo[3], 8 * b + 7);
-  }
-  const float ah = blk == 0 ? 0.f : blk == 1 ? eh[0] : blk == 2 ? eh[1] : eh[2];
-  const float al = blk == 0 ? 0.f : blk == 1 ? el[0] : blk == 2 ? el[1] : el[2];
   auto put = [&](float* to) {
     reinterpret_cast<float4*>(to)[l] = make_float4(o[0], o[1], o[2], o[3]);
   };
-  reinterpret_cast<float4*>(v.hi)[l] = make_float4(hi[0], hi[1], hi[2], hi[3]);
-  reinterpret_cast<float4*>(v.lo)[l] = make_float4(lo[0], lo[1], lo[2], lo[3]);
+  if (part == 0) {
+    fill_weights<BACK>(hi, lo, scale, v.w);
+    const float eh = __shfl_sync(0xffffffffu, hi[3], 31), el = __shfl_sync(0xffffffffu, lo[3], 31);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = exp_diff(hi[i], lo[i], ah, al);
-  put(v.row);
-  bool small = true;  // every factor between e^-40 and e^40
+    for (int i = 0; i < 4; ++i)
+      o[i] = BACK ? exp_diff(eh, el, hi[i], lo[i]) : exp_diff(hi[i], lo[i], 0.f, 0.f);
+    put(v.far);
+  } else if (part == 1) {
+    reinterpret_cast<float4*>(v.hi)[l] = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    reinterpret_cast<float4*>(v.lo)[l] = make_float4(lo[0], lo[1], lo[2], lo[3]);
+    const int from = max(8 * blk - 1, 0);  // the lane with the end of the block before
+    float ah = __shfl_sync(0xffffffffu, hi[3], from), al = __shfl_sync(0xffffffffu, lo[3], from);
+    if (blk == 0) ah = al = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    small = small && o[i] > 4.3e-18f && o[i] < 2.3e17f;
-    o[i] = exp_diff(ah, al, hi[i], lo[i]);
-  }
-  put(v.own);
-  if (l == 0) v.mild = 0;
-  if (__all_sync(0xffffffffu, small) && l == 0) v.mild = 1;
+    for (int i = 0; i < 4; ++i) o[i] = exp_diff(hi[i], lo[i], ah, al);
+    put(v.row);
+    bool small = true;  // every factor between e^-40 and e^40
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = BACK ? exp_diff(eh[3], el[3], hi[i], lo[i]) : exp_diff(hi[i], lo[i], 0.f, 0.f);
-  put(v.far);
+    for (int i = 0; i < 4; ++i) {
+      small = small && o[i] > 4.3e-18f && o[i] < 2.3e17f;
+      o[i] = exp_diff(ah, al, hi[i], lo[i]);
+    }
+    put(v.own);
+    small = __all_sync(0xffffffffu, small);
+    if (l == 0) v.mild = small;
+  } else {
 #pragma unroll
-  for (int b = 0; b < 3; ++b) {
+    for (int b = 0; b < 3; ++b) {
+      const float eh = __shfl_sync(0xffffffffu, hi[3], 8 * b + 7);
+      const float el = __shfl_sync(0xffffffffu, lo[3], 8 * b + 7);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = blk <= b ? exp_diff(eh[b], el[b], hi[i], lo[i]) : 0.f;
-    put(v.tab[b]);
+      for (int i = 0; i < 4; ++i) o[i] = blk <= b ? exp_diff(eh, el, hi[i], lo[i]) : 0.f;
+      put(v.tab[b]);
+    }
   }
 }
 
@@ -285,14 +291,28 @@ __device__ __forceinline__ Who who() {
   t.lane = 32 * t.q4 + t.l;
   return t;
 }
-// Registers of the working warpgroups and of the third: together within what was launched.
-constexpr int REG_EPI = 216, REG_CTL = 64, REG_LAUNCH = 168;
-static_assert(256 * REG_EPI + 128 * REG_CTL <= NTHR * REG_LAUNCH, "the pool of the launch");
+// Registers of the working warpgroups and of the last one: together within what was launched.
+template <int THREADS>
+struct Regs {
+  static constexpr int LAUNCH = THREADS == 384 ? 168 : 96, EPI = THREADS == 384 ? 216 : 104, CTL = 64;
+  static_assert((THREADS - 128) * EPI + 128 * CTL <= THREADS * LAUNCH, "the pool of the launch");
+};
+template <int THREADS>
 __device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REG_EPI));
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(Regs<THREADS>::EPI));
 }
+template <int THREADS>
 __device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REG_CTL));
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<THREADS>::CTL));
+}
+// A warp's part of an event is done: its threads' tensor-memory accesses and, with SMEM,
+// their writes of operand tiles.
+template <bool SMEM>
+__device__ __forceinline__ void warp_done(uint64_t* bar) {
+  if (SMEM) fence_proxy_async_smem();
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 // The working warps meet, with the one for decay factors (ALL) or without it; true if any
 // has seen a wait run out.
@@ -303,7 +323,7 @@ __device__ __forceinline__ bool meet(volatile int* abort) {
       "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n"
       " selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(any)
-      : "r"(*abort), "n"(ALL ? 1 : 7), "n"(ALL ? NWORK : NWORK - 32)
+      : "r"(*abort), "n"(ALL ? 1 : 7), "n"(ALL ? NWORK : NWORK - 96)
       : "memory");
   return any != 0;
 }
@@ -326,6 +346,18 @@ __device__ __forceinline__ void load_tile(unsigned char* to, const CUtensorMap* 
   mbar_arrive_expect_tx(bar, D * TC * 2);
 #pragma unroll
   for (int c = 0; c < D; c += 64) tma_load_4d(to + (c >> 6) * HALF_TILE, map, c, h, tok, seq, bar);
+}
+// The same tile into L2 ahead of its load: with the slots that shared memory has room for, a
+// tile is asked for about half a chunk before its use, which covers L2's latency, not DRAM's.
+constexpr int AHEAD = 2;  // chunks
+template <int D>
+__device__ __forceinline__ void fetch_tile(const CUtensorMap* map, int h, int tok, int seq) {
+#pragma unroll
+  for (int c = 0; c < D; c += 64)
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];\n" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c), "r"(h), "r"(tok), "r"(seq)
+                 : "memory");
 }
 // Rows [len, TC) of a tile of D columns as zeros (a packed call's next sequence is there).
 template <int D>
@@ -418,43 +450,38 @@ __device__ __forceinline__ void add_state(uint32_t taddr, float by, float* s) {
     for (int j = 0; j < 32; ++j) s[i + j] = fmaf(by, s[i + j], d[j]);
   }
 }
-// An accumulator's N columns times `by` as packed bf16.
-template <int N>
-__device__ __forceinline__ void take_row(uint32_t taddr, float by, uint32_t* p) {
-#pragma unroll
+// An accumulator's N columns times `by` as bf16 rows in memory, through 2 KB of shared memory
+// of the warp's own: lanes hold different rows, and stored as they are every access would
+// touch 32 lines (2000 cycles of the load / store unit a chunk); read back it is 4 lanes to
+// the 64 bytes of a row. `taken` is called once the accumulator has been read.
+template <int N, class F>
+__device__ __forceinline__ void store_rows(uint32_t taddr, float by, unsigned char* stage, bf* out,
+                                           size_t ld, int rows, F taken) {
+  const int l = threadIdx.x & 31;
+#pragma unroll 1
   for (int i = 0; i < N; i += 32) {
     float v[32];
     tmem_ld32(taddr + i, v);
+    if (i + 32 == N) taken();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) p[i / 2 + j] = pack2bf(by * v[2 * j], by * v[2 * j + 1]);
+    for (int k = 0; k < 4; ++k) {
+      uint32_t u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = pack2bf(by * v[8 * k + 2 * j], by * v[8 * k + 2 * j + 1]);
+      *reinterpret_cast<uint4*>(stage + l * 64 + ((k ^ (l >> 1 & 3)) << 4)) =
+          make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 8 * k + (l >> 2), e = l & 3;
+      const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 64 + ((e ^ (r >> 1 & 3)) << 4));
+      if (r < rows) *reinterpret_cast<uint4*>(out + r * ld + i + 8 * e) = x;
+    }
+    __syncwarp();
   }
 }
-// A result's row into a tile that the copy engine stores: a warp's own stores, whose lanes
-// hold different rows, would touch 32 lines each and take the load / store unit 2000 cycles a
-// chunk. Or into memory, where the tile's last rows are another sequence's.
-template <int N>
-__device__ __forceinline__ void put_row(const uint32_t* p, unsigned char* tile, int r, int c, bf* to,
-                                        bool direct, bool on) {
-#pragma unroll
-  for (int i = 0; i < N / 2; i += 4) {
-    const uint4 x = make_uint4(p[i], p[i + 1], p[i + 2], p[i + 3]);
-    if (!direct)
-      *reinterpret_cast<uint4*>(at8(tile, HALF_TILE, r, c + 2 * i)) = x;
-    else if (on)
-      *reinterpret_cast<uint4*>(to + 2 * i) = x;
-  }
-}
-template <int D>
-__device__ __forceinline__ void store_tile(const CUtensorMap* map, const unsigned char* tile, int h,
-                                           int tok, int seq) {
-#pragma unroll
-  for (int c = 0; c < D; c += 64)
-    asm volatile(
-        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n" ::"l"(
-            reinterpret_cast<uint64_t>(map)),
-        "r"(c), "r"(h), "r"(tok), "r"(seq), "r"(smem_u32(tile + (c >> 6) * HALF_TILE))
-        : "memory");
-}
+constexpr uint32_t STAGE = 2048;  // bytes of a warp
 // After a wait that ran out: this CTA's copies still under way are waited for, with a
 // limit, before its shared memory is given up.
 __device__ __forceinline__ void drain(uint64_t* bars, int n, uint32_t phases) {
@@ -464,31 +491,37 @@ __device__ __forceinline__ void drain(uint64_t* bars, int n, uint32_t phases) {
   }
 }
 // Barriers, the abort flag and tensor memory; returns its address.
-__device__ __forceinline__ uint32_t set_up(const Who& t, uint64_t* bars, int n, uint32_t* tslot,
-                                           volatile int* abort) {
-  if (t.tid == CTL * 32) {
-    for (int i = 0; i < n; ++i) mbar_init(bars + i, 1);
+__device__ __forceinline__ uint32_t set_up(const Who& t, int ctl, uint64_t* bars, int n, int decs,
+                                           int teams, int both, uint32_t* tslot, volatile int* abort) {
+  // n barriers (the last `decs` events of the decay warps), then events of the 8 warps of a
+  // team, then of two teams
+  if (t.tid == ctl * 32) {
+    for (int i = 0; i < n + teams + both; ++i)
+      mbar_init(bars + i, i < n - decs ? 1 : i < n ? DEC_WARPS : i < n + teams ? 8 : 16);
     *abort = 0;
     fence_mbar_init();
   }
-  if (t.w == CTL) tmem_alloc(tslot, 512);
+  if (t.w == ctl) tmem_alloc(tslot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   return *tslot;
 }
-__device__ __forceinline__ void tear_down(const Who& t, uint64_t* full, int n, uint32_t tm,
+__device__ __forceinline__ void tear_down(const Who& t, int ctl, uint64_t* full, int n, uint32_t tm,
                                           volatile int* abort, int* status) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (t.tid == CTL * 32 && *abort) {
+  if (t.tid == ctl * 32 && *abort) {
     *status = DEV_TIMEOUT;
     drain(full, n, 0);
     drain(full, n, ~0u);
   }
   __syncthreads();
-  if (t.w == CTL) tmem_dealloc(tm, 512);
+  if (t.w == ctl) {
+    __syncwarp();
+    tmem_dealloc(tm, 512);
+  }
 }
 
 constexpr uint32_t slot_bytes(int a, int b) { return (a > b ? a : b) * TC * 2; }
@@ -500,6 +533,7 @@ constexpr uint32_t slot_bytes(int a, int b) { return (a > b ? a : b) * TC * 2; }
 // the next one and the update from the one before; three chunks' tiles are in flight.
 template <int DY, int DZ>
 struct StateSm {
+  static constexpr int THREADS = NTHR;
   static constexpr uint32_t SLOT = slot_bytes(DY, DZ), STAGES = 3;
   static constexpr uint32_t VEC = 2 * STAGES * SLOT, BAR = VEC + 4 * sizeof(Weights);
   static constexpr uint32_t BYTES = BAR + 128 + 1024;
@@ -526,7 +560,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   const int nch = (u.len + TC - 1) / TC;
-  const uint32_t tm = set_up(t, full, ST + 2, tslot, abort);
+  const uint32_t tm = set_up(t, CTL, full, ST + 2, 0, 0, 0, tslot, abort);
   auto chunk = [&](int i) { return REV ? nch - 1 - i : i; };
   auto raw = [&](int i) {
     const int c = chunk(i);
@@ -603,47 +637,57 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       __syncwarp();
     }
-  } else if (t.w == DEC) {
+  } else {
     auto fill = [&](const Raw& r, int i) {
       float hi[4], lo[4];
       sum_decay(r, a.decay != nullptr, hi, lo);
       fill_weights<REV>(hi, lo, a.scale, vec[i & 3]);
     };
-    fill(raw(0), 0);
-    if (nch > 1) fill(raw(1), 1);
+    const bool fills = t.w == DEC;  // the others only meet
     Raw ahead = {};
-    if (nch > 2) ahead = raw(2);
+    if (fills) {
+      fill(raw(0), 0);
+      if (nch > 1) fill(raw(1), 1);
+      if (nch > 2) ahead = raw(2);
+    }
     meet<true>(abort);
     for (int i = 0; i < nch; ++i) {
       if (meet<true>(abort)) break;
       // two ahead: visible behind the next chunk's meeting; four kept, for the chunk before
       // this one is still to be added
-      if (i + 2 < nch) fill(ahead, i + 2);
-      if (i + 3 < nch) ahead = raw(i + 3);
+      if (fills && i + 2 < nch) fill(ahead, i + 2);
+      if (fills && i + 3 < nch) ahead = raw(i + 3);
     }
   }
-  tear_down(t, full, ST, tm, abort, a.status);
+  tear_down(t, CTL, full, ST, tm, abort, a.status);
 }
 
 // ------------------------------------------------------------------ forward and dq
-// Per chunk, on the accumulators: P = x y^T masked, y weighed, x S scaled; then P z onto it,
-// the result, the state's sum. x y^T of the next chunk runs under the result and the state,
-// x S under P, so the MMAs that the warps wait for are P z and the sum. The tiles x, y, z
-// take the four slots in turn: y and z of the next chunk are copied as soon as x and y are
-// done with, x of the one after behind z.
+// Two teams of 8 warps work on a chunk's accumulators at the same time, each 128 rows x 2
+// groups of columns, and tell the warp that issues the MMAs by events. One takes P = x y^T
+// (masked, in place), scales x S and, once P z is on it, the result; the other weighs y and
+// adds up the state. In one team of either size the two strings of loads, arithmetic and
+// waits stood one behind the other (7 to 10 thousand cycles a chunk).
+//   MMAs: x S (state ready, result read) | P z, the state's sum (P, x S and y ready) | x y^T
+//   of the next chunk (P z done)
+// The tiles x, y, z take the four slots in turn: y and z of the next chunk are copied as soon
+// as x and y are done with, x of the one after when the result has left z's slot.
+constexpr int P_CTL = 16, P_DEC = 17, P_NTHR = 640;
+constexpr long long WAIT_LIMIT = 1ll << 32;  // cycles without progress (mbar_wait's own limit)
+static_assert((P_DEC + DEC_WARPS) * 32 == P_NTHR, "the last warpgroup");
 template <int DY, int DZ>
 struct PassSm {
+  static constexpr int THREADS = P_NTHR;
   static constexpr uint32_t SLOT = slot_bytes(DY, DZ), STATE = DY * DZ * 2, HALF_S = DY * 128;
   static constexpr uint32_t S_HI = 4 * SLOT, S_LO = S_HI + STATE, VEC = S_LO + STATE;
-  static constexpr uint32_t PART = VEC + 2 * sizeof(Vec), BAR = PART + 2 * TC * 4;
-  static constexpr uint32_t BYTES = BAR + 128 + 1024;
+  static constexpr uint32_t PART = VEC + 2 * sizeof(Vec), OUT = PART + 4 * TC * 4;
+  static constexpr uint32_t BAR = OUT + 8 * STAGE, BYTES = BAR + 192 + 1024;
 };
 template <int DY, int DZ, bool DQ>
-__global__ void __launch_bounds__(NTHR, 1)
+__global__ void __launch_bounds__(P_NTHR, 1)
     k_lin_tc_pass(Args a, const float* S_in, const float* S_unit, float* S_out, bf* out, const bf* q,
                   long long ldq, float* far, bool clear, const __grid_constant__ CUtensorMap mx,
-                  const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz,
-                  const __grid_constant__ CUtensorMap mo) {
+                  const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz) {
   using L = PassSm<DY, DZ>;
   constexpr int N = DZ / 2;
   constexpr uint32_t P0 = 0, O0 = 128, Y0 = 256, D0 = 384;
@@ -659,29 +703,29 @@ __global__ void __launch_bounds__(NTHR, 1)
   Vec* vec = reinterpret_cast<Vec*>(sb + L::VEC);
   float* part = reinterpret_cast<float*>(sb + L::PART);
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [4]
-  // MMAs: x y^T, x S, P z, the state's sum
-  uint64_t *bar_p = full + 4, *bar_s = full + 5, *bar_o = full + 6, *bar_d = full + 7;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 8);
+  // MMAs: x y^T, x S, P z, the state's sum; decay factors are there [2 buffers]
+  uint64_t *bar_p = full + 4, *bar_s = full + 5, *bar_o = full + 6, *bar_d = full + 7, *ev_v = full + 8;
+  // events of a team: P and x S ready; result read; y weighed; state ready; of both: decay
+  // factors used [2]. A barrier's next phase but one always depends on all who wait for it,
+  // so nobody can miss a phase.
+  uint64_t *ev_p = full + 10, *ev_o = full + 11, *ev_y = full + 12, *ev_s = full + 13, *ev_u = full + 14;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 16);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   const int nch = (u.len + TC - 1) / TC;
-  const uint32_t tm = set_up(t, full, 8, tslot, abort);
+  const uint32_t tm = set_up(t, P_CTL, full, 10, 2, 4, 2, tslot, abort);
+  const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
   auto tile = [&](int n) { return sb + (n & 3) * L::SLOT; };  // tile n: x, y or z of chunk n / 3
   auto wait_tile = [&](int n) { return mbar_wait(full + (n & 3), (n >> 2) & 1, abort); };
-  if (t.w < CTL) {
-    more_registers();
-    const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
-    const size_t sh = ((size_t)u.seq * a.H + h) * DY * DZ, uh = ((size_t)unit * a.H + h) * DY * DZ;
-    float s[N];
-    load_state<DY, DZ, DQ, N>(u.at ? S_unit + uh : S_in ? S_in + sh : nullptr, t.lane, N * t.cg, s);
-    if (t.lane < DY) put_split<N, DQ>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
-    fence_proxy_async_smem();
-    bool off = meet<true>(abort);
-    for (int c = 0; c < nch && !off; ++c) {
-      const int len = min(TC, u.len - c * TC), n0 = 3 * c;
-      const Vec& v = vec[c & 1];
+  // After a wait that ran out every role goes through its chunks without waiting.
+  if (t.w < 8) {  // ---- P and the result
+    more_registers<P_NTHR>();
+    for (int c = 0; c < nch; ++c) {
+      const int len = min(TC, u.len - c * TC), ph = c & 1;
+      const Vec& v = vec[ph];
       const int row = u.row + c * TC + t.lane;  // of this thread's result
       const bool on = t.lane < len;
-      // P: this thread's row t, columns [64 cg, 64 cg + 64) of x y^T, 32 at a time; as bf16 pairs
+      mbar_wait(ev_v + ph, (c >> 1) & 1, abort);
+      // This thread's row t, columns [64 cg, 64 cg + 64) of x y^T, 32 at a time; as bf16 pairs
       // into the first half of the same columns. So the second group, whose pairs go where the
       // first one's products are, waits until those have been read. The factors are loaded
       // together: under the MMAs a load of shared memory takes hundreds of cycles.
@@ -700,7 +744,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           }
         }
         if (j == 0) {
-          mbar_wait(bar_p, c & 1, abort);
+          mbar_wait(bar_p, ph, abort);
           tc_fence_after();
         }
         uint32_t p[16];
@@ -735,9 +779,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
         tmem_st16(tl + P0 + 32 * t.cg + 16 * j, p);
       }
-      wait_tile(n0 + 1);
-      if (t.lane < DY) weigh(tile(n0 + 1), t, v.w, len, tl + Y0);
-      mbar_wait(bar_s, c & 1, abort);
+      mbar_wait(bar_s, ph, abort);
       tc_fence_after();
       const float up = v.far[t.lane];
       float f = 0.f;  // q_t . (far part of dq_t)
@@ -770,39 +812,59 @@ __global__ void __launch_bounds__(NTHR, 1)
           }
         }
       }
-      if (DQ) part[t.cg * TC + t.lane] = a.scale * f;
       tmem_st_wait();
+      warp_done<false>(ev_p);
+      if (t.l == 0) mbar_arrive(ev_u + ph);
+      if (DQ) {
+        float* sums = part + 2 * TC * ph;
+        sums[t.cg * TC + t.lane] = a.scale * f;
+        named_bar(6, 256);
+        if (t.tid < len) far[(size_t)row * a.H + h] = sums[t.tid] + sums[TC + t.tid];
+      }
+      mbar_wait(bar_o, ph, abort);
+      tc_fence_after();
+      store_rows<N>(tl + O0 + N * t.cg, a.scale, sb + L::OUT + t.w * STAGE,
+                    out + ((size_t)(u.row + c * TC + 32 * t.q4) * a.H + h) * DZ + N * t.cg,
+                    (size_t)a.H * DZ, len - 32 * t.q4, [&] { warp_done<false>(ev_o); });
+    }
+  } else if (t.w < 16) {  // ---- the state
+    more_registers<P_NTHR>();
+    const size_t sh = ((size_t)u.seq * a.H + h) * DY * DZ, uh = ((size_t)unit * a.H + h) * DY * DZ;
+    float s[N];
+    load_state<DY, DZ, DQ, N>(u.at ? S_unit + uh : S_in ? S_in + sh : nullptr, t.lane, N * t.cg, s);
+    if (t.lane < DY) put_split<N, DQ>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
+    warp_done<true>(ev_s);
+    for (int c = 0; c < nch; ++c) {
+      const int len = min(TC, u.len - c * TC), n0 = 3 * c, ph = c & 1;
+      const Vec& v = vec[ph];
+      mbar_wait(ev_v + ph, (c >> 1) & 1, abort);
+      wait_tile(n0 + 1);
+      if (t.lane < DY) {
+        weigh(tile(n0 + 1), t, v.w, len, tl + Y0);
+        tmem_st_wait();
+      }
       if (len < TC && a.m.cu) {
         wait_tile(n0 + 2);
-        zero_rows<DZ>(tile(n0 + 2), len, t.tid);
-        fence_proxy_async_smem();
+        zero_rows<DZ>(tile(n0 + 2), len, t.tid - 256);
       }
-      tc_fence_before();
-      off = meet<false>(abort);
-      if (DQ && t.tid < len) far[(size_t)row * a.H + h] = part[t.tid] + part[TC + t.tid];
-      mbar_wait(bar_o, c & 1, abort);
-      tc_fence_after();
-      uint32_t res[N / 2];
-      take_row<N>(tl + O0 + N * t.cg, a.scale, res);
-      mbar_wait(bar_d, c & 1, abort);
+      warp_done<true>(ev_y);
+      mbar_wait(bar_d, ph, abort);
       tc_fence_after();
       if (t.lane < DY) {
         add_state<N>(tl + D0 + N * t.cg, v.w.whole, s);
+        mbar_wait(bar_s, ph, abort);  // x S has read the tiles
         put_split<N, DQ>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
       }
-      put_row<N>(res, tile(n0 + 2), t.lane, N * t.cg,  // z is done with
-                 out + ((size_t)row * a.H + h) * DZ + N * t.cg, len < TC && a.m.cu, on);
-      fence_proxy_async_smem();
-      tc_fence_before();
-      off = meet<true>(abort) || off;
+      warp_done<true>(ev_s);
+      if (t.l == 0) mbar_arrive(ev_u + ph);
     }
     if (u.at == u.n - 1 && S_out) store_state<DY, DZ, DQ, N>(S_out + sh, t.lane, N * t.cg, s);
   } else {
-    fewer_registers();
-    if (t.w == CTL) {
+    fewer_registers<P_NTHR>();
+    if (t.w == P_CTL && t.l == 0) {
       auto load = [&](int n) {
         const int c = n / 3, kind = n - 3 * c;
-        if (c >= nch) return;
+        if (c >= nch || *abort) return;
         const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
         uint64_t* bar = full + (n & 3);
         if (kind == 0)
@@ -812,28 +874,66 @@ __global__ void __launch_bounds__(NTHR, 1)
         else
           load_tile<DZ>(tile(n), &mz, h, tok, seq, bar);
       };
-      auto products = [&](int c) {  // x y^T
-        wait_tile(3 * c);
-        wait_tile(3 * c + 1);
-        const uint32_t x = smem_u32(tile(3 * c)), y = smem_u32(tile(3 * c + 1));
-#pragma unroll
-        for (int kk = 0; kk < DY / 16; ++kk)
-          umma_bf16(tm + P0, kmaj(x, HALF_TILE, kk), kmaj(y, HALF_TILE, kk),
-                    umma_idesc(128, 128, 0, 0), kk > 0);
-        umma_commit(bar_p);
+      auto fetch = [&](int c) {
+        if (c >= nch) return;
+        const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
+        fetch_tile<DY>(&mx, h, tok, seq);
+        fetch_tile<DY>(&my, h, tok, seq);
+        fetch_tile<DZ>(&mz, h, tok, seq);
       };
-      int kept = -1;  // the chunk whose result was stored last
-      if (t.l == 0) {
-        for (int n = 0; n < 4; ++n) load(n);
-        if (nch) products(0);
-      }
-      __syncwarp();
-      bool off = meet<true>(abort);
-      for (int c = 0; c < nch && !off; ++c) {
-        const int n0 = 3 * c;
-        if (t.l == 0) {
+      for (int n = 0; n < 4; ++n) load(n);
+      for (int c = 1; c < AHEAD; ++c) fetch(c);
+      // Each kind of work goes out as soon as what it needs is there, the products that a team
+      // waits for first. Issued so far: P z, the state's sum, x S, x y^T (chunks), tiles; seen
+      // done of each, and of the teams' events. Nothing is issued before its forerunner has
+      // been seen done, and nothing that lets an event happen again before that event has been
+      // seen: so no barrier is ever two phases ahead of what is asked about it.
+      int cz = 0, cd = 0, cs = 0, cp = 0, n = 4;
+      int bz = 0, bd = 0, bs = 0, bp = 0, wp = 0, wy = 0, ws = 0, wo = 0;
+      const int last = 3 * nch;
+      auto see = [&](uint64_t* bar, int& i, int most) {
+        if (i < most && mbar_test(bar, i & 1)) ++i;
+      };
+      auto have = [&](int n) { return mbar_test(full + (n & 3), (n >> 2) & 1); };
+      long long t0 = clock64();
+      while ((cz < nch || cd < nch || n < last) && !*abort) {
+        see(bar_o, bz, cz);
+        see(bar_d, bd, cd);
+        see(bar_s, bs, cs);
+        see(bar_p, bp, cp);
+        see(ev_p, wp, nch);
+        see(ev_y, wy, nch);
+        see(ev_s, ws, nch);
+        see(ev_o, wo, nch);
+        bool idle = true;
+        if (cz < cs && cz == bz && wp > cz && have(3 * cz + 2) &&
+            (!a.m.cu || u.len - cz * TC >= TC || wy > cz)) {  // a tail's z has been zeroed
           tc_fence_after();
-          const uint32_t x = smem_u32(tile(n0));
+          const uint32_t z = smem_u32(tile(3 * cz + 2));
+#pragma unroll
+          for (int kk = 0; kk < TC / 16; ++kk)
+            umma_ts(tm + O0, tm + P0 + 8 * kk, mnmaj(z, HALF_TILE, kk), umma_idesc(128, DZ, 0, 1), true);
+          umma_commit(bar_o);
+          ++cz;
+          idle = false;
+        }
+        if (cd < cp && cd <= cz && cd == bd && wy > cd && ws > cd && have(3 * cd + 2)) {
+          tc_fence_after();
+          const uint32_t z = smem_u32(tile(3 * cd + 2));
+#pragma unroll 1
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int kk = 0; kk < TC / 16; ++kk)
+              umma_ts(tm + D0, tm + Y0 + 64 * p + 8 * kk, mnmaj(z, HALF_TILE, kk),
+                      umma_idesc(128, DZ, 0, 1), p || kk);
+          umma_commit(bar_d);
+          ++cd;
+          idle = false;
+        }
+        // the state and x are ready, the result before has been read
+        if (cs < cp && cs <= cz && cs == bs && ws > cs && wo >= cs) {
+          tc_fence_after();
+          const uint32_t x = smem_u32(tile(3 * cs));
           // the forward's result takes the first part alone, which is as good as its own bits
 #pragma unroll 1
           for (int p = 0; p < (DQ ? 2 : 1); ++p)
@@ -842,65 +942,51 @@ __global__ void __launch_bounds__(NTHR, 1)
               umma_bf16(tm + O0, kmaj(x, HALF_TILE, kk), mnmaj(smem_u32(p ? s_lo : s_hi), L::HALF_S, kk),
                         umma_idesc(128, DZ, 0, 1), p || kk);
           umma_commit(bar_s);
-          if (kept >= 0) {  // the result before has left z's tile: x of the next chunk takes it
-            bulk_wait_read();
-            load(3 * kept + 6);
-          }
+          ++cs;
+          idle = false;
         }
-        __syncwarp();
-        off = meet<false>(abort);
-        if (t.l == 0) {
+        // P of the chunk before has been read
+        if (cp < nch && cp == bp && bz >= cp && have(3 * cp) && have(3 * cp + 1)) {
           tc_fence_after();
-          wait_tile(n0 + 2);
-          const uint32_t z = smem_u32(tile(n0 + 2));
-          constexpr uint32_t id = umma_idesc(128, DZ, 0, 1);
+          const uint32_t x = smem_u32(tile(3 * cp)), y = smem_u32(tile(3 * cp + 1));
 #pragma unroll
-          for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + O0, tm + P0 + 8 * kk, mnmaj(z, HALF_TILE, kk), id, true);
-          umma_commit(bar_o);
-#pragma unroll 1
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int kk = 0; kk < TC / 16; ++kk)
-              umma_ts(tm + D0, tm + Y0 + 64 * p + 8 * kk, mnmaj(z, HALF_TILE, kk), id, p || kk);
-          umma_commit(bar_d);
-          if (!*abort) {  // x and y are done with
-            load(n0 + 4);
-            load(n0 + 5);
-          }
-          mbar_wait(bar_o, c & 1, abort);  // P has been read
-          if (c + 1 < nch) products(c + 1);
+          for (int kk = 0; kk < DY / 16; ++kk)
+            umma_bf16(tm + P0, kmaj(x, HALF_TILE, kk), kmaj(y, HALF_TILE, kk),
+                      umma_idesc(128, 128, 0, 0), kk > 0);
+          umma_commit(bar_p);
+          ++cp;
+          fetch(cp + AHEAD - 1);
+          idle = false;
         }
-        __syncwarp();
-        off = meet<true>(abort) || off;
-        if (t.l == 0 && !off) {  // the result is in z's tile
-          if (!a.m.cu || u.len - c * TC >= TC) {
-            const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC;
-            store_tile<DZ>(&mo, tile(n0 + 2), h, tok, a.m.cu ? 0 : u.seq);
-            bulk_commit();
+        if (n < last) {  // tile n - 4, whose slot it takes, is done with
+          const int c = (n - 4) / 3, kind = n - 4 - 3 * c;
+          if (kind == 0 ? bs > c && bp > c : kind == 1 ? bp > c && wy > c : bz > c && bd > c) {
+            load(n++);
+            idle = false;
           }
-          kept = c;
         }
-        __syncwarp();
+        if (!idle)
+          t0 = clock64();
+        else if (clock64() - t0 > WAIT_LIMIT)
+          *abort = 1;
       }
-      if (t.l == 0) bulk_wait_all();
-    } else if (t.w == DEC) {
+    } else if (t.w >= P_DEC) {
       auto raw = [&](int c) {
         return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
       };
       const bool wide = a.decay != nullptr;
       Raw ahead = {};
-      if (nch) fill_vec<false>(raw(0), wide, 1.f, vec[0]);
-      if (nch > 1) ahead = raw(1);
-      bool off = meet<true>(abort);
-      for (int c = 0; c < nch && !off; ++c) {
-        if (c + 1 < nch) fill_vec<false>(ahead, wide, 1.f, vec[(c + 1) & 1]);
-        if (c + 2 < nch) ahead = raw(c + 2);
-        off = meet<true>(abort);
+      if (nch) ahead = raw(0);
+      for (int c = 0; c < nch; ++c) {
+        if (c > 1) mbar_wait(ev_u + (c & 1), ((c >> 1) + 1) & 1, abort);  // those of chunk c - 2
+        fill_vec<false>(t.w - P_DEC, ahead, wide, 1.f, vec[c & 1]);
+        if (c + 1 < nch) ahead = raw(c + 1);
+        __syncwarp();
+        if (t.l == 0) mbar_arrive(ev_v + (c & 1));
       }
     }
   }
-  tear_down(t, full, 4, tm, abort, a.status);
+  tear_down(t, P_CTL, full, 4, tm, abort, a.status);
 }
 
 // ------------------------------------------------------------------ dk, dv and dg
@@ -915,10 +1001,11 @@ __global__ void __launch_bounds__(NTHR, 1)
 // X = <S, R> behind the chunk, taken from the states themselves at the unit's end.
 template <int DK, int DV>
 struct BackSm {
+  static constexpr int THREADS = NTHR;
   static constexpr uint32_t SLOT = slot_bytes(DK, DV), STATE = DK * DV * 2, HALF_R = DK * 128;
   static constexpr uint32_t R_HI = 4 * SLOT, R_LO = R_HI + STATE, VEC = R_LO + STATE;
   static constexpr uint32_t ROWS = VEC + 2 * sizeof(Vec), COLS = ROWS + 4 * TC * 4,
-                            FAR = COLS + 2 * TC * 4, RED = FAR + 2 * TC * 4, BAR = RED + 64;
+                            FAR = COLS + 2 * TC * 4, RED = FAR + 2 * TC * 4, OUT = RED + 64, BAR = OUT + 8 * STAGE;
   static constexpr uint32_t BYTES = BAR + 128 + 1024;
 };
 // x[0..31] summed over the warp's lanes; lane j returns the sum of x[j].
@@ -942,8 +1029,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                   const float* S_end, float* dS_in, const float* far, bf* dk, bf* dv, bf* dg,
                   float* dgsum, const __grid_constant__ CUtensorMap mq,
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                  const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mdk,
-                  const __grid_constant__ CUtensorMap mdv) {
+                  const __grid_constant__ CUtensorMap mo) {
   using L = BackSm<DK, DV>;
   constexpr int NK = DK / 2, NV = DV / 2;
   // A1: k q^T, then P1; A2: v dO^T, then P2; G1: the weighed q, then dk; G2: R's sum, then dv
@@ -967,16 +1053,16 @@ __global__ void __launch_bounds__(NTHR, 1)
   float* red = reinterpret_cast<float*>(sb + L::RED);
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [4] v, k, q, dO
   // q and dO of a chunk take the slots of v and k of the one before, which are done with
-  // early; v and k those of q and dO, which first take the results on their way out
+  // early, v and k those of q and dO
   auto slot = [&](int kind, int i) { return sb + (kind ^ (i & 1 ? 2 : 0)) * L::SLOT; };
   // MMAs: R's sum, k q^T and v dO^T, products with R, results
   uint64_t *bar_e = full + 4, *bar_a = full + 5, *bar_f = full + 6, *bar_c = full + 7;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 8);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   const int nch = (u.len + TC - 1) / TC;
-  const uint32_t tm = set_up(t, full, 8, tslot, abort);
+  const uint32_t tm = set_up(t, CTL, full, 8, 0, 0, 0, tslot, abort);
   if (t.w < CTL) {
-    more_registers();
+    more_registers<NTHR>();
     const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
     const size_t sh = ((size_t)u.seq * a.H + h) * DK * DV;
     const bool last = u.at == u.n - 1;
@@ -1009,8 +1095,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     for (int i = 0; i < nch && !off; ++i) {
       const int c = nch - 1 - i, len = min(TC, u.len - c * TC), ph = i & 1;
       const Vec& v = vec[ph];
-      const int row0 = u.row + c * TC, row = row0 + t.lane;
-      const bool on = t.lane < len;
+      const int row0 = u.row + c * TC;
       float fa[4] = {};  // a of the tokens 4 l ..
       if (forms) {
 #pragma unroll
@@ -1163,23 +1248,12 @@ __global__ void __launch_bounds__(NTHR, 1)
       mbar_wait(bar_c, ph, abort);
       tc_fence_after();
       {
-        const bool direct = len < TC && a.m.cu;
-#pragma unroll 1
-        for (int e = 0; e < NK; e += 32) {
-          uint32_t res[16];
-          take_row<32>(tl + G1 + NK * t.cg + e, 1.f, res);
-          put_row<32>(res, slot(2, i), t.lane, NK * t.cg + e,
-                      dk + ((size_t)row * a.H + h) * DK + NK * t.cg + e, direct, on);
-        }
-        fence_proxy_async_smem();
-        off = meet<false>(abort) || off;  // dk is in q's slot
-#pragma unroll 1
-        for (int e = 0; e < NV; e += 32) {
-          uint32_t res[16];
-          take_row<32>(tl + G2 + NV * t.cg + e, 1.f, res);
-          put_row<32>(res, slot(3, i), t.lane, NV * t.cg + e,
-                      dv + ((size_t)row * a.H + h) * DV + NV * t.cg + e, direct, on);
-        }
+        unsigned char* stage = sb + L::OUT + t.w * STAGE;
+        const size_t first = (size_t)(row0 + 32 * t.q4) * a.H + h;
+        store_rows<NK>(tl + G1 + NK * t.cg, 1.f, stage, dk + first * DK + NK * t.cg, (size_t)a.H * DK,
+                       len - 32 * t.q4, [] {});
+        store_rows<NV>(tl + G2 + NV * t.cg, 1.f, stage, dv + first * DV + NV * t.cg, (size_t)a.H * DV,
+                       len - 32 * t.q4, [] {});
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -1191,7 +1265,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       if (t.l == 0) dgsum[uh] = sum;
     }
   } else {
-    fewer_registers();
+    fewer_registers<NTHR>();
     if (t.w == CTL) {
       auto load = [&](int kind, int i) {  // a tile of the i-th chunk from the end
         if (i >= nch) return;
@@ -1207,19 +1281,26 @@ __global__ void __launch_bounds__(NTHR, 1)
         else
           load_tile<DV>(to, &mo, h, tok, seq, full + 3);
       };
-      if (t.l == 0)
+      auto fetch = [&](int i) {
+        if (i >= nch) return;
+        const int c = nch - 1 - i;
+        const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
+        fetch_tile<DK>(&mq, h, tok, seq);
+        fetch_tile<DV>(&mo, h, tok, seq);
+        fetch_tile<DK>(&mk, h, tok, seq);
+        fetch_tile<DV>(&mv, h, tok, seq);
+      };
+      if (t.l == 0) {
         for (int k = 3; k >= 0; --k) load(k, 0);
+        for (int i = 1; i < AHEAD; ++i) fetch(i);
+      }
       __syncwarp();
       bool off = meet<true>(abort);
       for (int i = 0; i < nch && !off; ++i) {
         const int ph = i & 1;
+        if (t.l == 0) fetch(i + AHEAD);
         const uint32_t sv = smem_u32(slot(0, i)), sk = smem_u32(slot(1, i)),
                        sq = smem_u32(slot(2, i)), so = smem_u32(slot(3, i));
-        if (t.l == 0 && i) {  // dv of the chunk before has left: k
-          bulk_wait_read();
-          load(1, i);
-        }
-        __syncwarp();
         off = meet<false>(abort);  // the weighed q is there (and a tail's rows are zeros)
         if (t.l == 0) {
           tc_fence_after();
@@ -1279,46 +1360,32 @@ __global__ void __launch_bounds__(NTHR, 1)
           umma_commit(bar_c);
         }
         __syncwarp();
-        off = meet<false>(abort) || off;
-        const int c = nch - 1 - i, tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC;
-        const bool whole = !a.m.cu || u.len - c * TC >= TC;
-        if (t.l == 0 && !off) {
-          if (whole) {
-            store_tile<DK>(&mdk, slot(2, i), h, tok, a.m.cu ? 0 : u.seq);
-            bulk_commit();
-            bulk_wait_read();
-          }
+        if (t.l == 0 && !off) {  // the last products are done: q and dO
+          mbar_wait(bar_c, ph, abort);
+          load(1, i + 1);
           load(0, i + 1);
         }
         __syncwarp();
         off = meet<true>(abort) || off;
-        if (t.l == 0 && !off) {
-          if (whole) {
-            store_tile<DV>(&mdv, slot(3, i), h, tok, a.m.cu ? 0 : u.seq);
-            bulk_commit();
-          }
-        }
-        __syncwarp();
       }
-      if (t.l == 0) bulk_wait_all();
-    } else if (t.w == DEC) {
+    } else {
       auto raw = [&](int i) {
         const int c = nch - 1 - i;
         return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
       };
       const bool wide = a.decay != nullptr;
       Raw ahead = {};
-      if (nch) fill_vec<true>(raw(0), wide, a.scale, vec[0]);
+      if (nch) fill_vec<true>(t.w - DEC, raw(0), wide, a.scale, vec[0]);
       if (nch > 1) ahead = raw(1);
       bool off = meet<true>(abort);
       for (int i = 0; i < nch && !off; ++i) {
-        if (i + 1 < nch) fill_vec<true>(ahead, wide, a.scale, vec[(i + 1) & 1]);
+        if (i + 1 < nch) fill_vec<true>(t.w - DEC, ahead, wide, a.scale, vec[(i + 1) & 1]);
         if (i + 2 < nch) ahead = raw(i + 2);
         off = meet<true>(abort);
       }
     }
   }
-  tear_down(t, full, 4, tm, abort, a.status);
+  tear_down(t, CTL, full, 4, tm, abort, a.status);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1412,27 +1479,20 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   const gdn_lin_shape& s = c.s;
   const TcPlan p = tc_plan(s, c.cu, c.cu != nullptr, back, c.ws);
   const Args a = {p.m, s.H, s.scale, (const bf*)c.g, c.decay, s.ldg, p.status};
-  CUtensorMap mq, mk, mv, mo, mdq, mdk, mdv;
+  CUtensorMap mq, mk, mv, mo;
   cudaError_t e;
   if ((e = tile_map(&mq, c.q, s, DK, s.ldq)) || (e = tile_map(&mk, c.k, s, DK, s.ldk)) ||
       (e = tile_map(&mv, c.v, s, DV, s.ldv)))
     return e;
-  const long long rk = (long long)s.H * DK, rv = (long long)s.H * DV;
-  if (back) {
-    if ((e = tile_map(&mo, c.dout, s, DV, rv)) || (e = tile_map(&mdq, c.dq, s, DK, rk)) ||
-        (e = tile_map(&mdk, c.dk, s, DK, rk)) || (e = tile_map(&mdv, c.dv, s, DV, rv)))
-      return e;
-  } else if ((e = tile_map(&mo, c.o, s, DV, rv))) {
-    return e;
-  }
+  if (back && (e = tile_map(&mo, c.dout, s, DV, (long long)s.H * DV))) return e;
   if (c.cu && (e = lin_plan(p.m, p.first, p.owner, p.status, c.st))) return e;
   bool clear = !c.cu;  // the first kernel of an unpacked call resets the status word
-  const dim3 grid(p.m.cap * s.H), block(NTHR);
-  auto go = [&](auto kernel, cudaError_t ready, uint32_t smem, auto... rest) {
-    return ready ? ready : launch(kernel, grid, block, (int)smem, c.st, 1, a, rest...);
+  const dim3 grid(p.m.cap * s.H);
+  auto go = [&](auto kernel, cudaError_t ready, uint32_t smem, int threads, auto... rest) {
+    return ready ? ready : launch(kernel, grid, dim3(threads), (int)smem, c.st, 1, a, rest...);
   };
 #define GO(kernel, Sm, regs, ...) \
-  go(kernel, allow<kernel>(Sm::BYTES, regs), Sm::BYTES, __VA_ARGS__)
+  go(kernel, allow<kernel>(Sm::BYTES, regs), Sm::BYTES, Sm::THREADS, __VA_ARGS__)
   using SmKV = StateSm<DK, DV>;
   using SmVK = StateSm<DV, DK>;
   if (p.many) {
@@ -1454,16 +1514,14 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   using Back = BackSm<DK, DV>;
   prof_mark(c.st, back ? "lin_tc_dq" : "lin_tc_fwd");
   if (!back)
-    return GO((k_lin_tc_pass<DK, DV, false>), PassKV, REG_LAUNCH, c.S_in, p.D, c.S_out, (bf*)c.o,
-              (const bf*)nullptr, 0ll, (float*)nullptr, clear, mq, mk, mv, mo);
-  e = GO((k_lin_tc_pass<DV, DK, true>), PassVK, REG_LAUNCH, c.S_in, p.D,
-         c.dS_out ? p.S_end : (float*)nullptr, (bf*)c.dq, (const bf*)c.q, s.ldq, p.far, clear, mo, mv, mk,
-         mdq);
+    return GO((k_lin_tc_pass<DK, DV, false>), PassKV, Regs<P_NTHR>::LAUNCH, c.S_in, p.D, c.S_out, (bf*)c.o,
+              (const bf*)nullptr, 0ll, (float*)nullptr, clear, mq, mk, mv);
+  e = GO((k_lin_tc_pass<DV, DK, true>), PassVK, Regs<P_NTHR>::LAUNCH, c.S_in, p.D,
+         c.dS_out ? p.S_end : (float*)nullptr, (bf*)c.dq, (const bf*)c.q, s.ldq, p.far, clear, mo, mv, mk);
   if (e) return e;
   prof_mark(c.st, "lin_tc_back");
-  e = GO((k_lin_tc_back<DK, DV>), Back, REG_LAUNCH, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
-         (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo, mdk,
-         mdv);
+  e = GO((k_lin_tc_back<DK, DV>), Back, Regs<NTHR>::LAUNCH, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
+         (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo);
 #undef GO
   if (e) return e;
   if (c.ddecay) e = col_sum(p.dgsum, p.m.cap, s.H, s.H, c.ddecay, nullptr, nullptr, c.st);
