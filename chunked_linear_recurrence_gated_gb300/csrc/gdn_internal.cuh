@@ -45,9 +45,9 @@ cudaError_t tc_bwd(const SeqMap& m, int dv, const void* q, const void* k, const 
 // workspace array [nbh][rows][row_stride] with 64-element x box_rows boxes.
 cudaError_t make_tok_map(CUtensorMap* map, const void* base, int d, const SeqMap& m);
 // make_tile_map: any 4-D bf16 tensor (strides in bytes of dimensions 1 to 3) in boxes of
-// 64 elements x 1 x box x 1.
+// cols (64 or 32) elements x 1 x box x 1, with the swizzle of that width.
 cudaError_t make_tile_map(CUtensorMap* map, const void* base, const cuuint64_t* dims,
-                          const cuuint64_t* strides, int box);
+                          const cuuint64_t* strides, int cols, int box);
 cudaError_t make_ws_map(CUtensorMap* map, const void* base, int inner, int rows, int row_stride,
                         long long nbh, int box_rows);
 

@@ -143,8 +143,8 @@ struct Weights {
   float whole, pad[3];  // e^{gamma_C}
 };
 // Of a chunk: L_ts = row[t] tab[b - 1][s] for t in the block b of 32 behind that of s. Within
-// a block it is row[t] own[s] where the block's decay leaves the second factor small
-// (`mild`), else the exponential of the difference.
+// a block it is row[t] own[s] where the block's decay leaves both factors within fp32's range
+// (`mild`, a block's), else the exponential of the difference.
 struct Vec {
   Weights w;
   float hi[TC], lo[TC];  // gamma, as the sum of two floats
@@ -152,7 +152,7 @@ struct Vec {
   float far[TC];         // forward: e^{gamma_t}; back: e^{gamma_C - gamma_t}
   float own[TC];         // e^{gamma_a - gamma_s}
   float tab[3][TC];      // [b - 1][s]: e^{gamma_{32 b - 1} - gamma_s} for s < 32 b
-  int mild, pad[3];
+  int mild[4];
 };
 
 // The log-decays of a chunk, 4 tokens for each lane of a warp: loaded a chunk ahead of their
@@ -229,9 +229,9 @@ __device__ __forceinline__ void fill_weights(const float* hi, const float* lo, f
   for (int i = 0; i < 2; ++i) split2(o[2 * i], o[2 * i + 1], w.hi[2 * l + i], w.lo[2 * l + i]);
   if (l == 0) w.whole = exp_diff(eh, el, 0.f, 0.f);
 }
-// One of three warps' part of a chunk's factors (each sums gamma for itself: one warp took
+// One of two warps' part of a chunk's factors (each sums gamma for itself: one warp took
 // 9 thousand cycles for all of them, twice what the rest of a chunk needs).
-constexpr int DEC_WARPS = 3;
+constexpr int DEC_WARPS = 2;
 template <bool BACK>
 __device__ __forceinline__ void fill_vec(int part, const Raw& r, bool wide, float scale, Vec& v) {
   const int l = threadIdx.x & 31, blk = l >> 3;  // this lane's block of 32 tokens
@@ -240,14 +240,24 @@ __device__ __forceinline__ void fill_vec(int part, const Raw& r, bool wide, floa
   auto put = [&](float* to) {
     reinterpret_cast<float4*>(to)[l] = make_float4(o[0], o[1], o[2], o[3]);
   };
+  auto put_tab = [&](int b) {
+    const float eh = __shfl_sync(0xffffffffu, hi[3], 8 * b + 7);
+    const float el = __shfl_sync(0xffffffffu, lo[3], 8 * b + 7);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = blk <= b ? exp_diff(eh, el, hi[i], lo[i]) : 0.f;
+    put(v.tab[b]);
+  };
   if (part == 0) {
+    put_tab(0);
     fill_weights<BACK>(hi, lo, scale, v.w);
     const float eh = __shfl_sync(0xffffffffu, hi[3], 31), el = __shfl_sync(0xffffffffu, lo[3], 31);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       o[i] = BACK ? exp_diff(eh, el, hi[i], lo[i]) : exp_diff(hi[i], lo[i], 0.f, 0.f);
     put(v.far);
-  } else if (part == 1) {
+  } else {
+    put_tab(1);
+    put_tab(2);
     reinterpret_cast<float4*>(v.hi)[l] = make_float4(hi[0], hi[1], hi[2], hi[3]);
     reinterpret_cast<float4*>(v.lo)[l] = make_float4(lo[0], lo[1], lo[2], lo[3]);
     const int from = max(8 * blk - 1, 0);  // the lane with the end of the block before
@@ -256,24 +266,15 @@ __device__ __forceinline__ void fill_vec(int part, const Raw& r, bool wide, floa
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = exp_diff(hi[i], lo[i], ah, al);
     put(v.row);
-    bool small = true;  // every factor between e^-40 and e^40
+    bool small = true;  // every factor between e^-80 and e^80
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      small = small && o[i] > 4.3e-18f && o[i] < 2.3e17f;
+      small = small && o[i] > 1.9e-35f && o[i] < 5.5e34f;
       o[i] = exp_diff(ah, al, hi[i], lo[i]);
     }
     put(v.own);
-    small = __all_sync(0xffffffffu, small);
-    if (l == 0) v.mild = small;
-  } else {
-#pragma unroll
-    for (int b = 0; b < 3; ++b) {
-      const float eh = __shfl_sync(0xffffffffu, hi[3], 8 * b + 7);
-      const float el = __shfl_sync(0xffffffffu, lo[3], 8 * b + 7);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = blk <= b ? exp_diff(eh, el, hi[i], lo[i]) : 0.f;
-      put(v.tab[b]);
-    }
+    const uint32_t all = __ballot_sync(0xffffffffu, small);
+    if (l < 4) v.mild[l] = (all >> (8 * l) & 0xffu) == 0xffu;
   }
 }
 
@@ -346,18 +347,6 @@ __device__ __forceinline__ void load_tile(unsigned char* to, const CUtensorMap* 
   mbar_arrive_expect_tx(bar, D * TC * 2);
 #pragma unroll
   for (int c = 0; c < D; c += 64) tma_load_4d(to + (c >> 6) * HALF_TILE, map, c, h, tok, seq, bar);
-}
-// The same tile into L2 ahead of its load: with the slots that shared memory has room for, a
-// tile is asked for about half a chunk before its use, which covers L2's latency, not DRAM's.
-constexpr int AHEAD = 2;  // chunks
-template <int D>
-__device__ __forceinline__ void fetch_tile(const CUtensorMap* map, int h, int tok, int seq) {
-#pragma unroll
-  for (int c = 0; c < D; c += 64)
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];\n" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c), "r"(h), "r"(tok), "r"(seq)
-                 : "memory");
 }
 // Rows [len, TC) of a tile of D columns as zeros (a packed call's next sequence is there).
 template <int D>
@@ -450,35 +439,53 @@ __device__ __forceinline__ void add_state(uint32_t taddr, float by, float* s) {
     for (int j = 0; j < 32; ++j) s[i + j] = fmaf(by, s[i + j], d[j]);
   }
 }
-// An accumulator's N columns times `by` as bf16 rows in memory, through 2 KB of shared memory
-// of the warp's own: lanes hold different rows, and stored as they are every access would
-// touch 32 lines (2000 cycles of the load / store unit a chunk); read back it is 4 lanes to
-// the 64 bytes of a row. `taken` is called once the accumulator has been read.
+// An accumulator's N columns times `by` as bf16, through 2 KB of shared memory of the warp's
+// own (32 rows of 32 columns, 64-byte swizzle) that the copy engine stores: it writes while
+// the warp goes on, which would wait for its own stores (an SM sends about 25 bytes a cycle).
+// `taken` is called once the accumulator has been read. direct: a tile whose last rows are
+// another sequence's, stored row by row.
 template <int N, class F>
-__device__ __forceinline__ void store_rows(uint32_t taddr, float by, unsigned char* stage, bf* out,
-                                           size_t ld, int rows, F taken) {
+__device__ __forceinline__ void store_rows(uint32_t taddr, float by, unsigned char* stage,
+                                           const CUtensorMap* map, int col, int h, int tok, int seq,
+                                           bf* out, bool direct, int rows, F taken) {
   const int l = threadIdx.x & 31;
-#pragma unroll 1
+  uint32_t p[N / 2];
+#pragma unroll
   for (int i = 0; i < N; i += 32) {
     float v[32];
     tmem_ld32(taddr + i, v);
-    if (i + 32 == N) taken();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) p[i / 2 + j] = pack2bf(by * v[2 * j], by * v[2 * j + 1]);
+  }
+  taken();
+  if (direct) {
+    if (l < rows)
+#pragma unroll
+      for (int i = 0; i < N / 2; i += 4)
+        *reinterpret_cast<uint4*>(out + 2 * i) = make_uint4(p[i], p[i + 1], p[i + 2], p[i + 3]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 32) {
+    if (l == 0) bulk_wait_read();  // the rows before have left
+    __syncwarp();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      uint32_t u[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = pack2bf(by * v[8 * k + 2 * j], by * v[8 * k + 2 * j + 1]);
+      const uint32_t* u = p + i / 2 + 4 * k;
       *reinterpret_cast<uint4*>(stage + l * 64 + ((k ^ (l >> 1 & 3)) << 4)) =
           make_uint4(u[0], u[1], u[2], u[3]);
     }
+    fence_proxy_async_smem();
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = 8 * k + (l >> 2), e = l & 3;
-      const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 64 + ((e ^ (r >> 1 & 3)) << 4));
-      if (r < rows) *reinterpret_cast<uint4*>(out + r * ld + i + 8 * e) = x;
+    if (l == 0) {
+      if (rows > 0)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n" ::"l"(
+                reinterpret_cast<uint64_t>(map)),
+            "r"(col + i), "r"(h), "r"(tok), "r"(seq), "r"(smem_u32(stage))
+            : "memory");
+      bulk_commit();
     }
-    __syncwarp();
   }
 }
 constexpr uint32_t STAGE = 2048;  // bytes of a warp
@@ -501,6 +508,7 @@ __device__ __forceinline__ uint32_t set_up(const Who& t, int ctl, uint64_t* bars
     *abort = 0;
     fence_mbar_init();
   }
+  if (t.tid < 8) (reinterpret_cast<volatile int*>(tslot + 2))[t.tid] = 0;  // counters behind the flag
   if (t.w == ctl) tmem_alloc(tslot, 512);
   tc_fence_before();
   __syncthreads();
@@ -670,25 +678,29 @@ __global__ void __launch_bounds__(NTHR, 1)
 // waits stood one behind the other (7 to 10 thousand cycles a chunk).
 //   MMAs: x S (state ready, result read) | P z, the state's sum (P, x S and y ready) | x y^T
 //   of the next chunk (P z done)
-// The tiles x, y, z take the four slots in turn: y and z of the next chunk are copied as soon
-// as x and y are done with, x of the one after when the result has left z's slot.
-constexpr int P_CTL = 16, P_DEC = 17, P_NTHR = 640;
+// The tiles x, y, z take the slots in turn, each as soon as the one before is done with it.
+constexpr int P_CTL = 16, P_DEC = 17, P_LOAD = 19, P_NTHR = 640;
 constexpr long long WAIT_LIMIT = 1ll << 32;  // cycles without progress (mbar_wait's own limit)
-static_assert((P_DEC + DEC_WARPS) * 32 == P_NTHR, "the last warpgroup");
-template <int DY, int DZ>
+static_assert(P_DEC + DEC_WARPS == P_LOAD && (P_LOAD + 1) * 32 == P_NTHR, "the last warpgroup");
+template <int DY, int DZ, bool DQ>
 struct PassSm {
   static constexpr int THREADS = P_NTHR;
+  // the forward, without second parts of the state, has room for the next chunk's y ahead of
+  // the slot of this one's x
+  static constexpr int SLOTS = DQ ? 4 : 5;
   static constexpr uint32_t SLOT = slot_bytes(DY, DZ), STATE = DY * DZ * 2, HALF_S = DY * 128;
-  static constexpr uint32_t S_HI = 4 * SLOT, S_LO = S_HI + STATE, VEC = S_LO + STATE;
-  static constexpr uint32_t PART = VEC + 2 * sizeof(Vec), OUT = PART + 4 * TC * 4;
+  static constexpr uint32_t S_HI = SLOTS * SLOT, S_LO = S_HI + STATE, VEC = S_LO + (DQ ? STATE : 0);
+  static constexpr uint32_t PART = VEC + 2 * sizeof(Vec), OUT = (PART + 4 * TC * 4 + 511) / 512 * 512;
   static constexpr uint32_t BAR = OUT + 8 * STAGE, BYTES = BAR + 192 + 1024;
 };
 template <int DY, int DZ, bool DQ>
 __global__ void __launch_bounds__(P_NTHR, 1)
     k_lin_tc_pass(Args a, const float* S_in, const float* S_unit, float* S_out, bf* out, const bf* q,
                   long long ldq, float* far, bool clear, const __grid_constant__ CUtensorMap mx,
-                  const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz) {
-  using L = PassSm<DY, DZ>;
+                  const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz,
+                  const __grid_constant__ CUtensorMap mo) {
+  using L = PassSm<DY, DZ, DQ>;
+  constexpr int SL = L::SLOTS;
   constexpr int N = DZ / 2;
   constexpr uint32_t P0 = 0, O0 = 128, Y0 = 256, D0 = 384;
   chain();
@@ -702,20 +714,22 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   unsigned char *s_hi = sb + L::S_HI, *s_lo = sb + L::S_LO;
   Vec* vec = reinterpret_cast<Vec*>(sb + L::VEC);
   float* part = reinterpret_cast<float*>(sb + L::PART);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [4]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [SL]
   // MMAs: x y^T, x S, P z, the state's sum; decay factors are there [2 buffers]
-  uint64_t *bar_p = full + 4, *bar_s = full + 5, *bar_o = full + 6, *bar_d = full + 7, *ev_v = full + 8;
+  uint64_t *bar_p = full + SL, *bar_s = bar_p + 1, *bar_o = bar_p + 2, *bar_d = bar_p + 3, *ev_v = bar_p + 4;
   // events of a team: P and x S ready; result read; y weighed; state ready; of both: decay
   // factors used [2]. A barrier's next phase but one always depends on all who wait for it,
   // so nobody can miss a phase.
-  uint64_t *ev_p = full + 10, *ev_o = full + 11, *ev_y = full + 12, *ev_s = full + 13, *ev_u = full + 14;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 16);
+  uint64_t *ev_p = ev_v + 2, *ev_o = ev_p + 1, *ev_y = ev_p + 2, *ev_s = ev_p + 3, *ev_u = ev_p + 4;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(ev_u + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+  // what the issuing thread has seen done: P z, the state's sum, x S, x y^T, y weighed
+  volatile int* seen = reinterpret_cast<volatile int*>(tslot + 2);
   const int nch = (u.len + TC - 1) / TC;
-  const uint32_t tm = set_up(t, P_CTL, full, 10, 2, 4, 2, tslot, abort);
+  const uint32_t tm = set_up(t, P_CTL, full, SL + 6, 2, 4, 2, tslot, abort);
   const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
-  auto tile = [&](int n) { return sb + (n & 3) * L::SLOT; };  // tile n: x, y or z of chunk n / 3
-  auto wait_tile = [&](int n) { return mbar_wait(full + (n & 3), (n >> 2) & 1, abort); };
+  auto tile = [&](int n) { return sb + n % SL * L::SLOT; };  // tile n: x, y or z of chunk n / 3
+  auto wait_tile = [&](int n) { return mbar_wait(full + n % SL, n / SL & 1, abort); };
   // After a wait that ran out every role goes through its chunks without waiting.
   if (t.w < 8) {  // ---- P and the result
     more_registers<P_NTHR>();
@@ -730,7 +744,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       // first one's products are, waits until those have been read. The factors are loaded
       // together: under the MMAs a load of shared memory takes hundreds of cycles.
       const float r = v.row[t.lane];
-      const bool mild = v.mild;
+      const bool mild = v.mild[t.q4];
 #pragma unroll 1
       for (int j = 0; j < 2; ++j) {
         const int blk = 2 * t.cg + j;
@@ -823,10 +837,12 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       }
       mbar_wait(bar_o, ph, abort);
       tc_fence_after();
-      store_rows<N>(tl + O0 + N * t.cg, a.scale, sb + L::OUT + t.w * STAGE,
-                    out + ((size_t)(u.row + c * TC + 32 * t.q4) * a.H + h) * DZ + N * t.cg,
-                    (size_t)a.H * DZ, len - 32 * t.q4, [&] { warp_done<false>(ev_o); });
+      const int tok = (a.m.cu ? u.row : u.at * a.m.unit) + c * TC + 32 * t.q4;
+      store_rows<N>(tl + O0 + N * t.cg, a.scale, sb + L::OUT + t.w * STAGE, &mo, N * t.cg, h, tok,
+                    a.m.cu ? 0 : u.seq, out + ((size_t)row * a.H + h) * DZ + N * t.cg,
+                    len < TC && a.m.cu, len - 32 * t.q4, [&] { warp_done<false>(ev_o); });
     }
+    if (t.l == 0) bulk_wait_all();
   } else if (t.w < 16) {  // ---- the state
     more_registers<P_NTHR>();
     const size_t sh = ((size_t)u.seq * a.H + h) * DY * DZ, uh = ((size_t)unit * a.H + h) * DY * DZ;
@@ -861,12 +877,12 @@ __global__ void __launch_bounds__(P_NTHR, 1)
     if (u.at == u.n - 1 && S_out) store_state<DY, DZ, DQ, N>(S_out + sh, t.lane, N * t.cg, s);
   } else {
     fewer_registers<P_NTHR>();
-    if (t.w == P_CTL && t.l == 0) {
+    if (t.w == P_LOAD && t.l == 0) {  // ---- copies
       auto load = [&](int n) {
         const int c = n / 3, kind = n - 3 * c;
         if (c >= nch || *abort) return;
         const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
-        uint64_t* bar = full + (n & 3);
+        uint64_t* bar = full + n % SL;
         if (kind == 0)
           load_tile<DY>(tile(n), &mx, h, tok, seq, bar);
         else if (kind == 1)
@@ -874,37 +890,41 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         else
           load_tile<DZ>(tile(n), &mz, h, tok, seq, bar);
       };
-      auto fetch = [&](int c) {
-        if (c >= nch) return;
-        const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
-        fetch_tile<DY>(&mx, h, tok, seq);
-        fetch_tile<DY>(&my, h, tok, seq);
-        fetch_tile<DZ>(&mz, h, tok, seq);
-      };
-      for (int n = 0; n < 4; ++n) load(n);
-      for (int c = 1; c < AHEAD; ++c) fetch(c);
+      for (int n = 0; n < SL; ++n) load(n);
+      const long long t0 = clock64();
+      for (int n = SL; n < 3 * nch; ++n) {  // tile n - SL, whose slot it takes, is done with
+        const int c = (n - SL) / 3, kind = n - SL - 3 * c;
+        while (!*abort && !(kind == 0   ? seen[2] > c && seen[3] > c
+                            : kind == 1 ? seen[3] > c && seen[4] > c
+                                        : seen[0] > c && seen[1] > c))
+          if (clock64() - t0 > 64 * WAIT_LIMIT) *abort = 1;  // the issuing thread gives up before
+        load(n);
+      }
+    } else if (t.w == P_CTL && t.l == 0) {  // ---- MMAs
       // Each kind of work goes out as soon as what it needs is there, the products that a team
       // waits for first. Issued so far: P z, the state's sum, x S, x y^T (chunks), tiles; seen
       // done of each, and of the teams' events. Nothing is issued before its forerunner has
       // been seen done, and nothing that lets an event happen again before that event has been
       // seen: so no barrier is ever two phases ahead of what is asked about it.
-      int cz = 0, cd = 0, cs = 0, cp = 0, n = 4;
+      int cz = 0, cd = 0, cs = 0, cp = 0;
       int bz = 0, bd = 0, bs = 0, bp = 0, wp = 0, wy = 0, ws = 0, wo = 0;
-      const int last = 3 * nch;
-      auto see = [&](uint64_t* bar, int& i, int most) {
-        if (i < most && mbar_test(bar, i & 1)) ++i;
+      auto see = [&](uint64_t* bar, int& i, int most, int tell) {
+        if (i < most && mbar_test(bar, i & 1)) {
+          ++i;
+          if (tell >= 0) seen[tell] = i;
+        }
       };
-      auto have = [&](int n) { return mbar_test(full + (n & 3), (n >> 2) & 1); };
+      auto have = [&](int n) { return mbar_test(full + n % SL, n / SL & 1); };
       long long t0 = clock64();
-      while ((cz < nch || cd < nch || n < last) && !*abort) {
-        see(bar_o, bz, cz);
-        see(bar_d, bd, cd);
-        see(bar_s, bs, cs);
-        see(bar_p, bp, cp);
-        see(ev_p, wp, nch);
-        see(ev_y, wy, nch);
-        see(ev_s, ws, nch);
-        see(ev_o, wo, nch);
+      while ((bz < nch || bd < nch) && !*abort) {
+        see(bar_o, bz, cz, 0);
+        see(bar_d, bd, cd, 1);
+        see(bar_s, bs, cs, 2);
+        see(bar_p, bp, cp, 3);
+        see(ev_y, wy, nch, 4);
+        see(ev_p, wp, nch, -1);
+        see(ev_s, ws, nch, -1);
+        see(ev_o, wo, nch, -1);
         bool idle = true;
         if (cz < cs && cz == bz && wp > cz && have(3 * cz + 2) &&
             (!a.m.cu || u.len - cz * TC >= TC || wy > cz)) {  // a tail's z has been zeroed
@@ -955,22 +975,14 @@ __global__ void __launch_bounds__(P_NTHR, 1)
                       umma_idesc(128, 128, 0, 0), kk > 0);
           umma_commit(bar_p);
           ++cp;
-          fetch(cp + AHEAD - 1);
           idle = false;
-        }
-        if (n < last) {  // tile n - 4, whose slot it takes, is done with
-          const int c = (n - 4) / 3, kind = n - 4 - 3 * c;
-          if (kind == 0 ? bs > c && bp > c : kind == 1 ? bp > c && wy > c : bz > c && bd > c) {
-            load(n++);
-            idle = false;
-          }
         }
         if (!idle)
           t0 = clock64();
         else if (clock64() - t0 > WAIT_LIMIT)
           *abort = 1;
       }
-    } else if (t.w >= P_DEC) {
+    } else if (t.w >= P_DEC && t.w < P_LOAD) {
       auto raw = [&](int c) {
         return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
       };
@@ -986,7 +998,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       }
     }
   }
-  tear_down(t, P_CTL, full, 4, tm, abort, a.status);
+  tear_down(t, P_CTL, full, SL, tm, abort, a.status);
 }
 
 // ------------------------------------------------------------------ dk, dv and dg
@@ -1005,7 +1017,7 @@ struct BackSm {
   static constexpr uint32_t SLOT = slot_bytes(DK, DV), STATE = DK * DV * 2, HALF_R = DK * 128;
   static constexpr uint32_t R_HI = 4 * SLOT, R_LO = R_HI + STATE, VEC = R_LO + STATE;
   static constexpr uint32_t ROWS = VEC + 2 * sizeof(Vec), COLS = ROWS + 4 * TC * 4,
-                            FAR = COLS + 2 * TC * 4, RED = FAR + 2 * TC * 4, OUT = RED + 64, BAR = OUT + 8 * STAGE;
+                            FAR = COLS + 2 * TC * 4, RED = FAR + 2 * TC * 4, OUT = (RED + 64 + 511) / 512 * 512, BAR = OUT + 8 * STAGE;
   static constexpr uint32_t BYTES = BAR + 128 + 1024;
 };
 // x[0..31] summed over the warp's lanes; lane j returns the sum of x[j].
@@ -1029,7 +1041,8 @@ __global__ void __launch_bounds__(NTHR, 1)
                   const float* S_end, float* dS_in, const float* far, bf* dk, bf* dv, bf* dg,
                   float* dgsum, const __grid_constant__ CUtensorMap mq,
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                  const __grid_constant__ CUtensorMap mo) {
+                  const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mdk,
+                  const __grid_constant__ CUtensorMap mdv) {
   using L = BackSm<DK, DV>;
   constexpr int NK = DK / 2, NV = DV / 2;
   // A1: k q^T, then P1; A2: v dO^T, then P2; G1: the weighed q, then dk; G2: R's sum, then dv
@@ -1140,7 +1153,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             const bool diag = blk == t.q4;
             const float gh = v.hi[t.lane], gl = v.lo[t.lane];
             const float tb = a.scale * (diag ? v.own[t.lane] : v.tab[blk - 1][t.lane]);
-            const bool direct = diag && !v.mild;
+            const bool direct = diag && !v.mild[blk];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 f2 = *reinterpret_cast<const float2*>(v.row + 32 * blk + e);
@@ -1249,16 +1262,19 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc_fence_after();
       {
         unsigned char* stage = sb + L::OUT + t.w * STAGE;
-        const size_t first = (size_t)(row0 + 32 * t.q4) * a.H + h;
-        store_rows<NK>(tl + G1 + NK * t.cg, 1.f, stage, dk + first * DK + NK * t.cg, (size_t)a.H * DK,
-                       len - 32 * t.q4, [] {});
-        store_rows<NV>(tl + G2 + NV * t.cg, 1.f, stage, dv + first * DV + NV * t.cg, (size_t)a.H * DV,
-                       len - 32 * t.q4, [] {});
+        const size_t mine = (size_t)(row0 + t.lane) * a.H + h;
+        const int tok = (a.m.cu ? u.row : u.at * a.m.unit) + c * TC + 32 * t.q4, seq = a.m.cu ? 0 : u.seq;
+        const bool direct = len < TC && a.m.cu;
+        store_rows<NK>(tl + G1 + NK * t.cg, 1.f, stage, &mdk, NK * t.cg, h, tok, seq,
+                       dk + mine * DK + NK * t.cg, direct, len - 32 * t.q4, [] {});
+        store_rows<NV>(tl + G2 + NV * t.cg, 1.f, stage, &mdv, NV * t.cg, h, tok, seq,
+                       dv + mine * DV + NV * t.cg, direct, len - 32 * t.q4, [] {});
       }
       fence_proxy_async_smem();
       tc_fence_before();
       off = meet<true>(abort) || off;
     }
+    if (t.l == 0) bulk_wait_all();
     if (u.at == 0 && dS_in) store_state<DK, DV, false, NV>(dS_in + sh, t.lane, NV * t.cg, r);
     if (forms && dgsum) {
       sum = lane_sum<32>(sum);
@@ -1281,24 +1297,13 @@ __global__ void __launch_bounds__(NTHR, 1)
         else
           load_tile<DV>(to, &mo, h, tok, seq, full + 3);
       };
-      auto fetch = [&](int i) {
-        if (i >= nch) return;
-        const int c = nch - 1 - i;
-        const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
-        fetch_tile<DK>(&mq, h, tok, seq);
-        fetch_tile<DV>(&mo, h, tok, seq);
-        fetch_tile<DK>(&mk, h, tok, seq);
-        fetch_tile<DV>(&mv, h, tok, seq);
-      };
       if (t.l == 0) {
         for (int k = 3; k >= 0; --k) load(k, 0);
-        for (int i = 1; i < AHEAD; ++i) fetch(i);
       }
       __syncwarp();
       bool off = meet<true>(abort);
       for (int i = 0; i < nch && !off; ++i) {
         const int ph = i & 1;
-        if (t.l == 0) fetch(i + AHEAD);
         const uint32_t sv = smem_u32(slot(0, i)), sk = smem_u32(slot(1, i)),
                        sq = smem_u32(slot(2, i)), so = smem_u32(slot(3, i));
         off = meet<false>(abort);  // the weighed q is there (and a tail's rows are zeros)
@@ -1375,11 +1380,12 @@ __global__ void __launch_bounds__(NTHR, 1)
       };
       const bool wide = a.decay != nullptr;
       Raw ahead = {};
-      if (nch) fill_vec<true>(t.w - DEC, raw(0), wide, a.scale, vec[0]);
+      const bool fills = t.w < DEC + DEC_WARPS;
+      if (fills && nch) fill_vec<true>(t.w - DEC, raw(0), wide, a.scale, vec[0]);
       if (nch > 1) ahead = raw(1);
       bool off = meet<true>(abort);
       for (int i = 0; i < nch && !off; ++i) {
-        if (i + 1 < nch) fill_vec<true>(t.w - DEC, ahead, wide, a.scale, vec[(i + 1) & 1]);
+        if (fills && i + 1 < nch) fill_vec<true>(t.w - DEC, ahead, wide, a.scale, vec[(i + 1) & 1]);
         if (i + 2 < nch) ahead = raw(i + 2);
         off = meet<true>(abort);
       }
@@ -1459,7 +1465,13 @@ TcPlan tc_plan(const gdn_lin_shape& s, const int* cu, bool packed, bool back, un
 cudaError_t tile_map(CUtensorMap* map, const void* base, const gdn_lin_shape& s, int d, long long ld) {
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)s.H, (cuuint64_t)s.T, (cuuint64_t)s.B};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * s.T};
-  return make_tile_map(map, base, dims, strides, TC);
+  return make_tile_map(map, base, dims, strides, 64, TC);
+}
+// A result [B][T][H][d], contiguous, as boxes of 32 columns of 32 tokens.
+cudaError_t out_map(CUtensorMap* map, const void* base, const gdn_lin_shape& s, int d) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)s.H, (cuuint64_t)s.T, (cuuint64_t)s.B};
+  const cuuint64_t ld = (cuuint64_t)s.H * d * 2, strides[3] = {(cuuint64_t)d * 2, ld, ld * s.T};
+  return make_tile_map(map, base, dims, strides, 32, 32);
 }
 
 // Shared memory of a kernel, and whether its launch holds the registers that its warpgroups
@@ -1479,12 +1491,18 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   const gdn_lin_shape& s = c.s;
   const TcPlan p = tc_plan(s, c.cu, c.cu != nullptr, back, c.ws);
   const Args a = {p.m, s.H, s.scale, (const bf*)c.g, c.decay, s.ldg, p.status};
-  CUtensorMap mq, mk, mv, mo;
+  CUtensorMap mq, mk, mv, mo, mdq, mdk, mdv;
   cudaError_t e;
   if ((e = tile_map(&mq, c.q, s, DK, s.ldq)) || (e = tile_map(&mk, c.k, s, DK, s.ldk)) ||
       (e = tile_map(&mv, c.v, s, DV, s.ldv)))
     return e;
-  if (back && (e = tile_map(&mo, c.dout, s, DV, (long long)s.H * DV))) return e;
+  if (back) {
+    if ((e = tile_map(&mo, c.dout, s, DV, (long long)s.H * DV)) || (e = out_map(&mdq, c.dq, s, DK)) ||
+        (e = out_map(&mdk, c.dk, s, DK)) || (e = out_map(&mdv, c.dv, s, DV)))
+      return e;
+  } else if ((e = out_map(&mo, c.o, s, DV))) {
+    return e;
+  }
   if (c.cu && (e = lin_plan(p.m, p.first, p.owner, p.status, c.st))) return e;
   bool clear = !c.cu;  // the first kernel of an unpacked call resets the status word
   const dim3 grid(p.m.cap * s.H);
@@ -1509,19 +1527,21 @@ cudaError_t run_tc(const LinCall& c, bool back) {
     e = lin_scan(p.m, s, p.whole[0], p.D, c.S_in, p.E, p.whole[1], c.dS_out, back, p.status, c.st);
     if (e) return e;
   }
-  using PassKV = PassSm<DK, DV>;
-  using PassVK = PassSm<DV, DK>;
+  using PassKV = PassSm<DK, DV, false>;
+  using PassVK = PassSm<DV, DK, true>;
   using Back = BackSm<DK, DV>;
   prof_mark(c.st, back ? "lin_tc_dq" : "lin_tc_fwd");
   if (!back)
     return GO((k_lin_tc_pass<DK, DV, false>), PassKV, Regs<P_NTHR>::LAUNCH, c.S_in, p.D, c.S_out, (bf*)c.o,
-              (const bf*)nullptr, 0ll, (float*)nullptr, clear, mq, mk, mv);
+              (const bf*)nullptr, 0ll, (float*)nullptr, clear, mq, mk, mv, mo);
   e = GO((k_lin_tc_pass<DV, DK, true>), PassVK, Regs<P_NTHR>::LAUNCH, c.S_in, p.D,
-         c.dS_out ? p.S_end : (float*)nullptr, (bf*)c.dq, (const bf*)c.q, s.ldq, p.far, clear, mo, mv, mk);
+         c.dS_out ? p.S_end : (float*)nullptr, (bf*)c.dq, (const bf*)c.q, s.ldq, p.far, clear, mo, mv, mk,
+         mdq);
   if (e) return e;
   prof_mark(c.st, "lin_tc_back");
   e = GO((k_lin_tc_back<DK, DV>), Back, Regs<NTHR>::LAUNCH, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
-         (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo);
+         (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo, mdk,
+         mdv);
 #undef GO
   if (e) return e;
   if (c.ddecay) e = col_sum(p.dgsum, p.m.cap, s.H, s.H, c.ddecay, nullptr, nullptr, c.st);

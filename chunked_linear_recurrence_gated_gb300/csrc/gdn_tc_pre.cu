@@ -469,17 +469,18 @@ cudaError_t make_tok_map(CUtensorMap* map, const void* base, int d, const SeqMap
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)m.H, T, Bn};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)m.H * d * 2,
                                  (cuuint64_t)m.H * d * 2 * T};
-  return make_tile_map(map, base, dims, strides, BT);
+  return make_tile_map(map, base, dims, strides, 64, BT);
 }
 
 cudaError_t make_tile_map(CUtensorMap* map, const void* base, const cuuint64_t* dims,
-                          const cuuint64_t* strides, int tokens) {
+                          const cuuint64_t* strides, int cols, int tokens) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)tokens, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)cols, 1, (cuuint32_t)tokens, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
-                        strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
