@@ -360,11 +360,10 @@ __device__ __forceinline__ __nv_bfloat162 bf2(uint32_t x) {
   return *reinterpret_cast<__nv_bfloat162*>(&x);
 }
 // The weighted transpose of a warp's 32 columns of a tile (64 tokens) into tensor memory,
-// an operand with the tokens as reduced dimension: first parts at `to`, rests 64 columns
-// on. With y a value and w = wh + wl its weight, hi = y wh rounded, and y wh - hi + y wl is
+// an operand with the tokens as reduced dimension: first parts at `to`, rests at `rest`. With y a value and w = wh + wl its weight, hi = y wh rounded, and y wh - hi + y wl is
 // the rest: fused multiply-adds of pairs, the first difference exact.
 __device__ __forceinline__ void weigh(const unsigned char* tile, const Who& t, const Weights& w,
-                                      int len, uint32_t to) {
+                                      int len, uint32_t to, uint32_t rest) {
   const uint32_t base = smem_u32(tile) + (t.q4 >> 1) * HALF_TILE;
   const int piece = (t.q4 & 1) * 4 + (t.l >> 3), r7 = t.l & 7;
   const uint32_t at = base + (64 * t.cg + r7) * 128 + ((piece ^ r7) << 4);
@@ -393,7 +392,7 @@ __device__ __forceinline__ void weigh(const unsigned char* tile, const Who& t, c
 #pragma unroll
     for (int j = 0; j < 2; ++j) {  // 16 lanes
       tmem_st_frag(to + (16u * j << 16) + 32 * t.cg + 16 * g, hi[j]);
-      tmem_st_frag(to + (16u * j << 16) + 64 + 32 * t.cg + 16 * g, lo[j]);
+      tmem_st_frag(rest + (16u * j << 16) + 32 * t.cg + 16 * g, lo[j]);
     }
   }
 }
@@ -439,17 +438,9 @@ __device__ __forceinline__ void add_state(uint32_t taddr, float by, float* s) {
     for (int j = 0; j < 32; ++j) s[i + j] = fmaf(by, s[i + j], d[j]);
   }
 }
-// An accumulator's N columns times `by` as bf16, through 2 KB of shared memory of the warp's
-// own (32 rows of 32 columns, 64-byte swizzle) that the copy engine stores: it writes while
-// the warp goes on, which would wait for its own stores (an SM sends about 25 bytes a cycle).
-// `taken` is called once the accumulator has been read. direct: a tile whose last rows are
-// another sequence's, stored row by row.
-template <int N, class F>
-__device__ __forceinline__ void store_rows(uint32_t taddr, float by, unsigned char* stage,
-                                           const CUtensorMap* map, int col, int h, int tok, int seq,
-                                           bf* out, bool direct, int rows, F taken) {
-  const int l = threadIdx.x & 31;
-  uint32_t p[N / 2];
+// An accumulator's N columns times `by` as packed bf16.
+template <int N>
+__device__ __forceinline__ void take_row(uint32_t taddr, float by, uint32_t* p) {
 #pragma unroll
   for (int i = 0; i < N; i += 32) {
     float v[32];
@@ -457,7 +448,16 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, float by, unsigned ch
 #pragma unroll
     for (int j = 0; j < 16; ++j) p[i / 2 + j] = pack2bf(by * v[2 * j], by * v[2 * j + 1]);
   }
-  taken();
+}
+// These rows into memory through 2 KB of shared memory of the warp's own (32 rows of 32
+// columns, 64-byte swizzle) that the copy engine stores: it writes while the warp goes on,
+// which would wait for its own stores (an SM sends about 25 bytes a cycle). direct: a tile
+// whose last rows are another sequence's, stored row by row.
+template <int N>
+__device__ __forceinline__ void leave_rows(const uint32_t* p, unsigned char* stage, const CUtensorMap* map,
+                                           int col, int h, int tok, int seq, bf* out, bool direct,
+                                           int rows) {
+  const int l = threadIdx.x & 31;
   if (direct) {
     if (l < rows)
 #pragma unroll
@@ -508,7 +508,7 @@ __device__ __forceinline__ uint32_t set_up(const Who& t, int ctl, uint64_t* bars
     *abort = 0;
     fence_mbar_init();
   }
-  if (t.tid < 8) (reinterpret_cast<volatile int*>(tslot + 2))[t.tid] = 0;  // counters behind the flag
+  if (t.tid < 8) reinterpret_cast<volatile int*>(tslot + 2)[t.tid] = 0;  // counters behind the flag
   if (t.w == ctl) tmem_alloc(tslot, 512);
   tc_fence_before();
   __syncthreads();
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       const int len = min(TC, u.len - chunk(i) * TC);
       mbar_wait(full + i % ST, (i / ST) & 1, abort);
       if (t.lane < DY) {
-        weigh(tile(i), t, vec[i & 3], len, tl + Y0 + 128 * (i & 1));
+        weigh(tile(i), t, vec[i & 3], len, tl + Y0 + 128 * (i & 1), tl + Y0 + 128 * (i & 1) + 64);
         tmem_st_wait();
       }
       if (len < TC && a.m.cu) {
@@ -838,9 +838,11 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       mbar_wait(bar_o, ph, abort);
       tc_fence_after();
       const int tok = (a.m.cu ? u.row : u.at * a.m.unit) + c * TC + 32 * t.q4;
-      store_rows<N>(tl + O0 + N * t.cg, a.scale, sb + L::OUT + t.w * STAGE, &mo, N * t.cg, h, tok,
-                    a.m.cu ? 0 : u.seq, out + ((size_t)row * a.H + h) * DZ + N * t.cg,
-                    len < TC && a.m.cu, len - 32 * t.q4, [&] { warp_done<false>(ev_o); });
+      uint32_t res[N / 2];
+      take_row<N>(tl + O0 + N * t.cg, a.scale, res);
+      warp_done<false>(ev_o);
+      leave_rows<N>(res, sb + L::OUT + t.w * STAGE, &mo, N * t.cg, h, tok, a.m.cu ? 0 : u.seq,
+                    out + ((size_t)row * a.H + h) * DZ + N * t.cg, len < TC && a.m.cu, len - 32 * t.q4);
     }
     if (t.l == 0) bulk_wait_all();
   } else if (t.w < 16) {  // ---- the state
@@ -856,7 +858,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       mbar_wait(ev_v + ph, (c >> 1) & 1, abort);
       wait_tile(n0 + 1);
       if (t.lane < DY) {
-        weigh(tile(n0 + 1), t, v.w, len, tl + Y0);
+        weigh(tile(n0 + 1), t, v.w, len, tl + Y0, tl + Y0 + 64);
         tmem_st_wait();
       }
       if (len < TC && a.m.cu) {
@@ -1004,27 +1006,29 @@ __global__ void __launch_bounds__(P_NTHR, 1)
 // ------------------------------------------------------------------ dk, dv and dg
 // From a unit's last chunk to its first, with R in registers (row: key, as in memory). The
 // rows of a chunk's accumulators are its tokens s, the columns the tokens t they act on:
-//   k q^T, v dO^T (masked by L_ts, t >= s), v R^T and k R (scaled by e^{gamma_C - gamma_s});
-//   dk = P2 q onto the one, dv = P1 dO onto the other.
-// R's sum scale (e^gamma q)^T dO needs only q and dO and comes first, so that R's next tiles
-// are written under the last products. dg runs along: with rows and cols the sums of A
-// (gdn_lin.cu) over s and over t,
+//   k q^T, v dO^T (masked by L_ts, t >= s, as P1 and P2), v R^T and k R (scaled by
+//   e^{gamma_C - gamma_s}); dk = P2 q onto the one, dv = P1 dO onto the other;
+//   R <- e^{gamma_C} R + (weighed q)^T dO.
+// Two teams as above: one takes the masked products and the results, the other weighs q,
+// adds up R, scales the products with R and writes R's next tiles. dg runs along in the warp
+// that issues the copies: with rows and cols the sums of A (gdn_lin.cu) over s and over t,
 //   dg_u = X + sum_{t >= u} (rows_t + a_t - cols_t - b_t),  X' = X + sum_t (a_t - b_t),
 // X = <S, R> behind the chunk, taken from the states themselves at the unit's end.
 template <int DK, int DV>
 struct BackSm {
-  static constexpr int THREADS = NTHR;
+  static constexpr int THREADS = P_NTHR;
   static constexpr uint32_t SLOT = slot_bytes(DK, DV), STATE = DK * DV * 2, HALF_R = DK * 128;
   static constexpr uint32_t R_HI = 4 * SLOT, R_LO = R_HI + STATE, VEC = R_LO + STATE;
   static constexpr uint32_t ROWS = VEC + 2 * sizeof(Vec), COLS = ROWS + 4 * TC * 4,
-                            FAR = COLS + 2 * TC * 4, RED = FAR + 2 * TC * 4, OUT = (RED + 64 + 511) / 512 * 512, BAR = OUT + 8 * STAGE;
-  static constexpr uint32_t BYTES = BAR + 128 + 1024;
+                            FAR = COLS + 2 * TC * 4, RED = FAR + 2 * TC * 4;
+  static constexpr uint32_t OUT = (RED + 64 + 511) / 512 * 512, BAR = OUT + 8 * STAGE;
+  static constexpr uint32_t BYTES = BAR + 256 + 1024;
 };
-// x[0..31] summed over the warp's lanes; lane j returns the sum of x[j].
+// x[0..15] summed over the warp's lanes; lanes j and j + 16 return the sum of x[j].
 __device__ __forceinline__ float lane_columns(float* x) {
   const int l = threadIdx.x & 31;
 #pragma unroll
-  for (int o = 16, n = 16; o >= 1; o >>= 1, n >>= 1) {
+  for (int o = 8, n = 8; o >= 1; o >>= 1, n >>= 1) {
     const bool up = (l & o) != 0;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
@@ -1032,11 +1036,11 @@ __device__ __forceinline__ float lane_columns(float* x) {
       x[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
     }
   }
-  return x[0];
+  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(NTHR, 1)
+__global__ void __launch_bounds__(P_NTHR, 1)
     k_lin_tc_back(Args a, const float* dS_out, const float* R_unit, const float* S_unit,
                   const float* S_end, float* dS_in, const float* far, bf* dk, bf* dv, bf* dg,
                   float* dgsum, const __grid_constant__ CUtensorMap mq,
@@ -1045,7 +1049,8 @@ __global__ void __launch_bounds__(NTHR, 1)
                   const __grid_constant__ CUtensorMap mdv) {
   using L = BackSm<DK, DV>;
   constexpr int NK = DK / 2, NV = DV / 2;
-  // A1: k q^T, then P1; A2: v dO^T, then P2; G1: the weighed q, then dk; G2: R's sum, then dv
+  // A1: k q^T, then P1; A2: v dO^T, then P2; both upper halves: the weighed q of the next
+  // chunk; G1: products with R for dk; G2: R's sum, then products with R for dv
   constexpr uint32_t A1 = 0, A2 = 128, G1 = 256, G2 = 384;
   chain();
   const int unit = blockIdx.x / a.H, h = blockIdx.x - unit * a.H;
@@ -1065,25 +1070,113 @@ __global__ void __launch_bounds__(NTHR, 1)
   float* farb = reinterpret_cast<float*>(sb + L::FAR);   // [column group][s]
   float* red = reinterpret_cast<float*>(sb + L::RED);
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [4] v, k, q, dO
+  // MMAs: R's sum, k q^T and v dO^T, products with R, results; decay factors are there [2]
+  uint64_t *bar_e = full + 4, *bar_a = full + 5, *bar_f = full + 6, *bar_c = full + 7, *ev_v = full + 8;
+  // events of a team: q weighed; R's sum added; products with R scaled; R's tiles written; P1
+  // and P2 written; results read; of both: decay factors used [2]
+  uint64_t *ev_q = full + 10, *ev_g = full + 11, *ev_x = full + 12, *ev_r = full + 13, *ev_p = full + 14,
+           *ev_o = full + 15, *ev_u = full + 16;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 18);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+  // what the issuing thread has seen done: A, products with R, results; events ev_x, ev_p, ev_r
+  volatile int* seen = reinterpret_cast<volatile int*>(tslot + 2);
   // q and dO of a chunk take the slots of v and k of the one before, which are done with
   // early, v and k those of q and dO
   auto slot = [&](int kind, int i) { return sb + (kind ^ (i & 1 ? 2 : 0)) * L::SLOT; };
-  // MMAs: R's sum, k q^T and v dO^T, products with R, results
-  uint64_t *bar_e = full + 4, *bar_a = full + 5, *bar_f = full + 6, *bar_c = full + 7;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 8);
-  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   const int nch = (u.len + TC - 1) / TC;
-  const uint32_t tm = set_up(t, CTL, full, 8, 0, 0, 0, tslot, abort);
-  if (t.w < CTL) {
-    more_registers<NTHR>();
-    const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
-    const size_t sh = ((size_t)u.seq * a.H + h) * DK * DV;
-    const bool last = u.at == u.n - 1;
+  const uint32_t tm = set_up(t, P_CTL, full, 10, 2, 6, 2, tslot, abort);
+  const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
+  const size_t sh = ((size_t)u.seq * a.H + h) * DK * DV;
+  const bool last = u.at == u.n - 1;
+  if (t.w < 8) {  // ---- masked products and results
+    more_registers<P_NTHR>();
+    for (int i = 0; i < nch; ++i) {
+      const int c = nch - 1 - i, len = min(TC, u.len - c * TC), ph = i & 1;
+      const Vec& v = vec[ph];
+      mbar_wait(ev_v + ph, (i >> 1) & 1, abort);
+      const float gh = v.hi[t.lane], gl = v.lo[t.lane];
+      mbar_wait(bar_a, ph, abort);
+      tc_fence_after();
+      // this thread's row s, columns t in [64 cg, 64 cg + 64), 16 at a time; in place as above
+      float cs = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j) {
+        const int blk = 2 * t.cg + j;
+        uint32_t p1[16], p2[16];
+        if (blk < t.q4) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) p1[e] = p2[e] = 0;
+          rows[t.q4 * TC + 32 * blk + t.l] = 0.f;
+        } else {
+          const bool diag = blk == t.q4;
+          const float tb = a.scale * (diag ? v.own[t.lane] : v.tab[blk - 1][t.lane]);
+          const bool direct = diag && !v.mild[blk];
+#pragma unroll
+          for (int g = 0; g < 32; g += 16) {
+            float x[16], y[16];
+            tmem_ld16(tl + A1 + 32 * blk + g, x);
+            tmem_ld16(tl + A2 + 32 * blk + g, y);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float2 f2 = *reinterpret_cast<const float2*>(v.row + 32 * blk + g + e);
+              float f[2] = {tb * f2.x, tb * f2.y};
+              if (direct) {
+                const float2 h2 = *reinterpret_cast<const float2*>(v.hi + 32 * blk + g + e);
+                const float2 l2 = *reinterpret_cast<const float2*>(v.lo + 32 * blk + g + e);
+                f[0] = a.scale * __expf((h2.x - gh) + (l2.x - gl));
+                f[1] = a.scale * __expf((h2.y - gh) + (l2.y - gl));
+              }
+              float px[2], py[2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const bool in = !diag || g + e + z >= t.l;
+                px[z] = in ? x[e + z] * f[z] : 0.f;
+                py[z] = in ? y[e + z] * f[z] : 0.f;
+                const float pair = !diag || g + e + z > t.l ? x[e + z] * py[z] : 0.f;
+                x[e + z] = pair;
+                cs += pair;
+              }
+              p1[(g + e) / 2] = pack2bf(px[0], px[1]);
+              p2[(g + e) / 2] = pack2bf(py[0], py[1]);
+            }
+            const float sum = lane_columns(x);
+            if (t.l < 16) rows[t.q4 * TC + 32 * blk + g + t.l] = sum;
+          }
+        }
+        if (j != t.cg) {
+          tc_fence_before();
+          named_bar(2 + t.q4, 64);
+          tc_fence_after();
+        }
+        tmem_st16(tl + A1 + 32 * t.cg + 16 * j, p1);
+        tmem_st16(tl + A2 + 32 * t.cg + 16 * j, p2);
+      }
+      cols[t.cg * TC + t.lane] = cs;
+      tmem_st_wait();
+      warp_done<false>(ev_p);
+      if (t.l == 0) mbar_arrive(ev_u + ph);
+      mbar_wait(bar_c, ph, abort);
+      tc_fence_after();
+      uint32_t rk[NK / 2], rv[NV / 2];
+      take_row<NK>(tl + G1 + NK * t.cg, 1.f, rk);
+      take_row<NV>(tl + G2 + NV * t.cg, 1.f, rv);
+      warp_done<false>(ev_o);
+      unsigned char* stage = sb + L::OUT + t.w * STAGE;
+      const size_t mine = (size_t)(u.row + c * TC + t.lane) * a.H + h;
+      const int tok = (a.m.cu ? u.row : u.at * a.m.unit) + c * TC + 32 * t.q4, seq = a.m.cu ? 0 : u.seq;
+      const bool direct = len < TC && a.m.cu;
+      leave_rows<NK>(rk, stage, &mdk, NK * t.cg, h, tok, seq, dk + mine * DK + NK * t.cg, direct,
+                     len - 32 * t.q4);
+      leave_rows<NV>(rv, stage, &mdv, NV * t.cg, h, tok, seq, dv + mine * DV + NV * t.cg, direct,
+                     len - 32 * t.q4);
+    }
+    if (t.l == 0) bulk_wait_all();
+  } else if (t.w < 16) {  // ---- R and the products with it
+    more_registers<P_NTHR>();
     float r[NV];
     const float* from = last ? (dS_out ? dS_out + sh : nullptr) : R_unit + uh * DK * DV;
     load_state<DK, DV, false, NV>(from, t.lane, NV * t.cg, r);
     if (t.lane < DK) put_split<NV, true>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
-    fence_proxy_async_smem();
     {
       const float* S = !from ? nullptr : last ? S_end + sh : S_unit + (uh + a.H) * DK * DV;
       float x = 0.f;
@@ -1098,107 +1191,42 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
       }
       x = lane_sum<32>(x);
-      if (t.l == 0) red[t.w] = x;
+      if (t.l == 0) red[t.w - 8] = x;
     }
-    bool off = meet<true>(abort);
-    float X = 0.f, sum = 0.f;  // of the warp that forms dg: the one with the fewest pairs
-    const bool forms = t.w == 3;
-    if (forms)
-      for (int i = 0; i < NEPI / 32; ++i) X += red[i];
-    for (int i = 0; i < nch && !off; ++i) {
+    warp_done<true>(ev_r);
+    for (int i = 0; i < nch; ++i) {
       const int c = nch - 1 - i, len = min(TC, u.len - c * TC), ph = i & 1;
       const Vec& v = vec[ph];
-      const int row0 = u.row + c * TC;
-      float fa[4] = {};  // a of the tokens 4 l ..
-      if (forms) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (4 * t.l + j < len) fa[j] = far[(size_t)(row0 + 4 * t.l + j) * a.H + h];
-      }
+      mbar_wait(ev_v + ph, (i >> 1) & 1, abort);
       mbar_wait(full + 2, ph, abort);
       if (len < TC && a.m.cu) {
         mbar_wait(full + 3, ph, abort);
-        zero_rows<DK>(slot(2, i), len, t.tid);
-        zero_rows<DV>(slot(3, i), len, t.tid);
-        fence_proxy_async_smem();
-        named_bar(6, NEPI);
+        zero_rows<DK>(slot(2, i), len, t.tid - 256);
+        zero_rows<DV>(slot(3, i), len, t.tid - 256);
+        named_bar(6, 256);
       }
+      if (i) mbar_wait(ev_p, ph ^ 1, abort);  // the products have been read
+      tc_fence_after();
       if (t.lane < DK) {
-        weigh(slot(2, i), t, v.w, len, tl + G1);
+        weigh(slot(2, i), t, v.w, len, tl + A1 + 64, tl + A2 + 64);
         tmem_st_wait();
       }
-      tc_fence_before();
-      off = meet<false>(abort);
+      warp_done<true>(ev_q);
       mbar_wait(bar_e, ph, abort);
       tc_fence_after();
       if (t.lane < DK) add_state<NV>(tl + G2 + NV * t.cg, v.w.whole, r);
-      tc_fence_before();
-      off = meet<false>(abort) || off;  // G1 and G2 are free: the products with R follow
-      mbar_wait(bar_a, ph, abort);
-      tc_fence_after();
-      {  // this thread's row s, columns t in [64 cg, 64 cg + 64); P1 and P2 in place as above
-        float cs = 0.f;
-#pragma unroll 1
-        for (int j = 0; j < 2; ++j) {
-          const int blk = 2 * t.cg + j;
-          uint32_t p1[16], p2[16];
-          if (blk < t.q4) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) p1[e] = p2[e] = 0;
-            rows[t.q4 * TC + 32 * blk + t.l] = 0.f;
-          } else {
-            float x[32], y[32];
-            tmem_ld32(tl + A1 + 32 * blk, x);
-            tmem_ld32(tl + A2 + 32 * blk, y);
-            const bool diag = blk == t.q4;
-            const float gh = v.hi[t.lane], gl = v.lo[t.lane];
-            const float tb = a.scale * (diag ? v.own[t.lane] : v.tab[blk - 1][t.lane]);
-            const bool direct = diag && !v.mild[blk];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 f2 = *reinterpret_cast<const float2*>(v.row + 32 * blk + e);
-              float f[2] = {tb * f2.x, tb * f2.y};
-              if (direct) {
-                const float2 h2 = *reinterpret_cast<const float2*>(v.hi + 32 * blk + e);
-                const float2 l2 = *reinterpret_cast<const float2*>(v.lo + 32 * blk + e);
-                f[0] = a.scale * __expf((h2.x - gh) + (l2.x - gl));
-                f[1] = a.scale * __expf((h2.y - gh) + (l2.y - gl));
-              }
-              float px[2], py[2];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const bool in = !diag || e + z >= t.l;
-                px[z] = in ? x[e + z] * f[z] : 0.f;
-                py[z] = in ? y[e + z] * f[z] : 0.f;
-                const float pair = !diag || e + z > t.l ? x[e + z] * py[z] : 0.f;
-                x[e + z] = pair;
-                cs += pair;
-              }
-              p1[e / 2] = pack2bf(px[0], px[1]);
-              p2[e / 2] = pack2bf(py[0], py[1]);
-            }
-            rows[t.q4 * TC + 32 * blk + t.l] = lane_columns(x);
-          }
-          if (j != t.cg) {
-            tc_fence_before();
-            named_bar(2 + t.q4, 64);
-            tc_fence_after();
-          }
-          tmem_st16(tl + A1 + 32 * t.cg + 16 * j, p1);
-          tmem_st16(tl + A2 + 32 * t.cg + 16 * j, p2);
-        }
-        cols[t.cg * TC + t.lane] = cs;
-      }
+      warp_done<false>(ev_g);
+      const float down = v.far[t.lane];
       mbar_wait(bar_f, ph, abort);
       tc_fence_after();
-      const float down = v.far[t.lane];
       float b = 0.f;
 #pragma unroll 1
-      for (int e = 0; e < NK; e += 32) {
-        float x[32];
-        tmem_ld32(tl + G1 + NK * t.cg + e, x);
+      for (int e = 0; e < NK; e += 16) {
+        float x[16];
+        uint32_t y[16];
+        tmem_ld16(tl + G1 + NK * t.cg + e, x);
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
+        for (int j = 0; j < 16; j += 8) {
           const uint4 k4 = *reinterpret_cast<const uint4*>(
               at8(slot(1, i), HALF_TILE, t.lane, NK * t.cg + e + j));
           const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -1210,22 +1238,68 @@ __global__ void __launch_bounds__(NTHR, 1)
             b = fmaf(__uint_as_float(kk[z] & 0xffff0000u), x[j + 2 * z + 1], b);
           }
         }
-        tmem_st32(tl + G1 + NK * t.cg + e, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(x[j]);
+        tmem_st16(tl + G1 + NK * t.cg + e, y);
       }
       farb[t.cg * TC + t.lane] = b;
 #pragma unroll 1
-      for (int e = 0; e < NV; e += 32) {
-        float x[32];
-        tmem_ld32(tl + G2 + NV * t.cg + e, x);
+      for (int e = 0; e < NV; e += 16) {
+        float x[16];
+        uint32_t y[16];
+        tmem_ld16(tl + G2 + NV * t.cg + e, x);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] *= down;
-        tmem_st32(tl + G2 + NV * t.cg + e, x);
+        for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(x[j] * down);
+        tmem_st16(tl + G2 + NV * t.cg + e, y);
       }
       tmem_st_wait();
-      tc_fence_before();
-      off = meet<false>(abort) || off;
+      warp_done<false>(ev_x);
+      if (t.l == 0) mbar_arrive(ev_u + ph);
       if (t.lane < DK) put_split<NV, true>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
-      if (forms) {  // dg: 4 tokens for each lane
+      warp_done<true>(ev_r);
+    }
+    if (u.at == 0 && dS_in) store_state<DK, DV, false, NV>(dS_in + sh, t.lane, NV * t.cg, r);
+  } else {
+    fewer_registers<P_NTHR>();
+    if (t.w == P_LOAD) {  // ---- copies, and dg
+      auto load = [&](int kind, int i) {  // a tile of the i-th chunk from the end
+        if (i >= nch || *abort || t.l) return;
+        const int c = nch - 1 - i;
+        const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
+        if (kind == 0)
+          load_tile<DV>(slot(kind, i), &mv, h, tok, seq, full);
+        else if (kind == 1)
+          load_tile<DK>(slot(kind, i), &mk, h, tok, seq, full + 1);
+        else if (kind == 2)
+          load_tile<DK>(slot(kind, i), &mq, h, tok, seq, full + 2);
+        else
+          load_tile<DV>(slot(kind, i), &mo, h, tok, seq, full + 3);
+      };
+      const long long t0 = clock64();
+      auto until = [&](int which, int n) {  // the issuing thread has seen `which` n times
+        while (!*abort && seen[which] < n)
+          if (clock64() - t0 > 64 * WAIT_LIMIT) *abort = 1;  // it gives up long before
+        __threadfence_block();
+        __syncwarp();
+      };
+      for (int k = 3; k >= 0; --k) load(k, 0);
+      float X = 0.f, sum = 0.f;
+      if (nch) {
+        until(5, 1);
+        for (int i = 0; i < 8; ++i) X += red[i];
+      }
+      for (int i = 0; i < nch; ++i) {
+        const int c = nch - 1 - i, len = min(TC, u.len - c * TC), row0 = u.row + c * TC;
+        float fa[4] = {};  // a of the tokens 4 l ..
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * t.l + j < len) fa[j] = far[(size_t)(row0 + 4 * t.l + j) * a.H + h];
+        until(0, i + 1);
+        until(1, i + 1);
+        load(2, i + 1);  // where v was
+        until(3, i + 1);
+        load(3, i + 1);  // where k was
+        until(4, i + 1);
         float x[4], ab = 0.f, suf = 0.f;
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
@@ -1247,6 +1321,11 @@ __global__ void __launch_bounds__(NTHR, 1)
           if (t.l + o < 32) all += y;
         }
         const float behind = all - suf + X;
+        X += lane_sum<32>(ab);
+        // k before the sums are stored: the next chunk's sums are written behind its products
+        until(2, i + 1);
+        load(1, i + 1);
+        load(0, i + 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = 4 * t.l + j;
@@ -1256,84 +1335,83 @@ __global__ void __launch_bounds__(NTHR, 1)
           else
             sum += x[j] + behind;
         }
-        X += lane_sum<32>(ab);
+        __syncwarp();
       }
-      mbar_wait(bar_c, ph, abort);
-      tc_fence_after();
-      {
-        unsigned char* stage = sb + L::OUT + t.w * STAGE;
-        const size_t mine = (size_t)(row0 + t.lane) * a.H + h;
-        const int tok = (a.m.cu ? u.row : u.at * a.m.unit) + c * TC + 32 * t.q4, seq = a.m.cu ? 0 : u.seq;
-        const bool direct = len < TC && a.m.cu;
-        store_rows<NK>(tl + G1 + NK * t.cg, 1.f, stage, &mdk, NK * t.cg, h, tok, seq,
-                       dk + mine * DK + NK * t.cg, direct, len - 32 * t.q4, [] {});
-        store_rows<NV>(tl + G2 + NV * t.cg, 1.f, stage, &mdv, NV * t.cg, h, tok, seq,
-                       dv + mine * DV + NV * t.cg, direct, len - 32 * t.q4, [] {});
+      if (dgsum) {
+        sum = lane_sum<32>(sum);
+        if (t.l == 0) dgsum[uh] = sum;
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      off = meet<true>(abort) || off;
-    }
-    if (t.l == 0) bulk_wait_all();
-    if (u.at == 0 && dS_in) store_state<DK, DV, false, NV>(dS_in + sh, t.lane, NV * t.cg, r);
-    if (forms && dgsum) {
-      sum = lane_sum<32>(sum);
-      if (t.l == 0) dgsum[uh] = sum;
-    }
-  } else {
-    fewer_registers<NTHR>();
-    if (t.w == CTL) {
-      auto load = [&](int kind, int i) {  // a tile of the i-th chunk from the end
-        if (i >= nch) return;
-        const int c = nch - 1 - i;
-        const int tok = a.m.cu ? u.row + c * TC : u.at * a.m.unit + c * TC, seq = a.m.cu ? 0 : u.seq;
-        unsigned char* to = slot(kind, i);
-        if (kind == 0)
-          load_tile<DV>(to, &mv, h, tok, seq, full);
-        else if (kind == 1)
-          load_tile<DK>(to, &mk, h, tok, seq, full + 1);
-        else if (kind == 2)
-          load_tile<DK>(to, &mq, h, tok, seq, full + 2);
-        else
-          load_tile<DV>(to, &mo, h, tok, seq, full + 3);
+    } else if (t.w == P_CTL && t.l == 0) {  // ---- MMAs, as in the forward
+      int ce = 0, ca = 0, cf = 0, cc = 0, be = 0, ba = 0, bfr = 0, bc = 0;
+      int wq = 0, wg = 0, wx = 0, wr = 0, wp = 0, wo = 0;
+      auto see = [&](uint64_t* bar, int& i, int most, int tell) {
+        if (i < most && mbar_test(bar, i & 1)) {
+          ++i;
+          if (tell >= 0) seen[tell] = i;
+        }
       };
-      if (t.l == 0) {
-        for (int k = 3; k >= 0; --k) load(k, 0);
-      }
-      __syncwarp();
-      bool off = meet<true>(abort);
-      for (int i = 0; i < nch && !off; ++i) {
-        const int ph = i & 1;
-        const uint32_t sv = smem_u32(slot(0, i)), sk = smem_u32(slot(1, i)),
-                       sq = smem_u32(slot(2, i)), so = smem_u32(slot(3, i));
-        off = meet<false>(abort);  // the weighed q is there (and a tail's rows are zeros)
-        if (t.l == 0) {
+      auto have = [&](int kind, int i) { return mbar_test(full + kind, i & 1); };
+      long long t0 = clock64();
+      while (bc < nch && !*abort) {
+        see(bar_c, bc, cc, 2);
+        see(ev_x, wx, nch, 3);
+        see(ev_p, wp, nch, 4);
+        see(bar_f, bfr, cf, 1);
+        see(bar_e, be, ce, -1);
+        see(bar_a, ba, ca, 0);
+        see(ev_g, wg, nch, -1);
+        see(ev_q, wq, nch, -1);
+        see(ev_o, wo, nch, -1);
+        see(ev_r, wr, nch, 5);
+        bool idle = true;
+        if (cc < nch && cc == bc && wp > cc && wx > cc) {  // results
           tc_fence_after();
-          mbar_wait(full + 3, ph, abort);
+          const uint32_t sq = smem_u32(slot(2, cc)), so = smem_u32(slot(3, cc));
+#pragma unroll
+          for (int kk = 0; kk < TC / 16; ++kk)
+            umma_ts(tm + G1, tm + A2 + 8 * kk, mnmaj(sq, HALF_TILE, kk), umma_idesc(128, DK, 0, 1), true);
+#pragma unroll
+          for (int kk = 0; kk < TC / 16; ++kk)
+            umma_ts(tm + G2, tm + A1 + 8 * kk, mnmaj(so, HALF_TILE, kk), umma_idesc(128, DV, 0, 1), true);
+          umma_commit(bar_c);
+          ++cc;
+          idle = false;
+        }
+        // R's sum: q weighed, the results before read
+        if (ce < nch && ce == be && wq > ce && wo >= ce && have(3, ce)) {
+          tc_fence_after();
+          const uint32_t so = smem_u32(slot(3, ce));
 #pragma unroll 1
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int kk = 0; kk < TC / 16; ++kk)
-              umma_ts(tm + G2, tm + G1 + 64 * p + 8 * kk, mnmaj(so, HALF_TILE, kk),
+              umma_ts(tm + G2, tm + (p ? A2 : A1) + 64 + 8 * kk, mnmaj(so, HALF_TILE, kk),
                       umma_idesc(128, DV, 0, 1), p || kk);
           umma_commit(bar_e);
-          mbar_wait(full + 1, ph, abort);
-          mbar_wait(full + 2, ph, abort);
+          ++ce;
+          idle = false;
+        }
+        // products: the weighed q has been used
+        if (ca < be && ca == ba && have(2, ca) && have(1, ca) && have(0, ca)) {
+          tc_fence_after();
+          const uint32_t sv = smem_u32(slot(0, ca)), sk = smem_u32(slot(1, ca)),
+                         sq = smem_u32(slot(2, ca)), so = smem_u32(slot(3, ca));
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk)
             umma_bf16(tm + A1, kmaj(sk, HALF_TILE, kk), kmaj(sq, HALF_TILE, kk),
                       umma_idesc(128, 128, 0, 0), kk > 0);
-          mbar_wait(full + 0, ph, abort);
 #pragma unroll
           for (int kk = 0; kk < DV / 16; ++kk)
             umma_bf16(tm + A2, kmaj(sv, HALF_TILE, kk), kmaj(so, HALF_TILE, kk),
                       umma_idesc(128, 128, 0, 0), kk > 0);
           umma_commit(bar_a);
+          ++ca;
+          idle = false;
         }
-        __syncwarp();
-        off = meet<false>(abort) || off;
-        if (t.l == 0) {
+        // products with R: its tiles written, its sum added from where they go
+        if (cf < ca && cf == bfr && wg > cf && wr > cf) {
           tc_fence_after();
+          const uint32_t sv = smem_u32(slot(0, cf)), sk = smem_u32(slot(1, cf));
 #pragma unroll 1
           for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -1346,52 +1424,32 @@ __global__ void __launch_bounds__(NTHR, 1)
             umma_bf16(tm + G2, kmaj(sk, HALF_TILE, kk), mnmaj(smem_u32(r_hi), L::HALF_R, kk),
                       umma_idesc(128, DV, 0, 1), kk > 0);
           umma_commit(bar_f);
+          ++cf;
+          idle = false;
         }
-        __syncwarp();
-        off = meet<false>(abort) || off;
-        if (t.l == 0) {
-          tc_fence_after();
-          if (!*abort) {
-            load(2, i + 1);
-            load(3, i + 1);
-          }
-#pragma unroll
-          for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + G1, tm + A2 + 8 * kk, mnmaj(sq, HALF_TILE, kk),
-                    umma_idesc(128, DK, 0, 1), true);
-#pragma unroll
-          for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + G2, tm + A1 + 8 * kk, mnmaj(so, HALF_TILE, kk), umma_idesc(128, DV, 0, 1), true);
-          umma_commit(bar_c);
-        }
-        __syncwarp();
-        if (t.l == 0 && !off) {  // the last products are done: q and dO
-          mbar_wait(bar_c, ph, abort);
-          load(1, i + 1);
-          load(0, i + 1);
-        }
-        __syncwarp();
-        off = meet<true>(abort) || off;
+        if (!idle)
+          t0 = clock64();
+        else if (clock64() - t0 > WAIT_LIMIT)
+          *abort = 1;
       }
-    } else {
+    } else if (t.w >= P_DEC && t.w < P_LOAD) {
       auto raw = [&](int i) {
         const int c = nch - 1 - i;
         return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
       };
       const bool wide = a.decay != nullptr;
       Raw ahead = {};
-      const bool fills = t.w < DEC + DEC_WARPS;
-      if (fills && nch) fill_vec<true>(t.w - DEC, raw(0), wide, a.scale, vec[0]);
-      if (nch > 1) ahead = raw(1);
-      bool off = meet<true>(abort);
-      for (int i = 0; i < nch && !off; ++i) {
-        if (fills && i + 1 < nch) fill_vec<true>(t.w - DEC, ahead, wide, a.scale, vec[(i + 1) & 1]);
-        if (i + 2 < nch) ahead = raw(i + 2);
-        off = meet<true>(abort);
+      if (nch) ahead = raw(0);
+      for (int i = 0; i < nch; ++i) {
+        if (i > 1) mbar_wait(ev_u + (i & 1), ((i >> 1) + 1) & 1, abort);  // those of chunk i - 2
+        fill_vec<true>(t.w - P_DEC, ahead, wide, a.scale, vec[i & 1]);
+        if (i + 1 < nch) ahead = raw(i + 1);
+        __syncwarp();
+        if (t.l == 0) mbar_arrive(ev_v + (i & 1));
       }
     }
   }
-  tear_down(t, CTL, full, 4, tm, abort, a.status);
+  tear_down(t, P_CTL, full, 4, tm, abort, a.status);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1404,7 +1462,7 @@ int unit_chunks(const gdn_lin_shape& s, bool packed) {
   const long long nc = std::max(1, (s.T + TC - 1) / TC);
   if (packed) {  // the lengths are known on the device only: some waves of equal units
     const long long all = (nc + s.nseq / 2) * s.H;
-    return (int)std::min(64ll, std::max(4ll, (all + SMS * 4 - 1) / (SMS * 4)));
+    return (int)std::min(64ll, std::max(4ll, (all + SMS * 2 - 1) / (SMS * 2)));
   }
   const long long chains = (long long)s.nseq * s.H;
   double best = 1e300;
@@ -1539,7 +1597,7 @@ cudaError_t run_tc(const LinCall& c, bool back) {
          mdq);
   if (e) return e;
   prof_mark(c.st, "lin_tc_back");
-  e = GO((k_lin_tc_back<DK, DV>), Back, Regs<NTHR>::LAUNCH, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
+  e = GO((k_lin_tc_back<DK, DV>), Back, Regs<P_NTHR>::LAUNCH, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
          (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo, mdk,
          mdv);
 #undef GO
