@@ -679,9 +679,12 @@ __global__ void __launch_bounds__(NTHR, 1)
 //   MMAs: x S (state ready, result read) | P z, the state's sum (P, x S and y ready) | x y^T
 //   of the next chunk (P z done)
 // The tiles x, y, z take the slots in turn, each as soon as the one before is done with it.
-constexpr int P_CTL = 16, P_DEC = 17, P_LOAD = 19, P_NTHR = 640;
+// The warp that issues the MMAs keeps asking the barriers: beside the warps of lane quarter 3,
+// which have the least to do with P (on the scheduler of quarter 0 the backward took 588 us
+// instead of 578 for 32768 tokens x 16 heads).
+constexpr int P_LOAD = 16, P_DEC = 17, P_CTL = 19, P_NTHR = 640;
 constexpr long long WAIT_LIMIT = 1ll << 32;  // cycles without progress (mbar_wait's own limit)
-static_assert(P_DEC + DEC_WARPS == P_LOAD && (P_LOAD + 1) * 32 == P_NTHR, "the last warpgroup");
+static_assert(P_DEC + DEC_WARPS == P_CTL && (P_CTL + 1) * 32 == P_NTHR, "the last warpgroup");
 template <int DY, int DZ, bool DQ>
 struct PassSm {
   static constexpr int THREADS = P_NTHR;
@@ -849,7 +852,9 @@ __global__ void __launch_bounds__(P_NTHR, 1)
     more_registers<P_NTHR>();
     const size_t sh = ((size_t)u.seq * a.H + h) * DY * DZ, uh = ((size_t)unit * a.H + h) * DY * DZ;
     float s[N];
-    load_state<DY, DZ, DQ, N>(u.at ? S_unit + uh : S_in ? S_in + sh : nullptr, t.lane, N * t.cg, s);
+    // S_out may be S_in: a sequence's last unit writes it at any time, so the first of many
+    // starts from the scan's copy
+    load_state<DY, DZ, DQ, N>(u.n > 1 ? S_unit + uh : S_in ? S_in + sh : nullptr, t.lane, N * t.cg, s);
     if (t.lane < DY) put_split<N, DQ>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
     warp_done<true>(ev_s);
     for (int c = 0; c < nch; ++c) {
@@ -898,8 +903,10 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         const int c = (n - SL) / 3, kind = n - SL - 3 * c;
         while (!*abort && !(kind == 0   ? seen[2] > c && seen[3] > c
                             : kind == 1 ? seen[3] > c && seen[4] > c
-                                        : seen[0] > c && seen[1] > c))
+                                        : seen[0] > c && seen[1] > c)) {
+          __nanosleep(40);  // its scheduler is others' too
           if (clock64() - t0 > 64 * WAIT_LIMIT) *abort = 1;  // the issuing thread gives up before
+        }
         load(n);
       }
     } else if (t.w == P_CTL && t.l == 0) {  // ---- MMAs
@@ -984,7 +991,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         else if (clock64() - t0 > WAIT_LIMIT)
           *abort = 1;
       }
-    } else if (t.w >= P_DEC && t.w < P_LOAD) {
+    } else if (t.w >= P_DEC && t.w < P_DEC + DEC_WARPS) {
       auto raw = [&](int c) {
         return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
       };
@@ -1174,7 +1181,8 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   } else if (t.w < 16) {  // ---- R and the products with it
     more_registers<P_NTHR>();
     float r[NV];
-    const float* from = last ? (dS_out ? dS_out + sh : nullptr) : R_unit + uh * DK * DV;
+    // dS_in may be dS_out: of many units none reads it
+    const float* from = last && !dS_out ? nullptr : u.n > 1 ? R_unit + uh * DK * DV : dS_out + sh;
     load_state<DK, DV, false, NV>(from, t.lane, NV * t.cg, r);
     if (t.lane < DK) put_split<NV, true>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
     {
@@ -1277,8 +1285,10 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       };
       const long long t0 = clock64();
       auto until = [&](int which, int n) {  // the issuing thread has seen `which` n times
-        while (!*abort && seen[which] < n)
+        while (!*abort && seen[which] < n) {
+          __nanosleep(40);
           if (clock64() - t0 > 64 * WAIT_LIMIT) *abort = 1;  // it gives up long before
+        }
         __threadfence_block();
         __syncwarp();
       };
@@ -1432,7 +1442,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         else if (clock64() - t0 > WAIT_LIMIT)
           *abort = 1;
       }
-    } else if (t.w >= P_DEC && t.w < P_LOAD) {
+    } else if (t.w >= P_DEC && t.w < P_DEC + DEC_WARPS) {
       auto raw = [&](int i) {
         const int c = nch - 1 - i;
         return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);

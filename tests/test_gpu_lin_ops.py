@@ -257,6 +257,32 @@ def test_lin_states_in_place_and_repeatable(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_lin_states_in_place_over_many_units(dtype, packed):
+    """A sequence that many CTAs share, its last state written where its first one is read."""
+    T, H = 9001, 20
+    x = lin_inputs(1, T, H, 64, 64, DT[dtype], "weak", seed=5)
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda") if packed else None
+    a = [x[i] for i in "qkvg"]
+    o, S = gdn.gdn_lin_fwd(*a, x["S"], cu_seqlens=cu)
+    want = gdn.gdn_lin_bwd(*a, x["S"], x["do"], x["dS"], cu_seqlens=cu)
+    sh = gdn.gdn_lin_shape(1, T, H, 64, 64, 0 if dtype == "f32" else 1, 1, *(t.stride(1) for t in a), 1.0)
+    lib, p = gdn.load(), lambda t: None if t is None else t.data_ptr()
+    for _ in range(5):
+        S2 = x["S"].clone()
+        o2, _ = gdn.gdn_lin_fwd(*a, S2, S_out=S2, cu_seqlens=cu)
+        assert torch.equal(o, o2) and torch.equal(S, S2)
+        dS = x["dS"].clone()
+        got = [torch.full_like(t, float("nan")) for t in want[:4]]
+        ws = torch.empty(lib.gdn_lin_workspace_bytes(sh, 1), dtype=torch.uint8, device="cuda")
+        assert lib.gdn_lin_bwd(sh, *map(p, a), None, p(x["S"]), p(cu), p(x["do"]), p(dS), *map(p, got),
+                               None, p(dS), p(ws), ws.numel(),
+                               torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert all(torch.equal(i, j) for i, j in zip(want, got + [dS]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_lin_on_another_stream_and_in_a_graph(dtype):
     x = lin_inputs(1, 700, 2, 128, 64, DT[dtype], seed=21)
     a = [x[i] for i in "qkvg"]
