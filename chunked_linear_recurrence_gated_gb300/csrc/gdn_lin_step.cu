@@ -11,13 +11,19 @@
 namespace gdn {
 namespace {
 
+// Columns of a block and blocks of an SM. The states' bytes bound it: 256 sequences x 32 heads
+// of 128 x 128 take 152 us, the measured copy rate (64 columns by 5 blocks 151, but one
+// sequence 2.9 us instead of 2.5); 45 sequences x 24 heads with 1 to 8 tokens 25 us (63 %, 64
+// columns 28), where the arithmetic of the longer ones stands beside the loads.
+constexpr int LS_COLS = 32, LS_BLOCKS = 8;
 constexpr int LS_NT = 128;   // threads of a block
 constexpr int LS_TILE = 8;   // tokens whose q, k and v are in shared memory together
 
 // One block: COLS columns of one head's state of one sequence, in registers: a
 // thread has 4 columns of R consecutive rows. Per token S <- a S + k v^T and the
 // thread's part of q S (3 fp32 multiply-adds per element, two at a time), whose
-// sums over the block's row groups are joined once per tile of tokens.
+// sums over the block's row groups are joined once per tile of tokens. ONE: every sequence
+// has one token, which is asked for together with the state (167 -> 151 us of the batch).
 template <typename T, int DK, int COLS>
 struct LinStep {
   static constexpr int CG = COLS / 4;        // threads of a row
@@ -26,16 +32,16 @@ struct LinStep {
   static_assert(R % 4 == 0 && CG <= 32, "whole 16-byte pieces of k and q, rows inside a warp");
 };
 
-template <typename T, int DK, int DV, int COLS>
-__global__ void __launch_bounds__(LS_NT)
+template <typename T, int DK, int DV, int COLS, bool ONE>
+__global__ void __launch_bounds__(LS_NT, LS_BLOCKS)
     k_lin_step(Cache cache, FastDiv byHP, int G, long long ldq, long long ldk, long long ldv,
                long long ldg, float scale, const T* q, const T* k, const T* v, const T* g,
                const float* decay, float* S, T* o) {
   using L = LinStep<T, DK, COLS>;
-  constexpr int PARTS = DV / COLS, NW = LS_NT / 32;
-  __shared__ __align__(16) float sk[LS_TILE][DK], sq[LS_TILE][DK], sv[LS_TILE][COLS];
-  __shared__ __align__(16) float red[LS_TILE][NW][COLS];
-  __shared__ float sa[LS_TILE];
+  constexpr int PARTS = DV / COLS, NW = LS_NT / 32, TILE = ONE ? 1 : LS_TILE;
+  __shared__ __align__(16) float sk[TILE][DK], sq[TILE][DK], sv[TILE][COLS];
+  __shared__ __align__(16) float red[TILE][NW][COLS];
+  __shared__ float sa[TILE];
   chain();
   uint32_t seq, hp;
   byHP(blockIdx.x, seq, hp);
@@ -45,17 +51,19 @@ __global__ void __launch_bounds__(LS_NT)
   const int tid = threadIdx.x, cg = tid % L::CG, rg = tid / L::CG, warp = tid >> 5;
   const size_t base = ((size_t)h * DK + rg * L::R) * DV + c0 + cg * 4;
   f32x2 s[L::R][2];
+  float4 x[L::R];
+#pragma unroll
+  for (int i = 0; i < L::R; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (sc.in >= 0) {
     const float* p = S + (size_t)sc.in * H * DK * DV + base;
-    float4 x[L::R];
 #pragma unroll
     for (int i = 0; i < L::R; ++i) x[i] = *reinterpret_cast<const float4*>(p + (size_t)i * DV);
+  }
+  auto take = [&]() {
 #pragma unroll
     for (int i = 0; i < L::R; ++i) s[i][0] = pack2(x[i].x, x[i].y), s[i][1] = pack2(x[i].z, x[i].w);
-  } else {
-#pragma unroll
-    for (int i = 0; i < L::R; ++i) s[i][0] = s[i][1] = pack2(0.f, 0.f);
-  }
+  };
+  if (!ONE) take();
   auto store = [&]() {
     float* p = S + (size_t)sc.out * H * DK * DV + base;
 #pragma unroll
@@ -66,26 +74,33 @@ __global__ void __launch_bounds__(LS_NT)
       *reinterpret_cast<float4*>(p + (size_t)i * DV) = x;
     }
   };
-  if (sc.store && sc.commit == 0) store();
-  for (int tb = 0; tb < sc.len; tb += LS_TILE) {
-    const int nb = min(LS_TILE, sc.len - tb);
-    if (tb) __syncthreads();  // the tile before is done with
+  auto load_tile = [&](int tb, int nb) {
     for (int i = tid; i < nb * (DK / 8) * 2; i += LS_NT) {
       const int t = i / (DK / 4), e = i % (DK / 8) * 8;
       const bool is_q = i / (DK / 8) & 1;
       const size_t row = (size_t)(sc.t0 + tb + t);
-      float x[8];
-      ld8((is_q ? q + row * ldq : k + row * ldk) + (size_t)(h / G) * DK + e, x);
-      st8((is_q ? sq[t] : sk[t]) + e, x);
+      float y[8];
+      ld8((is_q ? q + row * ldq : k + row * ldk) + (size_t)(h / G) * DK + e, y);
+      st8((is_q ? sq[t] : sk[t]) + e, y);
     }
     for (int i = tid; i < nb * (COLS / 8); i += LS_NT) {
       const int t = i / (COLS / 8), e = i % (COLS / 8) * 8;
-      float x[8];
-      ld8(v + (size_t)(sc.t0 + tb + t) * ldv + (size_t)h * DV + c0 + e, x);
-      st8(sv[t] + e, x);
+      float y[8];
+      ld8(v + (size_t)(sc.t0 + tb + t) * ldv + (size_t)h * DV + c0 + e, y);
+      st8(sv[t] + e, y);
     }
     if (tid < nb)
       sa[tid] = expf(decay ? decay[h] : ldf(g + (size_t)(sc.t0 + tb + tid) * ldg + h));
+  };
+  if (ONE) {
+    load_tile(0, 1);
+    take();
+  }
+  if (sc.store && sc.commit == 0) store();
+  for (int tb = 0; tb < (ONE ? 1 : sc.len); tb += TILE) {
+    const int nb = ONE ? 1 : min(TILE, sc.len - tb);
+    if (tb) __syncthreads();  // the tile before is done with
+    if (!ONE) load_tile(tb, nb);
     __syncthreads();
     for (int t = 0; t < nb; ++t) {
       const f32x2 a = both2(sa[t]);
@@ -133,13 +148,19 @@ void launch_cols(const gdn_lin_step_shape& s, const Cache& c, const void* q, con
                  const void* v, const void* g, const float* decay, float* S, void* o,
                  cudaStream_t st) {
   constexpr int parts = DV / COLS;
-  launch(k_lin_step<T, DK, DV, COLS>, dim3((unsigned)s.N * s.H * parts), dim3(LS_NT), 0, st, 1, c,
-         FastDiv(s.H * parts), s.H / s.Hk, s.ldq, s.ldk, s.ldv, s.ldg, s.scale, (const T*)q,
-         (const T*)k, (const T*)v, (const T*)g, decay, S, (T*)o);
+  auto go = [&](auto kernel) {
+    launch(kernel, dim3((unsigned)s.N * s.H * parts), dim3(LS_NT), 0, st, 1, c, FastDiv(s.H * parts),
+           s.H / s.Hk, s.ldq, s.ldk, s.ldv, s.ldg, s.scale, (const T*)q, (const T*)k, (const T*)v,
+           (const T*)g, decay, S, (T*)o);
+  };
+  if (c.cu)
+    go(k_lin_step<T, DK, DV, COLS, false>);
+  else
+    go(k_lin_step<T, DK, DV, COLS, true>);
 }
 template <typename T, int DK, int DV, typename... A>
 void launch_lin_step(const gdn_lin_step_shape& s, A... a) {
-  launch_cols<T, DK, DV, 64>(s, a...);
+  launch_cols<T, DK, DV, LS_COLS>(s, a...);
 }
 template <typename T, typename... A>
 void dispatch_lin_step(const gdn_lin_step_shape& s, A... a) {
