@@ -28,8 +28,8 @@ namespace {
 
 constexpr int LC = 64;    // tokens of a chunk
 constexpr int LN_NT = 256;
-constexpr int LP = 12;    // floats between rows: both ways to read a fragment (rows 8 apart
-                          // by 4 columns, 4 by 8) hit every bank at most twice
+constexpr int LP = 4;     // floats between rows: both ways to read a fragment (8 rows by 4
+                          // columns, 4 by 8) hit every bank at most twice
 
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
@@ -38,10 +38,11 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
 
 // C += A B by one warp: 16 rows, NT x 8 columns, K deep; a(m, k) and b(k, n) give the
 // operands' elements. Each takes two TF32 parts, the product of the second parts is left out.
-template <int NT, int K, class FA, class FB>
+// U steps of K are unrolled: for operands in global memory enough that their loads overlap.
+template <int NT, int K, int U = 2, class FA, class FB>
 __device__ __forceinline__ void mm(float (*c)[4], FA a, FB b) {
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-#pragma unroll 2
+#pragma unroll U
   for (int k0 = 0; k0 < K; k0 += 8) {
     uint32_t ah[4], al[4];
 #pragma unroll
@@ -58,8 +59,7 @@ __device__ __forceinline__ void mm(float (*c)[4], FA a, FB b) {
   }
 }
 
-// gamma of a chunk as a sum of two floats: summed in 64 bits, because differences of
-// neighbours have to keep their 24 bits where gamma itself is in the thousands.
+// gamma of a chunk, in two floats.
 struct Gamma {
   float hi[LC], lo[LC];
   __device__ __forceinline__ float to(int t, int s) const {  // gamma_t - gamma_s
@@ -70,41 +70,50 @@ template <typename T>
 __device__ __forceinline__ void chunk_gamma(const LinUnit& u, int h, const T* g, long long ldg,
                                             const float* decay, Gamma& out) {  // one warp
   const int l = threadIdx.x & 31;
-  double x[2];
+  Two c[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = 2 * l + i;
-    x[i] = t < u.len ? lin_decay(decay ? decay[h] : ldf(g + (size_t)(u.row + t) * ldg + h)) : 0.f;
+    c[i] = {t < u.len ? lin_decay(decay ? decay[h] : ldf(g + (size_t)(u.row + t) * ldg + h)) : 0.f, 0.f};
   }
-  double sum = x[0] + x[1];
+  c[1] = add_two(c[0], c[1]);
+  const Two before = sum_before(c[1]);
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, sum, d);
-    if (l >= d) sum += y;
+  for (int i = 0; i < 2; ++i) {
+    const Two x = add_two(before, c[i]);
+    out.hi[2 * l + i] = x.hi;
+    out.lo[2 * l + i] = x.lo;
   }
-  const double first = sum - x[1];
-  out.hi[2 * l] = (float)first;
-  out.lo[2 * l] = (float)(first - (double)out.hi[2 * l]);
-  out.hi[2 * l + 1] = (float)sum;
-  out.lo[2 * l + 1] = (float)(sum - (double)out.hi[2 * l + 1]);
 }
 
-// A chunk's rows as fp32, zeros behind its end, row t times f(t).
-template <typename T, int D, class F>
-__device__ __forceinline__ void load_rows(float* to, const T* from, long long ld, const LinUnit& u,
-                                          F f) {
-  for (int i = threadIdx.x; i < LC * D / 8; i += LN_NT) {
-    const int t = i / (D / 8), e = i % (D / 8) * 8;
-    float x[8] = {};
-    if (t < u.len) {
-      ld8(from + (size_t)(u.row + t) * ld + e, x);
-      const float by = f(t);
+// A chunk's rows, all asked for at once (get) and later written as fp32 to shared memory
+// (put): zeros behind the chunk's end, row t times f(t).
+template <typename T, int D>
+struct Rows {
+  static constexpr int N = LC * D / 8 / LN_NT;
+  Raw8<T> raw[N];
+  __device__ __forceinline__ void get(const T* from, long long ld, const LinUnit& u) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * LN_NT, t = i / (D / 8);
+      raw[n] = Raw8<T>{};
+      if (t < u.len) raw[n] = ldraw8(from + (size_t)(u.row + t) * ld + i % (D / 8) * 8);
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void put(float* to, const LinUnit& u, F f) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * LN_NT, t = i / (D / 8);
+      float x[8];
+      cvt8(raw[n], x);
+      const float by = t < u.len ? f(t) : 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= by;
+      st8(to + t * (D + LP) + i % (D / 8) * 8, x);
     }
-    st8(to + t * (D + LP) + e, x);
   }
-}
+};
 
 template <typename T>
 struct LinIn {
@@ -114,7 +123,7 @@ struct LinIn {
   float scale;
 };
 
-// D (and E) of a chunk, and e^{gamma_C}. Grid (chunk, head).
+// D (or E) of a chunk, and e^{gamma_C}. Grid (chunk, head, D or E).
 template <typename T, int DK, int DV, bool BACK>
 __global__ void __launch_bounds__(LN_NT)
     k_lin_sum(LinMap m, LinIn<T> in, float* whole, float* D, float* E) {
@@ -126,23 +135,19 @@ __global__ void __launch_bounds__(LN_NT)
   const int h = blockIdx.y, H = gridDim.y, w = threadIdx.x >> 5;
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
   const size_t uh = (size_t)blockIdx.x * H + h;
+  const int pass = BACK ? blockIdx.z : 0;
+  Rows<T, DK> rx;
+  Rows<T, DV> ry;
+  rx.get((pass ? in.q : in.k) + (size_t)h * DK, pass ? in.ldq : in.ldk, u);
+  ry.get((pass ? in.dout : in.v) + (size_t)h * DV, pass ? in.ldo : in.ldv, u);
   if (w == 0) chunk_gamma(u, h, in.g, in.ldg, in.decay, gm);
   __syncthreads();
-  if (threadIdx.x == 0) whole[uh] = expf(gm.to(LC - 1, 0) + gm.hi[0]);
+  if (threadIdx.x == 0 && pass == 0) whole[uh] = expf(gm.to(LC - 1, 0) + gm.hi[0]);
   float *x = sm, *y = sm + LC * (DK + LP);
-#pragma unroll
-  for (int pass = 0; pass < (BACK ? 2 : 1); ++pass) {
-    if (pass) __syncthreads();
-    if (pass == 0) {
-      load_rows<T, DK>(x, in.k + (size_t)h * DK, in.ldk, u,
-                       [&](int r) { return expf(gm.to(LC - 1, r)); });
-      load_rows<T, DV>(y, in.v + (size_t)h * DV, in.ldv, u, [](int) { return 1.f; });
-    } else {
-      load_rows<T, DK>(x, in.q + (size_t)h * DK, in.ldq, u,
-                       [&](int r) { return in.scale * expf(gm.hi[r]); });
-      load_rows<T, DV>(y, in.dout + (size_t)h * DV, in.ldo, u, [](int) { return 1.f; });
-    }
-    __syncthreads();
+  rx.put(x, u, [&](int r) { return pass ? in.scale * expf(gm.hi[r]) : expf(gm.to(LC - 1, r)); });
+  ry.put(y, u, [](int) { return 1.f; });
+  __syncthreads();
+  {
     // 8 warps: 16 rows each of 128, or 4 x 2 halves of the columns
     constexpr int WN = DK == 128 ? 1 : 2, NT = DV / 8 / WN;
     const int m0 = w / WN * 16, n0 = w % WN * (DV / WN);
@@ -225,9 +230,16 @@ __global__ void __launch_bounds__(LN_NT)
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
   S += ((size_t)blockIdx.x * H + h) * DK * DV;
   auto one = [](int) { return 1.f; };
-  load_rows<T, DK>(q, in.q + (size_t)h * DK, in.ldq, u, one);
-  load_rows<T, DK>(k, in.k + (size_t)h * DK, in.ldk, u, one);
-  load_rows<T, DV>(v, in.v + (size_t)h * DV, in.ldv, u, one);
+  {
+    Rows<T, DK> rq, rk;
+    Rows<T, DV> rv;
+    rq.get(in.q + (size_t)h * DK, in.ldq, u);
+    rk.get(in.k + (size_t)h * DK, in.ldk, u);
+    rv.get(in.v + (size_t)h * DV, in.ldv, u);
+    rq.put(q, u, one);
+    rk.put(k, u, one);
+    rv.put(v, u, one);
+  }
   if (w == 0) chunk_gamma(u, h, in.g, in.ldg, in.decay, gm);
   __syncthreads();
   const int m0 = w / 2 * 16;
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(LN_NT)
   constexpr int NT = DV / 16;
   const int n0 = w % 2 * (DV / 2);
   float c[NT][4] = {};
-  mm<NT, DK>(c, [&](int i, int e) { return q[(m0 + i) * LK + e]; },
+  mm<NT, DK, 8>(c, [&](int i, int e) { return q[(m0 + i) * LK + e]; },
              [&](int e, int j) { return S[(size_t)e * DV + n0 + j]; });
   const float up[2] = {expf(gm.hi[m0 + g]), expf(gm.hi[m0 + g + 8])};
 #pragma unroll
@@ -273,7 +285,7 @@ __global__ void __launch_bounds__(LN_NT)
 // The gradients of a chunk from the state before it and the gradient of the one behind
 // it. dgsum [unit, H]: the sum of dg over the chunk (one decay for each head).
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(LN_NT)
+__global__ void __launch_bounds__(LN_NT, DK + DV == 128 ? 2 : 1)
     k_lin_grad(LinMap m, LinIn<T> in, const float* S, const float* R, T* dq, T* dk, T* dv, T* dg,
                float* dgsum) {
   chain();
@@ -294,10 +306,18 @@ __global__ void __launch_bounds__(LN_NT)
   S += uh * DK * DV;
   R += uh * DK * DV;
   auto one = [](int) { return 1.f; };
-  load_rows<T, DK>(q, in.q + (size_t)h * DK, in.ldq, u, one);
-  load_rows<T, DK>(k, in.k + (size_t)h * DK, in.ldk, u, one);
-  load_rows<T, DV>(v, in.v + (size_t)h * DV, in.ldv, u, one);
-  load_rows<T, DV>(d, in.dout + (size_t)h * DV, in.ldo, u, one);
+  {
+    Rows<T, DK> rq, rk;
+    Rows<T, DV> rv, rd;
+    rq.get(in.q + (size_t)h * DK, in.ldq, u);
+    rk.get(in.k + (size_t)h * DK, in.ldk, u);
+    rv.get(in.v + (size_t)h * DV, in.ldv, u);
+    rd.get(in.dout + (size_t)h * DV, in.ldo, u);
+    rq.put(q, u, one);
+    rk.put(k, u, one);
+    rv.put(v, u, one);
+    rd.put(d, u, one);
+  }
   if (w == 0) chunk_gamma(u, h, in.g, in.ldg, in.decay, gm);
   __syncthreads();
   const int m0 = w / 2 * 16, half = w % 2;
@@ -337,7 +357,11 @@ __global__ void __launch_bounds__(LN_NT)
   }
   {
     float x = 0.f;
-    for (int i = threadIdx.x; i < DK * DV; i += LN_NT) x = fmaf(S[i], R[i], x);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < DK * DV / 4; i += LN_NT) {
+      const float4 a = reinterpret_cast<const float4*>(S)[i], b = reinterpret_cast<const float4*>(R)[i];
+      x = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, x))));
+    }
     x = lane_sum<32>(x);
     if (lane == 0) cross[w] = x;
   }
@@ -381,7 +405,7 @@ __global__ void __launch_bounds__(LN_NT)
   {
     const int n0 = half * (DK / 2);
     float c[DK / 16][4] = {};
-    mm<DK / 16, DV>(c, [&](int i, int e) { return d[(m0 + i) * LV + e]; },
+    mm<DK / 16, DV, 8>(c, [&](int i, int e) { return d[(m0 + i) * LV + e]; },
                     [&](int e, int j) { return S[(size_t)(n0 + j) * DV + e]; });
     finish(c, up, q, LK, n0, far_q[half]);
     mm<DK / 16, LC>(c, [&](int i, int s) { return wm[(m0 + i) * LL + s]; },
@@ -391,7 +415,7 @@ __global__ void __launch_bounds__(LN_NT)
   {
     const int n0 = half * (DK / 2);
     float c[DK / 16][4] = {};
-    mm<DK / 16, DV>(c, [&](int i, int e) { return v[(m0 + i) * LV + e]; },
+    mm<DK / 16, DV, 8>(c, [&](int i, int e) { return v[(m0 + i) * LV + e]; },
                     [&](int e, int j) { return R[(size_t)(n0 + j) * DV + e]; });
     finish(c, down, k, LK, n0, far_k[half]);
     mm<DK / 16, LC>(c, [&](int i, int s) { return wm[s * LL + m0 + i]; },
@@ -401,7 +425,7 @@ __global__ void __launch_bounds__(LN_NT)
   {
     const int n0 = half * (DV / 2);
     float c[DV / 16][4] = {};
-    mm<DV / 16, DK>(c, [&](int i, int e) { return k[(m0 + i) * LK + e]; },
+    mm<DV / 16, DK, 8>(c, [&](int i, int e) { return k[(m0 + i) * LK + e]; },
                     [&](int e, int j) { return R[(size_t)e * DV + n0 + j]; });
     finish(c, down, k, LK, n0, (float*)nullptr);
     mm<DV / 16, LC>(c, [&](int i, int s) { return p[s * LL + m0 + i]; },
@@ -527,7 +551,7 @@ cudaError_t run_simt(const LinCall& c, bool back) {
                        (long long)s.H * DV, s.scale};
   cudaError_t e = cudaSuccess;
   if (c.cu && (e = lin_plan(p.m, p.first, p.owner, p.status, c.st))) return e;
-  const dim3 grid(p.m.cap, s.H);
+  dim3 grid(p.m.cap, s.H, back ? 2 : 1);
   constexpr int rows_k = LC * (DK + LP) * 4, rows_v = LC * (DV + LP) * 4, square = LC * (LC + LP) * 4;
   auto go = [&](auto kernel, int smem, auto... a) {
     const cudaError_t f =
@@ -538,6 +562,7 @@ cudaError_t run_simt(const LinCall& c, bool back) {
   e = back ? go(k_lin_sum<T, DK, DV, true>, rows_k + rows_v, p.whole, p.D, p.E)
            : go(k_lin_sum<T, DK, DV, false>, rows_k + rows_v, p.whole, p.D, p.E);
   if (e) return e;
+  grid.z = 1;
   const int n4 = DK * DV / 4;
   prof_mark(c.st, "lin_scan");
   e = launch(k_lin_scan, dim3((n4 + SC_NT - 1) / SC_NT, s.nseq * s.H, back ? 2 : 1), dim3(SC_NT), 0,

@@ -51,6 +51,31 @@ __device__ __forceinline__ void lin_seq(const LinMap& m, int s, int& first, int&
 // the clamped values stay finite where those of -inf would give NaN differences.
 __device__ __forceinline__ float lin_decay(float g) { return g < -1e4f ? -1e4f : g; }
 
+// gamma summed as pairs of floats (2^-47 of itself: differences of neighbours keep their
+// 24 bits where gamma itself is in the thousands; FP64 has 1/64 of the rate, and all wait for it).
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add_two(Two a, Two b) {
+  const float s = a.hi + b.hi, v = s - a.hi;
+  const float e = (a.hi - (s - v)) + (b.hi - v) + (a.lo + b.lo);
+  Two r;
+  r.hi = s + e;
+  r.lo = e - (r.hi - s);
+  return r;
+}
+// The sum of the lanes before this one.
+__device__ __forceinline__ Two sum_before(Two x) {
+  const int l = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Two y = {__shfl_up_sync(0xffffffffu, x.hi, d), __shfl_up_sync(0xffffffffu, x.lo, d)};
+    if (l >= d) x = add_two(y, x);
+  }
+  const Two r = {__shfl_up_sync(0xffffffffu, x.hi, 1), __shfl_up_sync(0xffffffffu, x.lo, 1)};
+  return l ? r : Two{0.f, 0.f};
+}
+
 // What a whole call takes.
 struct LinCall {
   gdn_lin_shape s;

@@ -177,33 +177,13 @@ __device__ __forceinline__ Raw raw_decay(int row, int len, int h, const bf* g, l
 __device__ __forceinline__ float decay_value(uint32_t x, bool wide) {
   return lin_decay(__uint_as_float(wide ? x : x << 16));
 }
-// gamma summed as pairs of floats (2^-47 of itself: differences of neighbours keep their
-// 24 bits however large it is; FP64 has 1/64 of the rate, and this warp is waited for).
-struct Two {
-  float hi, lo;
-};
-__device__ __forceinline__ Two add_two(Two a, Two b) {
-  const float s = a.hi + b.hi, v = s - a.hi;
-  const float e = (a.hi - (s - v)) + (b.hi - v) + (a.lo + b.lo);
-  Two r;
-  r.hi = s + e;
-  r.lo = e - (r.hi - s);
-  return r;
-}
 __device__ __forceinline__ void sum_decay(const Raw& r, bool wide, float* hi, float* lo) {
   const int l = threadIdx.x & 31;
   Two c[4];
   c[0] = {decay_value(r.x[0], wide), 0.f};
 #pragma unroll
   for (int i = 1; i < 4; ++i) c[i] = add_two(c[i - 1], {decay_value(r.x[i], wide), 0.f});
-  Two all = c[3];
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const Two y = {__shfl_up_sync(0xffffffffu, all.hi, d), __shfl_up_sync(0xffffffffu, all.lo, d)};
-    if (l >= d) all = add_two(y, all);
-  }
-  Two before = {__shfl_up_sync(0xffffffffu, all.hi, 1), __shfl_up_sync(0xffffffffu, all.lo, 1)};
-  if (l == 0) before = {0.f, 0.f};
+  const Two before = sum_before(c[3]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const Two x = add_two(before, c[i]);
