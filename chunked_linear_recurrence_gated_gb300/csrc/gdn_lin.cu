@@ -166,12 +166,13 @@ __global__ void __launch_bounds__(LN_NT)
 
 // In place over the units of a sequence: D_b becomes the state before unit b
 // (z = 0), E_b the gradient of the state behind it (z = 1, from the last unit). `open`:
-// the last one to be visited has no sum of its own, and nothing is wanted behind it.
+// the last one to be visited has no sum of its own, and nothing is wanted behind it. D and
+// E have the units' layouts (LinLayout), the states of the call their own.
 constexpr int SC_NT = 128, SC_U = 8;
 __global__ void __launch_bounds__(SC_NT)
-    k_lin_scan(LinMap m, int H, int n4, const float* whole_d, float* D, const float* S_in,
-               float* S_out, const float* whole_e, float* E, const float* dS_out, float* dS_in,
-               bool open, int* status) {
+    k_lin_scan(LinMap m, int H, int dk, int dv, LinLayout lay_d, const float* whole_d, float* D,
+               const float* S_in, float* S_out, LinLayout lay_e, const float* whole_e, float* E,
+               const float* dS_out, float* dS_in, bool open, int* status) {
   chain();
   if (m.cu) {
     if (*status != DEV_OK) return;
@@ -179,17 +180,30 @@ __global__ void __launch_bounds__(SC_NT)
     *status = DEV_OK;
   }
   const int e = blockIdx.x * SC_NT + threadIdx.x, h = blockIdx.y % H, seq = blockIdx.y / H;
+  const int n4 = dk * dv / 4;
   const bool back = blockIdx.z;
   if (e >= n4) return;
   int first, n;
   lin_seq(m, seq, first, n);
+  if (open && n < 2) return;  // its one unit starts from S_in itself
   float4* at = reinterpret_cast<float4*>(back ? E : D) + e;
   const float* whole = back ? whole_e : whole_d;
   const float* from = back ? dS_out : S_in;
   float* to = back ? dS_in : S_out;
   const size_t sh = (size_t)seq * H + h;
-  float4 s = from ? reinterpret_cast<const float4*>(from)[sh * n4 + e]
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (from) {
+    from += sh * n4 * 4;
+    const LinLayout lay = back ? lay_e : lay_d;
+    if (lay == LIN_ROWS) {
+      s = reinterpret_cast<const float4*>(from)[e];
+    } else if (lay == LIN_KEYS) {
+      s = *reinterpret_cast<const float4*>(from + (size_t)(e % dk) * dv + e / dk * 4);
+    } else {
+      const float* p = from + (size_t)(e / dv * 4) * dv + e % dv;
+      s = make_float4(p[0], p[dv], p[2 * dv], p[3 * dv]);
+    }
+  }
   for (int b0 = 0; b0 < n; b0 += SC_U) {
     float4 d[SC_U];
     float a[SC_U];
@@ -563,11 +577,10 @@ cudaError_t run_simt(const LinCall& c, bool back) {
            : go(k_lin_sum<T, DK, DV, false>, rows_k + rows_v, p.whole, p.D, p.E);
   if (e) return e;
   grid.z = 1;
-  const int n4 = DK * DV / 4;
   prof_mark(c.st, "lin_scan");
-  e = launch(k_lin_scan, dim3((n4 + SC_NT - 1) / SC_NT, s.nseq * s.H, back ? 2 : 1), dim3(SC_NT), 0,
-             c.st, 1, p.m, s.H, n4, p.whole, p.D, c.S_in, c.S_out, p.whole, p.E, c.dS_out, c.dS_in,
-             false, p.status);
+  e = launch(k_lin_scan, dim3((DK * DV / 4 + SC_NT - 1) / SC_NT, s.nseq * s.H, back ? 2 : 1),
+             dim3(SC_NT), 0, c.st, 1, p.m, s.H, DK, DV, LIN_ROWS, p.whole, p.D, c.S_in, c.S_out,
+             LIN_ROWS, p.whole, p.E, c.dS_out, c.dS_in, false, p.status);
   if (e) return e;
   prof_mark(c.st, back ? "lin_grad" : "lin_out");
   e = back ? go(k_lin_grad<T, DK, DV>, 2 * (rows_k + rows_v + square), p.D, p.E, (T*)c.dq, (T*)c.dk,
@@ -634,10 +647,9 @@ cudaError_t lin_scan(const LinMap& m, const gdn_lin_shape& s, const float* whole
                      const float* S_in, float* E, const float* whole_e, const float* dS_out,
                      bool back, int* status, cudaStream_t st) {
   prof_mark(st, "lin_scan");
-  const int n4 = s.dk * s.dv / 4;
-  return launch(k_lin_scan, dim3((n4 + SC_NT - 1) / SC_NT, s.nseq * s.H, back ? 2 : 1), dim3(SC_NT),
-                0, st, 1, m, s.H, n4, whole, D, S_in, (float*)nullptr, whole_e, E, dS_out,
-                (float*)nullptr, true, status);
+  return launch(k_lin_scan, dim3((s.dk * s.dv / 4 + SC_NT - 1) / SC_NT, s.nseq * s.H, back ? 2 : 1),
+                dim3(SC_NT), 0, st, 1, m, s.H, s.dk, s.dv, back ? LIN_VALUES : LIN_KEYS, whole, D, S_in,
+                (float*)nullptr, LIN_KEYS, whole_e, E, dS_out, (float*)nullptr, true, status);
 }
 
 size_t lin_simt_bytes(const gdn_lin_shape& s, bool packed, bool back) {

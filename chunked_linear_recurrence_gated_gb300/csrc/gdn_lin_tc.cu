@@ -178,7 +178,6 @@ __device__ __forceinline__ float decay_value(uint32_t x, bool wide) {
   return lin_decay(__uint_as_float(wide ? x : x << 16));
 }
 __device__ __forceinline__ void sum_decay(const Raw& r, bool wide, float* hi, float* lo) {
-  const int l = threadIdx.x & 31;
   Two c[4];
   c[0] = {decay_value(r.x[0], wide), 0.f};
 #pragma unroll
@@ -407,6 +406,25 @@ __device__ __forceinline__ void store_state(float* to, int lane, int c0, const f
           make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
   }
 }
+// The same of a unit's state in the workspace, [DZ / 4][DY][4]: whole lines for a warp, where
+// rows of DZ would take 32 pieces of 16 bytes (8 thousand cycles for 64 KB).
+template <int DY, int N>
+__device__ __forceinline__ void load_unit(const float* from, int lane, int c0, float* s) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane < DY) x = *reinterpret_cast<const float4*>(from + ((size_t)(c0 + i) / 4 * DY + lane) * 4);
+    s[i] = x.x, s[i + 1] = x.y, s[i + 2] = x.z, s[i + 3] = x.w;
+  }
+}
+template <int DY, int N>
+__device__ __forceinline__ void store_unit(float* to, int lane, int c0, const float* s) {
+  if (lane >= DY) return;
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    *reinterpret_cast<float4*>(to + ((size_t)(c0 + i) / 4 * DY + lane) * 4) =
+        make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+}
 // s <- by s + an accumulator's N columns (an even number of 32s).
 template <int N>
 __device__ __forceinline__ void add_state(uint32_t taddr, float by, float* s) {
@@ -548,12 +566,14 @@ __global__ void __launch_bounds__(NTHR, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   const int nch = (u.len + TC - 1) / TC;
-  const uint32_t tm = set_up(t, CTL, full, ST + 2, 0, 0, 0, tslot, abort);
   auto chunk = [&](int i) { return REV ? nch - 1 - i : i; };
   auto raw = [&](int i) {
     const int c = chunk(i);
     return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
   };
+  Raw ahead = {};  // of the first chunk, on its way while barriers and tensor memory are set up
+  if (t.w == DEC && nch) ahead = raw(0);
+  const uint32_t tm = set_up(t, CTL, full, ST + 2, 0, 0, 0, tslot, abort);
   auto tile = [&](int i) { return sb + 2 * (i % ST) * L::SLOT; };  // y, and z a slot behind it
   if (t.w < CTL) {
     const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
@@ -586,7 +606,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     if (nch) update(nch - 1);
     const size_t uh = (size_t)unit * a.H + h;
-    store_state<DY, DZ, TR, N>(out + uh * DY * DZ, t.lane, N * t.cg, s);
+    store_unit<DY, N>(out + uh * DY * DZ, t.lane, N * t.cg, s);
     if (t.tid == 0) whole[uh] = all;
   } else if (t.w == CTL) {
     auto load = [&](int i) {
@@ -632,10 +652,10 @@ __global__ void __launch_bounds__(NTHR, 1)
       fill_weights<REV>(hi, lo, a.scale, vec[i & 3]);
     };
     const bool fills = t.w == DEC;  // the others only meet
-    Raw ahead = {};
     if (fills) {
-      fill(raw(0), 0);
-      if (nch > 1) fill(raw(1), 1);
+      const Raw second = nch > 1 ? raw(1) : Raw{};
+      fill(ahead, 0);
+      if (nch > 1) fill(second, 1);
       if (nch > 2) ahead = raw(2);
     }
     meet<true>(abort);
@@ -709,6 +729,12 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   // what the issuing thread has seen done: P z, the state's sum, x S, x y^T, y weighed
   volatile int* seen = reinterpret_cast<volatile int*>(tslot + 2);
   const int nch = (u.len + TC - 1) / TC;
+  auto raw = [&](int c) {
+    return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
+  };
+  const bool decs = t.w >= P_DEC && t.w < P_DEC + DEC_WARPS;
+  Raw ahead = {};  // of the first chunk, on its way while barriers and tensor memory are set up
+  if (decs && nch) ahead = raw(0);
   const uint32_t tm = set_up(t, P_CTL, full, SL + 6, 2, 4, 2, tslot, abort);
   const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
   auto tile = [&](int n) { return sb + n % SL * L::SLOT; };  // tile n: x, y or z of chunk n / 3
@@ -834,7 +860,10 @@ __global__ void __launch_bounds__(P_NTHR, 1)
     float s[N];
     // S_out may be S_in: a sequence's last unit writes it at any time, so the first of many
     // starts from the scan's copy
-    load_state<DY, DZ, DQ, N>(u.n > 1 ? S_unit + uh : S_in ? S_in + sh : nullptr, t.lane, N * t.cg, s);
+    if (u.n > 1)
+      load_unit<DY, N>(S_unit + uh, t.lane, N * t.cg, s);
+    else
+      load_state<DY, DZ, DQ, N>(S_in ? S_in + sh : nullptr, t.lane, N * t.cg, s);
     if (t.lane < DY) put_split<N, DQ>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
     warp_done<true>(ev_s);
     for (int c = 0; c < nch; ++c) {
@@ -971,13 +1000,8 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         else if (clock64() - t0 > WAIT_LIMIT)
           *abort = 1;
       }
-    } else if (t.w >= P_DEC && t.w < P_DEC + DEC_WARPS) {
-      auto raw = [&](int c) {
-        return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
-      };
+    } else if (decs) {
       const bool wide = a.decay != nullptr;
-      Raw ahead = {};
-      if (nch) ahead = raw(0);
       for (int c = 0; c < nch; ++c) {
         if (c > 1) mbar_wait(ev_u + (c & 1), ((c >> 1) + 1) & 1, abort);  // those of chunk c - 2
         fill_vec<false>(t.w - P_DEC, ahead, wide, 1.f, vec[c & 1]);
@@ -1071,6 +1095,13 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   // early, v and k those of q and dO
   auto slot = [&](int kind, int i) { return sb + (kind ^ (i & 1 ? 2 : 0)) * L::SLOT; };
   const int nch = (u.len + TC - 1) / TC;
+  auto raw = [&](int i) {
+    const int c = nch - 1 - i;
+    return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
+  };
+  const bool decs = t.w >= P_DEC && t.w < P_DEC + DEC_WARPS;
+  Raw ahead = {};  // of the first chunk to be taken, as above
+  if (decs && nch) ahead = raw(0);
   const uint32_t tm = set_up(t, P_CTL, full, 10, 2, 6, 2, tslot, abort);
   const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
   const size_t sh = ((size_t)u.seq * a.H + h) * DK * DV;
@@ -1162,16 +1193,26 @@ __global__ void __launch_bounds__(P_NTHR, 1)
     more_registers<P_NTHR>();
     float r[NV];
     // dS_in may be dS_out: of many units none reads it
-    const float* from = last && !dS_out ? nullptr : u.n > 1 ? R_unit + uh * DK * DV : dS_out + sh;
-    load_state<DK, DV, false, NV>(from, t.lane, NV * t.cg, r);
+    const bool none = last && !dS_out;
+    if (u.n > 1)
+      load_unit<DK, NV>(R_unit + uh * DK * DV, t.lane, NV * t.cg, r);
+    else
+      load_state<DK, DV, false, NV>(none ? nullptr : dS_out + sh, t.lane, NV * t.cg, r);
     if (t.lane < DK) put_split<NV, true>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
     {
-      const float* S = !from ? nullptr : last ? S_end + sh : S_unit + (uh + a.H) * DK * DV;
+      // S as the units' of the transposed kernels, or as the call's
+      const float* S = last ? S_end + sh : S_unit + (uh + a.H) * DK * DV;
       float x = 0.f;
-      if (S && t.lane < DK) {
+      if (!none && t.lane < DK) {
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
-          const float4 y = *reinterpret_cast<const float4*>(S + (size_t)t.lane * DV + NV * t.cg + i);
+          float4 y;
+          if (last) {
+            y = *reinterpret_cast<const float4*>(S + (size_t)t.lane * DV + NV * t.cg + i);
+          } else {
+            const float* p = S + ((size_t)(t.lane >> 2) * DV + NV * t.cg + i) * 4 + (t.lane & 3);
+            y = make_float4(p[0], p[4], p[8], p[12]);
+          }
           x = fmaf(r[i], y.x, x);
           x = fmaf(r[i + 1], y.y, x);
           x = fmaf(r[i + 2], y.z, x);
@@ -1422,14 +1463,8 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         else if (clock64() - t0 > WAIT_LIMIT)
           *abort = 1;
       }
-    } else if (t.w >= P_DEC && t.w < P_DEC + DEC_WARPS) {
-      auto raw = [&](int i) {
-        const int c = nch - 1 - i;
-        return raw_decay(u.row + c * TC, min(TC, u.len - c * TC), h, a.g, a.ldg, a.decay);
-      };
+    } else if (decs) {
       const bool wide = a.decay != nullptr;
-      Raw ahead = {};
-      if (nch) ahead = raw(0);
       for (int i = 0; i < nch; ++i) {
         if (i > 1) mbar_wait(ev_u + (i & 1), ((i >> 1) + 1) & 1, abort);  // those of chunk i - 2
         fill_vec<true>(t.w - P_DEC, ahead, wide, a.scale, vec[i & 1]);
