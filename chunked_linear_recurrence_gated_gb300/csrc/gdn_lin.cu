@@ -480,13 +480,17 @@ __global__ void __launch_bounds__(LN_NT, DK + DV == 128 ? 2 : 1)
 }
 
 // The units of a packed call, one at least for each sequence. One block: each thread
-// counts a run of sequences.
-constexpr int PL_NT = 1024;
-__global__ void __launch_bounds__(PL_NT) k_lin_plan(LinMap m, int* first, int* owner, int* status) {
-  __shared__ int sums[32], bad;
+// counts a run of sequences. The order is a counting sort by the units' chunks; how units of
+// the same length stand among each other changes no result.
+constexpr int PL_NT = 1024, PL_BINS = 65;
+__global__ void __launch_bounds__(PL_NT)
+    k_lin_plan(LinMap m, int* first, int* owner, int* order, int chunk, int* status) {
+  __shared__ int sums[32], bad, bins[PL_BINS];
   chain();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   if (tid == 0) bad = m.cu[0] < 0 || m.cu[m.nseq] > m.T;
+  if (tid < PL_BINS) bins[tid] = 0;
+  auto bin = [&](int len) { return PL_BINS - 1 - min((len + chunk - 1) / chunk, PL_BINS - 1); };
   __syncthreads();
   const int run = (m.nseq + PL_NT - 1) / PL_NT, s0 = min(tid * run, m.nseq),
             s1 = min(s0 + run, m.nseq);
@@ -515,13 +519,52 @@ __global__ void __launch_bounds__(PL_NT) k_lin_plan(LinMap m, int* first, int* o
         off ? 0 : max(1, (int)(((unsigned)(m.cu[s + 1] - m.cu[s]) + m.unit - 1) / m.unit));
     for (int i = 0; i < k; ++i)
       if (before + i < m.cap) owner[before + i] = s;
+    if (order && k) {
+      if (k > 1) atomicAdd(bins + bin(m.unit), k - 1);
+      atomicAdd(bins + bin(m.cu[s + 1] - m.cu[s] - (k - 1) * m.unit), 1);
+    }
     before += k;
   }
   __shared__ int total;
   if (tid == PL_NT - 1) total = off ? 0 : before;
   __syncthreads();
   if (tid == 0) first[m.nseq] = total;
-  for (int i = total + tid; i < m.cap; i += PL_NT) owner[i] = -1;
+  for (int i = total + tid; i < m.cap; i += PL_NT) {
+    owner[i] = -1;
+    if (order) order[i] = i;
+  }
+  if (!order || off) return;
+  if (w == 0) {  // bins to first places
+    int x[3], at = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      x[i] = 3 * lane + i < PL_BINS ? bins[3 * lane + i] : 0;
+      at += x[i];
+    }
+    int all = at;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, all, d);
+      if (lane >= d) all += y;
+    }
+    at = all - at;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (3 * lane + i < PL_BINS) bins[3 * lane + i] = at;
+      at += x[i];
+    }
+  }
+  __syncthreads();
+  for (int s = s0; s < s1; ++s) {
+    const int u = first[s], k = max(1, (int)(((unsigned)(m.cu[s + 1] - m.cu[s]) + m.unit - 1) / m.unit));
+    if (k > 1) {
+      const int at = atomicAdd(bins + bin(m.unit), k - 1);
+      for (int i = 0; i < k - 1; ++i)
+        if (at + i < m.cap) order[at + i] = u + i;
+    }
+    const int at = atomicAdd(bins + bin(m.cu[s + 1] - m.cu[s] - (k - 1) * m.unit), 1);
+    if (at < m.cap) order[at] = u + k - 1;
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -564,7 +607,7 @@ cudaError_t run_simt(const LinCall& c, bool back) {
                        (const T*)c.dout, c.decay, s.ldq, s.ldk, s.ldv, s.ldg,
                        (long long)s.H * DV, s.scale};
   cudaError_t e = cudaSuccess;
-  if (c.cu && (e = lin_plan(p.m, p.first, p.owner, p.status, c.st))) return e;
+  if (c.cu && (e = lin_plan(p.m, p.first, p.owner, nullptr, LC, p.status, c.st))) return e;
   dim3 grid(p.m.cap, s.H, back ? 2 : 1);
   constexpr int rows_k = LC * (DK + LP) * 4, rows_v = LC * (DV + LP) * 4, square = LC * (LC + LP) * 4;
   auto go = [&](auto kernel, int smem, auto... a) {
@@ -638,9 +681,10 @@ gdn_status run(const LinCall& c, size_t ws_bytes, bool back) {
 
 }  // namespace
 
-cudaError_t lin_plan(const LinMap& m, int* first, int* owner, int* status, cudaStream_t st) {
+cudaError_t lin_plan(const LinMap& m, int* first, int* owner, int* order, int chunk, int* status,
+                     cudaStream_t st) {
   prof_mark(st, "lin_plan");
-  return launch(k_lin_plan, dim3(1), dim3(PL_NT), 0, st, 1, m, first, owner, status);
+  return launch(k_lin_plan, dim3(1), dim3(PL_NT), 0, st, 1, m, first, owner, order, chunk, status);
 }
 
 cudaError_t lin_scan(const LinMap& m, const gdn_lin_shape& s, const float* whole, float* D,

@@ -15,7 +15,12 @@ struct LinMap {
   const int* first;  // packed: first unit of each sequence [nseq + 1]
   const int* owner;  // packed: sequence of each unit [cap] (-1: none)
   int nseq, T, unit, per, cap;
+  const int* order;  // packed, or nullptr: the units, longest first [cap]
 };
+// Unit that the i-th group of blocks takes. Blocks start in order, so the long units do not
+// stand behind the short ones.
+__device__ __forceinline__ int lin_nth(const LinMap& m, int i) { return m.order ? m.order[i] : i; }
+
 struct LinUnit {
   int seq, row, len;  // its sequence, first row and tokens
   int at, n;          // its index in the sequence and the sequence's units
@@ -99,8 +104,10 @@ struct LinCall {
   cudaStream_t st;
 };
 
-// Writes the tables of a packed call; the status word: DEV_OK or DEV_BAD_CU_SEQLENS.
-cudaError_t lin_plan(const LinMap& m, int* first, int* owner, int* status, cudaStream_t st);
+// Writes the tables of a packed call (order: units of at most 64 times `chunk` tokens, or
+// nullptr); the status word: DEV_OK or DEV_BAD_CU_SEQLENS.
+cudaError_t lin_plan(const LinMap& m, int* first, int* owner, int* order, int chunk, int* status,
+                     cudaStream_t st);
 
 // In place over the units of a sequence, D[unit, H, dk, dv] with the units' decays
 // whole[unit, H]: D becomes the state before each unit; with `back` also E the gradient

@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   constexpr uint32_t D0 = 0, Y0 = 256;  // two accumulators, two operands of two parts
   chain();
   if (clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = DEV_OK;
-  const int unit = blockIdx.x / a.H, h = blockIdx.x - unit * a.H;
+  const int nth = blockIdx.x / a.H, h = blockIdx.x - nth * a.H, unit = lin_nth(a.m, nth);
   LinUnit u;
   if (!lin_unit(a.m, unit, u)) return;
   if (u.at == (REV ? 0 : u.n - 1)) return;
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   constexpr uint32_t P0 = 0, O0 = 128, Y0 = 256, D0 = 384;
   chain();
   if (clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = DEV_OK;
-  const int unit = blockIdx.x / a.H, h = blockIdx.x - unit * a.H;
+  const int nth = blockIdx.x / a.H, h = blockIdx.x - nth * a.H, unit = lin_nth(a.m, nth);
   LinUnit u;
   if (!lin_unit(a.m, unit, u)) return;
   const Who t = who();
@@ -1064,7 +1064,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   // chunk; G1: products with R for dk; G2: R's sum, then products with R for dv
   constexpr uint32_t A1 = 0, A2 = 128, G1 = 256, G2 = 384;
   chain();
-  const int unit = blockIdx.x / a.H, h = blockIdx.x - unit * a.H;
+  const int nth = blockIdx.x / a.H, h = blockIdx.x - nth * a.H, unit = lin_nth(a.m, nth);
   const size_t uh = (size_t)unit * a.H + h;
   LinUnit u;
   if (!lin_unit(a.m, unit, u)) {
@@ -1482,12 +1482,12 @@ __global__ void __launch_bounds__(P_NTHR, 1)
 // for the GPU's SMs, each as long as a unit (plus about a chunk to start); more than one
 // unit of a sequence also needs the units' own sums (y and z only: half a chunk's time)
 // and the scan.
-constexpr int SMS = 152;
+constexpr int SMS = 152, MOST_CHUNKS = 64;
 int unit_chunks(const gdn_lin_shape& s, bool packed) {
   const long long nc = std::max(1, (s.T + TC - 1) / TC);
-  if (packed) {  // the lengths are known on the device only: some waves of equal units
+  if (packed) {  // the lengths are known on the device only: no unit longer than an SM's share
     const long long all = (nc + s.nseq / 2) * s.H;
-    return (int)std::min(64ll, std::max(4ll, (all + SMS * 2 - 1) / (SMS * 2)));
+    return (int)std::min((long long)MOST_CHUNKS, std::max(4ll, (all + SMS - 1) / SMS));
   }
   const long long chains = (long long)s.nseq * s.H;
   double best = 1e300;
@@ -1509,7 +1509,7 @@ struct TcPlan {
   LinMap m;
   int chunks;
   bool many;  // a sequence may have several units
-  int *status, *first, *owner;
+  int *status, *first, *owner, *order;
   float *whole[2], *dgsum, *D, *E, *S_end, *far;
   size_t bytes;
 };
@@ -1529,6 +1529,7 @@ TcPlan tc_plan(const gdn_lin_shape& s, const int* cu, bool packed, bool back, un
   p.status = (int*)take(4);
   p.first = (int*)take(packed ? (size_t)(s.nseq + 1) * 4 : 0);
   p.owner = (int*)take(packed ? (size_t)p.m.cap * 4 : 0);
+  p.order = (int*)take(packed ? (size_t)p.m.cap * 4 : 0);
   p.whole[0] = (float*)take(uh * 4);
   p.D = (float*)take(p.many ? uh * one : 0);
   if (back) {
@@ -1540,6 +1541,7 @@ TcPlan tc_plan(const gdn_lin_shape& s, const int* cu, bool packed, bool back, un
   }
   p.m.first = p.first;
   p.m.owner = p.owner;
+  p.m.order = packed ? p.order : nullptr;
   p.bytes = at;
   return p;
 }
@@ -1586,7 +1588,7 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   } else if ((e = out_map(&mo, c.o, s, DV))) {
     return e;
   }
-  if (c.cu && (e = lin_plan(p.m, p.first, p.owner, p.status, c.st))) return e;
+  if (c.cu && (e = lin_plan(p.m, p.first, p.owner, p.order, TC, p.status, c.st))) return e;
   bool clear = !c.cu;  // the first kernel of an unpacked call resets the status word
   const dim3 grid(p.m.cap * s.H);
   auto go = [&](auto kernel, cudaError_t ready, uint32_t smem, int threads, auto... rest) {
