@@ -60,6 +60,27 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 // 16 lanes x 16 columns as ldmatrix leaves them: in register 2 k + j thread i has lane
 // 8 j + i / 4, column 4 k + i % 4.
 __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) {
@@ -339,8 +360,10 @@ __device__ __forceinline__ __nv_bfloat162 bf2(uint32_t x) {
   return *reinterpret_cast<__nv_bfloat162*>(&x);
 }
 // The weighted transpose of a warp's 32 columns of a tile (64 tokens) into tensor memory,
-// an operand with the tokens as reduced dimension: first parts at `to`, rests at `rest`. With y a value and w = wh + wl its weight, hi = y wh rounded, and y wh - hi + y wl is
+// an operand with the tokens as reduced dimension, 32 of them STEP columns apart: first parts
+// at `to`, rests at `rest`. With y a value and w = wh + wl its weight, hi = y wh rounded, and y wh - hi + y wl is
 // the rest: fused multiply-adds of pairs, the first difference exact.
+template <int STEP = 16>
 __device__ __forceinline__ void weigh(const unsigned char* tile, const Who& t, const Weights& w,
                                       int len, uint32_t to, uint32_t rest) {
   const uint32_t base = smem_u32(tile) + (t.q4 >> 1) * HALF_TILE;
@@ -370,8 +393,8 @@ __device__ __forceinline__ void weigh(const unsigned char* tile, const Who& t, c
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {  // 16 lanes
-      tmem_st_frag(to + (16u * j << 16) + 32 * t.cg + 16 * g, hi[j]);
-      tmem_st_frag(rest + (16u * j << 16) + 32 * t.cg + 16 * g, lo[j]);
+      tmem_st_frag(to + (16u * j << 16) + STEP * (2 * t.cg + g), hi[j]);
+      tmem_st_frag(rest + (16u * j << 16) + STEP * (2 * t.cg + g), lo[j]);
     }
   }
 }
@@ -802,22 +825,24 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         }
         tmem_st16(tl + P0 + 32 * t.cg + 16 * j, p);
       }
+      // this thread's part of q's row, and of the next chunk's into the L2
+      uint4 qr[DQ ? N / 8 : 1];
+      if (DQ) {
+        const bf* from = q + (size_t)row * ldq + (size_t)h * DZ + N * t.cg;
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) {
+          qr[j] = make_uint4(0, 0, 0, 0);
+          if (on) qr[j] = reinterpret_cast<const uint4*>(from)[j];
+        }
+        if ((c + 1) * TC + t.lane < u.len)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(from + (size_t)TC * ldq));
+      }
       mbar_wait(bar_s, ph, abort);
       tc_fence_after();
       const float up = v.far[t.lane];
       float f = 0.f;  // q_t . (far part of dq_t)
-#pragma unroll 1
+#pragma unroll(DQ ? 2 : 1)
       for (int i = 0; i < N; i += 32) {
-        uint4 qr[DQ ? 4 : 1];
-        if (DQ) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            qr[j] = make_uint4(0, 0, 0, 0);
-            if (on)
-              qr[j] = *reinterpret_cast<const uint4*>(q + (size_t)row * ldq + (size_t)h * DZ +
-                                                      N * t.cg + i + 8 * j);
-          }
-        }
         float o[32];
         tmem_ld32(tl + O0 + N * t.cg + i, o);
 #pragma unroll
@@ -826,7 +851,8 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         if (DQ) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t w4[4] = {qr[j].x, qr[j].y, qr[j].z, qr[j].w};
+            const uint4 y = qr[i / 8 + j];
+            const uint32_t w4[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               f = fmaf(__uint_as_float(w4[e] << 16), o[8 * j + 2 * e], f);
@@ -1031,15 +1057,16 @@ struct BackSm {
   static constexpr uint32_t SLOT = slot_bytes(DK, DV), STATE = DK * DV * 2, HALF_R = DK * 128;
   static constexpr uint32_t R_HI = 4 * SLOT, R_LO = R_HI + STATE, VEC = R_LO + STATE;
   static constexpr uint32_t ROWS = VEC + 2 * sizeof(Vec), COLS = ROWS + 4 * TC * 4,
-                            FAR = COLS + 2 * TC * 4, RED = FAR + 2 * TC * 4;
+                            FAR = COLS + 4 * TC * 4, RED = FAR + 2 * TC * 4;
   static constexpr uint32_t OUT = (RED + 64 + 511) / 512 * 512, BAR = OUT + 8 * STAGE;
   static constexpr uint32_t BYTES = BAR + 256 + 1024;
 };
-// x[0..15] summed over the warp's lanes; lanes j and j + 16 return the sum of x[j].
+// x[0..W-1] summed over the warp's lanes; lane j < W returns the sum of x[j].
+template <int W>
 __device__ __forceinline__ float lane_columns(float* x) {
   const int l = threadIdx.x & 31;
 #pragma unroll
-  for (int o = 8, n = 8; o >= 1; o >>= 1, n >>= 1) {
+  for (int o = W / 2, n = W / 2; o >= 1; o >>= 1, n >>= 1) {
     const bool up = (l & o) != 0;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
@@ -1047,7 +1074,68 @@ __device__ __forceinline__ float lane_columns(float* x) {
       x[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
     }
   }
-  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
+#pragma unroll
+  for (int o = 16; o >= W; o >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], o);
+  return x[0];
+}
+// This thread's row s of k q^T and v dO^T at the 32 columns t of block blk, W at a time: as
+// masked P1 and P2 in bf16 pairs over the first half of the same columns. Returns the row's
+// sum of A, and leaves the columns' sums over the warp in rows[0..31].
+template <int W>
+__device__ __forceinline__ float mask_block(uint32_t a1, uint32_t a2, const Vec& v, int blk, const Who& t,
+                                            float scale, float* rows) {
+  const bool diag = blk == t.q4, direct = diag && !v.mild[blk];
+  const float tb = scale * (diag ? v.own[t.lane] : v.tab[blk - 1][t.lane]);
+  float gh = 0.f, gl = 0.f, cs = 0.f;
+  if (direct) gh = v.hi[t.lane], gl = v.lo[t.lane];
+  a1 += 32 * blk;
+  a2 += 32 * blk;
+#pragma unroll 1
+  for (int g = 0; g < 32; g += W) {
+    float x[W], y[W];
+    uint32_t p1[W / 2], p2[W / 2];
+    if (W == 16) {
+      tmem_ld16(a1 + g, x);
+      tmem_ld16(a2 + g, y);
+    } else {
+      tmem_ld8(a1 + g, x);
+      tmem_ld8(a2 + g, y);
+    }
+#pragma unroll
+    for (int e = 0; e < W; e += 2) {
+      const int col = 32 * blk + g + e;
+      const float2 f2 = *reinterpret_cast<const float2*>(v.row + col);
+      float f[2] = {tb * f2.x, tb * f2.y};
+      if (direct) {
+        const float2 h2 = *reinterpret_cast<const float2*>(v.hi + col);
+        const float2 l2 = *reinterpret_cast<const float2*>(v.lo + col);
+        f[0] = scale * __expf((h2.x - gh) + (l2.x - gl));
+        f[1] = scale * __expf((h2.y - gh) + (l2.y - gl));
+      }
+      float px[2], py[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const bool in = !diag || g + e + z >= t.l;
+        px[z] = in ? x[e + z] * f[z] : 0.f;
+        py[z] = in ? y[e + z] * f[z] : 0.f;
+        const float pair = !diag || g + e + z > t.l ? x[e + z] * py[z] : 0.f;
+        x[e + z] = pair;
+        cs += pair;
+      }
+      p1[e / 2] = pack2bf(px[0], px[1]);
+      p2[e / 2] = pack2bf(py[0], py[1]);
+    }
+    if (W == 16) {
+      tmem_st8(a1 + g / 2, p1);
+      tmem_st8(a2 + g / 2, p2);
+    } else {
+      tmem_st4(a1 + g / 2, p1);
+      tmem_st4(a2 + g / 2, p2);
+    }
+    const float sum = lane_columns<W>(x);
+    if (t.l < W) rows[g + t.l] = sum;
+  }
+  return cs;
 }
 
 template <int DK, int DV>
@@ -1060,8 +1148,8 @@ __global__ void __launch_bounds__(P_NTHR, 1)
                   const __grid_constant__ CUtensorMap mdv) {
   using L = BackSm<DK, DV>;
   constexpr int NK = DK / 2, NV = DV / 2;
-  // A1: k q^T, then P1; A2: v dO^T, then P2; both upper halves: the weighed q of the next
-  // chunk; G1: products with R for dk; G2: R's sum, then products with R for dv
+  // A1: k q^T, then P1 in the first half of every 32 columns; A2: v dO^T, then P2; the second
+  // halves: the weighed q of the next chunk; G1: products with R for dk; G2: R's sum, then products with R for dv
   constexpr uint32_t A1 = 0, A2 = 128, G1 = 256, G2 = 384;
   chain();
   const int nth = blockIdx.x / a.H, h = blockIdx.x - nth * a.H, unit = lin_nth(a.m, nth);
@@ -1077,16 +1165,16 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   unsigned char *r_hi = sb + L::R_HI, *r_lo = sb + L::R_LO;
   Vec* vec = reinterpret_cast<Vec*>(sb + L::VEC);
   float* rows = reinterpret_cast<float*>(sb + L::ROWS);  // [lane quarter][t]
-  float* cols = reinterpret_cast<float*>(sb + L::COLS);  // [column group][s]
+  float* cols = reinterpret_cast<float*>(sb + L::COLS);  // [team and column group][s]
   float* farb = reinterpret_cast<float*>(sb + L::FAR);   // [column group][s]
   float* red = reinterpret_cast<float*>(sb + L::RED);
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [4] v, k, q, dO
   // MMAs: R's sum, k q^T and v dO^T, products with R, results; decay factors are there [2]
   uint64_t *bar_e = full + 4, *bar_a = full + 5, *bar_f = full + 6, *bar_c = full + 7, *ev_v = full + 8;
-  // events of a team: q weighed; R's sum added; products with R scaled; R's tiles written; P1
-  // and P2 written; results read; of both: decay factors used [2]
-  uint64_t *ev_q = full + 10, *ev_g = full + 11, *ev_x = full + 12, *ev_r = full + 13, *ev_p = full + 14,
-           *ev_o = full + 15, *ev_u = full + 16;
+  // events of a team: q weighed; R's sum added; products with R scaled; R's tiles written;
+  // results read; of both: P1 and P2 written; decay factors used [2]
+  uint64_t *ev_q = full + 10, *ev_g = full + 11, *ev_x = full + 12, *ev_r = full + 13, *ev_o = full + 14,
+           *ev_p = full + 15, *ev_u = full + 16;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 18);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   // what the issuing thread has seen done: A, products with R, results; events ev_x, ev_p, ev_r
@@ -1102,7 +1190,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   const bool decs = t.w >= P_DEC && t.w < P_DEC + DEC_WARPS;
   Raw ahead = {};  // of the first chunk to be taken, as above
   if (decs && nch) ahead = raw(0);
-  const uint32_t tm = set_up(t, P_CTL, full, 10, 2, 6, 2, tslot, abort);
+  const uint32_t tm = set_up(t, P_CTL, full, 10, 2, 5, 3, tslot, abort);
   const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
   const size_t sh = ((size_t)u.seq * a.H + h) * DK * DV;
   const bool last = u.at == u.n - 1;
@@ -1112,63 +1200,18 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       const int c = nch - 1 - i, len = min(TC, u.len - c * TC), ph = i & 1;
       const Vec& v = vec[ph];
       mbar_wait(ev_v + ph, (i >> 1) & 1, abort);
-      const float gh = v.hi[t.lane], gl = v.lo[t.lane];
       mbar_wait(bar_a, ph, abort);
       tc_fence_after();
-      // this thread's row s, columns t in [64 cg, 64 cg + 64), 16 at a time; in place as above
       float cs = 0.f;
-#pragma unroll 1
-      for (int j = 0; j < 2; ++j) {
-        const int blk = 2 * t.cg + j;
-        uint32_t p1[16], p2[16];
-        if (blk < t.q4) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) p1[e] = p2[e] = 0;
-          rows[t.q4 * TC + 32 * blk + t.l] = 0.f;
-        } else {
-          const bool diag = blk == t.q4;
-          const float tb = a.scale * (diag ? v.own[t.lane] : v.tab[blk - 1][t.lane]);
-          const bool direct = diag && !v.mild[blk];
-#pragma unroll
-          for (int g = 0; g < 32; g += 16) {
-            float x[16], y[16];
-            tmem_ld16(tl + A1 + 32 * blk + g, x);
-            tmem_ld16(tl + A2 + 32 * blk + g, y);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float2 f2 = *reinterpret_cast<const float2*>(v.row + 32 * blk + g + e);
-              float f[2] = {tb * f2.x, tb * f2.y};
-              if (direct) {
-                const float2 h2 = *reinterpret_cast<const float2*>(v.hi + 32 * blk + g + e);
-                const float2 l2 = *reinterpret_cast<const float2*>(v.lo + 32 * blk + g + e);
-                f[0] = a.scale * __expf((h2.x - gh) + (l2.x - gl));
-                f[1] = a.scale * __expf((h2.y - gh) + (l2.y - gl));
-              }
-              float px[2], py[2];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const bool in = !diag || g + e + z >= t.l;
-                px[z] = in ? x[e + z] * f[z] : 0.f;
-                py[z] = in ? y[e + z] * f[z] : 0.f;
-                const float pair = !diag || g + e + z > t.l ? x[e + z] * py[z] : 0.f;
-                x[e + z] = pair;
-                cs += pair;
-              }
-              p1[(g + e) / 2] = pack2bf(px[0], px[1]);
-              p2[(g + e) / 2] = pack2bf(py[0], py[1]);
-            }
-            const float sum = lane_columns(x);
-            if (t.l < 16) rows[t.q4 * TC + 32 * blk + g + t.l] = sum;
-          }
+      if (t.q4 + t.cg < 4)
+        cs = mask_block<16>(tl + A1, tl + A2, v, t.q4 + t.cg, t, a.scale, rows + t.q4 * TC + 32 * (t.q4 + t.cg));
+      if (t.cg == 1 || t.q4 == 3)  // nothing in the blocks before the diagonal
+        for (int b = t.cg == 1 ? 0 : 2; b < (t.cg == 1 && t.q4 == 3 ? 2 : t.q4); ++b) {
+          const uint32_t none[16] = {};
+          tmem_st16(tl + A1 + 32 * b, none);
+          tmem_st16(tl + A2 + 32 * b, none);
+          rows[t.q4 * TC + 32 * b + t.l] = 0.f;
         }
-        if (j != t.cg) {
-          tc_fence_before();
-          named_bar(2 + t.q4, 64);
-          tc_fence_after();
-        }
-        tmem_st16(tl + A1 + 32 * t.cg + 16 * j, p1);
-        tmem_st16(tl + A2 + 32 * t.cg + 16 * j, p2);
-      }
       cols[t.cg * TC + t.lane] = cs;
       tmem_st_wait();
       warp_done<false>(ev_p);
@@ -1237,7 +1280,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       if (i) mbar_wait(ev_p, ph ^ 1, abort);  // the products have been read
       tc_fence_after();
       if (t.lane < DK) {
-        weigh(slot(2, i), t, v.w, len, tl + A1 + 64, tl + A2 + 64);
+        weigh<32>(slot(2, i), t, v.w, len, tl + A1 + 16, tl + A2 + 16);
         tmem_st_wait();
       }
       warp_done<true>(ev_q);
@@ -1245,6 +1288,17 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       tc_fence_after();
       if (t.lane < DK) add_state<NV>(tl + G2 + NV * t.cg, v.w.whole, r);
       warp_done<false>(ev_g);
+      // the third and fourth block behind the diagonal: the first lane quarters have most of P
+      mbar_wait(bar_a, ph, abort);
+      tc_fence_after();
+      float cs = 0.f;
+      if (t.q4 + t.cg < 2) {
+        const int blk = t.q4 + t.cg + 2;
+        cs = mask_block<8>(tl + A1, tl + A2, v, blk, t, a.scale, rows + t.q4 * TC + 32 * blk);
+        tmem_st_wait();
+      }
+      cols[(2 + t.cg) * TC + t.lane] = cs;
+      warp_done<false>(ev_p);
       const float down = v.far[t.lane];
       mbar_wait(bar_f, ph, abort);
       tc_fence_after();
@@ -1339,7 +1393,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
           if (e < len) {
             f = fa[j];
             rw = (rows[e] + rows[TC + e]) + (rows[2 * TC + e] + rows[3 * TC + e]);
-            cl = cols[e] + cols[TC + e];
+            cl = (cols[e] + cols[TC + e]) + (cols[2 * TC + e] + cols[3 * TC + e]);
             bb = farb[e] + farb[TC + e];
           }
           ab += f - bb;
@@ -1382,6 +1436,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         }
       };
       auto have = [&](int kind, int i) { return mbar_test(full + kind, i & 1); };
+      auto at16 = [](int kk) { return 32 * (kk >> 1) + 8 * (kk & 1); };  // columns of a step of P
       long long t0 = clock64();
       while (bc < nch && !*abort) {
         see(bar_c, bc, cc, 2);
@@ -1400,10 +1455,10 @@ __global__ void __launch_bounds__(P_NTHR, 1)
           const uint32_t sq = smem_u32(slot(2, cc)), so = smem_u32(slot(3, cc));
 #pragma unroll
           for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + G1, tm + A2 + 8 * kk, mnmaj(sq, HALF_TILE, kk), umma_idesc(128, DK, 0, 1), true);
+            umma_ts(tm + G1, tm + A2 + at16(kk), mnmaj(sq, HALF_TILE, kk), umma_idesc(128, DK, 0, 1), true);
 #pragma unroll
           for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + G2, tm + A1 + 8 * kk, mnmaj(so, HALF_TILE, kk), umma_idesc(128, DV, 0, 1), true);
+            umma_ts(tm + G2, tm + A1 + at16(kk), mnmaj(so, HALF_TILE, kk), umma_idesc(128, DV, 0, 1), true);
           umma_commit(bar_c);
           ++cc;
           idle = false;
@@ -1416,7 +1471,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int kk = 0; kk < TC / 16; ++kk)
-              umma_ts(tm + G2, tm + (p ? A2 : A1) + 64 + 8 * kk, mnmaj(so, HALF_TILE, kk),
+              umma_ts(tm + G2, tm + (p ? A2 : A1) + 16 + at16(kk), mnmaj(so, HALF_TILE, kk),
                       umma_idesc(128, DV, 0, 1), p || kk);
           umma_commit(bar_e);
           ++ce;
