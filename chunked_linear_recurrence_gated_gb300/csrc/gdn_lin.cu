@@ -33,7 +33,7 @@ constexpr int LP = 4;     // floats between rows: both ways to read a fragment (
 
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;  // keeps a NaN, which hi does not
 }
 
 // C += A B by one warp: 16 rows, NT x 8 columns, K deep; a(m, k) and b(k, n) give the
@@ -52,9 +52,14 @@ __device__ __forceinline__ void mm(float (*c)[4], FA a, FB b) {
       uint32_t bh[2], bl[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_tf32(b(k0 + t + 4 * i, 8 * j + g), bh[i], bl[i]);
-      mma_tf32(c[j], al, bh[0], bh[1]);
-      mma_tf32(c[j], ah, bl[0], bl[1]);
-      mma_tf32(c[j], ah, bh[0], bh[1]);
+      // 8 products at a time in the tensor core, whose sums drop what does not fit; the rest of
+      // the sum is rounded (error of a 128-term product 4 times smaller, time the same)
+      float d[4] = {};
+      mma_tf32(d, al, bh[0], bh[1]);
+      mma_tf32(d, ah, bl[0], bl[1]);
+      mma_tf32(d, ah, bh[0], bh[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[j][i] += d[i];
     }
   }
 }

@@ -550,3 +550,169 @@ def test_layer_over_a_prompt_and_token_by_token(dtype):
     err = np.abs(np64(torch.cat(outs, 1)) - ref)
     assert err.max() <= by * np.abs(ref).max()
     assert np.abs(np64(S) - rS).max() <= by * np.abs(rS).max()
+
+
+# --------------------------------------------------------- large and unusual calls
+def wide_check(x, cu=None, scale=0.1):
+    """A bf16 call too large for the oracle, against the fp32 kernels (held to the oracle
+    above, 2^-17 A) on the same values, with A from the magnitudes by the same kernels."""
+    d = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    f = {i: None if x[i] is None else x[i].float() for i in ("q", "k", "v", "g", "S", "do", "dS")}
+    m = {i: t if i == "g" or t is None else t.abs() for i, t in f.items()}
+
+    def both(a):
+        b = [a[i] for i in ("q", "k", "v", "g", "S")]
+        return (gdn.gdn_lin_fwd(*b, scale=scale, cu_seqlens=d),
+                gdn.gdn_lin_bwd(*b, a["do"], a["dS"], scale=scale, cu_seqlens=d))
+
+    (o, S), (dq, dk, dv, dg, dS) = both(x)
+    (ro, rS), ref = both(f)
+    (ao, aS), mag = both(m)
+    for name, got, want, a, e in (("o", o, ro, ao, HALF), ("S", S, rS, aS, 3 * 2.0 ** -16),
+                                  ("dq", dq, ref[0], mag[0], HALF), ("dk", dk, ref[1], mag[1], HALF),
+                                  ("dv", dv, ref[2], mag[2], HALF),
+                                  ("dS", dS, ref[4], mag[4], 3 * 2.0 ** -16)):
+        tol = (e + 2.0 ** -16) * a + 1e-30 + (HALF * want.abs() if got.dtype == torch.bfloat16 else 0.0)
+        off = (got.float() - want).abs() - tol
+        assert not (off > 0).any() and not off.isnan().any(), (name, off.max())
+    # dg sums the chunk's pairs: as dg_tol, over blocks of 128 tokens on either side
+    near = torch.nn.functional.max_pool1d(mag[3].transpose(1, 2), 257, 1, 128).transpose(1, 2)
+    off = (dg.float() - ref[3]).abs() - ((HALF + 2.0 ** -16) * near + HALF * ref[3].abs() + 1e-30)
+    assert not (off > 0).any() and not off.isnan().any(), ("dg", off.max())
+
+
+@pytest.mark.parametrize("B,T,H,dk,dv,decay", [(1, 20000, 5, 128, 128, "weak"), (2, 3333, 40, 64, 128, "mid"),
+                                               (9, 1025, 17, 128, 64, "mixed"), (160, 129, 2, 64, 64, "weak")])
+def test_lin_large(B, T, H, dk, dv, decay):
+    wide_check(lin_inputs(B, T, H, dk, dv, torch.bfloat16, decay, seed=T))
+
+
+@pytest.mark.parametrize("case", ["many short", "one long", "units of the most chunks"])
+def test_lin_packed_large(case):
+    rng = np.random.default_rng(3)
+    if case == "many short":  # more sequences than the planning block has threads, empty ones too
+        lens, H = np.concatenate([rng.integers(0, 9, 2500), [700, 0, 1]]), 2
+        rng.shuffle(lens)
+    elif case == "one long":
+        lens, H = np.array([0, 5, 9000, 128, 0]), 3
+    else:
+        lens, H = np.array([8300, 300, 40]), 170
+    cu = [2] + (2 + np.cumsum(lens)).tolist()
+    x = lin_inputs(1, cu[-1] + 3, H, 64, 64, torch.bfloat16, "weak", seed=4, nseq=len(lens))
+    for i in "qkvg":  # rows of no sequence: the fp32 call leaves them unwritten too
+        x[i] = x[i].contiguous()
+    d = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o = torch.zeros_like(x["v"])
+    a = [x[i] for i in "qkvg"]
+    _, S = gdn.gdn_lin_fwd(*a, x["S"], cu_seqlens=d, o=o)
+    f = [t.float() for t in a]
+    ro, ao = (torch.zeros_like(f[2]) for _ in range(2))
+    _, rS = gdn.gdn_lin_fwd(*f, x["S"], cu_seqlens=d, o=ro)
+    _, aS = gdn.gdn_lin_fwd(*(t.abs() for t in f[:3]), f[3], x["S"].abs(), cu_seqlens=d, o=ao)
+    assert ((o.float() - ro).abs() <= (HALF + 2.0 ** -16) * ao + HALF * ro.abs()).all()
+    assert ((S - rS).abs() <= 2.0 ** -14 * aS + 1e-30).all()
+    s = slice(cu[0], cu[-1])
+    got = gdn.gdn_lin_bwd(*a, x["S"], x["do"], x["dS"], cu_seqlens=d)
+    ref = gdn.gdn_lin_bwd(*f, x["S"], x["do"].float(), x["dS"], cu_seqlens=d)
+    mag = gdn.gdn_lin_bwd(*(t.abs() for t in f[:3]), f[3], x["S"].abs(), x["do"].float().abs(),
+                          x["dS"].abs(), cu_seqlens=d)
+    for i in range(3):
+        off = (got[i][:, s].float() - ref[i][:, s]).abs()
+        assert (off <= (HALF + 2.0 ** -16) * mag[i][:, s] + HALF * ref[i][:, s].abs() + 1e-30).all(), i
+    assert ((got[4] - ref[4]).abs() <= 2.0 ** -14 * mag[4] + 1e-30).all()
+    near = torch.nn.functional.max_pool1d(mag[3][:, s].float().transpose(1, 2), 257, 1, 128)
+    off = (got[3][:, s].float() - ref[3][:, s]).abs()
+    assert (off <= (HALF + 2.0 ** -16) * near.transpose(1, 2) + HALF * ref[3][:, s].abs() + 1e-30).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lin_rows_past_32_bits(dtype):
+    """Token rows so far apart that the last ones' offsets pass 2^32 elements."""
+    T, H = 300, 2
+    ld = (1 << 32) // 256 + 64
+    x = lin_inputs(1, T, H, 64, 128, DT[dtype], seed=6)
+    wide = torch.empty(T * ld, dtype=DT[dtype], device="cuda")
+    far = {}
+    at = 0
+    for i in "qkvg":
+        w = x[i].shape[2] * (x[i].shape[3] if i != "g" else 1)
+        far[i] = wide.as_strided(x[i].shape, (T * ld, ld) + x[i].stride()[2:] if i == "g" else
+                                 (T * ld, ld, x[i].shape[3], 1), at)
+        far[i].copy_(x[i])
+        at += -(-w // 8) * 8
+    a, b = [x[i] for i in "qkvg"], [far[i] for i in "qkvg"]
+    for r, w in zip(gdn.gdn_lin_fwd(*b, x["S"]), gdn.gdn_lin_fwd(*a, x["S"])):
+        assert torch.equal(r, w)
+    for r, w in zip(gdn.gdn_lin_bwd(*b, x["S"], x["do"], x["dS"]),
+                    gdn.gdn_lin_bwd(*a, x["S"], x["do"], x["dS"])):
+        assert torch.equal(r, w)
+
+
+def test_lin_broadcast_rows():
+    """One row for all tokens (a stride of zero), which the tiles' copies cannot describe."""
+    x = lin_inputs(1, 200, 2, 64, 64, torch.bfloat16, seed=8)
+    k = x["k"][:, 5:6].expand(-1, 200, -1, -1)
+    assert k.stride(1) == 0
+    x["k"] = k
+    against_oracle(x, scale=0.2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lin_graph_reads_its_offsets_at_replay(dtype):
+    x = lin_inputs(1, 900, 2, 64, 64, DT[dtype], seed=10, nseq=3)
+    a = [x[i] for i in "qkvg"]
+    cu = torch.tensor([0, 100, 300, 900], dtype=torch.int32, device="cuda")
+    run = lambda: (gdn.gdn_lin_fwd(*a, x["S"], cu_seqlens=cu)
+                   + gdn.gdn_lin_bwd(*a, x["S"], x["do"], x["dS"], cu_seqlens=cu))
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for at in ([0, 900, 900, 900], [0, 0, 450, 900], [0, 100, 300, 900]):
+        cu.copy_(torch.tensor(at, dtype=torch.int32))
+        want = run()
+        for t in got:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(i, j) for i, j in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lin_calls_on_two_streams_at_once(dtype):
+    xs = [lin_inputs(1, 3000, 6, 128, 128, DT[dtype], seed=s) for s in (1, 2)]
+    call = lambda x, **kw: (gdn.gdn_lin_fwd(*(x[i] for i in "qkvg"), x["S"], **kw)
+                            + gdn.gdn_lin_bwd(*(x[i] for i in "qkvg"), x["S"], x["do"], x["dS"], **kw))
+    want = [call(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [call(x, stream=s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for w, g in zip(want, got):
+            assert all(torch.equal(i, j) for i, j in zip(w, g))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lin_graphs_that_share_a_workspace(dtype):
+    """Two graphs captured with one workspace, replayed in turn on one stream."""
+    xs = [lin_inputs(1, T, 3, 64, 128, DT[dtype], seed=T) for T in (1500, 400)]
+    args = [[x[i] for i in "qkvg"] + [x["S"]] for x in xs]
+    ws = gdn.alloc_workspace(1 << 27, "cuda")
+    want = [gdn.gdn_lin_fwd(*a) + gdn.gdn_lin_bwd(*a, x["do"], x["dS"]) for a, x in zip(args, xs)]
+    graphs, got = [], []
+    for a, x in zip(args, xs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(gdn.gdn_lin_fwd(*a, workspace=ws)
+                       + gdn.gdn_lin_bwd(*a, x["do"], x["dS"], workspace=ws))
+        graphs.append(g)
+    for n in (0, 1, 1, 0):
+        for t in got[n]:
+            t.fill_(float("nan"))
+        graphs[n].replay()
+        graphs[1 - n].replay()
+    torch.cuda.synchronize()
+    assert gdn.gdn_workspace_status(ws) == 0
+    for w, r in zip(want, got):
+        assert all(torch.equal(i, j) for i, j in zip(w, r))
