@@ -157,6 +157,14 @@ LAYER_KERNELS = {
                                      2 * C * dk * dv + 2 * C * C * (dk + dv)),
     "lin_grad": lambda dk, dv, e, C: (C * (4 * dk + 3 * dv + 2) * e + 8 * dk * dv,
                                       6 * C * dk * dv + 2 * C * C * (3 * dk + 2 * dv)),
+    # bf16: chunks of 128 tokens, states' products in two parts
+    "lin_tc_state": lambda dk, dv, e, C: (C * (dk + dv + 1) * e, 4 * C * dk * dv),
+    "lin_tc_fwd": lambda dk, dv, e, C: (C * (2 * dk + 2 * dv + 1) * e,
+                                        C * (6 * dk * dv + 256 * (dk + dv))),
+    "lin_tc_dq": lambda dk, dv, e, C: (C * ((3 * dk + 2 * dv + 1) * e + 4),
+                                       C * (8 * dk * dv + 256 * (dk + dv))),
+    "lin_tc_back": lambda dk, dv, e, C: (C * ((3 * dk + 3 * dv + 2) * e + 4),
+                                         C * (10 * dk * dv + 512 * (dk + dv))),
 }
 
 
@@ -606,7 +614,7 @@ def op_roofline(w, ms, which="fwd+bwd"):
 KERNEL_PHASE = {"tc_grad": "bwd", "simt_grad": "bwd", "tc_chains_bwd": "bwd",
                 "tc_chain_rev": "bwd", "simt_st_bwd": "bwd",
                 "prep_bwd": "bwd", "gate_norm_bwd": "bwd", "res_norm_bwd": "bwd",
-                "qk_norm_bwd": "bwd", "lin_grad": "bwd"}
+                "qk_norm_bwd": "bwd", "lin_grad": "bwd", "lin_tc_dq": "bwd", "lin_tc_back": "bwd"}
 
 
 def kernel_roofline(name, per_launch_ms, units_per_launch, w, hbm, peak_kind):

@@ -653,8 +653,11 @@ gdn_status check_lin(const gdn_lin_shape* s) {
 
 // A call of one sequence may be packed or not.
 size_t lin_bytes(const gdn_lin_shape& s, bool back) {
-  if (lin_tc_takes(s)) return std::max(lin_tc_bytes(s, true, back), lin_tc_bytes(s, false, back));
-  return std::max(lin_simt_bytes(s, true, back), lin_simt_bytes(s, false, back));
+  size_t most = 0;
+  for (const bool packed : {false, true})
+    if (packed ? s.B == 1 : s.nseq == s.B)
+      most = std::max(most, lin_tc_takes(s) ? lin_tc_bytes(s, packed, back) : lin_simt_bytes(s, packed, back));
+  return most;
 }
 
 gdn_status run(const LinCall& c, size_t ws_bytes, bool back) {

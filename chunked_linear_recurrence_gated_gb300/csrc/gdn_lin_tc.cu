@@ -35,9 +35,9 @@ typedef __nv_bfloat16 bf;
 
 constexpr int TC = 128;          // tokens of a chunk
 constexpr int NEPI = 256;        // 8 warps on the accumulators: 4 lane quarters x 2 column groups
-constexpr int CTL = 8, DEC = 9;  // a warp that copies and issues the MMAs, three for decay factors
-constexpr int NWORK = 384;       // threads of these
-constexpr int NTHR = 384;        // launched: whole warpgroups, for the registers' redistribution
+// The kernel of the units' own sums: these, a warp that copies and issues the MMAs, one for
+// the weights.
+constexpr int CTL = 8, DEC = 9, NTHR = 320;
 constexpr uint32_t HALF_TILE = TC * 128;  // 64 columns of a chunk's rows
 
 // ------------------------------------------------------------------ TMEM access
@@ -287,20 +287,6 @@ __device__ __forceinline__ Who who() {
   t.lane = 32 * t.q4 + t.l;
   return t;
 }
-// Registers of the working warpgroups and of the last one: together within what was launched.
-template <int THREADS>
-struct Regs {
-  static constexpr int LAUNCH = THREADS == 384 ? 168 : 96, EPI = THREADS == 384 ? 216 : 104, CTL = 64;
-  static_assert((THREADS - 128) * EPI + 128 * CTL <= THREADS * LAUNCH, "the pool of the launch");
-};
-template <int THREADS>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(Regs<THREADS>::EPI));
-}
-template <int THREADS>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<THREADS>::CTL));
-}
 // A warp's part of an event is done: its threads' tensor-memory accesses and, with SMEM,
 // their writes of operand tiles.
 template <bool SMEM>
@@ -310,19 +296,8 @@ __device__ __forceinline__ void warp_done(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
-// The working warps meet, with the one for decay factors (ALL) or without it; true if any
-// has seen a wait run out.
-template <bool ALL>
-__device__ __forceinline__ bool meet(volatile int* abort) {
-  uint32_t any;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(any)
-      : "r"(*abort), "n"(ALL ? 1 : 7), "n"(ALL ? NWORK : NWORK - 96)
-      : "memory");
-  return any != 0;
-}
+// The warps of the own sums' kernel meet; true if any has seen a wait run out.
+__device__ __forceinline__ bool meet(volatile int* abort) { return __syncthreads_or(*abort) != 0; }
 
 // What the kernels of a call share.
 struct Args {
@@ -606,7 +581,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       all *= wh;
       tc_fence_before();
     };
-    meet<true>(abort);
+    meet(abort);
     for (int i = 0; i < nch; ++i) {
       const int len = min(TC, u.len - chunk(i) * TC);
       mbar_wait(full + i % ST, (i / ST) & 1, abort);
@@ -619,7 +594,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         fence_proxy_async_smem();
       }
       tc_fence_before();
-      if (meet<true>(abort)) break;
+      if (meet(abort)) break;
       if (i) update(i - 1);
     }
     if (nch) update(nch - 1);
@@ -642,9 +617,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (t.l == 0)
       for (int i = 0; i < min(nch, ST); ++i) load(i);
     __syncwarp();
-    meet<true>(abort);
+    meet(abort);
     for (int i = 0; i < nch; ++i) {
-      if (meet<true>(abort)) break;
+      if (meet(abort)) break;
       if (t.l == 0) {
         tc_fence_after();
         mbar_wait(full + i % ST, (i / ST) & 1, abort);
@@ -669,20 +644,19 @@ __global__ void __launch_bounds__(NTHR, 1)
       sum_decay(r, a.decay != nullptr, hi, lo);
       fill_weights<REV>(hi, lo, a.scale, vec[i & 3]);
     };
-    const bool fills = t.w == DEC;  // the others only meet
-    if (fills) {
+    if (nch) {
       const Raw second = nch > 1 ? raw(1) : Raw{};
       fill(ahead, 0);
       if (nch > 1) fill(second, 1);
       if (nch > 2) ahead = raw(2);
     }
-    meet<true>(abort);
+    meet(abort);
     for (int i = 0; i < nch; ++i) {
-      if (meet<true>(abort)) break;
+      if (meet(abort)) break;
       // two ahead: visible behind the next chunk's meeting; four kept, for the chunk before
       // this one is still to be added
-      if (fills && i + 2 < nch) fill(ahead, i + 2);
-      if (fills && i + 3 < nch) ahead = raw(i + 3);
+      if (i + 2 < nch) fill(ahead, i + 2);
+      if (i + 3 < nch) ahead = raw(i + 3);
     }
   }
   tear_down(t, CTL, full, ST, tm, abort, a.status);
@@ -701,6 +675,15 @@ __global__ void __launch_bounds__(NTHR, 1)
 // which have the least to do with P (on the scheduler of quarter 0 the backward took 588 us
 // instead of 578 for 32768 tokens x 16 heads).
 constexpr int P_LOAD = 16, P_DEC = 17, P_CTL = 19, P_NTHR = 640;
+// Registers of the two teams' warpgroups and of the last one: together within what is launched.
+constexpr int P_REGS = 96, TEAM_REGS = 104, LAST_REGS = 64;
+static_assert((P_NTHR - 128) * TEAM_REGS + 128 * LAST_REGS <= P_NTHR * P_REGS, "the pool of the launch");
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(TEAM_REGS));
+}
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(LAST_REGS));
+}
 constexpr long long WAIT_LIMIT = 1ll << 32;  // cycles without progress (mbar_wait's own limit)
 static_assert(P_DEC + DEC_WARPS == P_CTL && (P_CTL + 1) * 32 == P_NTHR, "the last warpgroup");
 template <int DY, int DZ, bool DQ>
@@ -759,7 +742,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   auto wait_tile = [&](int n) { return mbar_wait(full + n % SL, n / SL & 1, abort); };
   // After a wait that ran out every role goes through its chunks without waiting.
   if (t.w < 8) {  // ---- P and the result
-    more_registers<P_NTHR>();
+    more_registers();
     for (int c = 0; c < nch; ++c) {
       const int len = min(TC, u.len - c * TC), ph = c & 1;
       const Vec& v = vec[ph];
@@ -876,7 +859,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
     }
     if (t.l == 0) bulk_wait_all();
   } else if (t.w < 16) {  // ---- the state
-    more_registers<P_NTHR>();
+    more_registers();
     const size_t sh = ((size_t)u.seq * a.H + h) * DY * DZ, uh = ((size_t)unit * a.H + h) * DY * DZ;
     float s[N];
     // S_out may be S_in: a sequence's last unit writes it at any time, so the first of many
@@ -913,7 +896,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
     }
     if (u.at == u.n - 1 && S_out) store_state<DY, DZ, DQ, N>(S_out + sh, t.lane, N * t.cg, s);
   } else {
-    fewer_registers<P_NTHR>();
+    fewer_registers();
     if (t.w == P_LOAD && t.l == 0) {  // ---- copies
       auto load = [&](int n) {
         const int c = n / 3, kind = n - 3 * c;
@@ -1183,7 +1166,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   const size_t sh = ((size_t)u.seq * a.H + h) * DK * DV;
   const bool last = u.at == u.n - 1;
   if (t.w < 8) {  // ---- masked products and results
-    more_registers<P_NTHR>();
+    more_registers();
     for (int i = 0; i < nch; ++i) {
       const int c = nch - 1 - i, len = min(TC, u.len - c * TC), ph = i & 1;
       const Vec& v = vec[ph];
@@ -1221,7 +1204,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
     }
     if (t.l == 0) bulk_wait_all();
   } else if (t.w < 16) {  // ---- R and the products with it
-    more_registers<P_NTHR>();
+    more_registers();
     float r[NV];
     // dS_in may be dS_out: of many units none reads it
     const bool none = last && !dS_out;
@@ -1331,7 +1314,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
     }
     if (u.at == 0 && dS_in) store_state<DK, DV, false, NV>(dS_in + sh, t.lane, NV * t.cg, r);
   } else {
-    fewer_registers<P_NTHR>();
+    fewer_registers();
     if (t.w == P_LOAD) {  // ---- copies, and dg
       auto load = [&](int kind, int i) {  // a tile of the i-th chunk from the end
         if (i >= nch || *abort || t.l) return;
@@ -1660,14 +1643,14 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   using Back = BackSm<DK, DV>;
   prof_mark(c.st, back ? "lin_tc_dq" : "lin_tc_fwd");
   if (!back)
-    return GO((k_lin_tc_pass<DK, DV, false>), PassKV, Regs<P_NTHR>::LAUNCH, c.S_in, p.D, c.S_out, (bf*)c.o,
+    return GO((k_lin_tc_pass<DK, DV, false>), PassKV, P_REGS, c.S_in, p.D, c.S_out, (bf*)c.o,
               (const bf*)nullptr, 0ll, (float*)nullptr, clear, mq, mk, mv, mo);
-  e = GO((k_lin_tc_pass<DV, DK, true>), PassVK, Regs<P_NTHR>::LAUNCH, c.S_in, p.D,
+  e = GO((k_lin_tc_pass<DV, DK, true>), PassVK, P_REGS, c.S_in, p.D,
          c.dS_out ? p.S_end : (float*)nullptr, (bf*)c.dq, (const bf*)c.q, s.ldq, p.far, clear, mo, mv, mk,
          mdq);
   if (e) return e;
   prof_mark(c.st, "lin_tc_back");
-  e = GO((k_lin_tc_back<DK, DV>), Back, Regs<P_NTHR>::LAUNCH, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
+  e = GO((k_lin_tc_back<DK, DV>), Back, P_REGS, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
          (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo, mdk,
          mdv);
 #undef GO

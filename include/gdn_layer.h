@@ -167,7 +167,7 @@ gdn_status gdn_prep_bwd(const gdn_prep_shape* shape, const void* q, const void* 
  * [rot / 2], finite and below 2^40 in size; pos DEVICE int32 [rows] (NULL: row
  * mod T). qn, kn contiguous: [rows, Hq, d] and [rows, Hk, d] (H = 0), or both
  * [rows, H, d], each head repeated for its H / Hq (H / Hk) heads as gdn_prep_fwd
- * does. Sines and cosines are fp32. */
+ * does. Sines and cosines are fp32 (off by 2^-20 with GDN_DTYPE_BF16). */
 #define GDN_ROPE_HALF 0
 #define GDN_ROPE_PAIRS 1
 

@@ -19,7 +19,18 @@
  *
  * Sums, states and decay factors are fp32. With GDN_DTYPE_F32 products are taken
  * on the tensor cores with each operand as two TF32 parts: operands are held to
- * 2^-23, products good to 2^-21.6 of themselves.
+ * 2^-23, products good to 2^-21.6 of themselves. With GDN_DTYPE_BF16, where rows
+ * lie ld >= H * d apart (others take the fp32 kernels), products of inputs are
+ * exact; what a state receives, and a state in the products that dg is summed
+ * from, is taken as two bf16 parts (3 2^-16 of a term's magnitude, so S_out and
+ * dS_in are good to that of the sums of magnitudes); a masked product (q k^T) L or
+ * (dout v^T) L, and the state in o and dv, is rounded to bf16 once before it meets
+ * its other factor, as the result itself is.
+ *
+ * Whole sequences work on chunks of 64 (fp32) or 128 (bf16) tokens by products with
+ * zeros above the diagonal: a NaN or an infinity in a token reaches the results of
+ * its chunk's earlier tokens too, and an infinite operand may come out as NaN. It
+ * stays within its sequence.
  */
 #ifndef GDN_LIN_H_
 #define GDN_LIN_H_
@@ -55,7 +66,8 @@ typedef struct {
 
 /* Workspace bytes of gdn_lin_fwd (is_bwd = 0) or gdn_lin_bwd (is_bwd = 1); 0 if the
  * shape is invalid or unsupported. 256-byte aligned; not shared by calls that may
- * run at the same time. */
+ * run at the same time. A kernel's wait that ran out is reported by
+ * gdn_workspace_status as GDN_ERR_TIMEOUT. */
 size_t gdn_lin_workspace_bytes(const gdn_lin_shape* shape, int is_bwd);
 
 /* S_in NULL: zero states. S_out NULL: not written; it may be S_in. */

@@ -103,6 +103,19 @@ def test_lin_workspace(lib):
     assert lib.gdn_lin_fwd(None, *[None] * 9, None, 0, None) == 1
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_lin_workspace_of_packed_calls(lib, dtype):
+    """Sized by the tokens and the sequences, not by their product: at most a state, a row of
+    factors and some words for each 64 tokens and each sequence."""
+    s = shape(gdn.gdn_lin_shape, LIN, dict(B=1, T=20001, H=32, nseq=13, dtype=dtype, ldq=4096, ldk=4096,
+                                           ldv=2048, ldg=32))
+    unit = 32 * (128 * 64 * 4 + 1024)
+    for back in (0, 1):
+        assert lib.gdn_lin_workspace_bytes(s, back) <= (1 + back) * (20001 // 64 + 2 * 13 + 1) * unit
+    s = shape(gdn.gdn_lin_shape, LIN, dict(B=2, nseq=3))
+    assert lib.gdn_lin_workspace_bytes(s, 0) == 0  # neither packed nor one for each of the batch
+
+
 QK = dict(rows=7, T=7, Hq=4, Hk=2, H=0, d=128, rot=64, style=0, dtype=1, ldq=512, ldk=256,
           q_scale=1.0, eps=1e-6)
 
