@@ -1529,8 +1529,9 @@ int unit_chunks(const gdn_lin_shape& s, bool packed) {
   const long long chains = (long long)s.nseq * s.H;
   double best = 1e300;
   int per = (int)nc;
-  for (long long n = 1; n <= nc && n <= 256; ++n) {
-    const long long len = (nc + n - 1) / n, units = (nc + len - 1) / len;
+  for (long long n = 1, len = nc; n <= nc && n <= 256; n = (nc - 1) / (len - 1) + 1) {
+    len = (nc + n - 1) / n;  // the next n is the first with a smaller one
+    const long long units = (nc + len - 1) / len;
     const double waves = (double)((chains * units + SMS - 1) / SMS);
     double cost = waves * (len + 1.0);
     if (units > 1) {
@@ -1538,6 +1539,7 @@ int unit_chunks(const gdn_lin_shape& s, bool packed) {
       cost += first * (0.5 * len + 1.0) + 2.0 + 0.0135 * chains * units;
     }
     if (cost < best) best = cost, per = (int)len;
+    if (len == 1) break;
   }
   return per;
 }
