@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(LN_NT, DK + DV == 128 ? 2 : 1)
   if (dg) {
     if (t0 < u.len) stf(dg + (size_t)(u.row + t0) * H + h, d0);
     if (t0 + 1 < u.len) stf(dg + (size_t)(u.row + t0 + 1) * H + h, d1);
-  } else {
+  } else if (dgsum) {  // a call without tokens has neither
     const float sum = lane_sum<32>((t0 < u.len ? d0 : 0.f) + (t0 + 1 < u.len ? d1 : 0.f));
     if (lane == 0) dgsum[uh] = sum;
   }
