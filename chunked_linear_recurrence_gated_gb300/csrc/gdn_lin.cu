@@ -14,8 +14,9 @@
 // and for the decay every pair (s, t) with s < u <= t counts once in dg_u:
 //   dg_u = sum_{s < u <= t} A_ts + sum_{t >= u} a_t + sum_{s < u} b_s + e^{gamma_C} <S, R>,
 //   A = scale (q k^T) (dO v^T) L,  a_t = q_t . (far part of dq_t),  b_s = k_s . (that of dk_s):
-// sums over the chunk only, of terms that all carry the decay between their tokens, so
-// strong decays leave nothing to cancel.
+// sums over the chunk only, of terms that all carry the decay between their tokens. Sums over
+// s < u and over t >= u are formed as such, never as a difference of longer ones, so what lies
+// behind a token's decay leaves no rounding in its dg.
 #include <stdint.h>
 
 #include <algorithm>
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(LN_NT, DK + DV == 128 ? 2 : 1)
   chain();
   extern __shared__ __align__(16) float sm[];
   __shared__ Gamma gm;
-  __shared__ float rows[2][LC], cols[4][LC], far_q[2][LC], far_k[2][LC], cross[LN_NT / 32];
+  __shared__ float rows[LC], cols[4][LC], far_q[2][LC], far_k[2][LC], cross[LN_NT / 32];
   LinUnit u;
   const int h = blockIdx.y, H = gridDim.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t uh = (size_t)blockIdx.x * H + h;
@@ -348,36 +349,51 @@ __global__ void __launch_bounds__(LN_NT, DK + DV == 128 ? 2 : 1)
   {
     constexpr int NT = LC / 16;
     const int n0 = half * (LC / 2);
-    float a[NT][4] = {}, b[NT][4] = {}, rs[2] = {};
+    float a[NT][4] = {}, b[NT][4] = {}, before[2] = {};
     mm<NT, DK>(a, [&](int i, int e) { return q[(m0 + i) * LK + e]; },
                [&](int e, int j) { return k[(n0 + j) * LK + e]; });
     mm<NT, DV>(b, [&](int i, int e) { return d[(m0 + i) * LV + e]; },
                [&](int e, int j) { return v[(n0 + j) * LV + e]; });
+    // Pairs s < u <= t with s in this half of the columns: before = a row's sum over s < u, and
+    // cols [16 rows][u] its sum over the rows t >= u. rows: the first half's whole sums, which
+    // the second half's u are all behind.
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float cs[2] = {};
+      const int u = n0 + 8 * j + 2 * t;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = m0 + g + 8 * (i >> 1), s = n0 + 8 * j + 2 * t + (i & 1);
-        const float f = s <= r ? in.scale * expf(gm.to(r, s)) : 0.f;
-        const float x = s < r ? a[j][i] * b[j][i] * f : 0.f;
-        rs[i >> 1] += x;
-        cs[i & 1] += x;
-        p[r * LL + s] = s <= r ? a[j][i] * f : 0.f;
-        wm[r * LL + s] = s <= r ? b[j][i] * f : 0.f;
+      for (int z = 0; z < 2; ++z) {
+        const int r = m0 + g + 8 * z;
+        float x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int s = u + i;
+          const float f = s <= r ? in.scale * expf(gm.to(r, s)) : 0.f;
+          const float c = a[j][2 * z + i], e = b[j][2 * z + i];
+          x[i] = s < r ? c * e * f : 0.f;
+          p[r * LL + s] = s <= r ? c * f : 0.f;
+          wm[r * LL + s] = s <= r ? e * f : 0.f;
+        }
+        float up = x[0] + x[1];  // of the lanes up to this one
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, up, o, 4);
+          if (t >= o) up += y;
+        }
+        float lanes = __shfl_up_sync(0xffffffffu, up, 1, 4);
+        if (t == 0) lanes = 0.f;
+        if (u <= r) cs[0] += before[z] + lanes;
+        if (u < r) cs[1] += before[z] + (lanes + x[0]);
+        before[z] += __shfl_sync(0xffffffffu, up, 3, 4);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) cs[i] += __shfl_xor_sync(0xffffffffu, cs[i], o);
-        if (g == 0) cols[w / 2][n0 + 8 * j + 2 * t + i] = cs[i];
+        if (g == 0) cols[w / 2][u + i] = cs[i];
       }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float x = lane_sum<4>(rs[i]);
-      if (t == 0) rows[half][m0 + g + 8 * i] = x;
-    }
+    if (half == 0 && t == 0) rows[m0 + g] = before[0], rows[m0 + g + 8] = before[1];
   }
   {
     float x = 0.f;
@@ -462,23 +478,33 @@ __global__ void __launch_bounds__(LN_NT, DK + DV == 128 ? 2 : 1)
 #pragma unroll
   for (int i = 0; i < LN_NT / 32; ++i) x += cross[i];
   x *= expf(gm.to(LC - 1, 0) + gm.hi[0]);
-  // sums from the right of rows - columns + a, from the left of b; lane: rows 2l, 2l + 1
-  float late[2], b[2];
+  // of this lane's tokens u = 2 l, 2 l + 1: pairs of the chunk; a, and pairs across the
+  // halves, over t >= u; b over s < u
+  float near[2], a[2], b[2], far[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = 2 * lane + i;
-    late[i] = rows[0][r] + rows[1][r] + far_q[0][r] + far_q[1][r] -
-              (cols[0][r] + cols[1][r] + cols[2][r] + cols[3][r]);
+    near[i] = (cols[0][r] + cols[1][r]) + (cols[2][r] + cols[3][r]);
+    a[i] = far_q[0][r] + far_q[1][r];
     b[i] = far_k[0][r] + far_k[1][r];
+    far[i] = rows[r];
   }
-  float ls = late[0] + late[1], bs = b[0] + b[1];
+  float as = a[0] + a[1], bs = b[0] + b[1], fs = far[0] + far[1];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float y = __shfl_down_sync(0xffffffffu, ls, o), z = __shfl_up_sync(0xffffffffu, bs, o);
-    if (lane + o < 32) ls += y;
+    const float y = __shfl_down_sync(0xffffffffu, as, o), z = __shfl_up_sync(0xffffffffu, bs, o),
+                f = __shfl_down_sync(0xffffffffu, fs, o);
+    if (lane + o < 32) as += y, fs += f;
     if (lane >= o) bs += z;
   }
-  const float d0 = ls + (bs - b[0] - b[1]) + x, d1 = (ls - late[0]) + (bs - b[1]) + x;
+  // the lanes behind, and before
+  as = __shfl_down_sync(0xffffffffu, as, 1), fs = __shfl_down_sync(0xffffffffu, fs, 1);
+  bs = __shfl_up_sync(0xffffffffu, bs, 1);
+  if (lane == 31) as = fs = 0.f;
+  if (lane == 0) bs = 0.f;
+  const bool second = 2 * lane >= LC / 2;
+  const float d1 = near[1] + (as + a[1]) + (bs + b[0]) + x + (second ? fs + far[1] : 0.f);
+  const float d0 = near[0] + (as + a[1] + a[0]) + bs + x + (second ? fs + far[1] + far[0] : 0.f);
   const int t0 = 2 * lane;
   if (dg) {
     if (t0 < u.len) stf(dg + (size_t)(u.row + t0) * H + h, d0);

@@ -1,10 +1,12 @@
 """Linear attention and the query / key norms (include/gdn_lin.h, gdn_layer.h) in calls that
 lie at the edge of what their headers allow. Inputs and tolerances as in test_gpu_lin_ops."""
+import numpy as np
 import pytest
 import torch
 
 from chunked_linear_recurrence_gated_gb300 import gdn
-from test_gpu_lin_ops import DT, lin_inputs
+from oracle import lin_ops as lo
+from test_gpu_lin_ops import DT, check, host, lin_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +27,60 @@ def test_no_tokens(dtype, packed, decay):
         torch.cuda.synchronize()
         assert torch.equal(r[4], want)
         assert r[3].shape == (x["g"].shape if decay == "mid" else (2,)) and (r[3] == 0).all()
+
+
+# ------------------------------------------------------------------ dg by the token
+# dg_u is the sum, over the pairs s < u <= t, of A_ts = scale (q_t . k_s) (dO_t . v_s) times
+# the decay between them, with the states of the call as a first and a last such token; M_u is
+# that sum of magnitudes, the oracle's on absolute values. Whatever is rounded on the way is a
+# factor of these terms, so dg_u is off by a multiple of M_u, however large terms of other
+# tokens are. fp32: a product of two operands of two TF32 parts, of two such products, decay
+# factors of 2^-21, and states good to 2^-17 of their magnitudes: 2^-16 in all.
+DG_TOL = {"f32": 2.0 ** -16}
+
+
+def dg_inputs(kind, dtype, T, H, dk, dv, cut, seed, decay="weak", nseq=1):
+    """Tokens from `cut` on 1024 times as large in v and dO as those before it."""
+    x = lin_inputs(1, T, H, dk, dv, DT[dtype], decay, seed=seed, nseq=nseq)
+    x["v"][:, cut:] *= 1024
+    x["do"][:, cut:] *= 1024
+    x["dS"] *= 1024
+    if kind != "decays":
+        x["g"][:, cut] = -float("inf")  # a boundary that nothing crosses
+    if kind == "no gradient before":
+        x["do"][:, :cut] = 0
+    return x
+
+
+def dg_check(x, dtype, cu=None, scale=0.2):
+    q, k, v, g, S, do, dS = host(*(x[i] for i in ("q", "k", "v", "g", "S", "do", "dS")))
+    d = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    got = gdn.gdn_lin_bwd(*(x[i] for i in "qkvg"), x["S"], x["do"], x["dS"], scale=scale,
+                          cu_seqlens=d)[3]
+    with np.errstate(invalid="ignore"):
+        ref = lo.lin_bwd(q, k, v, g, S, do, dS, scale, cu)[3]
+        mag = lo.lin_bwd(*map(np.abs, (q, k, v)), g, *map(np.abs, (S, do, dS)), scale, cu)[3]
+    if x["g"].dim() == 1:
+        ref, mag = ref.sum((0, 1)), mag.sum((0, 1))
+    check("dg", got, ref, DG_TOL[dtype] * mag)
+    return got
+
+
+@pytest.mark.parametrize("dtype", sorted(DG_TOL))
+@pytest.mark.parametrize("kind", ["boundary", "no gradient before", "decays"])
+@pytest.mark.parametrize("cut", [40, 64, 300, 511])
+@pytest.mark.parametrize("packed", [False, True])
+def test_dg_beside_larger_tokens(dtype, kind, cut, packed):
+    """Packed: the tokens around the boundary are in one unit of several chunks."""
+    x = dg_inputs(kind, dtype, 700, 2, 64, 64, cut, cut)
+    got = dg_check(x, dtype, [0, 700] if packed else None)
+    if kind == "no gradient before":
+        assert (got[:, :cut + 1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", sorted(DG_TOL))
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("decay", ["none", "mid", "strong", "mixed", "head"])
+def test_dg_of_each_token(dtype, dk, dv, decay):
+    x = dg_inputs("decays", dtype, 500, 2, dk, dv, 390, dk, decay, nseq=3)
+    dg_check(x, dtype, [0, 13, 400, 500])
