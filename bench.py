@@ -161,9 +161,9 @@ LAYER_KERNELS = {
     "lin_tc_state": lambda dk, dv, e, C: (C * (dk + dv + 1) * e, 4 * C * dk * dv),
     "lin_tc_fwd": lambda dk, dv, e, C: (C * (2 * dk + 2 * dv + 1) * e,
                                         C * (6 * dk * dv + 256 * (dk + dv))),
-    "lin_tc_dq": lambda dk, dv, e, C: (C * ((3 * dk + 2 * dv + 1) * e + 4),
+    "lin_tc_dq": lambda dk, dv, e, C: (C * ((3 * dk + 2 * dv + 1) * e + 4 + dk * dv // 32),
                                        C * (8 * dk * dv + 256 * (dk + dv))),
-    "lin_tc_back": lambda dk, dv, e, C: (C * ((3 * dk + 3 * dv + 2) * e + 4),
+    "lin_tc_back": lambda dk, dv, e, C: (C * ((3 * dk + 3 * dv + 2) * e + 4 + dk * dv // 32),
                                          C * (10 * dk * dv + 512 * (dk + dv))),
 }
 

@@ -178,9 +178,9 @@ __global__ void __launch_bounds__(LN_NT)
 // elements are asked for at once (33 units of 64 x 64: 7 us; 16 at once 11).
 constexpr int SC_NT = 128, SC_U = 8;
 __global__ void __launch_bounds__(SC_NT)
-    k_lin_scan(LinMap m, int H, int dk, int dv, LinLayout lay_d, const float* whole_d, float* D,
-               const float* S_in, float* S_out, LinLayout lay_e, const float* whole_e, float* E,
-               const float* dS_out, float* dS_in, bool open, int* status) {
+    k_lin_scan(LinMap m, int H, int dk, int dv, LinLayout lay, const float* whole_d, float* D,
+               const float* S_in, float* S_out, const float* whole_e, float* E, const float* dS_out,
+               float* dS_in, bool open, int* status) {
   chain();
   if (m.cu) {
     if (*status != DEV_OK) return;
@@ -202,15 +202,10 @@ __global__ void __launch_bounds__(SC_NT)
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (from) {
     from += sh * n4 * 4;
-    const LinLayout lay = back ? lay_e : lay_d;
-    if (lay == LIN_ROWS) {
+    if (lay == LIN_ROWS)
       s = reinterpret_cast<const float4*>(from)[e];
-    } else if (lay == LIN_KEYS) {
+    else
       s = *reinterpret_cast<const float4*>(from + (size_t)(e % dk) * dv + e / dk * 4);
-    } else {
-      const float* p = from + (size_t)(e / dv * 4) * dv + e % dv;
-      s = make_float4(p[0], p[dv], p[2 * dv], p[3 * dv]);
-    }
   }
   for (int b0 = 0; b0 < n; b0 += SC_U) {
     float4 d[SC_U];
@@ -659,7 +654,7 @@ cudaError_t run_simt(const LinCall& c, bool back) {
   prof_mark(c.st, "lin_scan");
   e = launch(k_lin_scan, dim3((DK * DV / 4 + SC_NT - 1) / SC_NT, s.nseq * s.H, back ? 2 : 1),
              dim3(SC_NT), 0, c.st, 1, p.m, s.H, DK, DV, LIN_ROWS, p.whole, p.D, c.S_in, c.S_out,
-             LIN_ROWS, p.whole, p.E, c.dS_out, c.dS_in, false, p.status);
+             p.whole, p.E, c.dS_out, c.dS_in, false, p.status);
   if (e) return e;
   prof_mark(c.st, back ? "lin_grad" : "lin_out");
   e = back ? go(k_lin_grad<T, DK, DV>, 2 * (rows_k + rows_v + square), p.D, p.E, (T*)c.dq, (T*)c.dk,
@@ -731,8 +726,8 @@ cudaError_t lin_scan(const LinMap& m, const gdn_lin_shape& s, const float* whole
                      bool back, int* status, cudaStream_t st) {
   prof_mark(st, "lin_scan");
   return launch(k_lin_scan, dim3((s.dk * s.dv / 4 + SC_NT - 1) / SC_NT, s.nseq * s.H, back ? 2 : 1),
-                dim3(SC_NT), 0, st, 1, m, s.H, s.dk, s.dv, back ? LIN_VALUES : LIN_KEYS, whole, D, S_in,
-                (float*)nullptr, LIN_KEYS, whole_e, E, dS_out, (float*)nullptr, true, status);
+                dim3(SC_NT), 0, st, 1, m, s.H, s.dk, s.dv, LIN_KEYS, whole, D, S_in,
+                (float*)nullptr, whole_e, E, dS_out, (float*)nullptr, true, status);
 }
 
 size_t lin_simt_bytes(const gdn_lin_shape& s, bool packed, bool back) {

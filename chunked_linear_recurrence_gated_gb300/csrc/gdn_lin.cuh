@@ -82,9 +82,8 @@ __device__ __forceinline__ Two sum_before(Two x) {
 }
 
 // Layouts of a unit's state [dk][dv] in the workspace: as it is, or so that a warp whose
-// threads have a key's (a value's) row each moves 4 elements of 32 rows in one piece:
-// [dv / 4][dk][4] and [dk / 4][dv][4].
-enum LinLayout { LIN_ROWS, LIN_KEYS, LIN_VALUES };
+// threads have a key's row each moves 4 elements of 32 rows in one piece: [dv / 4][dk][4].
+enum LinLayout { LIN_ROWS, LIN_KEYS };
 
 // What a whole call takes.
 struct LinCall {

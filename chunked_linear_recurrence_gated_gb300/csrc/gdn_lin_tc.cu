@@ -4,9 +4,9 @@
 // One pass over a sequence carries a state through chunks of C = 128 tokens. With x, y,
 // z the rows of three tensors and gamma, L, S, R as in gdn_lin.cu,
 //   out_t = sum_{s <= t} L_ts (x_t . y_s) z_s + e^{gamma_t} x_t S
-//   S <- e^{gamma_C} S + sum_s e^{gamma_C - gamma_s} y_s z_s^T
-// is the forward (x, y, z = q, k, v) and dq (dO, v, k with the state's transpose). dk, dv
-// and dg come from one pass from the end, which carries R.
+//   S <- e^{gamma_C} S + sum_s e^{gamma_C - gamma_s} k_s v_s^T
+// is the forward (x, y, z = q, k, v) and dq (dO, v, k with S^T for S). dk, dv and dg come from
+// one pass from the end, which carries R.
 //
 // A sequence is cut into units of chunks, so that there is a CTA for every SM where
 // there are few sequences and heads: k_lin_tc_state sums each unit's own contribution to
@@ -15,10 +15,10 @@
 //
 // Rounding. Products of inputs are exact in the tensor core's fp32 sums. A state, and a
 // weighted operand of a state's update, is taken as two bf16 parts (2^-17 of itself),
-// because states leave the call in fp32 and because dg is a running difference of sums
-// over whole units; o and dv, which are rounded to bf16 themselves, take a state's first part
-// alone. The masked products P = L x y^T are rounded to bf16 once before they
-// meet z, as their result is when it is stored.
+// because states leave the call in fp32 and because ddecay, which does too, sums products with
+// them; o and dv, which are rounded to bf16 themselves, take a state's first part alone. The
+// masked products P = L x y^T are rounded to bf16 once before they meet z, as their result is
+// when it is stored.
 #include <cuda.h>
 #include <stdint.h>
 
@@ -326,6 +326,16 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int len, int tid)
   for (int i = tid; i < (TC - len) * P; i += NEPI)
     *reinterpret_cast<uint4*>(at8(tile, HALF_TILE, len + i / P, i % P * 8)) = make_uint4(0, 0, 0, 0);
 }
+// dg needs e^{gamma_C} <S, R>, S the state before a chunk and R the gradient of the one behind
+// it, and they are never together: dq leaves S of every chunk where both are more than zeros
+// in the workspace, as units' states.
+__device__ __forceinline__ bool crossed(const LinUnit& u, int c, int nch, bool in, bool out) {
+  return (c > 0 || u.at > 0 || in) && (c < nch - 1 || u.at < u.n - 1 || out);
+}
+// Its index: one more for each chunk, as later sequences start on later rows.
+__device__ __forceinline__ size_t crossing(const LinUnit& u, int c) {
+  return (size_t)((u.row + c * TC) / TC + u.seq);
+}
 __device__ __forceinline__ uint32_t bf2(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ __nv_bfloat162 bf2(uint32_t x) {
   return *reinterpret_cast<__nv_bfloat162*>(&x);
@@ -369,36 +379,25 @@ __device__ __forceinline__ void weigh(const unsigned char* tile, const Who& t, c
     }
   }
 }
-// This thread's N elements (row lane, columns c0..) of a state [DY][DZ], or of one that is
-// kept transposed in memory (TR).
-template <int DY, int DZ, bool TR, int N>
+// This thread's N elements (row lane, columns c0..) of a state [DK][DV].
+template <int DK, int DV, int N>
 __device__ __forceinline__ void load_state(const float* from, int lane, int c0, float* s) {
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] = 0.f;
-  if (!from || lane >= DY) return;
-  if (TR) {
+  if (!from || lane >= DK) return;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = from[(size_t)(c0 + i) * DY + lane];
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(from + (size_t)lane * DZ + c0 + i);
-      s[i] = x.x, s[i + 1] = x.y, s[i + 2] = x.z, s[i + 3] = x.w;
-    }
+  for (int i = 0; i < N; i += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(from + (size_t)lane * DV + c0 + i);
+    s[i] = x.x, s[i + 1] = x.y, s[i + 2] = x.z, s[i + 3] = x.w;
   }
 }
-template <int DY, int DZ, bool TR, int N>
+template <int DK, int DV, int N>
 __device__ __forceinline__ void store_state(float* to, int lane, int c0, const float* s) {
-  if (!to || lane >= DY) return;
-  if (TR) {
+  if (!to || lane >= DK) return;
 #pragma unroll
-    for (int i = 0; i < N; ++i) to[(size_t)(c0 + i) * DY + lane] = s[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      *reinterpret_cast<float4*>(to + (size_t)lane * DZ + c0 + i) =
-          make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
-  }
+  for (int i = 0; i < N; i += 4)
+    *reinterpret_cast<float4*>(to + (size_t)lane * DV + c0 + i) =
+        make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
 }
 // The same of a unit's state in the workspace, [DZ / 4][DY][4]: whole lines for a warp, where
 // rows of DZ would take 32 pieces of 16 bytes (8 thousand cycles for 64 KB).
@@ -540,7 +539,7 @@ struct StateSm {
   static constexpr uint32_t VEC = 2 * STAGES * SLOT, BAR = VEC + 4 * sizeof(Weights);
   static constexpr uint32_t BYTES = BAR + 128 + 1024;
 };
-template <int DY, int DZ, bool REV, bool TR>
+template <int DY, int DZ, bool REV>
 __global__ void __launch_bounds__(NTHR, 1)
     k_lin_tc_state(Args a, float* whole, float* out, bool clear, const __grid_constant__ CUtensorMap my,
                    const __grid_constant__ CUtensorMap mz) {
@@ -668,15 +667,16 @@ __global__ void __launch_bounds__(NTHR, 1)
 // ------------------------------------------------------------------ forward and dq
 // Two teams of 8 warps work on a chunk's accumulators at the same time, each 128 rows x 2
 // groups of columns, and tell the warp that issues the MMAs by events. One takes P = x y^T
-// (masked, in place), scales x S and, once P z is on it, the result; the other weighs y and
+// (masked, in place), scales x S and, once P z is on it, the result; the other weighs k and
 // adds up the state. In one team of either size the two strings of loads, arithmetic and
 // waits stood one behind the other (7 to 10 thousand cycles a chunk).
-//   MMAs: x S (state ready, result read) | P z, the state's sum (P, x S and y ready) | x y^T
+//   MMAs: x S (state ready, result read) | P z, the state's sum (P, x S and k ready) | x y^T
 //   of the next chunk (P z done)
 // The tiles x, y, z take the slots in turn, each as soon as the one before is done with it.
 // Bound by the chain products -> mask -> P z -> result of a chunk, 7.5 thousand cycles: 115 us
 // for the forward of 32768 tokens x 16 heads of 128 (4.6 TB/s; issue 41 %, tensor pipe 36 %),
-// 150 us for dq, whose state's product has two parts.
+// 175 us for dq, whose state's product has two parts and which leaves 64 KB of states a chunk
+// for dg (153 without).
 // The warp that issues the MMAs keeps asking the barriers: beside the warps of lane quarter 3,
 // which have the least to do with P (on the scheduler of quarter 0 the backward took 588 us
 // instead of 578 for 32768 tokens x 16 heads).
@@ -698,7 +698,8 @@ struct PassSm {
   // the forward, without second parts of the state, has room for the next chunk's y ahead of
   // the slot of this one's x
   static constexpr int SLOTS = DQ ? 4 : 5;
-  static constexpr uint32_t SLOT = slot_bytes(DY, DZ), STATE = DY * DZ * 2, HALF_S = DY * 128;
+  static constexpr int DK = DQ ? DZ : DY, DV = DQ ? DY : DZ;
+  static constexpr uint32_t SLOT = slot_bytes(DY, DZ), STATE = DY * DZ * 2, HALF_S = DK * 128;
   static constexpr uint32_t S_HI = SLOTS * SLOT, S_LO = S_HI + STATE, VEC = S_LO + (DQ ? STATE : 0);
   static constexpr uint32_t PART = VEC + 2 * sizeof(Vec), OUT = (PART + 4 * TC * 4 + 511) / 512 * 512;
   static constexpr uint32_t BAR = OUT + 8 * STAGE, BYTES = BAR + 192 + 1024;
@@ -706,12 +707,13 @@ struct PassSm {
 template <int DY, int DZ, bool DQ>
 __global__ void __launch_bounds__(P_NTHR, 1)
     k_lin_tc_pass(Args a, const float* S_in, const float* S_unit, float* S_out, bf* out, const bf* q,
-                  long long ldq, float* far, bool clear, const __grid_constant__ CUtensorMap mx,
-                  const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz,
-                  const __grid_constant__ CUtensorMap mo) {
+                  long long ldq, float* far, float* S_chunk, bool end, bool clear,
+                  const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
+                  const __grid_constant__ CUtensorMap mz, const __grid_constant__ CUtensorMap mo) {
   using L = PassSm<DY, DZ, DQ>;
-  constexpr int SL = L::SLOTS;
-  constexpr int N = DZ / 2;
+  constexpr int SL = L::SLOTS, DK = L::DK, DV = L::DV;
+  constexpr int N = DZ / 2, NS = DV / 2;  // columns of a thread: of the result, of the state
+  constexpr int KEYS = DQ ? 2 : 1, VALUES = 3 - KEYS;  // which of a chunk's tiles are k's and v's
   constexpr uint32_t P0 = 0, O0 = 128, Y0 = 256, D0 = 384;
   chain();
   if (clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = DEV_OK;
@@ -727,13 +729,13 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [SL]
   // MMAs: x y^T, x S, P z, the state's sum; decay factors are there [2 buffers]
   uint64_t *bar_p = full + SL, *bar_s = bar_p + 1, *bar_o = bar_p + 2, *bar_d = bar_p + 3, *ev_v = bar_p + 4;
-  // events of a team: P and x S ready; result read; y weighed; state ready; of both: decay
+  // events of a team: P and x S ready; result read; k weighed; state ready; of both: decay
   // factors used [2]. A barrier's next phase but one always depends on all who wait for it,
   // so nobody can miss a phase.
   uint64_t *ev_p = ev_v + 2, *ev_o = ev_p + 1, *ev_y = ev_p + 2, *ev_s = ev_p + 3, *ev_u = ev_p + 4;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(ev_u + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
-  // what the issuing thread has seen done: P z, the state's sum, x S, x y^T, y weighed
+  // what the issuing thread has seen done: P z, the state's sum, x S, x y^T, k weighed
   volatile int* seen = reinterpret_cast<volatile int*>(tslot + 2);
   const int nch = (u.len + TC - 1) / TC;
   auto raw = [&](int c) {
@@ -867,40 +869,47 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   } else if (t.w < 16) {  // ---- the state
     more_registers();
     const size_t sh = ((size_t)u.seq * a.H + h) * DY * DZ, uh = ((size_t)unit * a.H + h) * DY * DZ;
-    float s[N];
+    float s[NS];
     // S_out may be S_in: a sequence's last unit writes it at any time, so the first of many
     // starts from the scan's copy
     if (u.n > 1)
-      load_unit<DY, N>(S_unit + uh, t.lane, N * t.cg, s);
+      load_unit<DK, NS>(S_unit + uh, t.lane, NS * t.cg, s);
     else
-      load_state<DY, DZ, DQ, N>(S_in ? S_in + sh : nullptr, t.lane, N * t.cg, s);
-    if (t.lane < DY) put_split<N, DQ>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
+      load_state<DK, DV, NS>(S_in ? S_in + sh : nullptr, t.lane, NS * t.cg, s);
+    if (t.lane < DK) put_split<NS, DQ>(s_hi, s_lo, L::HALF_S, t.lane, NS * t.cg, s);
     warp_done<true>(ev_s);
     for (int c = 0; c < nch; ++c) {
       const int len = min(TC, u.len - c * TC), n0 = 3 * c, ph = c & 1;
       const Vec& v = vec[ph];
+      // ahead of the weighing (behind it dq takes 185 us instead of 175 for 32768 x 16 heads)
+      if (DQ && crossed(u, c, nch, S_in, end))
+        store_unit<DK, NS>(S_chunk + (crossing(u, c) * a.H + h) * DK * DV, t.lane, NS * t.cg, s);
       mbar_wait(ev_v + ph, (c >> 1) & 1, abort);
-      wait_tile(n0 + 1);
-      if (t.lane < DY) {
-        weigh(tile(n0 + 1), t, v.w, len, tl + Y0, tl + Y0 + 64);
-        tmem_st_wait();
+      wait_tile(n0 + KEYS);
+      if (len < TC && a.m.cu) {  // rows of the next sequence would meet zeros, which NaN survives
+        wait_tile(n0 + VALUES);
+        zero_rows<DV>(tile(n0 + VALUES), len, t.tid - 256);
+        if (DQ) {
+          zero_rows<DK>(tile(n0 + KEYS), len, t.tid - 256);
+          named_bar(7, 256);
+        }
       }
-      if (len < TC && a.m.cu) {
-        wait_tile(n0 + 2);
-        zero_rows<DZ>(tile(n0 + 2), len, t.tid - 256);
+      if (t.lane < DK) {
+        weigh(tile(n0 + KEYS), t, v.w, len, tl + Y0, tl + Y0 + 64);
+        tmem_st_wait();
       }
       warp_done<true>(ev_y);
       mbar_wait(bar_d, ph, abort);
       tc_fence_after();
-      if (t.lane < DY) {
-        add_state<N>(tl + D0 + N * t.cg, v.w.whole, s);
+      if (t.lane < DK) {
+        add_state<NS>(tl + D0 + NS * t.cg, v.w.whole, s);
         mbar_wait(bar_s, ph, abort);  // x S has read the tiles
-        put_split<N, DQ>(s_hi, s_lo, L::HALF_S, t.lane, N * t.cg, s);
+        put_split<NS, DQ>(s_hi, s_lo, L::HALF_S, t.lane, NS * t.cg, s);
       }
       warp_done<true>(ev_s);
       if (t.l == 0) mbar_arrive(ev_u + ph);
     }
-    if (u.at == u.n - 1 && S_out) store_state<DY, DZ, DQ, N>(S_out + sh, t.lane, N * t.cg, s);
+    if (!DQ && u.at == u.n - 1 && S_out) store_state<DK, DV, NS>(S_out + sh, t.lane, NS * t.cg, s);
   } else {
     fewer_registers();
     if (t.w == P_LOAD && t.l == 0) {  // ---- copies
@@ -920,9 +929,9 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       const long long t0 = clock64();
       for (int n = SL; n < 3 * nch; ++n) {  // tile n - SL, whose slot it takes, is done with
         const int c = (n - SL) / 3, kind = n - SL - 3 * c;
-        while (!*abort && !(kind == 0   ? seen[2] > c && seen[3] > c
-                            : kind == 1 ? seen[3] > c && seen[4] > c
-                                        : seen[0] > c && seen[1] > c)) {
+        while (!*abort && !(kind == 0      ? seen[2] > c && seen[3] > c
+                            : kind == KEYS ? seen[4] > c && seen[DQ ? 0 : 3] > c
+                                           : seen[1] > c && seen[DQ ? 3 : 0] > c)) {
           __nanosleep(40);  // its scheduler is others' too
           if (clock64() - t0 > 64 * WAIT_LIMIT) *abort = 1;  // the issuing thread gives up before
         }
@@ -965,15 +974,15 @@ __global__ void __launch_bounds__(P_NTHR, 1)
           ++cz;
           idle = false;
         }
-        if (cd < cp && cd <= cz && cd == bd && wy > cd && ws > cd && have(3 * cd + 2)) {
+        if (cd < cp && cd <= cz && cd == bd && wy > cd && ws > cd && have(3 * cd + VALUES)) {
           tc_fence_after();
-          const uint32_t z = smem_u32(tile(3 * cd + 2));
+          const uint32_t z = smem_u32(tile(3 * cd + VALUES));
 #pragma unroll 1
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int kk = 0; kk < TC / 16; ++kk)
               umma_ts(tm + D0, tm + Y0 + 64 * p + 8 * kk, mnmaj(z, HALF_TILE, kk),
-                      umma_idesc(128, DZ, 0, 1), p || kk);
+                      umma_idesc(128, DV, 0, 1), p || kk);
           umma_commit(bar_d);
           ++cd;
           idle = false;
@@ -987,15 +996,19 @@ __global__ void __launch_bounds__(P_NTHR, 1)
 #pragma unroll 1
           for (int p = 0; p < (DQ ? 2 : 1); ++p)
 #pragma unroll 4
-            for (int kk = 0; kk < DY / 16; ++kk)
-              umma_bf16(tm + O0, kmaj(x, HALF_TILE, kk), mnmaj(smem_u32(p ? s_lo : s_hi), L::HALF_S, kk),
-                        umma_idesc(128, DZ, 0, 1), p || kk);
+            for (int kk = 0; kk < DY / 16; ++kk) {
+              const uint32_t st = smem_u32(p ? s_lo : s_hi);
+              umma_bf16(tm + O0, kmaj(x, HALF_TILE, kk),
+                        DQ ? kmaj(st, L::HALF_S, kk) : mnmaj(st, L::HALF_S, kk),
+                        umma_idesc(128, DZ, 0, DQ ? 0 : 1), p || kk);
+            }
           umma_commit(bar_s);
           ++cs;
           idle = false;
         }
-        // P of the chunk before has been read
-        if (cp < nch && cp == bp && bz >= cp && have(3 * cp) && have(3 * cp + 1)) {
+        // P of the chunk before has been read (dq: and a tail's y has been zeroed)
+        if (cp < nch && cp == bp && bz >= cp && have(3 * cp) && have(3 * cp + 1) &&
+            (!DQ || !a.m.cu || u.len - cp * TC >= TC || wy > cp)) {
           tc_fence_after();
           const uint32_t x = smem_u32(tile(3 * cp)), y = smem_u32(tile(3 * cp + 1));
 #pragma unroll 4
@@ -1032,20 +1045,26 @@ __global__ void __launch_bounds__(P_NTHR, 1)
 //   e^{gamma_C - gamma_s}); dk = P2 q onto the one, dv = P1 dO onto the other;
 //   R <- e^{gamma_C} R + (weighed q)^T dO.
 // Two teams as above: one takes the masked products and the results, the other weighs q,
-// adds up R, scales the products with R and writes R's next tiles. dg runs along in the warp
-// that issues the copies: with rows and cols the sums of A (gdn_lin.cu) over s and over t,
-//   dg_u = X + sum_{t >= u} (rows_t + a_t - cols_t - b_t),  X' = X + sum_t (a_t - b_t),
-// X = <S, R> behind the chunk, taken from the states themselves at the unit's end.
+// adds up R, scales the products with R and writes R's next tiles. dg is summed in the warp
+// that issues the copies, of every pair s < u <= t of tokens (or states) for itself and never
+// as a difference of longer sums, in which what lies behind a forgotten state would leave its
+// roundings: with b, k the blocks of 32 tokens of t and u,
+//   dg_u = sum_{t >= u} a_t + sum_{s < u} b_s + e^{gamma_C} <S, R>            (gdn_lin.cu)
+//        + pairs in u's block + (s in it, t in later ones) + (s in earlier ones, t in it)
+//        + (s in earlier blocks, t in later ones).
+// <S, R> takes S as dq left it and R from the second team's registers, while R's sum is on its
+// way (by the first team from R's tiles, with warp-level MMAs, the kernel took 280 us instead of
+// 243 for 32768 x 16 heads; by the decay warps 352).
 // Bound by the chain P -> results -> R's sum -> products of the next chunk, 14 thousand cycles
-// of which the MMAs are 7: 224 us for 32768 tokens x 16 heads of 128 (issue 40 %, tensor pipe
-// 32 %; P by one team of the two 280 us).
+// of which the MMAs are 7: 243 us for 32768 tokens x 16 heads of 128 (224 without <S, R>; P by
+// one team of the two 280 us).
 template <int DK, int DV>
 struct BackSm {
   static constexpr int THREADS = P_NTHR;
   static constexpr uint32_t SLOT = slot_bytes(DK, DV), STATE = DK * DV * 2, HALF_R = DK * 128;
   static constexpr uint32_t R_HI = 4 * SLOT, R_LO = R_HI + STATE, VEC = R_LO + STATE;
   static constexpr uint32_t ROWS = VEC + 2 * sizeof(Vec), COLS = ROWS + 4 * TC * 4,
-                            FAR = COLS + 4 * TC * 4, RED = FAR + 2 * TC * 4;
+                            FAR = COLS + 3 * TC * 4, RED = FAR + 2 * TC * 4;
   static constexpr uint32_t OUT = (RED + 64 + 511) / 512 * 512, BAR = OUT + 8 * STAGE;
   static constexpr uint32_t BYTES = BAR + 256 + 1024;
 };
@@ -1067,10 +1086,11 @@ __device__ __forceinline__ float lane_columns(float* x) {
   return x[0];
 }
 // This thread's row s of k q^T and v dO^T at the 32 columns t of block blk: as masked P1 and
-// P2 in bf16 pairs over the first half of the same columns. Returns the row's sum of A, and
-// leaves the columns' sums over the warp in rows[0..31]. 8 columns at a time in a loop that
-// stays rolled, for the instruction cache (16 columns twice unrolled: the kernel takes 250 us
-// instead of 226 for 32768 tokens x 16 heads).
+// P2 in bf16 pairs over the second half of the same columns. Of the sums of A it leaves, in
+// rows[0..31] by columns, those over the warp; in s's own block those of the pairs s < u <= t
+// by u. Returns the row's sum over a later block. 8 columns at a time from the last, so that
+// sums over t >= u run along, in a loop that stays rolled for the instruction cache (16 columns
+// twice unrolled: the kernel takes 250 us instead of 226 for 32768 tokens x 16 heads).
 __device__ __forceinline__ float mask_block(uint32_t a1, uint32_t a2, const Vec& v, int blk, const Who& t,
                                             float scale, float* rows) {
   const bool diag = blk == t.q4, direct = diag && !v.mild[blk];
@@ -1081,13 +1101,13 @@ __device__ __forceinline__ float mask_block(uint32_t a1, uint32_t a2, const Vec&
   a1 += 32 * blk;
   a2 += 32 * blk;
 #pragma unroll 1
-  for (int g = 0; g < 32; g += W) {
+  for (int g = 32 - W; g >= 0; g -= W) {
     float x[W], y[W];
     uint32_t p1[W / 2], p2[W / 2];
     tmem_ld8(a1 + g, x);
     tmem_ld8(a2 + g, y);
 #pragma unroll
-    for (int e = 0; e < W; e += 2) {
+    for (int e = W - 2; e >= 0; e -= 2) {
       const int col = 32 * blk + g + e;
       const float2 f2 = *reinterpret_cast<const float2*>(v.row + col);
       float f[2] = {tb * f2.x, tb * f2.y};
@@ -1099,19 +1119,19 @@ __device__ __forceinline__ float mask_block(uint32_t a1, uint32_t a2, const Vec&
       }
       float px[2], py[2];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const bool in = !diag || g + e + z >= t.l;
+      for (int z = 1; z >= 0; --z) {
+        const bool in = !diag || g + e + z >= t.l, behind = !diag || g + e + z > t.l;
         px[z] = in ? x[e + z] * f[z] : 0.f;
         py[z] = in ? y[e + z] * f[z] : 0.f;
-        const float pair = !diag || g + e + z > t.l ? x[e + z] * py[z] : 0.f;
-        x[e + z] = pair;
+        const float pair = behind ? x[e + z] * py[z] : 0.f;
         cs += pair;
+        x[e + z] = !diag ? pair : behind ? cs : 0.f;
       }
       p1[e / 2] = pack2bf(px[0], px[1]);
       p2[e / 2] = pack2bf(py[0], py[1]);
     }
-    tmem_st4(a1 + g / 2, p1);
-    tmem_st4(a2 + g / 2, p2);
+    tmem_st4(a1 + 16 + g / 2, p1);
+    tmem_st4(a2 + 16 + g / 2, p2);
     const float sum = lane_columns<W>(x);
     if (t.l < W) rows[g + t.l] = sum;
   }
@@ -1120,15 +1140,14 @@ __device__ __forceinline__ float mask_block(uint32_t a1, uint32_t a2, const Vec&
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(P_NTHR, 1)
-    k_lin_tc_back(Args a, const float* dS_out, const float* R_unit, const float* S_unit,
-                  const float* S_end, float* dS_in, const float* far, bf* dk, bf* dv, bf* dg,
-                  float* dgsum, const __grid_constant__ CUtensorMap mq,
-                  const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                  const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mdk,
-                  const __grid_constant__ CUtensorMap mdv) {
+    k_lin_tc_back(Args a, const float* dS_out, const float* R_unit, const float* S_chunk, bool start,
+                  float* dS_in, const float* far, bf* dk, bf* dv, bf* dg, float* dgsum,
+                  const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                  const __grid_constant__ CUtensorMap mdk, const __grid_constant__ CUtensorMap mdv) {
   using L = BackSm<DK, DV>;
   constexpr int NK = DK / 2, NV = DV / 2;
-  // A1: k q^T, then P1 in the first half of every 32 columns; A2: v dO^T, then P2; the second
+  // A1: k q^T, then P1 in the second half of every 32 columns; A2: v dO^T, then P2; the first
   // halves: the weighed q of the next chunk; G1: products with R for dk; G2: R's sum, then products with R for dv
   constexpr uint32_t A1 = 0, A2 = 128, G1 = 256, G2 = 384;
   chain();
@@ -1145,9 +1164,9 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   unsigned char *r_hi = sb + L::R_HI, *r_lo = sb + L::R_LO;
   Vec* vec = reinterpret_cast<Vec*>(sb + L::VEC);
   float* rows = reinterpret_cast<float*>(sb + L::ROWS);  // [lane quarter][t]
-  float* cols = reinterpret_cast<float*>(sb + L::COLS);  // [team and column group][s]
+  float* cols = reinterpret_cast<float*>(sb + L::COLS);  // [the block's distance - 1][s]
   float* farb = reinterpret_cast<float*>(sb + L::FAR);   // [column group][s]
-  float* red = reinterpret_cast<float*>(sb + L::RED);
+  float* red = reinterpret_cast<float*>(sb + L::RED);    // [2][warp] parts of e^{gamma_C} <S, R>
   uint64_t* full = reinterpret_cast<uint64_t*>(sb + L::BAR);  // [4] v, k, q, dO
   // MMAs: R's sum, k q^T and v dO^T, products with R, results; decay factors are there [2]
   uint64_t *bar_e = full + 4, *bar_a = full + 5, *bar_f = full + 6, *bar_c = full + 7, *ev_v = full + 8;
@@ -1157,7 +1176,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
            *ev_p = full + 15, *ev_u = full + 16;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 18);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
-  // what the issuing thread has seen done: A, products with R, results; events ev_x, ev_p, ev_r
+  // what the issuing thread has seen done: A, products with R, results; events ev_x, ev_p
   volatile int* seen = reinterpret_cast<volatile int*>(tslot + 2);
   // q and dO of a chunk take the slots of v and k of the one before, which are done with
   // early, v and k those of q and dO
@@ -1173,7 +1192,6 @@ __global__ void __launch_bounds__(P_NTHR, 1)
   const uint32_t tm = set_up(t, P_CTL, full, 10, 2, 5, 3, tslot, abort);
   const uint32_t tl = tm + ((uint32_t)(32 * t.q4) << 16);
   const size_t sh = ((size_t)u.seq * a.H + h) * DK * DV;
-  const bool last = u.at == u.n - 1;
   if (t.w < 8) {  // ---- masked products and results
     more_registers();
     for (int i = 0; i < nch; ++i) {
@@ -1188,11 +1206,10 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       if (t.cg == 1 || t.q4 == 3)  // nothing in the blocks before the diagonal
         for (int b = t.cg == 1 ? 0 : 2; b < (t.cg == 1 && t.q4 == 3 ? 2 : t.q4); ++b) {
           const uint32_t none[16] = {};
-          tmem_st16(tl + A1 + 32 * b, none);
-          tmem_st16(tl + A2 + 32 * b, none);
-          rows[t.q4 * TC + 32 * b + t.l] = 0.f;
+          tmem_st16(tl + A1 + 32 * b + 16, none);
+          tmem_st16(tl + A2 + 32 * b + 16, none);
         }
-      cols[t.cg * TC + t.lane] = cs;
+      if (t.cg) cols[t.lane] = cs;
       tmem_st_wait();
       warp_done<false>(ev_p);
       if (t.l == 0) mbar_arrive(ev_u + ph);
@@ -1216,35 +1233,11 @@ __global__ void __launch_bounds__(P_NTHR, 1)
     more_registers();
     float r[NV];
     // dS_in may be dS_out: of many units none reads it
-    const bool none = last && !dS_out;
     if (u.n > 1)
       load_unit<DK, NV>(R_unit + uh * DK * DV, t.lane, NV * t.cg, r);
     else
-      load_state<DK, DV, false, NV>(none ? nullptr : dS_out + sh, t.lane, NV * t.cg, r);
+      load_state<DK, DV, NV>(dS_out ? dS_out + sh : nullptr, t.lane, NV * t.cg, r);
     if (t.lane < DK) put_split<NV, true>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
-    {
-      // S as the units' of the transposed kernels, or as the call's
-      const float* S = last ? S_end + sh : S_unit + (uh + a.H) * DK * DV;
-      float x = 0.f;
-      if (!none && t.lane < DK) {
-#pragma unroll
-        for (int i = 0; i < NV; i += 4) {
-          float4 y;
-          if (last) {
-            y = *reinterpret_cast<const float4*>(S + (size_t)t.lane * DV + NV * t.cg + i);
-          } else {
-            const float* p = S + ((size_t)(t.lane >> 2) * DV + NV * t.cg + i) * 4 + (t.lane & 3);
-            y = make_float4(p[0], p[4], p[8], p[12]);
-          }
-          x = fmaf(r[i], y.x, x);
-          x = fmaf(r[i + 1], y.y, x);
-          x = fmaf(r[i + 2], y.z, x);
-          x = fmaf(r[i + 3], y.w, x);
-        }
-      }
-      x = lane_sum<32>(x);
-      if (t.l == 0) red[t.w - 8] = x;
-    }
     warp_done<true>(ev_r);
     for (int i = 0; i < nch; ++i) {
       const int c = nch - 1 - i, len = min(TC, u.len - c * TC), ph = i & 1;
@@ -1260,10 +1253,29 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       if (i) mbar_wait(ev_p, ph ^ 1, abort);  // the products have been read
       tc_fence_after();
       if (t.lane < DK) {
-        weigh<32>(slot(2, i), t, v.w, len, tl + A1 + 16, tl + A2 + 16);
+        weigh<32>(slot(2, i), t, v.w, len, tl + A1, tl + A2);
         tmem_st_wait();
       }
       warp_done<true>(ev_q);
+      // this thread's part of <S, R>, while R's sum is on its way; infinities behind a forgotten
+      // state do not count
+      const float whole = v.w.whole;
+      float dot = 0.f;
+      if (whole != 0.f && crossed(u, c, nch, start, dS_out)) {
+        const float* S = S_chunk + (crossing(u, c) * a.H + h) * DK * DV;
+        if (t.lane < DK) {
+#pragma unroll
+          for (int e = 0; e < NV; e += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(S + ((size_t)(NV * t.cg + e) / 4 * DK + t.lane) * 4);
+            dot = fmaf(r[e], y.x, dot);
+            dot = fmaf(r[e + 1], y.y, dot);
+            dot = fmaf(r[e + 2], y.z, dot);
+            dot = fmaf(r[e + 3], y.w, dot);
+          }
+        }
+      }
+      dot = lane_sum<32>(dot);
+      if (t.l == 0) red[8 * ph + t.w - 8] = whole == 0.f ? 0.f : whole * dot;
       mbar_wait(bar_e, ph, abort);
       tc_fence_after();
       if (t.lane < DK) add_state<NV>(tl + G2 + NV * t.cg, v.w.whole, r);
@@ -1277,7 +1289,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         cs = mask_block(tl + A1, tl + A2, v, blk, t, a.scale, rows + t.q4 * TC + 32 * blk);
         tmem_st_wait();
       }
-      cols[(2 + t.cg) * TC + t.lane] = cs;
+      cols[(1 + t.cg) * TC + t.lane] = cs;
       warp_done<false>(ev_p);
       const float down = v.far[t.lane];
       mbar_wait(bar_f, ph, abort);
@@ -1321,7 +1333,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       if (t.lane < DK) put_split<NV, true>(r_hi, r_lo, L::HALF_R, t.lane, NV * t.cg, r);
       warp_done<true>(ev_r);
     }
-    if (u.at == 0 && dS_in) store_state<DK, DV, false, NV>(dS_in + sh, t.lane, NV * t.cg, r);
+    if (u.at == 0 && dS_in) store_state<DK, DV, NV>(dS_in + sh, t.lane, NV * t.cg, r);
   } else {
     fewer_registers();
     if (t.w == P_LOAD) {  // ---- copies, and dg
@@ -1348,13 +1360,15 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         __syncwarp();
       };
       for (int k = 3; k >= 0; --k) load(k, 0);
-      float X = 0.f, sum = 0.f;
-      if (nch) {
-        until(5, 1);
-        for (int i = 0; i < 8; ++i) X += red[i];
-      }
+      float sum = 0.f;
       for (int i = 0; i < nch; ++i) {
         const int c = nch - 1 - i, len = min(TC, u.len - c * TC), row0 = u.row + c * TC;
+        // the next chunk's S into the L2
+        if (t.l == 0 && c > 0 && crossed(u, c - 1, nch, start, dS_out))
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(
+                           S_chunk + (crossing(u, c - 1) * a.H + h) * DK * DV),
+                       "r"(DK * DV * 4)
+                       : "memory");
         float fa[4] = {};  // a of the tokens 4 l ..
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -1365,40 +1379,75 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         until(3, i + 1);
         load(3, i + 1);  // where k was
         until(4, i + 1);
-        float x[4], ab = 0.f, suf = 0.f;
+        // of this lane's tokens e in the block k: pairs in it; ones with s in an earlier block
+        // and t = e; with s = e and t in a later block; b; and the sums over the lane's t of
+        // the pairs with s in the first and in the second block
+        const int k = t.l >> 3;
+        float own[4], with_t[4], with_s[4], fb[4], first = 0.f, second = 0.f;
 #pragma unroll
-        for (int j = 3; j >= 0; --j) {
+        for (int j = 0; j < 4; ++j) {
           const int e = 4 * t.l + j;
-          float rw = 0.f, cl = 0.f, bb = 0.f, f = 0.f;
-          if (e < len) {
-            f = fa[j];
-            rw = (rows[e] + rows[TC + e]) + (rows[2 * TC + e] + rows[3 * TC + e]);
-            cl = (cols[e] + cols[TC + e]) + (cols[2 * TC + e] + cols[3 * TC + e]);
-            bb = farb[e] + farb[TC + e];
-          }
-          ab += f - bb;
-          x[j] = (suf += (rw - cl) + (f - bb));
+          own[j] = with_t[j] = with_s[j] = fb[j] = 0.f;
+          if (e >= len) continue;
+          const float r0 = rows[e], r1 = rows[TC + e], r2 = rows[2 * TC + e], r3 = rows[3 * TC + e];
+          own[j] = k == 0 ? r0 : k == 1 ? r1 : k == 2 ? r2 : r3;
+          with_t[j] = k == 0 ? 0.f : k == 1 ? r0 : k == 2 ? r0 + r1 : r0 + r1 + r2;
+          with_s[j] = cols[e] + (cols[TC + e] + cols[2 * TC + e]);
+          fb[j] = farb[e] + farb[TC + e];
+          first += r0;
+          second += r1;
         }
-        float all = suf;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float y = __shfl_down_sync(0xffffffffu, all, o);
-          if (t.l + o < 32) all += y;
-        }
-        const float behind = all - suf + X;
-        X += lane_sum<32>(ab);
+        float X = 0.f;
+        for (int j = 0; j < 8; ++j) X += red[8 * (i & 1) + j];
         // k before the sums are stored: the next chunk's sums are written behind its products
         until(2, i + 1);
         load(1, i + 1);
         load(0, i + 1);
 #pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          first += __shfl_xor_sync(0xffffffffu, first, o);
+          second += __shfl_xor_sync(0xffffffffu, second, o);
+        }
+        const float p02 = __shfl_sync(0xffffffffu, first, 16), p03 = __shfl_sync(0xffffffffu, first, 24),
+                    p13 = __shfl_sync(0xffffffffu, second, 24);
+        const float across = k == 1 ? p02 + p03 : k == 2 ? p03 + p13 : 0.f;
+        // a and with_t over the lanes behind (the latter in the block), b and with_s over those before
+        float sa = (fa[0] + fa[1]) + (fa[2] + fa[3]), st = (with_t[0] + with_t[1]) + (with_t[2] + with_t[3]);
+        float sb = (fb[0] + fb[1]) + (fb[2] + fb[3]), ss = (with_s[0] + with_s[1]) + (with_s[2] + with_s[3]);
+        const int l8 = t.l & 7;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_down_sync(0xffffffffu, sa, o), z = __shfl_up_sync(0xffffffffu, sb, o);
+          if (t.l + o < 32) sa += y;
+          if (t.l >= o) sb += z;
+          if (o < 8) {
+            const float yt = __shfl_down_sync(0xffffffffu, st, o, 8), zs = __shfl_up_sync(0xffffffffu, ss, o, 8);
+            if (l8 + o < 8) st += yt;
+            if (l8 >= o) ss += zs;
+          }
+        }
+        sa = __shfl_down_sync(0xffffffffu, sa, 1), st = __shfl_down_sync(0xffffffffu, st, 1, 8);
+        sb = __shfl_up_sync(0xffffffffu, sb, 1), ss = __shfl_up_sync(0xffffffffu, ss, 1, 8);
+        if (t.l == 31) sa = 0.f;
+        if (l8 == 7) st = 0.f;
+        if (t.l == 0) sb = 0.f;
+        if (l8 == 0) ss = 0.f;
+        float x[4];
+#pragma unroll
+        for (int j = 3; j >= 0; --j) x[j] = (sa += fa[j]) + (st += with_t[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] += own[j] + ((sb + ss) + (across + X));
+          sb += fb[j], ss += with_s[j];
+        }
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = 4 * t.l + j;
           if (e >= len) break;
           if (dg)
-            dg[(size_t)(row0 + e) * a.H + h] = __float2bfloat16_rn(x[j] + behind);
+            dg[(size_t)(row0 + e) * a.H + h] = __float2bfloat16_rn(x[j]);
           else
-            sum += x[j] + behind;
+            sum += x[j];
         }
         __syncwarp();
       }
@@ -1430,17 +1479,17 @@ __global__ void __launch_bounds__(P_NTHR, 1)
         see(ev_g, wg, nch, -1);
         see(ev_q, wq, nch, -1);
         see(ev_o, wo, nch, -1);
-        see(ev_r, wr, nch, 5);
+        see(ev_r, wr, nch, -1);
         bool idle = true;
         if (cc < nch && cc == bc && wp > cc && wx > cc) {  // results
           tc_fence_after();
           const uint32_t sq = smem_u32(slot(2, cc)), so = smem_u32(slot(3, cc));
 #pragma unroll
           for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + G1, tm + A2 + at16(kk), mnmaj(sq, HALF_TILE, kk), umma_idesc(128, DK, 0, 1), true);
+            umma_ts(tm + G1, tm + A2 + 16 + at16(kk), mnmaj(sq, HALF_TILE, kk), umma_idesc(128, DK, 0, 1), true);
 #pragma unroll
           for (int kk = 0; kk < TC / 16; ++kk)
-            umma_ts(tm + G2, tm + A1 + at16(kk), mnmaj(so, HALF_TILE, kk), umma_idesc(128, DV, 0, 1), true);
+            umma_ts(tm + G2, tm + A1 + 16 + at16(kk), mnmaj(so, HALF_TILE, kk), umma_idesc(128, DV, 0, 1), true);
           umma_commit(bar_c);
           ++cc;
           idle = false;
@@ -1453,7 +1502,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int kk = 0; kk < TC / 16; ++kk)
-              umma_ts(tm + G2, tm + (p ? A2 : A1) + 16 + at16(kk), mnmaj(so, HALF_TILE, kk),
+              umma_ts(tm + G2, tm + (p ? A2 : A1) + at16(kk), mnmaj(so, HALF_TILE, kk),
                       umma_idesc(128, DV, 0, 1), p || kk);
           umma_commit(bar_e);
           ++ce;
@@ -1549,7 +1598,7 @@ struct TcPlan {
   int chunks;
   bool many;  // a sequence may have several units
   int *status, *first, *owner, *order;
-  float *whole[2], *dgsum, *D, *E, *S_end, *far;
+  float *whole[2], *dgsum, *D, *E, *S_chunk, *far;
   size_t bytes;
 };
 TcPlan tc_plan(const gdn_lin_shape& s, const int* cu, bool packed, bool back, unsigned char* ws) {
@@ -1575,7 +1624,7 @@ TcPlan tc_plan(const gdn_lin_shape& s, const int* cu, bool packed, bool back, un
     p.whole[1] = (float*)take(uh * 4);
     p.E = (float*)take(p.many ? uh * one : 0);
     p.dgsum = (float*)take(uh * 4);
-    p.S_end = (float*)take((size_t)s.nseq * s.H * one);
+    p.S_chunk = (float*)take(((size_t)s.B * s.T / TC + s.nseq) * s.H * one);
     p.far = (float*)take((size_t)s.B * s.T * s.H * 4);
   }
   p.m.first = p.first;
@@ -1635,17 +1684,15 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   };
 #define GO(kernel, Sm, regs, ...) \
   go(kernel, allow<kernel>(Sm::BYTES, regs), Sm::BYTES, Sm::THREADS, __VA_ARGS__)
-  using SmKV = StateSm<DK, DV>;
-  using SmVK = StateSm<DV, DK>;
+  using State = StateSm<DK, DV>;
   if (p.many) {
     prof_mark(c.st, "lin_tc_state");
-    e = back ? GO((k_lin_tc_state<DV, DK, false, true>), SmVK, 0, p.whole[0], p.D, clear, mv, mk)
-             : GO((k_lin_tc_state<DK, DV, false, false>), SmKV, 0, p.whole[0], p.D, clear, mk, mv);
+    e = GO((k_lin_tc_state<DK, DV, false>), State, 0, p.whole[0], p.D, clear, mk, mv);
     if (e) return e;
     clear = false;
     if (back) {
       prof_mark(c.st, "lin_tc_state");
-      e = GO((k_lin_tc_state<DK, DV, true, false>), SmKV, 0, p.whole[1], p.E, false, mq, mo);
+      e = GO((k_lin_tc_state<DK, DV, true>), State, 0, p.whole[1], p.E, false, mq, mo);
       if (e) return e;
     }
     e = lin_scan(p.m, s, p.whole[0], p.D, c.S_in, p.E, p.whole[1], c.dS_out, back, p.status, c.st);
@@ -1657,15 +1704,13 @@ cudaError_t run_tc(const LinCall& c, bool back) {
   prof_mark(c.st, back ? "lin_tc_dq" : "lin_tc_fwd");
   if (!back)
     return GO((k_lin_tc_pass<DK, DV, false>), PassKV, P_REGS, c.S_in, p.D, c.S_out, (bf*)c.o,
-              (const bf*)nullptr, 0ll, (float*)nullptr, clear, mq, mk, mv, mo);
-  e = GO((k_lin_tc_pass<DV, DK, true>), PassVK, P_REGS, c.S_in, p.D,
-         c.dS_out ? p.S_end : (float*)nullptr, (bf*)c.dq, (const bf*)c.q, s.ldq, p.far, clear, mo, mv, mk,
-         mdq);
+              (const bf*)nullptr, 0ll, (float*)nullptr, (float*)nullptr, false, clear, mq, mk, mv, mo);
+  e = GO((k_lin_tc_pass<DV, DK, true>), PassVK, P_REGS, c.S_in, p.D, (float*)nullptr, (bf*)c.dq,
+         (const bf*)c.q, s.ldq, p.far, p.S_chunk, c.dS_out != nullptr, clear, mo, mv, mk, mdq);
   if (e) return e;
   prof_mark(c.st, "lin_tc_back");
-  e = GO((k_lin_tc_back<DK, DV>), Back, P_REGS, c.dS_out, p.E, p.D, p.S_end, c.dS_in, p.far,
-         (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo, mdk,
-         mdv);
+  e = GO((k_lin_tc_back<DK, DV>), Back, P_REGS, c.dS_out, p.E, p.S_chunk, c.S_in != nullptr, c.dS_in,
+         p.far, (bf*)c.dk, (bf*)c.dv, (bf*)c.dg, c.ddecay ? p.dgsum : nullptr, mq, mk, mv, mo, mdk, mdv);
 #undef GO
   if (e) return e;
   if (c.ddecay) e = col_sum(p.dgsum, p.m.cap, s.H, s.H, c.ddecay, nullptr, nullptr, c.st);

@@ -21,11 +21,17 @@
  * on the tensor cores with each operand as two TF32 parts: operands are held to
  * 2^-23, products good to 2^-21.6 of themselves. With GDN_DTYPE_BF16, where rows
  * lie ld >= H * d apart (others take the fp32 kernels), products of inputs are
- * exact; what a state receives, and a state in the products that dg is summed
- * from, is taken as two bf16 parts (3 2^-16 of a term's magnitude, so S_out and
- * dS_in are good to that of the sums of magnitudes); a masked product (q k^T) L or
+ * exact; what a state receives, and a state before it meets a row for dg, is
+ * taken as two bf16 parts (3 2^-16 of a term's magnitude, so S_out and dS_in are
+ * good to that of the sums of magnitudes); a masked product (q k^T) L or
  * (dout v^T) L, and the state in o and dv, is rounded to bf16 once before it meets
  * its other factor, as the result itself is.
+ *
+ * dg_t is the sum over s < t <= u of the tokens' (and states') products
+ * scale (q_u . k_s) (dout_u . v_s) times the decay between them. Each is summed for
+ * itself: dg_t, and ddecay as the sum of dg, are good to 2^-16 (F32) or 2^-13 (BF16)
+ * of the magnitudes of their own terms before they are stored, whatever the rest of
+ * the sequence holds.
  *
  * Whole sequences work on chunks of 64 (fp32) or 128 (bf16) tokens by products with
  * zeros above the diagonal: a NaN or an infinity in a token reaches the results of
@@ -65,7 +71,9 @@ typedef struct {
 } gdn_lin_shape;
 
 /* Workspace bytes of gdn_lin_fwd (is_bwd = 0) or gdn_lin_bwd (is_bwd = 1); 0 if the
- * shape is invalid or unsupported. 256-byte aligned; not shared by calls that may
+ * shape is invalid or unsupported. With F32 it holds an fp32 state for every 64
+ * tokens of a head (the backward's two), with BF16 the backward's one for every 128.
+ * 256-byte aligned; not shared by calls that may
  * run at the same time. A kernel's wait that ran out is reported by
  * gdn_workspace_status as GDN_ERR_TIMEOUT. */
 size_t gdn_lin_workspace_bytes(const gdn_lin_shape* shape, int is_bwd);

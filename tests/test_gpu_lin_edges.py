@@ -6,7 +6,7 @@ import torch
 
 from chunked_linear_recurrence_gated_gb300 import gdn
 from oracle import lin_ops as lo
-from test_gpu_lin_ops import DT, check, host, lin_inputs
+from test_gpu_lin_ops import DT, HALF, check, host, lin_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -35,13 +35,15 @@ def test_no_tokens(dtype, packed, decay):
 # that sum of magnitudes, the oracle's on absolute values. Whatever is rounded on the way is a
 # factor of these terms, so dg_u is off by a multiple of M_u, however large terms of other
 # tokens are. fp32: a product of two operands of two TF32 parts, of two such products, decay
-# factors of 2^-21, and states good to 2^-17 of their magnitudes: 2^-16 in all.
-DG_TOL = {"f32": 2.0 ** -16}
+# factors of 2^-21, and states good to 2^-17 of their magnitudes: 2^-16 in all. bf16: states
+# good to 3 2^-16 of their magnitudes, and one of two states (or a state before it meets a
+# token) as two bf16 parts, 2^-16 more: 7 2^-16, and decay factors of 2^-21 and fp32 sums.
+DG_TOL = {"f32": 2.0 ** -16, "bf16": 2.0 ** -13}
 
 
-def dg_inputs(kind, dtype, T, H, dk, dv, cut, seed, decay="weak", nseq=1):
+def dg_inputs(kind, dtype, T, H, dk, dv, cut, seed, decay="weak", nseq=1, B=1):
     """Tokens from `cut` on 1024 times as large in v and dO as those before it."""
-    x = lin_inputs(1, T, H, dk, dv, DT[dtype], decay, seed=seed, nseq=nseq)
+    x = lin_inputs(B, T, H, dk, dv, DT[dtype], decay, seed=seed, nseq=nseq)
     x["v"][:, cut:] *= 1024
     x["do"][:, cut:] *= 1024
     x["dS"] *= 1024
@@ -84,3 +86,23 @@ def test_dg_beside_larger_tokens(dtype, kind, cut, packed):
 def test_dg_of_each_token(dtype, dk, dv, decay):
     x = dg_inputs("decays", dtype, 500, 2, dk, dv, 390, dk, decay, nseq=3)
     dg_check(x, dtype, [0, 13, 400, 500])
+
+
+@pytest.mark.parametrize("B,T,H,decay", [(1, 8200, 160, "weak"), (3, 2500, 60, "mid"), (1, 30000, 5, "weak"),
+                                         (160, 400, 1, "none"), (1, 8200, 160, "head")])
+def test_dg_of_long_units(B, T, H, decay):
+    """bf16 against the fp32 kernels (held to the oracle above): units of up to a whole
+    sequence, and sequences of many units; tokens behind forgotten states 1024 times as large."""
+    x = dg_inputs("decays", "bf16", T, H, 64, 64, T - 200, 4, decay, nseq=B, B=B)
+    if decay != "head":
+        x["g"][:, T - 200] = -float("inf")
+    f = {i: t.float() for i, t in x.items()}
+
+    def dg(x, m=lambda t: t):
+        return gdn.gdn_lin_bwd(m(x["q"]), m(x["k"]), m(x["v"]), x["g"], m(x["S"]), m(x["do"]),
+                               m(x["dS"]), scale=0.2)[3].double()
+
+    ref, mag = dg(f), dg(f, torch.abs)
+    tol = (2.0 ** -13 + 2.0 ** -16) * mag + 1e-30 + (0.0 if decay == "head" else HALF * ref.abs())
+    off = (dg(x) - ref).abs() - tol
+    assert not (off > 0).any() and not off.isnan().any(), (off.max(), ref.abs().max())
