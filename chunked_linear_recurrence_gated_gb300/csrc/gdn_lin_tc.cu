@@ -212,6 +212,12 @@ __device__ __forceinline__ void sum_decay(const Raw& r, bool wide, float* hi, fl
 __device__ __forceinline__ float exp_diff(float h1, float l1, float h0, float l0) {
   return __expf((h1 - h0) + (l1 - l0));
 }
+// e^{gamma_C}: it is multiplied up over all chunks that a state passes, so it is good to the
+// last bits (2^-23 of itself).
+__device__ __forceinline__ float exp_whole(float h, float l) {
+  const float e = expf(h);
+  return fmaf(e, l, e);
+}
 // Weights of the state's update: to the chunk's end, or (BACK) scale times from its start.
 template <bool BACK>
 __device__ __forceinline__ void fill_weights(const float* hi, const float* lo, float scale, Weights& w) {
@@ -223,7 +229,7 @@ __device__ __forceinline__ void fill_weights(const float* hi, const float* lo, f
     o[i] = BACK ? scale * exp_diff(hi[i], lo[i], 0.f, 0.f) : exp_diff(eh, el, hi[i], lo[i]);
 #pragma unroll
   for (int i = 0; i < 2; ++i) split2(o[2 * i], o[2 * i + 1], w.hi[2 * l + i], w.lo[2 * l + i]);
-  if (l == 0) w.whole = exp_diff(eh, el, 0.f, 0.f);
+  if (l == 0) w.whole = exp_whole(eh, el);
 }
 // One of two warps' part of a chunk's factors (each sums gamma for itself: one warp took
 // 9 thousand cycles for all of them, twice what the rest of a chunk needs).

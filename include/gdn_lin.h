@@ -17,21 +17,22 @@
  * meant to be <= 0; g = -inf (the state is forgotten) gives factors of 0. Positive
  * values are taken as they are, and overflow where e^g over a sequence does.
  *
- * Sums, states and decay factors are fp32. With GDN_DTYPE_F32 products are taken
- * on the tensor cores with each operand as two TF32 parts: operands are held to
- * 2^-23, products good to 2^-21.6 of themselves. With GDN_DTYPE_BF16, where rows
- * lie ld >= H * d apart (others take the fp32 kernels), products of inputs are
- * exact; what a state receives, and a state before it meets a row for dg, is
- * taken as two bf16 parts (3 2^-16 of a term's magnitude, so S_out and dS_in are
- * good to that of the sums of magnitudes); a masked product (q k^T) L or
- * (dout v^T) L, and the state in o and dv, is rounded to bf16 once before it meets
- * its other factor, as the result itself is.
+ * Sums, states and decay factors are fp32; each chunk (64 tokens of F32, 128 of BF16)
+ * that a state passes rounds it by 2^-22 of itself at most. With GDN_DTYPE_F32 products
+ * are taken on the tensor cores with each operand as two TF32 parts: operands are held
+ * to 2^-23, products good to 2^-21.6 of themselves. With GDN_DTYPE_BF16, where rows lie
+ * ld >= H * d apart (others take the fp32 kernels), products of inputs are exact; what
+ * a state receives, and a state before it meets a row for dg, is taken as two bf16
+ * parts (3 2^-16 of a term's magnitude, so S_out and dS_in are good to that of the sums
+ * of magnitudes, and to the chunks' roundings); a masked product (q k^T) L or
+ * (dout v^T) L, and the state in o and dv, is rounded to bf16 once before it meets its
+ * other factor, as the result itself is.
  *
  * dg_t is the sum over s < t <= u of the tokens' (and states') products
  * scale (q_u . k_s) (dout_u . v_s) times the decay between them. Each is summed for
  * itself: dg_t, and ddecay as the sum of dg, are good to 2^-16 (F32) or 2^-13 (BF16)
- * of the magnitudes of their own terms before they are stored, whatever the rest of
- * the sequence holds.
+ * of the magnitudes of their own terms before they are stored (and to the roundings of
+ * the chunks between the tokens), whatever the rest of the sequence holds.
  *
  * Whole sequences work on chunks of 64 (fp32) or 128 (bf16) tokens by products with
  * zeros above the diagonal: a NaN or an infinity in a token reaches the results of

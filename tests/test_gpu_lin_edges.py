@@ -6,7 +6,7 @@ import torch
 
 from chunked_linear_recurrence_gated_gb300 import gdn
 from oracle import lin_ops as lo
-from test_gpu_lin_ops import DT, HALF, check, host, lin_inputs
+from test_gpu_lin_ops import DT, HALF, check, gen, host, lin_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,22 @@ def test_dg_of_long_units(B, T, H, decay):
     tol = (2.0 ** -13 + 2.0 ** -16) * mag + 1e-30 + (0.0 if decay == "head" else HALF * ref.abs())
     off = (dg(x) - ref).abs() - tol
     assert not (off > 0).any() and not off.isnan().any(), (off.max(), ref.abs().max())
+
+
+@pytest.mark.parametrize("dtype,T,C", [("f32", 65536, 64), ("bf16", 262144, 128)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_states_that_hardly_decay(dtype, T, C, packed):
+    """Nothing but the decay acts on a state over thousands of chunks. A chunk's factor is
+    good to 2^-23 of itself, and it, its product with others and the state's round by 2^-24
+    each: 2^-22 a chunk."""
+    H = 12
+    r = gen(2)
+    x = torch.zeros(1, T, H, 64, dtype=DT[dtype], device="cuda")
+    S = 1 + r(1, H, 64, 64).abs()
+    decay = -torch.logspace(-7, -3.7, H, device="cuda")
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda") if packed else None
+    got = (gdn.gdn_lin_fwd(x, x, x, decay, S, cu_seqlens=cu)[1],
+           gdn.gdn_lin_bwd(x, x, x, decay, S, x, S, cu_seqlens=cu)[4])
+    want = S.double() * torch.exp(T * decay.double())[None, :, None, None]
+    for t in got:
+        assert ((t - want).abs() <= T / C * 2.0 ** -22 * want).all()
