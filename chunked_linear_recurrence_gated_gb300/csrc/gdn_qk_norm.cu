@@ -21,17 +21,18 @@ constexpr int QN_UB = 2, QN_BLOCKS_B = 2;
 constexpr int QN_HEADS = 16;   // most heads that share one set of sines and cosines
 constexpr int QN_PARTS = QN_SMS * QN_BLOCKS_B;  // most blocks of the backward: partial sums of dw
 
-// f / (2 pi) as a fraction of a turn in units of 2^-64, for |f| < 2^40. With f =
-// m 2^e (m < 2^53) and C = floor(2^66 / (2 pi)), it is m C 2^(e - 2) up to one unit:
-// whole-number products only, so that pos times it, modulo 2^64, is the angle's
-// fraction of a turn to 2^-33 for any 32-bit position.
+// f / (2 pi) as a fraction of a turn in units of 2^-64, for |f| < 2^40, less than a unit below
+// the exact one. With f = m 2^e (m < 2^53) and C = floor(2^130 / (2 pi)), it is m C 2^(e - 66) in
+// whole numbers (64 bits of C alone would be off by f / 4 units), so that pos times it, modulo
+// 2^64, is the angle's fraction of a turn to 2^-33 for any 32-bit position.
 __device__ __forceinline__ unsigned long long turn_step(double f) {
-  constexpr unsigned long long C = 0xA2F9836E4E441529ull;  // 2^66 / (2 pi) = 2^65 / pi
+  constexpr unsigned long long C = 0xA2F9836E4E441529ull, REST = 0xFC2757D1F534DDC0ull;  // 2 / pi
   const unsigned long long u = (unsigned long long)__double_as_longlong(f);
   const int ex = (int)(u >> 52) & 0x7ff;
   const unsigned long long m = (u & 0xfffffffffffffull) | (ex ? 1ull << 52 : 0);
-  const int s = 2 + 1075 - max(ex, 1);  // right shift of the 128-bit product
-  const unsigned long long lo = m * C, hi = __umul64hi(m, C);
+  const int s = 2 + 1075 - max(ex, 1);  // right shift of the upper 128 bits of the product
+  const unsigned long long low = __umul64hi(m, REST), lo = m * C + low;
+  const unsigned long long hi = __umul64hi(m, C) + (lo < low);
   unsigned long long r = 0;
   if (s <= 0)
     r = lo << min(-s, 63);

@@ -161,8 +161,9 @@ gdn_status gdn_prep_bwd(const gdn_prep_shape* shape, const void* q, const void* 
  *     y = n with its first rot values turned, times q_scale for q
  * Of the pair i (values i and i + rot / 2 for GDN_ROPE_HALF, 2i and 2i + 1 for
  * GDN_ROPE_PAIRS), with a = pos inv_freq[i]: (x0, x1) -> (x0 cos a - x1 sin a,
- * x1 cos a + x0 sin a). The angle is reduced to a fraction of a turn in 64-bit whole
- * numbers, so far positions lose nothing (below 2^-32 of a turn for any int32).
+ * x1 cos a + x0 sin a). The angle is reduced to a fraction of a turn in whole numbers
+ * before it is rounded to fp32, so far positions and large frequencies lose nothing
+ * (2^-31 of a turn at most for any int32 and any frequency below).
  * q [rows, Hq, d], k [rows, Hk, d] vector rows; wq, wk [d]; inv_freq DEVICE fp64
  * [rot / 2], finite and below 2^40 in size; pos DEVICE int32 [rows] (NULL: row
  * mod T). qn, kn contiguous: [rows, Hq, d] and [rows, Hk, d] (H = 0), or both

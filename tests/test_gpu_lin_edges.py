@@ -7,6 +7,7 @@ import torch
 from chunked_linear_recurrence_gated_gb300 import gdn
 from oracle import lin_ops as lo
 from test_gpu_lin_ops import DT, HALF, check, gen, host, lin_inputs
+from test_lin_edges_cpu import turns
 
 pytestmark = pytest.mark.gpu
 
@@ -125,3 +126,20 @@ def test_states_that_hardly_decay(dtype, T, C, packed):
     want = S.double() * torch.exp(T * decay.double())[None, :, None, None]
     for t in got:
         assert ((t - want).abs() <= T / C * 2.0 ** -22 * want).all()
+
+
+@pytest.mark.parametrize("style", ["half", "pairs"])
+def test_far_positions_of_large_frequencies(style):
+    """Exact angles of the farthest positions at any frequency up to 2^40: below 2^-31 of a
+    turn in whole numbers, the fraction of half a turn rounded by 2^-25, sine and cosine by
+    2^-23, and the norm's factor by 2^-22: below 2^-20 of the sum of two terms of size 1."""
+    f = torch.tensor([1.0, -100.25, 1e4, 1e6, 123456789.0, -2.0 ** 39, 3.3e11, 0.1], dtype=torch.float64)
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 12345, 1 << 30, 7, -1]
+    x = torch.ones(1, len(pos), 1, 64, device="cuda")
+    y = gdn.gdn_qk_norm_fwd(x, x, None, None, f.cuda(), style=style, eps=1e-30,
+                            pos=torch.tensor([pos], dtype=torch.int32, device="cuda"))[0][0, :, 0].cpu()
+    at = np.array([[2 * np.pi * float(turns(g, p) % 1) for g in f.tolist()] for p in pos])
+    a, b = (y[:, :8], y[:, 8:16]) if style == "half" else (y[:, 0:16:2], y[:, 1:16:2])
+    assert np.abs(a.numpy() - (np.cos(at) - np.sin(at))).max() < 2.0 ** -20
+    assert np.abs(b.numpy() - (np.cos(at) + np.sin(at))).max() < 2.0 ** -20
+    assert (y[:, 16:] - 1).abs().max() < 2.0 ** -20
