@@ -941,6 +941,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
           __nanosleep(40);  // its scheduler is others' too
           if (clock64() - t0 > 64 * WAIT_LIMIT) *abort = 1;  // the issuing thread gives up before
         }
+        __threadfence_block();
         load(n);
       }
     } else if (t.w == P_CTL && t.l == 0) {  // ---- MMAs
@@ -954,6 +955,7 @@ __global__ void __launch_bounds__(P_NTHR, 1)
       auto see = [&](uint64_t* bar, int& i, int most, int tell) {
         if (i < most && mbar_test(bar, i & 1)) {
           ++i;
+          if (tell == 4) __threadfence_block();  // the teams' reads of the tile are seen with it
           if (tell >= 0) seen[tell] = i;
         }
       };

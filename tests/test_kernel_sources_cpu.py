@@ -32,3 +32,20 @@ def test_asynchronous_copies_are_compiler_barriers():
     assert len(found) >= 8
     bad = [(f, line) for f, line, text in found if '"memory"' not in text or "volatile" not in text]
     assert not bad, bad
+
+
+def test_flags_between_warps_are_fenced():
+    """A thread that tells others through a plain flag in shared memory what it has seen of the
+    teams' events fences in between, and so does who acts on the flag: the event itself orders
+    the teams' accesses for the thread that waited for it only."""
+    with open(os.path.join(CSRC, "gdn_lin_tc.cu")) as f:
+        text = f.read()
+    tells = re.findall(r"auto see = .*?\n      };", text, re.S)
+    assert len(tells) == 2
+    for body in tells:
+        assert "__threadfence_block();" in body.split("seen[tell]")[0], body
+    waits = [m.end() for m in re.finditer(r"while \(!\*abort && [^{]*seen\[", text)]
+    assert len(waits) == 2
+    for at in waits:
+        behind = text[at:at + 700]
+        assert "__threadfence_block();" in behind.split("load(")[0], behind
