@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "gdn_internal.cuh"
 #include "gdn_lin.cuh"
@@ -1659,11 +1660,14 @@ cudaError_t out_map(CUtensorMap* map, const void* base, const gdn_lin_shape& s, 
 // share out (a smaller pool would leave them waiting).
 template <auto KERNEL>
 cudaError_t allow(uint32_t bytes, int registers) {
-  static const int has = [] {
+  static std::atomic<int> has{0};  // asked again after a failure
+  if (!has.load(std::memory_order_relaxed)) {
     cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? f.numRegs : 0;
-  }();
-  if (has < registers) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncGetAttributes(&f, KERNEL);
+    if (e) return e;
+    has.store(f.numRegs, std::memory_order_relaxed);
+  }
+  if (has.load(std::memory_order_relaxed) < registers) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 

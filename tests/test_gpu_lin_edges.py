@@ -1,5 +1,8 @@
 """Linear attention and the query / key norms (include/gdn_lin.h, gdn_layer.h) in calls that
 lie at the edge of what their headers allow. Inputs and tolerances as in test_gpu_lin_ops."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -143,3 +146,30 @@ def test_far_positions_of_large_frequencies(style):
     assert np.abs(a.numpy() - (np.cos(at) - np.sin(at))).max() < 2.0 ** -20
     assert np.abs(b.numpy() - (np.cos(at) + np.sin(at))).max() < 2.0 ** -20
     assert (y[:, 16:] - 1).abs().max() < 2.0 ** -20
+
+
+FIRST_IN_A_GRAPH = """
+import torch
+from chunked_linear_recurrence_gated_gb300 import gdn
+r = lambda *s: torch.randn(*s, device="cuda")
+for dt in (torch.bfloat16, torch.float32):
+    q, k, v, do = (r(1, 700, 2, 64).to(dt) for _ in range(4))
+    g, S, w = -r(1, 700, 2).abs().to(dt), r(1, 2, 64, 64), r(64)
+    f = torch.rand(8, dtype=torch.float64, device="cuda")
+    call = lambda: (gdn.gdn_lin_fwd(q, k, v, g, S) + gdn.gdn_lin_bwd(q, k, v, g, S, do, S)
+                    + gdn.gdn_qk_norm_fwd(q, k, w, w, f) + gdn.gdn_qk_norm_bwd(q, k, w, w, f, q, k)
+                    + (gdn.gdn_lin_step(q[0, :1], k[0, :1], v[0, :1], g[0, :1], S.clone()),))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, call()))
+print("the same")
+"""
+
+
+def test_first_call_of_a_process_is_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "the same" in r.stdout, r.stderr[-2000:]
