@@ -537,8 +537,8 @@ constexpr uint32_t slot_bytes(int a, int b) { return (a > b ? a : b) * TC * 2; }
 // times scale) y z^T, and the unit's whole decay. Not for a sequence's last unit (REV: its
 // first), whose state nobody starts from. The MMAs of a chunk run under the weighing of
 // the next one and the update from the one before; three chunks' tiles are in flight. Bound by
-// the loads and the weighing side by side: 52 us for k and v of 32768 tokens x 16 heads (5.1
-// TB/s; issue 30 %, tensor pipe 30 %).
+// the loads and the weighing side by side: 53 us for k and v of 32768 tokens x 16 heads (5.1
+// TB/s; issue 28 %, tensor pipe 29 %).
 template <int DY, int DZ>
 struct StateSm {
   static constexpr int THREADS = NTHR;
@@ -1065,8 +1065,8 @@ __global__ void __launch_bounds__(P_NTHR, 1)
 // way (by the first team from R's tiles, with warp-level MMAs, the kernel took 280 us instead of
 // 243 for 32768 x 16 heads; by the decay warps 352).
 // Bound by the chain P -> results -> R's sum -> products of the next chunk, 14 thousand cycles
-// of which the MMAs are 7: 243 us for 32768 tokens x 16 heads of 128 (224 without <S, R>; P by
-// one team of the two 280 us).
+// of which the MMAs are 7: 243 us for 32768 tokens x 16 heads of 128 (issue 41 %, tensor pipe
+// 31 %; without <S, R> 224 us; P by one team of the two 280).
 template <int DK, int DV>
 struct BackSm {
   static constexpr int THREADS = P_NTHR;
@@ -1099,7 +1099,7 @@ __device__ __forceinline__ float lane_columns(float* x) {
 // rows[0..31] by columns, those over the warp; in s's own block those of the pairs s < u <= t
 // by u. Returns the row's sum over a later block. 8 columns at a time from the last, so that
 // sums over t >= u run along, in a loop that stays rolled for the instruction cache (16 columns
-// twice unrolled: the kernel takes 250 us instead of 226 for 32768 tokens x 16 heads).
+// twice unrolled: the kernel takes 24 us more for 32768 tokens x 16 heads).
 __device__ __forceinline__ float mask_block(uint32_t a1, uint32_t a2, const Vec& v, int blk, const Who& t,
                                             float scale, float* rows) {
   const bool diag = blk == t.q4, direct = diag && !v.mild[blk];
