@@ -65,7 +65,8 @@ def dg_check(x, dtype, cu=None, scale=0.2):
                           cu_seqlens=d)[3]
     with np.errstate(invalid="ignore"):
         ref = lo.lin_bwd(q, k, v, g, S, do, dS, scale, cu)[3]
-        mag = lo.lin_bwd(*map(np.abs, (q, k, v)), g, *map(np.abs, (S, do, dS)), scale, cu)[3]
+        mag = lo.lin_bwd(*map(np.abs, (q, k, v)), g, *(None if t is None else np.abs(t) for t in (S, do, dS)),
+                         scale, cu)[3]
     if x["g"].dim() == 1:
         ref, mag = ref.sum((0, 1)), mag.sum((0, 1))
     check("dg", got, ref, DG_TOL[dtype] * mag)
@@ -90,6 +91,20 @@ def test_dg_beside_larger_tokens(dtype, kind, cut, packed):
 def test_dg_of_each_token(dtype, dk, dv, decay):
     x = dg_inputs("decays", dtype, 500, 2, dk, dv, 390, dk, decay, nseq=3)
     dg_check(x, dtype, [0, 13, 400, 500])
+
+
+@pytest.mark.parametrize("dtype", sorted(DG_TOL))
+@pytest.mark.parametrize("S,dS", [(False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("T", [1, 100, 128, 129, 256, 385, 700])
+@pytest.mark.parametrize("packed", [False, True])
+def test_dg_with_and_without_states(dtype, S, dS, T, packed):
+    """Chunks that nothing comes into or goes out of, and ones that only tokens do."""
+    x = dg_inputs("decays", dtype, T, 2, 64, 128, T // 2, T, nseq=4 if packed else 2, B=1 if packed else 2)
+    if not S:
+        x["S"] = None
+    if not dS:
+        x["dS"] = None
+    dg_check(x, dtype, [0, T // 3, T // 3, T // 3 + T // 2, T] if packed else None)
 
 
 @pytest.mark.parametrize("B,T,H,decay", [(1, 8200, 160, "weak"), (3, 2500, 60, "mid"), (1, 30000, 5, "weak"),
